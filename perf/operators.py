@@ -335,8 +335,8 @@ def run(st):
             return fa.kv_read(st["k_cache"], st["v_cache"], st["table"], st["kv_len"], st["kv_indptr"], st["rows"],
                               k_scale=st["k_scale"], v_scale=st["v_scale"])
         return fa.forward_paged(st["q"], st["k_cache"], st["v_cache"], st["table"], st["kv_len"], st["q_indptr"],
-                                st["max_new"], k_scale=st["k_scale"], v_scale=st["v_scale"], window=st["window"],
-                                sinks=st["sinks"])
+                                st["max_new"], k_scale=st["k_scale"], v_scale=st["v_scale"],
+                                window=st["window"] or None, sinks=st["sinks"])
     if op == "window":
         return _plain_window(st)
     if op == "append":
