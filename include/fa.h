@@ -129,6 +129,22 @@ int fa_fwd(const void* q, const void* k, const void* v, void* o, float* lse, int
            int causal, float scale, int stable, float beta, const fa_row_stats* stats, void* stream);
 
 /*
+ * fa_fwd_window -- the forward of fa_fwd with a causal sliding window and sinks.  (The pages
+ * have no counterpart; the softmax, the shift rule and the statistics are fa_fwd's over the
+ * keys that a row sees.)
+ *   window : >= 1; query i sees the keys j <= i with i - j < window (its own key is always
+ *            among them, so no row is empty); a window of N or more is plain causal attention
+ *   sinks  : >= 0; the first `sinks` keys (j < sinks, j <= i) stay visible to every query
+ *   the other arguments are those of fa_fwd
+ * Key blocks that no row of a tile sees are neither loaded nor multiplied.  Like the other
+ * dense entry points it multiplies whole 128-key blocks: a hidden key of a visited block must
+ * have a finite V row (0 * Inf = NaN).
+ * Returns FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED or FA_ERR_CUDA.
+ */
+int fa_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int N, int d,
+                  int window, int sinks, float scale, int stable, float beta, const fa_row_stats* stats, void* stream);
+
+/*
  * fa_quantize_fp8 -- dynamic per-tensor FP8 scaling ([ijyty §6.1]: the stabilised
  * shift carries over to FP8 when paired with dynamic scaling factors; the page gives no
  * formula, this is the usual amax rule).
@@ -201,6 +217,15 @@ enum { FA_BWD_PREPROCESS = 1, FA_BWD_MAIN = 2, FA_BWD_DQ_CONVERT = 4, FA_BWD_ALL
 int fa_bwd_staged(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO,
                   void* dq, void* dk, void* dv, float* delta_out, int B, int H, int N, int d, int causal,
                   float scale, void* workspace, size_t workspace_bytes, void* stream, int stages);
+
+/*
+ * fa_bwd_window -- the backward of fa_fwd_window: fa_bwd with the mask of `window` and `sinks`
+ * (see fa_fwd_window; o and lse are that forward's).  Workspace, outputs and errors are
+ * fa_bwd's; the gradients of keys that no query sees are zero.
+ */
+int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO,
+                  void* dq, void* dk, void* dv, float* delta_out, int B, int H, int N, int d, int window, int sinks,
+                  float scale, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * fa_bwd_noalloc -- the backward of fa_bwd for callers that cannot allocate device

@@ -29,9 +29,9 @@ OUTPUT_NAMES = ("o", "lse", "dq", "dk", "dv")
 FA_DEVFLAG_TIMEOUT, FA_DEVFLAG_BOUNDS, FA_DEVFLAG_NONFINITE = 1, 2, 4
 
 # every symbol include/fa.h declares
-EXPORTS = ("fa_fwd", "fa_fwd_fp8", "fa_quantize_fp8", "fa_bwd", "fa_bwd_staged", "fa_bwd_noalloc",
-           "fa_bwd_noalloc_status", "fa_bwd_workspace_size", "fa_device_status", "fa_device_report_read",
-           "fa_last_error", "fa_version")
+EXPORTS = ("fa_fwd", "fa_fwd_window", "fa_fwd_fp8", "fa_quantize_fp8", "fa_bwd", "fa_bwd_window", "fa_bwd_staged",
+           "fa_bwd_noalloc", "fa_bwd_noalloc_status", "fa_bwd_workspace_size", "fa_device_status",
+           "fa_device_report_read", "fa_last_error", "fa_version")
 
 # size of the fixed device scratch behind fa_bwd_noalloc (FA_NOALLOC_SCRATCH_BYTES in fa.h)
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
@@ -76,6 +76,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     vp, ci, cf, cs = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
     L.fa_fwd.argtypes = [vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, cf, ci, cf, ctypes.POINTER(RowStats), vp]
     L.fa_fwd.restype = ci
+    L.fa_fwd_window.argtypes = [vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, ci, cf, ci, cf, ctypes.POINTER(RowStats), vp]
+    L.fa_fwd_window.restype = ci
     L.fa_fwd_fp8.argtypes = [vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, cf, ci, cf, ctypes.POINTER(RowStats), vp]
     L.fa_fwd_fp8.restype = ci
     L.fa_quantize_fp8.argtypes = [vp, cs, vp, vp, vp]
@@ -84,6 +86,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.fa_bwd_workspace_size.restype = cs
     L.fa_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, cf, vp, cs, vp]
     L.fa_bwd.restype = ci
+    L.fa_bwd_window.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, ci, cf, vp, cs, vp]
+    L.fa_bwd_window.restype = ci
     L.fa_bwd_staged.argtypes = L.fa_bwd.argtypes + [ci]
     L.fa_bwd_staged.restype = ci
     L.fa_bwd_noalloc.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, cf, vp]
@@ -139,6 +143,15 @@ def fa_fwd(q, k, v, o, lse, causal: bool, scale: float, stable: int, beta: float
                          _stream(stream))
 
 
+def fa_fwd_window(q, k, v, o, lse, window: int, sinks: int, scale: float, stable: int, beta: float, stats=None,
+                  stream=None) -> int:
+    B, H, N, d = q.shape
+    st = _row_stats(stats)
+    return load().fa_fwd_window(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H, N, d, int(window), int(sinks),
+                                float(scale), int(stable), float(beta), ctypes.byref(st) if st is not None else None,
+                                _stream(stream))
+
+
 def _row_stats(stats):
     if stats is None:
         return None
@@ -172,6 +185,15 @@ def fa_bwd(q, k, v, o, lse, do, dq, dk, dv, delta, causal: bool, scale: float, w
     if stages == FA_BWD_ALL:
         return load().fa_bwd(*args)
     return load().fa_bwd_staged(*args, int(stages))
+
+
+def fa_bwd_window(q, k, v, o, lse, do, dq, dk, dv, delta, window: int, sinks: int, scale: float, workspace,
+                  stream=None) -> int:
+    B, H, N, d = q.shape
+    nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    return load().fa_bwd_window(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(do), _ptr(dq), _ptr(dk), _ptr(dv),
+                                _ptr(delta), B, H, N, d, int(window), int(sinks), float(scale), _ptr(workspace),
+                                nbytes, _stream(stream))
 
 
 def fa_bwd_noalloc(q, k, v, o, lse, do, dq, dk, dv, delta, causal: bool, scale: float, stream=None) -> int:
@@ -210,16 +232,32 @@ def _stats_dict(B, H, N, device):
             "row_min_raw": torch.empty((B, H, N), device=device, dtype=torch.float32)}
 
 
+def _check_window(causal, window, sinks):
+    if window is None:
+        if sinks:
+            raise ValueError("sinks need a window")
+    elif not causal:
+        raise ValueError("a window needs causal=True")
+
+
 def forward(q, k, v, causal: bool = True, scale=None, stable: int = 1, beta: float = 1.25, stats: bool = False,
-            stream=None):
-    """Returns (o, lse) or (o, lse, stats_dict); outputs are freshly allocated."""
+            stream=None, window=None, sinks: int = 0):
+    """Returns (o, lse) or (o, lse, stats_dict); outputs are freshly allocated.
+
+    With a window (causal only), query i sees the keys j <= i with i - j < window and the
+    first ``sinks`` keys.
+    """
     _check_qkv(q, k, v)
+    _check_window(causal, window, sinks)
     B, H, N, d = q.shape
     scale = 1.0 / math.sqrt(d) if scale is None else scale
     o = torch.empty_like(q)
     lse = torch.empty((B, H, N), device=q.device, dtype=torch.float32)
     sd = _stats_dict(B, H, N, q.device) if stats else None
-    _check(fa_fwd(q, k, v, o, lse, causal, scale, stable, beta, sd, stream))
+    if window is None:
+        _check(fa_fwd(q, k, v, o, lse, causal, scale, stable, beta, sd, stream))
+    else:
+        _check(fa_fwd_window(q, k, v, o, lse, window, sinks, scale, stable, beta, sd, stream))
     return (o, lse, sd) if stats else (o, lse)
 
 
@@ -256,16 +294,20 @@ def forward_fp8(q8, k8, v8, descale, causal: bool = True, scale=None, stable: in
 
 
 def backward(q, k, v, o, lse, do, causal: bool = True, scale=None, workspace=None, want_delta: bool = False,
-             stream=None):
-    """Returns (dq, dk, dv) or (dq, dk, dv, delta)."""
+             stream=None, window=None, sinks: int = 0):
+    """Returns (dq, dk, dv) or (dq, dk, dv, delta); window and sinks are the forward's."""
     _check_qkv(q, k, v, o, do)
+    _check_window(causal, window, sinks)
     B, H, N, d = q.shape
     scale = 1.0 / math.sqrt(d) if scale is None else scale
     if workspace is None:
         workspace = torch.empty(fa_bwd_workspace_size(B, H, N, d), device=q.device, dtype=torch.uint8)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     delta = torch.empty((B, H, N), device=q.device, dtype=torch.float32) if want_delta else None
-    _check(fa_bwd(q, k, v, o, lse, do, dq, dk, dv, delta, causal, scale, workspace, stream))
+    if window is None:
+        _check(fa_bwd(q, k, v, o, lse, do, dq, dk, dv, delta, causal, scale, workspace, stream))
+    else:
+        _check(fa_bwd_window(q, k, v, o, lse, do, dq, dk, dv, delta, window, sinks, scale, workspace, stream))
     return (dq, dk, dv, delta) if want_delta else (dq, dk, dv)
 
 

@@ -126,6 +126,7 @@ struct Params {
   int N_pad;        // N rounded up to 128
   int n_tiles;      // N_pad / 128
   int causal;
+  int window, sinks;  // windowed kernels: query i sees keys j <= i with i - j < window or j < sinks
   float scale;
   float scale_log2;
   int inject_stall;  // test builds only (FA_TEST_HOOKS): make the MMA warp's first wait run out
@@ -215,7 +216,23 @@ __device__ __forceinline__ bool work_item(const Params& p, int n, int& jt, int& 
   return true;
 }
 
-template <int D, bool kWalk>
+// The query tiles of key tile jt: its first one, i0, and their number.  With a window they end at
+// the last tile that the window of one of its keys reaches; a tile that holds sinks keeps all.
+template <bool kWin>
+__device__ __forceinline__ int query_tiles(const Params& p, int jt, int& i0) {
+  i0 = (kWin || p.causal) ? jt : 0;
+  if constexpr (kWin) {
+    const int last_key = min(jt * kBlock + kBlock, p.N) - 1;
+    // the last key's window ends before row N (the sum below is then under N and cannot overflow)
+    if (jt * kBlock >= p.sinks && p.window < p.N - last_key) return (last_key + p.window - 1) / kBlock - jt + 1;
+  }
+  return p.n_tiles - i0;
+}
+
+// kWin: causal with a window and sinks (p.window, p.sinks) instead of p.causal.  Key tiles then
+// meet window / 128 + 1 query tiles, but the first ones, which hold the sinks, meet them all;
+// those come first in the work order.
+template <int D, bool kWalk, bool kWin>
 __global__ void __launch_bounds__(kThreads, 1)
     fa_bwd_main(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
@@ -296,8 +313,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_3d(kv + C::kTileBytes + c * 16384, &tmV, &sh.kv_full[b], c * 64, jt * kBlock, bh);
         }
         nkv = n + 1;
-        const int i0 = p.causal ? jt : 0;  // first query tile that sees this key tile
-        const int n_it = p.n_tiles - i0;
+        int i0;  // first query tile that sees this key tile
+        const int n_it = query_tiles<kWin>(p, jt, i0);
         const size_t stat_base = (size_t)bh * p.N_pad;
         for (int it = 0; it < n_it; ++it, ++g) {
           const int s = g % C::kStages;
@@ -354,7 +371,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!work_item(p, n, jt, bh)) break;
         const int b = n % C::kKVBufs;
         const uint32_t sK = smem_u32(smem + C::kKOff + b * C::kKVBytes), sV = sK + C::kTileBytes;
-        const int n_it = p.n_tiles - (p.causal ? jt : 0);
+        int i0;
+        const int n_it = query_tiles<kWin>(p, jt, i0);
         if (!(ok = mbar_wait(&sh.kv_full[b], (n / C::kKVBufs) & 1, abort_flag, p.status))) break;
         // the lambdas take the item's step `it`; barriers and buffers go by the CTA's step g0 + it
         auto issue_s = [&](int it) {  // S^T = K_j Q_i^T
@@ -475,11 +493,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int n = 0; ok && (C::kMultiItem || n == 0); ++n) {
     int jt, bh;
     if (!work_item(p, n, jt, bh)) break;
-    const int n_it = p.n_tiles - (p.causal ? jt : 0);
+    int i0;
+    const int n_it = query_tiles<kWin>(p, jt, i0);
     for (int it = 0; it < n_it; ++it) {
       const int g = g0 + it;
       const int s = g % C::kStages;
-      const bool diag = p.causal && it == 0;  // query tile i0 == key tile jt: mask q < key
+      const bool diag = (kWin || p.causal) && it == 0;  // query tile i0 == key tile jt: mask q < key
       const uint32_t tS = tS0 + C::s_col(g);
       const float4* lse4 = reinterpret_cast<const float4*>(smem + C::kLseOff + s * kBlock * 4) + 16 * h;
       const float4* dl4 = reinterpret_cast<const float4*>(smem + C::kDeltaOff + s * kBlock * 4) + 16 * h;
@@ -509,6 +528,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         // query column 64h + j is visible to key row r iff 64h + j >= r
 #pragma unroll
         for (int j = 0; j < 64; ++j) pr[j] = (64 * h + j >= r) ? pr[j] : 0.f;
+      }
+      if constexpr (kWin) {
+        // query columns past the key's window (key jt * 128 + r, queries from it * 128 further
+        // on), unless the key is a sink
+        const int w_hi = r + p.window - it * kBlock - 64 * h;
+        if (w_hi < 64 && jt * kBlock + r >= p.sinks) {
+#pragma unroll
+          for (int j = 0; j < 64; ++j) pr[j] = (j < w_hi) ? pr[j] : 0.f;
+        }
       }
       {
         uint32_t pk[32];
@@ -630,8 +658,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int n = 0; ok && (C::kMultiItem || n == 0); ++n) {
     int jt, bh;
     if (!work_item(p, n, jt, bh)) break;
-    const int i0 = p.causal ? jt : 0;
-    const int n_it = p.n_tiles - i0;
+    int i0;
+    const int n_it = query_tiles<kWin>(p, jt, i0);
     for (int it = 0; it < n_it; ++it) {
       if (!(ok = mbar_wait(&sh.dq_full, (g0 + it) & 1, abort_flag, p.status))) break;
       tc_fence_after();
@@ -713,12 +741,12 @@ Scratch carve_scratch(void* base, int B, int H, int N, int d) {
   return s;
 }
 
-template <int D, bool kWalk>
+template <int D, bool kWalk, bool kWin>
 int launch_main(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tdo,
                 const CUtensorMap& tdq, const fa::bwd::Params& p, cudaStream_t stream) {
   using namespace fa;
   using C = bwd::Cfg<D, kWalk>;
-  auto kern = bwd::fa_bwd_main<D, kWalk>;
+  auto kern = bwd::fa_bwd_main<D, kWalk, kWin>;
   // setmaxnreg.inc waits until the block's launch registers cover the new split: refuse to
   // launch a build whose launch allocation is smaller than the split needs
   constexpr int kSplit = 2 * 128 * bwd::kRegPdS + 128 * bwd::kRegDQ + 128 * bwd::kRegOther;
@@ -741,10 +769,11 @@ int launch_main(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap&
   return check_cuda(cudaGetLastError(), "launch fa_bwd_main");
 }
 
+// window = 0: the mask is `causal`'s; else causal with a window and sinks.
 template <int D>
 int launch_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO, void* dq,
-               void* dk, void* dv, float* delta_out, int B, int H, int N, int causal, float scale,
-               const Scratch& sc, cudaStream_t stream, int stages, fa::DevStatus* status_word = nullptr) {
+               void* dk, void* dv, float* delta_out, int B, int H, int N, int causal, int window,
+               int sinks, float scale, const Scratch& sc, cudaStream_t stream, int stages, fa::DevStatus* status_word = nullptr) {
   using namespace fa;
   const long long rows = (long long)B * H * N;
   int rc;
@@ -778,6 +807,8 @@ int launch_bwd(const void* q, const void* k, const void* v, const void* o, const
   p.N_pad = N_pad;
   p.n_tiles = N_pad / bwd::kBlock;
   p.causal = causal;
+  p.window = window < N ? window : N;
+  p.sinks = sinks < N ? sinks : N;
   p.scale = scale;
   p.scale_log2 = scale * 1.4426950408889634f;
 #ifdef FA_TEST_HOOKS
@@ -791,10 +822,15 @@ int launch_bwd(const void* q, const void* k, const void* v, const void* o, const
   // buffer: one CTA per item.
   constexpr int kItemWalkMaxTiles = 32;
   if constexpr (D == 64) {
-    if (p.n_tiles <= kItemWalkMaxTiles) rc = launch_main<D, true>(tq, tk, tv, tdo, tdq, p, stream);
-    else rc = launch_main<D, false>(tq, tk, tv, tdo, tdq, p, stream);
+    if (p.n_tiles <= kItemWalkMaxTiles)
+      rc = window ? launch_main<D, true, true>(tq, tk, tv, tdo, tdq, p, stream)
+                  : launch_main<D, true, false>(tq, tk, tv, tdo, tdq, p, stream);
+    else
+      rc = window ? launch_main<D, false, true>(tq, tk, tv, tdo, tdq, p, stream)
+                  : launch_main<D, false, false>(tq, tk, tv, tdo, tdq, p, stream);
   } else {
-    rc = launch_main<D, false>(tq, tk, tv, tdo, tdq, p, stream);
+    rc = window ? launch_main<D, false, true>(tq, tk, tv, tdo, tdq, p, stream)
+                : launch_main<D, false, false>(tq, tk, tv, tdo, tdq, p, stream);
   }
   if (rc) return rc;
   }
@@ -814,11 +850,11 @@ extern "C" size_t fa_bwd_workspace_size(int B, int H, int N, int d) {
   return scratch_bytes(B, H, N, d);
 }
 
-extern "C" int fa_bwd_staged(const void* q, const void* k, const void* v, const void* o, const float* lse,
-                             const void* dO, void* dq, void* dk, void* dv, float* delta_out, int B, int H, int N,
-                             int d, int causal, float scale, void* workspace, size_t workspace_bytes, void* stream,
-                             int stages) {
-  fa::NvtxRange nvtx_range("fa_bwd_staged");
+// Argument checks and launches of the backward entry points with a caller's workspace.
+static int bwd_checked(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO,
+                       void* dq, void* dk, void* dv, float* delta_out, int B, int H, int N, int d, int causal,
+                       int window, int sinks, float scale, void* workspace, size_t workspace_bytes, void* stream,
+                       int stages) {
   using namespace fa;
   clear_error();
   int rc;
@@ -839,10 +875,31 @@ extern "C" int fa_bwd_staged(const void* q, const void* k, const void* v, const 
     return set_error(FA_ERR_INVALID_ARG, "workspace too small: %zu bytes given, %zu needed", workspace_bytes, need);
   const Scratch sc = carve_scratch(workspace, B, H, N, d);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return d == 64 ? launch_bwd<64>(q, k, v, o, lse, dO, dq, dk, dv, delta_out, B, H, N, causal ? 1 : 0, scale, sc, s,
-                                  stages)
-                 : launch_bwd<128>(q, k, v, o, lse, dO, dq, dk, dv, delta_out, B, H, N, causal ? 1 : 0, scale, sc, s,
-                                   stages);
+  return d == 64 ? launch_bwd<64>(q, k, v, o, lse, dO, dq, dk, dv, delta_out, B, H, N, causal ? 1 : 0, window,
+                                  sinks, scale, sc, s, stages)
+                 : launch_bwd<128>(q, k, v, o, lse, dO, dq, dk, dv, delta_out, B, H, N, causal ? 1 : 0, window,
+                                   sinks, scale, sc, s, stages);
+}
+
+extern "C" int fa_bwd_staged(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                             const void* dO, void* dq, void* dk, void* dv, float* delta_out, int B, int H, int N,
+                             int d, int causal, float scale, void* workspace, size_t workspace_bytes, void* stream,
+                             int stages) {
+  fa::NvtxRange nvtx_range("fa_bwd_staged");
+  return bwd_checked(q, k, v, o, lse, dO, dq, dk, dv, delta_out, B, H, N, d, causal, 0, 0, scale, workspace,
+                     workspace_bytes, stream, stages);
+}
+
+extern "C" int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                             const void* dO, void* dq, void* dk, void* dv, float* delta_out, int B, int H, int N,
+                             int d, int window, int sinks, float scale, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  fa::NvtxRange nvtx_range("fa_bwd_window");
+  fa::clear_error();
+  const int rc = fa::check_window(window, sinks);
+  if (rc) return rc;
+  return bwd_checked(q, k, v, o, lse, dO, dq, dk, dv, delta_out, B, H, N, d, 1, window, sinks, scale, workspace,
+                     workspace_bytes, stream, FA_BWD_ALL);
 }
 
 extern "C" int fa_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO,
@@ -928,10 +985,10 @@ extern "C" int fa_bwd_noalloc(const void* q, const void* k, const void* v, const
   if ((rc = noalloc_scratch(&scratch, &status))) return rc;
   const Scratch sc = carve_scratch(scratch, B, H, N, d);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return d == 64 ? launch_bwd<64>(q, k, v, o, lse, dO, dq, dk, dv, delta_out, B, H, N, causal ? 1 : 0, scale, sc, s,
-                                  FA_BWD_ALL, status)
-                 : launch_bwd<128>(q, k, v, o, lse, dO, dq, dk, dv, delta_out, B, H, N, causal ? 1 : 0, scale, sc, s,
-                                   FA_BWD_ALL, status);
+  return d == 64 ? launch_bwd<64>(q, k, v, o, lse, dO, dq, dk, dv, delta_out, B, H, N, causal ? 1 : 0, 0, 0, scale,
+                                  sc, s, FA_BWD_ALL, status)
+                 : launch_bwd<128>(q, k, v, o, lse, dO, dq, dk, dv, delta_out, B, H, N, causal ? 1 : 0, 0, 0, scale,
+                                   sc, s, FA_BWD_ALL, status);
 }
 
 extern "C" int fa_bwd_noalloc_status(void* stream, fa_device_report* out) {

@@ -155,6 +155,12 @@ int check_shape(int B, int H, int N, int d) {
   return FA_OK;
 }
 
+int check_window(int window, int sinks) {
+  if (window < 1) return set_error(FA_ERR_INVALID_ARG, "window must be >= 1 (got %d)", window);
+  if (sinks < 0) return set_error(FA_ERR_INVALID_ARG, "sinks must be >= 0 (got %d)", sinks);
+  return FA_OK;
+}
+
 int check_ptr(const void* p, const char* name) {
   if (!p) return set_error(FA_ERR_INVALID_ARG, "%s is NULL", name);
   if (reinterpret_cast<uintptr_t>(p) & 15) return set_error(FA_ERR_INVALID_ARG, "%s is not 16-byte aligned", name);

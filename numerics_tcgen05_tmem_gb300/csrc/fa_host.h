@@ -58,6 +58,7 @@ int make_tmap_f32_bhnd(CUtensorMap* map, const void* base, int BH, int N, int d,
 
 // Common argument checks for [B,H,N,d] problems.
 int check_shape(int B, int H, int N, int d);
+int check_window(int window, int sinks);
 int check_ptr(const void* p, const char* name);
 
 inline size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
