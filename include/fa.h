@@ -290,6 +290,103 @@ int fa_device_status(void* stream);
  */
 int fa_device_report_read(void* stream, fa_device_report* out);
 
+/*
+ * Paged key/value caches (serving; the pages have no counterpart).
+ *
+ * A cache is a pool of pages for K and one for V, [num_pages][Hkv][page_size][d], shared by B
+ * sequences: position t of sequence b lies in page block_table[b * table_stride + t / page_size]
+ * at slot t % page_size.  Pages may be shared by sequences that only read them.
+ *   dtype        : FA_KV_BF16, or FA_KV_E4M3: one byte per element and one FP32 scale per vector
+ *                  (one head's key or value of one token), [num_pages][Hkv][page_size]; the
+ *                  value is code * scale.  fa_kv_append writes power-of-two scales, for which
+ *                  the value is exact in BF16 (from 2^-124 on); otherwise it is rounded where a
+ *                  kernel needs BF16.
+ *   page_stride  : elements of k (and of v) from one page to the next; a page itself is
+ *                  contiguous, so K and V may be interleaved page by page in one buffer.
+ *                  scale_stride: the same for the scales, in floats.
+ *   block_table  : int32 [B][max_pages], rows table_stride apart; entries behind a sequence's
+ *                  last page, and those of pages no query sees, are not used
+ *   kv_len       : int32 [B], keys of each sequence (the new tokens included)
+ * Every pointer is a DEVICE pointer owned by the caller; k, v, k_scale, v_scale are 16-byte
+ * aligned.  page_size is 16, 32, 64, 128 or 256; d is 64 or 128; page_stride keeps 16-byte
+ * alignment and scale_stride is a multiple of 4.  Slots behind a sequence's last key may hold
+ * anything (NaN included).
+ *
+ * Packed rows: new tokens are [T, heads, d] with sequence b's at rows q_indptr[b] ..
+ * q_indptr[b + 1] - 1 (int32 [B + 1] on the device, not decreasing); they are the last
+ * positions of the sequence, kv_len[b] - n .. kv_len[b] - 1.  Rows behind the last sequence
+ * (padding of a captured batch) are neither read nor written.
+ *
+ * The lengths, offsets and table are read on the device: a captured call follows them.  An
+ * entry that is out of range (a page outside the pool, a length beyond the table) is recorded as
+ * FA_ERR_DEVICE_BOUNDS (fa_device_status) and not followed; the results of that sequence are
+ * then undefined, memory outside the tensors is never touched.
+ */
+enum { FA_KV_BF16 = 0, FA_KV_E4M3 = 1 };
+
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale; /* FA_KV_E4M3 only */
+  float* v_scale; /* FA_KV_E4M3 only */
+  int64_t page_stride;
+  int64_t scale_stride;
+  const int32_t* block_table;
+  int64_t table_stride;
+  const int32_t* kv_len;
+  int32_t B, Hkv, d, page_size, num_pages, max_pages, dtype;
+} fa_paged_kv;
+
+/*
+ * fa_kv_append -- write T new tokens' keys and values into the cache.
+ *   k_new, v_new : BF16 [T, Hkv, d], tokens new_stride elements apart (a multiple of 8, at least
+ *                  Hkv * d: slices of a fused projection need no copy)
+ *   q_indptr     : int32 [B + 1], see above; kv_len already counts the new tokens
+ * E4M3 caches: scale = the least power of two (>= 2^-126) with max|x| <= 448 scale, 1 for a zero
+ * vector; code = E4M3(x / scale), rounded to nearest even (magnitudes above
+ * 1.875 2^127, whose value would overflow, are stored as that).  A vector with a NaN or an Inf is
+ * stored with a NaN scale and reads back as NaN.
+ * Two tokens written to one slot in the same call race.  Returns FA_OK, FA_ERR_INVALID_ARG,
+ * FA_ERR_UNSUPPORTED or FA_ERR_CUDA; T = 0 launches nothing.
+ */
+int fa_kv_append(const fa_paged_kv* kv, const void* k_new, const void* v_new, int64_t new_stride,
+                 const int32_t* q_indptr, int T, void* stream);
+
+/*
+ * fa_kv_read -- read sequences back as packed BF16 rows, E4M3 values dequantised.
+ *   kv_indptr    : int32 [B + 1]: sequence b's positions 0, 1, ... go to rows kv_indptr[b],
+ *                  kv_indptr[b] + 1, ... up to kv_indptr[b + 1] or its length
+ *   k_out, v_out : BF16 [rows, Hkv, d], contiguous, 16-byte aligned; other rows stay as they were
+ * Returns FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED or FA_ERR_CUDA; rows = 0 launches nothing.
+ */
+int fa_kv_read(const fa_paged_kv* kv, const int32_t* kv_indptr, void* k_out, void* v_out, int rows, void* stream);
+
+/*
+ * fa_fwd_paged -- attention of each sequence's newest tokens (one, or a chunk) over its cache.
+ *   kv       : the cache; the new tokens' keys and values are already in it (fa_kv_append)
+ *   q        : BF16 [T, Hq, d], tokens q_stride elements apart (a multiple of 8, at least Hq * d);
+ *              Hq is a multiple of kv->Hkv, at most 128 times it; query head i uses kv head
+ *              i / (Hq / Hkv)
+ *   q_indptr : int32 [B + 1], the sequences' packed rows
+ *   max_q    : at least the largest number of new tokens of a sequence
+ *   o        : BF16 [T, Hq, d], contiguous;  lse: FP32 [T, Hq], or NULL (not written)
+ *   window   : 0 = none; else the token at position p sees the keys p - window < j <= p and the
+ *              first `sinks` keys; without a window every key j <= p
+ * A row that sees no key (a length shorter than the new tokens) gives O = 0 and LSE = -inf.
+ * Pages of which no new token sees a key are not read.  A key that some but not all rows of a tile
+ * see must have finite values, as in the dense entry points (0 * Inf = NaN).
+ * workspace: device scratch of at least fa_fwd_paged_workspace_size(T, B, max_q, Hq, Hkv, d,
+ * max_pages * page_size) bytes, 256-byte aligned (NULL where that is 0); its contents on entry do
+ * not matter.  Calls that may overlap need workspaces of their own.
+ * Results do not depend on timing: the same call on the same data gives the same bits.
+ * Returns FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED or FA_ERR_CUDA; T = 0 launches nothing.
+ */
+size_t fa_fwd_paged_workspace_size(int T, int B, int max_q, int Hq, int Hkv, int d, int max_kv);
+
+int fa_fwd_paged(const fa_paged_kv* kv, const void* q, int64_t q_stride, const int32_t* q_indptr, int T, int max_q,
+                 int Hq, void* o, float* lse, int window, int sinks, float scale, void* workspace,
+                 size_t workspace_bytes, void* stream);
+
 /* Message for the last non-OK return on the calling thread ("" if none). */
 const char* fa_last_error(void);
 

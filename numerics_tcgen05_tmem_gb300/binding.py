@@ -31,7 +31,8 @@ FA_DEVFLAG_TIMEOUT, FA_DEVFLAG_BOUNDS, FA_DEVFLAG_NONFINITE = 1, 2, 4
 # every symbol include/fa.h declares
 EXPORTS = ("fa_fwd", "fa_fwd_window", "fa_fwd_fp8", "fa_quantize_fp8", "fa_bwd", "fa_bwd_window", "fa_bwd_staged",
            "fa_bwd_noalloc", "fa_bwd_noalloc_status", "fa_bwd_workspace_size", "fa_device_status",
-           "fa_device_report_read", "fa_last_error", "fa_version")
+           "fa_device_report_read", "fa_last_error", "fa_version", "fa_kv_append", "fa_kv_read",
+           "fa_fwd_paged", "fa_fwd_paged_workspace_size")
 
 # size of the fixed device scratch behind fa_bwd_noalloc (FA_NOALLOC_SCRATCH_BYTES in fa.h)
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
@@ -49,6 +50,19 @@ class RowStats(ctypes.Structure):
     _fields_ = [("row_max_raw", ctypes.c_void_p), ("row_ties", ctypes.c_void_p),
                 ("row_branch", ctypes.c_void_p), ("row_ones", ctypes.c_void_p),
                 ("row_min_raw", ctypes.c_void_p)]
+
+
+# element types of a paged cache (fa_paged_kv.dtype)
+FA_KV_BF16, FA_KV_E4M3 = 0, 1
+
+
+class PagedKV(ctypes.Structure):
+    """fa_paged_kv: a paged key/value cache with its block table and lengths."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("scale_stride", ctypes.c_int64),
+                ("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("kv_len", ctypes.c_void_p),
+                ("B", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("d", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
 class DeviceReport(ctypes.Structure):
@@ -90,6 +104,14 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.fa_bwd_window.restype = ci
     L.fa_bwd_staged.argtypes = L.fa_bwd.argtypes + [ci]
     L.fa_bwd_staged.restype = ci
+    L.fa_kv_append.argtypes = [ctypes.POINTER(PagedKV), vp, vp, ctypes.c_int64, vp, ci, vp]
+    L.fa_kv_append.restype = ci
+    L.fa_kv_read.argtypes = [ctypes.POINTER(PagedKV), vp, vp, vp, ci, vp]
+    L.fa_kv_read.restype = ci
+    L.fa_fwd_paged_workspace_size.argtypes = [ci] * 7
+    L.fa_fwd_paged_workspace_size.restype = cs
+    L.fa_fwd_paged.argtypes = [ctypes.POINTER(PagedKV), vp, ctypes.c_int64, vp, ci, ci, ci, vp, vp, ci, ci, cf, vp, cs, vp]
+    L.fa_fwd_paged.restype = ci
     L.fa_bwd_noalloc.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, cf, vp]
     L.fa_bwd_noalloc.restype = ci
     L.fa_device_status.argtypes = [vp]
@@ -170,6 +192,10 @@ def fa_fwd_fp8(q8, k8, v8, descale, o, lse, causal: bool, scale: float, stable: 
 
 def fa_quantize_fp8(x, x8, descale, stream=None) -> int:
     return load().fa_quantize_fp8(_ptr(x), int(x.numel()), _ptr(x8), _ptr(descale), _stream(stream))
+
+
+def fa_fwd_paged_workspace_size(T: int, B: int, max_q: int, Hq: int, Hkv: int, d: int, max_kv: int) -> int:
+    return int(load().fa_fwd_paged_workspace_size(T, B, max_q, Hq, Hkv, d, max_kv))
 
 
 def fa_bwd_workspace_size(B: int, H: int, N: int, d: int) -> int:
@@ -309,6 +335,141 @@ def backward(q, k, v, o, lse, do, causal: bool = True, scale=None, workspace=Non
     else:
         _check(fa_bwd_window(q, k, v, o, lse, do, dq, dk, dv, delta, window, sinks, scale, workspace, stream))
     return (dq, dk, dv, delta) if want_delta else (dq, dk, dv)
+
+
+# ----------------------------------------------------------------- paged key/value caches
+
+def _int32(t, n, name, device):
+    if not (t.dtype == torch.int32 and t.dim() == 1 and t.is_contiguous() and t.device == device):
+        raise ValueError(f"{name} must be a contiguous int32 vector on the cache's device")
+    if t.shape[0] != n:
+        raise ValueError(f"{name} must have {n} entries (got {t.shape[0]})")
+
+
+def _paged(k, v, table, kv_len, k_scale, v_scale):
+    """The fa_paged_kv of a cache's tensors (shapes, types and strides checked)."""
+    if not (k.is_cuda and k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype and k.device == v.device):
+        raise ValueError("expected CUDA cache tensors of one shape [pages, Hkv, page_size, d] and one type")
+    P, H, S, d = k.shape
+    if k.stride() != v.stride() or k.stride()[1:] != (S * d, d, 1):
+        raise ValueError("cache pages must be contiguous, with the same page stride for K and V")
+    if not (table.dtype == torch.int32 and table.dim() == 2 and table.device == k.device and table.stride(1) == 1):
+        raise ValueError("block_table must be an int32 tensor [B, max_pages] on the cache's device, rows contiguous")
+    _int32(kv_len, table.shape[0], "kv_len", k.device)
+    out = PagedKV(k.data_ptr(), v.data_ptr(), None, None, max(k.stride(0), H * S * d), 0, table.data_ptr(),
+                  max(table.stride(0), table.shape[1]), kv_len.data_ptr(), table.shape[0], H, d, S, P, table.shape[1],
+                  FA_KV_BF16)
+    if k.dtype == torch.bfloat16:
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("a bfloat16 cache has no scales")
+        return out
+    if k.dtype not in (torch.uint8, torch.float8_e4m3fn):
+        raise ValueError("cache tensors must be bfloat16, or uint8 (or float8_e4m3fn) E4M3 codes")
+    for s in (k_scale, v_scale):
+        if s is None or not (s.dtype == torch.float32 and s.shape == (P, H, S) and s.device == k.device and
+                             s.stride()[1:] == (S, 1) and s.stride(0) == k_scale.stride(0)):
+            raise ValueError("an E4M3 cache needs float32 k_scale and v_scale [pages, Hkv, page_size], pages "
+                             "contiguous, with the same page stride")
+    out.k_scale, out.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
+    out.scale_stride, out.dtype = max(k_scale.stride(0), H * S), FA_KV_E4M3
+    return out
+
+
+def _check_rows(x, heads, d, device, name):
+    if not (x.dtype == torch.bfloat16 and x.dim() == 3 and x.device == device and x.shape[1:] == (heads, d)):
+        raise ValueError(f"{name} must be a CUDA bfloat16 tensor [rows, {heads}, {d}] on the cache's device")
+    if x.shape[0] and x.stride()[1:] != (d, 1):
+        raise ValueError(f"{name}: a row's heads must be contiguous")
+
+
+def _row_stride(x):
+    return max(x.stride(0), x.shape[1] * x.shape[2])   # one row's stride may be anything
+
+
+def kv_append(k_new, v_new, k_cache, v_cache, block_table, kv_len, q_indptr, k_scale=None, v_scale=None, stream=None):
+    """Write new tokens into a paged cache (in place).
+
+    k_new, v_new: bfloat16 [T, Hkv, d], rows strided alike; sequence b's are the rows
+    q_indptr[b] .. q_indptr[b + 1] - 1 and become the positions kv_len[b] - n .. kv_len[b] - 1.
+    k_cache, v_cache: [pages, Hkv, page_size, d], bfloat16, or E4M3 codes (uint8 or float8_e4m3fn)
+    with float32 scales [pages, Hkv, page_size].  block_table: int32 [B, max_pages].
+    """
+    kv = _paged(k_cache, v_cache, block_table, kv_len, k_scale, v_scale)
+    _check_rows(k_new, kv.Hkv, kv.d, k_cache.device, "k_new")
+    _check_rows(v_new, kv.Hkv, kv.d, k_cache.device, "v_new")
+    if k_new.shape != v_new.shape or _row_stride(k_new) != _row_stride(v_new):
+        raise ValueError("k_new and v_new must have the same rows and row stride")
+    _int32(q_indptr, kv.B + 1, "q_indptr", k_cache.device)
+    if k_new.shape[0]:
+        with torch.cuda.device(k_cache.device):
+            _check(load().fa_kv_append(ctypes.byref(kv), _ptr(k_new), _ptr(v_new), _row_stride(k_new), _ptr(q_indptr),
+                                       k_new.shape[0], _stream(stream)))
+
+
+def kv_read(k_cache, v_cache, block_table, kv_len, kv_indptr, rows, k_scale=None, v_scale=None, out=None, stream=None):
+    """Read a paged cache back: (k, v) bfloat16 [rows, Hkv, d].
+
+    Sequence b's positions 0, 1, ... go to the rows kv_indptr[b], kv_indptr[b] + 1, ..., up to
+    kv_indptr[b + 1] or kv_len[b].  Other rows stay as they were (out: the pair of tensors to write
+    to) or are not defined (fresh tensors).
+    """
+    kv = _paged(k_cache, v_cache, block_table, kv_len, k_scale, v_scale)
+    _int32(kv_indptr, kv.B + 1, "kv_indptr", k_cache.device)
+    if out is None:
+        out = tuple(torch.empty((rows, kv.Hkv, kv.d), device=k_cache.device, dtype=torch.bfloat16) for _ in range(2))
+    k, v = out
+    for t in out:
+        _check_rows(t, kv.Hkv, kv.d, k_cache.device, "out")
+        if t.shape[0] != rows or not t.is_contiguous():
+            raise ValueError("out tensors must be contiguous with `rows` rows")
+    if rows:
+        with torch.cuda.device(k_cache.device):
+            _check(load().fa_kv_read(ctypes.byref(kv), _ptr(kv_indptr), _ptr(k), _ptr(v), int(rows), _stream(stream)))
+    return k, v
+
+
+def forward_paged(q, k_cache, v_cache, block_table, kv_len, q_indptr, max_q, k_scale=None, v_scale=None, scale=None,
+                  window=None, sinks: int = 0, out=None, lse=None, workspace=None, stream=None):
+    """Attention of each sequence's newest tokens over its paged cache: (o, lse).
+
+    q: bfloat16 [T, Hq, d] (rows may be strided); sequence b's new tokens are the rows q_indptr[b] ..
+    q_indptr[b + 1] - 1 and the last positions of its cache, which already holds their keys and
+    values (kv_append).  max_q: at least the largest number of new tokens of a sequence.  Hq is a
+    multiple of the cache's heads.  With a window, the token at position p sees the keys
+    p - window < j <= p and the first ``sinks`` keys; otherwise every key j <= p.
+    out, lse: tensors to write to ([T, Hq, d] bfloat16, [T, Hq] float32); rows behind the last
+    sequence stay as they were (undefined in fresh tensors).
+    """
+    kv = _paged(k_cache, v_cache, block_table, kv_len, k_scale, v_scale)
+    _check_window(True, window, sinks)
+    if window is not None and window < 1:
+        raise ValueError("window must be >= 1 (None: no window)")
+    dev, d = k_cache.device, kv.d
+    if q.dim() != 3:
+        raise ValueError("q must be [T, Hq, d]")
+    T, Hq = q.shape[0], q.shape[1]
+    _check_rows(q, Hq, d, dev, "q")
+    _int32(q_indptr, kv.B + 1, "q_indptr", dev)
+    if out is None:
+        out = torch.empty((T, Hq, d), device=dev, dtype=torch.bfloat16)
+    elif not (out.dtype == torch.bfloat16 and out.shape == q.shape and out.is_contiguous() and out.device == dev):
+        raise ValueError("out must be a contiguous bfloat16 tensor of q's shape")
+    if lse is None:
+        lse = torch.empty((T, Hq), device=dev, dtype=torch.float32)
+    elif not (lse.dtype == torch.float32 and lse.shape == q.shape[:2] and lse.is_contiguous() and lse.device == dev):
+        raise ValueError("lse must be a contiguous float32 tensor [T, Hq]")
+    if T == 0:
+        return out, lse
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    with torch.cuda.device(dev):
+        if workspace is None:
+            n = fa_fwd_paged_workspace_size(T, kv.B, max_q, Hq, kv.Hkv, d, kv.max_pages * kv.page_size)
+            workspace = torch.empty(n, device=dev, dtype=torch.uint8)
+        nbytes = workspace.numel() * workspace.element_size()
+        _check(load().fa_fwd_paged(ctypes.byref(kv), _ptr(q), _row_stride(q), _ptr(q_indptr), T, int(max_q), Hq,
+                                   _ptr(out), _ptr(lse), int(window or 0), int(sinks), float(scale),
+                                   _ptr(workspace) if nbytes else None, nbytes, _stream(stream)))
+    return out, lse
 
 
 def device_status(stream=None):

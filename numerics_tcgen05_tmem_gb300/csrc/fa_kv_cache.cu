@@ -1,0 +1,277 @@
+// Writing new tokens' keys and values into a paged cache (fa_kv_append) and reading a cache back
+// as packed BF16 rows (fa_kv_read).
+//
+// Both move each vector (one head's key or value of one token, d elements) once: bandwidth work.
+// A warp takes one token and walks its 2 Hkv vectors, several at a time with 16 bytes per lane of
+// the BF16 side, so all of a token's loads are in flight together while its page is looked up.
+// E4M3 caches: scale = least power of two with max|x| <= 448 scale, code = E4M3(x / scale) (the
+// division is exact, one rounding to nearest even), value = code * scale (exact in BF16, whose 8
+// significant bits hold the code's 4; only with scales under 2^-124 do the smallest codes fall
+// between BF16's subnormals and are rounded).  A vector that holds a NaN or an Inf gets a NaN scale and
+// reads back as NaN.
+#include "paged.cuh"
+
+namespace fa {
+namespace paged {
+
+constexpr int kThreads = 256;
+
+// Reduces a bit-pattern maximum over the `kLanes` lanes that hold one vector.
+template <int kLanes>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t m) {
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+
+__device__ __forceinline__ uint32_t amax8(const uint4& u) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = max(m, max((w[i] & 0x7FFFu) << 16, w[i] & 0x7FFF0000u));
+  return m;
+}
+
+__device__ __forceinline__ uint32_t quant4(uint32_t w0, uint32_t w1, float inv) {
+  return pack_e4m3x4(__uint_as_float(w0 << 16) * inv, __uint_as_float(w0 & 0xFFFF0000u) * inv,
+                     __uint_as_float(w1 << 16) * inv, __uint_as_float(w1 & 0xFFFF0000u) * inv);
+}
+
+// Magnitudes above 1.875 * 2^127 to that value: with the largest scale their code would be
+// 256 = 2^8, whose value 2^128 overflows.
+__device__ __forceinline__ uint4 clamp_top(const uint4& u) {
+  uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = min(w[i] & 0x7FFFu, 0x7F70u), hi = min(w[i] & 0x7FFF0000u, 0x7F700000u);
+    w[i] = (w[i] & 0x80008000u) | lo | hi;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// k_new, v_new: [T, Hkv, d] with `stride` elements between tokens.
+template <int D, bool kFp8>
+__global__ void __launch_bounds__(kThreads) kv_append_kernel(const Cache c, const __nv_bfloat16* __restrict__ k_new,
+                                                             const __nv_bfloat16* __restrict__ v_new,
+                                                             long long stride, const int32_t* __restrict__ q_indptr,
+                                                             int T) {
+  constexpr int kLanes = D / 8;           // lanes per vector
+  constexpr int kVecs = 32 / kLanes;      // vectors per warp and step
+  constexpr int kUnroll = 8;              // steps in flight
+  const int lane = threadIdx.x % 32;
+  const int token = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+  if (token >= T) return;
+  const int b = find_sequence(q_indptr, c.B, token);
+  if (b >= c.B) return;
+  const int pos = __ldg(c.kv_len + b) - __ldg(q_indptr + b + 1) + token;
+  const int page = find_page(c, b, pos, kSitePagedAppend);
+  if (page < 0) return;
+  const int page_size = 1 << c.page_shift, slot = pos & (page_size - 1);
+  const int sub = lane / kLanes, col = (lane % kLanes) * 8;
+  const int n = 2 * c.Hkv;  // vector i: head i / 2, K where i is even
+  for (int i0 = 0; i0 < n; i0 += kVecs * kUnroll) {
+    uint4 x[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int i = i0 + u * kVecs + sub;
+      x[u] = make_uint4(0, 0, 0, 0);
+      if (i < n)
+        x[u] = __ldg(reinterpret_cast<const uint4*>(((i & 1) ? v_new : k_new) + token * stride + (i >> 1) * D + col));
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int i = i0 + u * kVecs + sub;
+      if (i0 + u * kVecs >= n) break;  // the same for the whole warp
+      const int h = i >> 1;
+      const long long row = (long long)h * page_size + slot;
+      if constexpr (!kFp8) {
+        __nv_bfloat16* base = static_cast<__nv_bfloat16*>((i & 1) ? c.v : c.k);
+        if (i < n) *reinterpret_cast<uint4*>(base + page * c.page_stride + row * D + col) = x[u];
+      } else {
+        const uint32_t amax = lanes_max<kLanes>(amax8(x[u]));
+        float scale = 1.f, inv = 1.f;
+        int e = 0;
+        if (amax != 0) {
+          e = scale_exponent(amax);
+          scale = __uint_as_float((uint32_t)(e + 127) << 23);
+          inv = __uint_as_float((uint32_t)(127 - e) << 23);
+        }
+        if (e == kMaxScaleExp) x[u] = clamp_top(x[u]);
+        uint2 q = make_uint2(quant4(x[u].x, x[u].y, inv), quant4(x[u].z, x[u].w, inv));
+        if (amax >= 0x7F800000u) {  // Inf or NaN in the vector
+          scale = __uint_as_float(0x7FC00000u);
+          q = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+        }
+        if (i < n) {
+          uint8_t* base = static_cast<uint8_t*>((i & 1) ? c.v : c.k);
+          *reinterpret_cast<uint2*>(base + page * c.page_stride + row * D + col) = q;
+          if (col == 0) ((i & 1) ? c.v_scale : c.k_scale)[page * c.scale_stride + row] = scale;
+        }
+      }
+    }
+  }
+}
+
+// k_out, v_out: [rows, Hkv, d] contiguous.
+template <int D, bool kFp8>
+__global__ void __launch_bounds__(kThreads) kv_read_kernel(const Cache c, const int32_t* __restrict__ kv_indptr,
+                                                           __nv_bfloat16* __restrict__ k_out,
+                                                           __nv_bfloat16* __restrict__ v_out, int rows) {
+  constexpr int kElems = kFp8 ? 16 : 8;   // elements per lane: 16 bytes of the cache
+  constexpr int kLanes = D / kElems;
+  constexpr int kVecs = 32 / kLanes;
+  constexpr int kUnroll = kFp8 ? 4 : 8;
+  const int lane = threadIdx.x % 32;
+  const int r = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+  if (r >= rows) return;
+  const int b = find_sequence(kv_indptr, c.B, r);
+  if (b >= c.B) return;
+  const int pos = r - __ldg(kv_indptr + b);
+  if (pos >= __ldg(c.kv_len + b)) return;  // past the sequence: the row stays as it was
+  const int page = find_page(c, b, pos, kSitePagedRead);
+  if (page < 0) return;
+  const int page_size = 1 << c.page_shift, slot = pos & (page_size - 1);
+  const int sub = lane / kLanes, col = (lane % kLanes) * kElems;
+  const int n = 2 * c.Hkv;
+  constexpr int kBytes = kFp8 ? 1 : 2;
+  for (int i0 = 0; i0 < n; i0 += kVecs * kUnroll) {
+    uint4 x[kUnroll];
+    float sc[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int i = i0 + u * kVecs + sub;
+      x[u] = make_uint4(0, 0, 0, 0);
+      sc[u] = 0.f;
+      if (i < n) {
+        const long long row = (long long)(i >> 1) * page_size + slot;
+        const uint8_t* base = static_cast<const uint8_t*>((i & 1) ? c.v : c.k);
+        x[u] = __ldg(reinterpret_cast<const uint4*>(base + (page * c.page_stride + row * D + col) * kBytes));
+        if constexpr (kFp8) sc[u] = __ldg(((i & 1) ? c.v_scale : c.k_scale) + page * c.scale_stride + row);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int i = i0 + u * kVecs + sub;
+      if (i >= n) break;
+      uint4* dst = reinterpret_cast<uint4*>(((i & 1) ? v_out : k_out) + ((long long)r * c.Hkv + (i >> 1)) * D + col);
+      if constexpr (!kFp8) {
+        dst[0] = x[u];
+      } else {
+        const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+        uint32_t o[8];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const float2 lo = e4m3x2_to_float2(w[t]), hi = e4m3x2_to_float2(w[t] >> 16);
+          o[2 * t] = pack_bf16x2(lo.x * sc[u], lo.y * sc[u]);
+          o[2 * t + 1] = pack_bf16x2(hi.x * sc[u], hi.y * sc[u]);
+        }
+        dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+    }
+  }
+}
+
+int check_cache(const fa_paged_kv* kv, Cache* c) {
+  if (!kv) return set_error(FA_ERR_INVALID_ARG, "kv is NULL");
+  if (kv->B < 1 || kv->Hkv < 1) return set_error(FA_ERR_INVALID_ARG, "B, Hkv must be >= 1 (got %d, %d)", kv->B, kv->Hkv);
+  if (kv->d != 64 && kv->d != 128)
+    return set_error(FA_ERR_UNSUPPORTED, "head dim d=%d not supported (64 or 128)", kv->d);
+  if (kv->page_size < 16 || kv->page_size > 256 || (kv->page_size & (kv->page_size - 1)))
+    return set_error(FA_ERR_UNSUPPORTED, "page_size=%d not supported (16, 32, 64, 128 or 256)", kv->page_size);
+  if (kv->num_pages < 1 || kv->max_pages < 1)
+    return set_error(FA_ERR_INVALID_ARG, "num_pages, max_pages must be >= 1 (got %d, %d)", kv->num_pages, kv->max_pages);
+  // positions, and differences of two of them, stay within 32 bits
+  if ((long long)kv->max_pages * kv->page_size > (1ll << 30))
+    return set_error(FA_ERR_INVALID_ARG, "max_pages * page_size must be <= 2^30");
+  if (kv->dtype != FA_KV_BF16 && kv->dtype != FA_KV_E4M3)
+    return set_error(FA_ERR_UNSUPPORTED, "cache dtype %d not supported (FA_KV_BF16 or FA_KV_E4M3)", kv->dtype);
+  int rc;
+  if ((rc = check_ptr(kv->k, "kv->k")) || (rc = check_ptr(kv->v, "kv->v"))) return rc;
+  const long long page = (long long)kv->Hkv * kv->page_size;
+  const int align = kv->dtype == FA_KV_E4M3 ? 16 : 8;  // 16 bytes
+  if (kv->page_stride < page * kv->d || kv->page_stride % align)
+    return set_error(FA_ERR_INVALID_ARG, "page_stride %lld must be a multiple of %d and at least Hkv*page_size*d = %lld",
+                     (long long)kv->page_stride, align, page * kv->d);
+  if (kv->dtype == FA_KV_E4M3) {
+    if ((rc = check_ptr(kv->k_scale, "kv->k_scale")) || (rc = check_ptr(kv->v_scale, "kv->v_scale"))) return rc;
+    if (kv->scale_stride < page || kv->scale_stride % 4)
+      return set_error(FA_ERR_INVALID_ARG, "scale_stride %lld must be a multiple of 4 and at least Hkv*page_size = %lld",
+                       (long long)kv->scale_stride, page);
+  }
+  if (!kv->block_table || (reinterpret_cast<uintptr_t>(kv->block_table) & 3))
+    return set_error(FA_ERR_INVALID_ARG, "block_table must be a 4-byte aligned device pointer");
+  if (kv->table_stride < kv->max_pages)
+    return set_error(FA_ERR_INVALID_ARG, "table_stride %lld is less than max_pages %d", (long long)kv->table_stride,
+                     kv->max_pages);
+  if (!kv->kv_len || (reinterpret_cast<uintptr_t>(kv->kv_len) & 3))
+    return set_error(FA_ERR_INVALID_ARG, "kv_len must be a 4-byte aligned device pointer");
+  int shift = 4;
+  while ((1 << shift) < kv->page_size) ++shift;
+  *c = Cache{kv->k,     kv->v,     kv->k_scale, kv->v_scale, kv->page_stride, kv->scale_stride, kv->block_table,
+             kv->table_stride, kv->kv_len, kv->B, kv->Hkv, shift, kv->num_pages, kv->max_pages, nullptr};
+  return FA_OK;
+}
+
+// An offsets array of B + 1 entries on the device.
+static int check_indptr(const int32_t* p, const char* name) {
+  if (!p || (reinterpret_cast<uintptr_t>(p) & 3))
+    return set_error(FA_ERR_INVALID_ARG, "%s must be a 4-byte aligned device pointer", name);
+  return FA_OK;
+}
+
+}  // namespace paged
+}  // namespace fa
+
+extern "C" int fa_kv_append(const fa_paged_kv* kv, const void* k_new, const void* v_new, int64_t new_stride,
+                            const int32_t* q_indptr, int T, void* stream) {
+  fa::NvtxRange nvtx_range("fa_kv_append");
+  using namespace fa;
+  clear_error();
+  paged::Cache c;
+  int rc;
+  if ((rc = paged::check_cache(kv, &c))) return rc;
+  if (T < 0) return set_error(FA_ERR_INVALID_ARG, "T must be >= 0 (got %d)", T);
+  if ((rc = check_ptr(k_new, "k_new")) || (rc = check_ptr(v_new, "v_new")) ||
+      (rc = paged::check_indptr(q_indptr, "q_indptr")))
+    return rc;
+  if (new_stride < (int64_t)kv->Hkv * kv->d || new_stride % 8)
+    return set_error(FA_ERR_INVALID_ARG, "new_stride %lld must be a multiple of 8 and at least Hkv*d = %d",
+                     (long long)new_stride, kv->Hkv * kv->d);
+  if (T == 0) return FA_OK;
+  c.status = device_status_word();
+  if (!c.status) return set_error(FA_ERR_CUDA, "could not allocate the device status record");
+  const unsigned grid = (unsigned)((T + paged::kThreads / 32 - 1) / (paged::kThreads / 32));
+  const __nv_bfloat16 *k = static_cast<const __nv_bfloat16*>(k_new), *v = static_cast<const __nv_bfloat16*>(v_new);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool fp8 = kv->dtype == FA_KV_E4M3;
+  auto kern = kv->d == 64 ? (fp8 ? paged::kv_append_kernel<64, true> : paged::kv_append_kernel<64, false>)
+                          : (fp8 ? paged::kv_append_kernel<128, true> : paged::kv_append_kernel<128, false>);
+  kern<<<grid, paged::kThreads, 0, s>>>(c, k, v, new_stride, q_indptr, T);
+  return check_cuda(cudaGetLastError(), "launch fa_kv_append");
+}
+
+extern "C" int fa_kv_read(const fa_paged_kv* kv, const int32_t* kv_indptr, void* k_out, void* v_out, int rows,
+                          void* stream) {
+  fa::NvtxRange nvtx_range("fa_kv_read");
+  using namespace fa;
+  clear_error();
+  paged::Cache c;
+  int rc;
+  if ((rc = paged::check_cache(kv, &c))) return rc;
+  if (rows < 0) return set_error(FA_ERR_INVALID_ARG, "rows must be >= 0 (got %d)", rows);
+  if ((rc = check_ptr(k_out, "k_out")) || (rc = check_ptr(v_out, "v_out")) ||
+      (rc = paged::check_indptr(kv_indptr, "kv_indptr")))
+    return rc;
+  if (rows == 0) return FA_OK;
+  c.status = device_status_word();
+  if (!c.status) return set_error(FA_ERR_CUDA, "could not allocate the device status record");
+  const unsigned grid = (unsigned)((rows + paged::kThreads / 32 - 1) / (paged::kThreads / 32));
+  __nv_bfloat16 *k = static_cast<__nv_bfloat16*>(k_out), *v = static_cast<__nv_bfloat16*>(v_out);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool fp8 = kv->dtype == FA_KV_E4M3;
+  auto kern = kv->d == 64 ? (fp8 ? paged::kv_read_kernel<64, true> : paged::kv_read_kernel<64, false>)
+                          : (fp8 ? paged::kv_read_kernel<128, true> : paged::kv_read_kernel<128, false>);
+  kern<<<grid, paged::kThreads, 0, s>>>(c, kv_indptr, k, v, rows);
+  return check_cuda(cudaGetLastError(), "launch fa_kv_read");
+}

@@ -1,0 +1,802 @@
+// Paged attention for chunks of new tokens: sequences with more rows for a kv head than the few-rows
+// kernel takes.
+//
+// The products dominate here, so they run on the tensor core as in the dense forward: two tiles of
+// 128 rows per CTA against a shared stream of 128-key blocks, S and O in tensor memory, P~ fed back
+// from tensor memory, one softmax warpgroup per tile, a correction warpgroup, one MMA thread.
+//   * A tile's rows are (token, head of the group) pairs of one kv head, 128 / group tokens of
+//     `group` rows each: TMA brings Q in that order from the packed rows (a box of group heads by
+//     tokens), and K and V are read once for the whole group.  With a group that does not divide 128
+//     the last rows of a tile stay unused.
+//   * K and V blocks come page by page (BF16), or through a warpgroup that reads E4M3 codes from the
+//     pages, multiplies them by their vector's scale and writes the BF16 operand tiles (exact for
+//     power-of-two scales).  The conversion runs beside the softmax and needs no buffer in memory.
+//   * V rows that no row of the CTA sees (slots behind the sequence's end, keys before the window)
+//     may hold anything, and 0 * NaN is NaN: they are zeroed in shared memory before the product.
+//   * Few long rows would leave SMs idle: the host then splits a tile's keys over several CTAs, whose
+//     normalised FP32 results fa_chunk_combine joins (in order, whatever the timing).
+// Softmax: running maximum and sum in FP32 per row (one thread per row), P~ rounded to BF16 for the
+// product as the tensor core takes it.  Plain shift: the stabilised rule guards the training
+// backward, and the output does not depend on the shift.
+#include "paged_attn.cuh"
+
+namespace fa {
+namespace paged {
+
+constexpr int kM = 128;             // rows per tile (TMEM lanes)
+constexpr int kN = 128;             // keys per block
+constexpr int kStages = 2;
+constexpr int kSplitSteps = 4;      // fewest key blocks worth a split of their own
+
+template <int D, bool kFp8>
+struct ChunkCfg {
+  static constexpr int kThreads = kFp8 ? 640 : 512;
+  static constexpr int kMmaWarp = 12, kLoadWarp = 13, kGuardWarp = 14, kConvertWarp = 16;
+  // registers per thread after the launch: softmax, correction, MMA/TMA, conversion
+  static constexpr int kRegLaunch = kFp8 ? 96 : 128;
+  static constexpr int kRegSoftmax = kFp8 ? 160 : 176, kRegCorr = kFp8 ? 40 : 96, kRegOther = kFp8 ? 32 : 56,
+                       kRegConvert = 88;
+  static constexpr int kSplit =
+      256 * kRegSoftmax + 128 * kRegCorr + 128 * kRegOther + (kFp8 ? 128 * kRegConvert : 0);
+  static_assert(kSplit <= kThreads * kRegLaunch, "register split exceeds the launch allocation");
+  static constexpr int kAtoms = D / 64;              // 128-byte column blocks of a BF16 tile
+  static constexpr int kAtomBlock = 128 * 128;       // bytes of one
+  static constexpr int kTileBytes = kAtoms * kAtomBlock;
+  static constexpr int kQOff = 0, kKOff = 2 * kTileBytes, kVOff = kKOff + kStages * kTileBytes;
+  static constexpr int kSmemBytes = kVOff + kStages * kTileBytes + 1024;
+  static constexpr uint32_t kTmemO = 256;            // S0 | S1 | O0 | O1
+  static constexpr uint32_t kIdescS = idesc_bf16(128, kN, false, false);
+  static constexpr uint32_t kIdescO = idesc_bf16(128, D, false, true);
+};
+
+struct ChunkShared {
+  uint64_t q_full, k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+  // a V block with unseen rows: the MMA thread, which has seen it land, asks for the zeroing and
+  // waits for it (one request at a time, so the parities cannot alias)
+  uint64_t v_dirty, v_clean;
+  uint64_t s_full[2], p_half[2], p_full[2], pv_done[2], o_done[2], alpha_ready[2], o_ready[2], l_ready[2];
+  uint64_t mma_done;
+  float alpha[2][kM];
+  float lfin[2][kM];               // row sums; +inf for rows that saw nothing (O / l = 0)
+  uint32_t tmem_base, abort_flag;
+  int b, tile;                     // this CTA's sequence and pair of tiles; b = -1: none
+};
+
+// The work of one CTA: a pair of tiles of sequence b for kv head h, steps [js, je) of its walk.
+struct ChunkWork {
+  Seq s;
+  int tok0, tokens;      // first token of the pair, tokens per tile
+  int first, last;       // positions of its first and last token
+  int splits;            // pieces that the pair's keys are split into
+  KeyWalk<kN> w;
+  __device__ __forceinline__ ChunkWork(const Attn& p, int b, int tile, int max_splits)
+      : s(load_seq(p, b)),
+        tokens(kM / p.group),
+        w(p, s.pos0 + tile * 2 * (kM / p.group), s.pos0 + min((tile + 1) * 2 * (kM / p.group), s.n) - 1) {
+    tok0 = tile * 2 * tokens;
+    first = s.pos0 + tok0;
+    last = s.pos0 + min(tok0 + 2 * tokens, s.n) - 1;
+    splits = min(max_splits, max(1, w.steps / kSplitSteps));
+  }
+  // steps of tile t alone: up to the block of its last token
+  __device__ __forceinline__ int steps(int t) const {
+    const int t0 = tok0 + t * tokens;
+    if (t0 >= s.n) return 0;
+    const int hi = max(s.pos0 + min(t0 + tokens, s.n), 0);
+    return max(w.n_sink + (hi + kN - 1) / kN - w.b_lo, 1);
+  }
+};
+
+// Pairs of tiles of sequence b that are the chunk kernel's.
+__device__ __forceinline__ int chunk_tiles(const Attn& p, int b) {
+  const int n = load_seq(p, b).n, per = 2 * (kM / p.group);
+  return n * p.group <= p.few_rows ? 0 : (n + per - 1) / per;
+}
+
+template <int D, bool kFp8>
+__global__ void __launch_bounds__(ChunkCfg<D, kFp8>::kThreads, 1)
+    fa_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                    const __grid_constant__ CUtensorMap tmV, const Attn p, const int max_splits) {
+  using C = ChunkCfg<D, kFp8>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ ChunkShared sh;
+  volatile uint32_t* abort_flag = &sh.abort_flag;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  // blockIdx.x = (pair of tiles, kv head, split), split fastest
+  const int split = blockIdx.x % max_splits;
+  const int h = (blockIdx.x / max_splits) % p.c.Hkv;
+
+  if (warp == 0) {
+    // which sequence this pair of tiles belongs to: 32 sequences at a time
+    int want = blockIdx.x / (max_splits * p.c.Hkv), found = -1, tile = 0;
+    for (int b0 = 0; b0 < p.c.B && found < 0; b0 += 32) {
+      const int mine = b0 + lane < p.c.B ? chunk_tiles(p, b0 + lane) : 0;
+      int incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const int x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+      }
+      const uint32_t hit = __ballot_sync(0xffffffffu, want < incl);
+      const int at = hit ? __ffs(hit) - 1 : 31;
+      const int upto = __shfl_sync(0xffffffffu, incl, at), n = __shfl_sync(0xffffffffu, mine, at);
+      if (hit) {
+        found = b0 + at;
+        tile = n - 1 - (want - (upto - n));  // the last (longest) tiles of a sequence first
+      } else {
+        want -= upto;
+      }
+    }
+    if (lane == 0) {
+      sh.b = found;
+      sh.tile = tile;
+    }
+  }
+  if (threadIdx.x == 0) {
+    sh.abort_flag = 0;
+    mbar_init(&sh.q_full, 1);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&sh.k_full[s], kFp8 ? 128 : 1);
+      mbar_init(&sh.k_empty[s], 1);
+      mbar_init(&sh.v_full[s], kFp8 ? 128 : 1);
+      mbar_init(&sh.v_empty[s], 1);
+    }
+    mbar_init(&sh.v_dirty, 1);
+    mbar_init(&sh.v_clean, 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&sh.s_full[t], 1);
+      mbar_init(&sh.p_half[t], kM);
+      mbar_init(&sh.p_full[t], kM);
+      mbar_init(&sh.pv_done[t], 1);
+      mbar_init(&sh.o_done[t], 1);
+      mbar_init(&sh.alpha_ready[t], kM);
+      mbar_init(&sh.o_ready[t], kM);
+      mbar_init(&sh.l_ready[t], kM);
+    }
+    mbar_init(&sh.mma_done, 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  const int b = sh.b;
+  if (b < 0) return;
+  const ChunkWork wk(p, b, sh.tile, max_splits);
+  if (split >= wk.splits) return;
+  const int js = (int)((long long)wk.w.steps * split / wk.splits);
+  const int je = (int)((long long)wk.w.steps * (split + 1) / wk.splits);
+  // steps of this CTA for each tile (0 where the tile ends before the piece)
+  const int nb0 = max(0, min(je, wk.steps(0)) - js), nb1 = max(0, min(je, wk.steps(1)) - js);
+  const int nbmax = max(nb0, nb1);
+  // whether the block at `key` has rows that no row of the CTA sees
+  auto unseen = [&](int key) {
+    return key + kN > wk.w.hi || (key < wk.w.lo && key + kN > wk.w.sinks);
+  };
+
+  if (warp == C::kMmaWarp) {
+    tmem_alloc(&sh.tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem_base;
+
+  if (kFp8 && warp >= C::kConvertWarp) {
+    if constexpr (kFp8) {
+    // ------------------------------------------------------------ E4M3 -> BF16 operand tiles
+    // Thread = key of the block.  The codes of the next tile (K and V in turn) are loaded before the
+    // current one is converted, so their latency is covered.
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegConvert));
+    const int r = threadIdx.x - 32 * C::kConvertWarp;
+    const int page_size = 1 << p.c.page_shift;
+    uint4 next[D / 16];
+    float next_scale = 0.f;
+    long long row = 0;      // page and slot of this thread's key in the current block
+    bool have = false;
+    auto locate = [&](int j) {
+      const int key = wk.w.at(js + j) + r;
+      have = wk.w.seen(key);
+      int page = -1;
+      if (have) page = find_page(p.c, b, key, kSitePagedPage);
+      have = page >= 0;
+      row = have ? (long long)h * page_size + (key & (page_size - 1)) : 0;
+      return page;
+    };
+    int page = 0;
+    auto fetch = [&](const void* pool, const float* scales) {
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(pool) + page * p.c.page_stride + row * D);
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) next[i] = have ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+      next_scale = have ? __ldg(scales + page * p.c.scale_stride + row) : 0.f;
+    };
+    // row r of an operand tile: 16-byte chunk x (8 elements) of each 64-column block at (x ^ r % 8)
+    auto store = [&](uint8_t* tile, const uint4 (&codes)[D / 16], float scale) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+        uint32_t o[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 lo = e4m3x2_to_float2(w[e]), hi = e4m3x2_to_float2(w[e] >> 16);
+          o[2 * e] = pack_bf16x2(lo.x * scale, lo.y * scale);
+          o[2 * e + 1] = pack_bf16x2(hi.x * scale, hi.y * scale);
+        }
+        uint8_t* dst = tile + (i / 4) * C::kAtomBlock + r * 128;
+        const int x = (i % 4) * 2;
+        *reinterpret_cast<uint4*>(dst + ((x ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(dst + (((x + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+      fence_proxy_async_smem();
+    };
+    if (nbmax > 0) {
+      page = max(locate(0), 0);
+      fetch(p.c.k, p.c.k_scale);
+    }
+    bool ok = true;
+    for (int j = 0; ok && j < nbmax; ++j) {
+      const int s = j % kStages;
+      const uint32_t ph = (j / kStages) & 1;
+      uint4 cur[D / 16];
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) cur[i] = next[i];
+      float scale = next_scale;
+      fetch(p.c.v, p.c.v_scale);
+      if (!(ok = mbar_wait(&sh.k_empty[s], ph ^ 1, abort_flag, p.c.status))) break;
+      store(smem + C::kKOff + s * C::kTileBytes, cur, scale);
+      mbar_arrive(&sh.k_full[s]);
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) cur[i] = next[i];
+      scale = next_scale;
+      if (j + 1 < nbmax) {
+        page = max(locate(j + 1), 0);
+        fetch(p.c.k, p.c.k_scale);
+      }
+      if (!(ok = mbar_wait(&sh.v_empty[s], ph ^ 1, abort_flag, p.c.status))) break;
+      store(smem + C::kVOff + s * C::kTileBytes, cur, scale);
+      mbar_arrive(&sh.v_full[s]);
+    }
+    }
+  } else if (warp >= C::kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegOther));
+    if (warp == C::kLoadWarp) {
+      // ---------------------------------------------------------- loads: Q, and K and V page by page
+      const uint32_t base = smem_u32(smem);
+      const int ntiles = nb1 > 0 ? 2 : 1;
+      if (elect_one()) {
+        tma_prefetch_desc(&tmQ);
+        mbar_arrive_expect_tx(&sh.q_full, ntiles * wk.tokens * p.group * 128 * C::kAtoms);
+        for (int t = 0; t < ntiles; ++t)
+          for (int c = 0; c < C::kAtoms; ++c)
+            tma_load_3d(smem + C::kQOff + t * C::kTileBytes + c * C::kAtomBlock, &tmQ, &sh.q_full, c * 64, h * p.group,
+                        wk.s.q0 + wk.tok0 + t * wk.tokens);
+      }
+      __syncwarp();
+      if constexpr (!kFp8) {
+        const int page_size = 1 << p.c.page_shift;
+        const int box = min(page_size, kN), ppb = kN / box, per_group = 32 / ppb;
+        int nk = 0, nv = 0;
+        bool ok = true;
+        for (int jg = 0; ok && jg < nbmax; jg += per_group) {
+          const int jl = jg + lane / ppb;
+          int page = p.c.num_pages;  // out of range: zeros
+          if (jl < nbmax) {
+            const int key = wk.w.at(js + jl) + (lane % ppb) * box;
+            if (wk.w.any(key, box)) {
+              const int x = find_page(p.c, b, key, kSitePagedPage);
+              if (x >= 0) page = x;
+            }
+          }
+          for (int jj = 0; jj < per_group && jg + jj < nbmax; ++jj) {
+            const int j = jg + jj, s = j % kStages;
+            const uint32_t ph = (j / kStages) & 1;
+            const int pg = __shfl_sync(0xffffffffu, page, jj * ppb + lane % ppb);
+            const int slot = (wk.w.at(js + j) + lane * box) & (page_size - 1);
+            auto load = [&](const CUtensorMap* map, uint64_t* full, uint32_t tile) {
+              if (lane == 0) mbar_arrive_expect_tx(full, C::kTileBytes);
+              __syncwarp();
+              if (lane < ppb)
+                for (int c = 0; c < C::kAtoms; ++c)
+                  tma_load_page(base + tile + c * C::kAtomBlock + lane * box * 128, map, full, c * 64, slot, h, pg);
+            };
+            ok = __all_sync(0xffffffffu, mbar_wait(&sh.k_empty[s], ph ^ 1, abort_flag, p.c.status));
+            if (!ok) break;
+            load(&tmK, &sh.k_full[s], C::kKOff + s * C::kTileBytes);
+            nk = j + 1;
+            ok = __all_sync(0xffffffffu, mbar_wait(&sh.v_empty[s], ph ^ 1, abort_flag, p.c.status));
+            if (!ok) break;
+            load(&tmV, &sh.v_full[s], C::kVOff + s * C::kTileBytes);
+            nv = j + 1;
+          }
+        }
+        if (*abort_flag) {
+          // let copies still in flight land before the CTA's shared memory goes away
+          volatile uint32_t ignore_abort = 0;
+          for (int j = max(0, nk - kStages); j < nk; ++j)
+            mbar_wait(&sh.k_full[j % kStages], (j / kStages) & 1, &ignore_abort, p.c.status);
+          for (int j = max(0, nv - kStages); j < nv; ++j)
+            mbar_wait(&sh.v_full[j % kStages], (j / kStages) & 1, &ignore_abort, p.c.status);
+        }
+      }
+      if (*abort_flag) {
+        volatile uint32_t ignore_abort = 0;
+        mbar_wait(&sh.q_full, 0, &ignore_abort, p.c.status);
+      }
+    } else if (warp == C::kGuardWarp) {
+      // ---------------------------------------------------------- zero V rows that no row sees
+      if constexpr (!kFp8) {
+        bool ok = true;
+        int n = 0;
+        for (int j = 0; ok && j < nbmax; ++j) {
+          const int key0 = wk.w.at(js + j), s = j % kStages;
+          if (!unseen(key0)) continue;
+          ok = __all_sync(0xffffffffu, mbar_wait(&sh.v_dirty, n++ & 1, abort_flag, p.c.status));
+          if (!ok) break;
+          for (int r = 0; r < kN; ++r) {
+            if (wk.w.seen(key0 + r)) continue;
+            uint8_t* row = smem + C::kVOff + s * C::kTileBytes + r * 128;
+            if (lane < C::kAtoms * 8)
+              *reinterpret_cast<uint4*>(row + (lane / 8) * C::kAtomBlock + (lane % 8) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.v_clean);
+        }
+      }
+    } else if (warp == C::kMmaWarp) {
+      // ---------------------------------------------------------- MMA issuer
+      if (elect_one()) {
+        const uint32_t sQ = smem_u32(smem + C::kQOff), sK = smem_u32(smem + C::kKOff), sV = smem_u32(smem + C::kVOff);
+        const int nb[2] = {nb0, nb1};
+        bool ok = mbar_wait(&sh.q_full, 0, abort_flag, p.c.status);
+        tc_fence_after();
+        int cleaned = 0;  // V blocks that had rows zeroed
+        auto issue_s = [&](int t, int s) {
+          const uint32_t a0 = sQ + t * C::kTileBytes, b0 = sK + s * C::kTileBytes;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk / 4) * C::kAtomBlock + (kk % 4) * 32;
+            mma_ss(tmem + t * 128, sdesc_sw128(a0 + off, 16, 1024), sdesc_sw128(b0 + off, 16, 1024), C::kIdescS, kk > 0);
+          }
+          tc_commit(&sh.s_full[t]);
+        };
+        auto issue_pv = [&](int t, int s, int j, int k_lo, int k_hi) {
+          const uint32_t d = tmem + C::kTmemO + t * D, b0 = sV + s * C::kTileBytes;
+#pragma unroll
+          for (int kk = k_lo; kk < k_hi; ++kk)
+            mma_ts(d, tmem + t * 128 + kk * 8, sdesc_sw128(b0 + kk * 2048, C::kAtomBlock, 1024), C::kIdescO,
+                   (j > 0 || kk > 0) ? 1u : 0u);
+          if (k_hi == kN / 16) {
+            tc_commit(&sh.pv_done[t]);
+            if (j == nb[t] - 1) tc_commit(&sh.o_done[t]);
+          }
+        };
+        // S0_0 S1_0 | PV0_0 S0_1 PV1_0 S1_1 | ... ; P~ V in two halves over the keys, the first as
+        // soon as the softmax has stored it
+        for (int j = 0; ok && j <= nbmax; ++j) {
+          const int s = j % kStages, sp = (j + kStages - 1) % kStages;
+          if (j < nbmax) {
+            if (!(ok = mbar_wait(&sh.k_full[s], (j / kStages) & 1, abort_flag, p.c.status))) break;
+            tc_fence_after();
+          }
+          if (j > 0) {
+            if (!(ok = mbar_wait(&sh.v_full[sp], ((j - 1) / kStages) & 1, abort_flag, p.c.status))) break;
+            if (!kFp8 && unseen(wk.w.at(js + j - 1))) {
+              mbar_arrive(&sh.v_dirty);
+              if (!(ok = mbar_wait(&sh.v_clean, cleaned++ & 1, abort_flag, p.c.status))) break;
+            }
+            tc_fence_after();
+          }
+          for (int t = 0; t < 2; ++t) {
+            if (j > 0 && j - 1 < nb[t]) {
+              if (!(ok = mbar_wait(&sh.p_half[t], (j - 1) & 1, abort_flag, p.c.status))) break;
+              if (j - 1 > 0 && !(ok = mbar_wait(&sh.o_ready[t], (j - 2) & 1, abort_flag, p.c.status))) break;
+              tc_fence_after();
+              issue_pv(t, sp, j - 1, 0, kN / 32);
+              if (!(ok = mbar_wait(&sh.p_full[t], (j - 1) & 1, abort_flag, p.c.status))) break;
+              tc_fence_after();
+              issue_pv(t, sp, j - 1, kN / 32, kN / 16);
+            }
+            if (j < nb[t]) issue_s(t, s);
+          }
+          if (!ok) break;
+          if (j < nbmax) tc_commit(&sh.k_empty[s]);
+          if (j > 0) tc_commit(&sh.v_empty[sp]);
+        }
+        tc_commit(&sh.mma_done);
+        {
+          // MMAs still in flight must finish before TMEM is released, even after an abort
+          volatile uint32_t ignore_abort = 0;
+          mbar_wait(&sh.mma_done, 0, &ignore_abort, p.c.status);
+        }
+      }
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ softmax warpgroups
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegSoftmax));
+    const int t = warp / 4, r = (warp % 4) * 32 + lane;
+    const int nb = t == 0 ? nb0 : nb1;
+    const int tr = r / p.group, tok = wk.tok0 + t * wk.tokens + tr;
+    const bool valid = tr < wk.tokens && tok < wk.s.n;
+    const int pos = valid ? wk.s.pos0 + tok : -1;
+    const uint32_t tS = tmem + t * 128 + ((uint32_t)((warp % 4) * 32) << 16);
+    const float c = p.scale_log2;
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int j = 0; j < nb; ++j) {
+      if (!(ok = mbar_wait(&sh.s_full[t], j & 1, abort_flag, p.c.status))) break;
+      tc_fence_after();
+      uint32_t raw[kN];
+      float pmax[kN / 32];
+#pragma unroll
+      for (int c0 = 0; c0 < kN; c0 += 32)
+        tmem_ld32_max(tS + c0, *reinterpret_cast<uint32_t(*)[32]>(raw + c0), pmax[c0 / 32]);
+      tmem_ld_wait();
+      reg_fence(raw);
+      reg_fence(pmax);
+      float sv[kN];
+#pragma unroll
+      for (int i = 0; i < kN; ++i) sv[i] = __uint_as_float(raw[i]);
+      // mask: keys after the row's token, and keys before its window that are no sinks
+      const int col0 = wk.w.at(js + j);
+      const int lim = pos - col0 + 1, w_lo = p.window ? pos - p.window + 1 - col0 : 0, s_hi = p.sinks - col0;
+      const bool open = lim >= kN && (w_lo <= 0 || s_hi >= kN);
+      float bm;
+      if (__all_sync(0xffffffffu, open)) {
+        bm = fmaxf(max3f(pmax[0], pmax[1], pmax[2]), pmax[3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) sv[i] = (i < lim && (i >= w_lo || i < s_hi)) ? sv[i] : -INFINITY;
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < kN; i += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = max3f(mx[e], sv[i + 2 * e], sv[i + 2 * e + 1]);
+        bm = fmaxf(max3f(mx[0], mx[1], mx[2]), mx[3]);
+      }
+      const float m_new = fmaxf(m, bm);
+      const float mu = m_new == -INFINITY ? 0.f : m_new;   // nothing seen yet
+      const float alpha = ex2_approx((m - mu) * c);
+      m = m_new;
+      if (j > 0) {
+        sh.alpha[t][r] = alpha;
+        mbar_arrive(&sh.alpha_ready[t]);
+      }
+      const float nmc = -mu * c;
+      float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int i = 0; i < 64; i += 2) {
+          float x0, x1;
+          fma2(x0, x1, sv[half * 64 + i], sv[half * 64 + i + 1], c, c, nmc, nmc);
+          const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+          add2(sum0, sum1, sum0, sum1, p0, p1);
+          pk[i / 2] = pack_bf16x2(p0, p1);
+        }
+        __syncwarp();
+        tmem_st32(tS + half * 32, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(half == 0 ? &sh.p_half[t] : &sh.p_full[t]);
+      }
+      l = l * alpha + (sum0 + sum1);
+    }
+    if (ok) {
+      const bool empty = m == -INFINITY && l == 0.f;  // no visible key in this piece (a NaN score is not that)
+      sh.lfin[t][r] = empty ? INFINITY : l;
+      mbar_arrive(&sh.l_ready[t]);
+      const float lse = empty ? -INFINITY : m * p.scale + logf(l);
+      const long long row = (long long)(wk.s.q0 + tok) * p.Hq + h * p.group + (r - tr * p.group);
+      if (valid) {
+        if (wk.splits > 1)
+          p.part_lse[(long long)split * p.T * p.Hq + row] = lse;
+        else if (p.lse)
+          p.lse[row] = lse;
+      }
+      if (wk.splits == 1)
+        report_nonfinite((valid && !empty && !(fabsf(lse) < INFINITY)) ? 1u : 0u, p.c.status, kOutLse);
+    }
+  } else {
+    // ------------------------------------------------------------ correction warpgroup
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegCorr));
+    const int r = (warp % 4) * 32 + lane;
+    const uint32_t tO = tmem + C::kTmemO + ((uint32_t)((warp % 4) * 32) << 16);
+    const int nb[2] = {nb0, nb1};
+    bool ok = true;
+    for (int j = 1; ok && j < nbmax; ++j) {
+      for (int t = 0; t < 2; ++t) {
+        if (j >= nb[t]) continue;
+        if (!(ok = mbar_wait(&sh.alpha_ready[t], (j - 1) & 1, abort_flag, p.c.status))) break;
+        const float alpha = sh.alpha[t][r];
+        if (__any_sync(0xffffffffu, alpha != 1.f)) {
+          if (!(ok = mbar_wait(&sh.pv_done[t], (j - 1) & 1, abort_flag, p.c.status))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            uint32_t w[32];
+            tmem_ld32(tO + t * D + c0, w);
+            tmem_ld_wait();
+            reg_fence(w);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              float a0, a1;
+              mul2(a0, a1, __uint_as_float(w[i]), __uint_as_float(w[i + 1]), alpha, alpha);
+              w[i] = __float_as_uint(a0);
+              w[i + 1] = __float_as_uint(a1);
+            }
+            tmem_st32(tO + t * D + c0, w);
+          }
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        mbar_arrive(&sh.o_ready[t]);
+      }
+    }
+    // O / l, to the output or to this piece's partial result
+    for (int t = 0; ok && t < 2; ++t) {
+      if (nb[t] == 0) continue;
+      if (!(ok = mbar_wait(&sh.o_done[t], 0, abort_flag, p.c.status))) break;
+      if (!(ok = mbar_wait(&sh.l_ready[t], 0, abort_flag, p.c.status))) break;
+      tc_fence_after();
+      const float inv_l = 1.f / sh.lfin[t][r];
+      const int tr = r / p.group, tok = wk.tok0 + t * wk.tokens + tr;
+      const bool valid = tr < wk.tokens && tok < wk.s.n;
+      const long long row = valid ? (long long)(wk.s.q0 + tok) * p.Hq + h * p.group + (r - tr * p.group) : 0;
+      uint32_t bad = 0;
+#pragma unroll
+      for (int c0 = 0; c0 < D; c0 += 32) {
+        uint32_t w[32];
+        tmem_ld32(tO + t * D + c0, w);
+        tmem_ld_wait();
+        reg_fence(w);
+        if (wk.splits > 1) {
+          float4* dst = reinterpret_cast<float4*>(p.part_o + ((long long)split * p.T * p.Hq + row) * D + c0);
+          if (valid)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              dst[i] = make_float4(__uint_as_float(w[4 * i]) * inv_l, __uint_as_float(w[4 * i + 1]) * inv_l,
+                                   __uint_as_float(w[4 * i + 2]) * inv_l, __uint_as_float(w[4 * i + 3]) * inv_l);
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(p.o + row * D + c0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              x[e] = pack_bf16x2(__uint_as_float(w[8 * i + 2 * e]) * inv_l, __uint_as_float(w[8 * i + 2 * e + 1]) * inv_l);
+              bad += nonfinite_bf16x2(x[e]);
+            }
+            if (valid) dst[i] = make_uint4(x[0], x[1], x[2], x[3]);
+          }
+        }
+      }
+      if (wk.splits == 1) report_nonfinite(valid ? bad : 0u, p.c.status, kOutO);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the pieces of tiles whose keys were split: one warp per (token, query head).
+template <int D>
+__global__ void __launch_bounds__(256) fa_chunk_combine(const Attn p, const int max_splits) {
+  const int lane = threadIdx.x % 32;
+  const long long row = (long long)blockIdx.x * 8 + threadIdx.x / 32;
+  if (row >= (long long)p.T * p.Hq) return;
+  const int token = (int)(row / p.Hq);
+  const int b = find_sequence(p.q_indptr, p.c.B, token);
+  if (b >= p.c.B || chunk_tiles(p, b) == 0) return;
+  const int tile = (token - __ldg(p.q_indptr + b)) / (2 * (kM / p.group));
+  const int pieces = ChunkWork(p, b, tile, max_splits).splits;
+  if (pieces < 2) return;
+  const long long rows = (long long)p.T * p.Hq;
+  constexpr int kPer = D / 32;
+  const float mine = lane < pieces ? p.part_lse[lane * rows + row] : -INFINITY;
+  float top = mine;
+#pragma unroll
+  for (int off = 16; off > 0; off /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  const float tu = top == -INFINITY ? 0.f : top;
+  float sum = 0.f, acc[kPer];
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+  for (int i = 0; i < pieces; ++i) {
+    const float part = __shfl_sync(0xffffffffu, mine, i);
+    if (part == -INFINITY) continue;  // saw nothing: its output may not have been written
+    const float w = ex2_approx((part - tu) * 1.4426950408889634f);
+    sum += w;
+    const float* src = p.part_o + (i * rows + row) * D + lane * kPer;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] = fmaf(w, src[e], acc[e]);
+  }
+  const bool empty = top == -INFINITY && sum == 0.f;
+  const float inv = empty ? 0.f : 1.f / sum;
+  uint32_t w2[kPer / 2], bad = 0;
+#pragma unroll
+  for (int e = 0; e < kPer / 2; ++e) {
+    w2[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    bad += nonfinite_bf16x2(w2[e]);
+    reinterpret_cast<uint32_t*>(p.o + row * D)[lane * (kPer / 2) + e] = w2[e];
+  }
+  report_nonfinite(bad, p.c.status, kOutO);
+  const float lse = empty ? -INFINITY : top + logf(sum);
+  report_nonfinite((lane == 0 && !empty && !(fabsf(lse) < INFINITY)) ? 1u : 0u, p.c.status, kOutLse);
+  if (lane == 0 && p.lse) p.lse[row] = lse;
+}
+
+template <int D, bool kFp8>
+static int launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const Attn& p, int splits,
+                  cudaStream_t s) {
+  using C = ChunkCfg<D, kFp8>;
+  auto kern = fa_chunk_kernel<D, kFp8>;
+  static std::atomic<uint64_t> prepared{0};
+  int rc = prepare_kernel(reinterpret_cast<const void*>(kern), C::kSmemBytes, C::kThreads, C::kSplit, "chunk kernel",
+                          &prepared);
+  if (rc) return rc;
+  const long long grid = chunk_pairs(p.T, p.c.B, p.group) * p.c.Hkv * splits;
+  if (grid >= (1ll << 31)) return set_error(FA_ERR_INVALID_ARG, "too many tiles for one launch");
+  kern<<<(unsigned)grid, C::kThreads, C::kSmemBytes, s>>>(tq, tk, tv, p, splits);
+  if ((rc = check_cuda(cudaGetLastError(), "launch fa_chunk_kernel")) || splits == 1) return rc;
+  fa_chunk_combine<D><<<(unsigned)(((long long)p.T * p.Hq + 7) / 8), 256, 0, s>>>(p, splits);
+  return check_cuda(cudaGetLastError(), "launch fa_chunk_combine");
+}
+
+int launch_chunk(const Attn& p, int d, bool fp8, int splits, cudaStream_t s) {
+  const int page_size = 1 << p.c.page_shift;
+  CUtensorMap tq, tk{}, tv{};
+  int rc;
+  if ((rc = make_tmap_rows(&tq, p.q, p.T, p.Hq, d, p.q_stride, p.group, kM / p.group))) return rc;
+  if (!fp8) {
+    const int box = page_size < kN ? page_size : kN;
+    if ((rc = make_tmap_pages(&tk, p.c.k, false, d, page_size, p.c.Hkv, p.c.num_pages, p.c.page_stride, box)) ||
+        (rc = make_tmap_pages(&tv, p.c.v, false, d, page_size, p.c.Hkv, p.c.num_pages, p.c.page_stride, box)))
+      return rc;
+  }
+  if (d == 64) return fp8 ? launch<64, true>(tq, tk, tv, p, splits, s) : launch<64, false>(tq, tk, tv, p, splits, s);
+  return fp8 ? launch<128, true>(tq, tk, tv, p, splits, s) : launch<128, false>(tq, tk, tv, p, splits, s);
+}
+
+}  // namespace paged
+}  // namespace fa
+
+namespace {
+
+using fa::paged::kMaxFewRows;
+
+// Which kernels a call launches and how: from sizes that the host knows.
+struct Plan {
+  int few_rows;   // sequences of up to this many rows go to the few-rows kernel (0: it is not launched)
+  int splits;     // chunk kernel: most pieces of a tile's keys (0: it is not launched)
+};
+
+Plan make_plan(int T, int B, int max_q, int group, int Hkv, int max_kv) {
+  Plan pl{0, 0};
+  const long long rows = (long long)max_q * group;
+  if (rows <= kMaxFewRows) {
+    pl.few_rows = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
+    return pl;
+  }
+  // A batch of chunks may hold sequences with a token or two: those go to the few-rows kernel with one
+  // row tile (its fastest form), everything else to the chunk kernel.
+  if (B > 1 && group <= 16) pl.few_rows = 16;
+  // One CTA per SM: split the keys while the tiles leave half of the SMs without work.
+  const long long tiles = fa::paged::chunk_pairs(T, B, group) * Hkv;
+  long long s = fa::paged::kChunkSms / tiles;
+  const long long most = (max_kv + 128 * fa::paged::kSplitSteps - 1) / (128 * fa::paged::kSplitSteps);
+  if (s > most) s = most;
+  if (s > fa::paged::kMaxSplits) s = fa::paged::kMaxSplits;
+  pl.splits = s < 1 ? 1 : (int)s;
+  return pl;
+}
+
+struct Parts {
+  size_t o, lse, info, total;   // offsets
+};
+
+// The workspace: FP32 partial outputs, their log-sum-exps, and the few-rows kernel's records.  The two
+// kernels of a mixed batch have parts of their own.
+Parts carve(const Plan& pl, int T, int B, int Hq, int Hkv, int d, Parts* chunk) {
+  const size_t rows = pl.few_rows ? (size_t)2 * fa::paged::kRowsMaxCtas * pl.few_rows : 0;
+  Parts f;
+  f.o = 0;
+  f.lse = fa::round_up(rows * d * 4, 256);
+  f.info = f.lse + fa::round_up(rows * 4, 256);
+  f.total = f.info + (rows ? fa::round_up((size_t)B * Hkv * sizeof(int4), 256) : 0);
+  const size_t c_rows = pl.splits > 1 ? (size_t)pl.splits * T * Hq : 0;
+  chunk->o = f.total;
+  chunk->lse = chunk->o + fa::round_up(c_rows * d * 4, 256);
+  chunk->info = 0;
+  chunk->total = chunk->lse + fa::round_up(c_rows * 4, 256);
+  return f;
+}
+
+int check_attn(int T, int B, int max_q, int Hq, int Hkv, int d) {
+  using namespace fa;
+  if (T < 0 || max_q < 0) return set_error(FA_ERR_INVALID_ARG, "T, max_q must be >= 0 (got %d, %d)", T, max_q);
+  if (B < 1 || Hkv < 1 || Hq < 1) return set_error(FA_ERR_INVALID_ARG, "B, Hq, Hkv must be >= 1 (got %d, %d, %d)", B, Hq, Hkv);
+  if (Hq % Hkv) return set_error(FA_ERR_INVALID_ARG, "Hq = %d is not a multiple of Hkv = %d", Hq, Hkv);
+  if (Hq / Hkv > 128) return set_error(FA_ERR_UNSUPPORTED, "more than 128 query heads for a kv head (%d)", Hq / Hkv);
+  if (d != 64 && d != 128) return set_error(FA_ERR_UNSUPPORTED, "head dim d=%d not supported (64 or 128)", d);
+  if ((long long)T * Hq >= (1ll << 31) || (long long)B * Hkv >= (1ll << 31))
+    return set_error(FA_ERR_INVALID_ARG, "T*Hq and B*Hkv must be < 2^31");
+  return FA_OK;
+}
+
+}  // namespace
+
+extern "C" size_t fa_fwd_paged_workspace_size(int T, int B, int max_q, int Hq, int Hkv, int d, int max_kv) {
+  fa::clear_error();
+  if (check_attn(T, B, max_q, Hq, Hkv, d) || max_kv < 0 || T == 0) return 0;
+  Parts chunk;
+  carve(make_plan(T, B, max_q, Hq / Hkv, Hkv, max_kv), T, B, Hq, Hkv, d, &chunk);
+  return chunk.total;
+}
+
+extern "C" int fa_fwd_paged(const fa_paged_kv* kv, const void* q, int64_t q_stride, const int32_t* q_indptr, int T,
+                            int max_q, int Hq, void* o, float* lse, int window, int sinks, float scale, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  fa::NvtxRange nvtx_range("fa_fwd_paged");
+  using namespace fa;
+  clear_error();
+  paged::Attn p{};
+  int rc;
+  if ((rc = paged::check_cache(kv, &p.c)) || (rc = check_attn(T, kv->B, max_q, Hq, kv->Hkv, kv->d))) return rc;
+  if ((rc = check_ptr(q, "q")) || (rc = check_ptr(o, "o"))) return rc;
+  if (lse && (reinterpret_cast<uintptr_t>(lse) & 3)) return set_error(FA_ERR_INVALID_ARG, "lse is not 4-byte aligned");
+  if (!q_indptr || (reinterpret_cast<uintptr_t>(q_indptr) & 3))
+    return set_error(FA_ERR_INVALID_ARG, "q_indptr must be a 4-byte aligned device pointer");
+  if (q_stride < (int64_t)Hq * kv->d || q_stride % 8)
+    return set_error(FA_ERR_INVALID_ARG, "q_stride %lld must be a multiple of 8 and at least Hq*d = %d",
+                     (long long)q_stride, Hq * kv->d);
+  if (!(scale > 0.f) || !isfinite(scale)) return set_error(FA_ERR_INVALID_ARG, "scale must be finite and > 0");
+  if (window < 0 || sinks < 0) return set_error(FA_ERR_INVALID_ARG, "window and sinks must be >= 0 (got %d, %d)", window, sinks);
+  if (!window && sinks) return set_error(FA_ERR_INVALID_ARG, "sinks need a window");
+  if (T == 0 || max_q == 0) return FA_OK;
+  const int max_kv = kv->max_pages * kv->page_size;
+  const Plan pl = make_plan(T, kv->B, max_q, Hq / kv->Hkv, kv->Hkv, max_kv);
+  Parts chunk;
+  const Parts few = carve(pl, T, kv->B, Hq, kv->Hkv, kv->d, &chunk);
+  if (chunk.total) {
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255))
+      return set_error(FA_ERR_INVALID_ARG, "workspace must be a 256-byte aligned device pointer");
+    if (workspace_bytes < chunk.total)
+      return set_error(FA_ERR_INVALID_ARG, "workspace too small: %zu bytes given, %zu needed", workspace_bytes, chunk.total);
+  }
+  p.c.status = device_status_word();
+  if (!p.c.status) return set_error(FA_ERR_CUDA, "could not allocate the device status record");
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.q_stride = q_stride;
+  p.q_indptr = q_indptr;
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.T = T;
+  p.Hq = Hq;
+  p.group = Hq / kv->Hkv;
+  p.max_rows = (int)((long long)max_q * p.group < INT32_MAX ? max_q * p.group : INT32_MAX);
+  p.few_rows = pl.few_rows;
+  p.window = window < max_kv ? window : 0;  // a window of the whole cache is none
+  p.sinks = sinks < max_kv ? sinks : max_kv;
+  p.scale = scale;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  const bool fp8 = kv->dtype == FA_KV_E4M3;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  if (pl.splits) {
+    paged::Attn c = p;
+    c.part_o = reinterpret_cast<float*>(ws + chunk.o);
+    c.part_lse = reinterpret_cast<float*>(ws + chunk.lse);
+    if ((rc = paged::launch_chunk(c, kv->d, fp8, pl.splits, s))) return rc;
+  }
+  if (pl.few_rows) {
+    p.part_o = reinterpret_cast<float*>(ws + few.o);
+    p.part_lse = reinterpret_cast<float*>(ws + few.lse);
+    p.part_info = reinterpret_cast<int4*>(ws + few.info);
+    if ((rc = paged::launch_rows(p, kv->d, fp8, s))) return rc;
+  }
+  return FA_OK;
+}

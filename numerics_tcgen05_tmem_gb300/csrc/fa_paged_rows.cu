@@ -1,0 +1,699 @@
+// Paged attention for few rows (decoding): at most 64 rows for a kv head.
+//
+// With so few rows a key and its value are used for a handful of products only, so the kernel's
+// bound is reading the cache: the rest has to stay out of the way of that stream.
+//   * The keys of all sequences and kv heads are one list of 64-key blocks, sequence by sequence,
+//     dealt to the CTAs in equal contiguous shares: two CTAs per SM, whatever the lengths, and no
+//     long sequence that keeps one CTA busy after the others are done.  A share may end inside a
+//     sequence; such a piece leaves its normalised output and log-sum-exp in the workspace and
+//     fa_rows_combine joins the pieces in their order, so results do not depend on timing.
+//   * One warp loads: page numbers from the table, 32 at a time, then TMA boxes into a ring of K and
+//     V blocks (swizzled, so that the fragment loads meet no bank conflicts).  A page that no row
+//     sees is taken out of range, which fills zeros without a read.
+//   * Four warps compute with mma.sync: at 16 to 64 rows a tcgen05 tile (128 rows) would be mostly
+//     empty, and its softmax would hold one row per thread.  Row tiles of 16 are dealt to the warps
+//     first, the block's keys to the rest: for up to 16 rows each warp takes 16 keys of every block
+//     with its own running maximum and sum, joined once at the end of a piece.
+//   * E4M3: codes become FP16 with one conversion for two (exact), the vectors' scales multiply the
+//     FP32 scores (K) and the FP32 probabilities (V).  Q goes to FP16 with a power of two per row
+//     that brings its largest magnitude into [1, 2): exact but for elements 2^-14 below it, whose
+//     error stays under 2^-25 of that magnitude, the size of an FP32 product's rounding.  The
+//     probabilities are taken relative to the largest V scale seen, so they stay within FP16's
+//     range; the output is multiplied by it at the end.
+// Softmax statistics and sums are FP32; P is rounded to BF16 (FP16 with E4M3) for the product with V,
+// as the tensor core takes it.
+#include "paged_attn.cuh"
+
+namespace fa {
+namespace paged {
+
+constexpr int kRowsBlk = 64;
+constexpr int kRowsWarps = 4;                          // computing warps; one more loads
+constexpr int kRowsThreads = 32 * (kRowsWarps + 1);
+
+template <int D, bool kFp8>
+struct RowsCfg {
+  static constexpr int kElem = kFp8 ? 1 : 2;
+  static constexpr int kRowBytes = D * kElem;                          // 64, 128 or 256
+  static constexpr int kAtomBytes = kRowBytes >= 128 ? 128 : 64;       // swizzle atom row
+  static constexpr int kAtoms = kRowBytes / kAtomBytes;
+  static constexpr int kAtomElems = kAtomBytes / kElem;
+  static constexpr int kTile = kRowsBlk * kRowBytes;                   // K or V of one block
+  static constexpr int kFit = 96 * 1024 / (2 * kTile);
+  static constexpr int kStages = kFit < 8 ? kFit : 8;
+  static constexpr int kScaleOff = kStages * 2 * kTile;
+  static constexpr int kScaleBytes = kFp8 ? 2 * kRowsBlk * 4 : 0;      // per stage
+  static constexpr int kBufOff = kScaleOff + kStages * kScaleBytes;    // joining: 4 x 16 rows x 32 columns
+  static constexpr int kSmemBytes = kBufOff + kRowsWarps * 16 * 32 * 4 + 1024;
+  static_assert(2 * (kSmemBytes + 2048) <= 228 * 1024, "two CTAs must fit one SM's shared memory");
+  // shared-memory address of 16-byte chunk x of row r of a tile
+  __device__ static uint32_t chunk(uint32_t base, int r, int x) {
+    constexpr int kPer = kAtomBytes / 16;
+    const int sw = kAtomBytes == 128 ? (r & 7) : ((r >> 1) & 3);
+    return base + (x / kPer) * (kRowsBlk * kAtomBytes) + r * kAtomBytes + (((x % kPer) ^ sw) << 4);
+  }
+};
+
+struct RowsShared {
+  uint64_t full[8], empty[8], sync;
+  uint32_t abort_flag;
+  float m[kRowsWarps][16], l[kRowsWarps][16];
+  int scan[kRowsThreads / 32];
+  int first_b;               // the sequence of this CTA's first unit
+  long long first_unit;      // ... and that unit's number within the sequence
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+template <bool kHalf>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (kHalf)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Two E4M3 codes (low 16 bits of w) as FP16 pairs.
+__device__ __forceinline__ uint32_t codes_f16x2(uint32_t w) {
+  uint32_t h;
+  asm("{\n .reg .b16 c, x;\n mov.b32 {c, x}, %1;\n cvt.rn.f16x2.e4m3x2 %0, c;\n}" : "=r"(h) : "r"(w));
+  return h;
+}
+__device__ __forceinline__ uint32_t codes_hi_f16x2(uint32_t w) {
+  uint32_t h;
+  asm("{\n .reg .b16 c, x;\n mov.b32 {x, c}, %1;\n cvt.rn.f16x2.e4m3x2 %0, c;\n}" : "=r"(h) : "r"(w));
+  return h;
+}
+
+// A sequence as the few-rows kernel sees it: its walk, or no steps where it is not this kernel's.
+struct RowsItem {
+  Seq s;
+  int rows;
+  KeyWalk<kRowsBlk> w;
+  __device__ __forceinline__ RowsItem(const Attn& p, int b) : s(load_seq(p, b)), rows(s.n * p.group), w(p, s.pos0, s.kv - 1) {
+    if (rows == 0 || rows > p.few_rows) w.steps = 0;
+  }
+};
+
+// Blocks of the sequences [b0, b1), for one kv head.
+__device__ __forceinline__ int count_blocks(const Attn& p, int b0, int b1) {
+  int n = 0;
+  for (int b = b0; b < b1; ++b) n += RowsItem(p, b).w.steps;
+  return n;
+}
+
+// The CTA's pieces: unit u of the launch is (b, h, step j) with j fastest, then h; a CTA's share is
+// [u, u_end).
+struct Piece {
+  int b, h, j0, j1, steps;
+};
+
+template <int D, bool kFp8, int kMT>
+__global__ void __launch_bounds__(kRowsThreads, 2)
+    fa_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Attn p) {
+  using C = RowsCfg<D, kFp8>;
+  constexpr int kKG = kRowsWarps / kMT;        // key groups
+  constexpr int kKeys = kRowsBlk / kKG;        // keys of a block for one warp
+  constexpr int kNT = kKeys / 8;               // 8-key column tiles of S
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ RowsShared sh;
+  volatile uint32_t* abort_flag = &sh.abort_flag;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+  // ---- shares: every thread counts the blocks of a few sequences, the CTA scans the counts
+  const int per = (p.c.B + kRowsThreads - 1) / kRowsThreads;
+  const int b_from = min((int)threadIdx.x * per, p.c.B), b_to = min(b_from + per, p.c.B);
+  const int mine = count_blocks(p, b_from, b_to);
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) sh.scan[warp] = incl;
+  if (threadIdx.x == 0) {
+    sh.abort_flag = 0;
+    sh.first_b = -1;
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&sh.full[s], 1);
+      mbar_init(&sh.empty[s], kRowsWarps);
+    }
+    mbar_init(&sh.sync, 32 * kRowsWarps);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  int before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kRowsThreads / 32; ++w) {
+    if (w < warp) before += sh.scan[w];
+    total += sh.scan[w];
+  }
+  const long long units = (long long)total * p.c.Hkv;
+  const int share = (int)max((units + gridDim.x - 1) / gridDim.x, 1ll);
+  const long long u_first = (long long)blockIdx.x * share;
+  const long long u_end = min(u_first + share, units);
+  {
+    // the thread whose sequences hold the share's first unit finds the sequence
+    const long long from = (long long)before * p.c.Hkv, to = from + (long long)mine * p.c.Hkv;
+    if (u_first < u_end && u_first >= from && u_first < to) {
+      long long u = from;
+      for (int b = b_from; b < b_to; ++b) {
+        const long long n = (long long)RowsItem(p, b).w.steps * p.c.Hkv;
+        if (u_first < u + n) {
+          sh.first_b = b;
+          sh.first_unit = u_first - u;
+          break;
+        }
+        u += n;
+      }
+    }
+  }
+  __syncthreads();
+  if (u_first >= u_end) return;
+
+  if (warp == kRowsWarps) {
+    // ------------------------------------------------------------------ loading warp
+    if (lane == 0) {
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+    }
+    const int page_size = 1 << p.c.page_shift;
+    const int box = min(page_size, kRowsBlk), ppb = kRowsBlk / box;  // box rows, boxes per block
+    const int per_group = 32 / ppb;                                  // blocks whose pages one look-up covers
+    const uint32_t base = smem_u32(smem);
+    int n = 0;
+    bool ok = true;
+    int b = sh.first_b;
+    long long unit = sh.first_unit;
+    for (long long u = u_first; ok && u < u_end && b < p.c.B; ++b, unit = 0) {
+      const RowsItem it(p, b);
+      if (it.w.steps == 0) continue;
+      int h = (int)(unit / it.w.steps), j0 = (int)(unit - (long long)h * it.w.steps);
+      for (; ok && h < p.c.Hkv && u < u_end; ++h, j0 = 0) {
+        const int j1 = (int)min((long long)it.w.steps, j0 + (u_end - u));
+        u += j1 - j0;
+        for (int jg = j0; ok && jg < j1; jg += per_group) {
+          const int jl = jg + lane / ppb;
+          int page = p.c.num_pages;  // out of range: zeros
+          if (jl < j1) {
+            const int key = it.w.at(jl) + (lane % ppb) * box;
+            if (it.w.any(key, box)) {
+              const int x = find_page(p.c, b, key, kSitePagedPage);
+              if (x >= 0) page = x;
+            }
+          }
+          for (int jj = 0; jj < per_group && jg + jj < j1; ++jj, ++n) {
+            const int s = n % C::kStages;
+            ok = __all_sync(0xffffffffu,
+                            mbar_wait(&sh.empty[s], ((n / C::kStages) & 1) ^ 1, abort_flag, p.c.status));
+            if (!ok) break;
+            const int pg = __shfl_sync(0xffffffffu, page, jj * ppb + lane % ppb);
+            const bool loads = lane < ppb, real = loads && pg < p.c.num_pages;
+            const int scaled = kFp8 ? __popc(__ballot_sync(0xffffffffu, real)) : 0;
+            if (lane == 0) mbar_arrive_expect_tx(&sh.full[s], 2 * C::kTile + scaled * 2 * box * 4);
+            __syncwarp();
+            if (loads) {
+              const int slot = (it.w.at(jg + jj) + lane * box) & (page_size - 1);
+              const uint32_t dst = base + s * 2 * C::kTile + lane * box * C::kAtomBytes;
+#pragma unroll
+              for (int a = 0; a < C::kAtoms; ++a) {
+                tma_load_page(dst + a * kRowsBlk * C::kAtomBytes, &tmK, &sh.full[s], a * C::kAtomElems, slot, h, pg);
+                tma_load_page(dst + C::kTile + a * kRowsBlk * C::kAtomBytes, &tmV, &sh.full[s], a * C::kAtomElems, slot,
+                              h, pg);
+              }
+              if (kFp8 && real) {
+                uint8_t* sc = smem + C::kScaleOff + s * C::kScaleBytes + lane * box * 4;
+                const long long row = pg * p.c.scale_stride + (long long)h * page_size + slot;
+                bulk_load(sc, p.c.k_scale + row, box * 4, &sh.full[s]);
+                bulk_load(sc + kRowsBlk * 4, p.c.v_scale + row, box * 4, &sh.full[s]);
+              }
+            }
+          }
+        }
+      }
+    }
+    if (*abort_flag) {
+      // let copies still in flight land before the CTA's shared memory goes away
+      volatile uint32_t ignore_abort = 0;
+      for (int i = max(0, n - C::kStages); i < n; ++i)
+        mbar_wait(&sh.full[i % C::kStages], (i / C::kStages) & 1, &ignore_abort, p.c.status);
+    }
+    return;
+  }
+
+  // -------------------------------------------------------------------- computing warps
+  const int mt = warp / kKG, kg = warp % kKG;     // row tile, key group
+  const int r0 = mt * 16 + lane / 4;              // this thread's rows: r0 and r0 + 8
+  const int t4 = lane % 4;
+  const uint32_t base = smem_u32(smem);
+  float* buf = reinterpret_cast<float*>(smem + C::kBufOff);
+  int n = 0, syncs = 0;
+  bool ok = true;
+  auto warps_sync = [&]() {
+    mbar_arrive(&sh.sync);
+    return mbar_wait(&sh.sync, syncs++ & 1, abort_flag, p.c.status);
+  };
+  int b = sh.first_b;
+  long long unit = sh.first_unit;
+  bool first_piece = true;
+  for (long long u = u_first; ok && u < u_end && b < p.c.B; ++b, unit = 0) {
+    const RowsItem it(p, b);
+    if (it.w.steps == 0) continue;
+    int h = (int)(unit / it.w.steps), j0 = (int)(unit - (long long)h * it.w.steps);
+    for (; ok && h < p.c.Hkv && u < u_end; ++h, j0 = 0) {
+      const int steps = it.w.steps;
+      const int j1 = (int)min((long long)steps, j0 + (u_end - u));
+      const long long u_item = u - j0;   // the item's first unit
+      u += j1 - j0;
+      // ---- Q fragments of this warp's 16 rows
+      int pos[2];          // positions of the thread's two rows; -1 (sees nothing) past the last row
+      float c_row[2] = {p.scale_log2, p.scale_log2};
+      uint32_t qf[D / 16][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = r0 + 8 * i;
+        const int t = r / p.group;
+        const bool valid = r < it.rows;
+        pos[i] = valid ? it.s.pos0 + t : -1;
+        const __nv_bfloat16* qr =
+            p.q + (long long)(it.s.q0 + t) * p.q_stride + (long long)(h * p.group + (r - t * p.group)) * D;
+        if constexpr (!kFp8) {
+          // BF16: columns 2t, 2t + 1 and 2t + 8, 2t + 9 of each 16
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            qf[kk][i] = valid ? __ldg(reinterpret_cast<const uint32_t*>(qr + kk * 16 + 2 * t4)) : 0u;
+            qf[kk][i + 2] = valid ? __ldg(reinterpret_cast<const uint32_t*>(qr + kk * 16 + 8 + 2 * t4)) : 0u;
+          }
+        } else {
+          // E4M3: columns 4t .. 4t + 3 of each 16, the order in which K's codes arrive
+          uint2 w[D / 16];
+          uint32_t amax = 0;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            w[kk] = valid ? __ldg(reinterpret_cast<const uint2*>(qr + kk * 16 + 4 * t4)) : make_uint2(0, 0);
+            amax = max(amax, max(max((w[kk].x & 0x7FFFu) << 16, w[kk].x & 0x7FFF0000u),
+                                 max((w[kk].y & 0x7FFFu) << 16, w[kk].y & 0x7FFF0000u)));
+          }
+          amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+          amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+          int e = (int)(amax >> 23) - 127;
+          // zero rows, and rows under 2^-126 (whose factor would overflow), go unscaled by it; rows
+          // with Inf or NaN keep them
+          if (amax == 0 || amax >= 0x7F800000u) e = 0;
+          e = min(max(e, -126), 126);
+          const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+          c_row[i] = p.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            qf[kk][i] = pack_f16x2(__uint_as_float(w[kk].x << 16) * down, __uint_as_float(w[kk].x & 0xFFFF0000u) * down);
+            qf[kk][i + 2] =
+                pack_f16x2(__uint_as_float(w[kk].y << 16) * down, __uint_as_float(w[kk].y & 0xFFFF0000u) * down);
+          }
+        }
+      }
+      float o[D / 8][4];
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      float vref = 0.f;   // E4M3: O is in units of this V scale
+      for (int j = j0; j < j1; ++j, ++n) {
+        const int s = n % C::kStages;
+        ok = __all_sync(0xffffffffu, mbar_wait(&sh.full[s], (n / C::kStages) & 1, abort_flag, p.c.status));
+        if (!ok) break;
+        const uint32_t sK = base + s * 2 * C::kTile, sV = sK + C::kTile;
+        const int row_k = kg * kKeys;            // this warp's first key within the block
+        const int key0 = it.w.at(j) + row_k;     // ... and its position
+        const bool edge = !it.w.all(p, it.w.at(j), it.s.pos0, it.s.kv - 1);
+        if (edge) {
+          // V rows that no row sees may hold anything: 0 * NaN must not reach the product
+          for (int i = lane; i < kKeys * (C::kRowBytes / 16); i += 32) {
+            const int r = i / (C::kRowBytes / 16), x = i % (C::kRowBytes / 16);
+            if (!it.w.seen(key0 + r))
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(C::chunk(sV, row_k + r, x)), "r"(0)
+                           : "memory");
+          }
+          __syncwarp();
+        }
+        // ---- S = Q K^T
+        float sc[kNT][4];
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[nt][e] = 0.f;
+#pragma unroll
+          for (int x = 0; x < C::kRowBytes / 16; x += 4) {
+            uint32_t f[4];
+            ldsm4(f, C::chunk(sK, row_k + nt * 8 + (lane & 7), x + lane / 8));
+            if constexpr (!kFp8) {
+              mma16816<false>(sc[nt], qf[x / 2], f[0], f[1]);
+              mma16816<false>(sc[nt], qf[x / 2 + 1], f[2], f[3]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) mma16816<true>(sc[nt], qf[x + e], codes_f16x2(f[e]), codes_hi_f16x2(f[e]));
+            }
+          }
+        }
+        // ---- scores in units of log2, scales of K, mask
+        const float* ks = reinterpret_cast<const float*>(smem + C::kScaleOff + s * C::kScaleBytes) + row_k;
+        const float* vs = ks + kRowsBlk;
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) {
+          if constexpr (kFp8) {
+            const float2 f = *reinterpret_cast<const float2*>(ks + nt * 8 + 2 * t4);
+            sc[nt][0] *= f.x * c_row[0];
+            sc[nt][1] *= f.y * c_row[0];
+            sc[nt][2] *= f.x * c_row[1];
+            sc[nt][3] *= f.y * c_row[1];
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[nt][e] *= c_row[0];
+          }
+          if (edge) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int key = key0 + nt * 8 + 2 * t4 + (e & 1), at = pos[e >> 1];
+              const bool see = key <= at && (!p.window || at - key < p.window || key < p.sinks);
+              if (!see) sc[nt][e] = -INFINITY;
+            }
+          }
+        }
+        // ---- running maximum and sum of each row
+        float f_row[2], mu[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float mx = -INFINITY;
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt) mx = max3f(mx, sc[nt][2 * i], sc[nt][2 * i + 1]);
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const float m_new = fmaxf(m[i], mx);
+          mu[i] = m_new == -INFINITY ? 0.f : m_new;
+          f_row[i] = ex2_approx(m[i] - mu[i]);
+          m[i] = m_new;
+          float sum = 0.f;
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt) {
+            sc[nt][2 * i] = ex2_approx(sc[nt][2 * i] - mu[i]);
+            sc[nt][2 * i + 1] = ex2_approx(sc[nt][2 * i + 1] - mu[i]);
+            sum += sc[nt][2 * i] + sc[nt][2 * i + 1];
+          }
+          l[i] = l[i] * f_row[i] + sum;
+        }
+        if constexpr (kFp8) {
+          // V's scales, relative to the largest one that the output holds so far
+          float2 v2[kNT];
+          float top = 0.f;
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt) {
+            v2[nt] = *reinterpret_cast<const float2*>(vs + nt * 8 + 2 * t4);
+            if (edge) {
+              if (!it.w.seen(key0 + nt * 8 + 2 * t4)) v2[nt].x = 0.f;
+              if (!it.w.seen(key0 + nt * 8 + 2 * t4 + 1)) v2[nt].y = 0.f;
+            }
+            top = max3f(top, v2[nt].x, v2[nt].y);
+          }
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          if (top > vref) {
+            const float ratio = vref / top;
+            f_row[0] *= ratio;
+            f_row[1] *= ratio;
+            vref = top;
+          }
+          const float inv = vref > 0.f ? 1.f / vref : 0.f;
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt) {
+            const float a = v2[nt].x * inv, c = v2[nt].y * inv;
+            sc[nt][0] *= a;
+            sc[nt][1] *= c;
+            sc[nt][2] *= a;
+            sc[nt][3] *= c;
+          }
+        }
+        if (__any_sync(0xffffffffu, f_row[0] != 1.f || f_row[1] != 1.f)) {
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            mul2(o[i][0], o[i][1], o[i][0], o[i][1], f_row[0], f_row[0]);
+            mul2(o[i][2], o[i][3], o[i][2], o[i][3], f_row[1], f_row[1]);
+          }
+        }
+        // ---- O += P V: 16 keys per step
+#pragma unroll
+        for (int k2 = 0; k2 < kNT / 2; ++k2) {
+          uint32_t a[4];
+          if constexpr (!kFp8) {
+            a[0] = pack_bf16x2(sc[2 * k2][0], sc[2 * k2][1]);
+            a[1] = pack_bf16x2(sc[2 * k2][2], sc[2 * k2][3]);
+            a[2] = pack_bf16x2(sc[2 * k2 + 1][0], sc[2 * k2 + 1][1]);
+            a[3] = pack_bf16x2(sc[2 * k2 + 1][2], sc[2 * k2 + 1][3]);
+          } else {
+            a[0] = pack_f16x2(sc[2 * k2][0], sc[2 * k2][1]);
+            a[1] = pack_f16x2(sc[2 * k2][2], sc[2 * k2][3]);
+            a[2] = pack_f16x2(sc[2 * k2 + 1][0], sc[2 * k2 + 1][1]);
+            a[3] = pack_f16x2(sc[2 * k2 + 1][2], sc[2 * k2 + 1][3]);
+          }
+          const int vr = row_k + k2 * 16 + (lane & 15);  // matrices: keys 0-7, 8-15 of chunk x, then of x + 1
+#pragma unroll
+          for (int x = 0; x < C::kRowBytes / 16; x += 2) {
+            uint32_t f[4];
+            ldsm4_t(f, C::chunk(sV, vr, x + lane / 16));
+            if constexpr (!kFp8) {
+              mma16816<false>(o[x], a, f[0], f[1]);
+              mma16816<false>(o[x + 1], a, f[2], f[3]);
+            } else {
+              // each 16-bit element is two columns' codes: bytes (key, col) (key, col + 1) (key + 1, ..)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t lo = __byte_perm(f[2 * e], 0, 0x3120), hi = __byte_perm(f[2 * e + 1], 0, 0x3120);
+                mma16816<true>(o[2 * (x + e)], a, codes_f16x2(lo), codes_f16x2(hi));
+                mma16816<true>(o[2 * (x + e) + 1], a, codes_hi_f16x2(lo), codes_hi_f16x2(hi));
+              }
+            }
+          }
+        }
+        if (edge) fence_proxy_async_smem();  // the zeroed rows precede the stage's next TMA write
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.empty[s]);
+      }
+      if (!ok) break;
+      // ---- join the key groups and write
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+        if (t4 == 0) {
+          sh.m[warp][lane / 4 + 8 * i] = m[i];
+          sh.l[warp][lane / 4 + 8 * i] = l[i];
+        }
+      }
+      if (!(ok = __all_sync(0xffffffffu, warps_sync()))) break;
+      const bool whole = j0 == 0 && j1 == steps;
+      const int slot = 2 * blockIdx.x + (first_piece ? 0 : 1);
+      first_piece = false;
+      float w_row[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int rr = lane / 4 + 8 * i;
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < kKG; ++k) top = fmaxf(top, sh.m[mt * kKG + k][rr]);
+        const float tu = top == -INFINITY ? 0.f : top;
+#pragma unroll
+        for (int k = 0; k < kKG; ++k) sum += sh.l[mt * kKG + k][rr] * ex2_approx(sh.m[mt * kKG + k][rr] - tu);
+        const bool empty = top == -INFINITY && sum == 0.f;   // no visible key (a NaN score is not that)
+        w_row[i] = empty ? 0.f : ex2_approx(m[i] - tu) / sum * (kFp8 ? vref : 1.f);
+        const float lse = empty ? -INFINITY : top * 0.6931471805599453f + logf(sum);
+        const int r = r0 + 8 * i;
+        if (kg == 0 && t4 == 0 && r < it.rows) {
+          if (!whole) {
+            p.part_lse[(long long)slot * (16 * kMT) + r] = lse;
+          } else if (p.lse) {
+            const int t = r / p.group;
+            p.lse[(long long)(it.s.q0 + t) * p.Hq + h * p.group + (r - t * p.group)] = lse;
+          }
+        }
+        if (whole) report_nonfinite((kg == 0 && t4 == 0 && r < it.rows && !empty && !(fabsf(lse) < INFINITY)) ? 1u : 0u, p.c.status, kOutLse);
+      }
+      uint32_t bad = 0;
+#pragma unroll
+      for (int cc = 0; cc < D / 32; ++cc) {   // 32 columns at a time through the buffer
+        float* mine_buf = buf + warp * 16 * 32;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float* dst = mine_buf + (lane / 4 + 8 * i) * 32;
+          if constexpr (!kFp8) {
+#pragma unroll
+            for (int q4 = 0; q4 < 4; ++q4)
+              *reinterpret_cast<float2*>(dst + q4 * 8 + 2 * t4) =
+                  make_float2(o[cc * 4 + q4][2 * i] * w_row[i], o[cc * 4 + q4][2 * i + 1] * w_row[i]);
+          } else {
+#pragma unroll
+            for (int q2 = 0; q2 < 2; ++q2) {
+              const int c16 = cc * 2 + q2;
+              *reinterpret_cast<float4*>(dst + q2 * 16 + 4 * t4) =
+                  make_float4(o[2 * c16][2 * i] * w_row[i], o[2 * c16 + 1][2 * i] * w_row[i],
+                              o[2 * c16][2 * i + 1] * w_row[i], o[2 * c16 + 1][2 * i + 1] * w_row[i]);
+            }
+          }
+        }
+        if (!(ok = __all_sync(0xffffffffu, warps_sync()))) break;
+#pragma unroll
+        for (int i = 0; i < kMT; ++i) {
+          const int idx = threadIdx.x + i * 128;          // of 16 kMT rows x 8 groups of four columns
+          const int r = idx / 8, c4 = (idx % 8) * 4;
+          float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int k = 0; k < kKG; ++k) {
+            const float4 x =
+                *reinterpret_cast<const float4*>(buf + ((r / 16) * kKG + k) * 16 * 32 + (r % 16) * 32 + c4);
+            sum.x += x.x;
+            sum.y += x.y;
+            sum.z += x.z;
+            sum.w += x.w;
+          }
+          if (r < it.rows) {
+            if (!whole) {
+              *reinterpret_cast<float4*>(p.part_o + ((long long)slot * (16 * kMT) + r) * D + cc * 32 + c4) = sum;
+            } else {
+              const int t = r / p.group;
+              const uint2 v = make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
+              bad += nonfinite_bf16x2(v.x) + nonfinite_bf16x2(v.y);
+              *reinterpret_cast<uint2*>(
+                  p.o + ((long long)(it.s.q0 + t) * p.Hq + h * p.group + (r - t * p.group)) * D + cc * 32 + c4) = v;
+            }
+          }
+        }
+        if (!(ok = __all_sync(0xffffffffu, warps_sync()))) break;
+      }
+      if (!ok) break;
+      report_nonfinite(bad, p.c.status, kOutO);
+      // the CTA with an item's first step tells the joining kernel where its pieces are
+      if (j0 == 0 && threadIdx.x == 0) {
+        const int last_cta = (int)((u_item + steps - 1) / share);
+        p.part_info[b * p.c.Hkv + h] = make_int4((int)blockIdx.x, last_cta, slot, it.rows);
+      }
+    }
+  }
+}
+
+// Joins the pieces of split items: out = sum_i w_i o_i, w_i = exp(lse_i - lse), lse = log sum exp(lse_i).
+// One CTA per (sequence, kv head), one warp per row.  The first piece is in the slot that its CTA
+// recorded, the others are the first pieces of the CTAs that follow.
+template <int D>
+__global__ void __launch_bounds__(256) fa_rows_combine(const Attn p, int slot_rows) {
+  const int b = blockIdx.x / p.c.Hkv, h = blockIdx.x % p.c.Hkv;
+  const RowsItem it(p, b);
+  if (it.w.steps == 0) return;
+  const int4 info = p.part_info[blockIdx.x];
+  const int pieces = info.y - info.x + 1;
+  if (pieces < 2) return;
+  const int lane = threadIdx.x % 32;
+  constexpr int kPer = D / 32;   // columns per lane: 2 or 4
+  for (int r = threadIdx.x / 32; r < it.rows; r += 8) {
+    float top = -INFINITY;
+    for (int i = lane; i < pieces; i += 32) {
+      const long long slot = i == 0 ? info.z : 2ll * (info.x + i);
+      top = fmaxf(top, p.part_lse[slot * slot_rows + r]);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    const float tu = top == -INFINITY ? 0.f : top;
+    float sum = 0.f, acc[kPer];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+    for (int i = 0; i < pieces; ++i) {
+      const long long slot = i == 0 ? info.z : 2ll * (info.x + i);
+      const float w = ex2_approx((p.part_lse[slot * slot_rows + r] - tu) * 1.4426950408889634f);
+      const float* src = p.part_o + (slot * slot_rows + r) * D + lane * kPer;
+      sum += w;
+      if constexpr (kPer == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(src);
+        acc[0] = fmaf(w, x.x, acc[0]);
+        acc[1] = fmaf(w, x.y, acc[1]);
+        acc[2] = fmaf(w, x.z, acc[2]);
+        acc[3] = fmaf(w, x.w, acc[3]);
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(src);
+        acc[0] = fmaf(w, x.x, acc[0]);
+        acc[1] = fmaf(w, x.y, acc[1]);
+      }
+    }
+    const bool empty = top == -INFINITY && sum == 0.f;
+    const float inv = empty ? 0.f : 1.f / sum;
+    const int t = r / p.group;
+    const long long row = (long long)(it.s.q0 + t) * p.Hq + h * p.group + (r - t * p.group);
+    uint32_t w2[kPer / 2], bad = 0;
+#pragma unroll
+    for (int e = 0; e < kPer / 2; ++e) {
+      w2[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+      bad += nonfinite_bf16x2(w2[e]);
+    }
+    if constexpr (kPer == 4)
+      *reinterpret_cast<uint2*>(p.o + row * D + lane * 4) = make_uint2(w2[0], w2[1]);
+    else
+      *reinterpret_cast<uint32_t*>(p.o + row * D + lane * 2) = w2[0];
+    report_nonfinite(bad, p.c.status, kOutO);
+    const float lse = empty ? -INFINITY : top + logf(sum);
+    report_nonfinite((lane == 0 && !empty && !(fabsf(lse) < INFINITY)) ? 1u : 0u, p.c.status, kOutLse);
+    if (lane == 0 && p.lse) p.lse[row] = lse;
+  }
+}
+
+template <int D, bool kFp8, int kMT>
+static int launch(const CUtensorMap& tk, const CUtensorMap& tv, const Attn& p, int grid, cudaStream_t s) {
+  using C = RowsCfg<D, kFp8>;
+  auto kern = fa_rows_kernel<D, kFp8, kMT>;
+  static std::atomic<uint64_t> prepared{0};
+  int rc = prepare_kernel(reinterpret_cast<const void*>(kern), C::kSmemBytes, kRowsThreads, 0, "few-rows kernel",
+                          &prepared);
+  if (rc) return rc;
+  kern<<<grid, kRowsThreads, C::kSmemBytes, s>>>(tk, tv, p);
+  if ((rc = check_cuda(cudaGetLastError(), "launch fa_rows_kernel"))) return rc;
+  fa_rows_combine<D><<<p.c.B * p.c.Hkv, 256, 0, s>>>(p, 16 * kMT);
+  return check_cuda(cudaGetLastError(), "launch fa_rows_combine");
+}
+
+template <int D, bool kFp8>
+static int launch_tiles(const CUtensorMap& tk, const CUtensorMap& tv, const Attn& p, int grid, cudaStream_t s) {
+  if (p.few_rows <= 16) return launch<D, kFp8, 1>(tk, tv, p, grid, s);
+  if (p.few_rows <= 32) return launch<D, kFp8, 2>(tk, tv, p, grid, s);
+  return launch<D, kFp8, 4>(tk, tv, p, grid, s);
+}
+
+int launch_rows(const Attn& p, int d, bool fp8, cudaStream_t s) {
+  const int page_size = 1 << p.c.page_shift, box = page_size < kRowsBlk ? page_size : kRowsBlk;
+  CUtensorMap tk, tv;
+  int rc;
+  if ((rc = make_tmap_pages(&tk, p.c.k, fp8, d, page_size, p.c.Hkv, p.c.num_pages, p.c.page_stride, box)) ||
+      (rc = make_tmap_pages(&tv, p.c.v, fp8, d, page_size, p.c.Hkv, p.c.num_pages, p.c.page_stride, box)))
+    return rc;
+  int grid = 2 * sm_count();
+  if (grid > kRowsMaxCtas) grid = kRowsMaxCtas;
+  if (d == 64)
+    return fp8 ? launch_tiles<64, true>(tk, tv, p, grid, s) : launch_tiles<64, false>(tk, tv, p, grid, s);
+  return fp8 ? launch_tiles<128, true>(tk, tv, p, grid, s) : launch_tiles<128, false>(tk, tv, p, grid, s);
+}
+
+}  // namespace paged
+}  // namespace fa

@@ -50,7 +50,7 @@ __device__ __forceinline__ uint32_t nonfinite_bf16x2(uint32_t w) {
 }
 
 // Site ids of the device-side index checks (fa_device_report.bounds_site).  The alignment
-// check is always compiled; the others only in builds with FA_DEBUG_BOUNDS, where the
+// check and the paged caches' are always compiled; the others only in builds with FA_DEBUG_BOUNDS, where the
 // computed global, shared-memory, tensor-memory and TMA indices are checked before use (the
 // fixed tensor-memory plans are checked at compile time).
 enum : uint32_t {
@@ -68,6 +68,11 @@ enum : uint32_t {
   kSiteBwdDqStage = 23,    // backward: a dQ staging row leaves the staging ring
   kSiteBwdDqCoord = 24,    // backward: a dQ reduce-add box starts outside the accumulator
   kSiteBwdKVRow = 25,      // backward: a dK / dV row write runs past the output
+  // paged caches: entries of the caller's device arrays, checked in every build
+  kSitePagedAppend = 30,   // append: a position or a page of the table is out of range
+  kSitePagedRead = 31,     // read: a position or a page of the table is out of range
+  kSitePagedLen = 32,      // attention: a sequence's length exceeds its table, or its rows the tensor
+  kSitePagedPage = 33,     // attention: a page of the table is out of range
 };
 
 // Record a failed index check: the flag, and the site and index of the first one seen.
