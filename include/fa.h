@@ -221,7 +221,9 @@ int fa_bwd_staged(const void* q, const void* k, const void* v, const void* o, co
 /*
  * fa_bwd_window -- the backward of fa_fwd_window: fa_bwd with the mask of `window` and `sinks`
  * (see fa_fwd_window; o and lse are that forward's).  Workspace, outputs and errors are
- * fa_bwd's; the gradients of keys that no query sees are zero.
+ * fa_bwd's; the gradients of keys that no query sees are zero.  For queries that see at most 16
+ * keys delta is summed from probabilities recomputed in FP32, not from the rounded o, whose error
+ * would show in dq and dk there.
  */
 int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO,
                   void* dq, void* dk, void* dv, float* delta_out, int B, int H, int N, int d, int window, int sinks,

@@ -136,8 +136,25 @@ struct Params {
 // Over the padded rows (bh, q < N_pad): delta = rowsum(dO o O) in FP32, lse2 = lse log2(e)
 // and dQ_acc = 0 for q < N; delta = 0 and lse2 = +inf (so P = 0) for the padding.
 // d/8 lanes per row, 16-byte loads.
-template <int D>
-__global__ void __launch_bounds__(256) fa_bwd_preprocess(const __nv_bfloat16* __restrict__ o,
+//
+// kWin (windowed kernels): a row that sees few keys takes delta = sum_j P_ij (dO_i . V_j) from
+// probabilities recomputed in FP32 instead.  The stored O is rounded to BF16, which puts an error of
+// about 2^-9 |dO||O| on rowsum(dO o O); dS = P o (dP - delta) is a difference of terms of that size,
+// and with few keys nothing averages the error out: with 2 visible keys dq and dk were 0.6-1.0 %
+// off (relative Frobenius), 0.37 % from 16 keys on, whose BF16 rounding of dS and of the result
+// makes up 0.24 %.  At most kFewKeys keys per row, so the cost stays that of a short loop: windows
+// of that size only, and the first rows of longer ones.
+constexpr int kFewKeys = 16;
+
+// What the recomputation reads.
+struct FewKeys {
+  const __nv_bfloat16 *q, *k, *v;
+  int window, sinks;
+  float scale_log2;
+};
+
+template <int D, bool kWin>
+__global__ void __launch_bounds__(256) fa_bwd_preprocess(const FewKeys few, const __nv_bfloat16* __restrict__ o,
                                                          const __nv_bfloat16* __restrict__ dO,
                                                          const float* __restrict__ lse, float* __restrict__ delta,
                                                          float* __restrict__ lse2, float* __restrict__ delta_out,
@@ -172,6 +189,51 @@ __global__ void __launch_bounds__(256) fa_bwd_preprocess(const __nv_bfloat16* __
   }
 #pragma unroll
   for (int off = kLanesPerRow / 2; off > 0; off /= 2) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+  if constexpr (kWin) {
+    const int lo = max(0, q - few.window + 1), n_sink = min(few.sinks, lo);
+    const int seen = q + 1 - lo + n_sink;
+    const bool recompute = valid && seen <= kFewKeys;
+    const int most = (int)__reduce_max_sync(0xffffffffu, (unsigned)(recompute ? seen : 0));
+    if (most > 0) {   // the same for the whole warp
+      float qv[8], dv[8], sum = 0.f;
+      const float lse2_row = valid ? lse[row] * 1.4426950408889634f : 0.f;
+      auto widen = [](const __nv_bfloat16* src, float (&x)[8]) {
+        const uint4 u = *reinterpret_cast<const uint4*>(src);
+        const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = __bfloat1622float2(h[i]);
+          x[2 * i] = f.x;
+          x[2 * i + 1] = f.y;
+        }
+      };
+      if (recompute) {
+        widen(few.q + row * D + c, qv);
+        widen(dO + row * D + c, dv);
+      }
+      for (int j = 0; j < most; ++j) {
+        float s = 0.f, dp = 0.f;
+        if (recompute && j < seen) {
+          const long long key = bh * N + (j < n_sink ? j : lo + j - n_sink);
+          float kv[8], vv[8];
+          widen(few.k + key * D + c, kv);
+          widen(few.v + key * D + c, vv);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            s = fmaf(qv[i], kv[i], s);
+            dp = fmaf(dv[i], vv[i], dp);
+          }
+        }
+#pragma unroll
+        for (int off = kLanesPerRow / 2; off > 0; off /= 2) {
+          s += __shfl_xor_sync(0xffffffffu, s, off);
+          dp += __shfl_xor_sync(0xffffffffu, dp, off);
+        }
+        if (recompute && j < seen) sum = fmaf(ex2_approx(fmaf(s, few.scale_log2, -lse2_row)), dp, sum);
+      }
+      if (recompute) acc = sum;
+    }
+  }
   if (prow < rows_pad && (lane % kLanesPerRow) == 0) {
     delta[prow] = acc;
     lse2[prow] = valid ? lse[row] * 1.4426950408889634f : INFINITY;
@@ -782,8 +844,12 @@ int launch_bwd(const void* q, const void* k, const void* v, const void* o, const
     constexpr int rows_per_block = 8 * (32 / (D / 8));
     const long long rows_pad = (long long)B * H * N_pad;
     const long long grid = (rows_pad + rows_per_block - 1) / rows_per_block;
-    bwd::fa_bwd_preprocess<D><<<(unsigned)grid, 256, 0, stream>>>(
-        static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(dO), lse, sc.delta, sc.lse2,
+    const bwd::FewKeys few{static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
+                           static_cast<const __nv_bfloat16*>(v), window < N ? window : N, sinks < N ? sinks : N,
+                           scale * 1.4426950408889634f};
+    auto pre = window ? bwd::fa_bwd_preprocess<D, true> : bwd::fa_bwd_preprocess<D, false>;
+    pre<<<(unsigned)grid, 256, 0, stream>>>(
+        few, static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(dO), lse, sc.delta, sc.lse2,
         delta_out, sc.dq_acc, rows_pad, N, N_pad);
     if ((rc = check_cuda(cudaGetLastError(), "launch fa_bwd_preprocess"))) return rc;
   }
