@@ -138,21 +138,41 @@ def _check(rc: int):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    if torch.cuda.is_initialized():   # the current stream's handle, without a Stream object for it
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return torch.cuda.current_stream().cuda_stream
+
+
+class _OnDevice:
+    """Makes a tensor's device current for a call, where it is not already."""
+
+    def __init__(self, t):
+        self.dev, self.back = t.get_device(), None
+
+    def __enter__(self):
+        now = torch._C._cuda_getDevice()
+        if now != self.dev:
+            torch.cuda.set_device(self.dev)
+            self.back = now
+
+    def __exit__(self, *exc):
+        if self.back is not None:
+            torch.cuda.set_device(self.back)
 
 
 def _check_qkv(*ts):
+    shape, dev = ts[0].shape, ts[0].get_device()
     for t in ts:
-        if not (t.is_cuda and t.dtype == torch.bfloat16 and t.is_contiguous() and t.dim() == 4):
+        if not (t.is_cuda and t.dtype is torch.bfloat16 and t.is_contiguous() and t.dim() == 4):
             raise ValueError("expected contiguous CUDA bfloat16 tensors of shape [B, H, N, d]")
-    if any(t.shape != ts[0].shape for t in ts):
-        raise ValueError("q, k, v (and o, dO) must have the same shape")
+        if t.shape != shape or t.get_device() != dev:
+            raise ValueError("q, k, v (and o, dO) must have the same shape and device")
 
 
 # ----------------------------------------------------------------- raw C calls
@@ -280,10 +300,11 @@ def forward(q, k, v, causal: bool = True, scale=None, stable: int = 1, beta: flo
     o = torch.empty_like(q)
     lse = torch.empty((B, H, N), device=q.device, dtype=torch.float32)
     sd = _stats_dict(B, H, N, q.device) if stats else None
-    if window is None:
-        _check(fa_fwd(q, k, v, o, lse, causal, scale, stable, beta, sd, stream))
-    else:
-        _check(fa_fwd_window(q, k, v, o, lse, window, sinks, scale, stable, beta, sd, stream))
+    with _OnDevice(q):
+        if window is None:
+            _check(fa_fwd(q, k, v, o, lse, causal, scale, stable, beta, sd, stream))
+        else:
+            _check(fa_fwd_window(q, k, v, o, lse, window, sinks, scale, stable, beta, sd, stream))
     return (o, lse, sd) if stats else (o, lse)
 
 
@@ -330,60 +351,68 @@ def backward(q, k, v, o, lse, do, causal: bool = True, scale=None, workspace=Non
         workspace = torch.empty(fa_bwd_workspace_size(B, H, N, d), device=q.device, dtype=torch.uint8)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     delta = torch.empty((B, H, N), device=q.device, dtype=torch.float32) if want_delta else None
-    if window is None:
-        _check(fa_bwd(q, k, v, o, lse, do, dq, dk, dv, delta, causal, scale, workspace, stream))
-    else:
-        _check(fa_bwd_window(q, k, v, o, lse, do, dq, dk, dv, delta, window, sinks, scale, workspace, stream))
+    with _OnDevice(q):
+        if window is None:
+            _check(fa_bwd(q, k, v, o, lse, do, dq, dk, dv, delta, causal, scale, workspace, stream))
+        else:
+            _check(fa_bwd_window(q, k, v, o, lse, do, dq, dk, dv, delta, window, sinks, scale, workspace, stream))
     return (dq, dk, dv, delta) if want_delta else (dq, dk, dv)
 
 
 # ----------------------------------------------------------------- paged key/value caches
 
-def _int32(t, n, name, device):
-    if not (t.dtype == torch.int32 and t.dim() == 1 and t.is_contiguous() and t.device == device):
+def _int32(t, n, name, dev):
+    if t.dtype is not torch.int32 or t.get_device() != dev or t.dim() != 1 or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 vector on the cache's device")
-    if t.shape[0] != n:
-        raise ValueError(f"{name} must have {n} entries (got {t.shape[0]})")
+    if t.numel() != n:
+        raise ValueError(f"{name} must have {n} entries (got {t.numel()})")
+    return t.data_ptr()
 
 
 def _paged(k, v, table, kv_len, k_scale, v_scale):
     """The fa_paged_kv of a cache's tensors (shapes, types and strides checked)."""
-    if not (k.is_cuda and k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype and k.device == v.device):
+    shape, dtype, dev = k.shape, k.dtype, k.get_device()
+    if dev < 0 or len(shape) != 4 or v.shape != shape or v.dtype is not dtype or v.get_device() != dev:
         raise ValueError("expected CUDA cache tensors of one shape [pages, Hkv, page_size, d] and one type")
-    P, H, S, d = k.shape
-    if k.stride() != v.stride() or k.stride()[1:] != (S * d, d, 1):
+    P, H, S, d = shape
+    stride = k.stride()
+    if v.stride() != stride or stride[1:] != (S * d, d, 1):
         raise ValueError("cache pages must be contiguous, with the same page stride for K and V")
-    if not (table.dtype == torch.int32 and table.dim() == 2 and table.device == k.device and table.stride(1) == 1):
+    rows = table.stride()
+    if table.dtype is not torch.int32 or len(rows) != 2 or rows[1] != 1 or table.get_device() != dev:
         raise ValueError("block_table must be an int32 tensor [B, max_pages] on the cache's device, rows contiguous")
-    _int32(kv_len, table.shape[0], "kv_len", k.device)
-    out = PagedKV(k.data_ptr(), v.data_ptr(), None, None, max(k.stride(0), H * S * d), 0, table.data_ptr(),
-                  max(table.stride(0), table.shape[1]), kv_len.data_ptr(), table.shape[0], H, d, S, P, table.shape[1],
-                  FA_KV_BF16)
-    if k.dtype == torch.bfloat16:
+    B, width = table.shape
+    kv_ptr = _int32(kv_len, B, "kv_len", dev)
+    ks = vs = None
+    scale_stride, code = 0, FA_KV_BF16
+    if dtype is torch.bfloat16:
         if k_scale is not None or v_scale is not None:
             raise ValueError("a bfloat16 cache has no scales")
-        return out
-    if k.dtype not in (torch.uint8, torch.float8_e4m3fn):
+    elif dtype is torch.uint8 or dtype is torch.float8_e4m3fn:
+        if k_scale is None or v_scale is None:
+            raise ValueError("an E4M3 cache needs k_scale and v_scale")
+        scale_stride = k_scale.stride()[0] if k_scale.dim() else 0
+        for s in (k_scale, v_scale):
+            if s.dtype is not torch.float32 or s.shape != shape[:3] or s.get_device() != dev or \
+                    s.stride() != (scale_stride, S, 1):
+                raise ValueError("k_scale and v_scale must be float32 [pages, Hkv, page_size], pages contiguous, with "
+                                 "the same page stride")
+        ks, vs, code = k_scale.data_ptr(), v_scale.data_ptr(), FA_KV_E4M3
+        scale_stride = max(scale_stride, H * S)
+    else:
         raise ValueError("cache tensors must be bfloat16, or uint8 (or float8_e4m3fn) E4M3 codes")
-    for s in (k_scale, v_scale):
-        if s is None or not (s.dtype == torch.float32 and s.shape == (P, H, S) and s.device == k.device and
-                             s.stride()[1:] == (S, 1) and s.stride(0) == k_scale.stride(0)):
-            raise ValueError("an E4M3 cache needs float32 k_scale and v_scale [pages, Hkv, page_size], pages "
-                             "contiguous, with the same page stride")
-    out.k_scale, out.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
-    out.scale_stride, out.dtype = max(k_scale.stride(0), H * S), FA_KV_E4M3
-    return out
+    return PagedKV(k.data_ptr(), v.data_ptr(), ks, vs, max(stride[0], H * S * d), scale_stride, table.data_ptr(),
+                   max(rows[0], width), kv_ptr, B, H, d, S, P, width, code)
 
 
-def _check_rows(x, heads, d, device, name):
-    if not (x.dtype == torch.bfloat16 and x.dim() == 3 and x.device == device and x.shape[1:] == (heads, d)):
+def _check_rows(x, heads, d, dev, name):
+    """Packed rows [rows, heads, d], a row's heads contiguous: the rows' number and stride."""
+    shape, stride = x.shape, x.stride()
+    if x.dtype is not torch.bfloat16 or x.get_device() != dev or len(shape) != 3 or shape[1] != heads or shape[2] != d:
         raise ValueError(f"{name} must be a CUDA bfloat16 tensor [rows, {heads}, {d}] on the cache's device")
-    if x.shape[0] and x.stride()[1:] != (d, 1):
+    if shape[0] and (stride[2] != 1 or (heads > 1 and stride[1] != d)):
         raise ValueError(f"{name}: a row's heads must be contiguous")
-
-
-def _row_stride(x):
-    return max(x.stride(0), x.shape[1] * x.shape[2])   # one row's stride may be anything
+    return shape[0], max(stride[0], heads * d)   # a single row's stride may be anything
 
 
 def kv_append(k_new, v_new, k_cache, v_cache, block_table, kv_len, q_indptr, k_scale=None, v_scale=None, stream=None):
@@ -395,15 +424,15 @@ def kv_append(k_new, v_new, k_cache, v_cache, block_table, kv_len, q_indptr, k_s
     with float32 scales [pages, Hkv, page_size].  block_table: int32 [B, max_pages].
     """
     kv = _paged(k_cache, v_cache, block_table, kv_len, k_scale, v_scale)
-    _check_rows(k_new, kv.Hkv, kv.d, k_cache.device, "k_new")
-    _check_rows(v_new, kv.Hkv, kv.d, k_cache.device, "v_new")
-    if k_new.shape != v_new.shape or _row_stride(k_new) != _row_stride(v_new):
+    dev = k_cache.get_device()
+    T, stride = rows = _check_rows(k_new, kv.Hkv, kv.d, dev, "k_new")
+    if _check_rows(v_new, kv.Hkv, kv.d, dev, "v_new") != rows:
         raise ValueError("k_new and v_new must have the same rows and row stride")
-    _int32(q_indptr, kv.B + 1, "q_indptr", k_cache.device)
-    if k_new.shape[0]:
-        with torch.cuda.device(k_cache.device):
-            _check(load().fa_kv_append(ctypes.byref(kv), _ptr(k_new), _ptr(v_new), _row_stride(k_new), _ptr(q_indptr),
-                                       k_new.shape[0], _stream(stream)))
+    indptr = _int32(q_indptr, kv.B + 1, "q_indptr", dev)
+    if T:
+        with _OnDevice(k_cache):
+            _check(load().fa_kv_append(ctypes.byref(kv), k_new.data_ptr(), v_new.data_ptr(), stride, indptr, T,
+                                       _stream(stream)))
 
 
 def kv_read(k_cache, v_cache, block_table, kv_len, kv_indptr, rows, k_scale=None, v_scale=None, out=None, stream=None):
@@ -414,17 +443,18 @@ def kv_read(k_cache, v_cache, block_table, kv_len, kv_indptr, rows, k_scale=None
     to) or are not defined (fresh tensors).
     """
     kv = _paged(k_cache, v_cache, block_table, kv_len, k_scale, v_scale)
-    _int32(kv_indptr, kv.B + 1, "kv_indptr", k_cache.device)
+    dev, shape = k_cache.get_device(), (rows, kv.Hkv, kv.d)
+    indptr = _int32(kv_indptr, kv.B + 1, "kv_indptr", dev)
     if out is None:
-        out = tuple(torch.empty((rows, kv.Hkv, kv.d), device=k_cache.device, dtype=torch.bfloat16) for _ in range(2))
-    k, v = out
-    for t in out:
-        _check_rows(t, kv.Hkv, kv.d, k_cache.device, "out")
-        if t.shape[0] != rows or not t.is_contiguous():
-            raise ValueError("out tensors must be contiguous with `rows` rows")
+        k, v = (torch.empty(shape, device=k_cache.device, dtype=torch.bfloat16) for _ in range(2))
+    else:
+        k, v = out
+        for t in out:
+            if _check_rows(t, kv.Hkv, kv.d, dev, "out")[0] != rows or not t.is_contiguous():
+                raise ValueError("out tensors must be contiguous with `rows` rows")
     if rows:
-        with torch.cuda.device(k_cache.device):
-            _check(load().fa_kv_read(ctypes.byref(kv), _ptr(kv_indptr), _ptr(k), _ptr(v), int(rows), _stream(stream)))
+        with _OnDevice(k_cache):
+            _check(load().fa_kv_read(ctypes.byref(kv), indptr, k.data_ptr(), v.data_ptr(), int(rows), _stream(stream)))
     return k, v
 
 
@@ -441,34 +471,40 @@ def forward_paged(q, k_cache, v_cache, block_table, kv_len, q_indptr, max_q, k_s
     sequence stay as they were (undefined in fresh tensors).
     """
     kv = _paged(k_cache, v_cache, block_table, kv_len, k_scale, v_scale)
-    _check_window(True, window, sinks)
-    if window is not None and window < 1:
+    if window is None:
+        if sinks:
+            raise ValueError("sinks need a window")
+        window = 0
+    elif window < 1:
         raise ValueError("window must be >= 1 (None: no window)")
-    dev, d = k_cache.device, kv.d
+    dev, d = k_cache.get_device(), kv.d
     if q.dim() != 3:
         raise ValueError("q must be [T, Hq, d]")
-    T, Hq = q.shape[0], q.shape[1]
-    _check_rows(q, Hq, d, dev, "q")
-    _int32(q_indptr, kv.B + 1, "q_indptr", dev)
+    Hq = q.shape[1]
+    T, stride = _check_rows(q, Hq, d, dev, "q")
+    indptr = _int32(q_indptr, kv.B + 1, "q_indptr", dev)
     if out is None:
-        out = torch.empty((T, Hq, d), device=dev, dtype=torch.bfloat16)
-    elif not (out.dtype == torch.bfloat16 and out.shape == q.shape and out.is_contiguous() and out.device == dev):
+        out = torch.empty((T, Hq, d), device=q.device, dtype=torch.bfloat16)
+    elif out.dtype is not torch.bfloat16 or out.shape != q.shape or not out.is_contiguous() or out.get_device() != dev:
         raise ValueError("out must be a contiguous bfloat16 tensor of q's shape")
     if lse is None:
-        lse = torch.empty((T, Hq), device=dev, dtype=torch.float32)
-    elif not (lse.dtype == torch.float32 and lse.shape == q.shape[:2] and lse.is_contiguous() and lse.device == dev):
+        lse = torch.empty((T, Hq), device=q.device, dtype=torch.float32)
+    elif lse.dtype is not torch.float32 or lse.shape != q.shape[:2] or not lse.is_contiguous() or \
+            lse.get_device() != dev:
         raise ValueError("lse must be a contiguous float32 tensor [T, Hq]")
     if T == 0:
         return out, lse
-    scale = 1.0 / math.sqrt(d) if scale is None else scale
-    with torch.cuda.device(dev):
-        if workspace is None:
-            n = fa_fwd_paged_workspace_size(T, kv.B, max_q, Hq, kv.Hkv, d, kv.max_pages * kv.page_size)
-            workspace = torch.empty(n, device=dev, dtype=torch.uint8)
-        nbytes = workspace.numel() * workspace.element_size()
-        _check(load().fa_fwd_paged(ctypes.byref(kv), _ptr(q), _row_stride(q), _ptr(q_indptr), T, int(max_q), Hq,
-                                   _ptr(out), _ptr(lse), int(window or 0), int(sinks), float(scale),
-                                   _ptr(workspace) if nbytes else None, nbytes, _stream(stream)))
+    lib = load()
+    if workspace is None:
+        n = lib.fa_fwd_paged_workspace_size(T, kv.B, max_q, Hq, kv.Hkv, d, kv.max_pages * kv.page_size)
+        workspace = torch.empty(n, device=q.device, dtype=torch.uint8) if n else None
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the cache's device")
+    ws, nbytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    with _OnDevice(k_cache):
+        _check(lib.fa_fwd_paged(ctypes.byref(kv), q.data_ptr(), stride, indptr, T, int(max_q), Hq, out.data_ptr(),
+                                lse.data_ptr(), window, int(sinks), 1.0 / math.sqrt(d) if scale is None else float(scale),
+                                ws, nbytes, _stream(stream)))
     return out, lse
 
 

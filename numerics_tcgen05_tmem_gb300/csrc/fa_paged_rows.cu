@@ -133,6 +133,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
   constexpr int kKG = kRowsWarps / kMT;        // key groups
   constexpr int kKeys = kRowsBlk / kKG;        // keys of a block for one warp
   constexpr int kNT = kKeys / 8;               // 8-key column tiles of S
+  constexpr int kPair = kMT == 1 ? 2 : 1;      // blocks taken at a time
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ RowsShared sh;
@@ -264,6 +265,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
   const int mt = warp / kKG, kg = warp % kKG;     // row tile, key group
   const int r0 = mt * 16 + lane / 4;              // this thread's rows: r0 and r0 + 8
   const int t4 = lane % 4;
+  const int row_k = kg * kKeys;                   // this warp's first key within a block
   const uint32_t base = smem_u32(smem);
   float* buf = reinterpret_cast<float*>(smem + C::kBufOff);
   int n = 0, syncs = 0;
@@ -336,119 +338,150 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
       float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-      float vref = 0.f;   // E4M3: O is in units of this V scale
-      for (int j = j0; j < j1; ++j, ++n) {
-        const int s = n % C::kStages;
-        ok = __all_sync(0xffffffffu, mbar_wait(&sh.full[s], (n / C::kStages) & 1, abort_flag, p.c.status));
+      float vref = 0.f, v_inv = 0.f;   // E4M3: O is in units of this V scale; its reciprocal
+      // kPair blocks at a time: their products are independent of each other, and the bookkeeping of
+      // the running maximum is paid once for both
+      for (int j = j0; j < j1; j += kPair) {
+        const int nb = min(kPair, j1 - j);
+        float sc[kPair * kNT][4];
+        bool edge = false;
+#pragma unroll
+        for (int x = 0; x < kPair; ++x) {
+          if (x < nb) {
+            const int s = (n + x) % C::kStages, key0 = it.w.at(j + x);
+            ok = __all_sync(0xffffffffu, mbar_wait(&sh.full[s], ((n + x) / C::kStages) & 1, abort_flag, p.c.status));
+            if (!ok) break;
+            const uint32_t sK = base + s * 2 * C::kTile;
+            edge |= !it.w.all(p, key0, it.s.pos0, it.s.kv - 1);
+            // ---- S = Q K^T
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt) {
+              float (&acc)[4] = sc[x * kNT + nt];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[e] = 0.f;
+#pragma unroll
+              for (int c0 = 0; c0 < C::kRowBytes / 16; c0 += 4) {
+                uint32_t f[4];
+                ldsm4(f, C::chunk(sK, row_k + nt * 8 + (lane & 7), c0 + lane / 8));
+                if constexpr (!kFp8) {
+                  mma16816<false>(acc, qf[c0 / 2], f[0], f[1]);
+                  mma16816<false>(acc, qf[c0 / 2 + 1], f[2], f[3]);
+                } else {
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) mma16816<true>(acc, qf[c0 + e], codes_f16x2(f[e]), codes_hi_f16x2(f[e]));
+                }
+              }
+            }
+          } else {
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) sc[x * kNT + nt][e] = -INFINITY;
+          }
+        }
         if (!ok) break;
-        const uint32_t sK = base + s * 2 * C::kTile, sV = sK + C::kTile;
-        const int row_k = kg * kKeys;            // this warp's first key within the block
-        const int key0 = it.w.at(j) + row_k;     // ... and its position
-        const bool edge = !it.w.all(p, it.w.at(j), it.s.pos0, it.s.kv - 1);
+        // ---- scores in units of log2, scales of K
+#pragma unroll
+        for (int x = 0; x < kPair; ++x) {
+          if (x >= nb) break;
+          const float* ks = reinterpret_cast<const float*>(smem + C::kScaleOff + ((n + x) % C::kStages) * C::kScaleBytes) + row_k;
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt) {
+            float (&v)[4] = sc[x * kNT + nt];
+            if constexpr (kFp8) {
+              const float2 f = *reinterpret_cast<const float2*>(ks + nt * 8 + 2 * t4);
+              mul2(v[0], v[1], v[0], v[1], f.x * c_row[0], f.y * c_row[0]);
+              mul2(v[2], v[3], v[2], v[3], f.x * c_row[1], f.y * c_row[1]);
+            } else {
+              mul2(v[0], v[1], v[0], v[1], c_row[0], c_row[0]);
+              mul2(v[2], v[3], v[2], v[3], c_row[0], c_row[0]);
+            }
+          }
+        }
         if (edge) {
-          // V rows that no row sees may hold anything: 0 * NaN must not reach the product
-          for (int i = lane; i < kKeys * (C::kRowBytes / 16); i += 32) {
-            const int r = i / (C::kRowBytes / 16), x = i % (C::kRowBytes / 16);
-            if (!it.w.seen(key0 + r))
-              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(C::chunk(sV, row_k + r, x)), "r"(0)
-                           : "memory");
+#pragma unroll
+          for (int x = 0; x < kPair; ++x) {
+            if (x >= nb) break;
+            const int key0 = it.w.at(j + x) + row_k;
+            // V rows that no row sees may hold anything: 0 * NaN must not reach the product
+            const uint32_t sV = base + ((n + x) % C::kStages) * 2 * C::kTile + C::kTile;
+            for (int i = lane; i < kKeys * (C::kRowBytes / 16); i += 32) {
+              const int r = i / (C::kRowBytes / 16);
+              if (!it.w.seen(key0 + r))
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                 C::chunk(sV, row_k + r, i % (C::kRowBytes / 16))),
+                             "r"(0)
+                             : "memory");
+            }
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int key = key0 + nt * 8 + 2 * t4 + (e & 1), at = pos[e >> 1];
+                const bool see = key <= at && (!p.window || at - key < p.window || key < p.sinks);
+                if (!see) sc[x * kNT + nt][e] = -INFINITY;
+              }
           }
           __syncwarp();
         }
-        // ---- S = Q K^T
-        float sc[kNT][4];
-#pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sc[nt][e] = 0.f;
-#pragma unroll
-          for (int x = 0; x < C::kRowBytes / 16; x += 4) {
-            uint32_t f[4];
-            ldsm4(f, C::chunk(sK, row_k + nt * 8 + (lane & 7), x + lane / 8));
-            if constexpr (!kFp8) {
-              mma16816<false>(sc[nt], qf[x / 2], f[0], f[1]);
-              mma16816<false>(sc[nt], qf[x / 2 + 1], f[2], f[3]);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) mma16816<true>(sc[nt], qf[x + e], codes_f16x2(f[e]), codes_hi_f16x2(f[e]));
-            }
-          }
-        }
-        // ---- scores in units of log2, scales of K, mask
-        const float* ks = reinterpret_cast<const float*>(smem + C::kScaleOff + s * C::kScaleBytes) + row_k;
-        const float* vs = ks + kRowsBlk;
-#pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) {
-          if constexpr (kFp8) {
-            const float2 f = *reinterpret_cast<const float2*>(ks + nt * 8 + 2 * t4);
-            sc[nt][0] *= f.x * c_row[0];
-            sc[nt][1] *= f.y * c_row[0];
-            sc[nt][2] *= f.x * c_row[1];
-            sc[nt][3] *= f.y * c_row[1];
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sc[nt][e] *= c_row[0];
-          }
-          if (edge) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int key = key0 + nt * 8 + 2 * t4 + (e & 1), at = pos[e >> 1];
-              const bool see = key <= at && (!p.window || at - key < p.window || key < p.sinks);
-              if (!see) sc[nt][e] = -INFINITY;
-            }
-          }
-        }
         // ---- running maximum and sum of each row
-        float f_row[2], mu[2];
+        float f_row[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           float mx = -INFINITY;
 #pragma unroll
-          for (int nt = 0; nt < kNT; ++nt) mx = max3f(mx, sc[nt][2 * i], sc[nt][2 * i + 1]);
+          for (int nt = 0; nt < kPair * kNT; ++nt) mx = max3f(mx, sc[nt][2 * i], sc[nt][2 * i + 1]);
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
           const float m_new = fmaxf(m[i], mx);
-          mu[i] = m_new == -INFINITY ? 0.f : m_new;
-          f_row[i] = ex2_approx(m[i] - mu[i]);
+          const float mu = m_new == -INFINITY ? 0.f : m_new;
+          f_row[i] = ex2_approx(m[i] - mu);
           m[i] = m_new;
-          float sum = 0.f;
+          float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
-          for (int nt = 0; nt < kNT; ++nt) {
-            sc[nt][2 * i] = ex2_approx(sc[nt][2 * i] - mu[i]);
-            sc[nt][2 * i + 1] = ex2_approx(sc[nt][2 * i + 1] - mu[i]);
-            sum += sc[nt][2 * i] + sc[nt][2 * i + 1];
+          for (int nt = 0; nt < kPair * kNT; ++nt) {
+            float &x0 = sc[nt][2 * i], &x1 = sc[nt][2 * i + 1];
+            add2(x0, x1, x0, x1, -mu, -mu);
+            x0 = ex2_approx(x0);
+            x1 = ex2_approx(x1);
+            add2(sum0, sum1, sum0, sum1, x0, x1);
           }
-          l[i] = l[i] * f_row[i] + sum;
+          l[i] = l[i] * f_row[i] + (sum0 + sum1);
         }
         if constexpr (kFp8) {
           // V's scales, relative to the largest one that the output holds so far
-          float2 v2[kNT];
+          float2 v2[kPair * kNT];
           float top = 0.f;
 #pragma unroll
-          for (int nt = 0; nt < kNT; ++nt) {
-            v2[nt] = *reinterpret_cast<const float2*>(vs + nt * 8 + 2 * t4);
-            if (edge) {
-              if (!it.w.seen(key0 + nt * 8 + 2 * t4)) v2[nt].x = 0.f;
-              if (!it.w.seen(key0 + nt * 8 + 2 * t4 + 1)) v2[nt].y = 0.f;
+          for (int x = 0; x < kPair; ++x) {
+            const float* vs = reinterpret_cast<const float*>(smem + C::kScaleOff + ((n + x) % C::kStages) * C::kScaleBytes) + kRowsBlk + row_k;
+            const int key0 = it.w.at(j + x) + row_k;
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt) {
+              float2& v = v2[x * kNT + nt];
+              v = make_float2(0.f, 0.f);
+              if (x < nb) v = *reinterpret_cast<const float2*>(vs + nt * 8 + 2 * t4);
+              if (edge) {
+                if (!it.w.seen(key0 + nt * 8 + 2 * t4)) v.x = 0.f;
+                if (!it.w.seen(key0 + nt * 8 + 2 * t4 + 1)) v.y = 0.f;
+              }
+              top = max3f(top, v.x, v.y);
             }
-            top = max3f(top, v2[nt].x, v2[nt].y);
           }
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          if (top > vref) {
+          if (top > vref) {   // the same for the whole warp
             const float ratio = vref / top;
             f_row[0] *= ratio;
             f_row[1] *= ratio;
             vref = top;
+            v_inv = 1.f / top;
           }
-          const float inv = vref > 0.f ? 1.f / vref : 0.f;
 #pragma unroll
-          for (int nt = 0; nt < kNT; ++nt) {
-            const float a = v2[nt].x * inv, c = v2[nt].y * inv;
-            sc[nt][0] *= a;
-            sc[nt][1] *= c;
-            sc[nt][2] *= a;
-            sc[nt][3] *= c;
+          for (int nt = 0; nt < kPair * kNT; ++nt) {
+            const float a = v2[nt].x * v_inv, c = v2[nt].y * v_inv;
+            mul2(sc[nt][0], sc[nt][1], sc[nt][0], sc[nt][1], a, c);
+            mul2(sc[nt][2], sc[nt][3], sc[nt][2], sc[nt][3], a, c);
           }
         }
         if (__any_sync(0xffffffffu, f_row[0] != 1.f || f_row[1] != 1.f)) {
@@ -460,41 +493,49 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
         }
         // ---- O += P V: 16 keys per step
 #pragma unroll
-        for (int k2 = 0; k2 < kNT / 2; ++k2) {
-          uint32_t a[4];
-          if constexpr (!kFp8) {
-            a[0] = pack_bf16x2(sc[2 * k2][0], sc[2 * k2][1]);
-            a[1] = pack_bf16x2(sc[2 * k2][2], sc[2 * k2][3]);
-            a[2] = pack_bf16x2(sc[2 * k2 + 1][0], sc[2 * k2 + 1][1]);
-            a[3] = pack_bf16x2(sc[2 * k2 + 1][2], sc[2 * k2 + 1][3]);
-          } else {
-            a[0] = pack_f16x2(sc[2 * k2][0], sc[2 * k2][1]);
-            a[1] = pack_f16x2(sc[2 * k2][2], sc[2 * k2][3]);
-            a[2] = pack_f16x2(sc[2 * k2 + 1][0], sc[2 * k2 + 1][1]);
-            a[3] = pack_f16x2(sc[2 * k2 + 1][2], sc[2 * k2 + 1][3]);
-          }
-          const int vr = row_k + k2 * 16 + (lane & 15);  // matrices: keys 0-7, 8-15 of chunk x, then of x + 1
+        for (int x = 0; x < kPair; ++x) {
+          if (x >= nb) break;
+          const int s = (n + x) % C::kStages;
+          const uint32_t sV = base + s * 2 * C::kTile + C::kTile;
 #pragma unroll
-          for (int x = 0; x < C::kRowBytes / 16; x += 2) {
-            uint32_t f[4];
-            ldsm4_t(f, C::chunk(sV, vr, x + lane / 16));
+          for (int k2 = 0; k2 < kNT / 2; ++k2) {
+            const float (&p0)[4] = sc[x * kNT + 2 * k2], (&p1)[4] = sc[x * kNT + 2 * k2 + 1];
+            uint32_t a[4];
             if constexpr (!kFp8) {
-              mma16816<false>(o[x], a, f[0], f[1]);
-              mma16816<false>(o[x + 1], a, f[2], f[3]);
+              a[0] = pack_bf16x2(p0[0], p0[1]);
+              a[1] = pack_bf16x2(p0[2], p0[3]);
+              a[2] = pack_bf16x2(p1[0], p1[1]);
+              a[3] = pack_bf16x2(p1[2], p1[3]);
             } else {
-              // each 16-bit element is two columns' codes: bytes (key, col) (key, col + 1) (key + 1, ..)
+              a[0] = pack_f16x2(p0[0], p0[1]);
+              a[1] = pack_f16x2(p0[2], p0[3]);
+              a[2] = pack_f16x2(p1[0], p1[1]);
+              a[3] = pack_f16x2(p1[2], p1[3]);
+            }
+            const int vr = row_k + k2 * 16 + (lane & 15);  // matrices: keys 0-7, 8-15 of chunk c0, then of c0 + 1
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const uint32_t lo = __byte_perm(f[2 * e], 0, 0x3120), hi = __byte_perm(f[2 * e + 1], 0, 0x3120);
-                mma16816<true>(o[2 * (x + e)], a, codes_f16x2(lo), codes_f16x2(hi));
-                mma16816<true>(o[2 * (x + e) + 1], a, codes_hi_f16x2(lo), codes_hi_f16x2(hi));
+            for (int c0 = 0; c0 < C::kRowBytes / 16; c0 += 2) {
+              uint32_t f[4];
+              ldsm4_t(f, C::chunk(sV, vr, c0 + lane / 16));
+              if constexpr (!kFp8) {
+                mma16816<false>(o[c0], a, f[0], f[1]);
+                mma16816<false>(o[c0 + 1], a, f[2], f[3]);
+              } else {
+                // each 16-bit element is two columns' codes: bytes (key, col) (key, col + 1) (key + 1, ..)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const uint32_t lo = __byte_perm(f[2 * e], 0, 0x3120), hi = __byte_perm(f[2 * e + 1], 0, 0x3120);
+                  mma16816<true>(o[2 * (c0 + e)], a, codes_f16x2(lo), codes_f16x2(hi));
+                  mma16816<true>(o[2 * (c0 + e) + 1], a, codes_hi_f16x2(lo), codes_hi_f16x2(hi));
+                }
               }
             }
           }
+          if (edge) fence_proxy_async_smem();  // the zeroed rows precede the stage's next TMA write
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.empty[s]);
         }
-        if (edge) fence_proxy_async_smem();  // the zeroed rows precede the stage's next TMA write
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.empty[s]);
+        n += nb;
       }
       if (!ok) break;
       // ---- join the key groups and write
@@ -622,21 +663,34 @@ __global__ void __launch_bounds__(256) fa_rows_combine(const Attn p, int slot_ro
     float sum = 0.f, acc[kPer];
 #pragma unroll
     for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-    for (int i = 0; i < pieces; ++i) {
-      const long long slot = i == 0 ? info.z : 2ll * (info.x + i);
-      const float w = ex2_approx((p.part_lse[slot * slot_rows + r] - tu) * 1.4426950408889634f);
-      const float* src = p.part_o + (slot * slot_rows + r) * D + lane * kPer;
-      sum += w;
-      if constexpr (kPer == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(src);
-        acc[0] = fmaf(w, x.x, acc[0]);
-        acc[1] = fmaf(w, x.y, acc[1]);
-        acc[2] = fmaf(w, x.z, acc[2]);
-        acc[3] = fmaf(w, x.w, acc[3]);
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(src);
-        acc[0] = fmaf(w, x.x, acc[0]);
-        acc[1] = fmaf(w, x.y, acc[1]);
+    // eight pieces' loads in flight at a time
+    for (int i0 = 0; i0 < pieces; i0 += 8) {
+      float lse8[8], x[8][kPer];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int i = i0 + u;
+        const long long slot = i == 0 ? info.z : 2ll * (info.x + i);
+        lse8[u] = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) x[u][e] = 0.f;
+        if (i < pieces) {
+          lse8[u] = p.part_lse[slot * slot_rows + r];
+          const float* src = p.part_o + (slot * slot_rows + r) * D + lane * kPer;
+          if constexpr (kPer == 4) {
+            const float4 v = *reinterpret_cast<const float4*>(src);
+            x[u][0] = v.x, x[u][1] = v.y, x[u][2] = v.z, x[u][3] = v.w;
+          } else {
+            const float2 v = *reinterpret_cast<const float2*>(src);
+            x[u][0] = v.x, x[u][1] = v.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float w = ex2_approx((lse8[u] - tu) * 1.4426950408889634f);
+        sum += w;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) acc[e] = fmaf(w, x[u][e], acc[e]);
       }
     }
     const bool empty = top == -INFINITY && sum == 0.f;
