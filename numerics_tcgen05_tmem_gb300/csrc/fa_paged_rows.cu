@@ -28,8 +28,14 @@ namespace fa {
 namespace paged {
 
 constexpr int kRowsBlk = 64;
-constexpr int kRowsWarps = 4;                          // computing warps; one more loads
-constexpr int kRowsThreads = 32 * (kRowsWarps + 1);
+// A warpgroup computes, one warp of a second one loads.  The second is a whole warpgroup because
+// setmaxnreg moves registers between warpgroups: the computing threads hold Q, O and the scores of
+// two blocks (with E4M3 and 168 registers they spilled: 173 us instead of 161 on 64 sequences of up to 16k keys).
+constexpr int kRowsWarps = 4;
+constexpr int kRowsLoadWarp = 4;
+constexpr int kRowsThreads = 256;
+constexpr int kRowsRegLaunch = 128, kRowsRegCompute = 208, kRowsRegLoad = 48;
+static_assert(kRowsRegCompute + kRowsRegLoad <= 2 * kRowsRegLaunch, "register split exceeds the launch allocation");
 
 template <int D, bool kFp8>
 struct RowsCfg {
@@ -43,8 +49,9 @@ struct RowsCfg {
   static constexpr int kStages = kFit < 8 ? kFit : 8;
   static constexpr int kScaleOff = kStages * 2 * kTile;
   static constexpr int kScaleBytes = kFp8 ? 2 * kRowsBlk * 4 : 0;      // per stage
-  static constexpr int kBufOff = kScaleOff + kStages * kScaleBytes;    // joining: 4 x 16 rows x 32 columns
-  static constexpr int kSmemBytes = kBufOff + kRowsWarps * 16 * 32 * 4 + 1024;
+  static constexpr int kBufOff = kScaleOff + kStages * kScaleBytes;    // joining: four rows of each warp
+  static constexpr int kBufRow = D + 8;                                // floats; the pad spreads rows over banks
+  static constexpr int kSmemBytes = kBufOff + kRowsWarps * 4 * kBufRow * 4 + 1024;
   static_assert(2 * (kSmemBytes + 2048) <= 228 * 1024, "two CTAs must fit one SM's shared memory");
   // shared-memory address of 16-byte chunk x of row r of a tile
   __device__ static uint32_t chunk(uint32_t base, int r, int x) {
@@ -113,18 +120,23 @@ struct RowsItem {
   }
 };
 
-// Blocks of the sequences [b0, b1), for one kv head.
-__device__ __forceinline__ int count_blocks(const Attn& p, int b0, int b1) {
+// Work is dealt in units: an item (sequence, kv head) takes kItemUnits for loading its queries and
+// writing its rows, then one per 64-key block.  Unit u of the launch is (b, h, unit within the item),
+// the last fastest; a CTA's share is [u_first, u_end).
+// Measured on 64 sequences of 500 to 16k keys, E4M3: 147 us without item units, 134 with two, 125 with
+// six (the CTAs with short sequences were last).
+constexpr int kItemUnits = 6;
+constexpr int kMinShare = 2;   // for a batch of few keys: as many CTAs as there are pairs of blocks
+
+// Units of the sequences [b0, b1), for one kv head.
+__device__ __forceinline__ int count_units(const Attn& p, int b0, int b1) {
   int n = 0;
-  for (int b = b0; b < b1; ++b) n += RowsItem(p, b).w.steps;
+  for (int b = b0; b < b1; ++b) {
+    const int steps = RowsItem(p, b).w.steps;
+    n += steps ? steps + kItemUnits : 0;
+  }
   return n;
 }
-
-// The CTA's pieces: unit u of the launch is (b, h, step j) with j fastest, then h; a CTA's share is
-// [u, u_end).
-struct Piece {
-  int b, h, j0, j1, steps;
-};
 
 template <int D, bool kFp8, int kMT>
 __global__ void __launch_bounds__(kRowsThreads, 2)
@@ -134,16 +146,17 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
   constexpr int kKeys = kRowsBlk / kKG;        // keys of a block for one warp
   constexpr int kNT = kKeys / 8;               // 8-key column tiles of S
   constexpr int kPair = kMT == 1 ? 2 : 1;      // blocks taken at a time
+  static_assert(C::kStages >= kPair, "the ring must hold every block that is waited for at once");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ RowsShared sh;
   volatile uint32_t* abort_flag = &sh.abort_flag;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
-  // ---- shares: every thread counts the blocks of a few sequences, the CTA scans the counts
+  // ---- shares: every thread counts the units of a few sequences, the CTA scans the counts
   const int per = (p.c.B + kRowsThreads - 1) / kRowsThreads;
   const int b_from = min((int)threadIdx.x * per, p.c.B), b_to = min(b_from + per, p.c.B);
-  const int mine = count_blocks(p, b_from, b_to);
+  const int mine = count_units(p, b_from, b_to);
   int incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o *= 2) {
@@ -169,7 +182,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
     total += sh.scan[w];
   }
   const long long units = (long long)total * p.c.Hkv;
-  const int share = (int)max((units + gridDim.x - 1) / gridDim.x, 1ll);
+  const int share = (int)max((units + gridDim.x - 1) / gridDim.x, (long long)kMinShare);
   const long long u_first = (long long)blockIdx.x * share;
   const long long u_end = min(u_first + share, units);
   {
@@ -178,7 +191,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
     if (u_first < u_end && u_first >= from && u_first < to) {
       long long u = from;
       for (int b = b_from; b < b_to; ++b) {
-        const long long n = (long long)RowsItem(p, b).w.steps * p.c.Hkv;
+        const long long n = (long long)count_units(p, b, b + 1) * p.c.Hkv;
         if (u_first < u + n) {
           sh.first_b = b;
           sh.first_unit = u_first - u;
@@ -189,9 +202,11 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
     }
   }
   __syncthreads();
-  if (u_first >= u_end) return;
+  if (u_first >= u_end || sh.first_b < 0) return;
 
-  if (warp == kRowsWarps) {
+  if (warp >= kRowsWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRowsRegLoad));
+    if (warp != kRowsLoadWarp) return;
     // ------------------------------------------------------------------ loading warp
     if (lane == 0) {
       tma_prefetch_desc(&tmK);
@@ -208,10 +223,12 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
     for (long long u = u_first; ok && u < u_end && b < p.c.B; ++b, unit = 0) {
       const RowsItem it(p, b);
       if (it.w.steps == 0) continue;
-      int h = (int)(unit / it.w.steps), j0 = (int)(unit - (long long)h * it.w.steps);
-      for (; ok && h < p.c.Hkv && u < u_end; ++h, j0 = 0) {
-        const int j1 = (int)min((long long)it.w.steps, j0 + (u_end - u));
-        u += j1 - j0;
+      const int n_units = it.w.steps + kItemUnits;
+      int h = (int)(unit / n_units), x0 = (int)(unit - (long long)h * n_units);
+      for (; ok && h < p.c.Hkv && u < u_end; ++h, x0 = 0) {
+        const int x1 = (int)min((long long)n_units, x0 + (u_end - u));
+        u += x1 - x0;
+        const int j0 = max(x0 - kItemUnits, 0), j1 = max(x1 - kItemUnits, 0);  // this piece's blocks, if any
         for (int jg = j0; ok && jg < j1; jg += per_group) {
           const int jl = jg + lane / ppb;
           int page = p.c.num_pages;  // out of range: zeros
@@ -262,6 +279,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
   }
 
   // -------------------------------------------------------------------- computing warps
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowsRegCompute));
   const int mt = warp / kKG, kg = warp % kKG;     // row tile, key group
   const int r0 = mt * 16 + lane / 4;              // this thread's rows: r0 and r0 + 8
   const int t4 = lane % 4;
@@ -280,12 +298,14 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
   for (long long u = u_first; ok && u < u_end && b < p.c.B; ++b, unit = 0) {
     const RowsItem it(p, b);
     if (it.w.steps == 0) continue;
-    int h = (int)(unit / it.w.steps), j0 = (int)(unit - (long long)h * it.w.steps);
-    for (; ok && h < p.c.Hkv && u < u_end; ++h, j0 = 0) {
-      const int steps = it.w.steps;
-      const int j1 = (int)min((long long)steps, j0 + (u_end - u));
-      const long long u_item = u - j0;   // the item's first unit
-      u += j1 - j0;
+    const int steps = it.w.steps, n_units = steps + kItemUnits;
+    int h = (int)(unit / n_units), x0 = (int)(unit - (long long)h * n_units);
+    for (; ok && h < p.c.Hkv && u < u_end; ++h, x0 = 0) {
+      const int x1 = (int)min((long long)n_units, x0 + (u_end - u));
+      const long long u_blocks = u - x0 + kItemUnits;   // the unit of the item's first block
+      u += x1 - x0;
+      const int j0 = max(x0 - kItemUnits, 0), j1 = max(x1 - kItemUnits, 0);  // this piece's blocks
+      if (j1 == j0) continue;                                                // (the next CTA's)
       // ---- Q fragments of this warp's 16 rows
       int pos[2];          // positions of the thread's two rows; -1 (sees nothing) past the last row
       float c_row[2] = {p.scale_log2, p.scale_log2};
@@ -340,46 +360,60 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
       float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
       float vref = 0.f, v_inv = 0.f;   // E4M3: O is in units of this V scale; its reciprocal
       // kPair blocks at a time: their products are independent of each other, and the bookkeeping of
-      // the running maximum is paid once for both
-      for (int j = j0; j < j1; j += kPair) {
-        const int nb = min(kPair, j1 - j);
-        float sc[kPair * kNT][4];
-        bool edge = false;
+      // the running maximum is paid once for both.  (Computing the next pair's scores beside the
+      // current pair's softmax was slower: 128 -> 131 us for E4M3, d = 128, 97 -> 109 us for d = 64 on
+      // 64 sequences of up to 16k keys; the other CTA's warps fill those slots already.)
+      float sc[kPair * kNT][4];
+      // waits for the blocks of the pair at j (ring index m); true if all landed
+      auto landed = [&](int j, int m) {
 #pragma unroll
-        for (int x = 0; x < kPair; ++x) {
-          if (x < nb) {
-            const int s = (n + x) % C::kStages, key0 = it.w.at(j + x);
-            ok = __all_sync(0xffffffffu, mbar_wait(&sh.full[s], ((n + x) / C::kStages) & 1, abort_flag, p.c.status));
-            if (!ok) break;
-            const uint32_t sK = base + s * 2 * C::kTile;
-            edge |= !it.w.all(p, key0, it.s.pos0, it.s.kv - 1);
-            // ---- S = Q K^T
+        for (int x = 0; x < kPair; ++x)
+          if (j + x < j1 && !__all_sync(0xffffffffu, mbar_wait(&sh.full[(m + x) % C::kStages], ((m + x) / C::kStages) & 1,
+                                                              abort_flag, p.c.status)))
+            return false;
+        return true;
+      };
+      // S = Q K^T of the pair at j (ring index m); an odd last block's missing partner repeats it and
+      // is masked (a uniform body keeps the accumulation chains interleaved)
+      auto scores = [&](float (&acc)[kPair * kNT][4], int j, int m) {
 #pragma unroll
-            for (int nt = 0; nt < kNT; ++nt) {
-              float (&acc)[4] = sc[x * kNT + nt];
+        for (int i = 0; i < kPair * kNT; ++i)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) acc[e] = 0.f;
+          for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
+        uint32_t sK[kPair];
 #pragma unroll
-              for (int c0 = 0; c0 < C::kRowBytes / 16; c0 += 4) {
-                uint32_t f[4];
-                ldsm4(f, C::chunk(sK, row_k + nt * 8 + (lane & 7), c0 + lane / 8));
-                if constexpr (!kFp8) {
-                  mma16816<false>(acc, qf[c0 / 2], f[0], f[1]);
-                  mma16816<false>(acc, qf[c0 / 2 + 1], f[2], f[3]);
-                } else {
+        for (int x = 0; x < kPair; ++x) sK[x] = base + ((m + (j + x < j1 ? x : 0)) % C::kStages) * 2 * C::kTile;
 #pragma unroll
-                  for (int e = 0; e < 4; ++e) mma16816<true>(acc, qf[c0 + e], codes_f16x2(f[e]), codes_hi_f16x2(f[e]));
-                }
-              }
+        for (int c0 = 0; c0 < C::kRowBytes / 16; c0 += 4) {
+#pragma unroll
+          for (int g = 0; g < kPair * kNT; g += 2) {   // two 8-key tiles at a time
+            uint32_t f[2][4];
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+              ldsm4(f[y], C::chunk(sK[(g + y) / kNT], row_k + ((g + y) % kNT) * 8 + (lane & 7), c0 + lane / 8));
+            if constexpr (!kFp8) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) mma16816<false>(acc[g + y], qf[c0 / 2 + e], f[y][2 * e], f[y][2 * e + 1]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+                  mma16816<true>(acc[g + y], qf[c0 + e], codes_f16x2(f[y][e]), codes_hi_f16x2(f[y][e]));
             }
-          } else {
-#pragma unroll
-            for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) sc[x * kNT + nt][e] = -INFINITY;
           }
         }
-        if (!ok) break;
+      };
+      for (int j = j0; j < j1; j += kPair) {
+        const int nb = min(kPair, j1 - j);
+        bool edge = false;
+#pragma unroll
+        for (int x = 0; x < kPair; ++x)
+          if (x < nb) edge |= !it.w.all(p, it.w.at(j + x), it.s.pos0, it.s.kv - 1);
+        if (!(ok = landed(j, n))) break;
+        scores(sc, j, n);
         // ---- scores in units of log2, scales of K
 #pragma unroll
         for (int x = 0; x < kPair; ++x) {
@@ -397,6 +431,12 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
               mul2(v[2], v[3], v[2], v[3], c_row[0], c_row[0]);
             }
           }
+        }
+        if (kPair > 1 && nb < kPair) {
+#pragma unroll
+          for (int i = kNT; i < kPair * kNT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[i][e] = -INFINITY;
         }
         if (edge) {
 #pragma unroll
@@ -577,37 +617,38 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
         if (whole) report_nonfinite((kg == 0 && t4 == 0 && r < it.rows && !empty && !(fabsf(lse) < INFINITY)) ? 1u : 0u, p.c.status, kOutLse);
       }
       uint32_t bad = 0;
+      for (int rr = 0; rr < min(16, it.rows); rr += 4) {   // four rows of every row tile at a time
+        const int i = rr / 8;
+        if (((lane / 4) & 4) == (rr & 4)) {
+          float* dst = buf + (warp * 4 + ((lane / 4) & 3)) * C::kBufRow;
 #pragma unroll
-      for (int cc = 0; cc < D / 32; ++cc) {   // 32 columns at a time through the buffer
-        float* mine_buf = buf + warp * 16 * 32;
+          for (int half = 0; half < 2; ++half) {
+            if (i != half) continue;
+            if constexpr (!kFp8) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float* dst = mine_buf + (lane / 4 + 8 * i) * 32;
-          if constexpr (!kFp8) {
+              for (int x = 0; x < D / 8; ++x)
+                *reinterpret_cast<float2*>(dst + x * 8 + 2 * t4) =
+                    make_float2(o[x][2 * half] * w_row[half], o[x][2 * half + 1] * w_row[half]);
+            } else {
 #pragma unroll
-            for (int q4 = 0; q4 < 4; ++q4)
-              *reinterpret_cast<float2*>(dst + q4 * 8 + 2 * t4) =
-                  make_float2(o[cc * 4 + q4][2 * i] * w_row[i], o[cc * 4 + q4][2 * i + 1] * w_row[i]);
-          } else {
-#pragma unroll
-            for (int q2 = 0; q2 < 2; ++q2) {
-              const int c16 = cc * 2 + q2;
-              *reinterpret_cast<float4*>(dst + q2 * 16 + 4 * t4) =
-                  make_float4(o[2 * c16][2 * i] * w_row[i], o[2 * c16 + 1][2 * i] * w_row[i],
-                              o[2 * c16][2 * i + 1] * w_row[i], o[2 * c16 + 1][2 * i + 1] * w_row[i]);
+              for (int x = 0; x < D / 16; ++x)
+                *reinterpret_cast<float4*>(dst + x * 16 + 4 * t4) =
+                    make_float4(o[2 * x][2 * half] * w_row[half], o[2 * x + 1][2 * half] * w_row[half],
+                                o[2 * x][2 * half + 1] * w_row[half], o[2 * x + 1][2 * half + 1] * w_row[half]);
             }
           }
         }
         if (!(ok = __all_sync(0xffffffffu, warps_sync()))) break;
 #pragma unroll
-        for (int i = 0; i < kMT; ++i) {
-          const int idx = threadIdx.x + i * 128;          // of 16 kMT rows x 8 groups of four columns
-          const int r = idx / 8, c4 = (idx % 8) * 4;
+        for (int e = 0; e < (kMT * 4 * D / 4 + 127) / 128; ++e) {
+          const int idx = threadIdx.x + e * 128;          // of 4 kMT rows x D / 4 groups of four columns
+          if (kMT * 4 * D / 4 < 128 && idx >= kMT * 4 * D / 4) break;
+          const int q4 = idx / (D / 4), c4 = (idx % (D / 4)) * 4, tile = q4 / 4;
+          const int r = tile * 16 + rr + q4 % 4;
           float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
           for (int k = 0; k < kKG; ++k) {
-            const float4 x =
-                *reinterpret_cast<const float4*>(buf + ((r / 16) * kKG + k) * 16 * 32 + (r % 16) * 32 + c4);
+            const float4 x = *reinterpret_cast<const float4*>(buf + ((tile * kKG + k) * 4 + q4 % 4) * C::kBufRow + c4);
             sum.x += x.x;
             sum.y += x.y;
             sum.z += x.z;
@@ -615,13 +656,13 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
           }
           if (r < it.rows) {
             if (!whole) {
-              *reinterpret_cast<float4*>(p.part_o + ((long long)slot * (16 * kMT) + r) * D + cc * 32 + c4) = sum;
+              *reinterpret_cast<float4*>(p.part_o + ((long long)slot * (16 * kMT) + r) * D + c4) = sum;
             } else {
               const int t = r / p.group;
               const uint2 v = make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
               bad += nonfinite_bf16x2(v.x) + nonfinite_bf16x2(v.y);
               *reinterpret_cast<uint2*>(
-                  p.o + ((long long)(it.s.q0 + t) * p.Hq + h * p.group + (r - t * p.group)) * D + cc * 32 + c4) = v;
+                  p.o + ((long long)(it.s.q0 + t) * p.Hq + h * p.group + (r - t * p.group)) * D + c4) = v;
             }
           }
         }
@@ -631,87 +672,80 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
       report_nonfinite(bad, p.c.status, kOutO);
       // the CTA with an item's first step tells the joining kernel where its pieces are
       if (j0 == 0 && threadIdx.x == 0) {
-        const int last_cta = (int)((u_item + steps - 1) / share);
-        p.part_info[b * p.c.Hkv + h] = make_int4((int)blockIdx.x, last_cta, slot, it.rows);
+        const int last_cta = (int)((u_blocks + steps - 1) / share);
+        p.part_info[b * p.c.Hkv + h] = make_int4((int)blockIdx.x, last_cta, slot, 0);
       }
     }
   }
 }
 
 // Joins the pieces of split items: out = sum_i w_i o_i, w_i = exp(lse_i - lse), lse = log sum exp(lse_i).
-// One CTA per (sequence, kv head), one warp per row.  The first piece is in the slot that its CTA
-// recorded, the others are the first pieces of the CTAs that follow.
+// A warp per row, four rows per CTA.  The first piece is in the slot that its CTA recorded, the others
+// are the first pieces of the CTAs that follow.  Launched while the pieces are still being computed
+// (programmatic launch): what it reads of them comes after the wait.
 template <int D>
-__global__ void __launch_bounds__(256) fa_rows_combine(const Attn p, int slot_rows) {
-  const int b = blockIdx.x / p.c.Hkv, h = blockIdx.x % p.c.Hkv;
+__global__ void __launch_bounds__(128) fa_rows_combine(const Attn p, int slot_rows) {
+  const int groups = slot_rows / 4;
+  const int item = blockIdx.x / groups, b = item / p.c.Hkv, h = item - b * p.c.Hkv;
   const RowsItem it(p, b);
-  if (it.w.steps == 0) return;
-  const int4 info = p.part_info[blockIdx.x];
+  const int r = (blockIdx.x % groups) * 4 + threadIdx.x / 32, lane = threadIdx.x % 32;
+  // before any exit: the launch that follows this one must find the pieces' kernel complete
+  cudaGridDependencySynchronize();
+  if (it.w.steps == 0 || r >= it.rows) return;
+  const int4 info = p.part_info[item];
+  // a launch that gave up (a wait that ran out) may have left the record unwritten
+  if (info.x < 0 || info.y < info.x || info.y >= kRowsMaxCtas || (info.z >> 1) != info.x) {
+    if (lane == 0) report_bounds(p.c.status, kSitePagedPieces, info.x);
+    return;
+  }
   const int pieces = info.y - info.x + 1;
   if (pieces < 2) return;
-  const int lane = threadIdx.x % 32;
   constexpr int kPer = D / 32;   // columns per lane: 2 or 4
-  for (int r = threadIdx.x / 32; r < it.rows; r += 8) {
-    float top = -INFINITY;
-    for (int i = lane; i < pieces; i += 32) {
-      const long long slot = i == 0 ? info.z : 2ll * (info.x + i);
-      top = fmaxf(top, p.part_lse[slot * slot_rows + r]);
+  auto row_of = [&](int i) { return (i == 0 ? (long long)info.z : 2ll * (info.x + i)) * slot_rows + r; };
+  float top = -INFINITY;
+  for (int i = lane; i < pieces; i += 32) top = fmaxf(top, p.part_lse[row_of(i)]);
+#pragma unroll
+  for (int off = 16; off > 0; off /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  const float tu = top == -INFINITY ? 0.f : top;
+  float sum = 0.f, acc[kPer];
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < pieces; ++i) {
+    const long long row = row_of(i);
+    const float w = ex2_approx((p.part_lse[row] - tu) * 1.4426950408889634f);
+    const float* src = p.part_o + row * D + lane * kPer;
+    sum += w;
+    if constexpr (kPer == 4) {
+      const float4 x = *reinterpret_cast<const float4*>(src);
+      acc[0] = fmaf(w, x.x, acc[0]);
+      acc[1] = fmaf(w, x.y, acc[1]);
+      acc[2] = fmaf(w, x.z, acc[2]);
+      acc[3] = fmaf(w, x.w, acc[3]);
+    } else {
+      const float2 x = *reinterpret_cast<const float2*>(src);
+      acc[0] = fmaf(w, x.x, acc[0]);
+      acc[1] = fmaf(w, x.y, acc[1]);
     }
-#pragma unroll
-    for (int off = 16; off > 0; off /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    const float tu = top == -INFINITY ? 0.f : top;
-    float sum = 0.f, acc[kPer];
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-    // eight pieces' loads in flight at a time
-    for (int i0 = 0; i0 < pieces; i0 += 8) {
-      float lse8[8], x[8][kPer];
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int i = i0 + u;
-        const long long slot = i == 0 ? info.z : 2ll * (info.x + i);
-        lse8[u] = -INFINITY;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) x[u][e] = 0.f;
-        if (i < pieces) {
-          lse8[u] = p.part_lse[slot * slot_rows + r];
-          const float* src = p.part_o + (slot * slot_rows + r) * D + lane * kPer;
-          if constexpr (kPer == 4) {
-            const float4 v = *reinterpret_cast<const float4*>(src);
-            x[u][0] = v.x, x[u][1] = v.y, x[u][2] = v.z, x[u][3] = v.w;
-          } else {
-            const float2 v = *reinterpret_cast<const float2*>(src);
-            x[u][0] = v.x, x[u][1] = v.y;
-          }
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const float w = ex2_approx((lse8[u] - tu) * 1.4426950408889634f);
-        sum += w;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) acc[e] = fmaf(w, x[u][e], acc[e]);
-      }
-    }
-    const bool empty = top == -INFINITY && sum == 0.f;
-    const float inv = empty ? 0.f : 1.f / sum;
-    const int t = r / p.group;
-    const long long row = (long long)(it.s.q0 + t) * p.Hq + h * p.group + (r - t * p.group);
-    uint32_t w2[kPer / 2], bad = 0;
-#pragma unroll
-    for (int e = 0; e < kPer / 2; ++e) {
-      w2[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-      bad += nonfinite_bf16x2(w2[e]);
-    }
-    if constexpr (kPer == 4)
-      *reinterpret_cast<uint2*>(p.o + row * D + lane * 4) = make_uint2(w2[0], w2[1]);
-    else
-      *reinterpret_cast<uint32_t*>(p.o + row * D + lane * 2) = w2[0];
-    report_nonfinite(bad, p.c.status, kOutO);
-    const float lse = empty ? -INFINITY : top + logf(sum);
-    report_nonfinite((lane == 0 && !empty && !(fabsf(lse) < INFINITY)) ? 1u : 0u, p.c.status, kOutLse);
-    if (lane == 0 && p.lse) p.lse[row] = lse;
   }
+  const bool empty = top == -INFINITY && sum == 0.f;
+  const float inv = empty ? 0.f : 1.f / sum;
+  const int t = r / p.group;
+  const long long row = (long long)(it.s.q0 + t) * p.Hq + h * p.group + (r - t * p.group);
+  uint32_t w2[kPer / 2], bad = 0;
+#pragma unroll
+  for (int e = 0; e < kPer / 2; ++e) {
+    w2[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    bad += nonfinite_bf16x2(w2[e]);
+  }
+  if constexpr (kPer == 4)
+    *reinterpret_cast<uint2*>(p.o + row * D + lane * 4) = make_uint2(w2[0], w2[1]);
+  else
+    *reinterpret_cast<uint32_t*>(p.o + row * D + lane * 2) = w2[0];
+  report_nonfinite(bad, p.c.status, kOutO);
+  const float lse = empty ? -INFINITY : top + logf(sum);
+  report_nonfinite((lane == 0 && !empty && !(fabsf(lse) < INFINITY)) ? 1u : 0u, p.c.status, kOutLse);
+  if (lane == 0 && p.lse) p.lse[row] = lse;
 }
 
 template <int D, bool kFp8, int kMT>
@@ -719,13 +753,21 @@ static int launch(const CUtensorMap& tk, const CUtensorMap& tv, const Attn& p, i
   using C = RowsCfg<D, kFp8>;
   auto kern = fa_rows_kernel<D, kFp8, kMT>;
   static std::atomic<uint64_t> prepared{0};
-  int rc = prepare_kernel(reinterpret_cast<const void*>(kern), C::kSmemBytes, kRowsThreads, 0, "few-rows kernel",
+  int rc = prepare_kernel(reinterpret_cast<const void*>(kern), C::kSmemBytes, kRowsThreads, 128 * (kRowsRegCompute + kRowsRegLoad), "few-rows kernel",
                           &prepared);
   if (rc) return rc;
   kern<<<grid, kRowsThreads, C::kSmemBytes, s>>>(tk, tv, p);
   if ((rc = check_cuda(cudaGetLastError(), "launch fa_rows_kernel"))) return rc;
-  fa_rows_combine<D><<<p.c.B * p.c.Hkv, 256, 0, s>>>(p, 16 * kMT);
-  return check_cuda(cudaGetLastError(), "launch fa_rows_combine");
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(p.c.B * p.c.Hkv * (16 * kMT / 4)));
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return check_cuda(cudaLaunchKernelEx(&cfg, fa_rows_combine<D>, p, 16 * kMT), "launch fa_rows_combine");
 }
 
 template <int D, bool kFp8>

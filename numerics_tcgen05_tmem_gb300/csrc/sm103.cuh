@@ -73,6 +73,7 @@ enum : uint32_t {
   kSitePagedRead = 31,     // read: a position or a page of the table is out of range
   kSitePagedLen = 32,      // attention: a sequence's length exceeds its table, or its rows the tensor
   kSitePagedPage = 33,     // attention: a page of the table is out of range
+  kSitePagedPieces = 34,   // attention: the record of a split item's pieces is not a valid one
 };
 
 // Record a failed index check: the flag, and the site and index of the first one seen.
