@@ -678,12 +678,12 @@ Plan make_plan(int T, int B, int max_q, int group, int Hkv, int max_kv) {
   Plan pl{0, 0};
   const long long rows = (long long)max_q * group;
   if (rows <= kMaxFewRows) {
-    pl.few_rows = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
+    pl.few_rows = rows <= 8 ? 8 : (rows <= 16 ? 16 : (rows <= 32 ? 32 : 64));
     return pl;
   }
   // A batch of chunks may hold sequences with a token or two: those go to the few-rows kernel with one
-  // row tile (its fastest form), everything else to the chunk kernel.
-  if (B > 1 && group <= 16) pl.few_rows = 16;
+  // row group (its fastest forms), everything else to the chunk kernel.
+  if (B > 1 && group <= 16) pl.few_rows = group <= 8 ? 8 : 16;
   // One CTA per SM: split the keys while the tiles leave half of the SMs without work.
   const long long tiles = fa::paged::chunk_pairs(T, B, group) * Hkv;
   long long s = fa::paged::kChunkSms / tiles;

@@ -10,10 +10,13 @@
 //   * One warp loads: page numbers from the table, 32 at a time, then TMA boxes into a ring of K and
 //     V blocks (swizzled, so that the fragment loads meet no bank conflicts).  A page that no row
 //     sees is taken out of range, which fills zeros without a read.
-//   * Four warps compute with mma.sync: at 16 to 64 rows a tcgen05 tile (128 rows) would be mostly
-//     empty, and its softmax would hold one row per thread.  Row tiles of 16 are dealt to the warps
-//     first, the block's keys to the rest: for up to 16 rows each warp takes 16 keys of every block
-//     with its own running maximum and sum, joined once at the end of a piece.
+//   * Four warps compute with mma.sync: at 1 to 64 rows a tcgen05 tile (128 rows) would be mostly
+//     empty, and its softmax would hold one row per thread.  The products are taken transposed,
+//     S^T = K Q^T and O^T = V^T P^T, so that the rows are the instruction's narrow side: 8 of them
+//     where 16 x 8 tiles of S would have 16.  A head's K and V fragments, and E4M3's conversions, are
+//     then spent on 8 rows (kNR = 1) or 16 (2).  Row groups are dealt to the warps first, the block's
+//     keys to the rest: for up to 16 rows each warp takes 16 keys of every block with its own running
+//     maximum and sum, joined once at the end of a piece.
 //   * E4M3: codes become FP16 with one conversion for two (exact), the vectors' scales multiply the
 //     FP32 scores (K) and the FP32 probabilities (V).  Q goes to FP16 with a power of two per row
 //     that brings its largest magnitude into [1, 2): exact but for elements 2^-14 below it, whose
@@ -64,7 +67,7 @@ struct RowsCfg {
 struct RowsShared {
   uint64_t full[8], empty[8], sync;
   uint32_t abort_flag;
-  float m[kRowsWarps][16], l[kRowsWarps][16];
+  float m[kRowsWarps][16], l[kRowsWarps][16];   // by warp and row of its group
   int scan[kRowsThreads / 32];
   int first_b;               // the sequence of this CTA's first unit
   long long first_unit;      // ... and that unit's number within the sequence
@@ -81,6 +84,12 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr)
                : "memory");
+}
+// The 8 x 8 matrix of 16-bit elements that the warp holds (row lane / 4, two columns per lane), transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 template <bool kHalf>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -138,14 +147,16 @@ __device__ __forceinline__ int count_units(const Attn& p, int b0, int b1) {
   return n;
 }
 
-template <int D, bool kFp8, int kMT>
+// kRG row groups of 8 kNR rows: warp w takes row group w / (4 / kRG) and the keys of group w % (4 / kRG).
+template <int D, bool kFp8, int kRG, int kNR>
 __global__ void __launch_bounds__(kRowsThreads, 2)
     fa_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Attn p) {
   using C = RowsCfg<D, kFp8>;
-  constexpr int kKG = kRowsWarps / kMT;        // key groups
+  constexpr int kKG = kRowsWarps / kRG;        // key groups
   constexpr int kKeys = kRowsBlk / kKG;        // keys of a block for one warp
-  constexpr int kNT = kKeys / 8;               // 8-key column tiles of S
-  constexpr int kPair = kMT == 1 ? 2 : 1;      // blocks taken at a time
+  constexpr int kKT = kKeys / 16;              // 16-key tiles of S^T
+  constexpr int kPair = kRG == 1 ? 2 : 1;      // blocks taken at a time
+  constexpr int kRows = 8 * kNR * kRG;         // rows of a slot
   static_assert(C::kStages >= kPair, "the ring must hold every block that is waited for at once");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -280,12 +291,16 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
 
   // -------------------------------------------------------------------- computing warps
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowsRegCompute));
-  const int mt = warp / kKG, kg = warp % kKG;     // row tile, key group
-  const int r0 = mt * 16 + lane / 4;              // this thread's rows: r0 and r0 + 8
-  const int t4 = lane % 4;
+  const int rg = warp / kKG, kg = warp % kKG;     // row group, key group
+  const int l4 = lane / 4, t4 = lane % 4;
+  const int row0 = rg * 8 * kNR;                  // first row of the group
   const int row_k = kg * kKeys;                   // this warp's first key within a block
   const uint32_t base = smem_u32(smem);
   float* buf = reinterpret_cast<float*>(smem + C::kBufOff);
+  // the lane's row and 16-byte chunk within the 8 x 8 matrices of a fragment load: (8 keys, chunk)
+  // in the order (low, 0) (high, 0) (low, 1) (high, 1); V in BF16 takes (low, 0) (low, 1) (high, 0) ..
+  const int f_key = (lane & 7) + ((lane >> 3) & 1) * 8, f_chunk = lane >> 4;
+  const int v_key = kFp8 ? f_key : (lane & 7) + (lane >> 4) * 8, v_chunk = kFp8 ? f_chunk : (lane >> 3) & 1;
   int n = 0, syncs = 0;
   bool ok = true;
   auto warps_sync = [&]() {
@@ -306,24 +321,23 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
       u += x1 - x0;
       const int j0 = max(x0 - kItemUnits, 0), j1 = max(x1 - kItemUnits, 0);  // this piece's blocks
       if (j1 == j0) continue;                                                // (the next CTA's)
-      // ---- Q fragments of this warp's 16 rows
-      int pos[2];          // positions of the thread's two rows; -1 (sees nothing) past the last row
-      float c_row[2] = {p.scale_log2, p.scale_log2};
-      uint32_t qf[D / 16][4];
+      // ---- Q fragments (the B operand, columns = rows of the group): lane's column l4 of each 8
+      float c_row[kNR][2];   // score factors of the rows 2 t4, 2 t4 + 1 that the lane's scores belong to
+      int pos[kNR][2];       // their positions; -1 (sees nothing) past the last row
+      uint32_t qf[kNR][D / 16][2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = r0 + 8 * i;
-        const int t = r / p.group;
+      for (int nr = 0; nr < kNR; ++nr) {
+        const int r = row0 + 8 * nr + l4, t = r / p.group;
         const bool valid = r < it.rows;
-        pos[i] = valid ? it.s.pos0 + t : -1;
         const __nv_bfloat16* qr =
             p.q + (long long)(it.s.q0 + t) * p.q_stride + (long long)(h * p.group + (r - t * p.group)) * D;
+        float factor = p.scale_log2;
         if constexpr (!kFp8) {
           // BF16: columns 2t, 2t + 1 and 2t + 8, 2t + 9 of each 16
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            qf[kk][i] = valid ? __ldg(reinterpret_cast<const uint32_t*>(qr + kk * 16 + 2 * t4)) : 0u;
-            qf[kk][i + 2] = valid ? __ldg(reinterpret_cast<const uint32_t*>(qr + kk * 16 + 8 + 2 * t4)) : 0u;
+            qf[nr][kk][0] = valid ? __ldg(reinterpret_cast<const uint32_t*>(qr + kk * 16 + 2 * t4)) : 0u;
+            qf[nr][kk][1] = valid ? __ldg(reinterpret_cast<const uint32_t*>(qr + kk * 16 + 8 + 2 * t4)) : 0u;
           }
         } else {
           // E4M3: columns 4t .. 4t + 3 of each 16, the order in which K's codes arrive
@@ -338,105 +352,105 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
           amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
           amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
           int e = (int)(amax >> 23) - 127;
-          // zero rows, and rows under 2^-126 (whose factor would overflow), go unscaled by it; rows
-          // with Inf or NaN keep them
+          // zero rows and rows with Inf or NaN go unscaled; 2^-e and 2^e stay normal
           if (amax == 0 || amax >= 0x7F800000u) e = 0;
           e = min(max(e, -126), 126);
           const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-          c_row[i] = p.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+          factor *= __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            qf[kk][i] = pack_f16x2(__uint_as_float(w[kk].x << 16) * down, __uint_as_float(w[kk].x & 0xFFFF0000u) * down);
-            qf[kk][i + 2] =
-                pack_f16x2(__uint_as_float(w[kk].y << 16) * down, __uint_as_float(w[kk].y & 0xFFFF0000u) * down);
+            qf[nr][kk][0] = pack_f16x2(__uint_as_float(w[kk].x << 16) * down, __uint_as_float(w[kk].x & 0xFFFF0000u) * down);
+            qf[nr][kk][1] = pack_f16x2(__uint_as_float(w[kk].y << 16) * down, __uint_as_float(w[kk].y & 0xFFFF0000u) * down);
           }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int rr = row0 + 8 * nr + 2 * t4 + e;
+          pos[nr][e] = rr < it.rows ? it.s.pos0 + rr / p.group : -1;
+          c_row[nr][e] = kFp8 ? __shfl_sync(0xffffffffu, factor, (2 * t4 + e) * 4) : factor;
         }
       }
-      float o[D / 8][4];
+      float o[D / 16][kNR][4];   // O^T: 16 columns of O by 8 rows
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i)
+      for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        for (int nr = 0; nr < kNR; ++nr)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[i][nr][e] = 0.f;
+      float m[kNR][2], l[kNR][2];
+#pragma unroll
+      for (int nr = 0; nr < kNR; ++nr) m[nr][0] = m[nr][1] = -INFINITY, l[nr][0] = l[nr][1] = 0.f;
       float vref = 0.f, v_inv = 0.f;   // E4M3: O is in units of this V scale; its reciprocal
       // kPair blocks at a time: their products are independent of each other, and the bookkeeping of
-      // the running maximum is paid once for both.  (Computing the next pair's scores beside the
-      // current pair's softmax was slower: 128 -> 131 us for E4M3, d = 128, 97 -> 109 us for d = 64 on
-      // 64 sequences of up to 16k keys; the other CTA's warps fill those slots already.)
-      float sc[kPair * kNT][4];
-      // waits for the blocks of the pair at j (ring index m); true if all landed
-      auto landed = [&](int j, int m) {
-#pragma unroll
-        for (int x = 0; x < kPair; ++x)
-          if (j + x < j1 && !__all_sync(0xffffffffu, mbar_wait(&sh.full[(m + x) % C::kStages], ((m + x) / C::kStages) & 1,
-                                                              abort_flag, p.c.status)))
-            return false;
-        return true;
-      };
-      // S = Q K^T of the pair at j (ring index m); an odd last block's missing partner repeats it and
-      // is masked (a uniform body keeps the accumulation chains interleaved)
-      auto scores = [&](float (&acc)[kPair * kNT][4], int j, int m) {
-#pragma unroll
-        for (int i = 0; i < kPair * kNT; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
-        uint32_t sK[kPair];
-#pragma unroll
-        for (int x = 0; x < kPair; ++x) sK[x] = base + ((m + (j + x < j1 ? x : 0)) % C::kStages) * 2 * C::kTile;
-#pragma unroll
-        for (int c0 = 0; c0 < C::kRowBytes / 16; c0 += 4) {
-#pragma unroll
-          for (int g = 0; g < kPair * kNT; g += 2) {   // two 8-key tiles at a time
-            uint32_t f[2][4];
-#pragma unroll
-            for (int y = 0; y < 2; ++y)
-              ldsm4(f[y], C::chunk(sK[(g + y) / kNT], row_k + ((g + y) % kNT) * 8 + (lane & 7), c0 + lane / 8));
-            if constexpr (!kFp8) {
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-#pragma unroll
-                for (int y = 0; y < 2; ++y) mma16816<false>(acc[g + y], qf[c0 / 2 + e], f[y][2 * e], f[y][2 * e + 1]);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-#pragma unroll
-                for (int y = 0; y < 2; ++y)
-                  mma16816<true>(acc[g + y], qf[c0 + e], codes_f16x2(f[y][e]), codes_hi_f16x2(f[y][e]));
-            }
-          }
-        }
-      };
+      // the running maximum is paid once for both
       for (int j = j0; j < j1; j += kPair) {
         const int nb = min(kPair, j1 - j);
         bool edge = false;
 #pragma unroll
-        for (int x = 0; x < kPair; ++x)
-          if (x < nb) edge |= !it.w.all(p, it.w.at(j + x), it.s.pos0, it.s.kv - 1);
-        if (!(ok = landed(j, n))) break;
-        scores(sc, j, n);
-        // ---- scores in units of log2, scales of K
-#pragma unroll
         for (int x = 0; x < kPair; ++x) {
           if (x >= nb) break;
-          const float* ks = reinterpret_cast<const float*>(smem + C::kScaleOff + ((n + x) % C::kStages) * C::kScaleBytes) + row_k;
+          ok = __all_sync(0xffffffffu, mbar_wait(&sh.full[(n + x) % C::kStages], ((n + x) / C::kStages) & 1, abort_flag,
+                                                 p.c.status));
+          if (!ok) break;
+          edge |= !it.w.all(p, it.w.at(j + x), it.s.pos0, it.s.kv - 1);
+        }
+        if (!ok) break;
+        // ---- S^T = K Q^T; an odd last block's missing partner repeats it and is masked (a uniform
+        // body keeps the accumulation chains interleaved)
+        float sc[kPair * kKT][kNR][4];
 #pragma unroll
-          for (int nt = 0; nt < kNT; ++nt) {
-            float (&v)[4] = sc[x * kNT + nt];
-            if constexpr (kFp8) {
-              const float2 f = *reinterpret_cast<const float2*>(ks + nt * 8 + 2 * t4);
-              mul2(v[0], v[1], v[0], v[1], f.x * c_row[0], f.y * c_row[0]);
-              mul2(v[2], v[3], v[2], v[3], f.x * c_row[1], f.y * c_row[1]);
+        for (int i = 0; i < kPair * kKT; ++i)
+#pragma unroll
+          for (int nr = 0; nr < kNR; ++nr)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[i][nr][e] = 0.f;
+        uint32_t sK[kPair];
+#pragma unroll
+        for (int x = 0; x < kPair; ++x) sK[x] = base + ((n + (x < nb ? x : 0)) % C::kStages) * 2 * C::kTile;
+#pragma unroll
+        for (int c0 = 0; c0 < C::kRowBytes / 16; c0 += 2) {
+#pragma unroll
+          for (int i = 0; i < kPair * kKT; ++i) {
+            uint32_t f[4];
+            ldsm4(f, C::chunk(sK[i / kKT], row_k + (i % kKT) * 16 + f_key, c0 + f_chunk));
+            if constexpr (!kFp8) {
+#pragma unroll
+              for (int nr = 0; nr < kNR; ++nr) mma16816<false>(sc[i][nr], f, qf[nr][c0 / 2][0], qf[nr][c0 / 2][1]);
             } else {
-              mul2(v[0], v[1], v[0], v[1], c_row[0], c_row[0]);
-              mul2(v[2], v[3], v[2], v[3], c_row[0], c_row[0]);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t a[4] = {codes_f16x2(f[2 * e]), codes_f16x2(f[2 * e + 1]), codes_hi_f16x2(f[2 * e]),
+                                       codes_hi_f16x2(f[2 * e + 1])};
+#pragma unroll
+                for (int nr = 0; nr < kNR; ++nr) mma16816<true>(sc[i][nr], a, qf[nr][c0 + e][0], qf[nr][c0 + e][1]);
+              }
             }
+          }
+        }
+        // ---- scores in units of log2, scales of K (a lane's keys: l4 and l4 + 8 of each 16)
+#pragma unroll
+        for (int i = 0; i < kPair * kKT; ++i) {
+          float k0 = 1.f, k1 = 1.f;
+          if constexpr (kFp8) {
+            const float* ks = reinterpret_cast<const float*>(
+                smem + C::kScaleOff + ((n + (i / kKT < nb ? i / kKT : 0)) % C::kStages) * C::kScaleBytes);
+            k0 = ks[row_k + (i % kKT) * 16 + l4];
+            k1 = ks[row_k + (i % kKT) * 16 + l4 + 8];
+          }
+#pragma unroll
+          for (int nr = 0; nr < kNR; ++nr) {
+            float (&v)[4] = sc[i][nr];
+            mul2(v[0], v[1], v[0], v[1], k0 * c_row[nr][0], k0 * c_row[nr][1]);
+            mul2(v[2], v[3], v[2], v[3], k1 * c_row[nr][0], k1 * c_row[nr][1]);
           }
         }
         if (kPair > 1 && nb < kPair) {
 #pragma unroll
-          for (int i = kNT; i < kPair * kNT; ++i)
+          for (int i = kKT; i < kPair * kKT; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sc[i][e] = -INFINITY;
+            for (int nr = 0; nr < kNR; ++nr)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) sc[i][nr][e] = -INFINITY;
         }
         if (edge) {
 #pragma unroll
@@ -454,119 +468,131 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
                              : "memory");
             }
 #pragma unroll
-            for (int nt = 0; nt < kNT; ++nt)
+            for (int i = 0; i < kKT; ++i)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int key = key0 + nt * 8 + 2 * t4 + (e & 1), at = pos[e >> 1];
-                const bool see = key <= at && (!p.window || at - key < p.window || key < p.sinks);
-                if (!see) sc[x * kNT + nt][e] = -INFINITY;
-              }
+              for (int nr = 0; nr < kNR; ++nr)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const int key = key0 + i * 16 + l4 + (e >> 1) * 8, at = pos[nr][e & 1];
+                  const bool see = key <= at && (!p.window || at - key < p.window || key < p.sinks);
+                  if (!see) sc[x * kKT + i][nr][e] = -INFINITY;
+                }
           }
           __syncwarp();
         }
-        // ---- running maximum and sum of each row
-        float f_row[2];
+        // ---- running maximum and sum of each row; the lanes of one t4 hold a row's keys
+        float f_row[kNR][2];
+        bool moved = false;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float mx = -INFINITY;
+        for (int nr = 0; nr < kNR; ++nr)
 #pragma unroll
-          for (int nt = 0; nt < kPair * kNT; ++nt) mx = max3f(mx, sc[nt][2 * i], sc[nt][2 * i + 1]);
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const float m_new = fmaxf(m[i], mx);
-          const float mu = m_new == -INFINITY ? 0.f : m_new;
-          f_row[i] = ex2_approx(m[i] - mu);
-          m[i] = m_new;
-          float sum0 = 0.f, sum1 = 0.f;
+          for (int e = 0; e < 2; ++e) {
+            float mx = m[nr][e];
 #pragma unroll
-          for (int nt = 0; nt < kPair * kNT; ++nt) {
-            float &x0 = sc[nt][2 * i], &x1 = sc[nt][2 * i + 1];
-            add2(x0, x1, x0, x1, -mu, -mu);
-            x0 = ex2_approx(x0);
-            x1 = ex2_approx(x1);
-            add2(sum0, sum1, sum0, sum1, x0, x1);
+            for (int i = 0; i < kPair * kKT; ++i) mx = max3f(mx, sc[i][nr][e], sc[i][nr][e + 2]);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            const float mu = mx == -INFINITY ? 0.f : mx;
+            f_row[nr][e] = ex2_approx(m[nr][e] - mu);
+            m[nr][e] = mx;
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < kPair * kKT; ++i) {
+              float &a = sc[i][nr][e], &c = sc[i][nr][e + 2];
+              add2(a, c, a, c, -mu, -mu);
+              a = ex2_approx(a);
+              c = ex2_approx(c);
+              sum += a + c;
+            }
+            l[nr][e] = l[nr][e] * f_row[nr][e] + sum;
+            moved |= f_row[nr][e] != 1.f;
           }
-          l[i] = l[i] * f_row[i] + (sum0 + sum1);
-        }
         if constexpr (kFp8) {
           // V's scales, relative to the largest one that the output holds so far
-          float2 v2[kPair * kNT];
-          float top = 0.f;
+          float v0[kPair * kKT], v1[kPair * kKT], top = 0.f;
 #pragma unroll
-          for (int x = 0; x < kPair; ++x) {
-            const float* vs = reinterpret_cast<const float*>(smem + C::kScaleOff + ((n + x) % C::kStages) * C::kScaleBytes) + kRowsBlk + row_k;
-            const int key0 = it.w.at(j + x) + row_k;
-#pragma unroll
-            for (int nt = 0; nt < kNT; ++nt) {
-              float2& v = v2[x * kNT + nt];
-              v = make_float2(0.f, 0.f);
-              if (x < nb) v = *reinterpret_cast<const float2*>(vs + nt * 8 + 2 * t4);
+          for (int i = 0; i < kPair * kKT; ++i) {
+            const int x = i / kKT;
+            const float* vs = reinterpret_cast<const float*>(smem + C::kScaleOff + ((n + x) % C::kStages) * C::kScaleBytes) +
+                              kRowsBlk + row_k + (i % kKT) * 16 + l4;
+            v0[i] = v1[i] = 0.f;
+            if (x < nb) {
+              v0[i] = vs[0];
+              v1[i] = vs[8];
               if (edge) {
-                if (!it.w.seen(key0 + nt * 8 + 2 * t4)) v.x = 0.f;
-                if (!it.w.seen(key0 + nt * 8 + 2 * t4 + 1)) v.y = 0.f;
+                const int key = it.w.at(j + x) + row_k + (i % kKT) * 16 + l4;
+                if (!it.w.seen(key)) v0[i] = 0.f;
+                if (!it.w.seen(key + 8)) v1[i] = 0.f;
               }
-              top = max3f(top, v.x, v.y);
             }
+            top = max3f(top, v0[i], v1[i]);
           }
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          if (top > vref) {   // the same for the whole warp
+          if (__any_sync(0xffffffffu, top > vref)) {
+#pragma unroll
+            for (int off = 4; off < 32; off *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
             const float ratio = vref / top;
-            f_row[0] *= ratio;
-            f_row[1] *= ratio;
+#pragma unroll
+            for (int nr = 0; nr < kNR; ++nr) {
+              f_row[nr][0] *= ratio;
+              f_row[nr][1] *= ratio;
+            }
             vref = top;
             v_inv = 1.f / top;
+            moved = true;
           }
 #pragma unroll
-          for (int nt = 0; nt < kPair * kNT; ++nt) {
-            const float a = v2[nt].x * v_inv, c = v2[nt].y * v_inv;
-            mul2(sc[nt][0], sc[nt][1], sc[nt][0], sc[nt][1], a, c);
-            mul2(sc[nt][2], sc[nt][3], sc[nt][2], sc[nt][3], a, c);
-          }
-        }
-        if (__any_sync(0xffffffffu, f_row[0] != 1.f || f_row[1] != 1.f)) {
+          for (int i = 0; i < kPair * kKT; ++i) {
+            const float a = v0[i] * v_inv, c = v1[i] * v_inv;
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            mul2(o[i][0], o[i][1], o[i][0], o[i][1], f_row[0], f_row[0]);
-            mul2(o[i][2], o[i][3], o[i][2], o[i][3], f_row[1], f_row[1]);
+            for (int nr = 0; nr < kNR; ++nr) {
+              float (&v)[4] = sc[i][nr];
+              mul2(v[0], v[1], v[0], v[1], a, a);
+              mul2(v[2], v[3], v[2], v[3], c, c);
+            }
           }
         }
-        // ---- O += P V: 16 keys per step
+        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int nr = 0; nr < kNR; ++nr) {
+              float (&v)[4] = o[i][nr];
+              mul2(v[0], v[1], v[0], v[1], f_row[nr][0], f_row[nr][1]);
+              mul2(v[2], v[3], v[2], v[3], f_row[nr][0], f_row[nr][1]);
+            }
+        }
+        // ---- O^T += V^T P^T: 16 keys per step
 #pragma unroll
         for (int x = 0; x < kPair; ++x) {
           if (x >= nb) break;
           const int s = (n + x) % C::kStages;
           const uint32_t sV = base + s * 2 * C::kTile + C::kTile;
 #pragma unroll
-          for (int k2 = 0; k2 < kNT / 2; ++k2) {
-            const float (&p0)[4] = sc[x * kNT + 2 * k2], (&p1)[4] = sc[x * kNT + 2 * k2 + 1];
-            uint32_t a[4];
-            if constexpr (!kFp8) {
-              a[0] = pack_bf16x2(p0[0], p0[1]);
-              a[1] = pack_bf16x2(p0[2], p0[3]);
-              a[2] = pack_bf16x2(p1[0], p1[1]);
-              a[3] = pack_bf16x2(p1[2], p1[3]);
-            } else {
-              a[0] = pack_f16x2(p0[0], p0[1]);
-              a[1] = pack_f16x2(p0[2], p0[3]);
-              a[2] = pack_f16x2(p1[0], p1[1]);
-              a[3] = pack_f16x2(p1[2], p1[3]);
+          for (int i = 0; i < kKT; ++i) {
+            uint32_t pb[kNR][2];   // P^T as the B operand: keys along k, rows along n
+#pragma unroll
+            for (int nr = 0; nr < kNR; ++nr) {
+              const float (&v)[4] = sc[x * kKT + i][nr];
+              pb[nr][0] = transpose8(kFp8 ? pack_f16x2(v[0], v[1]) : pack_bf16x2(v[0], v[1]));
+              pb[nr][1] = transpose8(kFp8 ? pack_f16x2(v[2], v[3]) : pack_bf16x2(v[2], v[3]));
             }
-            const int vr = row_k + k2 * 16 + (lane & 15);  // matrices: keys 0-7, 8-15 of chunk c0, then of c0 + 1
 #pragma unroll
             for (int c0 = 0; c0 < C::kRowBytes / 16; c0 += 2) {
               uint32_t f[4];
-              ldsm4_t(f, C::chunk(sV, vr, c0 + lane / 16));
+              ldsm4_t(f, C::chunk(sV, row_k + i * 16 + v_key, c0 + v_chunk));
               if constexpr (!kFp8) {
-                mma16816<false>(o[c0], a, f[0], f[1]);
-                mma16816<false>(o[c0 + 1], a, f[2], f[3]);
+#pragma unroll
+                for (int nr = 0; nr < kNR; ++nr) mma16816<false>(o[c0 / 2][nr], f, pb[nr][0], pb[nr][1]);
               } else {
-                // each 16-bit element is two columns' codes: bytes (key, col) (key, col + 1) (key + 1, ..)
+                // each 16-bit element is two columns' codes, bytes (key, col) (key, col + 1) (key + 1, ..):
+                // the even columns become the tile's rows 0-7, the odd ones 8-15
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                   const uint32_t lo = __byte_perm(f[2 * e], 0, 0x3120), hi = __byte_perm(f[2 * e + 1], 0, 0x3120);
-                  mma16816<true>(o[2 * (c0 + e)], a, codes_f16x2(lo), codes_f16x2(hi));
-                  mma16816<true>(o[2 * (c0 + e) + 1], a, codes_hi_f16x2(lo), codes_hi_f16x2(hi));
+                  const uint32_t a[4] = {codes_f16x2(lo), codes_hi_f16x2(lo), codes_f16x2(hi), codes_hi_f16x2(hi)};
+#pragma unroll
+                  for (int nr = 0; nr < kNR; ++nr) mma16816<true>(o[c0 + e][nr], a, pb[nr][0], pb[nr][1]);
                 }
               }
             }
@@ -580,75 +606,77 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
       if (!ok) break;
       // ---- join the key groups and write
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-        if (t4 == 0) {
-          sh.m[warp][lane / 4 + 8 * i] = m[i];
-          sh.l[warp][lane / 4 + 8 * i] = l[i];
+      for (int nr = 0; nr < kNR; ++nr)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int off = 4; off < 32; off *= 2) l[nr][e] += __shfl_xor_sync(0xffffffffu, l[nr][e], off);
+          if (l4 == 0) {
+            sh.m[warp][8 * nr + 2 * t4 + e] = m[nr][e];
+            sh.l[warp][8 * nr + 2 * t4 + e] = l[nr][e];
+          }
         }
-      }
       if (!(ok = __all_sync(0xffffffffu, warps_sync()))) break;
       const bool whole = j0 == 0 && j1 == steps;
       const int slot = 2 * blockIdx.x + (first_piece ? 0 : 1);
       first_piece = false;
-      float w_row[2];
+      float w_row[kNR][2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int rr = lane / 4 + 8 * i;
-        float top = -INFINITY, sum = 0.f;
+      for (int nr = 0; nr < kNR; ++nr)
 #pragma unroll
-        for (int k = 0; k < kKG; ++k) top = fmaxf(top, sh.m[mt * kKG + k][rr]);
-        const float tu = top == -INFINITY ? 0.f : top;
+        for (int e = 0; e < 2; ++e) {
+          const int in = 8 * nr + 2 * t4 + e, r = row0 + in;
+          float top = -INFINITY, sum = 0.f;
 #pragma unroll
-        for (int k = 0; k < kKG; ++k) sum += sh.l[mt * kKG + k][rr] * ex2_approx(sh.m[mt * kKG + k][rr] - tu);
-        const bool empty = top == -INFINITY && sum == 0.f;   // no visible key (a NaN score is not that)
-        w_row[i] = empty ? 0.f : ex2_approx(m[i] - tu) / sum * (kFp8 ? vref : 1.f);
-        const float lse = empty ? -INFINITY : top * 0.6931471805599453f + logf(sum);
-        const int r = r0 + 8 * i;
-        if (kg == 0 && t4 == 0 && r < it.rows) {
-          if (!whole) {
-            p.part_lse[(long long)slot * (16 * kMT) + r] = lse;
-          } else if (p.lse) {
-            const int t = r / p.group;
-            p.lse[(long long)(it.s.q0 + t) * p.Hq + h * p.group + (r - t * p.group)] = lse;
+          for (int k = 0; k < kKG; ++k) top = fmaxf(top, sh.m[rg * kKG + k][in]);
+          const float tu = top == -INFINITY ? 0.f : top;
+#pragma unroll
+          for (int k = 0; k < kKG; ++k) sum += sh.l[rg * kKG + k][in] * ex2_approx(sh.m[rg * kKG + k][in] - tu);
+          const bool empty = top == -INFINITY && sum == 0.f;   // no visible key (a NaN score is not that)
+          w_row[nr][e] = empty ? 0.f : ex2_approx(m[nr][e] - tu) / sum * (kFp8 ? vref : 1.f);
+          const float lse = empty ? -INFINITY : top * 0.6931471805599453f + logf(sum);
+          const bool mine = kg == 0 && l4 == 0 && r < it.rows;
+          if (mine) {
+            if (!whole) {
+              p.part_lse[(long long)slot * kRows + r] = lse;
+            } else if (p.lse) {
+              const int t = r / p.group;
+              p.lse[(long long)(it.s.q0 + t) * p.Hq + h * p.group + (r - t * p.group)] = lse;
+            }
           }
+          if (whole) report_nonfinite((mine && !empty && !(fabsf(lse) < INFINITY)) ? 1u : 0u, p.c.status, kOutLse);
         }
-        if (whole) report_nonfinite((kg == 0 && t4 == 0 && r < it.rows && !empty && !(fabsf(lse) < INFINITY)) ? 1u : 0u, p.c.status, kOutLse);
-      }
       uint32_t bad = 0;
-      for (int rr = 0; rr < min(16, it.rows); rr += 4) {   // four rows of every row tile at a time
-        const int i = rr / 8;
-        if (((lane / 4) & 4) == (rr & 4)) {
-          float* dst = buf + (warp * 4 + ((lane / 4) & 3)) * C::kBufRow;
+      for (int rr = 0; rr < min(8 * kNR, it.rows); rr += 4) {   // four rows of every row group at a time
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            if (i != half) continue;
-            if constexpr (!kFp8) {
+        for (int nr = 0; nr < kNR; ++nr) {
+          if (rr / 8 != nr || (t4 & 2) != ((rr & 4) >> 1)) continue;
 #pragma unroll
-              for (int x = 0; x < D / 8; ++x)
-                *reinterpret_cast<float2*>(dst + x * 8 + 2 * t4) =
-                    make_float2(o[x][2 * half] * w_row[half], o[x][2 * half + 1] * w_row[half]);
-            } else {
+          for (int e = 0; e < 2; ++e) {
+            float* dst = buf + (warp * 4 + (2 * t4 & 3) + e) * C::kBufRow;
 #pragma unroll
-              for (int x = 0; x < D / 16; ++x)
-                *reinterpret_cast<float4*>(dst + x * 16 + 4 * t4) =
-                    make_float4(o[2 * x][2 * half] * w_row[half], o[2 * x + 1][2 * half] * w_row[half],
-                                o[2 * x][2 * half + 1] * w_row[half], o[2 * x + 1][2 * half + 1] * w_row[half]);
+            for (int i = 0; i < D / 16; ++i) {
+              const float a = o[i][nr][e] * w_row[nr][e], c = o[i][nr][e + 2] * w_row[nr][e];
+              if constexpr (kFp8) {
+                *reinterpret_cast<float2*>(dst + i * 16 + 2 * l4) = make_float2(a, c);
+              } else {
+                dst[i * 16 + l4] = a;
+                dst[i * 16 + l4 + 8] = c;
+              }
             }
           }
         }
         if (!(ok = __all_sync(0xffffffffu, warps_sync()))) break;
 #pragma unroll
-        for (int e = 0; e < (kMT * 4 * D / 4 + 127) / 128; ++e) {
-          const int idx = threadIdx.x + e * 128;          // of 4 kMT rows x D / 4 groups of four columns
-          if (kMT * 4 * D / 4 < 128 && idx >= kMT * 4 * D / 4) break;
-          const int q4 = idx / (D / 4), c4 = (idx % (D / 4)) * 4, tile = q4 / 4;
-          const int r = tile * 16 + rr + q4 % 4;
+        for (int e = 0; e < (kRG * D + 127) / 128; ++e) {
+          const int idx = threadIdx.x + e * 128;          // of 4 kRG rows x D / 4 groups of four columns
+          if (kRG * D < 128 && idx >= kRG * D) break;
+          const int q4 = idx / (D / 4), c4 = (idx % (D / 4)) * 4, g = q4 / 4;
+          const int r = g * 8 * kNR + rr + q4 % 4;
           float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
           for (int k = 0; k < kKG; ++k) {
-            const float4 x = *reinterpret_cast<const float4*>(buf + ((tile * kKG + k) * 4 + q4 % 4) * C::kBufRow + c4);
+            const float4 x = *reinterpret_cast<const float4*>(buf + ((g * kKG + k) * 4 + q4 % 4) * C::kBufRow + c4);
             sum.x += x.x;
             sum.y += x.y;
             sum.z += x.z;
@@ -656,7 +684,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
           }
           if (r < it.rows) {
             if (!whole) {
-              *reinterpret_cast<float4*>(p.part_o + ((long long)slot * (16 * kMT) + r) * D + c4) = sum;
+              *reinterpret_cast<float4*>(p.part_o + ((long long)slot * kRows + r) * D + c4) = sum;
             } else {
               const int t = r / p.group;
               const uint2 v = make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
@@ -748,10 +776,11 @@ __global__ void __launch_bounds__(128) fa_rows_combine(const Attn p, int slot_ro
   if (lane == 0 && p.lse) p.lse[row] = lse;
 }
 
-template <int D, bool kFp8, int kMT>
+template <int D, bool kFp8, int kRG, int kNR>
 static int launch(const CUtensorMap& tk, const CUtensorMap& tv, const Attn& p, int grid, cudaStream_t s) {
   using C = RowsCfg<D, kFp8>;
-  auto kern = fa_rows_kernel<D, kFp8, kMT>;
+  constexpr int kRows = 8 * kNR * kRG;
+  auto kern = fa_rows_kernel<D, kFp8, kRG, kNR>;
   static std::atomic<uint64_t> prepared{0};
   int rc = prepare_kernel(reinterpret_cast<const void*>(kern), C::kSmemBytes, kRowsThreads, 128 * (kRowsRegCompute + kRowsRegLoad), "few-rows kernel",
                           &prepared);
@@ -759,7 +788,7 @@ static int launch(const CUtensorMap& tk, const CUtensorMap& tv, const Attn& p, i
   kern<<<grid, kRowsThreads, C::kSmemBytes, s>>>(tk, tv, p);
   if ((rc = check_cuda(cudaGetLastError(), "launch fa_rows_kernel"))) return rc;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(p.c.B * p.c.Hkv * (16 * kMT / 4)));
+  cfg.gridDim = dim3((unsigned)(p.c.B * p.c.Hkv * (kRows / 4)));
   cfg.blockDim = dim3(128);
   cfg.stream = s;
   cudaLaunchAttribute early;
@@ -767,14 +796,15 @@ static int launch(const CUtensorMap& tk, const CUtensorMap& tv, const Attn& p, i
   early.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
-  return check_cuda(cudaLaunchKernelEx(&cfg, fa_rows_combine<D>, p, 16 * kMT), "launch fa_rows_combine");
+  return check_cuda(cudaLaunchKernelEx(&cfg, fa_rows_combine<D>, p, kRows), "launch fa_rows_combine");
 }
 
 template <int D, bool kFp8>
 static int launch_tiles(const CUtensorMap& tk, const CUtensorMap& tv, const Attn& p, int grid, cudaStream_t s) {
-  if (p.few_rows <= 16) return launch<D, kFp8, 1>(tk, tv, p, grid, s);
-  if (p.few_rows <= 32) return launch<D, kFp8, 2>(tk, tv, p, grid, s);
-  return launch<D, kFp8, 4>(tk, tv, p, grid, s);
+  if (p.few_rows == 8) return launch<D, kFp8, 1, 1>(tk, tv, p, grid, s);
+  if (p.few_rows == 16) return launch<D, kFp8, 1, 2>(tk, tv, p, grid, s);
+  if (p.few_rows == 32) return launch<D, kFp8, 2, 2>(tk, tv, p, grid, s);
+  return launch<D, kFp8, 4, 2>(tk, tv, p, grid, s);
 }
 
 int launch_rows(const Attn& p, int d, bool fp8, cudaStream_t s) {

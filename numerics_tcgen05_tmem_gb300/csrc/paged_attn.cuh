@@ -12,7 +12,7 @@
 namespace fa {
 namespace paged {
 
-// The few-rows kernel takes sequences of up to this many rows for a kv head (four tiles of 16).
+// The few-rows kernel takes sequences of up to this many rows for a kv head (four groups of 16).
 constexpr int kMaxFewRows = 64;
 
 struct Attn {   // arguments of both kernels
@@ -27,7 +27,7 @@ struct Attn {   // arguments of both kernels
   int4* part_info;
   int T, Hq, group;
   int max_rows;              // largest number of rows of a sequence (the caller's max_q)
-  int few_rows;              // sequences of up to this many rows are the few-rows kernel's, 0: none is
+  int few_rows;              // sequences of up to this many rows (8, 16, 32, 64) are the few-rows kernel's; 0: none
   int window, sinks;         // window 0: none
   float scale, scale_log2;   // scale_log2 = scale log2(e)
 };
@@ -94,8 +94,9 @@ __device__ __forceinline__ void tma_load_page(uint32_t dst, const CUtensorMap* m
       : "memory");
 }
 
-// Few rows: the grid that fa_rows_kernel is launched with, and its partial results: two slots of
-// 16 * row tiles rows for each CTA (the item that it continues, the item that it leaves unfinished).
+// Few rows: the most CTAs that fa_rows_kernel is launched with, and its partial results: two slots of
+// few_rows rows (8, 16, 32 or 64) for each CTA: the item that it continues, the item that it leaves
+// unfinished.
 constexpr int kRowsMaxCtas = 304;
 
 // Chunks: an upper bound of the pairs of tiles that T packed rows of B sequences need.

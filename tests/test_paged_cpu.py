@@ -83,10 +83,11 @@ def test_bad_attention_arguments_are_refused(lib, kw, code, word):
 
 def test_workspace_sizes(lib):
     size = binding.fa_fwd_paged_workspace_size
-    # single tokens: two slots of 16 rows for each of 304 CTAs (FP32 outputs and log-sum-exps), and 16
-    # bytes for each sequence and kv head
-    assert size(5, 5, 1, 8, 2, 64, 1000) == 2 * 304 * 16 * 64 * 4 + 2 * 304 * 16 * 4 + 256
-    assert size(64, 64, 1, 32, 8, 128, 1 << 20) == 2 * 304 * 16 * 129 * 4 + 64 * 8 * 16
+    # single tokens: two slots of 8 (16, 32, 64) rows for each of 304 CTAs (FP32 outputs and
+    # log-sum-exps), and 16 bytes for each sequence and kv head
+    assert size(5, 5, 1, 8, 2, 64, 1000) == 2 * 304 * 8 * 64 * 4 + 2 * 304 * 8 * 4 + 256
+    assert size(64, 64, 1, 32, 8, 128, 1 << 20) == 2 * 304 * 8 * 129 * 4 + 64 * 8 * 16
+    assert size(64, 64, 1, 32, 2, 128, 1 << 20) == 2 * 304 * 16 * 129 * 4 + 64 * 2 * 16
     # a chunk whose tiles fill the SMs needs none; one of few rows over many keys is split
     assert size(8192, 1, 8192, 32, 8, 128, 1 << 15) == 0
     assert size(128, 1, 128, 1, 1, 128, 1 << 15) > 0
