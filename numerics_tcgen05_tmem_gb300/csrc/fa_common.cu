@@ -146,13 +146,14 @@ static int encode_3d(CUtensorMap* map, CUtensorMapDataType dtype, int elem_bytes
 }
 
 int make_tmap_pages(CUtensorMap* map, const void* base, bool fp8, int d, int page_size, int heads, int pages,
-                    long long page_stride, int box_rows) {
+                    long long page_stride, int box_rows, bool linear) {
   const int elem = fp8 ? 1 : 2, row = d * elem, atom = row >= 128 ? 128 : 64;
   const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)page_size, (cuuint64_t)heads, (cuuint64_t)pages};
   const cuuint64_t strides[3] = {(cuuint64_t)row, (cuuint64_t)page_size * row, (cuuint64_t)page_stride * elem};
-  const cuuint32_t box[4] = {(cuuint32_t)(atom / elem), (cuuint32_t)box_rows, 1, 1};
+  const cuuint32_t box[4] = {(cuuint32_t)((linear ? row : atom) / elem), (cuuint32_t)box_rows, 1, 1};
   return encode(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box,
-                atom == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+                linear ? CU_TENSOR_MAP_SWIZZLE_NONE
+                       : (atom == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B));
 }
 
 int make_tmap_rows(CUtensorMap* map, const void* base, int tokens, int heads, int d, long long stride, int box_heads,

@@ -59,8 +59,9 @@ int make_tmap_f32_bhnd(CUtensorMap* map, const void* base, int BH, int N, int d,
 // Encode a 4-D tensor map over a page pool [pages][heads][page_size][d] of BF16 (fp8: 1-byte codes)
 // whose pages are page_stride elements apart: a box is one swizzle atom row wide (128 bytes; 64 with
 // a 64-byte swizzle for 1-byte d = 64) and box_rows slots high; a page out of range reads as zeros.
+// linear: whole rows without a swizzle instead (1-byte codes).
 int make_tmap_pages(CUtensorMap* map, const void* base, bool fp8, int d, int page_size, int heads, int pages,
-                    long long page_stride, int box_rows);
+                    long long page_stride, int box_rows, bool linear = false);
 
 // Encode a 3-D BF16 tensor map over packed rows [tokens, heads, d], tokens `stride` elements apart,
 // with a 128-byte swizzle and a (64 x box_heads x box_tokens) box; tokens out of range read as zeros.

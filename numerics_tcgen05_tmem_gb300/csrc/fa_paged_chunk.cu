@@ -8,9 +8,9 @@
 //     `group` rows each: TMA brings Q in that order from the packed rows (a box of group heads by
 //     tokens), and K and V are read once for the whole group.  With a group that does not divide 128
 //     the last rows of a tile stay unused.
-//   * K and V blocks come page by page (BF16), or through a warpgroup that reads E4M3 codes from the
-//     pages, multiplies them by their vector's scale and writes the BF16 operand tiles (exact for
-//     power-of-two scales).  The conversion runs beside the softmax and needs no buffer in memory.
+//   * K and V blocks come page by page.  E4M3 codes land in slots of their own, from which a warpgroup
+//     multiplies them by their vector's scale and writes the BF16 operand tiles (exact for power-of-two
+//     scales) beside the softmax.
 //   * V rows that no row of the CTA sees (slots behind the sequence's end, keys before the window)
 //     may hold anything, and 0 * NaN is NaN: they are zeroed in shared memory before the product.
 //   * Few long rows would leave SMs idle: the host then splits a tile's keys over several CTAs, whose
@@ -34,8 +34,8 @@ struct ChunkCfg {
   static constexpr int kMmaWarp = 12, kLoadWarp = 13, kGuardWarp = 14, kConvertWarp = 16;
   // registers per thread after the launch: softmax, correction, MMA/TMA, conversion
   static constexpr int kRegLaunch = kFp8 ? 96 : 128;
-  static constexpr int kRegSoftmax = kFp8 ? 160 : 176, kRegCorr = kFp8 ? 40 : 96, kRegOther = kFp8 ? 32 : 56,
-                       kRegConvert = 88;
+  static constexpr int kRegSoftmax = kFp8 ? 168 : 176, kRegCorr = kFp8 ? 40 : 96, kRegOther = kFp8 ? 32 : 56,
+                       kRegConvert = 72;
   static constexpr int kSplit =
       256 * kRegSoftmax + 128 * kRegCorr + 128 * kRegOther + (kFp8 ? 128 * kRegConvert : 0);
   static_assert(kSplit <= kThreads * kRegLaunch, "register split exceeds the launch allocation");
@@ -43,24 +43,37 @@ struct ChunkCfg {
   static constexpr int kAtomBlock = 128 * 128;       // bytes of one
   static constexpr int kTileBytes = kAtoms * kAtomBlock;
   static constexpr int kQOff = 0, kKOff = 2 * kTileBytes, kVOff = kKOff + kStages * kTileBytes;
-  static constexpr int kSmemBytes = kVOff + kStages * kTileBytes + 1024;
+  // E4M3: slots for the codes of a tile (K and V of a block in turn) and their vectors' scales; at
+  // d = 128 two fill what the tiles leave
+  static constexpr int kSlots = kFp8 ? (D == 128 ? 2 : 4) : 0;
+  static constexpr int kCodeOff = kVOff + kStages * kTileBytes, kCodeBytes = kN * D;
+  static constexpr int kScaleOff = kCodeOff + kSlots * kCodeBytes;
+  static constexpr int kBarOff = kScaleOff + kSlots * kN * 4;
   static constexpr uint32_t kTmemO = 256;            // S0 | S1 | O0 | O1
   static constexpr uint32_t kIdescS = idesc_bf16(128, kN, false, false);
   static constexpr uint32_t kIdescO = idesc_bf16(128, D, false, true);
 };
+
+constexpr int kMaxSlots = 4;
 
 struct ChunkShared {
   uint64_t q_full, k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
   // a V block with unseen rows: the MMA thread, which has seen it land, asks for the zeroing and
   // waits for it (one request at a time, so the parities cannot alias)
   uint64_t v_dirty, v_clean;
+  uint64_t code_full[kMaxSlots], code_empty[kMaxSlots];   // E4M3: a slot has landed / has been read
   uint64_t s_full[2], p_half[2], p_full[2], pv_done[2], o_done[2], alpha_ready[2], o_ready[2], l_ready[2];
   uint64_t mma_done;
   float alpha[2][kM];
-  float lfin[2][kM];               // row sums; +inf for rows that saw nothing (O / l = 0)
   uint32_t tmem_base, abort_flag;
   int b, tile;                     // this CTA's sequence and pair of tiles; b = -1: none
 };
+
+template <int D, bool kFp8>
+constexpr int chunk_smem() {
+  return ChunkCfg<D, kFp8>::kBarOff + (int)sizeof(ChunkShared);
+}
+static_assert(chunk_smem<128, true>() <= 227 * 1024, "shared-memory layout exceeds 227 KB");
 
 // The work of one CTA: a pair of tiles of sequence b for kv head h, steps [js, je) of its walk.
 struct ChunkWork {
@@ -98,9 +111,16 @@ __global__ void __launch_bounds__(ChunkCfg<D, kFp8>::kThreads, 1)
     fa_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const Attn p, const int max_splits) {
   using C = ChunkCfg<D, kFp8>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ ChunkShared sh;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  // the swizzled tiles need a 1024-byte aligned base (there is no slack for E4M3, d = 128)
+  if (smem_u32(smem) & 1023u) {
+    if (threadIdx.x == 0) report_bounds(p.c.status, kSiteSmemAlign, (long long)smem_u32(smem));
+    return;
+  }
+  ChunkShared& sh = *reinterpret_cast<ChunkShared*>(smem + C::kBarOff);
+  // row sums for the last step, +inf for rows that saw nothing (O / l = 0): in the tile's Q, which its
+  // last S has read by then
+  auto lfin = [&](int t) { return reinterpret_cast<float*>(smem + C::kQOff + t * C::kTileBytes); };
   volatile uint32_t* abort_flag = &sh.abort_flag;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   // blockIdx.x = (pair of tiles, kv head, split), split fastest
@@ -141,6 +161,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, kFp8>::kThreads, 1)
       mbar_init(&sh.k_empty[s], 1);
       mbar_init(&sh.v_full[s], kFp8 ? 128 : 1);
       mbar_init(&sh.v_empty[s], 1);
+    }
+    for (int s = 0; s < C::kSlots; ++s) {
+      mbar_init(&sh.code_full[s], 1);
+      mbar_init(&sh.code_empty[s], 128);
     }
     mbar_init(&sh.v_dirty, 1);
     mbar_init(&sh.v_clean, 1);
@@ -184,76 +208,68 @@ __global__ void __launch_bounds__(ChunkCfg<D, kFp8>::kThreads, 1)
   if (kFp8 && warp >= C::kConvertWarp) {
     if constexpr (kFp8) {
     // ------------------------------------------------------------ E4M3 -> BF16 operand tiles
-    // Thread = key of the block.  The codes of the next tile (K and V in turn) are loaded before the
-    // current one is converted, so their latency is covered.
+    // D / 16 neighbouring threads take one key's row, 16 codes each; a thread has D / 16 rows.
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegConvert));
-    const int r = threadIdx.x - 32 * C::kConvertWarp;
-    const int page_size = 1 << p.c.page_shift;
-    uint4 next[D / 16];
-    float next_scale = 0.f;
-    long long row = 0;      // page and slot of this thread's key in the current block
-    bool have = false;
-    auto locate = [&](int j) {
-      const int key = wk.w.at(js + j) + r;
-      have = wk.w.seen(key);
-      int page = -1;
-      if (have) page = find_page(p.c, b, key, kSitePagedPage);
-      have = page >= 0;
-      row = have ? (long long)h * page_size + (key & (page_size - 1)) : 0;
-      return page;
-    };
-    int page = 0;
-    auto fetch = [&](const void* pool, const float* scales) {
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(pool) + page * p.c.page_stride + row * D);
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) next[i] = have ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-      next_scale = have ? __ldg(scales + page * p.c.scale_stride + row) : 0.f;
-    };
-    // row r of an operand tile: 16-byte chunk x (8 elements) of each 64-column block at (x ^ r % 8)
-    auto store = [&](uint8_t* tile, const uint4 (&codes)[D / 16], float scale) {
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
-        uint32_t o[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 lo = e4m3x2_to_float2(w[e]), hi = e4m3x2_to_float2(w[e] >> 16);
-          o[2 * e] = pack_bf16x2(lo.x * scale, lo.y * scale);
-          o[2 * e + 1] = pack_bf16x2(hi.x * scale, hi.y * scale);
-        }
-        uint8_t* dst = tile + (i / 4) * C::kAtomBlock + r * 128;
-        const int x = (i % 4) * 2;
-        *reinterpret_cast<uint4*>(dst + ((x ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4*>(dst + (((x + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
-      }
-      fence_proxy_async_smem();
-    };
-    if (nbmax > 0) {
-      page = max(locate(0), 0);
-      fetch(p.c.k, p.c.k_scale);
-    }
+    constexpr int kPer = D / 16, kRowStep = 128 / kPer;
+    const int r0 = (threadIdx.x - 32 * C::kConvertWarp) / kPer, x = threadIdx.x % kPer;
+    // a row's 16 codes become two 16-byte chunks of a 64-column block, swizzled; the second block's
+    // threads store theirs in the other order, so that a row's threads meet different banks
+    const int flip = x / 4;
+    const uint32_t dst0 = (uint32_t)((x / 4) * C::kAtomBlock + r0 * 128 + ((((x % 4) * 2 + flip) ^ (r0 & 7)) << 4));
+    const uint32_t dst1 = (uint32_t)((x / 4) * C::kAtomBlock + r0 * 128 + ((((x % 4) * 2 + 1 - flip) ^ (r0 & 7)) << 4));
+    static_assert(kRowStep % 8 == 0, "a thread's rows share one swizzle phase");
     bool ok = true;
+    int n = 0;   // tiles converted
     for (int j = 0; ok && j < nbmax; ++j) {
-      const int s = j % kStages;
-      const uint32_t ph = (j / kStages) & 1;
-      uint4 cur[D / 16];
+      const int s = j % kStages, key0 = wk.w.at(js + j);
+      const bool gaps = unseen(key0);
+#pragma unroll 1
+      for (int kv = 0; kv < 2; ++kv, ++n) {
+        uint8_t* tile = smem + (kv ? C::kVOff : C::kKOff) + s * C::kTileBytes;
+        const int slot = n % C::kSlots;
+        if (!(ok = mbar_wait(&sh.code_full[slot], (n / C::kSlots) & 1, abort_flag, p.c.status))) break;
+        uint4 codes[kPer];
+        float scale[kPer];
+        const uint4* src = reinterpret_cast<const uint4*>(smem + C::kCodeOff + slot * C::kCodeBytes + r0 * D) + x;
+        const float* sc = reinterpret_cast<const float*>(smem + C::kScaleOff) + slot * kN + r0;
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) cur[i] = next[i];
-      float scale = next_scale;
-      fetch(p.c.v, p.c.v_scale);
-      if (!(ok = mbar_wait(&sh.k_empty[s], ph ^ 1, abort_flag, p.c.status))) break;
-      store(smem + C::kKOff + s * C::kTileBytes, cur, scale);
-      mbar_arrive(&sh.k_full[s]);
+        for (int i = 0; i < kPer; ++i) {
+          codes[i] = src[i * kRowStep * D / 16];
+          scale[i] = sc[i * kRowStep];
+        }
+        if (gaps) {  // slots that no row sees may hold anything
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) cur[i] = next[i];
-      scale = next_scale;
-      if (j + 1 < nbmax) {
-        page = max(locate(j + 1), 0);
-        fetch(p.c.k, p.c.k_scale);
+          for (int i = 0; i < kPer; ++i)
+            if (!wk.w.seen(key0 + i * kRowStep + r0)) {
+              codes[i] = make_uint4(0, 0, 0, 0);
+              scale[i] = 0.f;
+            }
+        }
+        mbar_arrive(&sh.code_empty[slot]);
+        // the products that read this stage's previous tile are done
+        if (!(ok = mbar_wait(kv ? &sh.v_empty[s] : &sh.k_empty[s], ((j / kStages) & 1) ^ 1, abort_flag, p.c.status))) break;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+          uint4 o[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint32_t y[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float2 f = e4m3x2_to_float2(w[2 * e + q / 2] >> (16 * (q & 1)));
+              float a, c;
+              mul2(a, c, f.x, f.y, scale[i], scale[i]);
+              y[q] = pack_bf16x2(a, c);
+            }
+            o[e] = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+          *reinterpret_cast<uint4*>(tile + dst0 + i * kRowStep * 128) = flip ? o[1] : o[0];
+          *reinterpret_cast<uint4*>(tile + dst1 + i * kRowStep * 128) = flip ? o[0] : o[1];
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(kv ? &sh.v_full[s] : &sh.k_full[s]);
       }
-      if (!(ok = mbar_wait(&sh.v_empty[s], ph ^ 1, abort_flag, p.c.status))) break;
-      store(smem + C::kVOff + s * C::kTileBytes, cur, scale);
-      mbar_arrive(&sh.v_full[s]);
     }
     }
   } else if (warp >= C::kMmaWarp) {
@@ -271,10 +287,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, kFp8>::kThreads, 1)
                         wk.s.q0 + wk.tok0 + t * wk.tokens);
       }
       __syncwarp();
-      if constexpr (!kFp8) {
+      {
         const int page_size = 1 << p.c.page_shift;
         const int box = min(page_size, kN), ppb = kN / box, per_group = 32 / ppb;
-        int nk = 0, nv = 0;
+        int nk = 0, nv = 0, n = 0;   // K and V tiles, or slots of codes, loaded
         bool ok = true;
         for (int jg = 0; ok && jg < nbmax; jg += per_group) {
           const int jl = jg + lane / ppb;
@@ -286,26 +302,45 @@ __global__ void __launch_bounds__(ChunkCfg<D, kFp8>::kThreads, 1)
               if (x >= 0) page = x;
             }
           }
-          for (int jj = 0; jj < per_group && jg + jj < nbmax; ++jj) {
+          for (int jj = 0; ok && jj < per_group && jg + jj < nbmax; ++jj) {
             const int j = jg + jj, s = j % kStages;
             const uint32_t ph = (j / kStages) & 1;
             const int pg = __shfl_sync(0xffffffffu, page, jj * ppb + lane % ppb);
             const int slot = (wk.w.at(js + j) + lane * box) & (page_size - 1);
-            auto load = [&](const CUtensorMap* map, uint64_t* full, uint32_t tile) {
-              if (lane == 0) mbar_arrive_expect_tx(full, C::kTileBytes);
-              __syncwarp();
-              if (lane < ppb)
-                for (int c = 0; c < C::kAtoms; ++c)
-                  tma_load_page(base + tile + c * C::kAtomBlock + lane * box * 128, map, full, c * 64, slot, h, pg);
-            };
-            ok = __all_sync(0xffffffffu, mbar_wait(&sh.k_empty[s], ph ^ 1, abort_flag, p.c.status));
-            if (!ok) break;
-            load(&tmK, &sh.k_full[s], C::kKOff + s * C::kTileBytes);
-            nk = j + 1;
-            ok = __all_sync(0xffffffffu, mbar_wait(&sh.v_empty[s], ph ^ 1, abort_flag, p.c.status));
-            if (!ok) break;
-            load(&tmV, &sh.v_full[s], C::kVOff + s * C::kTileBytes);
-            nv = j + 1;
+            if constexpr (kFp8) {
+              const bool real = lane < ppb && pg < p.c.num_pages;
+              const int scaled = __popc(__ballot_sync(0xffffffffu, real));
+              for (int kv = 0; kv < 2; ++kv, ++n) {
+                const int x = n % C::kSlots;
+                ok = __all_sync(0xffffffffu, mbar_wait(&sh.code_empty[x], ((n / C::kSlots) & 1) ^ 1, abort_flag, p.c.status));
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(&sh.code_full[x], C::kCodeBytes + scaled * box * 4);
+                __syncwarp();
+                if (lane < ppb)
+                  tma_load_page(base + C::kCodeOff + x * C::kCodeBytes + lane * box * D, kv ? &tmV : &tmK, &sh.code_full[x], 0,
+                                slot, h, pg);
+                if (real)
+                  bulk_load(smem + C::kScaleOff + (x * kN + lane * box) * 4,
+                            (kv ? p.c.v_scale : p.c.k_scale) + pg * p.c.scale_stride + (long long)h * page_size + slot, box * 4,
+                            &sh.code_full[x]);
+              }
+            } else {
+              auto load = [&](const CUtensorMap* map, uint64_t* full, uint32_t tile) {
+                if (lane == 0) mbar_arrive_expect_tx(full, C::kTileBytes);
+                __syncwarp();
+                if (lane < ppb)
+                  for (int c = 0; c < C::kAtoms; ++c)
+                    tma_load_page(base + tile + c * C::kAtomBlock + lane * box * 128, map, full, c * 64, slot, h, pg);
+              };
+              ok = __all_sync(0xffffffffu, mbar_wait(&sh.k_empty[s], ph ^ 1, abort_flag, p.c.status));
+              if (!ok) break;
+              load(&tmK, &sh.k_full[s], C::kKOff + s * C::kTileBytes);
+              nk = j + 1;
+              ok = __all_sync(0xffffffffu, mbar_wait(&sh.v_empty[s], ph ^ 1, abort_flag, p.c.status));
+              if (!ok) break;
+              load(&tmV, &sh.v_full[s], C::kVOff + s * C::kTileBytes);
+              nv = j + 1;
+            }
           }
         }
         if (*abort_flag) {
@@ -315,6 +350,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, kFp8>::kThreads, 1)
             mbar_wait(&sh.k_full[j % kStages], (j / kStages) & 1, &ignore_abort, p.c.status);
           for (int j = max(0, nv - kStages); j < nv; ++j)
             mbar_wait(&sh.v_full[j % kStages], (j / kStages) & 1, &ignore_abort, p.c.status);
+          if constexpr (kFp8)
+            for (int i = max(0, n - C::kSlots); i < n; ++i)
+              mbar_wait(&sh.code_full[i % C::kSlots], (i / C::kSlots) & 1, &ignore_abort, p.c.status);
         }
       }
       if (*abort_flag) {
@@ -484,7 +522,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kFp8>::kThreads, 1)
     }
     if (ok) {
       const bool empty = m == -INFINITY && l == 0.f;  // no visible key in this piece (a NaN score is not that)
-      sh.lfin[t][r] = empty ? INFINITY : l;
+      lfin(t)[r] = empty ? INFINITY : l;
       mbar_arrive(&sh.l_ready[t]);
       const float lse = empty ? -INFINITY : m * p.scale + logf(l);
       const long long row = (long long)(wk.s.q0 + tok) * p.Hq + h * p.group + (r - tr * p.group);
@@ -539,7 +577,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kFp8>::kThreads, 1)
       if (!(ok = mbar_wait(&sh.o_done[t], 0, abort_flag, p.c.status))) break;
       if (!(ok = mbar_wait(&sh.l_ready[t], 0, abort_flag, p.c.status))) break;
       tc_fence_after();
-      const float inv_l = 1.f / sh.lfin[t][r];
+      const float inv_l = 1.f / lfin(t)[r];
       const int tr = r / p.group, tok = wk.tok0 + t * wk.tokens + tr;
       const bool valid = tr < wk.tokens && tok < wk.s.n;
       const long long row = valid ? (long long)(wk.s.q0 + tok) * p.Hq + h * p.group + (r - tr * p.group) : 0;
@@ -635,12 +673,12 @@ static int launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMa
   using C = ChunkCfg<D, kFp8>;
   auto kern = fa_chunk_kernel<D, kFp8>;
   static std::atomic<uint64_t> prepared{0};
-  int rc = prepare_kernel(reinterpret_cast<const void*>(kern), C::kSmemBytes, C::kThreads, C::kSplit, "chunk kernel",
+  int rc = prepare_kernel(reinterpret_cast<const void*>(kern), chunk_smem<D, kFp8>(), C::kThreads, C::kSplit, "chunk kernel",
                           &prepared);
   if (rc) return rc;
   const long long grid = chunk_pairs(p.T, p.c.B, p.group) * p.c.Hkv * splits;
   if (grid >= (1ll << 31)) return set_error(FA_ERR_INVALID_ARG, "too many tiles for one launch");
-  kern<<<(unsigned)grid, C::kThreads, C::kSmemBytes, s>>>(tq, tk, tv, p, splits);
+  kern<<<(unsigned)grid, C::kThreads, chunk_smem<D, kFp8>(), s>>>(tq, tk, tv, p, splits);
   if ((rc = check_cuda(cudaGetLastError(), "launch fa_chunk_kernel")) || splits == 1) return rc;
   fa_chunk_combine<D><<<(unsigned)(((long long)p.T * p.Hq + 7) / 8), 256, 0, s>>>(p, splits);
   return check_cuda(cudaGetLastError(), "launch fa_chunk_combine");
@@ -648,15 +686,13 @@ static int launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMa
 
 int launch_chunk(const Attn& p, int d, bool fp8, int splits, cudaStream_t s) {
   const int page_size = 1 << p.c.page_shift;
-  CUtensorMap tq, tk{}, tv{};
+  CUtensorMap tq, tk, tv;
   int rc;
   if ((rc = make_tmap_rows(&tq, p.q, p.T, p.Hq, d, p.q_stride, p.group, kM / p.group))) return rc;
-  if (!fp8) {
-    const int box = page_size < kN ? page_size : kN;
-    if ((rc = make_tmap_pages(&tk, p.c.k, false, d, page_size, p.c.Hkv, p.c.num_pages, p.c.page_stride, box)) ||
-        (rc = make_tmap_pages(&tv, p.c.v, false, d, page_size, p.c.Hkv, p.c.num_pages, p.c.page_stride, box)))
-      return rc;
-  }
+  const int box = page_size < kN ? page_size : kN;
+  if ((rc = make_tmap_pages(&tk, p.c.k, fp8, d, page_size, p.c.Hkv, p.c.num_pages, p.c.page_stride, box, fp8)) ||
+      (rc = make_tmap_pages(&tv, p.c.v, fp8, d, page_size, p.c.Hkv, p.c.num_pages, p.c.page_stride, box, fp8)))
+    return rc;
   if (d == 64) return fp8 ? launch<64, true>(tq, tk, tv, p, splits, s) : launch<64, false>(tq, tk, tv, p, splits, s);
   return fp8 ? launch<128, true>(tq, tk, tv, p, splits, s) : launch<128, false>(tq, tk, tv, p, splits, s);
 }
