@@ -11,10 +11,14 @@
 //   * K and V blocks come page by page.  E4M3 codes land in slots of their own, from which a warpgroup
 //     multiplies them by their vector's scale and writes the BF16 operand tiles (exact for power-of-two
 //     scales) beside the softmax.
+//   * With rows for one tile only the tensor core would wait for each block's softmax and the softmax for
+//     each product.  Both warpgroups then work on that tile: one on the even blocks, the other on the odd
+//     ones, each with its own running maximum, sum and O, joined at the end (_DUAL_).
 //   * V rows that no row of the CTA sees (slots behind the sequence's end, keys before the window)
 //     may hold anything, and 0 * NaN is NaN: they are zeroed in shared memory before the product.
-//   * Few long rows would leave SMs idle: the host then splits a tile's keys over several CTAs, whose
-//     normalised FP32 results fa_chunk_combine joins (in order, whatever the timing).
+//   * The tiles that are left after whole rounds of one CTA per SM would leave SMs idle: their keys are
+//     split over several CTAs, whose normalised FP32 results fa_chunk_combine joins (in order, whatever
+//     the timing).
 // Softmax: running maximum and sum in FP32 per row (one thread per row), P~ rounded to BF16 for the
 // product as the tensor core takes it.  Plain shift: the stabilised rule guards the training
 // backward, and the output does not depend on the shift.
@@ -34,7 +38,7 @@ struct ChunkCfg {
   static constexpr int kMmaWarp = 12, kLoadWarp = 13, kGuardWarp = 14, kConvertWarp = 16;
   // registers per thread after the launch: softmax, correction, MMA/TMA, conversion
   static constexpr int kRegLaunch = kFp8 ? 96 : 128;
-  static constexpr int kRegSoftmax = kFp8 ? 168 : 176, kRegCorr = kFp8 ? 40 : 96, kRegOther = kFp8 ? 32 : 56,
+  static constexpr int kRegSoftmax = kFp8 ? 160 : 176, kRegCorr = kFp8 ? 48 : 96, kRegOther = kFp8 ? 40 : 56,
                        kRegConvert = 72;
   static constexpr int kSplit =
       256 * kRegSoftmax + 128 * kRegCorr + 128 * kRegOther + (kFp8 ? 128 * kRegConvert : 0);
@@ -100,16 +104,48 @@ struct ChunkWork {
   }
 };
 
+// How the launch's tiles (pair of tiles, kv head) are dealt: the first `whole` to one CTA each, every
+// other one to `splits` CTAs that take a share of its keys.
+struct ChunkGrid {
+  int whole, splits;
+};
+
 // Pairs of tiles of sequence b that are the chunk kernel's.
 __device__ __forceinline__ int chunk_tiles(const Attn& p, int b) {
   const int n = load_seq(p, b).n, per = 2 * (kM / p.group);
   return n * p.group <= p.few_rows ? 0 : (n + per - 1) / per;
 }
 
+// The sequence and pair of tiles that is number `want` of the launch (-1: none), 32 sequences at a
+// time; a sequence's last (longest) tiles come first.  The whole warp calls it.
+__device__ __forceinline__ void find_tiles(const Attn& p, int want, int& found, int& tile) {
+  const int lane = threadIdx.x % 32;
+  found = -1;
+  tile = 0;
+  for (int b0 = 0; b0 < p.c.B && found < 0; b0 += 32) {
+    const int mine = b0 + lane < p.c.B ? chunk_tiles(p, b0 + lane) : 0;
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, want < incl);
+    const int at = hit ? __ffs(hit) - 1 : 31;
+    const int upto = __shfl_sync(0xffffffffu, incl, at), n = __shfl_sync(0xffffffffu, mine, at);
+    if (hit) {
+      found = b0 + at;
+      tile = n - 1 - (want - (upto - n));
+    } else {
+      want -= upto;
+    }
+  }
+}
+
 template <int D, bool kFp8>
 __global__ void __launch_bounds__(ChunkCfg<D, kFp8>::kThreads, 1)
     fa_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                    const __grid_constant__ CUtensorMap tmV, const Attn p, const int max_splits) {
+                    const __grid_constant__ CUtensorMap tmV, const Attn p, const ChunkGrid g) {
   using C = ChunkCfg<D, kFp8>;
   extern __shared__ __align__(1024) uint8_t smem[];
   // the swizzled tiles need a 1024-byte aligned base (there is no slack for E4M3, d = 128)
@@ -118,36 +154,18 @@ __global__ void __launch_bounds__(ChunkCfg<D, kFp8>::kThreads, 1)
     return;
   }
   ChunkShared& sh = *reinterpret_cast<ChunkShared*>(smem + C::kBarOff);
-  // row sums for the last step, +inf for rows that saw nothing (O / l = 0): in the tile's Q, which its
-  // last S has read by then
-  auto lfin = [&](int t) { return reinterpret_cast<float*>(smem + C::kQOff + t * C::kTileBytes); };
   volatile uint32_t* abort_flag = &sh.abort_flag;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   // blockIdx.x = (pair of tiles, kv head, split), split fastest
-  const int split = blockIdx.x % max_splits;
-  const int h = (blockIdx.x / max_splits) % p.c.Hkv;
+  const int extra = (int)blockIdx.x - g.whole;   // number among the split tiles' CTAs; negative: a whole tile
+  const int max_splits = extra < 0 ? 1 : g.splits;
+  const int split = extra < 0 ? 0 : extra % g.splits;
+  const int unit = extra < 0 ? (int)blockIdx.x : g.whole + extra / g.splits;
+  const int h = unit % p.c.Hkv;
 
   if (warp == 0) {
-    // which sequence this pair of tiles belongs to: 32 sequences at a time
-    int want = blockIdx.x / (max_splits * p.c.Hkv), found = -1, tile = 0;
-    for (int b0 = 0; b0 < p.c.B && found < 0; b0 += 32) {
-      const int mine = b0 + lane < p.c.B ? chunk_tiles(p, b0 + lane) : 0;
-      int incl = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o *= 2) {
-        const int x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += x;
-      }
-      const uint32_t hit = __ballot_sync(0xffffffffu, want < incl);
-      const int at = hit ? __ffs(hit) - 1 : 31;
-      const int upto = __shfl_sync(0xffffffffu, incl, at), n = __shfl_sync(0xffffffffu, mine, at);
-      if (hit) {
-        found = b0 + at;
-        tile = n - 1 - (want - (upto - n));  // the last (longest) tiles of a sequence first
-      } else {
-        want -= upto;
-      }
-    }
+    int found, tile;
+    find_tiles(p, unit / p.c.Hkv, found, tile);
     if (lane == 0) {
       sh.b = found;
       sh.tile = tile;
@@ -189,8 +207,18 @@ __global__ void __launch_bounds__(ChunkCfg<D, kFp8>::kThreads, 1)
   const int js = (int)((long long)wk.w.steps * split / wk.splits);
   const int je = (int)((long long)wk.w.steps * (split + 1) / wk.splits);
   // steps of this CTA for each tile (0 where the tile ends before the piece)
-  const int nb0 = max(0, min(je, wk.steps(0)) - js), nb1 = max(0, min(je, wk.steps(1)) - js);
-  const int nbmax = max(nb0, nb1);
+  const int nbmax = je - js;
+  // rows for one tile only: chain t (its warpgroup, S and O) takes the blocks 2 i + t of that tile
+  const bool dual = wk.steps(1) == 0 && nbmax > 1;
+  const int nb0 = dual ? (nbmax + 1) / 2 : max(0, min(je, wk.steps(0)) - js);
+  const int nb1 = dual ? nbmax / 2 : max(0, min(je, wk.steps(1)) - js);
+  // block of step i of tile (or chain) t
+  auto block = [&](int t, int i) { return dual ? 2 * i + t : i; };
+  // the rows' sums for the last step, +inf for rows that saw nothing (O / l = 0), and with two chains
+  // their maxima: in the tile's Q, which its last S has read by then (two chains: in the unused tile)
+  auto fin = [&](int t) {
+    return reinterpret_cast<float*>(smem + C::kQOff + (dual ? C::kTileBytes + t * 2 * kM * 4 : t * C::kTileBytes));
+  };
   // whether the block at `key` has rows that no row of the CTA sees
   auto unseen = [&](int key) {
     return key + kN > wk.w.hi || (key < wk.w.lo && key + kN > wk.w.sinks);
@@ -220,11 +248,13 @@ __global__ void __launch_bounds__(ChunkCfg<D, kFp8>::kThreads, 1)
     static_assert(kRowStep % 8 == 0, "a thread's rows share one swizzle phase");
     bool ok = true;
     int n = 0;   // tiles converted
-    for (int j = 0; ok && j < nbmax; ++j) {
-      const int s = j % kStages, key0 = wk.w.at(js + j);
-      const bool gaps = unseen(key0);
+    for (int step = 0; ok && step <= nbmax; ++step) {
 #pragma unroll 1
-      for (int kv = 0; kv < 2; ++kv, ++n) {
+      for (int kv = 0; kv < 2; ++kv) {
+        const int j = step - kv;   // K of block `step`, then V of the block before
+        if (j < 0 || j >= nbmax) continue;
+        const int s = j % kStages, key0 = wk.w.at(js + j);
+        const bool gaps = unseen(key0);
         uint8_t* tile = smem + (kv ? C::kVOff : C::kKOff) + s * C::kTileBytes;
         const int slot = n % C::kSlots;
         if (!(ok = mbar_wait(&sh.code_full[slot], (n / C::kSlots) & 1, abort_flag, p.c.status))) break;
@@ -269,6 +299,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kFp8>::kThreads, 1)
         }
         fence_proxy_async_smem();
         mbar_arrive(kv ? &sh.v_full[s] : &sh.k_full[s]);
+        ++n;
       }
     }
     }
@@ -277,7 +308,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kFp8>::kThreads, 1)
     if (warp == C::kLoadWarp) {
       // ---------------------------------------------------------- loads: Q, and K and V page by page
       const uint32_t base = smem_u32(smem);
-      const int ntiles = nb1 > 0 ? 2 : 1;
+      const int ntiles = nb1 > 0 && !dual ? 2 : 1;
       if (elect_one()) {
         tma_prefetch_desc(&tmQ);
         mbar_arrive_expect_tx(&sh.q_full, ntiles * wk.tokens * p.group * 128 * C::kAtoms);
@@ -292,7 +323,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, kFp8>::kThreads, 1)
         const int box = min(page_size, kN), ppb = kN / box, per_group = 32 / ppb;
         int nk = 0, nv = 0, n = 0;   // K and V tiles, or slots of codes, loaded
         bool ok = true;
-        for (int jg = 0; ok && jg < nbmax; jg += per_group) {
+        // K of block j, then V of the block before it: a K load never waits behind the V of a block
+        // whose P~ V has yet to free the stage
+        int v_page = 0, v_slot = 0;   // of the block before
+        for (int jg = 0; ok && jg <= nbmax; jg += per_group) {
           const int jl = jg + lane / ppb;
           int page = p.c.num_pages;  // out of range: zeros
           if (jl < nbmax) {
@@ -302,45 +336,45 @@ __global__ void __launch_bounds__(ChunkCfg<D, kFp8>::kThreads, 1)
               if (x >= 0) page = x;
             }
           }
-          for (int jj = 0; ok && jj < per_group && jg + jj < nbmax; ++jj) {
-            const int j = jg + jj, s = j % kStages;
-            const uint32_t ph = (j / kStages) & 1;
-            const int pg = __shfl_sync(0xffffffffu, page, jj * ppb + lane % ppb);
-            const int slot = (wk.w.at(js + j) + lane * box) & (page_size - 1);
-            if constexpr (kFp8) {
-              const bool real = lane < ppb && pg < p.c.num_pages;
-              const int scaled = __popc(__ballot_sync(0xffffffffu, real));
-              for (int kv = 0; kv < 2; ++kv, ++n) {
+          for (int jj = 0; ok && jj < per_group && jg + jj <= nbmax; ++jj) {
+            const int k_page = __shfl_sync(0xffffffffu, page, jj * ppb + lane % ppb);
+            const int k_slot = jg + jj < nbmax ? (wk.w.at(js + jg + jj) + lane * box) & (page_size - 1) : 0;
+            for (int kv = 0; kv < 2; ++kv) {
+              const int j = jg + jj - kv, s = j & (kStages - 1);
+              if (j < 0 || j >= nbmax) continue;
+              const int pg = kv ? v_page : k_page, slot = kv ? v_slot : k_slot;
+              const CUtensorMap* map = kv ? &tmV : &tmK;
+              if constexpr (kFp8) {
+                const bool real = lane < ppb && pg < p.c.num_pages;
+                const int scaled = __popc(__ballot_sync(0xffffffffu, real));
                 const int x = n % C::kSlots;
                 ok = __all_sync(0xffffffffu, mbar_wait(&sh.code_empty[x], ((n / C::kSlots) & 1) ^ 1, abort_flag, p.c.status));
                 if (!ok) break;
                 if (lane == 0) mbar_arrive_expect_tx(&sh.code_full[x], C::kCodeBytes + scaled * box * 4);
                 __syncwarp();
                 if (lane < ppb)
-                  tma_load_page(base + C::kCodeOff + x * C::kCodeBytes + lane * box * D, kv ? &tmV : &tmK, &sh.code_full[x], 0,
-                                slot, h, pg);
+                  tma_load_page(base + C::kCodeOff + x * C::kCodeBytes + lane * box * D, map, &sh.code_full[x], 0, slot, h, pg);
                 if (real)
                   bulk_load(smem + C::kScaleOff + (x * kN + lane * box) * 4,
                             (kv ? p.c.v_scale : p.c.k_scale) + pg * p.c.scale_stride + (long long)h * page_size + slot, box * 4,
                             &sh.code_full[x]);
-              }
-            } else {
-              auto load = [&](const CUtensorMap* map, uint64_t* full, uint32_t tile) {
+                ++n;
+              } else {
+                uint64_t* full = kv ? &sh.v_full[s] : &sh.k_full[s];
+                ok = __all_sync(0xffffffffu, mbar_wait(kv ? &sh.v_empty[s] : &sh.k_empty[s], ((j / kStages) & 1) ^ 1,
+                                                       abort_flag, p.c.status));
+                if (!ok) break;
                 if (lane == 0) mbar_arrive_expect_tx(full, C::kTileBytes);
                 __syncwarp();
+                const uint32_t tile = base + (kv ? C::kVOff : C::kKOff) + s * C::kTileBytes + lane * box * 128;
                 if (lane < ppb)
                   for (int c = 0; c < C::kAtoms; ++c)
-                    tma_load_page(base + tile + c * C::kAtomBlock + lane * box * 128, map, full, c * 64, slot, h, pg);
-              };
-              ok = __all_sync(0xffffffffu, mbar_wait(&sh.k_empty[s], ph ^ 1, abort_flag, p.c.status));
-              if (!ok) break;
-              load(&tmK, &sh.k_full[s], C::kKOff + s * C::kTileBytes);
-              nk = j + 1;
-              ok = __all_sync(0xffffffffu, mbar_wait(&sh.v_empty[s], ph ^ 1, abort_flag, p.c.status));
-              if (!ok) break;
-              load(&tmV, &sh.v_full[s], C::kVOff + s * C::kTileBytes);
-              nv = j + 1;
+                    tma_load_page(tile + c * C::kAtomBlock, map, full, c * 64, slot, h, pg);
+                (kv ? nv : nk) = j + 1;
+              }
             }
+            v_page = k_page;
+            v_slot = k_slot;
           }
         }
         if (*abort_flag) {
@@ -389,7 +423,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kFp8>::kThreads, 1)
         tc_fence_after();
         int cleaned = 0;  // V blocks that had rows zeroed
         auto issue_s = [&](int t, int s) {
-          const uint32_t a0 = sQ + t * C::kTileBytes, b0 = sK + s * C::kTileBytes;
+          const uint32_t a0 = sQ + (dual ? 0 : t * C::kTileBytes), b0 = sK + s * C::kTileBytes;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = (kk / 4) * C::kAtomBlock + (kk % 4) * 32;
@@ -409,36 +443,41 @@ __global__ void __launch_bounds__(ChunkCfg<D, kFp8>::kThreads, 1)
           }
         };
         // S0_0 S1_0 | PV0_0 S0_1 PV1_0 S1_1 | ... ; P~ V in two halves over the keys, the first as
-        // soon as the softmax has stored it
-        for (int j = 0; ok && j <= nbmax; ++j) {
-          const int s = j % kStages, sp = (j + kStages - 1) % kStages;
-          if (j < nbmax) {
+        // soon as the softmax has stored it.  Two chains on one tile: S0_0 | S1_1 | PV0_0 S0_2 |
+        // PV1_1 S1_3 | ... (chain _ block), each block's P~ V two blocks later.
+        const int lag = dual ? 2 : 1;
+        for (int j = 0; ok && j < nbmax + lag; ++j) {
+          const int s = j % kStages, jp = j - lag, sp = jp & (kStages - 1);   // block jp's P~ V
+          const bool has_s = j < nbmax, has_pv = jp >= 0 && jp < nbmax;
+          if (has_s) {
             if (!(ok = mbar_wait(&sh.k_full[s], (j / kStages) & 1, abort_flag, p.c.status))) break;
             tc_fence_after();
           }
-          if (j > 0) {
-            if (!(ok = mbar_wait(&sh.v_full[sp], ((j - 1) / kStages) & 1, abort_flag, p.c.status))) break;
-            if (!kFp8 && unseen(wk.w.at(js + j - 1))) {
+          if (has_pv) {
+            if (!(ok = mbar_wait(&sh.v_full[sp], (jp / kStages) & 1, abort_flag, p.c.status))) break;
+            if (!kFp8 && unseen(wk.w.at(js + jp))) {
               mbar_arrive(&sh.v_dirty);
               if (!(ok = mbar_wait(&sh.v_clean, cleaned++ & 1, abort_flag, p.c.status))) break;
             }
             tc_fence_after();
           }
           for (int t = 0; t < 2; ++t) {
-            if (j > 0 && j - 1 < nb[t]) {
-              if (!(ok = mbar_wait(&sh.p_half[t], (j - 1) & 1, abort_flag, p.c.status))) break;
-              if (j - 1 > 0 && !(ok = mbar_wait(&sh.o_ready[t], (j - 2) & 1, abort_flag, p.c.status))) break;
+            if (dual && t != (j & 1)) continue;
+            const int i = dual ? j / 2 : j, ip = i - 1;   // the tile's (chain's) step, and the one whose P~ V is due
+            if (has_pv && ip < nb[t]) {
+              if (!(ok = mbar_wait(&sh.p_half[t], ip & 1, abort_flag, p.c.status))) break;
+              if (ip > 0 && !(ok = mbar_wait(&sh.o_ready[t], (ip - 1) & 1, abort_flag, p.c.status))) break;
               tc_fence_after();
-              issue_pv(t, sp, j - 1, 0, kN / 32);
-              if (!(ok = mbar_wait(&sh.p_full[t], (j - 1) & 1, abort_flag, p.c.status))) break;
+              issue_pv(t, sp, ip, 0, kN / 32);
+              if (!(ok = mbar_wait(&sh.p_full[t], ip & 1, abort_flag, p.c.status))) break;
               tc_fence_after();
-              issue_pv(t, sp, j - 1, kN / 32, kN / 16);
+              issue_pv(t, sp, ip, kN / 32, kN / 16);
             }
-            if (j < nb[t]) issue_s(t, s);
+            if (has_s && i < nb[t]) issue_s(t, s);
           }
           if (!ok) break;
-          if (j < nbmax) tc_commit(&sh.k_empty[s]);
-          if (j > 0) tc_commit(&sh.v_empty[sp]);
+          if (has_s) tc_commit(&sh.k_empty[s]);
+          if (has_pv) tc_commit(&sh.v_empty[sp]);
         }
         tc_commit(&sh.mma_done);
         {
@@ -453,7 +492,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kFp8>::kThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegSoftmax));
     const int t = warp / 4, r = (warp % 4) * 32 + lane;
     const int nb = t == 0 ? nb0 : nb1;
-    const int tr = r / p.group, tok = wk.tok0 + t * wk.tokens + tr;
+    const int tr = r / p.group, tok = wk.tok0 + (dual ? 0 : t * wk.tokens) + tr;
     const bool valid = tr < wk.tokens && tok < wk.s.n;
     const int pos = valid ? wk.s.pos0 + tok : -1;
     const uint32_t tS = tmem + t * 128 + ((uint32_t)((warp % 4) * 32) << 16);
@@ -475,7 +514,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kFp8>::kThreads, 1)
 #pragma unroll
       for (int i = 0; i < kN; ++i) sv[i] = __uint_as_float(raw[i]);
       // mask: keys after the row's token, and keys before its window that are no sinks
-      const int col0 = wk.w.at(js + j);
+      const int col0 = wk.w.at(js + block(t, j));
       const int lim = pos - col0 + 1, w_lo = p.window ? pos - p.window + 1 - col0 : 0, s_hi = p.sinks - col0;
       const bool open = lim >= kN && (w_lo <= 0 || s_hi >= kN);
       float bm;
@@ -522,17 +561,18 @@ __global__ void __launch_bounds__(ChunkCfg<D, kFp8>::kThreads, 1)
     }
     if (ok) {
       const bool empty = m == -INFINITY && l == 0.f;  // no visible key in this piece (a NaN score is not that)
-      lfin(t)[r] = empty ? INFINITY : l;
+      fin(t)[r] = empty && !dual ? INFINITY : l;
+      if (dual) fin(t)[kM + r] = m;
       mbar_arrive(&sh.l_ready[t]);
       const float lse = empty ? -INFINITY : m * p.scale + logf(l);
       const long long row = (long long)(wk.s.q0 + tok) * p.Hq + h * p.group + (r - tr * p.group);
-      if (valid) {
+      if (valid && !dual) {
         if (wk.splits > 1)
-          p.part_lse[(long long)split * p.T * p.Hq + row] = lse;
+          p.part_lse[(long long)extra * (2 * kM) + t * kM + r] = lse;
         else if (p.lse)
           p.lse[row] = lse;
       }
-      if (wk.splits == 1)
+      if (wk.splits == 1 && !dual)
         report_nonfinite((valid && !empty && !(fabsf(lse) < INFINITY)) ? 1u : 0u, p.c.status, kOutLse);
     }
   } else {
@@ -542,7 +582,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kFp8>::kThreads, 1)
     const uint32_t tO = tmem + C::kTmemO + ((uint32_t)((warp % 4) * 32) << 16);
     const int nb[2] = {nb0, nb1};
     bool ok = true;
-    for (int j = 1; ok && j < nbmax; ++j) {
+    for (int j = 1; ok && j < max(nb0, nb1); ++j) {
       for (int t = 0; t < 2; ++t) {
         if (j >= nb[t]) continue;
         if (!(ok = mbar_wait(&sh.alpha_ready[t], (j - 1) & 1, abort_flag, p.c.status))) break;
@@ -571,13 +611,71 @@ __global__ void __launch_bounds__(ChunkCfg<D, kFp8>::kThreads, 1)
         mbar_arrive(&sh.o_ready[t]);
       }
     }
+    // Two chains: their O weighted by exp(max - joint max) over the joint sum, and the row's lse
+    if (ok && dual) {
+      for (int t = 0; ok && t < 2; ++t)
+        ok = mbar_wait(&sh.o_done[t], 0, abort_flag, p.c.status) && mbar_wait(&sh.l_ready[t], 0, abort_flag, p.c.status);
+      if (ok) {
+        tc_fence_after();
+        const float m0 = fin(0)[kM + r], m1 = fin(1)[kM + r], top = fmaxf(m0, m1), tu = top == -INFINITY ? 0.f : top;
+        float w0 = ex2_approx((m0 - tu) * p.scale_log2), w1 = ex2_approx((m1 - tu) * p.scale_log2);
+        const float sum = fin(0)[r] * w0 + fin(1)[r] * w1;
+        const bool empty = top == -INFINITY && sum == 0.f;
+        const float lse = empty ? -INFINITY : top * p.scale + logf(sum);
+        w0 = empty ? 0.f : w0 / sum;
+        w1 = empty ? 0.f : w1 / sum;
+        const int tr = r / p.group, tok = wk.tok0 + tr;
+        const bool valid = tr < wk.tokens && tok < wk.s.n;
+        const long long row = valid ? (long long)(wk.s.q0 + tok) * p.Hq + h * p.group + (r - tr * p.group) : 0;
+        uint32_t bad = 0;
+#pragma unroll
+        for (int c0 = 0; c0 < D; c0 += 16) {
+          uint32_t x[16], y[16];
+          tmem_ld16(tO + c0, x);
+          tmem_ld16(tO + D + c0, y);
+          tmem_ld_wait();
+          reg_fence(x);
+          reg_fence(y);
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            x[i] = __float_as_uint(fmaf(__uint_as_float(x[i]), w0, __uint_as_float(y[i]) * w1));
+          if (wk.splits > 1) {
+            float4* dst = reinterpret_cast<float4*>(p.part_o + ((long long)extra * (2 * kM) + r) * D + c0);
+            if (valid)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                dst[i] = make_float4(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1]), __uint_as_float(x[4 * i + 2]),
+                                     __uint_as_float(x[4 * i + 3]));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              x[i] = pack_bf16x2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+              bad += nonfinite_bf16x2(x[i]);
+            }
+            uint4* dst = reinterpret_cast<uint4*>(p.o + row * D + c0);
+            if (valid) {
+              dst[0] = make_uint4(x[0], x[1], x[2], x[3]);
+              dst[1] = make_uint4(x[4], x[5], x[6], x[7]);
+            }
+          }
+        }
+        if (valid && wk.splits > 1)
+          p.part_lse[(long long)extra * (2 * kM) + r] = lse;
+        else if (valid && p.lse)
+          p.lse[row] = lse;
+        if (wk.splits == 1) {
+          report_nonfinite(valid ? bad : 0u, p.c.status, kOutO);
+          report_nonfinite((valid && !empty && !(fabsf(lse) < INFINITY)) ? 1u : 0u, p.c.status, kOutLse);
+        }
+      }
+    }
     // O / l, to the output or to this piece's partial result
-    for (int t = 0; ok && t < 2; ++t) {
+    for (int t = 0; ok && !dual && t < 2; ++t) {
       if (nb[t] == 0) continue;
       if (!(ok = mbar_wait(&sh.o_done[t], 0, abort_flag, p.c.status))) break;
       if (!(ok = mbar_wait(&sh.l_ready[t], 0, abort_flag, p.c.status))) break;
       tc_fence_after();
-      const float inv_l = 1.f / lfin(t)[r];
+      const float inv_l = 1.f / fin(t)[r];
       const int tr = r / p.group, tok = wk.tok0 + t * wk.tokens + tr;
       const bool valid = tr < wk.tokens && tok < wk.s.n;
       const long long row = valid ? (long long)(wk.s.q0 + tok) * p.Hq + h * p.group + (r - tr * p.group) : 0;
@@ -589,7 +687,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kFp8>::kThreads, 1)
         tmem_ld_wait();
         reg_fence(w);
         if (wk.splits > 1) {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + ((long long)split * p.T * p.Hq + row) * D + c0);
+          float4* dst = reinterpret_cast<float4*>(p.part_o + ((long long)extra * (2 * kM) + t * kM + r) * D + c0);
           if (valid)
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -621,21 +719,11 @@ __global__ void __launch_bounds__(ChunkCfg<D, kFp8>::kThreads, 1)
   }
 }
 
-// Joins the pieces of tiles whose keys were split: one warp per (token, query head).
+// Row `row` of the output from the `pieces` partial rows that are 2 kM apart from `base` on.
 template <int D>
-__global__ void __launch_bounds__(256) fa_chunk_combine(const Attn p, const int max_splits) {
-  const int lane = threadIdx.x % 32;
-  const long long row = (long long)blockIdx.x * 8 + threadIdx.x / 32;
-  if (row >= (long long)p.T * p.Hq) return;
-  const int token = (int)(row / p.Hq);
-  const int b = find_sequence(p.q_indptr, p.c.B, token);
-  if (b >= p.c.B || chunk_tiles(p, b) == 0) return;
-  const int tile = (token - __ldg(p.q_indptr + b)) / (2 * (kM / p.group));
-  const int pieces = ChunkWork(p, b, tile, max_splits).splits;
-  if (pieces < 2) return;
-  const long long rows = (long long)p.T * p.Hq;
+__device__ __forceinline__ void join_row(const Attn& p, long long base, int pieces, long long row, int lane) {
   constexpr int kPer = D / 32;
-  const float mine = lane < pieces ? p.part_lse[lane * rows + row] : -INFINITY;
+  const float mine = lane < pieces ? p.part_lse[base + lane * (2 * kM)] : -INFINITY;
   float top = mine;
 #pragma unroll
   for (int off = 16; off > 0; off /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
@@ -643,14 +731,24 @@ __global__ void __launch_bounds__(256) fa_chunk_combine(const Attn p, const int 
   float sum = 0.f, acc[kPer];
 #pragma unroll
   for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+#pragma unroll 4
   for (int i = 0; i < pieces; ++i) {
     const float part = __shfl_sync(0xffffffffu, mine, i);
     if (part == -INFINITY) continue;  // saw nothing: its output may not have been written
     const float w = ex2_approx((part - tu) * 1.4426950408889634f);
     sum += w;
-    const float* src = p.part_o + (i * rows + row) * D + lane * kPer;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) acc[e] = fmaf(w, src[e], acc[e]);
+    const float* src = p.part_o + (base + i * (2 * kM)) * D + lane * kPer;
+    if constexpr (kPer == 4) {
+      const float4 x = *reinterpret_cast<const float4*>(src);
+      acc[0] = fmaf(w, x.x, acc[0]);
+      acc[1] = fmaf(w, x.y, acc[1]);
+      acc[2] = fmaf(w, x.z, acc[2]);
+      acc[3] = fmaf(w, x.w, acc[3]);
+    } else {
+      const float2 x = *reinterpret_cast<const float2*>(src);
+      acc[0] = fmaf(w, x.x, acc[0]);
+      acc[1] = fmaf(w, x.y, acc[1]);
+    }
   }
   const bool empty = top == -INFINITY && sum == 0.f;
   const float inv = empty ? 0.f : 1.f / sum;
@@ -659,16 +757,45 @@ __global__ void __launch_bounds__(256) fa_chunk_combine(const Attn p, const int 
   for (int e = 0; e < kPer / 2; ++e) {
     w2[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
     bad += nonfinite_bf16x2(w2[e]);
-    reinterpret_cast<uint32_t*>(p.o + row * D)[lane * (kPer / 2) + e] = w2[e];
   }
+  if constexpr (kPer == 4)
+    *reinterpret_cast<uint2*>(p.o + row * D + lane * 4) = make_uint2(w2[0], w2[1]);
+  else
+    *reinterpret_cast<uint32_t*>(p.o + row * D + lane * 2) = w2[0];
   report_nonfinite(bad, p.c.status, kOutO);
   const float lse = empty ? -INFINITY : top + logf(sum);
   report_nonfinite((lane == 0 && !empty && !(fabsf(lse) < INFINITY)) ? 1u : 0u, p.c.status, kOutLse);
   if (lane == 0 && p.lse) p.lse[row] = lse;
 }
 
+// Joins the pieces of tiles whose keys were split: 32 rows of a tile per CTA, four per warp.  Launched
+// while the pieces are still being computed (programmatic launch).
+constexpr int kJoinRows = 32;
+
+template <int D>
+__global__ void __launch_bounds__(256) fa_chunk_combine(const Attn p, const ChunkGrid g) {
+  // before any exit: the launch that follows this one must find the pieces' kernel complete
+  cudaGridDependencySynchronize();
+  const int lane = threadIdx.x % 32;
+  constexpr int kParts = 2 * kM / kJoinRows;
+  const int unit = g.whole + blockIdx.x / kParts, h = unit % p.c.Hkv;
+  int b, tile;
+  find_tiles(p, unit / p.c.Hkv, b, tile);
+  if (b < 0) return;
+  const ChunkWork wk(p, b, tile, g.splits);
+  const int pieces = wk.splits;
+  if (pieces < 2) return;
+  for (int i = threadIdx.x / 32; i < kJoinRows; i += 8) {
+    const int x = (blockIdx.x % kParts) * kJoinRows + i, t = x / kM, r = x % kM, tr = r / p.group;
+    const int tok = wk.tok0 + t * wk.tokens + tr;
+    if (tr >= wk.tokens || tok >= wk.s.n) continue;   // the same for the whole warp
+    const long long row = (long long)(wk.s.q0 + tok) * p.Hq + h * p.group + (r - tr * p.group);
+    join_row<D>(p, (long long)(unit - g.whole) * g.splits * (2 * kM) + x, pieces, row, lane);
+  }
+}
+
 template <int D, bool kFp8>
-static int launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const Attn& p, int splits,
+static int launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const Attn& p, int whole, int splits,
                   cudaStream_t s) {
   using C = ChunkCfg<D, kFp8>;
   auto kern = fa_chunk_kernel<D, kFp8>;
@@ -676,15 +803,25 @@ static int launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMa
   int rc = prepare_kernel(reinterpret_cast<const void*>(kern), chunk_smem<D, kFp8>(), C::kThreads, C::kSplit, "chunk kernel",
                           &prepared);
   if (rc) return rc;
-  const long long grid = chunk_pairs(p.T, p.c.B, p.group) * p.c.Hkv * splits;
+  const long long tiles = chunk_pairs(p.T, p.c.B, p.group) * p.c.Hkv;
+  const long long grid = whole + (tiles - whole) * splits;
   if (grid >= (1ll << 31)) return set_error(FA_ERR_INVALID_ARG, "too many tiles for one launch");
-  kern<<<(unsigned)grid, C::kThreads, chunk_smem<D, kFp8>(), s>>>(tq, tk, tv, p, splits);
+  const ChunkGrid g{whole, splits};
+  kern<<<(unsigned)grid, C::kThreads, chunk_smem<D, kFp8>(), s>>>(tq, tk, tv, p, g);
   if ((rc = check_cuda(cudaGetLastError(), "launch fa_chunk_kernel")) || splits == 1) return rc;
-  fa_chunk_combine<D><<<(unsigned)(((long long)p.T * p.Hq + 7) / 8), 256, 0, s>>>(p, splits);
-  return check_cuda(cudaGetLastError(), "launch fa_chunk_combine");
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((tiles - whole) * (2 * kM / kJoinRows)));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return check_cuda(cudaLaunchKernelEx(&cfg, fa_chunk_combine<D>, p, g), "launch fa_chunk_combine");
 }
 
-int launch_chunk(const Attn& p, int d, bool fp8, int splits, cudaStream_t s) {
+int launch_chunk(const Attn& p, int d, bool fp8, int whole, int splits, cudaStream_t s) {
   const int page_size = 1 << p.c.page_shift;
   CUtensorMap tq, tk, tv;
   int rc;
@@ -693,8 +830,8 @@ int launch_chunk(const Attn& p, int d, bool fp8, int splits, cudaStream_t s) {
   if ((rc = make_tmap_pages(&tk, p.c.k, fp8, d, page_size, p.c.Hkv, p.c.num_pages, p.c.page_stride, box, fp8)) ||
       (rc = make_tmap_pages(&tv, p.c.v, fp8, d, page_size, p.c.Hkv, p.c.num_pages, p.c.page_stride, box, fp8)))
     return rc;
-  if (d == 64) return fp8 ? launch<64, true>(tq, tk, tv, p, splits, s) : launch<64, false>(tq, tk, tv, p, splits, s);
-  return fp8 ? launch<128, true>(tq, tk, tv, p, splits, s) : launch<128, false>(tq, tk, tv, p, splits, s);
+  if (d == 64) return fp8 ? launch<64, true>(tq, tk, tv, p, whole, splits, s) : launch<64, false>(tq, tk, tv, p, whole, splits, s);
+  return fp8 ? launch<128, true>(tq, tk, tv, p, whole, splits, s) : launch<128, false>(tq, tk, tv, p, whole, splits, s);
 }
 
 }  // namespace paged
@@ -707,11 +844,13 @@ using fa::paged::kMaxFewRows;
 // Which kernels a call launches and how: from sizes that the host knows.
 struct Plan {
   int few_rows;   // sequences of up to this many rows go to the few-rows kernel (0: it is not launched)
-  int splits;     // chunk kernel: most pieces of a tile's keys (0: it is not launched)
+  int splits;     // chunk kernel: most pieces of the keys of a tile past the first `whole` (0: not launched)
+  int whole;
+  long long extra;   // CTAs of split tiles
 };
 
-Plan make_plan(int T, int B, int max_q, int group, int Hkv, int max_kv) {
-  Plan pl{0, 0};
+Plan make_plan(int T, int B, int max_q, int group, int Hkv, int max_kv, int window) {
+  Plan pl{0, 0, 0, 0};
   const long long rows = (long long)max_q * group;
   if (rows <= kMaxFewRows) {
     pl.few_rows = rows <= 8 ? 8 : (rows <= 16 ? 16 : (rows <= 32 ? 32 : 64));
@@ -720,13 +859,30 @@ Plan make_plan(int T, int B, int max_q, int group, int Hkv, int max_kv) {
   // A batch of chunks may hold sequences with a token or two: those go to the few-rows kernel with one
   // row group (its fastest forms), everything else to the chunk kernel.
   if (B > 1 && group <= 16) pl.few_rows = group <= 8 ? 8 : 16;
-  // One CTA per SM: split the keys while the tiles leave half of the SMs without work.
+  // One CTA per SM at a time.  Whole rounds of tiles stay whole; the rest is split so that its pieces
+  // fill the SMs: the number of pieces that makes rounds * (steps of a piece + kPieceSteps) least, with
+  // kPieceSteps for a CTA's start and end and one more step for each piece's partial result.  (2048
+  // tokens over 32k keys, 256 tiles: 755 us whole, _US_ with the last 104 in four pieces each.)
+  constexpr int kPieceSteps = 4;
+  using fa::paged::kChunkSms;
   const long long tiles = fa::paged::chunk_pairs(T, B, group) * Hkv;
-  long long s = fa::paged::kChunkSms / tiles;
-  const long long most = (max_kv + 128 * fa::paged::kSplitSteps - 1) / (128 * fa::paged::kSplitSteps);
-  if (s > most) s = most;
-  if (s > fa::paged::kMaxSplits) s = fa::paged::kMaxSplits;
-  pl.splits = s < 1 ? 1 : (int)s;
+  const long long rest = tiles % kChunkSms;
+  long long steps = (max_kv + 127) / 128;
+  if (window && window / 128 + 3 < steps) steps = window / 128 + 3;
+  pl.splits = 1;
+  if (rest) {
+    long long best = 0;
+    for (int n = 1; n <= fa::paged::kMaxSplits && (n == 1 || steps / n >= fa::paged::kSplitSteps); ++n) {
+      const long long rounds = (rest * n + kChunkSms - 1) / kChunkSms;
+      const long long cost = rounds * ((steps + n - 1) / n + kPieceSteps) + (n > 1 ? n : 0);
+      if (best == 0 || cost < best) {
+        best = cost;
+        pl.splits = n;
+      }
+    }
+  }
+  pl.whole = (int)(pl.splits > 1 ? tiles - rest : tiles);
+  pl.extra = pl.splits > 1 ? rest * pl.splits : 0;
   return pl;
 }
 
@@ -736,14 +892,14 @@ struct Parts {
 
 // The workspace: FP32 partial outputs, their log-sum-exps, and the few-rows kernel's records.  The two
 // kernels of a mixed batch have parts of their own.
-Parts carve(const Plan& pl, int T, int B, int Hq, int Hkv, int d, Parts* chunk) {
+Parts carve(const Plan& pl, int B, int Hkv, int d, Parts* chunk) {
   const size_t rows = pl.few_rows ? (size_t)2 * fa::paged::kRowsMaxCtas * pl.few_rows : 0;
   Parts f;
   f.o = 0;
   f.lse = fa::round_up(rows * d * 4, 256);
   f.info = f.lse + fa::round_up(rows * 4, 256);
   f.total = f.info + (rows ? fa::round_up((size_t)B * Hkv * sizeof(int4), 256) : 0);
-  const size_t c_rows = pl.splits > 1 ? (size_t)pl.splits * T * Hq : 0;
+  const size_t c_rows = (size_t)pl.extra * 2 * fa::paged::kM;
   chunk->o = f.total;
   chunk->lse = chunk->o + fa::round_up(c_rows * d * 4, 256);
   chunk->info = 0;
@@ -765,11 +921,11 @@ int check_attn(int T, int B, int max_q, int Hq, int Hkv, int d) {
 
 }  // namespace
 
-extern "C" size_t fa_fwd_paged_workspace_size(int T, int B, int max_q, int Hq, int Hkv, int d, int max_kv) {
+extern "C" size_t fa_fwd_paged_workspace_size(int T, int B, int max_q, int Hq, int Hkv, int d, int max_kv, int window) {
   fa::clear_error();
-  if (check_attn(T, B, max_q, Hq, Hkv, d) || max_kv < 0 || T == 0) return 0;
+  if (check_attn(T, B, max_q, Hq, Hkv, d) || max_kv < 0 || window < 0 || T == 0) return 0;
   Parts chunk;
-  carve(make_plan(T, B, max_q, Hq / Hkv, Hkv, max_kv), T, B, Hq, Hkv, d, &chunk);
+  carve(make_plan(T, B, max_q, Hq / Hkv, Hkv, max_kv, window < max_kv ? window : 0), B, Hkv, d, &chunk);
   return chunk.total;
 }
 
@@ -794,9 +950,10 @@ extern "C" int fa_fwd_paged(const fa_paged_kv* kv, const void* q, int64_t q_stri
   if (!window && sinks) return set_error(FA_ERR_INVALID_ARG, "sinks need a window");
   if (T == 0 || max_q == 0) return FA_OK;
   const int max_kv = kv->max_pages * kv->page_size;
-  const Plan pl = make_plan(T, kv->B, max_q, Hq / kv->Hkv, kv->Hkv, max_kv);
+  if (window >= max_kv) window = 0;   // a window of the whole cache is none
+  const Plan pl = make_plan(T, kv->B, max_q, Hq / kv->Hkv, kv->Hkv, max_kv, window);
   Parts chunk;
-  const Parts few = carve(pl, T, kv->B, Hq, kv->Hkv, kv->d, &chunk);
+  const Parts few = carve(pl, kv->B, kv->Hkv, kv->d, &chunk);
   if (chunk.total) {
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255))
       return set_error(FA_ERR_INVALID_ARG, "workspace must be a 256-byte aligned device pointer");
@@ -815,7 +972,7 @@ extern "C" int fa_fwd_paged(const fa_paged_kv* kv, const void* q, int64_t q_stri
   p.group = Hq / kv->Hkv;
   p.max_rows = (int)((long long)max_q * p.group < INT32_MAX ? max_q * p.group : INT32_MAX);
   p.few_rows = pl.few_rows;
-  p.window = window < max_kv ? window : 0;  // a window of the whole cache is none
+  p.window = window;
   p.sinks = sinks < max_kv ? sinks : max_kv;
   p.scale = scale;
   p.scale_log2 = scale * 1.4426950408889634f;
@@ -826,7 +983,7 @@ extern "C" int fa_fwd_paged(const fa_paged_kv* kv, const void* q, int64_t q_stri
     paged::Attn c = p;
     c.part_o = reinterpret_cast<float*>(ws + chunk.o);
     c.part_lse = reinterpret_cast<float*>(ws + chunk.lse);
-    if ((rc = paged::launch_chunk(c, kv->d, fp8, pl.splits, s))) return rc;
+    if ((rc = paged::launch_chunk(c, kv->d, fp8, pl.whole, pl.splits, s))) return rc;
   }
   if (pl.few_rows) {
     p.part_o = reinterpret_cast<float*>(ws + few.o);

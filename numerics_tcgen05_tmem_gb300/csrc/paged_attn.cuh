@@ -103,12 +103,12 @@ constexpr int kRowsMaxCtas = 304;
 constexpr int kChunkSms = 152;   // CTAs that run at once, one per SM
 constexpr int kMaxSplits = 16;
 inline long long chunk_pairs(int T, int B, int group) {
-  const int per = 2 * (128 / group);
-  return T / per + (T < B ? T : B);
+  const int per = 2 * (128 / group), seqs = T < B ? T : B;   // each sequence may end inside a pair
+  return (T - seqs) / per + seqs;
 }
 
 int launch_rows(const Attn& p, int d, bool fp8, cudaStream_t s);
-int launch_chunk(const Attn& p, int d, bool fp8, int splits, cudaStream_t s);
+int launch_chunk(const Attn& p, int d, bool fp8, int whole, int splits, cudaStream_t s);
 
 }  // namespace paged
 }  // namespace fa

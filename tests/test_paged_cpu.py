@@ -88,9 +88,13 @@ def test_workspace_sizes(lib):
     assert size(5, 5, 1, 8, 2, 64, 1000) == 2 * 304 * 8 * 64 * 4 + 2 * 304 * 8 * 4 + 256
     assert size(64, 64, 1, 32, 8, 128, 1 << 20) == 2 * 304 * 8 * 129 * 4 + 64 * 8 * 16
     assert size(64, 64, 1, 32, 2, 128, 1 << 20) == 2 * 304 * 16 * 129 * 4 + 64 * 2 * 16
-    # a chunk whose tiles fill the SMs needs none; one of few rows over many keys is split
-    assert size(8192, 1, 8192, 32, 8, 128, 1 << 15) == 0
+    # chunks whose tiles (64 tokens by 4 heads of a group) fill whole rounds of 152 SMs need none; the
+    # tiles left over are split over the keys, unless the keys are few
+    assert size(152 * 64, 1, 152 * 64, 4, 1, 128, 1 << 15) == 0
+    assert size(153 * 64, 1, 153 * 64, 4, 1, 128, 1 << 15) > 0
+    assert size(153 * 64, 1, 153 * 64, 4, 1, 128, 256) == 0
     assert size(128, 1, 128, 1, 1, 128, 1 << 15) > 0
+    assert size(128, 1, 128, 1, 1, 128, 1 << 15, 100) == 0
     for bad in (dict(d=96), dict(Hq=7), dict(Hkv=0), dict(T=-1), dict(T=0), dict(B=0)):
         a = dict(T=5, B=5, max_q=1, Hq=8, Hkv=2, d=64, max_kv=1000)
         a.update(bad)

@@ -301,3 +301,14 @@ def test_dense_window_and_paged_attention_agree():
         M.assert_within("o", o, want, 2 * ref["o_tol"].transpose(0, 1))
         assert (lse.cpu() - lsed[0, :, rows].transpose(0, 1).cpu()).abs().max() <= 2 * M.LSE_TOL
     binding.device_status()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kv", [120, 128, 129, 256, 257, 384, 385, 513, 1300])
+def test_one_tile_of_rows_over_any_number_of_blocks(fmt, d, kv):
+    # 66 to 120 rows: one tile, whose blocks alternate between two chains (odd and even numbers of blocks)
+    for new, group in ((66, 1), (17, 6), (120, 1)):
+        c = P.make([kv], 2, d, 32, fmt, seed=kv + new)
+        check(c, [new], group)
+        check(c, [new], group, window=150, sinks=5)
