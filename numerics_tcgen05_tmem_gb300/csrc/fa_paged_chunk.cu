@@ -403,11 +403,12 @@ __global__ void __launch_bounds__(ChunkCfg<D, kFp8>::kThreads, 1)
           if (!unseen(key0)) continue;
           ok = __all_sync(0xffffffffu, mbar_wait(&sh.v_dirty, n++ & 1, abort_flag, p.c.status));
           if (!ok) break;
-          for (int r = 0; r < kN; ++r) {
+          for (int r = lane; r < kN; r += 32) {
             if (wk.w.seen(key0 + r)) continue;
             uint8_t* row = smem + C::kVOff + s * C::kTileBytes + r * 128;
-            if (lane < C::kAtoms * 8)
-              *reinterpret_cast<uint4*>(row + (lane / 8) * C::kAtomBlock + (lane % 8) * 16) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int x = 0; x < C::kAtoms * 8; ++x)   // a lane's chunks in an order that spreads the banks
+              *reinterpret_cast<uint4*>(row + (x / 8) * C::kAtomBlock + ((x ^ lane) & 7) * 16) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -494,13 +495,25 @@ __global__ void __launch_bounds__(ChunkCfg<D, kFp8>::kThreads, 1)
     const int nb = t == 0 ? nb0 : nb1;
     const int tr = r / p.group, tok = wk.tok0 + (dual ? 0 : t * wk.tokens) + tr;
     const bool valid = tr < wk.tokens && tok < wk.s.n;
-    const int pos = valid ? wk.s.pos0 + tok : -1;
+    // rows past the last token count as that token's: nothing of theirs is stored, and they must not
+    // send their warp through the masked path in every block
+    const int pos = valid ? wk.s.pos0 + tok : wk.last;
+    const bool idle = !__any_sync(0xffffffffu, valid);   // no row of the warp: only keeps the barriers going
     const uint32_t tS = tmem + t * 128 + ((uint32_t)((warp % 4) * 32) << 16);
     const float c = p.scale_log2;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int j = 0; j < nb; ++j) {
       if (!(ok = mbar_wait(&sh.s_full[t], j & 1, abort_flag, p.c.status))) break;
+      if (idle) {
+        if (j > 0) {
+          sh.alpha[t][r] = 1.f;
+          mbar_arrive(&sh.alpha_ready[t]);
+        }
+        mbar_arrive(&sh.p_half[t]);
+        mbar_arrive(&sh.p_full[t]);
+        continue;
+      }
       tc_fence_after();
       uint32_t raw[kN];
       float pmax[kN / 32];
