@@ -136,25 +136,8 @@ struct Params {
 // Over the padded rows (bh, q < N_pad): delta = rowsum(dO o O) in FP32, lse2 = lse log2(e)
 // and dQ_acc = 0 for q < N; delta = 0 and lse2 = +inf (so P = 0) for the padding.
 // d/8 lanes per row, 16-byte loads.
-//
-// kWin (windowed kernels): a row that sees few keys takes delta = sum_j P_ij (dO_i . V_j) from
-// probabilities recomputed in FP32 instead.  The stored O is rounded to BF16, which puts an error of
-// about 2^-9 |dO||O| on rowsum(dO o O); dS = P o (dP - delta) is a difference of terms of that size,
-// and with few keys nothing averages the error out: with 2 visible keys dq and dk were 0.6-1.0 %
-// off (relative Frobenius), 0.37 % from 16 keys on, whose BF16 rounding of dS and of the result
-// makes up 0.24 %.  At most kFewKeys keys per row, so the cost stays that of a short loop: windows
-// of that size only, and the first rows of longer ones.
-constexpr int kFewKeys = 16;
-
-// What the recomputation reads.
-struct FewKeys {
-  const __nv_bfloat16 *q, *k, *v;
-  int window, sinks;
-  float scale_log2;
-};
-
-template <int D, bool kWin>
-__global__ void __launch_bounds__(256) fa_bwd_preprocess(const FewKeys few, const __nv_bfloat16* __restrict__ o,
+template <int D>
+__global__ void __launch_bounds__(256) fa_bwd_preprocess(const __nv_bfloat16* __restrict__ o,
                                                          const __nv_bfloat16* __restrict__ dO,
                                                          const float* __restrict__ lse, float* __restrict__ delta,
                                                          float* __restrict__ lse2, float* __restrict__ delta_out,
@@ -189,55 +172,83 @@ __global__ void __launch_bounds__(256) fa_bwd_preprocess(const FewKeys few, cons
   }
 #pragma unroll
   for (int off = kLanesPerRow / 2; off > 0; off /= 2) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-  if constexpr (kWin) {
-    const int lo = max(0, q - few.window + 1), n_sink = min(few.sinks, lo);
-    const int seen = q + 1 - lo + n_sink;
-    const bool recompute = valid && seen <= kFewKeys;
-    const int most = (int)__reduce_max_sync(0xffffffffu, (unsigned)(recompute ? seen : 0));
-    if (most > 0) {   // the same for the whole warp
-      float qv[8], dv[8], sum = 0.f;
-      const float lse2_row = valid ? lse[row] * 1.4426950408889634f : 0.f;
-      auto widen = [](const __nv_bfloat16* src, float (&x)[8]) {
-        const uint4 u = *reinterpret_cast<const uint4*>(src);
-        const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = __bfloat1622float2(h[i]);
-          x[2 * i] = f.x;
-          x[2 * i + 1] = f.y;
-        }
-      };
-      if (recompute) {
-        widen(few.q + row * D + c, qv);
-        widen(dO + row * D + c, dv);
-      }
-      for (int j = 0; j < most; ++j) {
-        float s = 0.f, dp = 0.f;
-        if (recompute && j < seen) {
-          const long long key = bh * N + (j < n_sink ? j : lo + j - n_sink);
-          float kv[8], vv[8];
-          widen(few.k + key * D + c, kv);
-          widen(few.v + key * D + c, vv);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            s = fmaf(qv[i], kv[i], s);
-            dp = fmaf(dv[i], vv[i], dp);
-          }
-        }
-#pragma unroll
-        for (int off = kLanesPerRow / 2; off > 0; off /= 2) {
-          s += __shfl_xor_sync(0xffffffffu, s, off);
-          dp += __shfl_xor_sync(0xffffffffu, dp, off);
-        }
-        if (recompute && j < seen) sum = fmaf(ex2_approx(fmaf(s, few.scale_log2, -lse2_row)), dp, sum);
-      }
-      if (recompute) acc = sum;
-    }
-  }
   if (prow < rows_pad && (lane % kLanesPerRow) == 0) {
     delta[prow] = acc;
     lse2[prow] = valid ? lse[row] * 1.4426950408889634f : INFINITY;
     if (valid && delta_out) delta_out[row] = acc;
+  }
+}
+
+// --------------------------------------------------------------------------- delta of few keys
+// Windowed backward: a row that sees few keys takes delta = sum_j P_ij (dO_i . V_j) from probabilities
+// recomputed in FP32 instead.  The stored O is rounded to BF16, which puts an error of about
+// 2^-9 |dO||O| on rowsum(dO o O); dS = P o (dP - delta) is a difference of terms of that size, and
+// with few keys nothing averages the error out: with 2 visible keys dq and dk were 0.6-1.0 % off
+// (relative Frobenius), 0.37 % from 16 keys on, where the BF16 rounding of dS and of the result alone
+// makes 0.24 %.  Row i sees at most kFewKeys keys if i < kFewKeys or window + sinks <= kFewKeys, so
+// `rows` rows of each head are recomputed: the first kFewKeys, or all of them.  (Inside
+// fa_bwd_preprocess the code slowed every row down: 37 -> 57 us at 32 heads, 8k rows.)
+constexpr int kFewKeys = 16;
+
+template <int D>
+__global__ void __launch_bounds__(256) fa_bwd_delta_few(const __nv_bfloat16* __restrict__ q,
+                                                        const __nv_bfloat16* __restrict__ k,
+                                                        const __nv_bfloat16* __restrict__ v,
+                                                        const __nv_bfloat16* __restrict__ dO,
+                                                        const float* __restrict__ lse, float* __restrict__ delta,
+                                                        float* __restrict__ delta_out, int BH, int rows, int N, int N_pad,
+                                                        int window, int sinks, float scale_log2) {
+  constexpr int kLanesPerRow = D / 8;
+  constexpr int kRowsPerWarp = 32 / kLanesPerRow;
+  const int lane = threadIdx.x % 32;
+  const long long warp_global = (long long)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
+  const long long n = warp_global * kRowsPerWarp + lane / kLanesPerRow;
+  const long long bh = n / rows;
+  const int i = (int)(n - bh * rows);
+  const int c = (lane % kLanesPerRow) * 8;
+  const int lo = max(0, i - window + 1), n_sink = min(sinks, lo);
+  const int seen = bh < BH ? i + 1 - lo + n_sink : 0;
+  const int most = (int)__reduce_max_sync(0xffffffffu, (unsigned)seen);
+  const long long row = bh * N + i;
+  auto widen = [](const __nv_bfloat16* src, float (&x)[8]) {
+    const uint4 u = *reinterpret_cast<const uint4*>(src);
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = __bfloat1622float2(h[e]);
+      x[2 * e] = f.x;
+      x[2 * e + 1] = f.y;
+    }
+  };
+  float qv[8] = {}, gv[8] = {}, sum = 0.f, lse2 = 0.f;
+  if (seen > 0) {
+    widen(q + row * D + c, qv);
+    widen(dO + row * D + c, gv);
+    lse2 = lse[row] * 1.4426950408889634f;
+  }
+  for (int j = 0; j < most; ++j) {
+    float s = 0.f, dp = 0.f;
+    if (j < seen) {
+      const long long key = bh * N + (j < n_sink ? j : lo + j - n_sink);
+      float kx[8], vx[8];
+      widen(k + key * D + c, kx);
+      widen(v + key * D + c, vx);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        s = fmaf(qv[e], kx[e], s);
+        dp = fmaf(gv[e], vx[e], dp);
+      }
+    }
+#pragma unroll
+    for (int off = kLanesPerRow / 2; off > 0; off /= 2) {
+      s += __shfl_xor_sync(0xffffffffu, s, off);
+      dp += __shfl_xor_sync(0xffffffffu, dp, off);
+    }
+    if (j < seen) sum = fmaf(ex2_approx(fmaf(s, scale_log2, -lse2)), dp, sum);
+  }
+  if (seen > 0 && c == 0) {
+    delta[bh * N_pad + i] = sum;
+    if (delta_out) delta_out[row] = sum;
   }
 }
 
@@ -844,14 +855,20 @@ int launch_bwd(const void* q, const void* k, const void* v, const void* o, const
     constexpr int rows_per_block = 8 * (32 / (D / 8));
     const long long rows_pad = (long long)B * H * N_pad;
     const long long grid = (rows_pad + rows_per_block - 1) / rows_per_block;
-    const bwd::FewKeys few{static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
-                           static_cast<const __nv_bfloat16*>(v), window < N ? window : N, sinks < N ? sinks : N,
-                           scale * 1.4426950408889634f};
-    auto pre = window ? bwd::fa_bwd_preprocess<D, true> : bwd::fa_bwd_preprocess<D, false>;
-    pre<<<(unsigned)grid, 256, 0, stream>>>(
-        few, static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(dO), lse, sc.delta, sc.lse2,
+    bwd::fa_bwd_preprocess<D><<<(unsigned)grid, 256, 0, stream>>>(
+        static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(dO), lse, sc.delta, sc.lse2,
         delta_out, sc.dq_acc, rows_pad, N, N_pad);
     if ((rc = check_cuda(cudaGetLastError(), "launch fa_bwd_preprocess"))) return rc;
+    if (window) {
+      const int w = window < N ? window : N, sk = sinks < N ? sinks : N;
+      const int few = (w <= bwd::kFewKeys && sk <= bwd::kFewKeys - w) || N < bwd::kFewKeys ? N : bwd::kFewKeys;
+      const long long few_rows = (long long)B * H * few;
+      bwd::fa_bwd_delta_few<D><<<(unsigned)((few_rows + rows_per_block - 1) / rows_per_block), 256, 0, stream>>>(
+          static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v),
+          static_cast<const __nv_bfloat16*>(dO), lse, sc.delta, delta_out, B * H, few, N, N_pad, w, sk,
+          scale * 1.4426950408889634f);
+      if ((rc = check_cuda(cudaGetLastError(), "launch fa_bwd_delta_few"))) return rc;
+    }
   }
   if (stages & FA_BWD_MAIN) {
   CUtensorMap tq, tk, tv, tdo;

@@ -501,18 +501,28 @@ __global__ void __launch_bounds__(Shape<kT>::kThreads, Shape<kT>::kCtasPerSm)
       // mask: keys past N, and keys after the query on the causal diagonal
       const int col0 = walk.at(j) * kBlockN;
       const int lim = (kWin || p.causal) ? min(p.N - col0, row - col0 + 1) : (p.N - col0);
-      if (lim < kBlockN) {
-#pragma unroll
-        for (int i = 0; i < kBlockN; ++i) sv[i] = (i < lim) ? sv[i] : -INFINITY;
-      }
       bool full_row = lim >= kBlockN;
-      if constexpr (kWin) {
-        // keys before the window, unless they are sinks
-        const int w_lo = row - p.window + 1 - col0, s_hi = p.sinks - col0;
-        if (w_lo > 0 && s_hi < kBlockN) {
-          full_row = false;
+      if constexpr (!kWin) {
+        if (lim < kBlockN) {
 #pragma unroll
-          for (int i = 0; i < kBlockN; ++i) sv[i] = (i >= w_lo || i < s_hi) ? sv[i] : -INFINITY;
+          for (int i = 0; i < kBlockN; ++i) sv[i] = (i < lim) ? sv[i] : -INFINITY;
+        }
+      } else {
+        // ... and keys before the window, unless they are sinks.  With a short window most blocks have
+        // some masked column, so the row's visible columns are a bit mask (one test per entry whatever
+        // hides it), and only the 32-column chunks that are cut for a row of the warp are tested.
+        const int w_lo = row - p.window + 1 - col0, s_hi = p.sinks - col0;
+        full_row &= w_lo <= 0 || s_hi >= kBlockN;
+        if (__any_sync(0xffffffffu, !full_row)) {
+#pragma unroll
+          for (int c0 = 0; c0 < kBlockN / 32; ++c0) {
+            const uint32_t vis =
+                low_bits(lim - 32 * c0) & (~low_bits(w_lo - 32 * c0) | low_bits(s_hi - 32 * c0));
+            if (__any_sync(0xffffffffu, vis != 0xFFFFFFFFu)) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) sv[32 * c0 + i] = (vis & (1u << i)) ? sv[32 * c0 + i] : -INFINITY;
+            }
+          }
         }
       }
       // block max and each 32-column chunk's maximum: from the loads' reductions when no row

@@ -104,6 +104,10 @@ struct ChunkWork {
   }
 };
 
+__device__ __forceinline__ void sts128(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
 // How the launch's tiles (pair of tiles, kv head) are dealt: the first `whole` to one CTA each, every
 // other one to `splits` CTAs that take a share of its keys.
 struct ChunkGrid {
@@ -241,10 +245,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, kFp8>::kThreads, 1)
     constexpr int kPer = D / 16, kRowStep = 128 / kPer;
     const int r0 = (threadIdx.x - 32 * C::kConvertWarp) / kPer, x = threadIdx.x % kPer;
     // a row's 16 codes become two 16-byte chunks of a 64-column block, swizzled; the second block's
-    // threads store theirs in the other order, so that a row's threads meet different banks
+    // threads take theirs in the other order, so that a row's threads meet different banks
     const int flip = x / 4;
-    const uint32_t dst0 = (uint32_t)((x / 4) * C::kAtomBlock + r0 * 128 + ((((x % 4) * 2 + flip) ^ (r0 & 7)) << 4));
-    const uint32_t dst1 = (uint32_t)((x / 4) * C::kAtomBlock + r0 * 128 + ((((x % 4) * 2 + 1 - flip) ^ (r0 & 7)) << 4));
+    const uint32_t c0 = (uint32_t)((x / 4) * C::kAtomBlock + r0 * 128 + ((((x % 4) * 2 + flip) ^ (r0 & 7)) << 4));
+    const uint32_t c1 = (uint32_t)((x / 4) * C::kAtomBlock + r0 * 128 + ((((x % 4) * 2 + 1 - flip) ^ (r0 & 7)) << 4));
     static_assert(kRowStep % 8 == 0, "a thread's rows share one swizzle phase");
     bool ok = true;
     int n = 0;   // tiles converted
@@ -255,7 +259,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kFp8>::kThreads, 1)
         if (j < 0 || j >= nbmax) continue;
         const int s = j % kStages, key0 = wk.w.at(js + j);
         const bool gaps = unseen(key0);
-        uint8_t* tile = smem + (kv ? C::kVOff : C::kKOff) + s * C::kTileBytes;
+        const uint32_t tile = smem_u32(smem) + (kv ? C::kVOff : C::kKOff) + s * C::kTileBytes;
         const int slot = n % C::kSlots;
         if (!(ok = mbar_wait(&sh.code_full[slot], (n / C::kSlots) & 1, abort_flag, p.c.status))) break;
         uint4 codes[kPer];
@@ -280,7 +284,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, kFp8>::kThreads, 1)
         if (!(ok = mbar_wait(kv ? &sh.v_empty[s] : &sh.k_empty[s], ((j / kStages) & 1) ^ 1, abort_flag, p.c.status))) break;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-          const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+          const uint32_t w[4] = {flip ? codes[i].z : codes[i].x, flip ? codes[i].w : codes[i].y,
+                                 flip ? codes[i].x : codes[i].z, flip ? codes[i].y : codes[i].w};
           uint4 o[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
@@ -294,8 +299,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, kFp8>::kThreads, 1)
             }
             o[e] = make_uint4(y[0], y[1], y[2], y[3]);
           }
-          *reinterpret_cast<uint4*>(tile + dst0 + i * kRowStep * 128) = flip ? o[1] : o[0];
-          *reinterpret_cast<uint4*>(tile + dst1 + i * kRowStep * 128) = flip ? o[0] : o[1];
+          sts128(tile + c0 + i * kRowStep * 128, o[0]);
+          sts128(tile + c1 + i * kRowStep * 128, o[1]);
         }
         fence_proxy_async_smem();
         mbar_arrive(kv ? &sh.v_full[s] : &sh.k_full[s]);

@@ -431,6 +431,11 @@ __device__ __forceinline__ float eq_one(float a, float b) {
   return m;
 }
 
+// The low n bits (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n <= 0 ? 0u : 0xFFFFFFFFu >> (32 - min(n, 32));
+}
+
 // Three-input maximum (sm_100+).
 __device__ __forceinline__ float max3f(float a, float b, float c) {
   float d;
