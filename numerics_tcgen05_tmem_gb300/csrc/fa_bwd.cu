@@ -210,8 +210,7 @@ __global__ void __launch_bounds__(256) fa_bwd_delta_few(const __nv_bfloat16* __r
   const int seen = bh < BH ? i + 1 - lo + n_sink : 0;
   const int most = (int)__reduce_max_sync(0xffffffffu, (unsigned)seen);
   const long long row = bh * N + i;
-  auto widen = [](const __nv_bfloat16* src, float (&x)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4*>(src);
+  auto widen = [](const uint4& u, float (&x)[8]) {
     const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -220,31 +219,43 @@ __global__ void __launch_bounds__(256) fa_bwd_delta_few(const __nv_bfloat16* __r
       x[2 * e + 1] = f.y;
     }
   };
+  auto load = [&](const __nv_bfloat16* t, long long r) { return __ldg(reinterpret_cast<const uint4*>(t + r * D + c)); };
   float qv[8] = {}, gv[8] = {}, sum = 0.f, lse2 = 0.f;
   if (seen > 0) {
-    widen(q + row * D + c, qv);
-    widen(dO + row * D + c, gv);
+    widen(load(q, row), qv);
+    widen(load(dO, row), gv);
     lse2 = lse[row] * 1.4426950408889634f;
   }
-  for (int j = 0; j < most; ++j) {
-    float s = 0.f, dp = 0.f;
-    if (j < seen) {
-      const long long key = bh * N + (j < n_sink ? j : lo + j - n_sink);
-      float kx[8], vx[8];
-      widen(k + key * D + c, kx);
-      widen(v + key * D + c, vx);
+  constexpr int kBatch = 4;   // keys whose loads are in flight together
+  for (int j0 = 0; j0 < most; j0 += kBatch) {
+    uint4 ku[kBatch], vu[kBatch];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        s = fmaf(qv[e], kx[e], s);
-        dp = fmaf(gv[e], vx[e], dp);
+    for (int e = 0; e < kBatch; ++e) {
+      const int j = j0 + e;
+      ku[e] = vu[e] = make_uint4(0, 0, 0, 0);
+      if (j < seen) {
+        const long long key = bh * N + (j < n_sink ? j : lo + j - n_sink);
+        ku[e] = load(k, key);
+        vu[e] = load(v, key);
       }
     }
 #pragma unroll
-    for (int off = kLanesPerRow / 2; off > 0; off /= 2) {
-      s += __shfl_xor_sync(0xffffffffu, s, off);
-      dp += __shfl_xor_sync(0xffffffffu, dp, off);
+    for (int e = 0; e < kBatch; ++e) {
+      float kx[8], vx[8], s = 0.f, dp = 0.f;
+      widen(ku[e], kx);
+      widen(vu[e], vx);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        s = fmaf(qv[x], kx[x], s);
+        dp = fmaf(gv[x], vx[x], dp);
+      }
+#pragma unroll
+      for (int off = kLanesPerRow / 2; off > 0; off /= 2) {
+        s += __shfl_xor_sync(0xffffffffu, s, off);
+        dp += __shfl_xor_sync(0xffffffffu, dp, off);
+      }
+      if (j0 + e < seen) sum = fmaf(ex2_approx(fmaf(s, scale_log2, -lse2)), dp, sum);
     }
-    if (j < seen) sum = fmaf(ex2_approx(fmaf(s, scale_log2, -lse2)), dp, sum);
   }
   if (seen > 0 && c == 0) {
     delta[bh * N_pad + i] = sum;

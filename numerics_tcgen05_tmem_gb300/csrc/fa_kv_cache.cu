@@ -2,39 +2,46 @@
 // as packed BF16 rows (fa_kv_read).
 //
 // Both move each vector (one head's key or value of one token, d elements) once: bandwidth work.
-// A warp takes one token and walks its 2 Hkv vectors, several at a time with 16 bytes per lane of
-// the BF16 side, so all of a token's loads are in flight together while its page is looked up.
+// A CTA takes up to 16 tokens: one warp looks all of them up (sequence, page, slot: four loads that
+// wait for one another), a lane each, then each warp walks the 2 Hkv vectors of its tokens, several at
+// a time with all their loads in flight.  (27k tokens of 8 heads, d = 128, into E4M3: 33 us, 73 % of the
+// measured copy rate; into BF16 34 us, 91 %.  50k tokens back from E4M3: 56 us, 87 %, from BF16 67 us,
+// 97 %.  8 or 32 tokens for each CTA: 34-35 us for the first; 4 vectors in flight: 37 us.)
 // E4M3 caches: scale = least power of two with max|x| <= 448 scale, code = E4M3(x / scale) (the
 // division is exact, one rounding to nearest even), value = code * scale (exact in BF16, whose 8
 // significant bits hold the code's 4; only with scales under 2^-124 do the smallest codes fall
 // between BF16's subnormals and are rounded).  A vector that holds a NaN or an Inf gets a NaN scale and
 // reads back as NaN.
+#include <type_traits>
+
 #include "paged.cuh"
 
 namespace fa {
 namespace paged {
 
 constexpr int kThreads = 256;
+constexpr int kTokens = 16;   // most tokens per CTA
 
-// Reduces a bit-pattern maximum over the `kLanes` lanes that hold one vector.
-template <int kLanes>
-__device__ __forceinline__ uint32_t lanes_max(uint32_t m) {
-#pragma unroll
-  for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+// Largest magnitude of a vector whose 8-element parts (BF16) are with kLanes neighbouring lanes, as
+// FP32 bits: magnitudes order like unsigned integers (Inf and NaN above the rest), two per operation.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t m;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
   return m;
 }
-
-__device__ __forceinline__ uint32_t amax8(const uint4& u) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-  uint32_t m = 0;
+template <int kLanes>
+__device__ __forceinline__ uint32_t vector_amax(const uint4& u) {
+  uint32_t m = max_u16x2(max_u16x2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu), max_u16x2(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu));
 #pragma unroll
-  for (int i = 0; i < 4; ++i) m = max(m, max((w[i] & 0x7FFFu) << 16, w[i] & 0x7FFF0000u));
-  return m;
+  for (int o = kLanes / 2; o > 0; o >>= 1) m = max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return max(m << 16, m & 0xFFFF0000u);
 }
 
 __device__ __forceinline__ uint32_t quant4(uint32_t w0, uint32_t w1, float inv) {
-  return pack_e4m3x4(__uint_as_float(w0 << 16) * inv, __uint_as_float(w0 & 0xFFFF0000u) * inv,
-                     __uint_as_float(w1 << 16) * inv, __uint_as_float(w1 & 0xFFFF0000u) * inv);
+  float a, b, c, d;
+  mul2(a, b, __uint_as_float(w0 << 16), __uint_as_float(w0 & 0xFFFF0000u), inv, inv);
+  mul2(c, d, __uint_as_float(w1 << 16), __uint_as_float(w1 & 0xFFFF0000u), inv, inv);
+  return pack_e4m3x4(a, b, c, d);
 }
 
 // Magnitudes above 1.875 * 2^127 to that value: with the largest scale their code would be
@@ -49,128 +56,157 @@ __device__ __forceinline__ uint4 clamp_top(const uint4& u) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// k_new, v_new: [T, Hkv, d] with `stride` elements between tokens.
+// Where a CTA's tokens lie in the cache: page (negative: skip the token) and slot.
+struct Places {
+  int page[kTokens], slot[kTokens];
+};
+
+// k_new, v_new: [T, Hkv, d] with `stride` elements between tokens; `tokens` of them per CTA.
 template <int D, bool kFp8>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const Cache c, const __nv_bfloat16* __restrict__ k_new,
                                                              const __nv_bfloat16* __restrict__ v_new,
                                                              long long stride, const int32_t* __restrict__ q_indptr,
-                                                             int T) {
+                                                             int T, int tokens) {
   constexpr int kLanes = D / 8;           // lanes per vector
   constexpr int kVecs = 32 / kLanes;      // vectors per warp and step
   constexpr int kUnroll = 8;              // steps in flight
-  const int lane = threadIdx.x % 32;
-  const int token = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
-  if (token >= T) return;
-  const int b = find_sequence(q_indptr, c.B, token);
-  if (b >= c.B) return;
-  const int pos = __ldg(c.kv_len + b) - __ldg(q_indptr + b + 1) + token;
-  const int page = find_page(c, b, pos, kSitePagedAppend);
-  if (page < 0) return;
-  const int page_size = 1 << c.page_shift, slot = pos & (page_size - 1);
+  __shared__ Places at;
+  const int lane = threadIdx.x % 32, first = blockIdx.x * tokens;
+  const int page_size = 1 << c.page_shift;
+  if ((int)threadIdx.x < tokens) {
+    const int token = first + threadIdx.x;
+    int page = -1, pos = 0;
+    const int b = token < T ? find_sequence(q_indptr, c.B, token) : -1;
+    if (b >= 0) {
+      pos = __ldg(c.kv_len + b) - __ldg(q_indptr + b + 1) + token;
+      page = find_page(c, b, pos, kSitePagedAppend);
+    }
+    at.page[threadIdx.x] = page;
+    at.slot[threadIdx.x] = pos & (page_size - 1);
+  }
+  __syncthreads();
   const int sub = lane / kLanes, col = (lane % kLanes) * 8;
   const int n = 2 * c.Hkv;  // vector i: head i / 2, K where i is even
-  for (int i0 = 0; i0 < n; i0 += kVecs * kUnroll) {
-    uint4 x[kUnroll];
+  for (int t = threadIdx.x / 32; t < tokens; t += kThreads / 32) {
+    const int page = at.page[t], slot = at.slot[t], token = first + t;
+    if (page < 0) continue;
+    for (int i0 = 0; i0 < n; i0 += kVecs * kUnroll) {
+      uint4 x[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int i = i0 + u * kVecs + sub;
-      x[u] = make_uint4(0, 0, 0, 0);
-      if (i < n)
-        x[u] = __ldg(reinterpret_cast<const uint4*>(((i & 1) ? v_new : k_new) + token * stride + (i >> 1) * D + col));
-    }
+      for (int u = 0; u < kUnroll; ++u) {
+        const int i = i0 + u * kVecs + sub;
+        x[u] = make_uint4(0, 0, 0, 0);
+        if (i < n)
+          x[u] = __ldg(reinterpret_cast<const uint4*>(((i & 1) ? v_new : k_new) + token * stride + (i >> 1) * D + col));
+      }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int i = i0 + u * kVecs + sub;
-      if (i0 + u * kVecs >= n) break;  // the same for the whole warp
-      const int h = i >> 1;
-      const long long row = (long long)h * page_size + slot;
-      if constexpr (!kFp8) {
-        __nv_bfloat16* base = static_cast<__nv_bfloat16*>((i & 1) ? c.v : c.k);
-        if (i < n) *reinterpret_cast<uint4*>(base + page * c.page_stride + row * D + col) = x[u];
-      } else {
-        const uint32_t amax = lanes_max<kLanes>(amax8(x[u]));
-        float scale = 1.f, inv = 1.f;
-        int e = 0;
-        if (amax != 0) {
-          e = scale_exponent(amax);
-          scale = __uint_as_float((uint32_t)(e + 127) << 23);
-          inv = __uint_as_float((uint32_t)(127 - e) << 23);
-        }
-        if (e == kMaxScaleExp) x[u] = clamp_top(x[u]);
-        uint2 q = make_uint2(quant4(x[u].x, x[u].y, inv), quant4(x[u].z, x[u].w, inv));
-        if (amax >= 0x7F800000u) {  // Inf or NaN in the vector
-          scale = __uint_as_float(0x7FC00000u);
-          q = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-        }
-        if (i < n) {
-          uint8_t* base = static_cast<uint8_t*>((i & 1) ? c.v : c.k);
-          *reinterpret_cast<uint2*>(base + page * c.page_stride + row * D + col) = q;
-          if (col == 0) ((i & 1) ? c.v_scale : c.k_scale)[page * c.scale_stride + row] = scale;
+      for (int u = 0; u < kUnroll; ++u) {
+        const int i = i0 + u * kVecs + sub;
+        if (i0 + u * kVecs >= n) break;  // the same for the whole warp
+        const long long row = (long long)(i >> 1) * page_size + slot;
+        if constexpr (!kFp8) {
+          __nv_bfloat16* base = static_cast<__nv_bfloat16*>((i & 1) ? c.v : c.k);
+          if (i < n) *reinterpret_cast<uint4*>(base + page * c.page_stride + row * D + col) = x[u];
+        } else {
+          const uint32_t amax = vector_amax<kLanes>(x[u]);
+          float scale = 1.f, inv = 1.f;
+          int e = 0;
+          if (amax != 0) {
+            e = scale_exponent(amax);
+            scale = __uint_as_float((uint32_t)(e + 127) << 23);
+            inv = __uint_as_float((uint32_t)(127 - e) << 23);
+          }
+          if (e == kMaxScaleExp) x[u] = clamp_top(x[u]);
+          uint2 q = make_uint2(quant4(x[u].x, x[u].y, inv), quant4(x[u].z, x[u].w, inv));
+          if (amax >= 0x7F800000u) {  // Inf or NaN in the vector
+            scale = __uint_as_float(0x7FC00000u);
+            q = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+          }
+          if (i < n) {
+            uint8_t* base = static_cast<uint8_t*>((i & 1) ? c.v : c.k);
+            *reinterpret_cast<uint2*>(base + page * c.page_stride + row * D + col) = q;
+            if (col == 0) ((i & 1) ? c.v_scale : c.k_scale)[page * c.scale_stride + row] = scale;
+          }
         }
       }
     }
   }
 }
 
-// k_out, v_out: [rows, Hkv, d] contiguous.
+// k_out, v_out: [rows, Hkv, d] contiguous; `tokens` rows per CTA.
 template <int D, bool kFp8>
 __global__ void __launch_bounds__(kThreads) kv_read_kernel(const Cache c, const int32_t* __restrict__ kv_indptr,
                                                            __nv_bfloat16* __restrict__ k_out,
-                                                           __nv_bfloat16* __restrict__ v_out, int rows) {
-  constexpr int kElems = kFp8 ? 16 : 8;   // elements per lane: 16 bytes of the cache
+                                                           __nv_bfloat16* __restrict__ v_out, int rows, int tokens) {
+  // 8 elements per lane: a warp's stores then cover whole lines (with 16 codes per lane each 16-byte
+  // store left half of its sector to the next one)
+  constexpr int kElems = 8;
   constexpr int kLanes = D / kElems;
   constexpr int kVecs = 32 / kLanes;
-  constexpr int kUnroll = kFp8 ? 4 : 8;
-  const int lane = threadIdx.x % 32;
-  const int r = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
-  if (r >= rows) return;
-  const int b = find_sequence(kv_indptr, c.B, r);
-  if (b >= c.B) return;
-  const int pos = r - __ldg(kv_indptr + b);
-  if (pos >= __ldg(c.kv_len + b)) return;  // past the sequence: the row stays as it was
-  const int page = find_page(c, b, pos, kSitePagedRead);
-  if (page < 0) return;
-  const int page_size = 1 << c.page_shift, slot = pos & (page_size - 1);
+  constexpr int kUnroll = 8;
+  __shared__ Places at;
+  const int lane = threadIdx.x % 32, first = blockIdx.x * tokens;
+  const int page_size = 1 << c.page_shift;
+  if ((int)threadIdx.x < tokens) {
+    const int r = first + threadIdx.x;
+    int page = -1, pos = 0;
+    const int b = r < rows ? find_sequence(kv_indptr, c.B, r) : -1;
+    if (b >= 0) {
+      pos = r - __ldg(kv_indptr + b);
+      // past the sequence the row stays as it was
+      if (pos < __ldg(c.kv_len + b)) page = find_page(c, b, pos, kSitePagedRead);
+    }
+    at.page[threadIdx.x] = page;
+    at.slot[threadIdx.x] = pos & (page_size - 1);
+  }
+  __syncthreads();
   const int sub = lane / kLanes, col = (lane % kLanes) * kElems;
   const int n = 2 * c.Hkv;
   constexpr int kBytes = kFp8 ? 1 : 2;
-  for (int i0 = 0; i0 < n; i0 += kVecs * kUnroll) {
-    uint4 x[kUnroll];
-    float sc[kUnroll];
+  using Part = std::conditional_t<kFp8, uint2, uint4>;   // a lane's elements in the cache
+  for (int t = threadIdx.x / 32; t < tokens; t += kThreads / 32) {
+    const int page = at.page[t], slot = at.slot[t], r = first + t;
+    if (page < 0) continue;
+    for (int i0 = 0; i0 < n; i0 += kVecs * kUnroll) {
+      Part x[kUnroll];
+      float sc[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int i = i0 + u * kVecs + sub;
-      x[u] = make_uint4(0, 0, 0, 0);
-      sc[u] = 0.f;
-      if (i < n) {
-        const long long row = (long long)(i >> 1) * page_size + slot;
-        const uint8_t* base = static_cast<const uint8_t*>((i & 1) ? c.v : c.k);
-        x[u] = __ldg(reinterpret_cast<const uint4*>(base + (page * c.page_stride + row * D + col) * kBytes));
-        if constexpr (kFp8) sc[u] = __ldg(((i & 1) ? c.v_scale : c.k_scale) + page * c.scale_stride + row);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int i = i0 + u * kVecs + sub;
-      if (i >= n) break;
-      uint4* dst = reinterpret_cast<uint4*>(((i & 1) ? v_out : k_out) + ((long long)r * c.Hkv + (i >> 1)) * D + col);
-      if constexpr (!kFp8) {
-        dst[0] = x[u];
-      } else {
-        const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-        uint32_t o[8];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const float2 lo = e4m3x2_to_float2(w[t]), hi = e4m3x2_to_float2(w[t] >> 16);
-          o[2 * t] = pack_bf16x2(lo.x * sc[u], lo.y * sc[u]);
-          o[2 * t + 1] = pack_bf16x2(hi.x * sc[u], hi.y * sc[u]);
+      for (int u = 0; u < kUnroll; ++u) {
+        const int i = i0 + u * kVecs + sub;
+        x[u] = Part{};
+        sc[u] = 0.f;
+        if (i < n) {
+          const long long row = (long long)(i >> 1) * page_size + slot;
+          const uint8_t* base = static_cast<const uint8_t*>((i & 1) ? c.v : c.k);
+          x[u] = __ldg(reinterpret_cast<const Part*>(base + (page * c.page_stride + row * D + col) * kBytes));
+          if constexpr (kFp8) sc[u] = __ldg(((i & 1) ? c.v_scale : c.k_scale) + page * c.scale_stride + row);
         }
-        dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int i = i0 + u * kVecs + sub;
+        if (i >= n) break;
+        uint4* dst = reinterpret_cast<uint4*>(((i & 1) ? v_out : k_out) + ((long long)r * c.Hkv + (i >> 1)) * D + col);
+        if constexpr (!kFp8) {
+          *dst = x[u];
+        } else {
+          uint32_t o[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = e4m3x2_to_float2((e < 2 ? x[u].x : x[u].y) >> (16 * (e & 1)));
+            float lo, hi;
+            mul2(lo, hi, f.x, f.y, sc[u], sc[u]);
+            o[e] = pack_bf16x2(lo, hi);
+          }
+          *dst = make_uint4(o[0], o[1], o[2], o[3]);
+        }
       }
     }
   }
 }
+
+// Tokens per CTA: 16, or 8 (one for each warp) where that leaves SMs without a CTA.
+static int tokens_per_cta(int rows) { return rows > sm_count() * kTokens ? kTokens : kThreads / 32; }
 
 int check_cache(const fa_paged_kv* kv, Cache* c) {
   if (!kv) return set_error(FA_ERR_INVALID_ARG, "kv is NULL");
@@ -241,13 +277,14 @@ extern "C" int fa_kv_append(const fa_paged_kv* kv, const void* k_new, const void
   if (T == 0) return FA_OK;
   c.status = device_status_word();
   if (!c.status) return set_error(FA_ERR_CUDA, "could not allocate the device status record");
-  const unsigned grid = (unsigned)((T + paged::kThreads / 32 - 1) / (paged::kThreads / 32));
+  const int tokens = paged::tokens_per_cta(T);
+  const unsigned grid = (unsigned)(((long long)T + tokens - 1) / tokens);
   const __nv_bfloat16 *k = static_cast<const __nv_bfloat16*>(k_new), *v = static_cast<const __nv_bfloat16*>(v_new);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool fp8 = kv->dtype == FA_KV_E4M3;
   auto kern = kv->d == 64 ? (fp8 ? paged::kv_append_kernel<64, true> : paged::kv_append_kernel<64, false>)
                           : (fp8 ? paged::kv_append_kernel<128, true> : paged::kv_append_kernel<128, false>);
-  kern<<<grid, paged::kThreads, 0, s>>>(c, k, v, new_stride, q_indptr, T);
+  kern<<<grid, paged::kThreads, 0, s>>>(c, k, v, new_stride, q_indptr, T, tokens);
   return check_cuda(cudaGetLastError(), "launch fa_kv_append");
 }
 
@@ -266,12 +303,13 @@ extern "C" int fa_kv_read(const fa_paged_kv* kv, const int32_t* kv_indptr, void*
   if (rows == 0) return FA_OK;
   c.status = device_status_word();
   if (!c.status) return set_error(FA_ERR_CUDA, "could not allocate the device status record");
-  const unsigned grid = (unsigned)((rows + paged::kThreads / 32 - 1) / (paged::kThreads / 32));
+  const int tokens = paged::tokens_per_cta(rows);
+  const unsigned grid = (unsigned)(((long long)rows + tokens - 1) / tokens);
   __nv_bfloat16 *k = static_cast<__nv_bfloat16*>(k_out), *v = static_cast<__nv_bfloat16*>(v_out);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool fp8 = kv->dtype == FA_KV_E4M3;
   auto kern = kv->d == 64 ? (fp8 ? paged::kv_read_kernel<64, true> : paged::kv_read_kernel<64, false>)
                           : (fp8 ? paged::kv_read_kernel<128, true> : paged::kv_read_kernel<128, false>);
-  kern<<<grid, paged::kThreads, 0, s>>>(c, kv_indptr, k, v, rows);
+  kern<<<grid, paged::kThreads, 0, s>>>(c, kv_indptr, k, v, rows, tokens);
   return check_cuda(cudaGetLastError(), "launch fa_kv_read");
 }

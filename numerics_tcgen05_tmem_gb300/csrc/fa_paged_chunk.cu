@@ -151,6 +151,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, kFp8>::kThreads, 1)
     fa_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const Attn p, const ChunkGrid g) {
   using C = ChunkCfg<D, kFp8>;
+  // a few-rows launch of the same call, which touches none of this one's rows, may run beside it
+  cudaTriggerProgrammaticLaunchCompletion();
   extern __shared__ __align__(1024) uint8_t smem[];
   // the swizzled tiles need a 1024-byte aligned base (there is no slack for E4M3, d = 128)
   if (smem_u32(smem) & 1023u) {
@@ -826,7 +828,13 @@ static int launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMa
   if (grid >= (1ll << 31)) return set_error(FA_ERR_INVALID_ARG, "too many tiles for one launch");
   const ChunkGrid g{whole, splits};
   kern<<<(unsigned)grid, C::kThreads, chunk_smem<D, kFp8>(), s>>>(tq, tk, tv, p, g);
-  if ((rc = check_cuda(cudaGetLastError(), "launch fa_chunk_kernel")) || splits == 1) return rc;
+  return check_cuda(cudaGetLastError(), "launch fa_chunk_kernel");
+}
+
+template <int D>
+static int join(const Attn& p, int whole, int splits, cudaStream_t s) {
+  const long long tiles = chunk_pairs(p.T, p.c.B, p.group) * p.c.Hkv;
+  const ChunkGrid g{whole, splits};
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((tiles - whole) * (2 * kM / kJoinRows)));
   cfg.blockDim = dim3(256);
@@ -850,6 +858,10 @@ int launch_chunk(const Attn& p, int d, bool fp8, int whole, int splits, cudaStre
     return rc;
   if (d == 64) return fp8 ? launch<64, true>(tq, tk, tv, p, whole, splits, s) : launch<64, false>(tq, tk, tv, p, whole, splits, s);
   return fp8 ? launch<128, true>(tq, tk, tv, p, whole, splits, s) : launch<128, false>(tq, tk, tv, p, whole, splits, s);
+}
+
+int launch_chunk_combine(const Attn& p, int d, int whole, int splits, cudaStream_t s) {
+  return d == 64 ? join<64>(p, whole, splits, s) : join<128>(p, whole, splits, s);
 }
 
 }  // namespace paged
@@ -997,17 +1009,16 @@ extern "C" int fa_fwd_paged(const fa_paged_kv* kv, const void* q, int64_t q_stri
   const bool fp8 = kv->dtype == FA_KV_E4M3;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   char* ws = static_cast<char*>(workspace);
-  if (pl.splits) {
-    paged::Attn c = p;
-    c.part_o = reinterpret_cast<float*>(ws + chunk.o);
-    c.part_lse = reinterpret_cast<float*>(ws + chunk.lse);
-    if ((rc = paged::launch_chunk(c, kv->d, fp8, pl.whole, pl.splits, s))) return rc;
-  }
-  if (pl.few_rows) {
-    p.part_o = reinterpret_cast<float*>(ws + few.o);
-    p.part_lse = reinterpret_cast<float*>(ws + few.lse);
-    p.part_info = reinterpret_cast<int4*>(ws + few.info);
-    if ((rc = paged::launch_rows(p, kv->d, fp8, s))) return rc;
-  }
-  return FA_OK;
+  // Chunks first; the few-rows kernel of a mixed batch then starts beside them, on SMs that they leave
+  // free; the joining kernels come last.
+  paged::Attn c = p;
+  c.part_o = reinterpret_cast<float*>(ws + chunk.o);
+  c.part_lse = reinterpret_cast<float*>(ws + chunk.lse);
+  p.part_o = reinterpret_cast<float*>(ws + few.o);
+  p.part_lse = reinterpret_cast<float*>(ws + few.lse);
+  p.part_info = reinterpret_cast<int4*>(ws + few.info);
+  if (pl.splits && (rc = paged::launch_chunk(c, kv->d, fp8, pl.whole, pl.splits, s))) return rc;
+  if (pl.few_rows && (rc = paged::launch_rows(p, kv->d, fp8, pl.splits > 0, s))) return rc;
+  if (pl.splits > 1 && (rc = paged::launch_chunk_combine(c, kv->d, pl.whole, pl.splits, s))) return rc;
+  return pl.few_rows ? paged::launch_rows_combine(p, kv->d, s) : FA_OK;
 }

@@ -213,11 +213,20 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
     }
   }
   __syncthreads();
-  if (u_first >= u_end || sh.first_b < 0) return;
+  // Launched beside a chunk kernel, this launch must not end before it (what follows in the stream
+  // waits for this launch only): one idle warp waits for it.
+  const bool waits = blockIdx.x == 0 && warp == kRowsThreads / 32 - 1;
+  if (u_first >= u_end || sh.first_b < 0) {
+    if (waits) cudaGridDependencySynchronize();
+    return;
+  }
 
   if (warp >= kRowsWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRowsRegLoad));
-    if (warp != kRowsLoadWarp) return;
+    if (warp != kRowsLoadWarp) {
+      if (waits) cudaGridDependencySynchronize();
+      return;
+    }
     // ------------------------------------------------------------------ loading warp
     if (lane == 0) {
       tma_prefetch_desc(&tmK);
@@ -776,38 +785,48 @@ __global__ void __launch_bounds__(128) fa_rows_combine(const Attn p, int slot_ro
   if (lane == 0 && p.lse) p.lse[row] = lse;
 }
 
-template <int D, bool kFp8, int kRG, int kNR>
-static int launch(const CUtensorMap& tk, const CUtensorMap& tv, const Attn& p, int grid, cudaStream_t s) {
-  using C = RowsCfg<D, kFp8>;
-  constexpr int kRows = 8 * kNR * kRG;
-  auto kern = fa_rows_kernel<D, kFp8, kRG, kNR>;
-  static std::atomic<uint64_t> prepared{0};
-  int rc = prepare_kernel(reinterpret_cast<const void*>(kern), C::kSmemBytes, kRowsThreads, 128 * (kRowsRegCompute + kRowsRegLoad), "few-rows kernel",
-                          &prepared);
-  if (rc) return rc;
-  kern<<<grid, kRowsThreads, C::kSmemBytes, s>>>(tk, tv, p);
-  if ((rc = check_cuda(cudaGetLastError(), "launch fa_rows_kernel"))) return rc;
+// A launch that may start before the one before it in the stream has ended.
+template <typename... Args, typename... Given>
+static cudaError_t launch_early(void (*kern)(Args...), unsigned grid, unsigned threads, size_t smem, cudaStream_t s,
+                                const Given&... args) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(p.c.B * p.c.Hkv * (kRows / 4)));
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute early;
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
-  return check_cuda(cudaLaunchKernelEx(&cfg, fa_rows_combine<D>, p, kRows), "launch fa_rows_combine");
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <int D, bool kFp8, int kRG, int kNR>
+static int launch(const CUtensorMap& tk, const CUtensorMap& tv, const Attn& p, int grid, bool beside, cudaStream_t s) {
+  using C = RowsCfg<D, kFp8>;
+  auto kern = fa_rows_kernel<D, kFp8, kRG, kNR>;
+  static std::atomic<uint64_t> prepared{0};
+  int rc = prepare_kernel(reinterpret_cast<const void*>(kern), C::kSmemBytes, kRowsThreads,
+                          128 * (kRowsRegCompute + kRowsRegLoad), "few-rows kernel", &prepared);
+  if (rc) return rc;
+  if (beside)
+    return check_cuda(launch_early(kern, grid, kRowsThreads, C::kSmemBytes, s, tk, tv, p), "launch fa_rows_kernel");
+  kern<<<grid, kRowsThreads, C::kSmemBytes, s>>>(tk, tv, p);
+  return check_cuda(cudaGetLastError(), "launch fa_rows_kernel");
 }
 
 template <int D, bool kFp8>
-static int launch_tiles(const CUtensorMap& tk, const CUtensorMap& tv, const Attn& p, int grid, cudaStream_t s) {
-  if (p.few_rows == 8) return launch<D, kFp8, 1, 1>(tk, tv, p, grid, s);
-  if (p.few_rows == 16) return launch<D, kFp8, 1, 2>(tk, tv, p, grid, s);
-  if (p.few_rows == 32) return launch<D, kFp8, 2, 2>(tk, tv, p, grid, s);
-  return launch<D, kFp8, 4, 2>(tk, tv, p, grid, s);
+static int launch_groups(const CUtensorMap& tk, const CUtensorMap& tv, const Attn& p, int grid, bool beside,
+                         cudaStream_t s) {
+  if (p.few_rows == 8) return launch<D, kFp8, 1, 1>(tk, tv, p, grid, beside, s);
+  if (p.few_rows == 16) return launch<D, kFp8, 1, 2>(tk, tv, p, grid, beside, s);
+  if (p.few_rows == 32) return launch<D, kFp8, 2, 2>(tk, tv, p, grid, beside, s);
+  return launch<D, kFp8, 4, 2>(tk, tv, p, grid, beside, s);
 }
 
-int launch_rows(const Attn& p, int d, bool fp8, cudaStream_t s) {
+// beside: after a chunk kernel of the same call, without waiting for it.
+int launch_rows(const Attn& p, int d, bool fp8, bool beside, cudaStream_t s) {
   const int page_size = 1 << p.c.page_shift, box = page_size < kRowsBlk ? page_size : kRowsBlk;
   CUtensorMap tk, tv;
   int rc;
@@ -817,8 +836,14 @@ int launch_rows(const Attn& p, int d, bool fp8, cudaStream_t s) {
   int grid = 2 * sm_count();
   if (grid > kRowsMaxCtas) grid = kRowsMaxCtas;
   if (d == 64)
-    return fp8 ? launch_tiles<64, true>(tk, tv, p, grid, s) : launch_tiles<64, false>(tk, tv, p, grid, s);
-  return fp8 ? launch_tiles<128, true>(tk, tv, p, grid, s) : launch_tiles<128, false>(tk, tv, p, grid, s);
+    return fp8 ? launch_groups<64, true>(tk, tv, p, grid, beside, s) : launch_groups<64, false>(tk, tv, p, grid, beside, s);
+  return fp8 ? launch_groups<128, true>(tk, tv, p, grid, beside, s) : launch_groups<128, false>(tk, tv, p, grid, beside, s);
+}
+
+int launch_rows_combine(const Attn& p, int d, cudaStream_t s) {
+  const unsigned grid = (unsigned)(p.c.B * p.c.Hkv * (p.few_rows / 4));
+  return check_cuda(launch_early(d == 64 ? fa_rows_combine<64> : fa_rows_combine<128>, grid, 128, 0, s, p, p.few_rows),
+                    "launch fa_rows_combine");
 }
 
 }  // namespace paged

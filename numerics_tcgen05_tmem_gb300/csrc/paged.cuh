@@ -54,15 +54,18 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t codes) {
   return make_float2(lo, hi);
 }
 
-// The sequence of packed row `row`: the b with offsets[b] <= row < offsets[b + 1]; B when there is
-// none (a row behind the last sequence).  The whole warp calls it; its lanes read the B offsets
-// side by side, so the loads do not wait for one another.
+// The sequence of packed row `row`: the b with offsets[b] <= row < offsets[b + 1]; -1 when there is
+// none (a row behind the last sequence).
 __device__ __forceinline__ int find_sequence(const int32_t* offsets, int B, int row) {
-  const int lane = threadIdx.x % 32;
-  int before = 0;
-  for (int i = lane; i < B; i += 32) before += (__ldg(offsets + i + 1) <= row) ? 1 : 0;
-  const int b = (int)__reduce_add_sync(0xffffffffu, (unsigned)before);
-  return (row < __ldg(offsets)) ? B : b;
+  int lo = 0, hi = B + 1;   // offsets[0 .. lo) <= row < offsets[hi ..)
+  while (lo < hi) {
+    const int mid = (lo + hi) / 2;
+    if (__ldg(offsets + mid) <= row)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  return lo - 1 < B ? lo - 1 : -1;
 }
 
 // The page of position `pos` of sequence b; -1, recorded at `site`, where the table or the

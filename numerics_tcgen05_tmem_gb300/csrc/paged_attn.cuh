@@ -107,8 +107,10 @@ inline long long chunk_pairs(int T, int B, int group) {
   return (T - seqs) / per + seqs;
 }
 
-int launch_rows(const Attn& p, int d, bool fp8, cudaStream_t s);
+int launch_rows(const Attn& p, int d, bool fp8, bool beside, cudaStream_t s);
+int launch_rows_combine(const Attn& p, int d, cudaStream_t s);
 int launch_chunk(const Attn& p, int d, bool fp8, int whole, int splits, cudaStream_t s);
+int launch_chunk_combine(const Attn& p, int d, int whole, int splits, cudaStream_t s);
 
 }  // namespace paged
 }  // namespace fa

@@ -50,6 +50,20 @@ def test_forward_and_gradients(N, window, sinks, d):
         M.assert_within(name, got, want[name], tol[name])
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,H,N,window,sinks", [(4, 8, 1500, 200, 4), (5, 7, 1301, 100, 0), (8, 12, 700, 50, 140),
+                                                (8, 20, 400, 30, 1), (3, 11, 1100, 540, 200)])
+def test_gradients_with_more_items_than_SMs(B, H, N, window, sinks, d):
+    # (key tile, head) items dealt to the SMs: several light ones each, and fewer (none, more) with sinks
+    w = inputs.random_case(B, H, N, d, True, seed=B * H + N, std=1.5)
+    (o, lse), grads = run(w, window, sinks)
+    ref = M.forward(w.q, w.k, w.v, see(N, window, sinks), w.scale)
+    M.assert_within("o", o, ref["o"], ref["o_tol"])
+    want, tol = M.backward(w.q, w.k, w.v, w.do, see(N, window, sinks), w.scale, ref)
+    for name, got in zip(("dq", "dk", "dv"), grads):
+        M.assert_within(name, got, want[name], tol[name])
+
+
 @pytest.mark.parametrize("d,N", [(64, 1000), (64, 2300), (128, 700)])
 @pytest.mark.parametrize("stable", [0, 1, 2])
 def test_a_window_as_long_as_the_row_is_causal_attention(N, d, stable):
