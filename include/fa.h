@@ -374,7 +374,9 @@ int fa_kv_read(const fa_paged_kv* kv, const int32_t* kv_indptr, void* k_out, voi
  *   o        : BF16 [T, Hq, d], contiguous;  lse: FP32 [T, Hq], or NULL (not written)
  *   window   : 0 = none; else the token at position p sees the keys p - window < j <= p and the
  *              first `sinks` keys; without a window every key j <= p
- * A row that sees no key (a length shorter than the new tokens) gives O = 0 and LSE = -inf.
+ * A row that sees no key (a length shorter than the new tokens) gives O = 0 and LSE = -inf, which
+ * the monitor does not count as non-finite.  kv's contents, lengths and table must not change while
+ * the call runs.
  * Pages of which no new token sees a key are not read.  A key that some but not all rows of a tile
  * see must have finite values, as in the dense entry points (0 * Inf = NaN).
  * workspace: device scratch of at least fa_fwd_paged_workspace_size(T, B, max_q, Hq, Hkv, d,

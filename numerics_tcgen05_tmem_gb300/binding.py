@@ -149,6 +149,15 @@ def _stream(stream):
     return torch.cuda.current_stream().cuda_stream
 
 
+def _empty(shape, dtype, like, stream):
+    """A fresh tensor that belongs to the stream the call runs on, so that its memory is not handed out
+    to another stream's work while a kernel of the call still uses it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
 class _OnDevice:
     """Makes a tensor's device current for a call, where it is not already."""
 
@@ -298,8 +307,8 @@ def forward(q, k, v, causal: bool = True, scale=None, stable: int = 1, beta: flo
     _check_window(causal, window, sinks)
     B, H, N, d = q.shape
     scale = 1.0 / math.sqrt(d) if scale is None else scale
-    o = torch.empty_like(q)
-    lse = torch.empty((B, H, N), device=q.device, dtype=torch.float32)
+    o = _empty(q.shape, q.dtype, q, stream)
+    lse = _empty((B, H, N), torch.float32, q, stream)
     sd = _stats_dict(B, H, N, q.device) if stats else None
     with _OnDevice(q):
         if window is None:
@@ -349,9 +358,9 @@ def backward(q, k, v, o, lse, do, causal: bool = True, scale=None, workspace=Non
     B, H, N, d = q.shape
     scale = 1.0 / math.sqrt(d) if scale is None else scale
     if workspace is None:
-        workspace = torch.empty(fa_bwd_workspace_size(B, H, N, d), device=q.device, dtype=torch.uint8)
-    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    delta = torch.empty((B, H, N), device=q.device, dtype=torch.float32) if want_delta else None
+        workspace = _empty(fa_bwd_workspace_size(B, H, N, d), torch.uint8, q, stream)
+    dq, dk, dv = (_empty(q.shape, q.dtype, q, stream) for _ in range(3))
+    delta = _empty((B, H, N), torch.float32, q, stream) if want_delta else None
     with _OnDevice(q):
         if window is None:
             _check(fa_bwd(q, k, v, o, lse, do, dq, dk, dv, delta, causal, scale, workspace, stream))
@@ -361,6 +370,15 @@ def backward(q, k, v, o, lse, do, causal: bool = True, scale=None, workspace=Non
 
 
 # ----------------------------------------------------------------- paged key/value caches
+
+def _outer(n, stride, least, name):
+    """The stride of the outermost dimension (n entries); one entry's may be anything."""
+    if n <= 1:
+        return least
+    if stride < least:
+        raise ValueError(f"{name}: entries must not overlap (stride {stride} is less than {least})")
+    return stride
+
 
 def _int32(t, n, name, dev):
     if t.dtype is not torch.int32 or t.get_device() != dev or t.dim() != 1 or not t.is_contiguous():
@@ -399,11 +417,11 @@ def _paged(k, v, table, kv_len, k_scale, v_scale):
                 raise ValueError("k_scale and v_scale must be float32 [pages, Hkv, page_size], pages contiguous, with "
                                  "the same page stride")
         ks, vs, code = k_scale.data_ptr(), v_scale.data_ptr(), FA_KV_E4M3
-        scale_stride = max(scale_stride, H * S)
+        scale_stride = _outer(P, scale_stride, H * S, "k_scale")
     else:
         raise ValueError("cache tensors must be bfloat16, or uint8 (or float8_e4m3fn) E4M3 codes")
-    return PagedKV(k.data_ptr(), v.data_ptr(), ks, vs, max(stride[0], H * S * d), scale_stride, table.data_ptr(),
-                   max(rows[0], width), kv_ptr, B, H, d, S, P, width, code)
+    return PagedKV(k.data_ptr(), v.data_ptr(), ks, vs, _outer(P, stride[0], H * S * d, "cache"), scale_stride,
+                   table.data_ptr(), _outer(B, rows[0], width, "block_table"), kv_ptr, B, H, d, S, P, width, code)
 
 
 def _check_rows(x, heads, d, dev, name):
@@ -413,7 +431,7 @@ def _check_rows(x, heads, d, dev, name):
         raise ValueError(f"{name} must be a CUDA bfloat16 tensor [rows, {heads}, {d}] on the cache's device")
     if shape[0] and (stride[2] != 1 or (heads > 1 and stride[1] != d)):
         raise ValueError(f"{name}: a row's heads must be contiguous")
-    return shape[0], max(stride[0], heads * d)   # a single row's stride may be anything
+    return shape[0], _outer(shape[0], stride[0], heads * d, name)
 
 
 def kv_append(k_new, v_new, k_cache, v_cache, block_table, kv_len, q_indptr, k_scale=None, v_scale=None, stream=None):
@@ -447,7 +465,8 @@ def kv_read(k_cache, v_cache, block_table, kv_len, kv_indptr, rows, k_scale=None
     dev, shape = k_cache.get_device(), (rows, kv.Hkv, kv.d)
     indptr = _int32(kv_indptr, kv.B + 1, "kv_indptr", dev)
     if out is None:
-        k, v = (torch.empty(shape, device=k_cache.device, dtype=torch.bfloat16) for _ in range(2))
+        k = _empty(shape, torch.bfloat16, k_cache, stream)
+        v = _empty(shape, torch.bfloat16, k_cache, stream)
     else:
         k, v = out
         for t in out:
@@ -485,11 +504,11 @@ def forward_paged(q, k_cache, v_cache, block_table, kv_len, q_indptr, max_q, k_s
     T, stride = _check_rows(q, Hq, d, dev, "q")
     indptr = _int32(q_indptr, kv.B + 1, "q_indptr", dev)
     if out is None:
-        out = torch.empty((T, Hq, d), device=q.device, dtype=torch.bfloat16)
+        out = _empty((T, Hq, d), torch.bfloat16, q, stream)
     elif out.dtype is not torch.bfloat16 or out.shape != q.shape or not out.is_contiguous() or out.get_device() != dev:
         raise ValueError("out must be a contiguous bfloat16 tensor of q's shape")
     if lse is None:
-        lse = torch.empty((T, Hq), device=q.device, dtype=torch.float32)
+        lse = _empty((T, Hq), torch.float32, q, stream)
     elif lse.dtype is not torch.float32 or lse.shape != q.shape[:2] or not lse.is_contiguous() or \
             lse.get_device() != dev:
         raise ValueError("lse must be a contiguous float32 tensor [T, Hq]")
@@ -498,7 +517,7 @@ def forward_paged(q, k_cache, v_cache, block_table, kv_len, q_indptr, max_q, k_s
     lib = load()
     if workspace is None:
         n = lib.fa_fwd_paged_workspace_size(T, kv.B, max_q, Hq, kv.Hkv, d, kv.max_pages * kv.page_size, window)
-        workspace = torch.empty(n, device=q.device, dtype=torch.uint8) if n else None
+        workspace = _empty(n, torch.uint8, q, stream) if n else None
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the cache's device")
     ws, nbytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)

@@ -22,6 +22,8 @@
 // Softmax: running maximum and sum in FP32 per row (one thread per row), P~ rounded to BF16 for the
 // product as the tensor core takes it.  Plain shift: the stabilised rule guards the training
 // backward, and the output does not depend on the shift.
+#include <stdlib.h>
+
 #include "paged_attn.cuh"
 
 namespace fa {
@@ -68,6 +70,7 @@ struct ChunkShared {
   uint64_t code_full[kMaxSlots], code_empty[kMaxSlots];   // E4M3: a slot has landed / has been read
   uint64_t s_full[2], p_half[2], p_full[2], pv_done[2], o_done[2], alpha_ready[2], o_ready[2], l_ready[2];
   uint64_t mma_done;
+  uint64_t never;                  // test builds only: a barrier nothing arrives on
   float alpha[2][kM];
   uint32_t tmem_base, abort_flag;
   int b, tile;                     // this CTA's sequence and pair of tiles; b = -1: none
@@ -203,6 +206,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kFp8>::kThreads, 1)
       mbar_init(&sh.l_ready[t], kM);
     }
     mbar_init(&sh.mma_done, 1);
+    mbar_init(&sh.never, 1);
     fence_barrier_init();
   }
   __syncthreads();
@@ -428,6 +432,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, kFp8>::kThreads, 1)
         const uint32_t sQ = smem_u32(smem + C::kQOff), sK = smem_u32(smem + C::kKOff), sV = smem_u32(smem + C::kVOff);
         const int nb[2] = {nb0, nb1};
         bool ok = mbar_wait(&sh.q_full, 0, abort_flag, p.c.status);
+#ifdef FA_TEST_HOOKS
+        // failure-detection test: as in the few-rows kernel
+        if (p.inject_stall) ok = ok && mbar_wait(&sh.never, 0, abort_flag, p.c.status);
+#endif
         tc_fence_after();
         int cleaned = 0;  // V blocks that had rows zeroed
         auto issue_s = [&](int t, int s) {
@@ -1006,6 +1014,10 @@ extern "C" int fa_fwd_paged(const fa_paged_kv* kv, const void* q, int64_t q_stri
   p.sinks = sinks < max_kv ? sinks : max_kv;
   p.scale = scale;
   p.scale_log2 = scale * 1.4426950408889634f;
+#ifdef FA_TEST_HOOKS
+  const char* inject = getenv("FA_TEST_INJECT_STALL");
+  p.inject_stall = (inject && inject[0] == '1') ? 1 : 0;
+#endif
   const bool fp8 = kv->dtype == FA_KV_E4M3;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   char* ws = static_cast<char*>(workspace);

@@ -66,6 +66,7 @@ struct RowsCfg {
 
 struct RowsShared {
   uint64_t full[8], empty[8], sync;
+  uint64_t never;            // test builds only: a barrier nothing arrives on
   uint32_t abort_flag;
   float m[kRowsWarps][16], l[kRowsWarps][16];   // by warp and row of its group
   int scan[kRowsThreads / 32];
@@ -183,6 +184,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
       mbar_init(&sh.empty[s], kRowsWarps);
     }
     mbar_init(&sh.sync, 32 * kRowsWarps);
+    mbar_init(&sh.never, 1);
     fence_barrier_init();
   }
   __syncthreads();
@@ -316,6 +318,11 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
     mbar_arrive(&sh.sync);
     return mbar_wait(&sh.sync, syncs++ & 1, abort_flag, p.c.status);
   };
+#ifdef FA_TEST_HOOKS
+  // failure-detection test: wait on a barrier nothing arrives on; the bounded wait runs out, raises
+  // the CTA's abort flag and records a timeout, and every warp unwinds
+  if (p.inject_stall) ok = __all_sync(0xffffffffu, mbar_wait(&sh.never, 0, abort_flag, p.c.status));
+#endif
   int b = sh.first_b;
   long long unit = sh.first_unit;
   bool first_piece = true;
@@ -535,11 +542,12 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
                 if (!it.w.seen(key + 8)) v1[i] = 0.f;
               }
             }
-            top = max3f(top, v0[i], v1[i]);
+            top = max3f(top, fabsf(v0[i]), fabsf(v1[i]));
           }
           if (__any_sync(0xffffffffu, top > vref)) {
 #pragma unroll
             for (int off = 4; off < 32; off *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            top = fmaxf(top, 1.1754943508222875e-38f);   // 2^-126: the reciprocal stays finite
             const float ratio = vref / top;
 #pragma unroll
             for (int nr = 0; nr < kNR; ++nr) {

@@ -30,6 +30,7 @@ struct Attn {   // arguments of both kernels
   int few_rows;              // sequences of up to this many rows (8, 16, 32, 64) are the few-rows kernel's; 0: none
   int window, sinks;         // window 0: none
   float scale, scale_log2;   // scale_log2 = scale log2(e)
+  int inject_stall;          // test builds only (FA_TEST_HOOKS): make a warp's first wait run out
 };
 
 // The new tokens of one sequence and the keys they see.

@@ -136,6 +136,79 @@ def test_extreme_magnitudes(fmt, q_std, k_std):
         check(c, new, group, q=q, scale=0.125)
 
 
+def test_overlapping_tensors_are_refused():
+    # a stride below an entry's size (expand) would not describe the memory that the kernels address
+    c = P.make([40, 40], 2, 64, 16, "e4m3", seed=1)
+    q = queries([1, 1], 4, 64, 1).cuda()
+    ip = P.indptr([1, 1])
+    ok = dict(k_scale=c.ks, v_scale=c.vs)
+
+    def refused(*a, **kw):
+        with pytest.raises(ValueError):
+            binding.forward_paged(*a, **kw)
+
+    binding.forward_paged(q, c.k, c.v, c.table, c.kv_len, ip, 1, **ok)
+    refused(q[:1].expand(2, 4, 64), c.k, c.v, c.table, c.kv_len, ip, 1, **ok)
+    refused(q, c.k[:1].expand(4, 2, 16, 64), c.v[:1].expand(4, 2, 16, 64), c.table, c.kv_len, ip, 1,
+            k_scale=c.ks[:4], v_scale=c.vs[:4])
+    refused(q, c.k, c.v, c.table[:1].expand(2, c.table.shape[1]), c.kv_len, ip, 1, **ok)
+    refused(q, c.k, c.v, c.table, c.kv_len, ip, 1, k_scale=c.ks[:1].expand(c.P, 2, 16), v_scale=c.vs[:1].expand(c.P, 2, 16))
+    refused(q, c.k.transpose(1, 2), c.v.transpose(1, 2), c.table, c.kv_len, ip, 1, **ok)
+    with pytest.raises(ValueError):
+        binding.kv_append(q[:, :2], q[:1, :2].expand(2, 2, 64), c.k, c.v, c.table, c.kv_len, ip, **ok)
+    binding.device_status()
+
+
+@pytest.mark.parametrize("new,group", [([1, 2], 8), ([90, 3], 8)])
+def test_scales_of_other_quantisers(new, group):
+    # scales that are no powers of two, negative, zero and subnormal ones
+    c = P.make([300, 77], 1, 64, 16, "e4m3", seed=4)
+    g = torch.Generator().manual_seed(9)
+    c.ks *= (torch.rand(c.ks.shape, generator=g) + 0.5).cuda()
+    mult = torch.rand(c.vs.shape, generator=g) + 0.5
+    mult[torch.rand(c.vs.shape, generator=g) < 0.3] *= -1
+    mult[torch.rand(c.vs.shape, generator=g) < 0.1] = 0
+    mult[torch.rand(c.vs.shape, generator=g) < 0.1] = 2.0 ** -125   # times a scale near 2^-7: subnormal
+    c.vs *= mult.cuda()
+    for b, n in enumerate(c.lens):
+        t = torch.arange(n)
+        pg = c.table[b].cpu().long()[t // 16]
+        for w, (codes, s) in enumerate(((c.k, c.ks), (c.v, c.vs))):
+            x = codes.cpu()[pg, :, t % 16].view(P.E4M3).double() * s.cpu()[pg, :, t % 16].double()[..., None]
+            c.values[b][w] = x.transpose(0, 1)
+    q = queries(new, group, 64, 6)
+    o, lse = attend(c, q, new)
+    binding.device_status()
+    want, want_lse, tol = P.reference(c, q, new, 0.125)
+    # a kernel may round K and V to BF16 (half a step each): V adds 2^-8 of |O|'s terms, as much again as
+    # P~'s rounding; a score moves by at most 2^-8 sum |q_i k_i| scale, and P by that much relatively
+    s_err = 0.0
+    for b in range(2):
+        rows = slice(0, new[0]) if b == 0 else slice(new[0], sum(new))
+        s_err = max(s_err, (q[rows].double().abs() @ c.values[b][0][0].abs().T).max().item() * 0.125 * M.HALF)
+    M.assert_within("o", o, want, (2 + 2 * s_err / M.HALF) * tol)
+    fin = torch.isfinite(want_lse)
+    assert (lse.cpu().double() - want_lse)[fin].abs().max() <= s_err + M.LSE_TOL
+
+
+def test_a_side_stream_owns_its_workspace():
+    # with stream=... the call's own buffers must not be handed to the current stream's next allocation
+    c = P.make([20000] * 4, 2, 128, 64, "bf16", seed=3)
+    q = queries([1] * 4, 8, 128, 1).cuda()
+    want, _ = attend(c, q, [1] * 4)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    ip = P.indptr([1] * 4)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        o, _ = binding.forward_paged(q, c.k, c.v, c.table, c.kv_len, ip, 1, stream=side)
+        junk = [torch.full((1 << 22,), float("nan"), device="cuda") for _ in range(4)]
+        torch.cuda.synchronize()
+        assert torch.equal(o, want)
+        del junk
+
+
 @pytest.mark.parametrize("v_std", [1e-25, 1e25])
 def test_v_scales_of_any_size(v_std):
     # E4M3 vectors whose scales differ by many powers of two, in both kernels
