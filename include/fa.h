@@ -220,11 +220,14 @@ int fa_bwd_staged(const void* q, const void* k, const void* v, const void* o, co
 
 /*
  * fa_bwd_window -- the backward of fa_fwd_window: fa_bwd with the mask of `window` and `sinks`
- * (see fa_fwd_window; o and lse are that forward's).  Workspace, outputs and errors are
- * fa_bwd's; the gradients of keys that no query sees are zero.  For queries that see at most 16
- * keys delta is summed from probabilities recomputed in FP32, not from the rounded o, whose error
- * would show in dq and dk there.
+ * (see fa_fwd_window; o and lse are that forward's).  Outputs and errors are fa_bwd's; the
+ * workspace holds at least fa_bwd_window_workspace_size(...) bytes (fa_bwd's, and partial sums where
+ * key tiles with sinks are split over their queries; 0 for invalid sizes).  The gradients of keys that
+ * no query sees are zero.  For queries that see at most 16 keys delta is summed from probabilities
+ * recomputed in FP32, not from the rounded o, whose error would show in dq and dk there.
  */
+size_t fa_bwd_window_workspace_size(int B, int H, int N, int d, int window, int sinks);
+
 int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO,
                   void* dq, void* dk, void* dv, float* delta_out, int B, int H, int N, int d, int window, int sinks,
                   float scale, void* workspace, size_t workspace_bytes, void* stream);

@@ -29,7 +29,8 @@ OUTPUT_NAMES = ("o", "lse", "dq", "dk", "dv")
 FA_DEVFLAG_TIMEOUT, FA_DEVFLAG_BOUNDS, FA_DEVFLAG_NONFINITE = 1, 2, 4
 
 # every symbol include/fa.h declares
-EXPORTS = ("fa_fwd", "fa_fwd_window", "fa_fwd_fp8", "fa_quantize_fp8", "fa_bwd", "fa_bwd_window", "fa_bwd_staged",
+EXPORTS = ("fa_fwd", "fa_fwd_window", "fa_fwd_fp8", "fa_quantize_fp8", "fa_bwd", "fa_bwd_window",
+           "fa_bwd_window_workspace_size", "fa_bwd_staged",
            "fa_bwd_noalloc", "fa_bwd_noalloc_status", "fa_bwd_workspace_size", "fa_device_status",
            "fa_device_report_read", "fa_last_error", "fa_version", "fa_kv_append", "fa_kv_read",
            "fa_fwd_paged", "fa_fwd_paged_workspace_size")
@@ -102,6 +103,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.fa_bwd.restype = ci
     L.fa_bwd_window.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, ci, cf, vp, cs, vp]
     L.fa_bwd_window.restype = ci
+    L.fa_bwd_window_workspace_size.argtypes = [ci, ci, ci, ci, ci, ci]
+    L.fa_bwd_window_workspace_size.restype = cs
     L.fa_bwd_staged.argtypes = L.fa_bwd.argtypes + [ci]
     L.fa_bwd_staged.restype = ci
     L.fa_kv_append.argtypes = [ctypes.POINTER(PagedKV), vp, vp, ctypes.c_int64, vp, ci, vp]
@@ -243,6 +246,10 @@ def fa_bwd(q, k, v, o, lse, do, dq, dk, dv, delta, causal: bool, scale: float, w
     return load().fa_bwd_staged(*args, int(stages))
 
 
+def fa_bwd_window_workspace_size(B: int, H: int, N: int, d: int, window: int, sinks: int = 0) -> int:
+    return int(load().fa_bwd_window_workspace_size(B, H, N, d, window, sinks))
+
+
 def fa_bwd_window(q, k, v, o, lse, do, dq, dk, dv, delta, window: int, sinks: int, scale: float, workspace,
                   stream=None) -> int:
     B, H, N, d = q.shape
@@ -352,13 +359,16 @@ def forward_fp8(q8, k8, v8, descale, causal: bool = True, scale=None, stable: in
 
 def backward(q, k, v, o, lse, do, causal: bool = True, scale=None, workspace=None, want_delta: bool = False,
              stream=None, window=None, sinks: int = 0):
-    """Returns (dq, dk, dv) or (dq, dk, dv, delta); window and sinks are the forward's."""
+    """Returns (dq, dk, dv) or (dq, dk, dv, delta); window and sinks are the forward's, a workspace
+    has fa_bwd_workspace_size (with a window: fa_bwd_window_workspace_size) bytes."""
     _check_qkv(q, k, v, o, do)
     _check_window(causal, window, sinks)
     B, H, N, d = q.shape
     scale = 1.0 / math.sqrt(d) if scale is None else scale
     if workspace is None:
-        workspace = _empty(fa_bwd_workspace_size(B, H, N, d), torch.uint8, q, stream)
+        size = fa_bwd_workspace_size(B, H, N, d) if window is None else \
+            fa_bwd_window_workspace_size(B, H, N, d, window, sinks)
+        workspace = _empty(size, torch.uint8, q, stream)
     dq, dk, dv = (_empty(q.shape, q.dtype, q, stream) for _ in range(3))
     delta = _empty((B, H, N), torch.float32, q, stream) if want_delta else None
     with _OnDevice(q):

@@ -59,6 +59,7 @@ static_assert(2 * 128 * kRegPdS + 128 * kRegDQ + 128 * kRegOther <= kThreads * k
               "register split exceeds the launch allocation");
 constexpr int kMaxStages = 3;   // deepest Q-tile ring (dO is single-buffered)
 constexpr int kMaxKVBufs = 2;   // most K/V buffers
+constexpr int kItemWalkMaxTiles = 32;   // d = 64: most key tiles for the item walk
 
 template <int D, bool kWalk>
 struct Cfg {
@@ -127,6 +128,8 @@ struct Params {
   int n_tiles;      // N_pad / 128
   int causal;
   int window, sinks;  // windowed kernels: query i sees keys j <= i with i - j < window or j < sinks
+  int sink_tiles, sink_splits;  // key tiles that hold sinks; items that each of them is split into
+  float* sink_part;   // [split][sink tile][BH][dK, dV][128][d] FP32 partial sums, if sink_splits > 1
   float scale;
   float scale_log2;
   int inject_stall;  // test builds only (FA_TEST_HOOKS): make the MMA warp's first wait run out
@@ -286,36 +289,87 @@ __global__ void __launch_bounds__(256) fa_bwd_dq_convert(const float* __restrict
   reinterpret_cast<uint4*>(dq)[i] = out;
 }
 
+// --------------------------------------------------------------------------- split sink tiles
+// dK and dV of the key tiles that hold sinks: the splits' FP32 sums added in their order (so the
+// result does not depend on timing), dK times scale, rounded to BF16.  A thread per 8 entries.
+template <int D>
+__global__ void __launch_bounds__(256) fa_bwd_sink_join(const float* __restrict__ part, __nv_bfloat16* __restrict__ dk,
+                                                        __nv_bfloat16* __restrict__ dv, float scale, int splits,
+                                                        int sink_tiles, int BH, int N, DevStatus* status) {
+  const long long per_split = (long long)sink_tiles * BH * 2 * kBlock * D;
+  const long long n = ((long long)blockIdx.x * blockDim.x + threadIdx.x) * 8;   // entry within a split
+  const int c = (int)(n % D), r = (int)(n / D % kBlock), w = (int)(n / ((long long)D * kBlock) % 2);
+  const long long slot = n / ((long long)2 * D * kBlock);                       // jt * BH + bh
+  const long long key = slot / BH * kBlock + r, bh = slot % BH;
+  const bool in = n < per_split && key < N;
+  float a[8] = {};
+  if (in) {
+    for (int s = 0; s < splits; ++s) {
+      const float4* src = reinterpret_cast<const float4*>(part + s * per_split + n);
+      const float4 x = __ldg(src), y = __ldg(src + 1);
+      a[0] += x.x, a[1] += x.y, a[2] += x.z, a[3] += x.w;
+      a[4] += y.x, a[5] += y.y, a[6] += y.z, a[7] += y.w;
+    }
+  }
+  const float mul = w == 0 ? scale : 1.f;
+  uint32_t o[4], bad = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    o[i] = pack_bf16x2(a[2 * i] * mul, a[2 * i + 1] * mul);
+    bad += nonfinite_bf16x2(o[i]);
+  }
+  // a warp's 256 entries lie within one of dK and dV (128 rows of d each)
+  report_nonfinite(in ? bad : 0u, status, w == 0 ? kOutDk : kOutDv);
+  if (in) *reinterpret_cast<uint4*>((w == 0 ? dk : dv) + (bh * N + key) * D + c) = make_uint4(o[0], o[1], o[2], o[3]);
+}
+
 // --------------------------------------------------------------------------- main kernel
 // Work item n of this CTA.  Items are the (key tile, head) pairs in key-tile order, so the
 // items with the most query tiles come first when causal; they are dealt to the CTAs in rounds
 // of gridDim.x, every other round in reverse CTA order, which evens out each CTA's total.
 // With one CTA per item (gridDim.x = items) every CTA gets exactly one.
-__device__ __forceinline__ bool work_item(const Params& p, int n, int& jt, int& bh) {
+// With a window and one CTA per item, a key tile that holds sinks meets every query tile while the
+// others meet window / 128 + 1: it is split over its query tiles into sink_splits items, which come
+// first.
+template <bool kWin, bool kWalk>
+__device__ __forceinline__ bool work_item(const Params& p, int n, int& jt, int& bh, int& split) {
   const long long G = gridDim.x, c = blockIdx.x;
-  const long long pos = (long long)n * G + ((n & 1) ? (G - 1 - c) : c);
+  long long pos = (long long)n * G + ((n & 1) ? (G - 1 - c) : c);
+  split = 0;
+  if constexpr (kWin && !kWalk) {
+    const long long sink_items = (long long)p.sink_tiles * p.BH, extra = sink_items * (p.sink_splits - 1);
+    if (pos < sink_items + extra) {
+      split = (int)(pos / sink_items);
+      pos -= split * sink_items;
+    } else {
+      pos -= extra;
+    }
+  }
   if (pos >= (long long)p.n_tiles * p.BH) return false;
   jt = (int)(pos / p.BH);
   bh = (int)(pos % p.BH);
   return true;
 }
 
-// The query tiles of key tile jt: its first one, i0, and their number.  With a window they end at
-// the last tile that the window of one of its keys reaches; a tile that holds sinks keeps all.
+// The query tiles of an item (key tile jt, split): its first one, i0, and their number.  With a
+// window they end at the last tile that the window of one of its keys reaches; a tile that holds
+// sinks keeps all (its split's share of them).
 template <bool kWin>
-__device__ __forceinline__ int query_tiles(const Params& p, int jt, int& i0) {
+__device__ __forceinline__ int query_tiles(const Params& p, int jt, int split, int& i0) {
   i0 = (kWin || p.causal) ? jt : 0;
   if constexpr (kWin) {
-    const int last_key = min(jt * kBlock + kBlock, p.N) - 1;
+    const int last_key = min(jt * kBlock + kBlock, p.N) - 1, all = p.n_tiles - jt;
+    if (jt * kBlock < p.sinks) {
+      i0 = jt + (int)((long long)all * split / p.sink_splits);
+      return jt + (int)((long long)all * (split + 1) / p.sink_splits) - i0;
+    }
     // the last key's window ends before row N (the sum below is then under N and cannot overflow)
-    if (jt * kBlock >= p.sinks && p.window < p.N - last_key) return (last_key + p.window - 1) / kBlock - jt + 1;
+    if (p.window < p.N - last_key) return (last_key + p.window - 1) / kBlock - jt + 1;
   }
   return p.n_tiles - i0;
 }
 
-// kWin: causal with a window and sinks (p.window, p.sinks) instead of p.causal.  Key tiles then
-// meet window / 128 + 1 query tiles, but the first ones, which hold the sinks, meet them all;
-// those come first in the work order.
+// kWin: causal with a window and sinks (p.window, p.sinks) instead of p.causal.
 template <int D, bool kWalk, bool kWin>
 __global__ void __launch_bounds__(kThreads, 1)
     fa_bwd_main(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -385,8 +439,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       int nq = 0, ndo = 0, nkv = 0;  // loads issued: Q tiles, dO tiles, K/V pairs
       bool ok = true;
       for (int n = 0; ok && (C::kMultiItem || n == 0); ++n) {
-        int jt, bh;
-        if (!work_item(p, n, jt, bh)) break;
+        int jt, bh, split;
+        if (!work_item<kWin, kWalk>(p, n, jt, bh, split)) break;
         const int b = n % C::kKVBufs;
         // the buffer's previous item has issued its last MMA reading K or V
         if (!(ok = mbar_wait(&sh.kv_empty[b], ((n / C::kKVBufs) & 1) ^ 1, abort_flag, p.status))) break;
@@ -398,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         nkv = n + 1;
         int i0;  // first query tile that sees this key tile
-        const int n_it = query_tiles<kWin>(p, jt, i0);
+        const int n_it = query_tiles<kWin>(p, jt, split, i0);
         const size_t stat_base = (size_t)bh * p.N_pad;
         for (int it = 0; it < n_it; ++it, ++g) {
           const int s = g % C::kStages;
@@ -451,12 +505,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #endif
       int g0 = 0;  // query steps before the current item, over all items
       for (int n = 0; ok && (C::kMultiItem || n == 0); ++n) {
-        int jt, bh;
-        if (!work_item(p, n, jt, bh)) break;
+        int jt, bh, split;
+        if (!work_item<kWin, kWalk>(p, n, jt, bh, split)) break;
         const int b = n % C::kKVBufs;
         const uint32_t sK = smem_u32(smem + C::kKOff + b * C::kKVBytes), sV = sK + C::kTileBytes;
         int i0;
-        const int n_it = query_tiles<kWin>(p, jt, i0);
+        const int n_it = query_tiles<kWin>(p, jt, split, i0);
         if (!(ok = mbar_wait(&sh.kv_full[b], (n / C::kKVBufs) & 1, abort_flag, p.status))) break;
         // the lambdas take the item's step `it`; barriers and buffers go by the CTA's step g0 + it
         auto issue_s = [&](int it) {  // S^T = K_j Q_i^T
@@ -575,14 +629,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int g0 = 0;  // query steps before the current item, over all items
     for (int n = 0; ok && (C::kMultiItem || n == 0); ++n) {
-    int jt, bh;
-    if (!work_item(p, n, jt, bh)) break;
+    int jt, bh, split;
+    if (!work_item<kWin, kWalk>(p, n, jt, bh, split)) break;
     int i0;
-    const int n_it = query_tiles<kWin>(p, jt, i0);
+    const int n_it = query_tiles<kWin>(p, jt, split, i0);
     for (int it = 0; it < n_it; ++it) {
       const int g = g0 + it;
       const int s = g % C::kStages;
-      const bool diag = (kWin || p.causal) && it == 0;  // query tile i0 == key tile jt: mask q < key
+      const bool diag = kWin ? i0 + it == jt : (p.causal && it == 0);  // query tile == key tile jt: mask q < key
       const uint32_t tS = tS0 + C::s_col(g);
       const float4* lse4 = reinterpret_cast<const float4*>(smem + C::kLseOff + s * kBlock * 4) + 16 * h;
       const float4* dl4 = reinterpret_cast<const float4*>(smem + C::kDeltaOff + s * kBlock * 4) + 16 * h;
@@ -614,9 +668,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < 64; ++j) pr[j] = (64 * h + j >= r) ? pr[j] : 0.f;
       }
       if constexpr (kWin) {
-        // query columns past the key's window (key jt * 128 + r, queries from it * 128 further
-        // on), unless the key is a sink
-        const int w_hi = r + p.window - it * kBlock - 64 * h;
+        // query columns past the key's window (key jt * 128 + r), unless the key is a sink
+        const int w_hi = r + p.window - (i0 + it - jt) * kBlock - 64 * h;
         if (w_hi < 64 && jt * kBlock + r >= p.sinks) {
 #pragma unroll
           for (int j = 0; j < 64; ++j) pr[j] = (j < w_hi) ? pr[j] : 0.f;
@@ -693,12 +746,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float mul = h == 0 ? p.scale : 1.f;
       __nv_bfloat16* out = h == 0 ? p.dk : p.dv;
       uint32_t bad = 0;  // NaN/Inf entries of this row, as stored
+      // a split sink tile leaves its FP32 sums for fa_bwd_sink_join
+      const bool partial = kWin && !kWalk && p.sink_splits > 1 && jt < p.sink_tiles;
 #pragma unroll
       for (int c0 = 0; c0 < D; c0 += 32) {
         uint32_t w[32];
         tmem_ld32(t + c0, w);
         tmem_ld_wait();
         reg_fence(w);
+        if (partial) {
+          const long long slot = ((long long)split * p.sink_tiles + jt) * p.BH + bh;
+          float4* dst = reinterpret_cast<float4*>(p.sink_part + ((slot * 2 + h) * kBlock + r) * D + c0);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            dst[i] = make_float4(__uint_as_float(w[4 * i]), __uint_as_float(w[4 * i + 1]), __uint_as_float(w[4 * i + 2]),
+                                 __uint_as_float(w[4 * i + 3]));
+          continue;
+        }
         uint4 pkd[4];
         uint32_t* pw = reinterpret_cast<uint32_t*>(pkd);
 #pragma unroll
@@ -740,10 +804,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     int g0 = 0;       // query steps before the current item, over all items
     bool ok = true;
     for (int n = 0; ok && (C::kMultiItem || n == 0); ++n) {
-    int jt, bh;
-    if (!work_item(p, n, jt, bh)) break;
+    int jt, bh, split;
+    if (!work_item<kWin, kWalk>(p, n, jt, bh, split)) break;
     int i0;
-    const int n_it = query_tiles<kWin>(p, jt, i0);
+    const int n_it = query_tiles<kWin>(p, jt, split, i0);
     for (int it = 0; it < n_it; ++it) {
       if (!(ok = mbar_wait(&sh.dq_full, (g0 + it) & 1, abort_flag, p.status))) break;
       tc_fence_after();
@@ -804,7 +868,35 @@ struct Scratch {
   float* dq_acc;
   float* delta;
   float* lse2;
+  float* sink_part;   // windowed backward with split sink tiles
 };
+
+// Items that each key tile with sinks is split into.  Unsplit, such a tile is a chain of N / 128 query
+// steps.  It bounds the launch where the SMs' mean share of all work is less than that (an item costs
+// about four steps more than it has: its K and V, the start of the pipeline, its epilogue); it is
+// then split into pieces of half that share (eight steps at least, and in all no more than four items
+// per SM, which bounds the partial sums).  8 heads of 12000 rows, d = 128, window 256, 4 sinks: 90 us,
+// whole 195; 32 heads of 8192 rows, window 1024 (whole by this rule): 363 us, in three pieces 387.
+int sink_splits(int BH, int N, int d, int window, int sinks) {
+  constexpr int kSms = 152;
+  const long long tiles = ((long long)N + fa::bwd::kBlock - 1) / fa::bwd::kBlock;
+  const long long sink_tiles = ((long long)(sinks < N ? sinks : N) + fa::bwd::kBlock - 1) / fa::bwd::kBlock;
+  if (!window || !sink_tiles || (d == 64 && tiles <= fa::bwd::kItemWalkMaxTiles)) return 1;
+  const long long reach = (window < N ? window : N) / fa::bwd::kBlock + 1;   // query tiles of a light item
+  const long long light = (reach < tiles ? reach : tiles) + 4, heavy = tiles + 4;
+  const long long share = BH * ((tiles - sink_tiles) * light + sink_tiles * heavy) / kSms;
+  if (tiles <= share) return 1;
+  long long n = 2 * tiles / (share + 1);
+  if (n > 4 * kSms / (sink_tiles * BH)) n = 4 * kSms / (sink_tiles * BH);
+  if (n > (tiles - sink_tiles) / 8) n = (tiles - sink_tiles) / 8;   // every piece keeps some tiles
+  return n < 1 ? 1 : (int)n;
+}
+
+size_t sink_bytes(int BH, int N, int d, int window, int sinks) {
+  const int n = sink_splits(BH, N, d, window, sinks);
+  const size_t sink_tiles = ((size_t)(sinks < N ? sinks : N) + 127) / 128;
+  return n > 1 ? fa::round_up((size_t)n * sink_tiles * BH * 2 * 128 * d * 4, 256) : 0;
+}
 
 size_t scratch_bytes(int B, int H, int N, int d) {
   const size_t bh = (size_t)B * H;
@@ -822,6 +914,8 @@ Scratch carve_scratch(void* base, int B, int H, int N, int d) {
   s.delta = reinterpret_cast<float*>(p);
   p += fa::round_up(bh * n_pad * 4, 256);
   s.lse2 = reinterpret_cast<float*>(p);
+  p += fa::round_up(bh * n_pad * 4, 256);
+  s.sink_part = reinterpret_cast<float*>(p);
   return s;
 }
 
@@ -838,7 +932,7 @@ int launch_main(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap&
   int rc = prepare_kernel(reinterpret_cast<const void*>(kern), C::kSmemBytes, bwd::kThreads, kSplit,
                           "backward kernel", &prepared);
   if (rc) return rc;
-  const long long items = (long long)p.n_tiles * p.BH;
+  const long long items = ((long long)p.n_tiles + (kWin && !kWalk ? (long long)p.sink_tiles * (p.sink_splits - 1) : 0)) * p.BH;
   long long grid = items;
   if (kWalk) {
     const int sms = sm_count();
@@ -903,6 +997,9 @@ int launch_bwd(const void* q, const void* k, const void* v, const void* o, const
   p.causal = causal;
   p.window = window < N ? window : N;
   p.sinks = sinks < N ? sinks : N;
+  p.sink_tiles = window ? (p.sinks + bwd::kBlock - 1) / bwd::kBlock : 0;
+  p.sink_splits = sink_splits(p.BH, N, D, window, sinks);
+  p.sink_part = sc.sink_part;
   p.scale = scale;
   p.scale_log2 = scale * 1.4426950408889634f;
 #ifdef FA_TEST_HOOKS
@@ -914,9 +1011,8 @@ int launch_bwd(const void* q, const void* k, const void* v, const void* o, const
   // +3 % at 4096).  Longer rows have few, long items; one CTA per item (placed by the
   // hardware as SMs free up) is 1-3 % faster there.  d = 128 has no room for a second K/V
   // buffer: one CTA per item.
-  constexpr int kItemWalkMaxTiles = 32;
   if constexpr (D == 64) {
-    if (p.n_tiles <= kItemWalkMaxTiles)
+    if (p.n_tiles <= bwd::kItemWalkMaxTiles)
       rc = window ? launch_main<D, true, true>(tq, tk, tv, tdo, tdq, p, stream)
                   : launch_main<D, true, false>(tq, tk, tv, tdo, tdq, p, stream);
     else
@@ -927,6 +1023,12 @@ int launch_bwd(const void* q, const void* k, const void* v, const void* o, const
                 : launch_main<D, false, false>(tq, tk, tv, tdo, tdq, p, stream);
   }
   if (rc) return rc;
+  if (p.sink_splits > 1) {
+    const long long n = (long long)p.sink_tiles * p.BH * 2 * bwd::kBlock * D / 8;
+    bwd::fa_bwd_sink_join<D><<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(
+        p.sink_part, p.dk, p.dv, scale, p.sink_splits, p.sink_tiles, p.BH, N, p.status);
+    if ((rc = check_cuda(cudaGetLastError(), "launch fa_bwd_sink_join"))) return rc;
+  }
   }
   if (!(stages & FA_BWD_DQ_CONVERT)) return FA_OK;
   const long long n8 = rows * D / 8;
@@ -962,7 +1064,7 @@ static int bwd_checked(const void* q, const void* k, const void* v, const void* 
   if (delta_out && (reinterpret_cast<uintptr_t>(delta_out) & 3))
     return set_error(FA_ERR_INVALID_ARG, "delta_out is not 4-byte aligned");
   if (!(scale > 0.f) || !isfinite(scale)) return set_error(FA_ERR_INVALID_ARG, "scale must be finite and > 0");
-  const size_t need = fa_bwd_workspace_size(B, H, N, d);
+  const size_t need = fa_bwd_workspace_size(B, H, N, d) + (window ? sink_bytes(B * H, N, d, window, sinks) : 0);
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255))
     return set_error(FA_ERR_INVALID_ARG, "workspace must be a 256-byte aligned device pointer");
   if (workspace_bytes < need)
@@ -982,6 +1084,12 @@ extern "C" int fa_bwd_staged(const void* q, const void* k, const void* v, const 
   fa::NvtxRange nvtx_range("fa_bwd_staged");
   return bwd_checked(q, k, v, o, lse, dO, dq, dk, dv, delta_out, B, H, N, d, causal, 0, 0, scale, workspace,
                      workspace_bytes, stream, stages);
+}
+
+extern "C" size_t fa_bwd_window_workspace_size(int B, int H, int N, int d, int window, int sinks) {
+  fa::clear_error();
+  if (fa::check_shape(B, H, N, d) || fa::check_window(window, sinks)) return 0;
+  return scratch_bytes(B, H, N, d) + sink_bytes(B * H, N, d, window, sinks);
 }
 
 extern "C" int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, const float* lse,

@@ -45,6 +45,19 @@ def test_backward_workspace_is_checked(lib):
     assert "workspace too small" in binding.last_error()
 
 
+def test_backward_workspace_of_split_sinks(lib):
+    # a long row's key tile with sinks is split over its queries: FP32 partial dK and dV per part
+    plain = lib.fa_bwd_workspace_size(1, 1, 12000, 128)
+    assert lib.fa_bwd_window_workspace_size(1, 1, 12000, 128, 256, 0) == plain
+    part = 2 * 128 * 128 * 4
+    parts, rest = divmod(lib.fa_bwd_window_workspace_size(1, 1, 12000, 128, 256, 4) - plain, part)
+    assert parts >= 2 and rest == 0
+    assert bwd(lib, sinks=4, N=12000, d=128, window=256, ws=plain) == binding.FA_ERR_INVALID_ARG
+    assert "workspace too small" in binding.last_error()
+    for bad in ((0, 1, 128, 64, 5, 0), (1, 1, 128, 96, 5, 0), (1, 1, 128, 64, 0, 0), (1, 1, 128, 64, 5, -1)):
+        assert lib.fa_bwd_window_workspace_size(*bad) == 0
+
+
 def test_python_helpers_refuse_a_window_without_causal():
     x = torch.zeros((1, 1, 4, 64), dtype=torch.bfloat16)
     for kw in (dict(causal=False, window=2), dict(sinks=3)):

@@ -64,6 +64,27 @@ def test_gradients_with_more_items_than_SMs(B, H, N, window, sinks, d):
         M.assert_within(name, got, want[name], tol[name])
 
 
+# few heads and long rows: the key tiles with sinks are split over their queries (into 2 to 8 parts),
+# last tiles whole and ragged
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,H,N,window,sinks", [(1, 2, 4224, 100, 4), (2, 1, 6200, 1, 1), (1, 1, 8300, 64, 200),
+                                                (1, 2, 8200, 300, 500), (1, 1, 7900, 2900, 257)])
+def test_gradients_of_sinks_split_over_their_queries(B, H, N, window, sinks, d):
+    assert binding.fa_bwd_window_workspace_size(B, H, N, d, window, sinks) > binding.fa_bwd_workspace_size(B, H, N, d)
+    w = inputs.random_case(B, H, N, d, True, seed=N + window + d, std=1.2)
+    (o, lse), grads = run(w, window, sinks)
+    (_, _), again = run(w, window, sinks)
+    assert torch.equal(grads[1], again[1]) and torch.equal(grads[2], again[2])   # parts are joined in one order
+    for b in range(B):
+        for h in range(H):
+            one = [x[b:b + 1, h:h + 1] for x in (w.q, w.k, w.v, w.do)]
+            ref = M.forward(*one[:3], see(N, window, sinks), w.scale)
+            want, tol = M.backward(*one, see(N, window, sinks), w.scale, ref)
+            for name, got in zip(("dq", "dk", "dv"), grads):
+                M.assert_within(name, got[b:b + 1, h:h + 1], want[name], tol[name])
+            del ref, want, tol
+
+
 @pytest.mark.parametrize("d,N", [(64, 1000), (64, 2300), (128, 700)])
 @pytest.mark.parametrize("stable", [0, 1, 2])
 def test_a_window_as_long_as_the_row_is_causal_attention(N, d, stable):
