@@ -383,12 +383,15 @@ int fa_kv_read(const fa_paged_kv* kv, const int32_t* kv_indptr, void* k_out, voi
  * Pages of which no new token sees a key are not read.  A key that some but not all rows of a tile
  * see must have finite values, as in the dense entry points (0 * Inf = NaN).
  * workspace: device scratch of at least fa_fwd_paged_workspace_size(T, B, max_q, Hq, Hkv, d,
- * max_pages * page_size, window) bytes, 256-byte aligned (NULL where that is 0); its contents on
- * entry do not matter.  Calls that may overlap need workspaces of their own.
+ * max_pages * page_size, window, sinks, kv->dtype) bytes, 256-byte aligned (NULL where that is 0); its contents on
+ * entry do not matter.  Where many rows read each key of an E4M3 cache it includes room for a BF16
+ * copy of the keys and values that the new tokens may see (2 GiB at most; from max_pages, not from
+ * the lengths).  Calls that may overlap need workspaces of their own.
  * Results do not depend on timing: the same call on the same data gives the same bits.
  * Returns FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED or FA_ERR_CUDA; T = 0 launches nothing.
  */
-size_t fa_fwd_paged_workspace_size(int T, int B, int max_q, int Hq, int Hkv, int d, int max_kv, int window);
+size_t fa_fwd_paged_workspace_size(int T, int B, int max_q, int Hq, int Hkv, int d, int max_kv, int window, int sinks,
+                                   int dtype);
 
 int fa_fwd_paged(const fa_paged_kv* kv, const void* q, int64_t q_stride, const int32_t* q_indptr, int T, int max_q,
                  int Hq, void* o, float* lse, int window, int sinks, float scale, void* workspace,

@@ -111,7 +111,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.fa_kv_append.restype = ci
     L.fa_kv_read.argtypes = [ctypes.POINTER(PagedKV), vp, vp, vp, ci, vp]
     L.fa_kv_read.restype = ci
-    L.fa_fwd_paged_workspace_size.argtypes = [ci] * 8
+    L.fa_fwd_paged_workspace_size.argtypes = [ci] * 10
     L.fa_fwd_paged_workspace_size.restype = cs
     L.fa_fwd_paged.argtypes = [ctypes.POINTER(PagedKV), vp, ctypes.c_int64, vp, ci, ci, ci, vp, vp, ci, ci, cf, vp, cs, vp]
     L.fa_fwd_paged.restype = ci
@@ -227,8 +227,8 @@ def fa_quantize_fp8(x, x8, descale, stream=None) -> int:
 
 
 def fa_fwd_paged_workspace_size(T: int, B: int, max_q: int, Hq: int, Hkv: int, d: int, max_kv: int,
-                                window: int = 0) -> int:
-    return int(load().fa_fwd_paged_workspace_size(T, B, max_q, Hq, Hkv, d, max_kv, window))
+                                window: int = 0, sinks: int = 0, dtype: int = FA_KV_BF16) -> int:
+    return int(load().fa_fwd_paged_workspace_size(T, B, max_q, Hq, Hkv, d, max_kv, window, sinks, dtype))
 
 
 def fa_bwd_workspace_size(B: int, H: int, N: int, d: int) -> int:
@@ -526,7 +526,8 @@ def forward_paged(q, k_cache, v_cache, block_table, kv_len, q_indptr, max_q, k_s
         return out, lse
     lib = load()
     if workspace is None:
-        n = lib.fa_fwd_paged_workspace_size(T, kv.B, max_q, Hq, kv.Hkv, d, kv.max_pages * kv.page_size, window)
+        n = lib.fa_fwd_paged_workspace_size(T, kv.B, max_q, Hq, kv.Hkv, d, kv.max_pages * kv.page_size, window, sinks,
+                                            kv.dtype)
         workspace = _empty(n, torch.uint8, q, stream) if n else None
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the cache's device")

@@ -14,7 +14,7 @@
 // reads back as NaN.
 #include <type_traits>
 
-#include "paged.cuh"
+#include "paged_attn.cuh"
 
 namespace fa {
 namespace paged {
@@ -133,17 +133,63 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const Cache c, cons
   }
 }
 
-// k_out, v_out: [rows, Hkv, d] contiguous; `tokens` rows per CTA.
+// One token's K and V rows of all heads as BF16, by one warp: head h's go to k_out and v_out +
+// h * head_stride.
 template <int D, bool kFp8>
-__global__ void __launch_bounds__(kThreads) kv_read_kernel(const Cache c, const int32_t* __restrict__ kv_indptr,
-                                                           __nv_bfloat16* __restrict__ k_out,
-                                                           __nv_bfloat16* __restrict__ v_out, int rows, int tokens) {
+__device__ __forceinline__ void read_token(const Cache& c, int page, int slot, int lane, __nv_bfloat16* k_out,
+                                           __nv_bfloat16* v_out, long long head_stride) {
   // 8 elements per lane: a warp's stores then cover whole lines (with 16 codes per lane each 16-byte
   // store left half of its sector to the next one)
   constexpr int kElems = 8;
   constexpr int kLanes = D / kElems;
   constexpr int kVecs = 32 / kLanes;
   constexpr int kUnroll = 8;
+  constexpr int kBytes = kFp8 ? 1 : 2;
+  using Part = std::conditional_t<kFp8, uint2, uint4>;   // a lane's elements in the cache
+  const int sub = lane / kLanes, col = (lane % kLanes) * kElems;
+  const int n = 2 * c.Hkv, page_size = 1 << c.page_shift;
+  for (int i0 = 0; i0 < n; i0 += kVecs * kUnroll) {
+    Part x[kUnroll];
+    float sc[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int i = i0 + u * kVecs + sub;
+      x[u] = Part{};
+      sc[u] = 0.f;
+      if (i < n) {
+        const long long row = (long long)(i >> 1) * page_size + slot;
+        const uint8_t* base = static_cast<const uint8_t*>((i & 1) ? c.v : c.k);
+        x[u] = __ldg(reinterpret_cast<const Part*>(base + (page * c.page_stride + row * D + col) * kBytes));
+        if constexpr (kFp8) sc[u] = __ldg(((i & 1) ? c.v_scale : c.k_scale) + page * c.scale_stride + row);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int i = i0 + u * kVecs + sub;
+      if (i >= n) break;
+      uint4* dst = reinterpret_cast<uint4*>(((i & 1) ? v_out : k_out) + (i >> 1) * head_stride + col);
+      if constexpr (!kFp8) {
+        *dst = x[u];
+      } else {
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = e4m3x2_to_float2((e < 2 ? x[u].x : x[u].y) >> (16 * (e & 1)));
+          float lo, hi;
+          mul2(lo, hi, f.x, f.y, sc[u], sc[u]);
+          o[e] = pack_bf16x2(lo, hi);
+        }
+        *dst = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+  }
+}
+
+// k_out, v_out: [rows, Hkv, d] contiguous; `tokens` rows per CTA.
+template <int D, bool kFp8>
+__global__ void __launch_bounds__(kThreads) kv_read_kernel(const Cache c, const int32_t* __restrict__ kv_indptr,
+                                                           __nv_bfloat16* __restrict__ k_out,
+                                                           __nv_bfloat16* __restrict__ v_out, int rows, int tokens) {
   __shared__ Places at;
   const int lane = threadIdx.x % 32, first = blockIdx.x * tokens;
   const int page_size = 1 << c.page_shift;
@@ -160,49 +206,48 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const Cache c, const 
     at.slot[threadIdx.x] = pos & (page_size - 1);
   }
   __syncthreads();
-  const int sub = lane / kLanes, col = (lane % kLanes) * kElems;
-  const int n = 2 * c.Hkv;
-  constexpr int kBytes = kFp8 ? 1 : 2;
-  using Part = std::conditional_t<kFp8, uint2, uint4>;   // a lane's elements in the cache
   for (int t = threadIdx.x / 32; t < tokens; t += kThreads / 32) {
-    const int page = at.page[t], slot = at.slot[t], r = first + t;
-    if (page < 0) continue;
-    for (int i0 = 0; i0 < n; i0 += kVecs * kUnroll) {
-      Part x[kUnroll];
-      float sc[kUnroll];
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int i = i0 + u * kVecs + sub;
-        x[u] = Part{};
-        sc[u] = 0.f;
-        if (i < n) {
-          const long long row = (long long)(i >> 1) * page_size + slot;
-          const uint8_t* base = static_cast<const uint8_t*>((i & 1) ? c.v : c.k);
-          x[u] = __ldg(reinterpret_cast<const Part*>(base + (page * c.page_stride + row * D + col) * kBytes));
-          if constexpr (kFp8) sc[u] = __ldg(((i & 1) ? c.v_scale : c.k_scale) + page * c.scale_stride + row);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int i = i0 + u * kVecs + sub;
-        if (i >= n) break;
-        uint4* dst = reinterpret_cast<uint4*>(((i & 1) ? v_out : k_out) + ((long long)r * c.Hkv + (i >> 1)) * D + col);
-        if constexpr (!kFp8) {
-          *dst = x[u];
-        } else {
-          uint32_t o[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = e4m3x2_to_float2((e < 2 ? x[u].x : x[u].y) >> (16 * (e & 1)));
-            float lo, hi;
-            mul2(lo, hi, f.x, f.y, sc[u], sc[u]);
-            o[e] = pack_bf16x2(lo, hi);
-          }
-          *dst = make_uint4(o[0], o[1], o[2], o[3]);
-        }
-      }
-    }
+    if (at.page[t] < 0) continue;
+    const long long row = (long long)(first + t) * c.Hkv * D;
+    read_token<D, kFp8>(c, at.page[t], at.slot[t], lane, k_out + row, v_out + row, D);
   }
+}
+
+// The E4M3 keys and values that the chunk kernel's sequences see, as a BF16 cache of its own (p.copy: pages
+// of 128 tokens, a table and a pool in the workspace): a tile would multiply every code by its scale anew.
+// Sequence b's seen blocks of 128 keys have p.copy_pages pages from b * p.copy_pages on: those that
+// hold sinks, then those from its window on.  A CTA takes 16 tokens, all of one page of either cache.
+template <int D>
+__global__ void __launch_bounds__(kThreads) kv_copy_kernel(const Attn p, const Cache to) {
+  constexpr int kBlk = 1 << kCopyShift;
+  const int b = blockIdx.x / (kBlk / kTokens) / p.copy_pages, slot = blockIdx.x / (kBlk / kTokens) - b * p.copy_pages;
+  const Seq s = load_seq(p, b);
+  if (s.n == 0 || s.n * p.group <= p.few_rows) return;
+  const KeyWalk<kBlk> walk(p, s.pos0, s.kv - 1);
+  const int n_sink = (walk.sinks + kBlk - 1) / kBlk;
+  const int i = slot < n_sink ? slot : max(walk.b_lo, n_sink) + slot - n_sink;
+  const int part = blockIdx.x % (kBlk / kTokens) * kTokens, key = i * kBlk + part;
+  if (i >= to.max_pages) return;
+  const int page_to = b * p.copy_pages + slot;
+  if (part == 0 && threadIdx.x == 0) const_cast<int32_t*>(to.table)[b * to.table_stride + i] = page_to;
+  if (!walk.any(key, kTokens)) return;
+  const int page = find_page(p.c, b, key, kSitePagedPage);
+  if (page < 0) return;
+  const int from = key & ((1 << p.c.page_shift) - 1);
+  for (int t = threadIdx.x / 32; t < kTokens && key + t < walk.hi; t += kThreads / 32) {
+    const long long row = page_to * to.page_stride + (long long)(part + t) * D;
+    read_token<D, true>(p.c, page, from + t, threadIdx.x % 32, static_cast<__nv_bfloat16*>(to.k) + row,
+                        static_cast<__nv_bfloat16*>(to.v) + row, (long long)kBlk * D);
+  }
+}
+
+int launch_copy(const Attn& p, const Cache& to, int d, cudaStream_t s) {
+  const unsigned grid = (unsigned)p.copy_pages * p.c.B * ((1 << kCopyShift) / kTokens);
+  if (d == 64)
+    kv_copy_kernel<64><<<grid, kThreads, 0, s>>>(p, to);
+  else
+    kv_copy_kernel<128><<<grid, kThreads, 0, s>>>(p, to);
+  return check_cuda(cudaGetLastError(), "launch kv_copy_kernel");
 }
 
 // Tokens per CTA: 16, or 8 (one for each warp) where that leaves SMs without a CTA.

@@ -10,7 +10,8 @@
 //     the last rows of a tile stay unused.
 //   * K and V blocks come page by page.  E4M3 codes land in slots of their own, from which a warpgroup
 //     multiplies them by their vector's scale and writes the BF16 operand tiles (exact for power-of-two
-//     scales) beside the softmax.
+//     scales) beside the softmax.  Where enough tiles read each key, kv_copy_kernel does that once, into
+//     BF16 pages in the workspace, and this kernel reads those (copy_pays).
 //   * With rows for one tile only the tensor core would wait for each block's softmax and the softmax for
 //     each product.  Both warpgroups then work on that tile: one on the even blocks, the other on the odd
 //     ones, each with its own running maximum, sum and O, joined at the end (a mixed batch of eight
@@ -24,6 +25,8 @@
 // product as the tensor core takes it.  Plain shift: the stabilised rule guards the training
 // backward, and the output does not depend on the shift.
 #include <stdlib.h>
+
+#include <algorithm>
 
 #include "paged_attn.cuh"
 
@@ -886,10 +889,27 @@ struct Plan {
   int splits;     // chunk kernel: most pieces of the keys of a tile past the first `whole` (0: not launched)
   int whole;
   long long extra;   // CTAs of split tiles
+  int copy_pages;    // an E4M3 cache is copied to BF16 pages first: pages per sequence (0: it is not)
 };
 
-Plan make_plan(int T, int B, int max_q, int group, int Hkv, int max_kv, int window) {
-  Plan pl{0, 0, 0, 0};
+// Whether an E4M3 cache is copied to BF16 pages before the chunk kernel runs.  Else each tile of 256 rows
+// multiplies the codes of all its keys by their scales, which takes longer than its products: 2048
+// tokens (4 heads of a group, d = 128) over 16k keys 684 us, with the copy 428 (22 of them the copy's);
+// over 60k 2233 and 1344.  The copy costs a launch and three times a key's bytes in memory traffic: 128
+// tokens (two tiles per kv head) over 16k keys 73 us without, 78 with it; 512 tokens (eight tiles) 199
+// and 146; 16 sequences of some 200 tokens (three tiles each) 142 and 151.  So: where a copied key is
+// read by six tiles on average, of a copy of at most 2 GiB.
+bool copy_pays(int T, int B, int group, int max_q, int Hkv, int d, int max_kv, int window, long long pages) {
+  constexpr long long kTiles = 6, kMostBytes = 1ll << 31;
+  if (4 * pages * B * Hkv * d > kMostBytes >> fa::paged::kCopyShift) return false;
+  const long long tiles = (long long)T * group / (2 * fa::paged::kM);
+  const long long by_tile = window ? std::min<long long>(max_kv, window) : max_kv;                 // keys of a tile
+  const long long by_sequence = window ? std::min<long long>(max_kv, (long long)window + max_q) : max_kv;
+  return tiles * by_tile >= kTiles * B * by_sequence;
+}
+
+Plan make_plan(int T, int B, int max_q, int group, int Hkv, int d, int max_kv, int window, int sinks, int dtype) {
+  Plan pl{0, 0, 0, 0, 0};
   const long long rows = (long long)max_q * group;
   if (rows <= kMaxFewRows) {
     pl.few_rows = rows <= 8 ? 8 : (rows <= 16 ? 16 : (rows <= 32 ? 32 : 64));
@@ -922,18 +942,27 @@ Plan make_plan(int T, int B, int max_q, int group, int Hkv, int max_kv, int wind
   }
   pl.whole = (int)(pl.splits > 1 ? tiles - rest : tiles);
   pl.extra = pl.splits > 1 ? rest * pl.splits : 0;
+  if (dtype == FA_KV_E4M3) {
+    constexpr long long kBlk = 1 << fa::paged::kCopyShift;
+    long long pages = (max_kv + kBlk - 1) / kBlk;
+    if (window) {
+      const long long seen = (sinks + kBlk - 1) / kBlk + ((long long)window + max_q) / kBlk + 2;
+      if (seen < pages) pages = seen;
+    }
+    if (copy_pays(T, B, group, max_q, Hkv, d, max_kv, window, pages)) pl.copy_pages = (int)pages;
+  }
   return pl;
 }
 
 struct Parts {
-  size_t o, lse, info, total;   // offsets
+  size_t o, lse, info, k, v, table, total;   // offsets
 };
 
-// The workspace: FP32 partial outputs, their log-sum-exps, and the few-rows kernel's records.  The two
-// kernels of a mixed batch have parts of their own.
-Parts carve(const Plan& pl, int B, int Hkv, int d, Parts* chunk) {
+// The workspace: FP32 partial outputs, their log-sum-exps, the few-rows kernel's records, the copied
+// cache.  The two kernels of a mixed batch have parts of their own.
+Parts carve(const Plan& pl, int B, int Hkv, int d, int max_kv, Parts* chunk) {
   const size_t rows = pl.few_rows ? (size_t)2 * fa::paged::kRowsMaxCtas * pl.few_rows : 0;
-  Parts f;
+  Parts f{};
   f.o = 0;
   f.lse = fa::round_up(rows * d * 4, 256);
   f.info = f.lse + fa::round_up(rows * 4, 256);
@@ -942,7 +971,12 @@ Parts carve(const Plan& pl, int B, int Hkv, int d, Parts* chunk) {
   chunk->o = f.total;
   chunk->lse = chunk->o + fa::round_up(c_rows * d * 4, 256);
   chunk->info = 0;
-  chunk->total = chunk->lse + fa::round_up(c_rows * 4, 256);
+  constexpr size_t kBlk = 1 << fa::paged::kCopyShift;
+  const size_t pool = fa::round_up((size_t)pl.copy_pages * B * kBlk * Hkv * d * 2, 256);
+  chunk->k = chunk->lse + fa::round_up(c_rows * 4, 256);
+  chunk->v = chunk->k + pool;
+  chunk->table = chunk->v + pool;
+  chunk->total = chunk->table + (pl.copy_pages ? fa::round_up((max_kv + kBlk - 1) / kBlk * B * 4, 256) : 0);
   return f;
 }
 
@@ -960,11 +994,13 @@ int check_attn(int T, int B, int max_q, int Hq, int Hkv, int d) {
 
 }  // namespace
 
-extern "C" size_t fa_fwd_paged_workspace_size(int T, int B, int max_q, int Hq, int Hkv, int d, int max_kv, int window) {
+extern "C" size_t fa_fwd_paged_workspace_size(int T, int B, int max_q, int Hq, int Hkv, int d, int max_kv, int window,
+                                               int sinks, int dtype) {
   fa::clear_error();
-  if (check_attn(T, B, max_q, Hq, Hkv, d) || max_kv < 0 || window < 0 || T == 0) return 0;
+  if (check_attn(T, B, max_q, Hq, Hkv, d) || max_kv < 0 || window < 0 || sinks < 0 || T == 0) return 0;
   Parts chunk;
-  carve(make_plan(T, B, max_q, Hq / Hkv, Hkv, max_kv, window < max_kv ? window : 0), B, Hkv, d, &chunk);
+  carve(make_plan(T, B, max_q, Hq / Hkv, Hkv, d, max_kv, window < max_kv ? window : 0, std::min(sinks, max_kv), dtype), B, Hkv,
+        d, max_kv, &chunk);
   return chunk.total;
 }
 
@@ -990,9 +1026,10 @@ extern "C" int fa_fwd_paged(const fa_paged_kv* kv, const void* q, int64_t q_stri
   if (T == 0 || max_q == 0) return FA_OK;
   const int max_kv = kv->max_pages * kv->page_size;
   if (window >= max_kv) window = 0;   // a window of the whole cache is none
-  const Plan pl = make_plan(T, kv->B, max_q, Hq / kv->Hkv, kv->Hkv, max_kv, window);
+  sinks = std::min(sinks, max_kv);
+  const Plan pl = make_plan(T, kv->B, max_q, Hq / kv->Hkv, kv->Hkv, kv->d, max_kv, window, sinks, kv->dtype);
   Parts chunk;
-  const Parts few = carve(pl, kv->B, kv->Hkv, kv->d, &chunk);
+  const Parts few = carve(pl, kv->B, kv->Hkv, kv->d, max_kv, &chunk);
   if (chunk.total) {
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255))
       return set_error(FA_ERR_INVALID_ARG, "workspace must be a 256-byte aligned device pointer");
@@ -1012,14 +1049,15 @@ extern "C" int fa_fwd_paged(const fa_paged_kv* kv, const void* q, int64_t q_stri
   p.max_rows = (int)((long long)max_q * p.group < INT32_MAX ? max_q * p.group : INT32_MAX);
   p.few_rows = pl.few_rows;
   p.window = window;
-  p.sinks = sinks < max_kv ? sinks : max_kv;
+  p.sinks = sinks;
+  p.copy_pages = pl.copy_pages;
   p.scale = scale;
   p.scale_log2 = scale * 1.4426950408889634f;
 #ifdef FA_TEST_HOOKS
   const char* inject = getenv("FA_TEST_INJECT_STALL");
   p.inject_stall = (inject && inject[0] == '1') ? 1 : 0;
 #endif
-  const bool fp8 = kv->dtype == FA_KV_E4M3;
+  const bool fp8 = kv->dtype == FA_KV_E4M3, copy = pl.copy_pages > 0;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   char* ws = static_cast<char*>(workspace);
   // Chunks first; the few-rows kernel of a mixed batch then starts beside them, on SMs that they leave
@@ -1030,7 +1068,18 @@ extern "C" int fa_fwd_paged(const fa_paged_kv* kv, const void* q, int64_t q_stri
   p.part_o = reinterpret_cast<float*>(ws + few.o);
   p.part_lse = reinterpret_cast<float*>(ws + few.lse);
   p.part_info = reinterpret_cast<int4*>(ws + few.info);
-  if (pl.splits && (rc = paged::launch_chunk(c, kv->d, fp8, pl.whole, pl.splits, s))) return rc;
+  if (copy) {
+    c.c.k = ws + chunk.k;
+    c.c.v = ws + chunk.v;
+    c.c.table = reinterpret_cast<const int32_t*>(ws + chunk.table);
+    c.c.page_shift = paged::kCopyShift;
+    c.c.max_pages = (max_kv + (1 << paged::kCopyShift) - 1) >> paged::kCopyShift;
+    c.c.table_stride = c.c.max_pages;
+    c.c.num_pages = pl.copy_pages * kv->B;
+    c.c.page_stride = (long long)kv->Hkv * kv->d << paged::kCopyShift;
+    if ((rc = paged::launch_copy(p, c.c, kv->d, s))) return rc;
+  }
+  if (pl.splits && (rc = paged::launch_chunk(c, kv->d, fp8 && !copy, pl.whole, pl.splits, s))) return rc;
   if (pl.few_rows && (rc = paged::launch_rows(p, kv->d, fp8, pl.splits > 0, s))) return rc;
   if (pl.splits > 1 && (rc = paged::launch_chunk_combine(c, kv->d, pl.whole, pl.splits, s))) return rc;
   return pl.few_rows ? paged::launch_rows_combine(p, kv->d, s) : FA_OK;

@@ -28,6 +28,7 @@ struct Attn {   // arguments of both kernels
   int T, Hq, group;
   int max_rows;              // largest number of rows of a sequence (the caller's max_q)
   int few_rows;              // sequences of up to this many rows (8, 16, 32, 64) are the few-rows kernel's; 0: none
+  int copy_pages;            // pages of a sequence in the BF16 copy of an E4M3 cache (see launch_copy)
   int window, sinks;         // window 0: none
   float scale, scale_log2;   // scale_log2 = scale log2(e)
   int inject_stall;          // test builds only (FA_TEST_HOOKS): make a warp's first wait run out
@@ -108,6 +109,9 @@ inline long long chunk_pairs(int T, int B, int group) {
   return (T - seqs) / per + seqs;
 }
 
+constexpr int kCopyShift = 7;    // tokens of a page of the copied cache: 128, the chunk kernel's block
+
+int launch_copy(const Attn& p, const Cache& to, int d, cudaStream_t s);
 int launch_rows(const Attn& p, int d, bool fp8, bool beside, cudaStream_t s);
 int launch_rows_combine(const Attn& p, int d, cudaStream_t s);
 int launch_chunk(const Attn& p, int d, bool fp8, int whole, int splits, cudaStream_t s);

@@ -95,7 +95,17 @@ def test_workspace_sizes(lib):
     assert size(153 * 64, 1, 153 * 64, 4, 1, 128, 256) == 0
     assert size(128, 1, 128, 1, 1, 128, 1 << 15) > 0
     assert size(128, 1, 128, 1, 1, 128, 1 << 15, 100) == 0
-    for bad in (dict(d=96), dict(Hq=7), dict(Hkv=0), dict(T=-1), dict(T=0), dict(B=0)):
+    # E4M3 chunks whose tiles read each key often have room for BF16 pages of 128 keys (K and V) and a
+    # table: 512 tokens of 4 heads for each kv head over 16000 keys; seen keys only with a window
+    copy = lambda pages, B=1: 2 * pages * B * 128 * 8 * 128 * 2 + -(-125 * B * 4 // 256) * 256
+    a = (512, 1, 512, 32, 8, 128, 16000)
+    assert size(*a, dtype=binding.FA_KV_E4M3) == size(*a) + copy(125)
+    a = (4096, 1, 4096, 32, 8, 128, 16000, 5000)
+    assert size(*a, 130, binding.FA_KV_E4M3) == size(*a, 130) + copy(2 + (5000 + 4096) // 128 + 2)
+    for a in ((100, 1, 100, 32, 8, 128, 16000), (400, 40, 400, 32, 8, 128, 16000), (400, 1, 400, 32, 8, 128, 16000, 100),
+              (1 << 16, 1, 1 << 16, 32, 8, 128, 1 << 23)):   # too few tiles; a copy past 2 GiB
+        assert size(*a, dtype=binding.FA_KV_E4M3) == size(*a)
+    for bad in (dict(d=96), dict(Hq=7), dict(sinks=-1), dict(Hkv=0), dict(T=-1), dict(T=0), dict(B=0)):
         a = dict(T=5, B=5, max_q=1, Hq=8, Hkv=2, d=64, max_kv=1000)
         a.update(bad)
         assert size(**a) == 0

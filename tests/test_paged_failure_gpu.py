@@ -22,7 +22,7 @@ def lib():
     require_gpu()
     L = ctypes.CDLL(build.build(testhooks=True))
     vp, ci, cf = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
-    L.fa_fwd_paged_workspace_size.argtypes = [ci] * 8
+    L.fa_fwd_paged_workspace_size.argtypes = [ci] * 10
     L.fa_fwd_paged_workspace_size.restype = ctypes.c_size_t
     L.fa_fwd_paged.argtypes = [ctypes.POINTER(binding.PagedKV), vp, ctypes.c_int64, vp, ci, ci, ci, vp, vp, ci, ci, cf, vp,
                                ctypes.c_size_t, vp]
@@ -43,7 +43,8 @@ def test_a_wait_that_runs_out_is_reported_and_nothing_else_breaks(lib, monkeypat
     o = torch.zeros_like(qd)
     lse = torch.zeros((sum(new), hq), device="cuda")
     kv = binding._paged(c.k, c.v, c.table, c.kv_len, c.ks, c.vs)
-    n = lib.fa_fwd_paged_workspace_size(sum(new), len(new), max(new), hq, 2, d, kv.max_pages * 32, 0)
+    n = lib.fa_fwd_paged_workspace_size(sum(new), len(new), max(new), hq, 2, d, kv.max_pages * 32, 0, 0,
+                                        kv.dtype)
     stream = torch.cuda.current_stream().cuda_stream
 
     def call(fill):

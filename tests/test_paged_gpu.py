@@ -209,6 +209,71 @@ def test_a_side_stream_owns_its_workspace():
         del junk
 
 
+def bf16_twin(c):
+    """The same cache in BF16: each code times its scale (exact for the powers of two that scales are)."""
+    t = P.SimpleNamespace(**vars(c))
+    t.fmt, t.ks, t.vs = "bf16", None, None
+    t.k, t.v = ((x.view(torch.float8_e4m3fn).float() * s[..., None]).to(torch.bfloat16)
+                for x, s in ((c.k, c.ks), (c.v, c.vs)))
+    return t
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page", [16, 64, 256])
+@pytest.mark.parametrize("hkv,group,lens,new,window,sinks", [
+    (2, 4, [1500], [500], None, 0), (3, 1, [1700], [1700], None, 0), (1, 7, [3100, 900], [450, 500], None, 0),
+    (2, 16, [2000, 40, 600], [260, 1, 290], None, 0), (1, 4, [5000], [1500], 1300, 200),
+    (1, 8, [2600, 3000], [700, 900], 900, 0), (2, 4, [2900], [2000], 2000, 1), (1, 2, [900, 1800], [1000, 1500], None, 0)])
+def test_chunks_of_a_copied_cache(d, page, hkv, group, lens, new, window, sinks):
+    # E4M3 chunks with many tiles read BF16 pages that the call writes to its workspace first: the bits of
+    # the same call on a BF16 cache, whatever the workspace held, and nothing outside of it written
+    c = P.make(lens, hkv, d, page, "e4m3", seed=d + page + len(new))
+    cap = c.table.shape[1] * page
+    args = (sum(new), len(new), max(new), hkv * group, hkv, d, cap, window or 0, sinks)
+    n = binding.fa_fwd_paged_workspace_size(*args, binding.FA_KV_E4M3)
+    assert n > binding.fa_fwd_paged_workspace_size(*args)
+    q = queries(new, hkv * group, d, 3)
+    kw = dict(window=window, sinks=sinks)
+    want = attend(bf16_twin(c), q, new, **kw)
+    for fill in (0xFF, 0x7F, 0x00):
+        ws = torch.full((n + 4096,), fill, device="cuda", dtype=torch.uint8)
+        o, lse = attend(c, q, new, workspace=ws[:n], **kw)
+        torch.cuda.synchronize()
+        assert (ws[n:] == fill).all()
+        row = 0
+        for b, m in enumerate(new):
+            r = slice(row, row + m)
+            # (in the last case, rows before the sequence's first key see nothing: 0 and -inf in both)
+            if m * group > 16:   # the others' kernel reads the codes, and rounds elsewhere
+                assert torch.equal(o[r], want[0][r]) and torch.equal(lse[r], want[1][r]), b
+            row += m
+    check(c, new, group, q=q, **kw)
+
+
+def test_a_captured_chunk_of_a_copied_cache_follows_lengths():
+    c = P.make([1500, 1300], 2, 128, 32, "e4m3", seed=5)
+    new = [700, 500]
+    q = queries(new, 8, 128, 2).cuda()
+    kw = dict(window=1100, sinks=3)
+    ip = P.indptr(new)
+
+    def step(x):
+        return binding.forward_paged(q, x.k, x.v, x.table, x.kv_len, ip, max(new), k_scale=x.ks, v_scale=x.vs, **kw)
+
+    step(c)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = step(c)
+    for lens in ([1500, 1300], [700, 1299], [1201, 300], [900, 0]):
+        c.kv_len.copy_(torch.tensor(lens))
+        o.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        want, want_lse = step(bf16_twin(c))
+        assert torch.equal(o, want) and torch.equal(lse, want_lse)
+    binding.device_status()
+
+
 @pytest.mark.parametrize("v_std", [1e-25, 1e25])
 def test_v_scales_of_any_size(v_std):
     # E4M3 vectors whose scales differ by many powers of two, in both kernels
@@ -230,7 +295,7 @@ def test_v_scales_of_any_size(v_std):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
-@pytest.mark.parametrize("new", [[1, 1, 1, 1], [5, 150, 1, 64]])
+@pytest.mark.parametrize("new", [[1, 1, 1, 1], [5, 150, 1, 64], [100, 700, 900, 70]])
 def test_bad_entries_are_reported_and_not_followed(fmt, new):
     lens = [100, 400, 900, 70]
     q = queries(new, 8, 64, 8)
