@@ -2,11 +2,13 @@
 // as packed BF16 rows (fa_kv_read).
 //
 // Both move each vector (one head's key or value of one token, d elements) once: bandwidth work.
-// A CTA takes up to 16 tokens: one warp looks all of them up (sequence, page, slot: four loads that
-// wait for one another), a lane each, then each warp walks the 2 Hkv vectors of its tokens, several at
-// a time with all their loads in flight.  (27k tokens of 8 heads, d = 128, into E4M3: 33 us, 73 % of the
-// measured copy rate; into BF16 34 us, 91 %.  50k tokens back from E4M3: 56 us, 87 %, from BF16 67 us,
-// 97 %.  8 or 32 tokens for each CTA: 34-35 us for the first; 4 vectors in flight: 37 us.)
+// The threads of a CTA look its tokens up, one each (sequence, page, slot: four loads that wait for one
+// another), then its warps walk the tokens' vectors, eight loads of each lane in flight, so dealt
+// that neighbouring lanes take neighbouring slots of one head, which follow one another in the cache, as do
+// their scales.  27k tokens of 8 heads, d = 128: into E4M3 30 us, 80 % of the measured copy rate,
+// into BF16 34 us, 93 %; 50k tokens back from E4M3 54 us, 91 %, from BF16 67 us, 97 %; half the
+// elements (d = 64) 18, 19, 30, 36 us.  With a warp for each token and its 2 Hkv vectors instead: 33, 34,
+// 64, 67 us, at d = 64 21, 19, 47, 58, and 8 to 27 us with one head (now 4 to 9).
 // E4M3 caches: scale = least power of two with max|x| <= 448 scale, code = E4M3(x / scale) (the
 // division is exact, one rounding to nearest even), value = code * scale (exact in BF16, whose 8
 // significant bits hold the code's 4; only with scales under 2^-124 do the smallest codes fall
@@ -20,7 +22,6 @@ namespace fa {
 namespace paged {
 
 constexpr int kThreads = 256;
-constexpr int kTokens = 16;   // most tokens per CTA
 
 // Largest magnitude of a vector whose 8-element parts (BF16) are with kLanes neighbouring lanes, as
 // FP32 bits: magnitudes order like unsigned integers (Inf and NaN above the rest), two per operation.
@@ -58,20 +59,30 @@ __device__ __forceinline__ uint4 clamp_top(const uint4& u) {
 
 // Where a CTA's tokens lie in the cache: page (negative: skip the token) and slot.
 struct Places {
-  int page[kTokens], slot[kTokens];
+  int page[kThreads], slot[kThreads];
 };
 
-// k_new, v_new: [T, Hkv, d] with `stride` elements between tokens; `tokens` of them per CTA.
+// D / 8 lanes take 8 elements each of a vector, a warp kVecs vectors at a time, each lane kUnroll
+// of those in flight.
+template <int D>
+struct Deal {
+  static constexpr int kLanes = D / 8;
+  static constexpr int kVecs = 32 / kLanes;
+  static constexpr int kUnroll = 8;
+  static constexpr int kStep = kVecs * (kThreads / 32);   // vectors of the CTA's warps together
+};
+
+// k_new, v_new: [T, Hkv, d] with `stride` elements between tokens; 2^shift of them per CTA, where
+// 2^shift divides Deal::kStep: a thread's vectors are all of one token, K and V of every per_step-th
+// head, whose addresses cost an addition.  (Any deal over the CTA's tokens, as in read_tokens: 37 us.)
 template <int D, bool kFp8>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const Cache c, const __nv_bfloat16* __restrict__ k_new,
                                                              const __nv_bfloat16* __restrict__ v_new,
                                                              long long stride, const int32_t* __restrict__ q_indptr,
-                                                             int T, int tokens) {
-  constexpr int kLanes = D / 8;           // lanes per vector
-  constexpr int kVecs = 32 / kLanes;      // vectors per warp and step
-  constexpr int kUnroll = 8;              // steps in flight
+                                                             int T, int shift) {
+  using L = Deal<D>;
   __shared__ Places at;
-  const int lane = threadIdx.x % 32, first = blockIdx.x * tokens;
+  const int lane = threadIdx.x % 32, tokens = 1 << shift, first = blockIdx.x << shift;
   const int page_size = 1 << c.page_shift;
   if ((int)threadIdx.x < tokens) {
     const int token = first + threadIdx.x;
@@ -85,89 +96,85 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const Cache c, cons
     at.slot[threadIdx.x] = pos & (page_size - 1);
   }
   __syncthreads();
-  const int sub = lane / kLanes, col = (lane % kLanes) * 8;
-  const int n = 2 * c.Hkv;  // vector i: head i / 2, K where i is even
-  for (int t = threadIdx.x / 32; t < tokens; t += kThreads / 32) {
-    const int page = at.page[t], slot = at.slot[t], token = first + t;
-    if (page < 0) continue;
-    for (int i0 = 0; i0 < n; i0 += kVecs * kUnroll) {
-      uint4 x[kUnroll];
+  const int col = (lane % L::kLanes) * 8, v = threadIdx.x / L::kLanes, t = v & (tokens - 1);
+  const int page = at.page[t], slot = at.slot[t], per_step = L::kStep >> shift;
+  const int h_lane = v >> shift, h_warp = (threadIdx.x / 32 * L::kVecs) >> shift;   // the warp's least
+  const long long src = (first + t) * stride + col, dst = page * c.page_stride + (long long)slot * D + col;
+  const long long head = (long long)page_size * D, s_dst = page * c.scale_stride + slot;
+  for (int j0 = 0; j0 + h_warp < c.Hkv; j0 += L::kUnroll / 2 * per_step) {
+    uint4 x[L::kUnroll];
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int i = i0 + u * kVecs + sub;
-        x[u] = make_uint4(0, 0, 0, 0);
-        if (i < n)
-          x[u] = __ldg(reinterpret_cast<const uint4*>(((i & 1) ? v_new : k_new) + token * stride + (i >> 1) * D + col));
-      }
+    for (int u = 0; u < L::kUnroll; ++u) {
+      const int h = j0 + u / 2 * per_step + h_lane;
+      x[u] = make_uint4(0, 0, 0, 0);
+      if (h < c.Hkv && page >= 0) x[u] = __ldg(reinterpret_cast<const uint4*>((u & 1 ? v_new : k_new) + src + h * D));
+    }
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int i = i0 + u * kVecs + sub;
-        if (i0 + u * kVecs >= n) break;  // the same for the whole warp
-        const long long row = (long long)(i >> 1) * page_size + slot;
-        if constexpr (!kFp8) {
-          __nv_bfloat16* base = static_cast<__nv_bfloat16*>((i & 1) ? c.v : c.k);
-          if (i < n) *reinterpret_cast<uint4*>(base + page * c.page_stride + row * D + col) = x[u];
-        } else {
-          const uint32_t amax = vector_amax<kLanes>(x[u]);
-          float scale = 1.f, inv = 1.f;
-          int e = 0;
-          if (amax != 0) {
-            e = scale_exponent(amax);
-            scale = __uint_as_float((uint32_t)(e + 127) << 23);
-            inv = __uint_as_float((uint32_t)(127 - e) << 23);
-          }
-          if (e == kMaxScaleExp) x[u] = clamp_top(x[u]);
-          uint2 q = make_uint2(quant4(x[u].x, x[u].y, inv), quant4(x[u].z, x[u].w, inv));
-          if (amax >= 0x7F800000u) {  // Inf or NaN in the vector
-            scale = __uint_as_float(0x7FC00000u);
-            q = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-          }
-          if (i < n) {
-            uint8_t* base = static_cast<uint8_t*>((i & 1) ? c.v : c.k);
-            *reinterpret_cast<uint2*>(base + page * c.page_stride + row * D + col) = q;
-            if (col == 0) ((i & 1) ? c.v_scale : c.k_scale)[page * c.scale_stride + row] = scale;
-          }
+    for (int u = 0; u < L::kUnroll; ++u) {
+      const int h = j0 + u / 2 * per_step + h_lane;
+      if (j0 + u / 2 * per_step + h_warp >= c.Hkv) break;  // the same for the whole warp
+      const bool mine = h < c.Hkv && page >= 0;
+      if constexpr (!kFp8) {
+        __nv_bfloat16* base = static_cast<__nv_bfloat16*>(u & 1 ? c.v : c.k);
+        if (mine) *reinterpret_cast<uint4*>(base + dst + h * head) = x[u];
+      } else {
+        const uint32_t amax = vector_amax<L::kLanes>(x[u]);
+        float scale = 1.f, inv = 1.f;
+        int e = 0;
+        if (amax != 0) {
+          e = scale_exponent(amax);
+          scale = __uint_as_float((uint32_t)(e + 127) << 23);
+          inv = __uint_as_float((uint32_t)(127 - e) << 23);
+        }
+        if (e == kMaxScaleExp) x[u] = clamp_top(x[u]);
+        uint2 q = make_uint2(quant4(x[u].x, x[u].y, inv), quant4(x[u].z, x[u].w, inv));
+        if (amax >= 0x7F800000u) {  // Inf or NaN in the vector
+          scale = __uint_as_float(0x7FC00000u);
+          q = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+        }
+        if (mine) {
+          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(u & 1 ? c.v : c.k) + dst + h * head) = q;
+          if (col == 0) (u & 1 ? c.v_scale : c.k_scale)[s_dst + (long long)h * page_size] = scale;
         }
       }
     }
   }
 }
 
-// One token's K and V rows of all heads as BF16, by one warp: head h's go to k_out and v_out +
-// h * head_stride.
+// The K and V rows of a CTA's 2^shift tokens as BF16: token t's of head h go to k_out and v_out +
+// t * token_stride + h * head_stride.  Vector v is the one of token v % 2^shift and of head i / 2, K where
+// i = v / 2^shift is even: up to 256 tokens fill the warps' loads however few heads there are.
 template <int D, bool kFp8>
-__device__ __forceinline__ void read_token(const Cache& c, int page, int slot, int lane, __nv_bfloat16* k_out,
-                                           __nv_bfloat16* v_out, long long head_stride) {
+__device__ __forceinline__ void read_tokens(const Cache& c, const Places& at, int shift, __nv_bfloat16* k_out,
+                                            __nv_bfloat16* v_out, long long token_stride, long long head_stride) {
   // 8 elements per lane: a warp's stores then cover whole lines (with 16 codes per lane each 16-byte
   // store left half of its sector to the next one)
-  constexpr int kElems = 8;
-  constexpr int kLanes = D / kElems;
-  constexpr int kVecs = 32 / kLanes;
-  constexpr int kUnroll = 8;
+  using L = Deal<D>;
   constexpr int kBytes = kFp8 ? 1 : 2;
   using Part = std::conditional_t<kFp8, uint2, uint4>;   // a lane's elements in the cache
-  const int sub = lane / kLanes, col = (lane % kLanes) * kElems;
-  const int n = 2 * c.Hkv, page_size = 1 << c.page_shift;
-  for (int i0 = 0; i0 < n; i0 += kVecs * kUnroll) {
-    Part x[kUnroll];
-    float sc[kUnroll];
+  const int lane = threadIdx.x % 32, sub = lane / L::kLanes, col = (lane % L::kLanes) * 8;
+  const int tokens = 1 << shift, all = 2 * c.Hkv << shift, page_size = 1 << c.page_shift;
+  for (int v0 = threadIdx.x / 32 * L::kVecs; v0 < all; v0 += L::kUnroll * L::kStep) {
+    Part x[L::kUnroll];
+    float sc[L::kUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int i = i0 + u * kVecs + sub;
+    for (int u = 0; u < L::kUnroll; ++u) {
+      const int v = v0 + u * L::kStep + sub, t = v & (tokens - 1), i = v >> shift;
+      const int page = v < all ? at.page[t] : -1;
       x[u] = Part{};
       sc[u] = 0.f;
-      if (i < n) {
-        const long long row = (long long)(i >> 1) * page_size + slot;
+      if (page >= 0) {
+        const long long row = (long long)(i >> 1) * page_size + at.slot[t];
         const uint8_t* base = static_cast<const uint8_t*>((i & 1) ? c.v : c.k);
         x[u] = __ldg(reinterpret_cast<const Part*>(base + (page * c.page_stride + row * D + col) * kBytes));
         if constexpr (kFp8) sc[u] = __ldg(((i & 1) ? c.v_scale : c.k_scale) + page * c.scale_stride + row);
       }
     }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int i = i0 + u * kVecs + sub;
-      if (i >= n) break;
-      uint4* dst = reinterpret_cast<uint4*>(((i & 1) ? v_out : k_out) + (i >> 1) * head_stride + col);
+    for (int u = 0; u < L::kUnroll; ++u) {
+      const int v = v0 + u * L::kStep + sub, t = v & (tokens - 1), i = v >> shift;
+      if (v >= all || at.page[t] < 0) continue;
+      uint4* dst = reinterpret_cast<uint4*>(((i & 1) ? v_out : k_out) + t * token_stride + (i >> 1) * head_stride + col);
       if constexpr (!kFp8) {
         *dst = x[u];
       } else {
@@ -185,15 +192,14 @@ __device__ __forceinline__ void read_token(const Cache& c, int page, int slot, i
   }
 }
 
-// k_out, v_out: [rows, Hkv, d] contiguous; `tokens` rows per CTA.
+// k_out, v_out: [rows, Hkv, d] contiguous; 2^shift rows per CTA.
 template <int D, bool kFp8>
 __global__ void __launch_bounds__(kThreads) kv_read_kernel(const Cache c, const int32_t* __restrict__ kv_indptr,
                                                            __nv_bfloat16* __restrict__ k_out,
-                                                           __nv_bfloat16* __restrict__ v_out, int rows, int tokens) {
+                                                           __nv_bfloat16* __restrict__ v_out, int rows, int shift) {
   __shared__ Places at;
-  const int lane = threadIdx.x % 32, first = blockIdx.x * tokens;
-  const int page_size = 1 << c.page_shift;
-  if ((int)threadIdx.x < tokens) {
+  const int first = blockIdx.x << shift;
+  if (threadIdx.x < 1 << shift) {
     const int r = first + threadIdx.x;
     int page = -1, pos = 0;
     const int b = r < rows ? find_sequence(kv_indptr, c.B, r) : -1;
@@ -203,55 +209,62 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const Cache c, const 
       if (pos < __ldg(c.kv_len + b)) page = find_page(c, b, pos, kSitePagedRead);
     }
     at.page[threadIdx.x] = page;
-    at.slot[threadIdx.x] = pos & (page_size - 1);
+    at.slot[threadIdx.x] = pos & ((1 << c.page_shift) - 1);
   }
   __syncthreads();
-  for (int t = threadIdx.x / 32; t < tokens; t += kThreads / 32) {
-    if (at.page[t] < 0) continue;
-    const long long row = (long long)(first + t) * c.Hkv * D;
-    read_token<D, kFp8>(c, at.page[t], at.slot[t], lane, k_out + row, v_out + row, D);
-  }
+  const long long stride = (long long)c.Hkv * D;
+  read_tokens<D, kFp8>(c, at, shift, k_out + first * stride, v_out + first * stride, stride, D);
 }
 
-// The E4M3 keys and values that the chunk kernel's sequences see, as a BF16 cache of its own (p.copy: pages
-// of 128 tokens, a table and a pool in the workspace): a tile would multiply every code by its scale anew.
+// The E4M3 keys and values that the chunk kernel's sequences see, as a BF16 cache of its own (pages of 128
+// tokens, a table and a pool in the workspace): a tile would multiply every code by its scale anew.
 // Sequence b's seen blocks of 128 keys have p.copy_pages pages from b * p.copy_pages on: those that
-// hold sinks, then those from its window on.  A CTA takes 16 tokens, all of one page of either cache.
+// hold sinks, then those from its window on.  A CTA takes 2^shift <= 128 tokens of one of them.
 template <int D>
-__global__ void __launch_bounds__(kThreads) kv_copy_kernel(const Attn p, const Cache to) {
+__global__ void __launch_bounds__(kThreads) kv_copy_kernel(const Attn p, const Cache to, int shift) {
   constexpr int kBlk = 1 << kCopyShift;
-  const int b = blockIdx.x / (kBlk / kTokens) / p.copy_pages, slot = blockIdx.x / (kBlk / kTokens) - b * p.copy_pages;
+  __shared__ Places at;
+  const int parts = kBlk >> shift, b = blockIdx.x / parts / p.copy_pages, slot = blockIdx.x / parts - b * p.copy_pages;
   const Seq s = load_seq(p, b);
   if (s.n == 0 || s.n * p.group <= p.few_rows) return;
   const KeyWalk<kBlk> walk(p, s.pos0, s.kv - 1);
   const int n_sink = (walk.sinks + kBlk - 1) / kBlk;
   const int i = slot < n_sink ? slot : max(walk.b_lo, n_sink) + slot - n_sink;
-  const int part = blockIdx.x % (kBlk / kTokens) * kTokens, key = i * kBlk + part;
+  const int part = (blockIdx.x % parts) << shift, first = i * kBlk + part;
   if (i >= to.max_pages) return;
   const int page_to = b * p.copy_pages + slot;
   if (part == 0 && threadIdx.x == 0) const_cast<int32_t*>(to.table)[b * to.table_stride + i] = page_to;
-  if (!walk.any(key, kTokens)) return;
-  const int page = find_page(p.c, b, key, kSitePagedPage);
-  if (page < 0) return;
-  const int from = key & ((1 << p.c.page_shift) - 1);
-  for (int t = threadIdx.x / 32; t < kTokens && key + t < walk.hi; t += kThreads / 32) {
-    const long long row = page_to * to.page_stride + (long long)(part + t) * D;
-    read_token<D, true>(p.c, page, from + t, threadIdx.x % 32, static_cast<__nv_bfloat16*>(to.k) + row,
-                        static_cast<__nv_bfloat16*>(to.v) + row, (long long)kBlk * D);
+  if (!walk.any(first, 1 << shift)) return;
+  if (threadIdx.x < 1 << shift) {
+    const int key = first + threadIdx.x;
+    at.page[threadIdx.x] = walk.seen(key) ? find_page(p.c, b, key, kSitePagedPage) : -1;
+    at.slot[threadIdx.x] = key & ((1 << p.c.page_shift) - 1);
   }
+  __syncthreads();
+  const long long row = page_to * to.page_stride + (long long)part * D;
+  read_tokens<D, true>(p.c, at, shift, static_cast<__nv_bfloat16*>(to.k) + row, static_cast<__nv_bfloat16*>(to.v) + row, D,
+                       (long long)kBlk * D);
+}
+
+// log2 of the tokens of a CTA: as many as give it 32768 elements (two steps of eight loads for each
+// lane), a lookup per thread at most; fewer, but not under 8, where that leaves SMs without a CTA.
+static int tokens_shift(int Hkv, int d, long long rows) {
+  int shift = 8;
+  while (shift > 0 && (2ll * Hkv * d << shift) > 32768) --shift;
+  while (shift > 3 && rows < (long long)sm_count() << shift) --shift;
+  return shift;
 }
 
 int launch_copy(const Attn& p, const Cache& to, int d, cudaStream_t s) {
-  const unsigned grid = (unsigned)p.copy_pages * p.c.B * ((1 << kCopyShift) / kTokens);
+  const int tokens = tokens_shift(p.c.Hkv, d, (long long)p.copy_pages * p.c.B << kCopyShift);
+  const int shift = tokens < kCopyShift ? tokens : kCopyShift;
+  const unsigned grid = (unsigned)p.copy_pages * p.c.B << (kCopyShift - shift);
   if (d == 64)
-    kv_copy_kernel<64><<<grid, kThreads, 0, s>>>(p, to);
+    kv_copy_kernel<64><<<grid, kThreads, 0, s>>>(p, to, shift);
   else
-    kv_copy_kernel<128><<<grid, kThreads, 0, s>>>(p, to);
+    kv_copy_kernel<128><<<grid, kThreads, 0, s>>>(p, to, shift);
   return check_cuda(cudaGetLastError(), "launch kv_copy_kernel");
 }
-
-// Tokens per CTA: 16, or 8 (one for each warp) where that leaves SMs without a CTA.
-static int tokens_per_cta(int rows) { return rows > sm_count() * kTokens ? kTokens : kThreads / 32; }
 
 int check_cache(const fa_paged_kv* kv, Cache* c) {
   if (!kv) return set_error(FA_ERR_INVALID_ARG, "kv is NULL");
@@ -322,14 +335,15 @@ extern "C" int fa_kv_append(const fa_paged_kv* kv, const void* k_new, const void
   if (T == 0) return FA_OK;
   c.status = device_status_word();
   if (!c.status) return set_error(FA_ERR_CUDA, "could not allocate the device status record");
-  const int tokens = paged::tokens_per_cta(T);
-  const unsigned grid = (unsigned)(((long long)T + tokens - 1) / tokens);
+  const int most = kv->d == 64 ? 5 : 4, wanted = paged::tokens_shift(kv->Hkv, kv->d, T);   // kStep tokens
+  const int shift = wanted < most ? wanted : most;
+  const unsigned grid = (unsigned)((((long long)T - 1) >> shift) + 1);
   const __nv_bfloat16 *k = static_cast<const __nv_bfloat16*>(k_new), *v = static_cast<const __nv_bfloat16*>(v_new);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool fp8 = kv->dtype == FA_KV_E4M3;
   auto kern = kv->d == 64 ? (fp8 ? paged::kv_append_kernel<64, true> : paged::kv_append_kernel<64, false>)
                           : (fp8 ? paged::kv_append_kernel<128, true> : paged::kv_append_kernel<128, false>);
-  kern<<<grid, paged::kThreads, 0, s>>>(c, k, v, new_stride, q_indptr, T, tokens);
+  kern<<<grid, paged::kThreads, 0, s>>>(c, k, v, new_stride, q_indptr, T, shift);
   return check_cuda(cudaGetLastError(), "launch fa_kv_append");
 }
 
@@ -348,13 +362,13 @@ extern "C" int fa_kv_read(const fa_paged_kv* kv, const int32_t* kv_indptr, void*
   if (rows == 0) return FA_OK;
   c.status = device_status_word();
   if (!c.status) return set_error(FA_ERR_CUDA, "could not allocate the device status record");
-  const int tokens = paged::tokens_per_cta(rows);
-  const unsigned grid = (unsigned)(((long long)rows + tokens - 1) / tokens);
+  const int shift = paged::tokens_shift(kv->Hkv, kv->d, rows);
+  const unsigned grid = (unsigned)((((long long)rows - 1) >> shift) + 1);
   __nv_bfloat16 *k = static_cast<__nv_bfloat16*>(k_out), *v = static_cast<__nv_bfloat16*>(v_out);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool fp8 = kv->dtype == FA_KV_E4M3;
   auto kern = kv->d == 64 ? (fp8 ? paged::kv_read_kernel<64, true> : paged::kv_read_kernel<64, false>)
                           : (fp8 ? paged::kv_read_kernel<128, true> : paged::kv_read_kernel<128, false>);
-  kern<<<grid, paged::kThreads, 0, s>>>(c, kv_indptr, k, v, rows, tokens);
+  kern<<<grid, paged::kThreads, 0, s>>>(c, kv_indptr, k, v, rows, shift);
   return check_cuda(cudaGetLastError(), "launch fa_kv_read");
 }

@@ -163,3 +163,25 @@ def test_bad_entries_are_reported_and_skipped(fmt):
                             k_scale=c.ks, v_scale=c.vs, out=out)
             rc = binding.fa_device_report_read()[0]
             assert rc == (binding.FA_OK if what == "length" else binding.FA_ERR_DEVICE_BOUNDS)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hkv,d,page,lens", [(1, 64, 16, [39000, 1, 333]), (1, 128, 64, [20000, 4999]), (2, 64, 256, [10000]),
+                                             (3, 128, 32, [2500, 77]), (40, 128, 16, [35, 2]), (130, 128, 16, [19]),
+                                             (200, 64, 32, [3, 9])])
+def test_append_and_read_back_at_any_number_of_heads(fmt, hkv, d, page, lens):
+    # the tokens of a CTA depend on the heads and on the rows: 1 to 256
+    c = P.make(lens, hkv, d, page, fmt, seed=3)
+    T = sum(lens)
+    g = torch.Generator().manual_seed(T)
+    x = (torch.randn((2, T, hkv, d), generator=g) * torch.exp2(torch.randint(-9, 9, (2, T, hkv, 1), generator=g).float())).to(torch.bfloat16)
+    k, v = x.cuda()
+    ip = P.indptr(lens)
+    binding.kv_append(k, v, c.k, c.v, c.table, c.kv_len, ip, k_scale=c.ks, v_scale=c.vs)
+    got = binding.kv_read(c.k, c.v, c.table, c.kv_len, ip, T, k_scale=c.ks, v_scale=c.vs)
+    binding.device_status()
+    for a, b in zip(got, x):
+        if fmt == "e4m3":
+            codes, s = P.quantize(b)
+            b = (codes.view(P.E4M3).double() * s.double()[..., None]).to(torch.bfloat16)   # exact
+        assert torch.equal(a.cpu(), b)
