@@ -894,18 +894,20 @@ struct Plan {
 
 // Whether an E4M3 cache is copied to BF16 pages before the chunk kernel runs.  Else each tile of 256 rows
 // multiplies the codes of all its keys by their scales, which takes longer than its products: 2048
-// tokens (4 heads of a group, d = 128) over 16k keys 684 us, with the copy 428 (22 of them the copy's);
-// over 60k 2233 and 1344.  The copy costs a launch and three times a key's bytes in memory traffic: 128
-// tokens (two tiles per kv head) over 16k keys 73 us without, 78 with it; 512 tokens (eight tiles) 199
-// and 146; 16 sequences of some 200 tokens (three tiles each) 142 and 151.  So: where a copied key is
-// read by six tiles on average, of a copy of at most 2 GiB.
-bool copy_pays(int T, int B, int group, int max_q, int Hkv, int d, int max_kv, int window, long long pages) {
-  constexpr long long kTiles = 6, kMostBytes = 1ll << 31;
+// tokens (4 heads of a group, d = 128) over 16k keys 684 us, with the copy 428 (21 of them the copy's);
+// over 60k 2233 and 1344.  The copy costs a launch and three times a key's bytes in memory traffic: over
+// 16k keys 128 tokens (two tiles per kv head) take 72 us without, 77 with it, 200 tokens (three tiles)
+// 109 and 98, 512 (eight) 199 and 146; 12 sequences, one of them with most of 828 tokens (7 heads of a
+// group, d = 64), window 2000, 41 and 35; 16 sequences of some 75 tokens 142 and 151.  So: where 2.5 tiles or
+// more read a copied key, with the mean sequence taken as half the longest one, of a copy of at most
+// 2 GiB.
+bool copy_pays(int T, int B, int group, int Hkv, int d, int max_kv, int window, long long pages) {
+  constexpr long long kMostBytes = 1ll << 31;
   if (4 * pages * B * Hkv * d > kMostBytes >> fa::paged::kCopyShift) return false;
-  const long long tiles = (long long)T * group / (2 * fa::paged::kM);
-  const long long by_tile = window ? std::min<long long>(max_kv, window) : max_kv;                 // keys of a tile
-  const long long by_sequence = window ? std::min<long long>(max_kv, (long long)window + max_q) : max_kv;
-  return tiles * by_tile >= kTiles * B * by_sequence;
+  const double tiles = (double)T * group / (2 * fa::paged::kM);
+  const double by_tile = window ? window : max_kv;                              // keys
+  const double copied = (B + 1) / 2.0 * by_tile + (window ? T : 0);             // of all sequences
+  return tiles * by_tile >= 2.5 * copied;
 }
 
 Plan make_plan(int T, int B, int max_q, int group, int Hkv, int d, int max_kv, int window, int sinks, int dtype) {
@@ -949,7 +951,7 @@ Plan make_plan(int T, int B, int max_q, int group, int Hkv, int d, int max_kv, i
       const long long seen = (sinks + kBlk - 1) / kBlk + ((long long)window + max_q) / kBlk + 2;
       if (seen < pages) pages = seen;
     }
-    if (copy_pays(T, B, group, max_q, Hkv, d, max_kv, window, pages)) pl.copy_pages = (int)pages;
+    if (copy_pays(T, B, group, Hkv, d, max_kv, window, pages)) pl.copy_pages = (int)pages;
   }
   return pl;
 }
