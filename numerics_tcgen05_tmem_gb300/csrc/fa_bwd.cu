@@ -138,18 +138,17 @@ struct Params {
 // --------------------------------------------------------------------------- preprocess
 // Over the padded rows (bh, q < N_pad): delta = rowsum(dO o O) in FP32, lse2 = lse log2(e)
 // and dQ_acc = 0 for q < N; delta = 0 and lse2 = +inf (so P = 0) for the padding.
-// d/8 lanes per row, 16-byte loads.
+// d/8 lanes per row, 16-byte loads.  The delta of rows q < few is delta_few's, below.
 template <int D>
-__global__ void __launch_bounds__(256) fa_bwd_preprocess(const __nv_bfloat16* __restrict__ o,
-                                                         const __nv_bfloat16* __restrict__ dO,
-                                                         const float* __restrict__ lse, float* __restrict__ delta,
-                                                         float* __restrict__ lse2, float* __restrict__ delta_out,
-                                                         float* __restrict__ dq_acc, long long rows_pad, int N,
-                                                         int N_pad) {
+__device__ __forceinline__ void preprocess_rows(const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* __restrict__ dO,
+                                                const float* __restrict__ lse, float* __restrict__ delta,
+                                                float* __restrict__ lse2, float* __restrict__ delta_out,
+                                                float* __restrict__ dq_acc, long long rows_pad, int N, int N_pad, int block,
+                                                int few) {
   constexpr int kLanesPerRow = D / 8;
   constexpr int kRowsPerWarp = 32 / kLanesPerRow;
   const int lane = threadIdx.x % 32;
-  const long long warp_global = (long long)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
+  const long long warp_global = (long long)block * (blockDim.x / 32) + threadIdx.x / 32;
   const long long prow = warp_global * kRowsPerWarp + lane / kLanesPerRow;
   const long long bh = prow / N_pad;
   const int q = (int)(prow - bh * N_pad);
@@ -176,10 +175,21 @@ __global__ void __launch_bounds__(256) fa_bwd_preprocess(const __nv_bfloat16* __
 #pragma unroll
   for (int off = kLanesPerRow / 2; off > 0; off /= 2) acc += __shfl_xor_sync(0xffffffffu, acc, off);
   if (prow < rows_pad && (lane % kLanesPerRow) == 0) {
-    delta[prow] = acc;
+    const bool mine = !valid || q >= few;
+    if (mine) delta[prow] = acc;
     lse2[prow] = valid ? lse[row] * 1.4426950408889634f : INFINITY;
-    if (valid && delta_out) delta_out[row] = acc;
+    if (valid && mine && delta_out) delta_out[row] = acc;
   }
+}
+
+template <int D>
+__global__ void __launch_bounds__(256) fa_bwd_preprocess(const __nv_bfloat16* __restrict__ o,
+                                                         const __nv_bfloat16* __restrict__ dO,
+                                                         const float* __restrict__ lse, float* __restrict__ delta,
+                                                         float* __restrict__ lse2, float* __restrict__ delta_out,
+                                                         float* __restrict__ dq_acc, long long rows_pad, int N,
+                                                         int N_pad) {
+  preprocess_rows<D>(o, dO, lse, delta, lse2, delta_out, dq_acc, rows_pad, N, N_pad, blockIdx.x, 0);
 }
 
 // --------------------------------------------------------------------------- delta of few keys
@@ -189,22 +199,19 @@ __global__ void __launch_bounds__(256) fa_bwd_preprocess(const __nv_bfloat16* __
 // with few keys nothing averages the error out: with 2 visible keys dq and dk were 0.6-1.0 % off
 // (relative Frobenius), 0.37 % from 16 keys on, where the BF16 rounding of dS and of the result alone
 // makes 0.24 %.  Row i sees at most kFewKeys keys if i < kFewKeys or window + sinks <= kFewKeys, so
-// `rows` rows of each head are recomputed: the first kFewKeys, or all of them.  (Inside
-// fa_bwd_preprocess the code slowed every row down: 37 -> 57 us at 32 heads, 8k rows.)
+// `rows` rows of each head are recomputed: the first kFewKeys, or all of them.
 constexpr int kFewKeys = 16;
 
 template <int D>
-__global__ void __launch_bounds__(256) fa_bwd_delta_few(const __nv_bfloat16* __restrict__ q,
-                                                        const __nv_bfloat16* __restrict__ k,
-                                                        const __nv_bfloat16* __restrict__ v,
-                                                        const __nv_bfloat16* __restrict__ dO,
-                                                        const float* __restrict__ lse, float* __restrict__ delta,
-                                                        float* __restrict__ delta_out, int BH, int rows, int N, int N_pad,
-                                                        int window, int sinks, float scale_log2) {
+__device__ __forceinline__ void delta_few(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ k,
+                                          const __nv_bfloat16* __restrict__ v, const __nv_bfloat16* __restrict__ dO,
+                                          const float* __restrict__ lse, float* __restrict__ delta,
+                                          float* __restrict__ delta_out, int BH, int rows, int N, int N_pad, int window,
+                                          int sinks, float scale_log2, int block) {
   constexpr int kLanesPerRow = D / 8;
   constexpr int kRowsPerWarp = 32 / kLanesPerRow;
   const int lane = threadIdx.x % 32;
-  const long long warp_global = (long long)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
+  const long long warp_global = (long long)block * (blockDim.x / 32) + threadIdx.x / 32;
   const long long n = warp_global * kRowsPerWarp + lane / kLanesPerRow;
   const long long bh = n / rows;
   const int i = (int)(n - bh * rows);
@@ -264,6 +271,36 @@ __global__ void __launch_bounds__(256) fa_bwd_delta_few(const __nv_bfloat16* __r
     delta[bh * N_pad + i] = sum;
     if (delta_out) delta_out[row] = sum;
   }
+}
+
+// After fa_bwd_preprocess, whose deltas of these rows it replaces.  (In the same threads, one row after
+// the other, the preprocessing takes 57 us instead of 37 + 6 at 32 heads of 8k rows, d = 128.)
+template <int D>
+__global__ void __launch_bounds__(256) fa_bwd_delta_few(const __nv_bfloat16* __restrict__ q,
+                                                        const __nv_bfloat16* __restrict__ k,
+                                                        const __nv_bfloat16* __restrict__ v,
+                                                        const __nv_bfloat16* __restrict__ dO,
+                                                        const float* __restrict__ lse, float* __restrict__ delta,
+                                                        float* __restrict__ delta_out, int BH, int rows, int N, int N_pad,
+                                                        int window, int sinks, float scale_log2) {
+  delta_few<D>(q, k, v, dO, lse, delta, delta_out, BH, rows, N, N_pad, window, sinks, scale_log2, blockIdx.x);
+}
+
+// Both in one launch for small problems: the blocks from few_blocks on are fa_bwd_preprocess's, the first
+// ones, whose loads wait for one another longest, fa_bwd_delta_few's.  6 heads of 65 rows: 3.8 us, in
+// two launches 1.8 + 3.7 and the host's 4 us for the second one; but every block has the registers of the
+// larger part, and 32 heads of 8k rows take 64 us instead of 37 + 6.
+template <int D>
+__global__ void __launch_bounds__(256) fa_bwd_preprocess_window(
+    const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
+    const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* __restrict__ dO, const float* __restrict__ lse,
+    float* __restrict__ delta, float* __restrict__ lse2, float* __restrict__ delta_out, float* __restrict__ dq_acc, int BH,
+    int few, int few_blocks, int N, int N_pad, int window, int sinks, float scale_log2) {
+  if ((int)blockIdx.x < few_blocks)
+    delta_few<D>(q, k, v, dO, lse, delta, delta_out, BH, few, N, N_pad, window, sinks, scale_log2, blockIdx.x);
+  else
+    preprocess_rows<D>(o, dO, lse, delta, lse2, delta_out, dq_acc, (long long)BH * N_pad, N, N_pad, blockIdx.x - few_blocks,
+                       few);
 }
 
 // --------------------------------------------------------------------------- dQ convert
@@ -960,19 +997,31 @@ int launch_bwd(const void* q, const void* k, const void* v, const void* o, const
     constexpr int rows_per_block = 8 * (32 / (D / 8));
     const long long rows_pad = (long long)B * H * N_pad;
     const long long grid = (rows_pad + rows_per_block - 1) / rows_per_block;
-    bwd::fa_bwd_preprocess<D><<<(unsigned)grid, 256, 0, stream>>>(
-        static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(dO), lse, sc.delta, sc.lse2,
-        delta_out, sc.dq_acc, rows_pad, N, N_pad);
-    if ((rc = check_cuda(cudaGetLastError(), "launch fa_bwd_preprocess"))) return rc;
+    const auto *bo = static_cast<const __nv_bfloat16*>(o), *bdo = static_cast<const __nv_bfloat16*>(dO);
     if (window) {
       const int w = window < N ? window : N, sk = sinks < N ? sinks : N;
       const int few = (w <= bwd::kFewKeys && sk <= bwd::kFewKeys - w) || N < bwd::kFewKeys ? N : bwd::kFewKeys;
-      const long long few_rows = (long long)B * H * few;
-      bwd::fa_bwd_delta_few<D><<<(unsigned)((few_rows + rows_per_block - 1) / rows_per_block), 256, 0, stream>>>(
-          static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v),
-          static_cast<const __nv_bfloat16*>(dO), lse, sc.delta, delta_out, B * H, few, N, N_pad, w, sk,
-          scale * 1.4426950408889634f);
-      if ((rc = check_cuda(cudaGetLastError(), "launch fa_bwd_delta_few"))) return rc;
+      const long long few_blocks = ((long long)B * H * few + rows_per_block - 1) / rows_per_block;
+      const auto *bq = static_cast<const __nv_bfloat16*>(q), *bk = static_cast<const __nv_bfloat16*>(k),
+                 *bv = static_cast<const __nv_bfloat16*>(v);
+      const float scale_log2 = scale * 1.4426950408889634f;
+      if (few_blocks + grid <= 3 * sm_count()) {   // all at once: 3 of 256 threads and 80 registers per SM
+        bwd::fa_bwd_preprocess_window<D><<<(unsigned)(few_blocks + grid), 256, 0, stream>>>(
+            bq, bk, bv, bo, bdo, lse, sc.delta, sc.lse2, delta_out, sc.dq_acc, B * H, few, (int)few_blocks, N, N_pad, w, sk,
+            scale_log2);
+        if ((rc = check_cuda(cudaGetLastError(), "launch fa_bwd_preprocess_window"))) return rc;
+      } else {
+        bwd::fa_bwd_preprocess<D><<<(unsigned)grid, 256, 0, stream>>>(bo, bdo, lse, sc.delta, sc.lse2, delta_out, sc.dq_acc,
+                                                                    rows_pad, N, N_pad);
+        if ((rc = check_cuda(cudaGetLastError(), "launch fa_bwd_preprocess"))) return rc;
+        bwd::fa_bwd_delta_few<D><<<(unsigned)few_blocks, 256, 0, stream>>>(bq, bk, bv, bdo, lse, sc.delta, delta_out, B * H,
+                                                                         few, N, N_pad, w, sk, scale_log2);
+        if ((rc = check_cuda(cudaGetLastError(), "launch fa_bwd_delta_few"))) return rc;
+      }
+    } else {
+      bwd::fa_bwd_preprocess<D><<<(unsigned)grid, 256, 0, stream>>>(bo, bdo, lse, sc.delta, sc.lse2, delta_out, sc.dq_acc,
+                                                                  rows_pad, N, N_pad);
+      if ((rc = check_cuda(cudaGetLastError(), "launch fa_bwd_preprocess"))) return rc;
     }
   }
   if (stages & FA_BWD_MAIN) {
