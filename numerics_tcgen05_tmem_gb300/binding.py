@@ -499,6 +499,9 @@ def forward_paged(q, k_cache, v_cache, block_table, kv_len, q_indptr, max_q, k_s
     p - window < j <= p and the first ``sinks`` keys; otherwise every key j <= p.
     out, lse: tensors to write to ([T, Hq, d] bfloat16, [T, Hq] float32); rows behind the last
     sequence stay as they were (undefined in fresh tensors).
+    workspace: fa_fwd_paged_workspace_size bytes, for calls that do not overlap; else allocated.  For
+    long chunks over an E4M3 cache it holds a BF16 copy of what they see (2 GiB at most, from the
+    block table's width).
     """
     kv = _paged(k_cache, v_cache, block_table, kv_len, k_scale, v_scale)
     if window is None:

@@ -5,8 +5,8 @@
 // The threads of a CTA look its tokens up, one each (sequence, page, slot: four loads that wait for one
 // another), then its warps walk the tokens' vectors, eight loads of each lane in flight, so dealt
 // that neighbouring lanes take neighbouring slots of one head, which follow one another in the cache, as do
-// their scales.  27k tokens of 8 heads, d = 128: into E4M3 30 us, 80 % of the measured copy rate,
-// into BF16 34 us, 93 %; 50k tokens back from E4M3 54 us, 91 %, from BF16 67 us, 97 %; half the
+// their scales.  26k tokens of 8 heads, d = 128: into E4M3 30 us, 80 % of the measured copy rate,
+// into BF16 34 us, 93 %; 53k tokens back from E4M3 54 us, 91 %, from BF16 67 us, 97 %; half the
 // elements (d = 64) 18, 19, 30, 36 us.  With a warp for each token and its 2 Hkv vectors instead: 33, 34,
 // 64, 67 us, at d = 64 21, 19, 47, 58, and 8 to 27 us with one head (now 4 to 9).
 // E4M3 caches: scale = least power of two with max|x| <= 448 scale, code = E4M3(x / scale) (the
