@@ -450,3 +450,17 @@ def test_one_tile_of_rows_over_any_number_of_blocks(fmt, d, kv):
         c = P.make([kv], 2, d, 32, fmt, seed=kv + new)
         check(c, [new], group)
         check(c, [new], group, window=150, sinks=5)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new", [[1, 1, 1], [70, 3, 200], [300, 280, 290]])
+def test_sequences_that_share_pages(fmt, new):
+    # a common prefix held once: the sequences' tables name the same pages
+    page, lens = 32, [600, 500, 310]
+    c = P.make(lens, 2, 64, page, fmt, seed=9)
+    for b in (1, 2):
+        c.table[b, :9] = c.table[0, :9]
+        for w in range(2):
+            c.values[b][w][:, :9 * page] = c.values[0][w][:, :9 * page]
+    for kw in ({}, dict(window=260, sinks=40)):
+        check(c, new, 8, **kw)
