@@ -161,21 +161,43 @@ def _empty(shape, dtype, like, stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-class _OnDevice:
-    """Makes a tensor's device current for a call, where it is not already."""
+def _empty_like(t, stream):
+    """_empty with a contiguous tensor's shape and type (PyTorch makes it in four fifths of the time)."""
+    if stream is None:
+        return torch.empty_like(t)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(t)
 
-    def __init__(self, t):
-        self.dev, self.back = t.get_device(), None
 
+class _Here:
     def __enter__(self):
-        now = torch._C._cuda_getDevice()
-        if now != self.dev:
-            torch.cuda.set_device(self.dev)
-            self.back = now
+        pass
 
     def __exit__(self, *exc):
-        if self.back is not None:
-            torch.cuda.set_device(self.back)
+        pass
+
+
+class _OnDevice:
+    """Makes a device current for a call."""
+
+    def __init__(self, dev):
+        self.dev = dev
+
+    def __enter__(self):
+        self.back = torch._C._cuda_getDevice()
+        torch.cuda.set_device(self.dev)
+
+    def __exit__(self, *exc):
+        torch.cuda.set_device(self.back)
+
+
+_HERE = _Here()
+
+
+def _on_device(t):
+    """A context in which a tensor's device is current; nothing to do where it is already."""
+    dev = t.get_device()
+    return _HERE if torch._C._cuda_getDevice() == dev else _OnDevice(dev)
 
 
 def _check_qkv(*ts):
@@ -314,10 +336,10 @@ def forward(q, k, v, causal: bool = True, scale=None, stable: int = 1, beta: flo
     _check_window(causal, window, sinks)
     B, H, N, d = q.shape
     scale = 1.0 / math.sqrt(d) if scale is None else scale
-    o = _empty(q.shape, q.dtype, q, stream)
+    o = _empty_like(q, stream)
     lse = _empty((B, H, N), torch.float32, q, stream)
     sd = _stats_dict(B, H, N, q.device) if stats else None
-    with _OnDevice(q):
+    with _on_device(q):
         if window is None:
             _check(fa_fwd(q, k, v, o, lse, causal, scale, stable, beta, sd, stream))
         else:
@@ -369,9 +391,9 @@ def backward(q, k, v, o, lse, do, causal: bool = True, scale=None, workspace=Non
         size = fa_bwd_workspace_size(B, H, N, d) if window is None else \
             fa_bwd_window_workspace_size(B, H, N, d, window, sinks)
         workspace = _empty(size, torch.uint8, q, stream)
-    dq, dk, dv = (_empty(q.shape, q.dtype, q, stream) for _ in range(3))
+    dq, dk, dv = _empty_like(q, stream), _empty_like(q, stream), _empty_like(q, stream)
     delta = _empty((B, H, N), torch.float32, q, stream) if want_delta else None
-    with _OnDevice(q):
+    with _on_device(q):
         if window is None:
             _check(fa_bwd(q, k, v, o, lse, do, dq, dk, dv, delta, causal, scale, workspace, stream))
         else:
@@ -459,7 +481,7 @@ def kv_append(k_new, v_new, k_cache, v_cache, block_table, kv_len, q_indptr, k_s
         raise ValueError("k_new and v_new must have the same rows and row stride")
     indptr = _int32(q_indptr, kv.B + 1, "q_indptr", dev)
     if T:
-        with _OnDevice(k_cache):
+        with _on_device(k_cache):
             _check(load().fa_kv_append(ctypes.byref(kv), k_new.data_ptr(), v_new.data_ptr(), stride, indptr, T,
                                        _stream(stream)))
 
@@ -476,14 +498,14 @@ def kv_read(k_cache, v_cache, block_table, kv_len, kv_indptr, rows, k_scale=None
     indptr = _int32(kv_indptr, kv.B + 1, "kv_indptr", dev)
     if out is None:
         k = _empty(shape, torch.bfloat16, k_cache, stream)
-        v = _empty(shape, torch.bfloat16, k_cache, stream)
+        v = _empty_like(k, stream)
     else:
         k, v = out
         for t in out:
             if _check_rows(t, kv.Hkv, kv.d, dev, "out")[0] != rows or not t.is_contiguous():
                 raise ValueError("out tensors must be contiguous with `rows` rows")
     if rows:
-        with _OnDevice(k_cache):
+        with _on_device(k_cache):
             _check(load().fa_kv_read(ctypes.byref(kv), indptr, k.data_ptr(), v.data_ptr(), int(rows), _stream(stream)))
     return k, v
 
@@ -517,7 +539,7 @@ def forward_paged(q, k_cache, v_cache, block_table, kv_len, q_indptr, max_q, k_s
     T, stride = _check_rows(q, Hq, d, dev, "q")
     indptr = _int32(q_indptr, kv.B + 1, "q_indptr", dev)
     if out is None:
-        out = _empty((T, Hq, d), torch.bfloat16, q, stream)
+        out = _empty_like(q, stream) if stride == Hq * d else _empty((T, Hq, d), torch.bfloat16, q, stream)
     elif out.dtype is not torch.bfloat16 or out.shape != q.shape or not out.is_contiguous() or out.get_device() != dev:
         raise ValueError("out must be a contiguous bfloat16 tensor of q's shape")
     if lse is None:
@@ -535,7 +557,7 @@ def forward_paged(q, k_cache, v_cache, block_table, kv_len, q_indptr, max_q, k_s
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the cache's device")
     ws, nbytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
-    with _OnDevice(k_cache):
+    with _on_device(k_cache):
         _check(lib.fa_fwd_paged(ctypes.byref(kv), q.data_ptr(), stride, indptr, T, int(max_q), Hq, out.data_ptr(),
                                 lse.data_ptr(), window, int(sinks), 1.0 / math.sqrt(d) if scale is None else float(scale),
                                 ws, nbytes, _stream(stream)))
