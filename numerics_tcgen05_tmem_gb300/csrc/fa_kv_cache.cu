@@ -219,31 +219,36 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const Cache c, const 
 // The E4M3 keys and values that the chunk kernel's sequences see, as a BF16 cache of its own (pages of 128
 // tokens, a table and a pool in the workspace): a tile would multiply every code by its scale anew.
 // Sequence b's seen blocks of 128 keys have p.copy_pages pages from b * p.copy_pages on: those that
-// hold sinks, then those from its window on.  A CTA takes 2^shift <= 128 tokens of one of them.
+// hold sinks, then those from its window on.  per_seq CTAs share them, 2^shift <= 128 tokens of a page at
+// a time: their number follows the sequences, not the table's width, whose unused part costs nothing.
 template <int D>
-__global__ void __launch_bounds__(kThreads) kv_copy_kernel(const Attn p, const Cache to, int shift) {
+__global__ void __launch_bounds__(kThreads) kv_copy_kernel(const Attn p, const Cache to, int shift, int per_seq) {
   constexpr int kBlk = 1 << kCopyShift;
   __shared__ Places at;
-  const int parts = kBlk >> shift, b = blockIdx.x / parts / p.copy_pages, slot = blockIdx.x / parts - b * p.copy_pages;
+  const int b = blockIdx.x / per_seq, parts = kBlk >> shift;
   const Seq s = load_seq(p, b);
   if (s.n == 0 || s.n * p.group <= p.few_rows) return;
   const KeyWalk<kBlk> walk(p, s.pos0, s.kv - 1);
-  const int n_sink = (walk.sinks + kBlk - 1) / kBlk;
-  const int i = slot < n_sink ? slot : max(walk.b_lo, n_sink) + slot - n_sink;
-  const int part = (blockIdx.x % parts) << shift, first = i * kBlk + part;
-  if (i >= to.max_pages) return;
-  const int page_to = b * p.copy_pages + slot;
-  if (part == 0 && threadIdx.x == 0) const_cast<int32_t*>(to.table)[b * to.table_stride + i] = page_to;
-  if (!walk.any(first, 1 << shift)) return;
-  if (threadIdx.x < 1 << shift) {
-    const int key = first + threadIdx.x;
-    at.page[threadIdx.x] = walk.seen(key) ? find_page(p.c, b, key, kSitePagedPage) : -1;
-    at.slot[threadIdx.x] = key & ((1 << p.c.page_shift) - 1);
+  const int n_sink = (walk.sinks + kBlk - 1) / kBlk, from = max(walk.b_lo, n_sink);
+  const int pages = min(n_sink + max((walk.hi + kBlk - 1) / kBlk - from, 0), p.copy_pages);
+  for (int x = blockIdx.x - b * per_seq; x < pages * parts; x += per_seq) {
+    const int slot = x / parts, i = slot < n_sink ? slot : from + slot - n_sink;
+    const int part = (x - slot * parts) << shift, first = i * kBlk + part;
+    if (i >= to.max_pages) return;
+    const int page_to = b * p.copy_pages + slot;
+    if (part == 0 && threadIdx.x == 0) const_cast<int32_t*>(to.table)[b * to.table_stride + i] = page_to;
+    if (!walk.any(first, 1 << shift)) continue;
+    __syncthreads();   // the last part's places have been read
+    if (threadIdx.x < 1 << shift) {
+      const int key = first + threadIdx.x;
+      at.page[threadIdx.x] = walk.seen(key) ? find_page(p.c, b, key, kSitePagedPage) : -1;
+      at.slot[threadIdx.x] = key & ((1 << p.c.page_shift) - 1);
+    }
+    __syncthreads();
+    const long long row = page_to * to.page_stride + (long long)part * D;
+    read_tokens<D, true>(p.c, at, shift, static_cast<__nv_bfloat16*>(to.k) + row, static_cast<__nv_bfloat16*>(to.v) + row, D,
+                         (long long)kBlk * D);
   }
-  __syncthreads();
-  const long long row = page_to * to.page_stride + (long long)part * D;
-  read_tokens<D, true>(p.c, at, shift, static_cast<__nv_bfloat16*>(to.k) + row, static_cast<__nv_bfloat16*>(to.v) + row, D,
-                       (long long)kBlk * D);
 }
 
 // log2 of the tokens of a CTA: as many as give it 32768 elements (two steps of eight loads for each
@@ -258,11 +263,15 @@ static int tokens_shift(int Hkv, int d, long long rows) {
 int launch_copy(const Attn& p, const Cache& to, int d, cudaStream_t s) {
   const int tokens = tokens_shift(p.c.Hkv, d, (long long)p.copy_pages * p.c.B << kCopyShift);
   const int shift = tokens < kCopyShift ? tokens : kCopyShift;
-  const unsigned grid = (unsigned)p.copy_pages * p.c.B << (kCopyShift - shift);
+  // eight CTAs per SM over all sequences, but 64 for each, one of which may hold most keys
+  const long long most = (long long)p.copy_pages << (kCopyShift - shift);
+  const long long share = (8ll * sm_count() + p.c.B - 1) / p.c.B, wanted = share > 64 ? share : 64;
+  const int per_seq = (int)(wanted < most ? wanted : most);
+  const unsigned grid = (unsigned)per_seq * p.c.B;
   if (d == 64)
-    kv_copy_kernel<64><<<grid, kThreads, 0, s>>>(p, to, shift);
+    kv_copy_kernel<64><<<grid, kThreads, 0, s>>>(p, to, shift, per_seq);
   else
-    kv_copy_kernel<128><<<grid, kThreads, 0, s>>>(p, to, shift);
+    kv_copy_kernel<128><<<grid, kThreads, 0, s>>>(p, to, shift, per_seq);
   return check_cuda(cudaGetLastError(), "launch kv_copy_kernel");
 }
 
