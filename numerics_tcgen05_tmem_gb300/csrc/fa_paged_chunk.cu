@@ -924,7 +924,10 @@ Plan make_plan(int T, int B, int max_q, int group, int Hkv, int d, int max_kv, i
   // fill the SMs: the number of pieces that makes rounds * (steps of a piece + kPieceSteps) least, with
   // kPieceSteps for a CTA's start and end and one more step for each piece's partial result.  (2048
   // tokens over 32k keys, 256 tiles: 755 us whole, 700 with the last 104 in four pieces each.)
-  constexpr int kPieceSteps = 4;
+  // More than four rounds of pieces are not planned: the steps are counted from the table's width, and a
+  // piece that finds its sequence too short for it still costs a CTA's start (four sequences of up to
+  // 512 new tokens and 1.5k keys in a table for 128k: 56 us, without the limit 79).
+  constexpr int kPieceSteps = 4, kMostRounds = 4;
   using fa::paged::kChunkSms;
   const long long tiles = fa::paged::chunk_pairs(T, B, group) * Hkv;
   const long long rest = tiles % kChunkSms;
@@ -935,6 +938,7 @@ Plan make_plan(int T, int B, int max_q, int group, int Hkv, int d, int max_kv, i
     long long best = 0;
     for (int n = 1; n <= fa::paged::kMaxSplits && (n == 1 || steps / n >= fa::paged::kSplitSteps); ++n) {
       const long long rounds = (rest * n + kChunkSms - 1) / kChunkSms;
+      if (n > 1 && rounds > kMostRounds) break;
       const long long cost = rounds * ((steps + n - 1) / n + kPieceSteps) + (n > 1 ? n : 0);
       if (best == 0 || cost < best) {
         best = cost;
