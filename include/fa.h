@@ -382,6 +382,8 @@ int fa_kv_read(const fa_paged_kv* kv, const int32_t* kv_indptr, void* k_out, voi
  * the call runs.
  * Pages of which no new token sees a key are not read.  A key that some but not all rows of a tile
  * see must have finite values, as in the dense entry points (0 * Inf = NaN).
+ * Over an E4M3 cache, sequences of few rows (up to 64 of a kv head) round probability times V scale to
+ * FP16: 11 significant bits, and a key under 2^-30 of the row's largest such weight may count as zero.
  * workspace: device scratch of at least fa_fwd_paged_workspace_size(T, B, max_q, Hq, Hkv, d,
  * max_pages * page_size, window, sinks, kv->dtype) bytes, 256-byte aligned (NULL where that is 0); its contents on
  * entry do not matter.  Where many rows read each key of an E4M3 cache it includes room for a BF16

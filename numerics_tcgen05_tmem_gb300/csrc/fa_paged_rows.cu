@@ -18,11 +18,12 @@
 //     keys to the rest: for up to 16 rows each warp takes 16 keys of every block with its own running
 //     maximum and sum, joined once at the end of a piece.
 //   * E4M3: codes become FP16 with one conversion for two (exact), the vectors' scales multiply the
-//     FP32 scores (K) and the FP32 probabilities (V).  Q goes to FP16 with a power of two per row
+//     FP32 scores (K) and the FP32 probabilities (V, signs included).  Q goes to FP16 with a power of two per row
 //     that brings its largest magnitude into [1, 2): exact but for elements 2^-14 below it, whose
 //     error stays under 2^-25 of that magnitude, the size of an FP32 product's rounding.  The
-//     probabilities are taken relative to the largest V scale seen, so they stay within FP16's
-//     range; the output is multiplied by it at the end.
+//     weights, probability times scale, are rounded to FP16 relative to the piece's largest scale, or
+//     where scales differ much to the row's largest weight so far: a large vector that a row does not see, or
+//     gives next to no weight, would push all its other keys out of FP16's range.
 // Softmax statistics and sums are FP32; P is rounded to BF16 (FP16 with E4M3) for the product with V,
 // as the tensor core takes it.
 // 64 sequences with 284k keys in all, 32 query heads and 8 kv heads, d = 128: E4M3 96 us, 94 % of the
@@ -42,6 +43,17 @@ constexpr int kRowsLoadWarp = 4;
 constexpr int kRowsThreads = 256;
 constexpr int kRowsRegLaunch = 128, kRowsRegCompute = 208, kRowsRegLoad = 48;
 static_assert(kRowsRegCompute + kRowsRegLoad <= 2 * kRowsRegLaunch, "register split exceeds the launch allocation");
+
+// E4M3: the weights P~ (scale of V) go to FP16 with their reference at 2^kWeightExp, half of what FP16
+// holds: weights down to 2^-29 of it keep 11 bits, and one under 2^-40 of it is lost.  A piece's scales that
+// lie within kWideSpread of each other share the largest one as reference, at most that much above any row's
+// largest weight (the key with the largest score has P~ = 1); with others each row takes the largest weight
+// itself.  64 sequences of 4.4k keys, 8 kv heads, d = 128, at 8, 16, 32 and 64 rows: 99, 128, 199, 310 us; with a
+// reference for each row in all pieces 104, 151, 230, 348; with the largest scale alone, which loses keys, 98,
+// 123, 190, 302.
+constexpr int kWeightExp = 15;
+constexpr float kWideSpread = 1024.f;
+constexpr float kLeastRef = 3.8518598887744717e-34f;   // 2^-111: 2^kWeightExp over it stays finite
 
 template <int D, bool kFp8>
 struct RowsCfg {
@@ -399,7 +411,10 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
       float m[kNR][2], l[kNR][2];
 #pragma unroll
       for (int nr = 0; nr < kNR; ++nr) m[nr][0] = m[nr][1] = -INFINITY, l[nr][0] = l[nr][1] = 0.f;
-      float vref = 0.f, v_inv = 0.f;   // E4M3: O is in units of this V scale; its reciprocal
+      // E4M3: O is in units of v_ref / 2^kWeightExp, and v_inv is its reciprocal; once the scales seen
+      // spread too far (wide), each row has a reference of its own, w_ref.  v_low: the least scale seen
+      float v_ref = 0.f, v_inv = 0.f, v_low = INFINITY, w_ref[kNR][2];
+      bool wide = false;
       // kPair blocks at a time: their products are independent of each other, and the bookkeeping of
       // the running maximum is paid once for both
       for (int j = j0; j < j1; j += kPair) {
@@ -528,8 +543,8 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
             moved |= f_row[nr][e] != 1.f;
           }
         if constexpr (kFp8) {
-          // V's scales, relative to the largest one that the output holds so far
-          float v0[kPair * kKT], v1[kPair * kKT], top = 0.f;
+          // ---- weights P~ (scale of V), for FP16
+          float v0[kPair * kKT], v1[kPair * kKT], top = 0.f, low = INFINITY;
 #pragma unroll
           for (int i = 0; i < kPair * kKT; ++i) {
             const int x = i / kKT;
@@ -539,36 +554,83 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
             if (x < nb) {
               v0[i] = vs[0];
               v1[i] = vs[8];
-              if (edge) {
+              if (edge) {   // slots that no row sees may hold anything
                 const int key = it.w.at(j + x) + row_k + (i % kKT) * 16 + l4;
                 if (!it.w.seen(key)) v0[i] = 0.f;
                 if (!it.w.seen(key + 8)) v1[i] = 0.f;
               }
             }
             top = max3f(top, fabsf(v0[i]), fabsf(v1[i]));
+            low = min3f(low, v0[i] == 0.f ? INFINITY : fabsf(v0[i]), v1[i] == 0.f ? INFINITY : fabsf(v1[i]));
           }
-          if (__any_sync(0xffffffffu, top > vref)) {
+          // scales alike: the largest one so far is the reference of all rows
+          if (!wide && __any_sync(0xffffffffu, top > v_ref || low < v_low)) {
 #pragma unroll
-            for (int off = 4; off < 32; off *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-            top = fmaxf(top, 1.1754943508222875e-38f);   // 2^-126: the reciprocal stays finite
-            const float ratio = vref / top;
-#pragma unroll
-            for (int nr = 0; nr < kNR; ++nr) {
-              f_row[nr][0] *= ratio;
-              f_row[nr][1] *= ratio;
+            for (int off = 4; off < 32; off *= 2) {
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+              low = fminf(low, __shfl_xor_sync(0xffffffffu, low, off));
             }
-            vref = top;
-            v_inv = 1.f / top;
-            moved = true;
-          }
+            top = fmaxf(fmaxf(top, v_ref), kLeastRef);
+            v_low = fminf(low, v_low);
+            wide = v_low * kWideSpread < top;
+            if (wide) {
 #pragma unroll
-          for (int i = 0; i < kPair * kKT; ++i) {
-            const float a = v0[i] * v_inv, c = v1[i] * v_inv;
+              for (int nr = 0; nr < kNR; ++nr) w_ref[nr][0] = w_ref[nr][1] = v_ref;
+            } else if (top > v_ref) {
+              const float ratio = v_ref / top;
+#pragma unroll
+              for (int nr = 0; nr < kNR; ++nr) {
+                f_row[nr][0] *= ratio;
+                f_row[nr][1] *= ratio;
+              }
+              v_ref = top;
+              v_inv = (float)(1 << kWeightExp) / top;
+              moved = true;
+            }
+          }
+          if (!wide) {
+#pragma unroll
+            for (int i = 0; i < kPair * kKT; ++i) {
+              const float a = v0[i] * v_inv, c = v1[i] * v_inv;
+#pragma unroll
+              for (int nr = 0; nr < kNR; ++nr) {
+                float (&v)[4] = sc[i][nr];
+                mul2(v[0], v[1], v[0], v[1], a, a);
+                mul2(v[2], v[3], v[2], v[3], c, c);
+              }
+            }
+          } else {
+            // a row's reference is its largest weight so far (or above it); it falls with m's rise as O
+            // does, so O is rescaled only where a weight exceeds it
+            moved = false;
 #pragma unroll
             for (int nr = 0; nr < kNR; ++nr) {
-              float (&v)[4] = sc[i][nr];
-              mul2(v[0], v[1], v[0], v[1], a, a);
-              mul2(v[2], v[3], v[2], v[3], c, c);
+              float most[2] = {0.f, 0.f};
+#pragma unroll
+              for (int i = 0; i < kPair * kKT; ++i) {
+                float (&v)[4] = sc[i][nr];
+                mul2(v[0], v[1], v[0], v[1], v0[i], v0[i]);
+                mul2(v[2], v[3], v[2], v[3], v1[i], v1[i]);
+                most[0] = max3f(most[0], fabsf(v[0]), fabsf(v[2]));
+                most[1] = max3f(most[1], fabsf(v[1]), fabsf(v[3]));
+              }
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int off = 4; off < 32; off *= 2)
+                  most[e] = fmaxf(most[e], __shfl_xor_sync(0xffffffffu, most[e], off));
+                const float was = w_ref[nr][e] * f_row[nr][e];
+                w_ref[nr][e] = fmaxf(fmaxf(most[e], was), kLeastRef);
+                f_row[nr][e] = was / w_ref[nr][e];
+                moved |= f_row[nr][e] != 1.f;
+              }
+              const float inv0 = (float)(1 << kWeightExp) / w_ref[nr][0], inv1 = (float)(1 << kWeightExp) / w_ref[nr][1];
+#pragma unroll
+              for (int i = 0; i < kPair * kKT; ++i) {
+                float (&v)[4] = sc[i][nr];
+                mul2(v[0], v[1], v[0], v[1], inv0, inv1);
+                mul2(v[2], v[3], v[2], v[3], inv0, inv1);
+              }
             }
           }
         }
@@ -653,7 +715,8 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
 #pragma unroll
           for (int k = 0; k < kKG; ++k) sum += sh.l[rg * kKG + k][in] * ex2_approx(sh.m[rg * kKG + k][in] - tu);
           const bool empty = top == -INFINITY && sum == 0.f;   // no visible key (a NaN score is not that)
-          w_row[nr][e] = empty ? 0.f : ex2_approx(m[nr][e] - tu) / sum * (kFp8 ? vref : 1.f);
+          w_row[nr][e] = empty ? 0.f : ex2_approx(m[nr][e] - tu) / sum;
+          if constexpr (kFp8) w_row[nr][e] *= 1.f / (1 << kWeightExp);
           const float lse = empty ? -INFINITY : top * 0.6931471805599453f + logf(sum);
           const bool mine = kg == 0 && l4 == 0 && r < it.rows;
           if (mine) {
@@ -676,8 +739,11 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
             float* dst = buf + (warp * 4 + (2 * t4 & 3) + e) * C::kBufRow;
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
-              const float a = o[i][nr][e] * w_row[nr][e], c = o[i][nr][e + 2] * w_row[nr][e];
+              float a = o[i][nr][e] * w_row[nr][e], c = o[i][nr][e + 2] * w_row[nr][e];
               if constexpr (kFp8) {
+                const float ref = wide ? w_ref[nr][e] : v_ref;
+                a *= ref;   // (a product of its own: the factors' may be subnormal)
+                c *= ref;
                 *reinterpret_cast<float2*>(dst + i * 16 + 2 * l4) = make_float2(a, c);
               } else {
                 dst[i * 16 + l4] = a;
