@@ -412,6 +412,17 @@ def _outer(n, stride, least, name):
     return stride
 
 
+def _alike(a, b, inner):
+    """Whether two tensors of one shape have contiguous pages (strides `inner` behind the first dimension)
+    that lie the same distance apart; a dimension of one entry has no stride."""
+    sa, sb = a.stride(), b.stride()
+    if sa == sb and sa[1:] == inner:
+        return True
+    n = a.shape
+    return all(n[i + 1] == 1 or sa[i + 1] == sb[i + 1] == w for i, w in enumerate(inner)) and \
+        (n[0] == 1 or sa[0] == sb[0])
+
+
 def _int32(t, n, name, dev):
     if t.dtype is not torch.int32 or t.get_device() != dev or t.dim() != 1 or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 vector on the cache's device")
@@ -426,11 +437,11 @@ def _paged(k, v, table, kv_len, k_scale, v_scale):
     if dev < 0 or len(shape) != 4 or v.shape != shape or v.dtype is not dtype or v.get_device() != dev:
         raise ValueError("expected CUDA cache tensors of one shape [pages, Hkv, page_size, d] and one type")
     P, H, S, d = shape
-    stride = k.stride()
-    if v.stride() != stride or stride[1:] != (S * d, d, 1):
+    if not _alike(k, v, (S * d, d, 1)):
         raise ValueError("cache pages must be contiguous, with the same page stride for K and V")
     rows = table.stride()
-    if table.dtype is not torch.int32 or len(rows) != 2 or rows[1] != 1 or table.get_device() != dev:
+    if table.dtype is not torch.int32 or len(rows) != 2 or (rows[1] != 1 and table.shape[1] != 1) or \
+            table.get_device() != dev:
         raise ValueError("block_table must be an int32 tensor [B, max_pages] on the cache's device, rows contiguous")
     B, width = table.shape
     kv_ptr = _int32(kv_len, B, "kv_len", dev)
@@ -442,17 +453,16 @@ def _paged(k, v, table, kv_len, k_scale, v_scale):
     elif dtype is torch.uint8 or dtype is torch.float8_e4m3fn:
         if k_scale is None or v_scale is None:
             raise ValueError("an E4M3 cache needs k_scale and v_scale")
-        scale_stride = k_scale.stride()[0] if k_scale.dim() else 0
         for s in (k_scale, v_scale):
-            if s.dtype is not torch.float32 or s.shape != shape[:3] or s.get_device() != dev or \
-                    s.stride() != (scale_stride, S, 1):
-                raise ValueError("k_scale and v_scale must be float32 [pages, Hkv, page_size], pages contiguous, with "
-                                 "the same page stride")
+            if s.dtype is not torch.float32 or s.shape != shape[:3] or s.get_device() != dev:
+                raise ValueError("k_scale and v_scale must be float32 [pages, Hkv, page_size] on the cache's device")
+        if not _alike(k_scale, v_scale, (S, 1)):
+            raise ValueError("scale pages must be contiguous, with the same page stride for K and V")
         ks, vs, code = k_scale.data_ptr(), v_scale.data_ptr(), FA_KV_E4M3
-        scale_stride = _outer(P, scale_stride, H * S, "k_scale")
+        scale_stride = _outer(P, k_scale.stride(0), H * S, "k_scale")
     else:
         raise ValueError("cache tensors must be bfloat16, or uint8 (or float8_e4m3fn) E4M3 codes")
-    return PagedKV(k.data_ptr(), v.data_ptr(), ks, vs, _outer(P, stride[0], H * S * d, "cache"), scale_stride,
+    return PagedKV(k.data_ptr(), v.data_ptr(), ks, vs, _outer(P, k.stride(0), H * S * d, "cache"), scale_stride,
                    table.data_ptr(), _outer(B, rows[0], width, "block_table"), kv_ptr, B, H, d, S, P, width, code)
 
 
