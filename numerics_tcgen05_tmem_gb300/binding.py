@@ -200,6 +200,12 @@ def _on_device(t):
     return _HERE if torch._C._cuda_getDevice() == dev else _OnDevice(dev)
 
 
+def _c_int(x):
+    """A window, a number of sinks or a largest length as a C int.  Past 32 bits it means what the largest
+    int does (no tensor is that long), where ctypes would keep the low bits."""
+    return min(max(int(x), -2 ** 31), 2 ** 31 - 1)
+
+
 def _check_qkv(*ts):
     shape, dev = ts[0].shape, ts[0].get_device()
     for t in ts:
@@ -223,7 +229,7 @@ def fa_fwd_window(q, k, v, o, lse, window: int, sinks: int, scale: float, stable
                   stream=None) -> int:
     B, H, N, d = q.shape
     st = _row_stats(stats)
-    return load().fa_fwd_window(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H, N, d, int(window), int(sinks),
+    return load().fa_fwd_window(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H, N, d, _c_int(window), _c_int(sinks),
                                 float(scale), int(stable), float(beta), ctypes.byref(st) if st is not None else None,
                                 _stream(stream))
 
@@ -250,7 +256,8 @@ def fa_quantize_fp8(x, x8, descale, stream=None) -> int:
 
 def fa_fwd_paged_workspace_size(T: int, B: int, max_q: int, Hq: int, Hkv: int, d: int, max_kv: int,
                                 window: int = 0, sinks: int = 0, dtype: int = FA_KV_BF16) -> int:
-    return int(load().fa_fwd_paged_workspace_size(T, B, max_q, Hq, Hkv, d, max_kv, window, sinks, dtype))
+    return int(load().fa_fwd_paged_workspace_size(T, B, _c_int(max_q), Hq, Hkv, d, _c_int(max_kv), _c_int(window),
+                                                  _c_int(sinks), dtype))
 
 
 def fa_bwd_workspace_size(B: int, H: int, N: int, d: int) -> int:
@@ -269,7 +276,7 @@ def fa_bwd(q, k, v, o, lse, do, dq, dk, dv, delta, causal: bool, scale: float, w
 
 
 def fa_bwd_window_workspace_size(B: int, H: int, N: int, d: int, window: int, sinks: int = 0) -> int:
-    return int(load().fa_bwd_window_workspace_size(B, H, N, d, window, sinks))
+    return int(load().fa_bwd_window_workspace_size(B, H, N, d, _c_int(window), _c_int(sinks)))
 
 
 def fa_bwd_window(q, k, v, o, lse, do, dq, dk, dv, delta, window: int, sinks: int, scale: float, workspace,
@@ -277,7 +284,7 @@ def fa_bwd_window(q, k, v, o, lse, do, dq, dk, dv, delta, window: int, sinks: in
     B, H, N, d = q.shape
     nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     return load().fa_bwd_window(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(do), _ptr(dq), _ptr(dk), _ptr(dv),
-                                _ptr(delta), B, H, N, d, int(window), int(sinks), float(scale), _ptr(workspace),
+                                _ptr(delta), B, H, N, d, _c_int(window), _c_int(sinks), float(scale), _ptr(workspace),
                                 nbytes, _stream(stream))
 
 
@@ -542,6 +549,7 @@ def forward_paged(q, k_cache, v_cache, block_table, kv_len, q_indptr, max_q, k_s
         window = 0
     elif window < 1:
         raise ValueError("window must be >= 1 (None: no window)")
+    window, sinks, max_q = _c_int(window), _c_int(sinks), _c_int(max_q)
     dev, d = k_cache.get_device(), kv.d
     if q.dim() != 3:
         raise ValueError("q must be [T, Hq, d]")
@@ -568,8 +576,8 @@ def forward_paged(q, k_cache, v_cache, block_table, kv_len, q_indptr, max_q, k_s
         raise ValueError("workspace must be a contiguous tensor on the cache's device")
     ws, nbytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
     with _on_device(k_cache):
-        _check(lib.fa_fwd_paged(ctypes.byref(kv), q.data_ptr(), stride, indptr, T, int(max_q), Hq, out.data_ptr(),
-                                lse.data_ptr(), window, int(sinks), 1.0 / math.sqrt(d) if scale is None else float(scale),
+        _check(lib.fa_fwd_paged(ctypes.byref(kv), q.data_ptr(), stride, indptr, T, max_q, Hq, out.data_ptr(),
+                                lse.data_ptr(), window, sinks, 1.0 / math.sqrt(d) if scale is None else float(scale),
                                 ws, nbytes, _stream(stream)))
     return out, lse
 
