@@ -316,12 +316,10 @@ def fa_bwd_noalloc_status(stream=None):
 
 # ----------------------------------------------------------------- tensor-level helpers
 
-def _stats_dict(B, H, N, device):
-    return {"row_max_raw": torch.empty((B, H, N), device=device, dtype=torch.float32),
-            "row_ties": torch.empty((B, H, N), device=device, dtype=torch.int32),
-            "row_branch": torch.empty((B, H, N), device=device, dtype=torch.int8),
-            "row_ones": torch.empty((B, H, N), device=device, dtype=torch.int32),
-            "row_min_raw": torch.empty((B, H, N), device=device, dtype=torch.float32)}
+def _stats_dict(B, H, N, like, stream):
+    return {name: _empty((B, H, N), dtype, like, stream)
+            for name, dtype in (("row_max_raw", torch.float32), ("row_ties", torch.int32), ("row_branch", torch.int8),
+                                ("row_ones", torch.int32), ("row_min_raw", torch.float32))}
 
 
 def _check_window(causal, window, sinks):
@@ -345,7 +343,7 @@ def forward(q, k, v, causal: bool = True, scale=None, stable: int = 1, beta: flo
     scale = 1.0 / math.sqrt(d) if scale is None else scale
     o = _empty_like(q, stream)
     lse = _empty((B, H, N), torch.float32, q, stream)
-    sd = _stats_dict(B, H, N, q.device) if stats else None
+    sd = _stats_dict(B, H, N, q, stream) if stats else None
     with _on_device(q):
         if window is None:
             _check(fa_fwd(q, k, v, o, lse, causal, scale, stable, beta, sd, stream))
@@ -362,8 +360,8 @@ def quantize_fp8(x, stream=None):
     """
     if not (x.is_cuda and x.dtype == torch.bfloat16 and x.is_contiguous()):
         raise ValueError("expected a contiguous CUDA bfloat16 tensor")
-    x8 = torch.empty(x.shape, device=x.device, dtype=torch.uint8)
-    descale = torch.empty(1, device=x.device, dtype=torch.float32)
+    x8 = _empty(x.shape, torch.uint8, x, stream)
+    descale = _empty(1, torch.float32, x, stream)
     _check(fa_quantize_fp8(x, x8, descale, stream))
     return x8, descale
 
@@ -379,9 +377,9 @@ def forward_fp8(q8, k8, v8, descale, causal: bool = True, scale=None, stable: in
         raise ValueError("descale must be a contiguous CUDA float32 tensor of 3 elements")
     B, H, N, d = q8.shape
     scale = 1.0 / math.sqrt(d) if scale is None else scale
-    o = torch.empty((B, H, N, d), device=q8.device, dtype=torch.bfloat16)
-    lse = torch.empty((B, H, N), device=q8.device, dtype=torch.float32)
-    sd = _stats_dict(B, H, N, q8.device) if stats else None
+    o = _empty((B, H, N, d), torch.bfloat16, q8, stream)
+    lse = _empty((B, H, N), torch.float32, q8, stream)
+    sd = _stats_dict(B, H, N, q8, stream) if stats else None
     _check(fa_fwd_fp8(q8, k8, v8, descale, o, lse, causal, scale, stable, beta, sd, stream))
     return (o, lse, sd) if stats else (o, lse)
 
