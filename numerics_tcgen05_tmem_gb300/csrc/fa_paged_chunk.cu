@@ -993,8 +993,10 @@ int check_attn(int T, int B, int max_q, int Hq, int Hkv, int d) {
   if (Hq % Hkv) return set_error(FA_ERR_INVALID_ARG, "Hq = %d is not a multiple of Hkv = %d", Hq, Hkv);
   if (Hq / Hkv > 128) return set_error(FA_ERR_UNSUPPORTED, "more than 128 query heads for a kv head (%d)", Hq / Hkv);
   if (d != 64 && d != 128) return set_error(FA_ERR_UNSUPPORTED, "head dim d=%d not supported (64 or 128)", d);
-  if ((long long)T * Hq >= (1ll << 31) || (long long)B * Hkv >= (1ll << 31))
-    return set_error(FA_ERR_INVALID_ARG, "T*Hq and B*Hkv must be < 2^31");
+  // the few-rows join has up to kMaxFewRows / 4 CTAs for each sequence and kv head
+  constexpr long long kMostItems = (1ll << 31) / (kMaxFewRows / 4);
+  if ((long long)T * Hq >= (1ll << 31) || (long long)B * Hkv >= kMostItems)
+    return set_error(FA_ERR_INVALID_ARG, "T*Hq must be < 2^31 and B*Hkv < %lld", kMostItems);
   return FA_OK;
 }
 

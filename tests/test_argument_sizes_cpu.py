@@ -1,4 +1,6 @@
-"""Windows, sinks and lengths past 32 bits, and integers that are not Python's; nothing is launched here."""
+"""Windows, sinks, lengths and batches past 32 bits, and integers that are not Python's; nothing is launched here."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -41,3 +43,17 @@ def test_integers_of_other_libraries():
         assert size(9, 3, as_int(5), 8, 2, 64, as_int(1000), as_int(70), as_int(2)) == size(9, 3, 5, 8, 2, 64, 1000, 70, 2)
         assert binding.fa_bwd_window_workspace_size(1, 8, 12000, 128, as_int(256), as_int(4)) == \
             binding.fa_bwd_window_workspace_size(1, 8, 12000, 128, 256, 4)
+
+
+@pytest.mark.parametrize("B,Hkv,ok", [(1 << 26, 1, True), ((1 << 27) - 1, 1, True), (1 << 27, 1, False),
+                                     (1 << 24, 8, False), ((1 << 24) - 1, 8, True), (1 << 29, 1, False)])
+def test_batches_past_the_largest_launch_are_refused(B, Hkv, ok):
+    # the joining launch has 16 CTAs for each sequence and kv head at most, in 32 bits
+    n = binding.fa_fwd_paged_workspace_size(5, B, 64, Hkv, Hkv, 64, 1000)
+    assert (n > 0) == ok
+    if not ok:
+        assert "B*Hkv" in binding.last_error()
+        at = 1 << 20   # an aligned address that is never dereferenced
+        kv = binding.PagedKV(at, at, None, None, Hkv * 16 * 64, 0, at, 63, at, B, Hkv, 64, 16, 9, 63, binding.FA_KV_BF16)
+        assert binding.load().fa_fwd_paged(ctypes.byref(kv), at, Hkv * 64, at, 5, 64, Hkv, at, at, 0, 0, 0.125, at, 1 << 40,
+                                           None) == binding.FA_ERR_INVALID_ARG
