@@ -224,7 +224,9 @@ int fa_bwd_staged(const void* q, const void* k, const void* v, const void* o, co
  * workspace holds at least fa_bwd_window_workspace_size(...) bytes (fa_bwd's, and partial sums where
  * key tiles with sinks are split over their queries; 0 for invalid sizes).  The gradients of keys that
  * no query sees are zero.  For queries that see at most 16 keys delta is summed from probabilities
- * recomputed in FP32, not from the rounded o, whose error would show in dq and dk there.
+ * recomputed in FP32, not from the rounded o, whose error would show in dq and dk there.  dk and dv are
+ * the same bits in every call on the same data; dq, like fa_bwd's, is a sum of FP32 terms in the order in
+ * which they arrive.
  */
 size_t fa_bwd_window_workspace_size(int B, int H, int N, int d, int window, int sinks);
 
@@ -373,7 +375,8 @@ int fa_kv_read(const fa_paged_kv* kv, const int32_t* kv_indptr, void* k_out, voi
  *              Hq is a multiple of kv->Hkv, at most 128 times it; query head i uses kv head
  *              i / (Hq / Hkv)
  *   q_indptr : int32 [B + 1], the sequences' packed rows
- *   max_q    : at least the largest number of new tokens of a sequence
+ *   max_q    : at least the largest number of new tokens of a sequence (a sequence with more is recorded
+ *              as FA_ERR_DEVICE_BOUNDS); 0 says that there are none: nothing is launched, checked or written
  *   o        : BF16 [T, Hq, d], contiguous;  lse: FP32 [T, Hq], or NULL (not written)
  *   window   : 0 = none; else the token at position p sees the keys p - window < j <= p and the
  *              first `sinks` keys; without a window every key j <= p
@@ -390,6 +393,7 @@ int fa_kv_read(const fa_paged_kv* kv, const int32_t* kv_indptr, void* k_out, voi
  * copy of the keys and values that the new tokens may see (2 GiB at most; from max_pages, not from
  * the lengths).  Calls that may overlap need workspaces of their own.
  * Results do not depend on timing: the same call on the same data gives the same bits.
+ * T * Hq is under 2^31 and B * Hkv under 2^27.
  * Returns FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED or FA_ERR_CUDA; T = 0 launches nothing.
  */
 size_t fa_fwd_paged_workspace_size(int T, int B, int max_q, int Hq, int Hkv, int d, int max_kv, int window, int sinks,

@@ -531,8 +531,8 @@ def forward_paged(q, k_cache, v_cache, block_table, kv_len, q_indptr, max_q, k_s
 
     q: bfloat16 [T, Hq, d] (rows may be strided); sequence b's new tokens are the rows q_indptr[b] ..
     q_indptr[b + 1] - 1 and the last positions of its cache, which already holds their keys and
-    values (kv_append).  max_q: at least the largest number of new tokens of a sequence.  Hq is a
-    multiple of the cache's heads.  With a window, the token at position p sees the keys
+    values (kv_append).  max_q: at least the largest number of new tokens of a sequence; 0 says that there
+    are none, and nothing is written.  Hq is a multiple of the cache's heads.  With a window, the token at position p sees the keys
     p - window < j <= p and the first ``sinks`` keys; otherwise every key j <= p.
     out, lse: tensors to write to ([T, Hq, d] bfloat16, [T, Hq] float32); rows behind the last
     sequence stay as they were (undefined in fresh tensors).

@@ -90,7 +90,7 @@ static_assert(chunk_smem<128, true>() <= 227 * 1024, "shared-memory layout excee
 struct ChunkWork {
   Seq s;
   int tok0, tokens;      // first token of the pair, tokens per tile
-  int first, last;       // positions of its first and last token
+  int last;              // position of its last token
   int splits;            // pieces that the pair's keys are split into
   KeyWalk<kN> w;
   __device__ __forceinline__ ChunkWork(const Attn& p, int b, int tile, int max_splits)
@@ -98,7 +98,6 @@ struct ChunkWork {
         tokens(kM / p.group),
         w(p, s.pos0 + tile * 2 * (kM / p.group), s.pos0 + min((tile + 1) * 2 * (kM / p.group), s.n) - 1) {
     tok0 = tile * 2 * tokens;
-    first = s.pos0 + tok0;
     last = s.pos0 + min(tok0 + 2 * tokens, s.n) - 1;
     splits = min(max_splits, max(1, w.steps / kSplitSteps));
   }
@@ -800,8 +799,9 @@ __device__ __forceinline__ void join_row(const Attn& p, long long base, int piec
   if (lane == 0 && p.lse) p.lse[row] = lse;
 }
 
-// Joins the pieces of tiles whose keys were split: 32 rows of a tile per CTA, four per warp.  Launched
-// while the pieces are still being computed (programmatic launch).
+// Joins the pieces of tiles whose keys were split: 32 rows of a tile per CTA, four per warp.  A programmatic
+// launch: it starts while the pieces are still being computed, or, with a few-rows launch between, where
+// that one's CTAs have ended.
 constexpr int kJoinRows = 32;
 
 template <int D>

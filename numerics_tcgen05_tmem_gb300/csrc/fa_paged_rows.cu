@@ -26,9 +26,10 @@
 //     gives next to no weight, would push all its other keys out of FP16's range.
 // Softmax statistics and sums are FP32; P is rounded to BF16 (FP16 with E4M3) for the product with V,
 // as the tensor core takes it.
-// 64 sequences with 284k keys in all, 32 query heads and 8 kv heads, d = 128: E4M3 96 us, 94 % of the
-// measured copy rate (605 MB read once; tensor pipe 16 %).  One sequence of 4k keys, BF16: 7 us, of which
-// the bytes take 2.5: what is left is one block's chain of load, products and softmax, and the join.
+// 64 sequences with 284k keys in all, 32 query heads and 8 kv heads, d = 128: E4M3 99 us, 92 % of the
+// measured copy rate (605 MB read once; tensor pipe 16 %), BF16 173 us, at the copy rate; d = 64: 74 us, 63 %,
+// and 92 us, 95 %.  One sequence of 4k keys, BF16: 7 us, of which the bytes take 2.5: what is left is one
+// block's chain of load, products and softmax, and the join.
 #include "paged_attn.cuh"
 
 namespace fa {
@@ -795,8 +796,8 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
 
 // Joins the pieces of split items: out = sum_i w_i o_i, w_i = exp(lse_i - lse), lse = log sum exp(lse_i).
 // A warp per row, four rows per CTA.  The first piece is in the slot that its CTA recorded, the others
-// are the first pieces of the CTAs that follow.  Launched while the pieces are still being computed
-// (programmatic launch): what it reads of them comes after the wait.
+// are the first pieces of the CTAs that follow.  A programmatic launch: its CTAs start where the pieces' CTAs
+// have ended (none of those triggers before), and what they read of the pieces comes after the wait.
 template <int D>
 __global__ void __launch_bounds__(128) fa_rows_combine(const Attn p, int slot_rows) {
   const int groups = slot_rows / 4;
