@@ -403,6 +403,78 @@ int fa_fwd_paged(const fa_paged_kv* kv, const void* q, int64_t q_stride, const i
                  int Hq, void* o, float* lse, int window, int sinks, float scale, void* workspace,
                  size_t workspace_bytes, void* stream);
 
+/*
+ * Norm of queries and keys for each head and position rotation, in one pass (what comes between a model's
+ * projections and the attention calls; the pages have no counterpart).  For x, one head of one token:
+ *   r = 1 / sqrt(mean x^2 + eps),  y = weight o x r,
+ *   z_a = y_a cos(t) - y_b sin(t),  z_b = y_b cos(t) + y_a sin(t),  t = position * inv_freq[i],
+ * where pair i < rot / 2 is (a, b) = (i, i + rot / 2), or (2 i, 2 i + 1) with `interleaved`; the entries from rot on
+ * keep y.  Sums, angles and products are FP32 (angles modulo one turn in 64-bit integers, so that far positions
+ * lose nothing); the result is rounded once.  A vector whose sum of squares passes FP32's range gives zeros.
+ *   inv_freq : FP64 [rot / 2] on the device, radians for each position (not used with rot = 0)
+ *   q_weight, k_weight : [d] on the device, FP32, or BF16 with weight_bf16; NULL means ones
+ *   rot      : rotated entries, a multiple of 16 from 0 (the norm alone) to d
+ *   norm     : 0 leaves y = x (no weights then); eps is finite and >= 0
+ */
+typedef struct {
+  const double* inv_freq;
+  const void* q_weight;
+  const void* k_weight;
+  int32_t rot, interleaved, weight_bf16, norm;
+  float eps;
+} fa_rotation;
+
+/* A BF16 view [B, H, N, d] with the strides of its outer dimensions in elements (multiples of 8, not negative;
+ * those of dimensions with one entry are not used); d is contiguous, p 16-byte aligned.  A transposed slice of a
+ * fused projection [B, N, heads, d] is one. */
+typedef struct {
+  void* p;
+  int64_t stride_b, stride_h, stride_n;
+} fa_heads;
+
+/*
+ * fa_norm_rotate -- norm and rotation of q [B, Hq, N, d] and k [B, Hkv, N, d].
+ *   q_out, k_out : outputs, whose heads of tokens may not overlap; an output may be its input (same strides),
+ *                  and may not overlap an input otherwise
+ *   positions    : int32 on the device, sequence b's at positions + b * positions_stride (0: the same for all),
+ *                  any 32-bit value; NULL means 0 .. N - 1
+ * Returns FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED or FA_ERR_CUDA.
+ */
+int fa_norm_rotate(const fa_rotation* rotation, const fa_heads* q, const fa_heads* k, const fa_heads* q_out,
+                   const fa_heads* k_out, int B, int Hq, int Hkv, int N, int d, const int32_t* positions,
+                   int64_t positions_stride, void* stream);
+
+/*
+ * fa_norm_rotate_bwd -- its backward: from the inputs q, k of the forward and the gradients dzq, dzk of its outputs.
+ *   dq, dk       : outputs (each may be its dz or its input, with the same strides)
+ *   dq_weight, dk_weight : outputs, FP32 [d], both or neither (NULL); with the norm only.  Summed in a fixed order:
+ *                  the same bits in every call on the same data.
+ *   workspace    : device scratch of at least fa_norm_rotate_bwd_workspace_size(B, Hq, Hkv, N, d) bytes (0 for invalid
+ *                  sizes), 256-byte aligned, for the weights' gradients (else not used); its contents on entry do
+ *                  not matter.  Calls that may overlap need workspaces of their own.
+ */
+size_t fa_norm_rotate_bwd_workspace_size(int B, int Hq, int Hkv, int N, int d);
+
+int fa_norm_rotate_bwd(const fa_rotation* rotation, const fa_heads* q, const fa_heads* k, const fa_heads* dzq,
+                       const fa_heads* dzk, const fa_heads* dq, const fa_heads* dk, float* dq_weight, float* dk_weight,
+                       int B, int Hq, int Hkv, int N, int d, const int32_t* positions, int64_t positions_stride,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * fa_qkv_append -- the serving form: q normed and rotated, k normed, rotated and written with v into the cache
+ * (as fa_kv_append writes, one launch for all three).
+ *   q, k_new, v_new : BF16 [T, Hq, d], [T, Hkv, d], [T, Hkv, d], tokens q_stride and new_stride elements apart
+ *                  (multiples of 8, at least a token's elements)
+ *   q_out        : BF16 [T, Hq, d], contiguous; it does not overlap the inputs (q itself, where it is contiguous, is fine)
+ *   positions    : int32 [T] for the rotation, or NULL: each token's position in its sequence, kv_len - n ..
+ *                  (after an eviction the two differ)
+ * BF16 caches get the rounded z, as from fa_norm_rotate and fa_kv_append.  E4M3 caches get the codes of the
+ * FP32 z, rounded once, with fa_kv_append's scale rule.  Rows behind the last sequence are not written.
+ */
+int fa_qkv_append(const fa_paged_kv* kv, const fa_rotation* rotation, const void* q, int64_t q_stride, void* q_out, int Hq,
+                  const void* k_new, const void* v_new, int64_t new_stride, const int32_t* q_indptr,
+                  const int32_t* positions, int T, void* stream);
+
 /* Message for the last non-OK return on the calling thread ("" if none). */
 const char* fa_last_error(void);
 

@@ -33,7 +33,8 @@ EXPORTS = ("fa_fwd", "fa_fwd_window", "fa_fwd_fp8", "fa_quantize_fp8", "fa_bwd",
            "fa_bwd_window_workspace_size", "fa_bwd_staged",
            "fa_bwd_noalloc", "fa_bwd_noalloc_status", "fa_bwd_workspace_size", "fa_device_status",
            "fa_device_report_read", "fa_last_error", "fa_version", "fa_kv_append", "fa_kv_read",
-           "fa_fwd_paged", "fa_fwd_paged_workspace_size")
+           "fa_fwd_paged", "fa_fwd_paged_workspace_size", "fa_norm_rotate", "fa_norm_rotate_bwd",
+           "fa_norm_rotate_bwd_workspace_size", "fa_qkv_append")
 
 # size of the fixed device scratch behind fa_bwd_noalloc (FA_NOALLOC_SCRATCH_BYTES in fa.h)
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
@@ -64,6 +65,19 @@ class PagedKV(ctypes.Structure):
                 ("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("kv_len", ctypes.c_void_p),
                 ("B", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("d", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("num_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class Rotation(ctypes.Structure):
+    """fa_rotation: how queries and keys are normed and rotated."""
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("weight_bf16", ctypes.c_int32),
+                ("norm", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class Heads(ctypes.Structure):
+    """fa_heads: a view [B, H, N, d] with its strides."""
+    _fields_ = [("p", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64),
+                ("stride_n", ctypes.c_int64)]
 
 
 class DeviceReport(ctypes.Structure):
@@ -115,6 +129,15 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.fa_fwd_paged_workspace_size.restype = cs
     L.fa_fwd_paged.argtypes = [ctypes.POINTER(PagedKV), vp, ctypes.c_int64, vp, ci, ci, ci, vp, vp, ci, ci, cf, vp, cs, vp]
     L.fa_fwd_paged.restype = ci
+    heads, rotation, c64 = ctypes.POINTER(Heads), ctypes.POINTER(Rotation), ctypes.c_int64
+    L.fa_norm_rotate.argtypes = [rotation] + [heads] * 4 + [ci] * 5 + [vp, c64, vp]
+    L.fa_norm_rotate.restype = ci
+    L.fa_norm_rotate_bwd_workspace_size.argtypes = [ci] * 5
+    L.fa_norm_rotate_bwd_workspace_size.restype = cs
+    L.fa_norm_rotate_bwd.argtypes = [rotation] + [heads] * 6 + [vp, vp] + [ci] * 5 + [vp, c64, vp, cs, vp]
+    L.fa_norm_rotate_bwd.restype = ci
+    L.fa_qkv_append.argtypes = [ctypes.POINTER(PagedKV), rotation, vp, c64, vp, ci, vp, vp, c64, vp, vp, ci, vp]
+    L.fa_qkv_append.restype = ci
     L.fa_bwd_noalloc.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, cf, vp]
     L.fa_bwd_noalloc.restype = ci
     L.fa_device_status.argtypes = [vp]
@@ -578,6 +601,162 @@ def forward_paged(q, k_cache, v_cache, block_table, kv_len, q_indptr, max_q, k_s
                                 lse.data_ptr(), window, sinks, 1.0 / math.sqrt(d) if scale is None else float(scale),
                                 ws, nbytes, _stream(stream)))
     return out, lse
+
+
+# ----------------------------------------------------------------- norm and rotation of queries and keys
+
+def _rotation(inv_freq, d, dev, q_weight, k_weight, eps, interleaved, norm):
+    """The fa_rotation of these tensors (types, shapes and devices checked)."""
+    rot, freq = 0, None
+    if inv_freq is not None:
+        if inv_freq.dtype is not torch.float64 or inv_freq.get_device() != dev or inv_freq.dim() != 1 or \
+                not inv_freq.is_contiguous():
+            raise ValueError("inv_freq must be a contiguous float64 vector on the queries' device")
+        rot, freq = 2 * inv_freq.numel(), inv_freq.data_ptr()
+    if q_weight is None and k_weight is None:
+        return Rotation(freq, None, None, rot, bool(interleaved), 0, bool(norm), eps)
+    if q_weight is None or k_weight is None or q_weight.dtype is not k_weight.dtype:
+        raise ValueError("q_weight and k_weight are given together, in one type")
+    for w in (q_weight, k_weight):
+        if w.dtype not in (torch.float32, torch.bfloat16) or w.get_device() != dev or w.dim() != 1 or w.numel() != d or \
+                not w.is_contiguous():
+            raise ValueError(f"weights must be contiguous float32 or bfloat16 vectors of {d} on the queries' device")
+    return Rotation(freq, q_weight.data_ptr(), k_weight.data_ptr(), rot, bool(interleaved),
+                    q_weight.dtype is torch.bfloat16, bool(norm), eps)
+
+
+def _heads(t, name, shape, dev):
+    """The fa_heads of a view [B, H, N, d]."""
+    stride = t.stride()
+    if t.dtype is not torch.bfloat16 or t.get_device() != dev or t.shape != shape:
+        raise ValueError(f"{name} must be a CUDA bfloat16 tensor {list(shape)} on the queries' device")
+    if stride[3] != 1:
+        raise ValueError(f"{name}: heads must be contiguous")
+    return Heads(t.data_ptr(), stride[0], stride[1], stride[2])
+
+
+def _check_qk(q, k):
+    """The shapes of queries [B, Hq, N, d] and keys [B, Hkv, N, d] and their device."""
+    sq, sk, dev = q.shape, k.shape, q.get_device()
+    if dev < 0 or len(sq) != 4 or len(sk) != 4 or sq[0] != sk[0] or sq[2:] != sk[2:]:
+        raise ValueError("expected CUDA tensors q [B, Hq, N, d] and k [B, Hkv, N, d]")
+    return sq, sk, dev
+
+
+def _positions(positions, B, N, dev):
+    """(pointer, stride between sequences) of positions [N] or [B, N]."""
+    if positions is None:
+        return None, 0
+    shape, stride = positions.shape, positions.stride()
+    if positions.dtype is not torch.int32 or positions.get_device() != dev or tuple(shape) not in ((N,), (B, N)) or \
+            (stride[-1] != 1 and N > 1):
+        raise ValueError(f"positions must be an int32 tensor [{N}] or [{B}, {N}] on the queries' device, rows contiguous")
+    return positions.data_ptr(), stride[0] if len(shape) == 2 and B > 1 else 0
+
+
+def _empty_as(t, stream):
+    """A fresh tensor of t's shape, its tokens in front of its heads in memory where t's are."""
+    B, H, N, d = t.shape
+    if t.stride(1) < t.stride(2):
+        return _empty((B, N, H, d), t.dtype, t, stream).transpose(1, 2)
+    return _empty((B, H, N, d), t.dtype, t, stream)
+
+
+def norm_rotate(q, k, inv_freq, positions=None, q_weight=None, k_weight=None, eps: float = 1e-6, interleaved: bool = False,
+                norm: bool = True, out=None, stream=None):
+    """Queries and keys normed for each head and rotated by their positions: (q', k').
+
+    q: bfloat16 [B, Hq, N, d], k: [B, Hkv, N, d], views with any outer strides that are multiples of 8 (such as
+    transposed slices of a fused projection [B, N, heads, d]).  With r = 1 / sqrt(mean x^2 + eps) a head is
+    y = weight * x * r, and its pairs i (entries i and i + rot / 2, or 2 i and 2 i + 1 where ``interleaved``) turn by
+    position * inv_freq[i].  inv_freq: float64 [rot / 2], or None (the norm alone); rot is a multiple of 16.
+    norm=False: the rotation alone.  positions: int32 [N] or [B, N]; None: 0, 1, ...
+    q_weight, k_weight: float32 or bfloat16 [d]; None: ones.  out: the pair of tensors to write to (the inputs
+    themselves are fine); else fresh contiguous ones, as the attention calls take them.
+    """
+    sq, sk, dev = _check_qk(q, k)
+    plan = _rotation(inv_freq, sq[3], dev, q_weight, k_weight, eps, interleaved, norm)
+    hq, hk = _heads(q, "q", sq, dev), _heads(k, "k", sk, dev)
+    pos, pos_stride = _positions(positions, sq[0], sq[2], dev)
+    if out is None:
+        out = _empty(sq, torch.bfloat16, q, stream), _empty(sk, torch.bfloat16, q, stream)
+    oq, ok = out
+    hoq, hok = _heads(oq, "out", sq, dev), _heads(ok, "out", sk, dev)
+    with _on_device(q):
+        _check(load().fa_norm_rotate(plan, hq, hk, hoq, hok, sq[0], sq[1], sk[1], sq[2], sq[3], pos, pos_stride,
+                                     _stream(stream)))
+    return oq, ok
+
+
+def norm_rotate_backward(q, k, dq_out, dk_out, inv_freq, positions=None, q_weight=None, k_weight=None, eps: float = 1e-6,
+                         interleaved: bool = False, norm: bool = True, out=None, workspace=None, stream=None):
+    """The backward of norm_rotate: (dq, dk, dq_weight, dk_weight).
+
+    q, k: the forward's inputs; dq_out, dk_out: the gradients of its outputs (any strides); the other arguments are
+    the forward's.  dq, dk have the inputs' order of tokens and heads in memory (out: the pair of tensors to
+    write to, such as slices of a fused projection's gradient); dq_weight, dk_weight are float32 [d], or None without weights.
+    workspace: fa_norm_rotate_bwd_workspace_size bytes, for calls that do not overlap; else allocated.
+    """
+    sq, sk, dev = _check_qk(q, k)
+    B, Hq, N, d = sq
+    plan = _rotation(inv_freq, d, dev, q_weight, k_weight, eps, interleaved, norm)
+    hq, hk = _heads(q, "q", sq, dev), _heads(k, "k", sk, dev)
+    hzq, hzk = _heads(dq_out, "dq_out", sq, dev), _heads(dk_out, "dk_out", sk, dev)
+    pos, pos_stride = _positions(positions, B, N, dev)
+    dq, dk = (_empty_as(q, stream), _empty_as(k, stream)) if out is None else out
+    hdq, hdk = _heads(dq, "out", sq, dev), _heads(dk, "out", sk, dev)
+    lib = load()
+    dqw = dkw = ws = None
+    nbytes = 0
+    if q_weight is not None:
+        dqw, dkw = _empty(d, torch.float32, q, stream), _empty(d, torch.float32, q, stream)
+        if workspace is None:
+            workspace = _empty(lib.fa_norm_rotate_bwd_workspace_size(B, Hq, sk[1], N, d), torch.uint8, q, stream)
+        elif workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the queries' device")
+        ws, nbytes = workspace.data_ptr(), workspace.nbytes
+    with _on_device(q):
+        _check(lib.fa_norm_rotate_bwd(plan, hq, hk, hzq, hzk, hdq, hdk, _ptr(dqw), _ptr(dkw), B, Hq, sk[1], N, d, pos,
+                                      pos_stride, ws, nbytes, _stream(stream)))
+    return dq, dk, dqw, dkw
+
+
+def fa_norm_rotate_bwd_workspace_size(B: int, Hq: int, Hkv: int, N: int, d: int) -> int:
+    return int(load().fa_norm_rotate_bwd_workspace_size(B, Hq, Hkv, N, d))
+
+
+def qkv_append(q, k_new, v_new, k_cache, v_cache, block_table, kv_len, q_indptr, inv_freq, positions=None, q_weight=None,
+               k_weight=None, eps: float = 1e-6, interleaved: bool = False, norm: bool = True, k_scale=None, v_scale=None,
+               out=None, stream=None):
+    """norm_rotate and kv_append in one call, for packed rows: returns the queries normed and rotated, bfloat16 [T, Hq, d].
+
+    q: bfloat16 [T, Hq, d]; k_new, v_new: [T, Hkv, d], rows strided alike (slices of a fused projection need no
+    copy).  The keys are normed, rotated and written with the values into the cache, as kv_append writes them;
+    see there for the cache's tensors, kv_len and q_indptr, and norm_rotate for the rest.
+    positions: int32 [T], the tokens' positions for the rotation; None: their places in the cache.
+    out: the tensor to write the queries to; rows behind the last sequence stay as they were (undefined in a fresh one).
+    """
+    kv = _paged(k_cache, v_cache, block_table, kv_len, k_scale, v_scale)
+    dev, d = k_cache.get_device(), kv.d
+    plan = _rotation(inv_freq, d, dev, q_weight, k_weight, eps, interleaved, norm)
+    if q.dim() != 3:
+        raise ValueError("q must be [T, Hq, d]")
+    Hq = q.shape[1]
+    T, q_stride = _check_rows(q, Hq, d, dev, "q")
+    _, stride = rows = _check_rows(k_new, kv.Hkv, d, dev, "k_new")
+    if _check_rows(v_new, kv.Hkv, d, dev, "v_new") != rows or rows[0] != T:
+        raise ValueError("q, k_new and v_new must have the same rows, k_new and v_new the same row stride")
+    indptr = _int32(q_indptr, kv.B + 1, "q_indptr", dev)
+    pos = None if positions is None else _int32(positions, T, "positions", dev)
+    if out is None:
+        out = _empty_like(q, stream) if q.is_contiguous() else _empty((T, Hq, d), torch.bfloat16, q, stream)
+    elif out.dtype is not torch.bfloat16 or out.shape != q.shape or not out.is_contiguous() or out.get_device() != dev:
+        raise ValueError("out must be a contiguous bfloat16 tensor of q's shape")
+    if T:
+        with _on_device(k_cache):
+            _check(load().fa_qkv_append(kv, plan, q.data_ptr(), q_stride, out.data_ptr(), Hq, k_new.data_ptr(),
+                                        v_new.data_ptr(), stride, indptr, pos, T, _stream(stream)))
+    return out
 
 
 def device_status(stream=None):

@@ -316,8 +316,7 @@ int check_cache(const fa_paged_kv* kv, Cache* c) {
   return FA_OK;
 }
 
-// An offsets array of B + 1 entries on the device.
-static int check_indptr(const int32_t* p, const char* name) {
+int check_indptr(const int32_t* p, const char* name) {
   if (!p || (reinterpret_cast<uintptr_t>(p) & 3))
     return set_error(FA_ERR_INVALID_ARG, "%s must be a 4-byte aligned device pointer", name);
   return FA_OK;
