@@ -475,6 +475,50 @@ int fa_qkv_append(const fa_paged_kv* kv, const fa_rotation* rotation, const void
                   const void* k_new, const void* v_new, int64_t new_stride, const int32_t* q_indptr,
                   const int32_t* positions, int T, void* stream);
 
+/*
+ * Accumulated attention weights, and eviction by them (what keeps a cache within a budget; the pages have no
+ * counterpart).  weights: FP32, one for each key vector of the cache, [num_pages][Hkv][page_size], pages weight_stride
+ * floats apart; 4-byte aligned.
+ *
+ * fa_kv_accumulate -- adds what a step's new tokens give each key:
+ *   weight[j] = (j >= kv_len - n ? 0 : weight[j]) + sum over the sequence's n new tokens i and the query heads h of
+ *               the kv head, where i sees j, of exp(scale q_ih . k_j - lse_ih)
+ * so a new token's key starts from zero, and no weight has to be cleared before.
+ *   kv, q, q_stride, q_indptr, T, max_q, Hq, window, sinks, scale : fa_fwd_paged's (v is not read)
+ *   lse      : FP32 [T, Hq], that call's output; -inf (a row that saw no key) weighs nothing
+ * Weights of keys that no new token sees, of sequences without new tokens, and behind a sequence's end stay as they
+ * are.  Sums are FP32, each key's in a fixed order: the same bits in every call on the same data.  Sequences in
+ * one call must not share pages.
+ * workspace  : device scratch of at least fa_kv_accumulate_workspace_size(T, Hq, Hkv, d, dtype) bytes (0 for BF16 caches and
+ *              for invalid sizes), 256-byte aligned (NULL where that is 0); its contents on entry do not matter.
+ *              Calls that may overlap need workspaces of their own.
+ * Over an E4M3 cache q . k is exact but for the FP32 sum and for entries of q under 2^-23 of its head's largest one.
+ * Returns FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED or FA_ERR_CUDA; T = 0 or max_q = 0 launches nothing.
+ */
+size_t fa_kv_accumulate_workspace_size(int T, int Hq, int Hkv, int d, int dtype);
+
+int fa_kv_accumulate(const fa_paged_kv* kv, float* weights, int64_t weight_stride, const void* q, int64_t q_stride,
+                     const float* lse, const int32_t* q_indptr, int T, int max_q, int Hq, int window, int sinks, float scale,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * fa_kv_evict -- of each sequence and kv head, `keep` keys stay: the first `sinks`, the newest `recent`, and of the
+ * others those with the largest weights (of equal ones the first; NaN counts as the largest).  Sequences of at most `keep`
+ * keys keep all.  The kept vectors of K and V, their scales and weights go, in order, to the positions 0, 1, ...
+ * of the sequence: each head keeps keys of its own, and the lengths stay the same for all heads.
+ *   table_out : int32 [B][max_pages_out], rows table_out_stride apart: the pages to move to, with room for
+ *               min(keep, max_pages * page_size) keys; pages of the same pool that no sequence of the call has in
+ *               block_table.  The source pages stay as they are (and may be shared by sequences).  NULL, or
+ *               block_table itself: in place; no page may then belong to two sequences.
+ *   kept_len  : output, int32 [B]: min(kv_len, keep), the new lengths (kv_len is not written, and kept_len is not kv_len)
+ *   kept      : output, int32 [B, Hkv, keep]: the position of each kept key, -1 behind kept_len
+ *   sinks + recent <= keep
+ * Slots behind the new length stay as they were.  Returns FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED or FA_ERR_CUDA.
+ */
+int fa_kv_evict(const fa_paged_kv* kv, float* weights, int64_t weight_stride, const int32_t* table_out,
+                int64_t table_out_stride, int max_pages_out, int keep, int sinks, int recent, int32_t* kept_len,
+                int32_t* kept, void* stream);
+
 /* Message for the last non-OK return on the calling thread ("" if none). */
 const char* fa_last_error(void);
 

@@ -34,7 +34,8 @@ EXPORTS = ("fa_fwd", "fa_fwd_window", "fa_fwd_fp8", "fa_quantize_fp8", "fa_bwd",
            "fa_bwd_noalloc", "fa_bwd_noalloc_status", "fa_bwd_workspace_size", "fa_device_status",
            "fa_device_report_read", "fa_last_error", "fa_version", "fa_kv_append", "fa_kv_read",
            "fa_fwd_paged", "fa_fwd_paged_workspace_size", "fa_norm_rotate", "fa_norm_rotate_bwd",
-           "fa_norm_rotate_bwd_workspace_size", "fa_qkv_append")
+           "fa_norm_rotate_bwd_workspace_size", "fa_qkv_append", "fa_kv_accumulate",
+           "fa_kv_accumulate_workspace_size", "fa_kv_evict")
 
 # size of the fixed device scratch behind fa_bwd_noalloc (FA_NOALLOC_SCRATCH_BYTES in fa.h)
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
@@ -138,6 +139,12 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.fa_norm_rotate_bwd.restype = ci
     L.fa_qkv_append.argtypes = [ctypes.POINTER(PagedKV), rotation, vp, c64, vp, ci, vp, vp, c64, vp, vp, ci, vp]
     L.fa_qkv_append.restype = ci
+    L.fa_kv_accumulate_workspace_size.argtypes = [ci] * 5
+    L.fa_kv_accumulate_workspace_size.restype = cs
+    L.fa_kv_accumulate.argtypes = [ctypes.POINTER(PagedKV), vp, c64, vp, c64, vp, vp, ci, ci, ci, ci, ci, cf, vp, cs, vp]
+    L.fa_kv_accumulate.restype = ci
+    L.fa_kv_evict.argtypes = [ctypes.POINTER(PagedKV), vp, c64, vp, c64, ci, ci, ci, ci, vp, vp, vp]
+    L.fa_kv_evict.restype = ci
     L.fa_bwd_noalloc.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, cf, vp]
     L.fa_bwd_noalloc.restype = ci
     L.fa_device_status.argtypes = [vp]
@@ -757,6 +764,104 @@ def qkv_append(q, k_new, v_new, k_cache, v_cache, block_table, kv_len, q_indptr,
             _check(load().fa_qkv_append(kv, plan, q.data_ptr(), q_stride, out.data_ptr(), Hq, k_new.data_ptr(),
                                         v_new.data_ptr(), stride, indptr, pos, T, _stream(stream)))
     return out
+
+
+# ----------------------------------------------------------------- accumulated attention weights, eviction
+
+def fa_kv_accumulate_workspace_size(T: int, Hq: int, Hkv: int, d: int, dtype: int = FA_KV_BF16) -> int:
+    return int(load().fa_kv_accumulate_workspace_size(T, Hq, Hkv, d, dtype))
+
+
+def _weights(weights, kv, k_cache):
+    """(pointer, page stride) of a cache's accumulated weights."""
+    shape, stride = k_cache.shape, weights.stride()
+    if weights.dtype is not torch.float32 or weights.shape != shape[:3] or weights.get_device() != k_cache.get_device():
+        raise ValueError("weights must be a float32 tensor [pages, Hkv, page_size] on the cache's device")
+    if (shape[2] != 1 and stride[2] != 1) or (shape[1] != 1 and stride[1] != shape[2]):
+        raise ValueError("weights: pages must be contiguous")
+    return weights.data_ptr(), _outer(shape[0], stride[0], kv.Hkv * kv.page_size, "weights")
+
+
+def kv_accumulate(weights, q, lse, k_cache, v_cache, block_table, kv_len, q_indptr, max_q, k_scale=None, v_scale=None,
+                  scale=None, window=None, sinks: int = 0, workspace=None, stream=None):
+    """Add to each cached key the attention weight that the new tokens give it (in place; returns weights).
+
+    weights: float32 [pages, Hkv, page_size], one for each key of the cache.  For key j of a sequence and kv head:
+    weights[j] = (0 if j is a new token's else weights[j]) + the sum over the new tokens i that see j and the
+    query heads of the kv head of exp(scale q_i . k_j - lse_i).
+    q, lse and the other arguments are those of forward_paged and its output; the cache holds the new keys.
+    workspace: fa_kv_accumulate_workspace_size bytes (E4M3 caches), for calls that do not overlap; else allocated.
+    """
+    kv = _paged(k_cache, v_cache, block_table, kv_len, k_scale, v_scale)
+    at, weight_stride = _weights(weights, kv, k_cache)
+    if window is None:
+        if sinks:
+            raise ValueError("sinks need a window")
+        window = 0
+    elif window < 1:
+        raise ValueError("window must be >= 1 (None: no window)")
+    dev, d = k_cache.get_device(), kv.d
+    if q.dim() != 3:
+        raise ValueError("q must be [T, Hq, d]")
+    Hq = q.shape[1]
+    T, stride = _check_rows(q, Hq, d, dev, "q")
+    if lse.dtype is not torch.float32 or lse.shape != q.shape[:2] or not lse.is_contiguous() or lse.get_device() != dev:
+        raise ValueError("lse must be a contiguous float32 tensor [T, Hq]")
+    indptr = _int32(q_indptr, kv.B + 1, "q_indptr", dev)
+    if T == 0:
+        return weights
+    lib = load()
+    if workspace is None:
+        n = lib.fa_kv_accumulate_workspace_size(T, Hq, kv.Hkv, d, kv.dtype) if kv.dtype == FA_KV_E4M3 else 0
+        workspace = _empty(n, torch.uint8, q, stream) if n else None
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the cache's device")
+    ws, nbytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    with _on_device(k_cache):
+        _check(lib.fa_kv_accumulate(kv, at, weight_stride, q.data_ptr(), stride, lse.data_ptr(), indptr, T, _c_int(max_q), Hq,
+                                    _c_int(window), _c_int(sinks), 1.0 / math.sqrt(d) if scale is None else float(scale),
+                                    ws, nbytes, _stream(stream)))
+    return weights
+
+
+def kv_evict(weights, k_cache, v_cache, block_table, kv_len, keep, sinks: int = 0, recent: int = 0, table_out=None,
+             k_scale=None, v_scale=None, kept_len=None, kept=None, stream=None):
+    """Cut each sequence's cache to ``keep`` keys for each kv head: (kept_len, kept).
+
+    The first ``sinks`` keys, the newest ``recent`` ones and, of the others, those with the largest weights (of equal
+    ones the first) move in order, with their values, scales and weights, to the positions 0, 1, ... of the sequence
+    in table_out: int32 [B, pages], free pages of the same pool; None: in place, where no two sequences share pages.
+    weights: float32 [pages, Hkv, page_size] (kv_accumulate).
+    kept_len: int32 [B], min(kv_len, keep): the lengths for the calls that follow (kv_len itself is not
+    written).  kept: int32 [B, Hkv, keep], the kept keys' former positions, -1 behind kept_len.  Both are
+    allocated unless given.  Later tokens keep their own rotation: pass their positions to qkv_append.
+    """
+    kv = _paged(k_cache, v_cache, block_table, kv_len, k_scale, v_scale)
+    at, weight_stride = _weights(weights, kv, k_cache)
+    dev = k_cache.get_device()
+    out = out_stride = pages = 0
+    if table_out is not None:
+        rows = table_out.stride()
+        if table_out.dtype is not torch.int32 or len(rows) != 2 or table_out.shape[0] != kv.B or \
+                (rows[1] != 1 and table_out.shape[1] != 1) or table_out.get_device() != dev:
+            raise ValueError("table_out must be an int32 tensor [B, pages] on the cache's device, rows contiguous")
+        pages = table_out.shape[1]
+        out, out_stride = table_out.data_ptr(), _outer(kv.B, rows[0], pages, "table_out")
+    keep = int(keep)
+    if not 1 <= keep < 2 ** 31:
+        raise ValueError("keep must be from 1 to 2^31 - 1")
+    if kept_len is None:
+        kept_len = _empty(kv.B, torch.int32, k_cache, stream)
+    else:
+        _int32(kept_len, kv.B, "kept_len", dev)
+    if kept is None:
+        kept = _empty((kv.B, kv.Hkv, keep), torch.int32, k_cache, stream)
+    elif kept.dtype is not torch.int32 or kept.shape != (kv.B, kv.Hkv, keep) or not kept.is_contiguous() or kept.get_device() != dev:
+        raise ValueError("kept must be a contiguous int32 tensor [B, Hkv, keep] on the cache's device")
+    with _on_device(k_cache):
+        _check(load().fa_kv_evict(kv, at, weight_stride, out or None, out_stride, pages, keep, _c_int(sinks), _c_int(recent),
+                                  kept_len.data_ptr(), kept.data_ptr(), _stream(stream)))
+    return kept_len, kept
 
 
 def device_status(stream=None):

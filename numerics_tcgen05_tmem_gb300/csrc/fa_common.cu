@@ -164,6 +164,15 @@ int make_tmap_rows(CUtensorMap* map, const void* base, int tokens, int heads, in
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+int make_tmap_pieces(CUtensorMap* map, const void* base, int tokens, int heads, int d, int pieces, int box_heads,
+                     int box_tokens) {
+  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens, (cuuint64_t)pieces};
+  const cuuint64_t strides[3] = {(cuuint64_t)d, (cuuint64_t)heads * d, (cuuint64_t)tokens * heads * d};
+  const cuuint32_t box[4] = {(cuuint32_t)d, (cuuint32_t)box_heads, (cuuint32_t)box_tokens, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, base, dims, strides, box,
+                d >= 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
 int make_tmap_bhnd(CUtensorMap* map, const void* base, int BH, int N, int d, int box_rows) {
   return encode_3d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, BH, N, d, 64, box_rows);
 }

@@ -68,6 +68,11 @@ int make_tmap_pages(CUtensorMap* map, const void* base, bool fp8, int d, int pag
 int make_tmap_rows(CUtensorMap* map, const void* base, int tokens, int heads, int d, long long stride, int box_heads,
                    int box_tokens);
 
+// Encode a 4-D tensor map over `pieces` contiguous 1-byte copies of rows [tokens, heads, d], swizzled as
+// make_tmap_u8_bhnd does, and a (d x box_heads x box_tokens x 1) box; tokens out of range read as zeros.
+int make_tmap_pieces(CUtensorMap* map, const void* base, int tokens, int heads, int d, int pieces, int box_heads,
+                     int box_tokens);
+
 // Common argument checks for [B,H,N,d] problems.
 int check_shape(int B, int H, int N, int d);
 int check_window(int window, int sinks);

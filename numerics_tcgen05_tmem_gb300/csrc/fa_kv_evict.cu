@@ -1,0 +1,340 @@
+// Eviction from a paged cache by accumulated attention weight (fa_kv_evict): of each sequence and kv head `keep`
+// keys stay -- the first `sinks`, the newest `recent`, and of the others those with the largest weights (of equal
+// ones the first) -- and move, in order, to the first positions of the sequence in another block table, or
+// in the same one.
+//
+//   select  a CTA per (sequence, kv head): the smallest weight that stays, by three passes over the weights' bits
+//           (11, 11 and 10 of them, a histogram each in shared memory), then one pass in order that writes the
+//           kept positions.
+//   move    the kept vectors, their scales and weights: bandwidth work, 16 bytes a thread.
+// In place a vector only ever moves to a lower position, to where nothing is that is still to be read as long
+// as the vectors are taken in order: a CTA takes all of one head's K or V, 64 bytes wide, step by step, and
+// waits between a step's loads and its stores.
+#include <algorithm>
+
+#include "paged_attn.cuh"
+
+namespace fa {
+namespace paged {
+
+constexpr int kSelectThreads = 512;
+constexpr int kDigit = 11, kBins = 1 << kDigit;
+
+struct Evict {
+  Cache c;
+  float* weights;
+  long long weight_stride;
+  const int32_t* table_out;      // [B][..], rows table_out_stride apart
+  long long table_out_stride;
+  int max_pages_out;
+  int keep, sinks, recent;
+  int32_t* kept_len;             // [B]
+  int32_t* kept;                 // [B][Hkv][keep]
+};
+
+// Weights in the order of unsigned integers; NaN is the largest, -0 is 0.
+__device__ __forceinline__ uint32_t weight_order(float w) {
+  if (w != w) return 0xFFFFFFFFu;
+  const uint32_t u = __float_as_uint(w + 0.f);
+  return u ^ ((int)u < 0 ? 0xFFFFFFFFu : 0x80000000u);
+}
+
+// A sequence's length: 0, recorded, where it is out of range.
+__device__ __forceinline__ int evict_length(const Cache& c, int b) {
+  const int n = __ldg(c.kv_len + b);
+  if (n < 0 || n > c.max_pages << c.page_shift) {
+    if (threadIdx.x == 0) report_bounds(c.status, kSitePagedLen, n);
+    return 0;
+  }
+  return n;
+}
+
+__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __grid_constant__ Evict g) {
+  constexpr int kWarps = kSelectThreads / 32;
+  __shared__ uint32_t bins[kBins];
+  __shared__ int warp_sum[2][kWarps];
+  __shared__ int found_bin, found_above;
+  const int b = blockIdx.x / g.c.Hkv, h = blockIdx.x - b * g.c.Hkv;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int n = evict_length(g.c, b), kept = min(n, g.keep);
+  int32_t* out = g.kept + (long long)blockIdx.x * g.keep;
+  if (h == 0 && threadIdx.x == 0) g.kept_len[b] = kept;
+  for (int i = kept + (int)threadIdx.x; i < g.keep; i += kSelectThreads) out[i] = -1;
+  if (n <= g.keep) {
+    for (int i = threadIdx.x; i < n; i += kSelectThreads) out[i] = i;
+    return;
+  }
+  const int page_mask = (1 << g.c.page_shift) - 1;
+  auto order_at = [&](int key) {
+    const int page = __ldg(g.c.table + b * g.c.table_stride + (key >> g.c.page_shift));
+    if (page < 0 || page >= g.c.num_pages) {
+      report_bounds(g.c.status, kSitePagedEvict, page);
+      return 0u;
+    }
+    return weight_order(g.weights[page * g.weight_stride + ((long long)h << g.c.page_shift) + (key & page_mask)]);
+  };
+  // the candidates [lo, hi), of which `want` stay: those above `limit`, and the first `ties` that equal it
+  const int lo = g.sinks, hi = n - g.recent, want = g.keep - g.sinks - g.recent;
+  uint32_t limit = 0xFFFFFFFFu;
+  int ties = 0;
+  if (want > 0) {
+    uint32_t prefix = 0;
+    int left = want, shift = 32;
+    for (int pass = 0; pass < 3; ++pass) {
+      const int digit = pass < 2 ? kDigit : 32 - 2 * kDigit;
+      const int above = shift;          // bits from here on are settled
+      shift -= digit;
+      for (int i = threadIdx.x; i < kBins; i += kSelectThreads) bins[i] = 0;
+      __syncthreads();
+      for (int key = lo + (int)threadIdx.x; key < hi; key += kSelectThreads) {
+        const uint32_t x = order_at(key);
+        if (pass == 0 || (x >> above) == prefix) atomicAdd(&bins[x >> shift & ((1 << digit) - 1)], 1u);
+      }
+      __syncthreads();
+      // from the largest bin down: the one in which the count reaches `left`.  A thread has kBins / threads bins.
+      constexpr int kPer = kBins / kSelectThreads;
+      const int top = kBins - 1 - (int)threadIdx.x * kPer;
+      int mine = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) mine += (int)bins[top - i];
+      int incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const int x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+      }
+      if (lane == 31) warp_sum[0][warp] = incl;
+      __syncthreads();
+      int before = incl - mine;
+      for (int w = 0; w < warp; ++w) before += warp_sum[0][w];
+      if (before < left && before + mine >= left) {
+        int i = 0;
+        while (before + (int)bins[top - i] < left) before += (int)bins[top - i++];
+        found_bin = top - i;
+        found_above = before;
+      }
+      __syncthreads();
+      prefix = prefix << digit | (uint32_t)found_bin;
+      left -= found_above;
+    }
+    limit = prefix;
+    ties = left;
+  }
+  // in order: what stays, 512 positions at a time
+  int placed = 0, tied = 0;    // before this step
+  for (int base = 0; base < n; base += kSelectThreads) {
+    const int key = base + (int)threadIdx.x;
+    bool stays = key < n && (key < lo || key >= hi), equal = false;
+    if (key < n && !stays && want > 0) {
+      const uint32_t x = order_at(key);
+      stays = x > limit;
+      equal = x == limit;
+    }
+    const uint32_t equals = __ballot_sync(0xffffffffu, equal), sure = __ballot_sync(0xffffffffu, stays);
+    if (lane == 0) {
+      warp_sum[0][warp] = __popc(equals);
+      warp_sum[1][warp] = __popc(sure);
+    }
+    __syncthreads();
+    int eq_before = tied, at = placed;
+    for (int w = 0; w < kWarps; ++w) {
+      const int e = warp_sum[0][w], s = warp_sum[1][w];
+      if (w < warp) {
+        at += s + max(min(e, ties - eq_before), 0);
+        eq_before += e;
+      }
+      placed += s + max(min(e, ties - tied), 0);
+      tied += e;
+    }
+    const uint32_t lower = low_bits(lane);
+    const int my_eq = eq_before + __popc(equals & lower);
+    if (equal && my_eq < ties) stays = true;
+    // of this warp's lower lanes: the sure ones, and the equal ones that are still wanted
+    at += __popc(sure & lower) + max(min(my_eq, ties) - min(eq_before, ties), 0);
+    if (stays) out[at] = key;
+    __syncthreads();
+  }
+}
+
+// Where a key lies: its page and its offset within a page's head; page -1, recorded, where there is none.
+struct Spot {
+  int page, slot;
+};
+__device__ __forceinline__ Spot spot_of(const Cache& c, const int32_t* table, long long stride, int max_pages, int b, int key) {
+  const int i = key >> c.page_shift;
+  Spot s{-1, key & ((1 << c.page_shift) - 1)};
+  if (key < 0 || i >= max_pages) {
+    report_bounds(c.status, kSitePagedEvict, key);
+    return s;
+  }
+  s.page = __ldg(table + b * stride + i);
+  if (s.page < 0 || s.page >= c.num_pages) {
+    report_bounds(c.status, kSitePagedEvict, s.page);
+    s.page = -1;
+  }
+  return s;
+}
+
+// Into other pages.  A CTA has kMoveVecs kept keys of one (sequence, kv head), K and V; kRow / 16 lanes a vector.
+constexpr int kMoveThreads = 256, kMoveVecs = 64;
+
+template <int kRow>    // bytes of a vector
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ Evict g, int chunks) {
+  constexpr int kLanes = kRow / 16, kGroups = kMoveThreads / kLanes, kUnroll = 4;
+  __shared__ Spot from[kMoveVecs], to[kMoveVecs];
+  const int item = blockIdx.x / chunks, first = (blockIdx.x - item * chunks) * kMoveVecs;
+  const int b = item / g.c.Hkv, h = item - b * g.c.Hkv;
+  const int here = min(__ldg(g.kept_len + b) - first, kMoveVecs);
+  if (here <= 0) return;
+  const long long page_size = 1ll << g.c.page_shift;
+  if ((int)threadIdx.x < here) {
+    const int key = g.kept[(long long)item * g.keep + first + threadIdx.x];
+    const Spot f = spot_of(g.c, g.c.table, g.c.table_stride, g.c.max_pages, b, key);
+    Spot t = spot_of(g.c, g.table_out, g.table_out_stride, g.max_pages_out, b, first + threadIdx.x);
+    if (f.page < 0) t.page = -1;
+    from[threadIdx.x] = f;
+    to[threadIdx.x] = t;
+    if (t.page >= 0) {
+      const long long f_at = h * page_size + f.slot, t_at = h * page_size + t.slot;
+      g.weights[t.page * g.weight_stride + t_at] = g.weights[f.page * g.weight_stride + f_at];
+      if (g.c.k_scale != nullptr) {
+        g.c.k_scale[t.page * g.c.scale_stride + t_at] = g.c.k_scale[f.page * g.c.scale_stride + f_at];
+        g.c.v_scale[t.page * g.c.scale_stride + t_at] = g.c.v_scale[f.page * g.c.scale_stride + f_at];
+      }
+    }
+  }
+  __syncthreads();
+  const int elem = g.c.k_scale != nullptr ? 1 : 2;
+  const int col = threadIdx.x % kLanes * 16;
+  const long long page_bytes = g.c.page_stride * elem;
+  for (int i0 = threadIdx.x / kLanes; i0 < 2 * here; i0 += kUnroll * kGroups) {
+    uint4 x[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int i = i0 + u * kGroups, v = i >> 1;
+      if (i < 2 * here && to[v].page >= 0)
+        x[u] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>((i & 1) ? g.c.v : g.c.k) + from[v].page * page_bytes +
+                                               (h * page_size + from[v].slot) * kRow + col);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int i = i0 + u * kGroups, v = i >> 1;
+      if (i < 2 * here && to[v].page >= 0)
+        *reinterpret_cast<uint4*>(static_cast<uint8_t*>((i & 1) ? g.c.v : g.c.k) + to[v].page * page_bytes +
+                                  (h * page_size + to[v].slot) * kRow + col) = x[u];
+    }
+  }
+}
+
+// Within the same pages.  A CTA has one (sequence, kv head), K or V, 64 bytes of each vector; the first slice's
+// CTAs also move the scales, that of K the weights.
+constexpr int kSlice = 64;
+
+__global__ void __launch_bounds__(kMoveThreads) evict_shift_kernel(const __grid_constant__ Evict g, int row_bytes) {
+  constexpr int kLanes = kSlice / 16, kGroups = kMoveThreads / kLanes, kUnroll = 4, kStep = kGroups * kUnroll;
+  const int slices = row_bytes / kSlice;
+  const int slice = blockIdx.x % slices, is_v = blockIdx.x / slices % 2, item = blockIdx.x / slices / 2;
+  const int b = item / g.c.Hkv, h = item - b * g.c.Hkv;
+  const int kept = __ldg(g.kept_len + b);
+  const int32_t* keys = g.kept + (long long)item * g.keep;
+  const int group = threadIdx.x / kLanes, lane = threadIdx.x % kLanes, col = slice * kSlice + lane * 16;
+  const long long page_size = 1ll << g.c.page_shift;
+  const long long page_bytes = g.c.page_stride * (g.c.k_scale != nullptr ? 1 : 2);
+  uint8_t* pool = static_cast<uint8_t*>(is_v ? g.c.v : g.c.k);
+  float* scales = is_v ? g.c.v_scale : g.c.k_scale;
+  const bool moves_scale = scales != nullptr && slice == 0 && lane == 0, moves_weight = !is_v && slice == 0 && lane == 1;
+  for (int i0 = 0; i0 < kept; i0 += kStep) {
+    uint4 x[kUnroll];
+    float s[kUnroll];
+    Spot to[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int i = i0 + u * kGroups + group;
+      to[u].page = -1;
+      if (i >= kept) continue;
+      const int key = keys[i];
+      if (key == i) continue;            // it stays where it is
+      const Spot f = spot_of(g.c, g.c.table, g.c.table_stride, g.c.max_pages, b, key);
+      if (f.page < 0) continue;
+      to[u] = spot_of(g.c, g.c.table, g.c.table_stride, g.c.max_pages, b, i);
+      const long long at = h * page_size + f.slot;
+      x[u] = *reinterpret_cast<const uint4*>(pool + f.page * page_bytes + at * row_bytes + col);
+      if (moves_scale) s[u] = scales[f.page * g.c.scale_stride + at];
+      if (moves_weight) s[u] = g.weights[f.page * g.weight_stride + at];
+    }
+    __syncthreads();   // every load of this step comes before its stores; those of the next step read higher positions
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      if (to[u].page < 0) continue;
+      const long long at = h * page_size + to[u].slot;
+      *reinterpret_cast<uint4*>(pool + to[u].page * page_bytes + at * row_bytes + col) = x[u];
+      if (moves_scale) scales[to[u].page * g.c.scale_stride + at] = s[u];
+      if (moves_weight) g.weights[to[u].page * g.weight_stride + at] = s[u];
+    }
+  }
+}
+
+}  // namespace paged
+}  // namespace fa
+
+extern "C" int fa_kv_evict(const fa_paged_kv* kv, float* weights, int64_t weight_stride, const int32_t* table_out,
+                           int64_t table_out_stride, int max_pages_out, int keep, int sinks, int recent, int32_t* kept_len,
+                           int32_t* kept, void* stream) {
+  fa::NvtxRange nvtx_range("fa_kv_evict");
+  using namespace fa;
+  clear_error();
+  paged::Evict g{};
+  int rc;
+  if ((rc = paged::check_cache(kv, &g.c))) return rc;
+  const long long page = (long long)kv->Hkv * kv->page_size;
+  if (!weights || (reinterpret_cast<uintptr_t>(weights) & 3))
+    return set_error(FA_ERR_INVALID_ARG, "weights must be a 4-byte aligned device pointer");
+  if (weight_stride < page)
+    return set_error(FA_ERR_INVALID_ARG, "weight_stride %lld must be at least Hkv*page_size = %lld", (long long)weight_stride, page);
+  if (keep < 1 || sinks < 0 || recent < 0) return set_error(FA_ERR_INVALID_ARG, "keep must be >= 1, sinks and recent >= 0 (got %d, %d, %d)", keep, sinks, recent);
+  if ((long long)sinks + recent > keep)
+    return set_error(FA_ERR_INVALID_ARG, "sinks + recent = %lld must be at most keep = %d", (long long)sinks + recent, keep);
+  const bool in_place = !table_out || table_out == kv->block_table;
+  const long long max_kv = (long long)kv->max_pages * kv->page_size;
+  if (!in_place) {
+    if (reinterpret_cast<uintptr_t>(table_out) & 3) return set_error(FA_ERR_INVALID_ARG, "table_out is not 4-byte aligned");
+    if (max_pages_out < 1 || table_out_stride < max_pages_out)
+      return set_error(FA_ERR_INVALID_ARG, "table_out_stride %lld is less than max_pages_out %d, or that is under 1",
+                       (long long)table_out_stride, max_pages_out);
+    const long long need = keep < max_kv ? keep : max_kv;
+    if ((long long)max_pages_out * kv->page_size < need)
+      return set_error(FA_ERR_INVALID_ARG, "table_out has room for %lld keys of a sequence, %lld may be kept",
+                       (long long)max_pages_out * kv->page_size, need);
+  }
+  if (!kept_len || !kept || ((reinterpret_cast<uintptr_t>(kept_len) | reinterpret_cast<uintptr_t>(kept)) & 3))
+    return set_error(FA_ERR_INVALID_ARG, "kept_len and kept must be 4-byte aligned device pointers");
+  if (kept_len == kv->kv_len)   // every head's CTA reads the length
+    return set_error(FA_ERR_INVALID_ARG, "kept_len must not be kv_len itself");
+  const long long items = (long long)kv->B * kv->Hkv, most = keep < max_kv ? keep : max_kv;
+  const long long chunks = (most + paged::kMoveVecs - 1) / paged::kMoveVecs;
+  if (items * std::max(chunks, 8ll) >= (1ll << 31))
+    return set_error(FA_ERR_INVALID_ARG, "B*Hkv*keep/%d must be < 2^31", paged::kMoveVecs);
+  g.c.status = device_status_word();
+  if (!g.c.status) return set_error(FA_ERR_CUDA, "could not allocate the device status record");
+  g.weights = weights;
+  g.weight_stride = weight_stride;
+  g.table_out = in_place ? kv->block_table : table_out;
+  g.table_out_stride = in_place ? kv->table_stride : table_out_stride;
+  g.max_pages_out = in_place ? kv->max_pages : max_pages_out;
+  g.keep = keep;
+  g.sinks = sinks;
+  g.recent = recent;
+  g.kept_len = kept_len;
+  g.kept = kept;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  paged::evict_select_kernel<<<(unsigned)items, paged::kSelectThreads, 0, s>>>(g);
+  if ((rc = check_cuda(cudaGetLastError(), "launch evict_select_kernel"))) return rc;
+  const int row = kv->d * (kv->dtype == FA_KV_E4M3 ? 1 : 2);
+  if (in_place) {
+    paged::evict_shift_kernel<<<(unsigned)(items * 2 * (row / paged::kSlice)), paged::kMoveThreads, 0, s>>>(g, row);
+    return check_cuda(cudaGetLastError(), "launch evict_shift_kernel");
+  }
+  auto kern = row == 64 ? paged::evict_move_kernel<64> : (row == 128 ? paged::evict_move_kernel<128> : paged::evict_move_kernel<256>);
+  kern<<<(unsigned)(items * chunks), paged::kMoveThreads, 0, s>>>(g, (int)chunks);
+  return check_cuda(cudaGetLastError(), "launch evict_move_kernel");
+}

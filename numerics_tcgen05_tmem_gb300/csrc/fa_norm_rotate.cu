@@ -145,8 +145,13 @@ __device__ __forceinline__ void fill_angles(const Table& t, int rot, int tokens,
   for (int i = threadIdx.x; i < tokens * half; i += kThreads) {
     const int token = i / half, f = i - token * half;
     const uint64_t at = (uint64_t)(int64_t)position(token) * t.turns[f];
-    float s, c;
-    sincospif((float)(int32_t)(at >> 32) * 0x1p-31f, &s, &c);   // a turn is 2^32, sincospi's is 2
+    // the nearest quarter turn apart, the rest is within an eighth: its rounding to FP32 stays under 2^-25 rad
+    const uint32_t u = (uint32_t)(at >> 32), quarter = (u + 0x20000000u) >> 30;
+    float s0, c0;
+    sincospif((float)(int32_t)(u - (quarter << 30)) * 0x1p-31f, &s0, &c0);   // a turn is 2^32, sincospi's is 2
+    float s = quarter & 1 ? c0 : s0, c = quarter & 1 ? s0 : c0;
+    if (quarter & 2) s = -s;
+    if ((quarter + 1) & 2) c = -c;
     t.cos[i] = c;
     t.sin[i] = s;
   }
