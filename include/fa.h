@@ -478,7 +478,7 @@ int fa_qkv_append(const fa_paged_kv* kv, const fa_rotation* rotation, const void
 /*
  * Accumulated attention weights, and eviction by them (what keeps a cache within a budget; the pages have no
  * counterpart).  weights: FP32, one for each key vector of the cache, [num_pages][Hkv][page_size], pages weight_stride
- * floats apart; 4-byte aligned.
+ * floats apart (a multiple of 4); 16-byte aligned.
  *
  * fa_kv_accumulate -- adds what a step's new tokens give each key:
  *   weight[j] = (j >= kv_len - n ? 0 : weight[j]) + sum over the sequence's n new tokens i and the query heads h of
@@ -489,13 +489,14 @@ int fa_qkv_append(const fa_paged_kv* kv, const fa_rotation* rotation, const void
  * Weights of keys that no new token sees, of sequences without new tokens, and behind a sequence's end stay as they
  * are.  Sums are FP32, each key's in a fixed order: the same bits in every call on the same data.  Sequences in
  * one call must not share pages.
- * workspace  : device scratch of at least fa_kv_accumulate_workspace_size(T, Hq, Hkv, d, dtype) bytes (0 for BF16 caches and
- *              for invalid sizes), 256-byte aligned (NULL where that is 0); its contents on entry do not matter.
- *              Calls that may overlap need workspaces of their own.
- * Over an E4M3 cache q . k is exact but for the FP32 sum and for entries of q under 2^-23 of its head's largest one.
+ * workspace  : device scratch of at least fa_kv_accumulate_workspace_size(T, max_q, Hq, Hkv, d, dtype) bytes (0 where none is
+ *              needed and for invalid sizes), 256-byte aligned (NULL where that is 0); its contents on entry do
+ *              not matter.  Calls that may overlap need workspaces of their own.
+ * q . k is exact but for its FP32 sum, and, for few rows over an E4M3 cache, entries of q under 2^-23 of the head's
+ * largest one.
  * Returns FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED or FA_ERR_CUDA; T = 0 or max_q = 0 launches nothing.
  */
-size_t fa_kv_accumulate_workspace_size(int T, int Hq, int Hkv, int d, int dtype);
+size_t fa_kv_accumulate_workspace_size(int T, int max_q, int Hq, int Hkv, int d, int dtype);
 
 int fa_kv_accumulate(const fa_paged_kv* kv, float* weights, int64_t weight_stride, const void* q, int64_t q_stride,
                      const float* lse, const int32_t* q_indptr, int T, int max_q, int Hq, int window, int sinks, float scale,

@@ -139,7 +139,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.fa_norm_rotate_bwd.restype = ci
     L.fa_qkv_append.argtypes = [ctypes.POINTER(PagedKV), rotation, vp, c64, vp, ci, vp, vp, c64, vp, vp, ci, vp]
     L.fa_qkv_append.restype = ci
-    L.fa_kv_accumulate_workspace_size.argtypes = [ci] * 5
+    L.fa_kv_accumulate_workspace_size.argtypes = [ci] * 6
     L.fa_kv_accumulate_workspace_size.restype = cs
     L.fa_kv_accumulate.argtypes = [ctypes.POINTER(PagedKV), vp, c64, vp, c64, vp, vp, ci, ci, ci, ci, ci, cf, vp, cs, vp]
     L.fa_kv_accumulate.restype = ci
@@ -768,8 +768,8 @@ def qkv_append(q, k_new, v_new, k_cache, v_cache, block_table, kv_len, q_indptr,
 
 # ----------------------------------------------------------------- accumulated attention weights, eviction
 
-def fa_kv_accumulate_workspace_size(T: int, Hq: int, Hkv: int, d: int, dtype: int = FA_KV_BF16) -> int:
-    return int(load().fa_kv_accumulate_workspace_size(T, Hq, Hkv, d, dtype))
+def fa_kv_accumulate_workspace_size(T: int, max_q: int, Hq: int, Hkv: int, d: int, dtype: int = FA_KV_BF16) -> int:
+    return int(load().fa_kv_accumulate_workspace_size(T, _c_int(max_q), Hq, Hkv, d, dtype))
 
 
 def _weights(weights, kv, k_cache):
@@ -790,7 +790,7 @@ def kv_accumulate(weights, q, lse, k_cache, v_cache, block_table, kv_len, q_indp
     weights[j] = (0 if j is a new token's else weights[j]) + the sum over the new tokens i that see j and the
     query heads of the kv head of exp(scale q_i . k_j - lse_i).
     q, lse and the other arguments are those of forward_paged and its output; the cache holds the new keys.
-    workspace: fa_kv_accumulate_workspace_size bytes (E4M3 caches), for calls that do not overlap; else allocated.
+    workspace: fa_kv_accumulate_workspace_size bytes, for calls that do not overlap; else allocated.
     """
     kv = _paged(k_cache, v_cache, block_table, kv_len, k_scale, v_scale)
     at, weight_stride = _weights(weights, kv, k_cache)
@@ -810,15 +810,15 @@ def kv_accumulate(weights, q, lse, k_cache, v_cache, block_table, kv_len, q_indp
     indptr = _int32(q_indptr, kv.B + 1, "q_indptr", dev)
     if T == 0:
         return weights
-    lib = load()
+    lib, max_q = load(), _c_int(max_q)
     if workspace is None:
-        n = lib.fa_kv_accumulate_workspace_size(T, Hq, kv.Hkv, d, kv.dtype) if kv.dtype == FA_KV_E4M3 else 0
+        n = lib.fa_kv_accumulate_workspace_size(T, max_q, Hq, kv.Hkv, d, kv.dtype)
         workspace = _empty(n, torch.uint8, q, stream) if n else None
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the cache's device")
     ws, nbytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
     with _on_device(k_cache):
-        _check(lib.fa_kv_accumulate(kv, at, weight_stride, q.data_ptr(), stride, lse.data_ptr(), indptr, T, _c_int(max_q), Hq,
+        _check(lib.fa_kv_accumulate(kv, at, weight_stride, q.data_ptr(), stride, lse.data_ptr(), indptr, T, max_q, Hq,
                                     _c_int(window), _c_int(sinks), 1.0 / math.sqrt(d) if scale is None else float(scale),
                                     ws, nbytes, _stream(stream)))
     return weights

@@ -6,15 +6,19 @@
 // S^T = K Q^T on the tensor core: the keys are the 128 rows of the instruction, a row of tensor memory and a thread
 // each, so that a key's sum needs no exchange between threads, and a single token's few query heads are the
 // narrow side (16, 32 or 64 columns; 128 for chunks).  One kernel serves both:
-//   * a unit is 256 keys (two tiles) of one sequence and kv head; a persistent CTA takes a share of the
-//     units and streams, for each, the query blocks that see its keys.  A key belongs to one CTA: no atomics,
-//     the same bits in every call.
-//   * few rows (decoding): the bytes of K bound it; a ring of K tiles is kept full.
+//   * a unit is 256 keys (two tiles) of one sequence and kv head; a persistent CTA takes its units one after the
+//     other and streams, for each, the query blocks that see its keys.  No atomics, the same bits in every call.
+//   * few rows (decoding): the bytes of K bound it.  A CTA has a run of units, most of them of one head, whose
+//     queries stay in shared memory; a ring of K tiles is kept full.
 //   * chunks: one exponential per pair and head, 32 a clock and SM, against 512 clocks of tensor work for
-//     256 x 128 x 128: the exponentials bound it.
-// E4M3 caches: the codes are the operand as they are (kind::f8f6f4).  A query vector goes into three E5M2 vectors
-// that add up to it: BF16 has 8 significant bits, E5M2 3, and its exponents reach 2^-31 of the largest
-// entry, so the sum is exact down to entries of 2^-24 of it.  The key's scale multiplies S in FP32.
+//     256 x 128 x 128: the exponentials bound it.  Units are dealt round by round, early keys, which most tokens
+//     see, first.  Where there are few of them each is cut into parts by its query blocks, whose sums a second
+//     kernel joins in order.
+// E4M3 caches, few rows: the codes are the operand as they are (kind::f8f6f4).  A query vector goes into three E5M2
+// vectors that add up to it: BF16 has 8 significant bits, E5M2 3, and its exponents reach 2^-31 of the largest
+// entry, so the sum is exact down to entries of 2^-24 of it.  Chunks: a warpgroup turns the codes into BF16, once for
+// all the query blocks of a unit.  The key's scale multiplies S in FP32.
+#include <limits.h>
 #include <stdlib.h>
 
 #include <algorithm>
@@ -24,161 +28,252 @@
 namespace fa {
 namespace paged {
 
-constexpr int kAccThreads = 384;
 constexpr int kAccKeys = 256;        // of a unit
 constexpr int kAccTile = 128;        // keys of a tile
 constexpr int kPieces = 3;           // E5M2 vectors of a query vector
+constexpr int kColStages = 4;        // blocks of queries whose log-sum-exps are in shared memory
+// Chunks: units are cut into parts until there are about eight for each of 152 SMs, none of less than four
+// query blocks.
+constexpr int kMostParts = 1216, kPartBlocks = 4;
 
 struct Acc {
   Attn a;                  // queries, cache, lengths (o and lse are not used)
   const float* lse;        // [T, Hq]
   float* weights;          // [pages][Hkv][page_size]
   long long weight_stride;
-  const float* q_scale;    // E4M3: [T, Hq], what the pieces are to be multiplied by
+  const float* q_scale;    // E4M3, few rows: [T, Hq], what the pieces are to be multiplied by
+  float* part;             // chunks: [kMostParts][kAccKeys], the parts' sums
+  int max_parts;           // of a unit
 };
 
 template <int D, bool kFp8, int N>
 struct AccCfg {
-  static constexpr int kRowBytes = D * (kFp8 ? 1 : 2);
+  static constexpr bool kChunk = N == 128;
+  static constexpr bool kPieced = kFp8 && !kChunk, kConvert = kFp8 && kChunk;
+  // the pieces side by side, 3 N columns of S that are added afterwards: the tensor core then reads K once.  (64
+  // columns leave no room for that: S takes the pieces one after the other.)
+  static constexpr bool kWide = kPieced && N <= 32;
+  static constexpr int kThreads = kConvert ? 512 : 384;
+  // operands
+  static constexpr int kRowBytes = D * (kPieced ? 1 : 2);
   static constexpr int kAtomBytes = kRowBytes < 128 ? kRowBytes : 128;   // swizzle atom row
   static constexpr int kAtoms = kRowBytes / kAtomBytes, kAtomElems = D / kAtoms;
   static constexpr int kTileBytes = kAccTile * kRowBytes, kPairBytes = 2 * kTileBytes;
-  static constexpr int kQTile = N * kRowBytes, kQBytes = (kFp8 ? kPieces : 1) * kQTile;
-  static constexpr int kQStages = N == 128 ? 2 : 3;
-  static constexpr int kRoom = 220 * 1024 - kQStages * kQBytes;
+  static constexpr int kQTile = N * kRowBytes, kQBytes = (kPieced ? kPieces : 1) * kQTile;
+  static constexpr int kQStages = kChunk ? (kConvert ? 3 : 4) : 2;
+  static constexpr int kCodeBytes = kConvert ? kAccKeys * D : 0;         // a unit's codes
+  static constexpr int kColBytes = (kPieced ? 2 : 1) * N * 4;            // a block's columns: -lse, and pieces: the factor
+  static constexpr int kSideStages = kChunk ? 2 : 8;
+  static constexpr int kSideBytes = kAccKeys * 4 * (kFp8 ? 2 : 1) + 64;  // a unit's weights, scales and pages
+  static constexpr int kQOff = 0;
+  static constexpr int kCodeOff = kQOff + kQStages * kQBytes, kKOff = kCodeOff + kCodeBytes;
+  static constexpr int kRest = kColStages * kColBytes + kSideStages * kSideBytes;
+  static constexpr int kRoom = 226 * 1024 - kKOff - kRest;
   static constexpr int kKStages = kRoom / kPairBytes < 6 ? kRoom / kPairBytes : 6;
-  static constexpr int kBufs = N == 128 ? 2 : 4;                 // S buffers of a tile
-  static constexpr int kTmemCols = 2 * kBufs * N;
-  static constexpr int kQOff = kKStages * kPairBytes;
-  static constexpr int kColOff = kQOff + kQStages * kQBytes;     // per stage: -lse log2e, factor
-  static constexpr int kSharedOff = kColOff + kQStages * 2 * N * 4;
-  static constexpr uint32_t kIdesc = kFp8 ? idesc_e4m3(128, N, false, false) | (1u << 10)   // B: E5M2
-                                          : idesc_bf16(128, N, false, false);
-  static_assert(kKStages >= 2 && kTmemCols <= 512 && kTmemCols >= 32, "shared or tensor memory");
+  static constexpr int kColOff = kKOff + kKStages * kPairBytes, kSideOff = kColOff + kColStages * kColBytes;
+  static constexpr int kSharedOff = kColOff + kRest;
+  // S: buffers of a tile, each kBufCols columns of tensor memory
+  static constexpr int kSCols = kWide ? kPieces * N : N, kBufCols = kWide ? 4 * N : N;
+  static constexpr int kBufs = 2 * 4 * kBufCols <= 512 ? 4 : 2;
+  static constexpr int kTmemCols = 2 * kBufs * kBufCols;
+  static constexpr uint32_t kIdesc = kPieced ? idesc_e4m3(128, kSCols, false, false) | (1u << 10)   // B: E5M2
+                                             : idesc_bf16(128, N, false, false);
+  static_assert(kKStages >= 1 && kTmemCols <= 512 && kTmemCols >= 32, "shared or tensor memory");
 };
 
-constexpr int kMaxKStages = 6, kMaxQStages = 3, kMaxBufs = 4;
+constexpr int kMaxKStages = 6, kMaxQStages = 4, kMaxBufs = 4, kMaxSideStages = 8, kMaxWarps = 16;
 
 struct AccShared {
   uint64_t k_full[kMaxKStages], k_empty[kMaxKStages], q_full[kMaxQStages], q_empty[kMaxQStages];
+  uint64_t col_full[kColStages], col_empty[kColStages], side_full[kMaxSideStages], side_empty[kMaxSideStages];
   uint64_t s_full[2][kMaxBufs], s_empty[2][kMaxBufs];
+  uint64_t code_full, code_empty;  // E4M3 chunks: a unit's codes have landed / have been read
   uint64_t mma_done;
   uint64_t never;                  // test builds only: a barrier nothing arrives on
+  long long scan[kMaxWarps];
+  long long first;                 // this CTA's first unit (or part) within its sequence
   uint32_t tmem_base, abort_flag;
-  long long scan[kAccThreads / 32];
-  int first_b, first_unit;         // this CTA's first unit; first_b = -1: none
-  long long first_cost;            // what lies before it
+  int first_b;                     // that sequence; -1: none
 };
 
 template <int D, bool kFp8, int N>
 constexpr int acc_smem() {
   return AccCfg<D, kFp8, N>::kSharedOff + (int)sizeof(AccShared);
 }
-static_assert(acc_smem<128, false, 128>() <= 227 * 1024 && acc_smem<128, true, 128>() <= 227 * 1024 &&
-                  acc_smem<128, false, 64>() <= 227 * 1024 && acc_smem<128, true, 64>() <= 227 * 1024 &&
-                  acc_smem<128, false, 16>() <= 227 * 1024 && acc_smem<128, true, 16>() <= 227 * 1024,
+template <int D, bool kFp8>
+constexpr bool acc_fits() {
+  return acc_smem<D, kFp8, 16>() <= 227 * 1024 && acc_smem<D, kFp8, 32>() <= 227 * 1024 && acc_smem<D, kFp8, 64>() <= 227 * 1024 &&
+         acc_smem<D, kFp8, 128>() <= 227 * 1024;
+}
+static_assert(acc_fits<64, false>() && acc_fits<64, true>() && acc_fits<128, false>() && acc_fits<128, true>(),
               "shared-memory layout exceeds 227 KB");
 
-// A sequence's units: (kv head, block of its walk), the block fastest.  A unit costs kUnitCost for its keys
-// and one for each block of queries of the sequence.
-constexpr int kUnitCost = 2;
-
-template <int N>
+// A sequence's units: its walk's blocks of keys for each kv head.
 struct AccSeq {
   Seq s;
   KeyWalk<kAccKeys> w;
-  int blocks;              // of queries, `tokens` tokens each
   __device__ __forceinline__ AccSeq(const Attn& p, int b) : s(load_seq(p, b)), w(p, s.pos0, s.kv - 1) {
-    const int tokens = N / p.group;
-    blocks = (s.n + tokens - 1) / tokens;
     if (s.n == 0 || w.hi == 0) w.steps = 0;
   }
-  __device__ __forceinline__ int cost() const { return kUnitCost + blocks; }
-  __device__ __forceinline__ long long total(const Attn& p) const { return (long long)w.steps * p.c.Hkv * cost(); }
+  __device__ __forceinline__ long long units(const Attn& p) const { return (long long)w.steps * p.c.Hkv; }
 };
 
-// The units of a CTA's share, in order.  Every role walks them with a copy of its own.
-template <int N>
-struct AccCursor {
-  int b, h, j;             // sequence (B: no unit is left), kv head, step of the walk
-  long long left;          // cost until the end of the share
-  Seq s;
-  KeyWalk<kAccKeys> w;
-  int cost;
-  __device__ __forceinline__ void take(const AccSeq<N>& x) {
-    s = x.s;
-    w = x.w;
-    cost = x.cost();
+// Sums the sequences' units over the CTA, settles into how many parts each is cut, and finds what `range`
+// asks for: the sequence (first_b, -1: none) that holds number `want` of the launch's parts, the number within it
+// (first) and how many are wanted (count).  Returns the parts of a unit.
+template <int kThreads, class Range>
+__device__ __forceinline__ int find_units(const Attn& p, int max_parts, long long* scan, int& first_b, long long& first,
+                                          long long& count, Range range) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int per = (p.c.B + kThreads - 1) / kThreads;
+  const int b_from = min((int)threadIdx.x * per, p.c.B), b_to = min(b_from + per, p.c.B);
+  long long mine = 0;
+  for (int b = b_from; b < b_to; ++b) mine += AccSeq(p, b).units(p);
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
   }
-  __device__ __forceinline__ AccCursor(const Attn& p, int first_b, int first_unit, long long share)
-      : b(first_b), left(share), s{}, w(p, 0, -1), cost(0) {
-    const AccSeq<N> x(p, b);
-    take(x);
-    h = first_unit / max(w.steps, 1);
-    j = first_unit - h * max(w.steps, 1);
-    if (h >= p.c.Hkv) next_sequence(p);
-    if (left <= 0) b = p.c.B;
+  if (lane == 31) scan[warp] = incl;
+  if (threadIdx.x == 0) first_b = -1;
+  __syncthreads();
+  long long from = incl - mine, all = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) from += scan[w];
+    all += scan[w];
   }
-  __device__ __forceinline__ void next_sequence(const Attn& p) {
-    h = j = 0;
-    for (++b; b < p.c.B; ++b) {
-      const AccSeq<N> x(p, b);
-      if (x.w.steps == 0) continue;
-      take(x);
-      return;
+  const int parts = all > 0 ? (int)max(min((long long)max_parts, kMostParts / all), 1ll) : 1;
+  long long want;
+  count = range(all, parts, want);
+  from *= parts;
+  if (count > 0 && want >= from && want < from + mine * parts) {
+    for (int b = b_from; b < b_to; ++b) {
+      const long long n = AccSeq(p, b).units(p) * parts;
+      if (want < from + n) {
+        first = want - from;
+        first_b = b;
+        break;
+      }
+      from += n;
     }
   }
-  __device__ __forceinline__ bool valid(const Attn& p) const { return b < p.c.B; }
-  __device__ __forceinline__ void next(const Attn& p) {
-    left -= cost;
-    if (left <= 0) {
+  __syncthreads();
+  return parts;
+}
+
+// A CTA's units, in order.  Every role walks them with a copy of its own.  Few rows: a run of them, ordered by
+// sequence, kv head and block of keys.  Chunks: every gridDim.x-th part, ordered by sequence, block of keys,
+// kv head and part.
+template <bool kChunk>
+struct AccCursor {
+  int b, h, j, part;       // sequence (B: no unit is left), kv head, step of the walk, part
+  bool fresh;              // the first of its head in this CTA
+  long long left;          // few rows: units until the end of the run; chunks: number within the sequence
+  Seq s;
+  KeyWalk<kAccKeys> w;
+  __device__ __forceinline__ AccCursor(const Attn& p, int parts, int first_b, long long first, long long n)
+      : b(first_b), h(0), j(0), part(0), fresh(true), left(kChunk ? first : n), s{}, w(p, 0, -1) {
+    if (b < 0) {
       b = p.c.B;
       return;
     }
-    if (++j == w.steps) {
-      j = 0;
-      if (++h == p.c.Hkv) next_sequence(p);
+    const AccSeq x(p, b);
+    s = x.s;
+    w = x.w;
+    if constexpr (kChunk) {
+      place(p, parts);
+    } else {
+      h = (int)(first / w.steps);
+      j = (int)(first - (long long)h * w.steps);
     }
   }
+  __device__ __forceinline__ void place(const Attn& p, int parts) {
+    const int r = (int)(left / parts);   // (units are under 2^31: a sequence has 2^22 blocks of keys at most)
+    part = (int)(left - (long long)r * parts);
+    j = r / p.c.Hkv;
+    h = r - j * p.c.Hkv;
+  }
+  __device__ __forceinline__ bool valid(const Attn& p) const { return b < p.c.B; }
+  __device__ __forceinline__ void next(const Attn& p, int parts) {
+    if constexpr (kChunk) {
+      left += gridDim.x;
+      for (long long n = (long long)w.steps * p.c.Hkv * parts; left >= n; n = (long long)w.steps * p.c.Hkv * parts) {
+        left -= n;
+        if (++b >= p.c.B) return;
+        const AccSeq x(p, b);
+        s = x.s;
+        w = x.w;
+      }
+      place(p, parts);
+    } else {
+      fresh = false;
+      if (--left == 0) {
+        b = p.c.B;
+        return;
+      }
+      if (++j < w.steps) return;
+      j = 0;
+      fresh = true;
+      if (++h < p.c.Hkv) return;
+      h = 0;
+      for (++b; b < p.c.B; ++b) {
+        const AccSeq x(p, b);
+        if (x.w.steps == 0) continue;
+        s = x.s;
+        w = x.w;
+        return;
+      }
+    }
+  }
+  // whether the next unit has another head's queries, or there is none
+  __device__ __forceinline__ bool last() const { return left == 1 || j + 1 == w.steps; }
   __device__ __forceinline__ int key() const { return w.at(j); }
-  // the blocks of queries that see a key of the unit: [first, last)
-  __device__ __forceinline__ int first_block(int tokens) const { return max(key() - s.pos0, 0) / tokens; }
-  __device__ __forceinline__ int last_block(const Attn& p, int tokens) const {
-    const int all = (s.n + tokens - 1) / tokens;
-    if (!p.window || key() < p.sinks) return all;
-    const long long t = (long long)key() + kAccKeys - 1 + p.window - 1 - s.pos0;   // the last token that sees one
-    return t < 0 ? 0 : (int)min((long long)all, t / tokens + 1);
+  // the blocks of queries that see a key of the unit, or this part's share of them: [from, to).  (Few rows: one.)
+  __device__ __forceinline__ void blocks(const Attn& p, int parts, int tokens, int& from, int& to) const {
+    from = 0;
+    to = 1;
+    if constexpr (kChunk) {
+      const int lo = max(key() - s.pos0, 0) / tokens;
+      int hi = (s.n + tokens - 1) / tokens;
+      if (p.window && key() >= p.sinks) {
+        const long long t = (long long)key() + kAccKeys - 1 + p.window - 1 - s.pos0;   // the last token that sees one
+        hi = t < 0 ? 0 : (int)min((long long)hi, t / tokens + 1);
+      }
+      const int n = max(hi - lo, 0);
+      from = lo + (int)((long long)n * part / parts);
+      to = lo + (int)((long long)n * (part + 1) / parts);
+    }
   }
   // whether tile t of the unit has keys
   __device__ __forceinline__ bool tile(int t) const { return key() + t * kAccTile < w.hi; }
 };
 
-// A thread's key of a unit: where its weight lies, what was there.
-struct AccKey {
-  bool mine, fresh;        // a new token sees it; it is a new token's
-  int page;
-  long long at;            // slot within the page's head
-  float old, scale;
-};
-
-// sum += of the columns c0 .. c0 + W - 1 of S: exp2(S f - lse log2e), of those in `mask` alone where kMasked.
-template <int W, bool kFp8, bool kMasked>
+// sum += of the columns: exp(S f - lse), of those in `mask` alone where kMasked.  The difference is taken before it
+// goes to base 2: for the keys that weigh most it is small, and so is the error that the product adds.
+template <int W, bool kPieced, bool kScaled, bool kMasked>
 __device__ __forceinline__ void acc_columns(const uint32_t (&r)[W], const float* neg_lse, const float* factor, float scale,
-                                            uint32_t mask, float (&sum)[4]) {
+                                            float key_scale, uint32_t mask, float (&sum)[4]) {
+  constexpr float kLog2e = 1.4426950408889634f;
 #pragma unroll
   for (int i = 0; i < W; i += 4) {
     const float4 l = *reinterpret_cast<const float4*>(neg_lse + i);
     float s0 = __uint_as_float(r[i]), s1 = __uint_as_float(r[i + 1]), s2 = __uint_as_float(r[i + 2]), s3 = __uint_as_float(r[i + 3]);
-    if constexpr (kFp8) {
+    if constexpr (kScaled) {
+      mul2(s0, s1, s0, s1, key_scale, key_scale);
+      mul2(s2, s3, s2, s3, key_scale, key_scale);
+    }
+    if constexpr (kPieced) {
       const float4 f = *reinterpret_cast<const float4*>(factor + i);
-      mul2(s0, s1, s0, s1, scale, scale);
-      mul2(s2, s3, s2, s3, scale, scale);
       fma2(s0, s1, s0, s1, f.x, f.y, l.x, l.y);
       fma2(s2, s3, s2, s3, f.z, f.w, l.z, l.w);
     } else {
       fma2(s0, s1, s0, s1, scale, scale, l.x, l.y);
       fma2(s2, s3, s2, s3, scale, scale, l.z, l.w);
     }
+    mul2(s0, s1, s0, s1, kLog2e, kLog2e);
+    mul2(s2, s3, s2, s3, kLog2e, kLog2e);
     float e0 = ex2_approx(s0), e1 = ex2_approx(s1), e2 = ex2_approx(s2), e3 = ex2_approx(s3);
     if constexpr (kMasked) {
       e0 = mask >> i & 1 ? e0 : 0.f;
@@ -192,11 +287,12 @@ __device__ __forceinline__ void acc_columns(const uint32_t (&r)[W], const float*
 }
 
 template <int D, bool kFp8, int N>
-__global__ void __launch_bounds__(kAccThreads, 1)
+__global__ void __launch_bounds__(AccCfg<D, kFp8, N>::kThreads, 1)
     fa_accumulate_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ Acc g) {
   using C = AccCfg<D, kFp8, N>;
-  constexpr int kKWarp = 8, kQWarp = 9, kMmaWarp = 10;
+  using Cursor = AccCursor<C::kChunk>;
+  constexpr int kKWarp = 8, kQWarp = 9, kMmaWarp = 10, kColWarp = 11, kConvertWarp = 12;
   constexpr int W = N < 32 ? N : 32;    // columns taken at a time
   extern __shared__ __align__(1024) uint8_t smem[];
   const Attn& p = g.a;
@@ -209,105 +305,118 @@ __global__ void __launch_bounds__(kAccThreads, 1)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int tokens = N / p.group;       // of a block of queries
 
-  // ---- this CTA's share: every thread sums the costs of a few sequences, the CTA scans the sums
-  const int per = (p.c.B + kAccThreads - 1) / kAccThreads;
-  const int b_from = min((int)threadIdx.x * per, p.c.B), b_to = min(b_from + per, p.c.B);
-  long long mine = 0;
-  for (int b = b_from; b < b_to; ++b) mine += AccSeq<N>(p, b).total(p);
-  long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o *= 2) {
-    const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += x;
-  }
-  if (lane == 31) sh.scan[warp] = incl;
   if (threadIdx.x == 0) {
     sh.abort_flag = 0;
-    sh.first_b = -1;
     for (int s = 0; s < C::kKStages; ++s) {
-      mbar_init(&sh.k_full[s], 1);
+      mbar_init(&sh.k_full[s], C::kConvert ? 128 : 1);
       mbar_init(&sh.k_empty[s], 1);
     }
     for (int s = 0; s < C::kQStages; ++s) {
-      mbar_init(&sh.q_full[s], 33);     // the loading warp's lanes (column data) and the expected bytes
-      mbar_init(&sh.q_empty[s], 9);     // eight warps that sum and the products
+      mbar_init(&sh.q_full[s], 1);
+      mbar_init(&sh.q_empty[s], 1);
+    }
+    for (int s = 0; s < kColStages; ++s) {
+      mbar_init(&sh.col_full[s], 32);
+      mbar_init(&sh.col_empty[s], 8);   // the warps that sum
+    }
+    for (int s = 0; s < C::kSideStages; ++s) {
+      mbar_init(&sh.side_full[s], 32);  // the loading warp's lanes (pages), one of them with the expected bytes
+      mbar_init(&sh.side_empty[s], 8);
     }
     for (int t = 0; t < 2; ++t)
       for (int s = 0; s < C::kBufs; ++s) {
         mbar_init(&sh.s_full[t][s], 1);
         mbar_init(&sh.s_empty[t][s], 4);
       }
+    mbar_init(&sh.code_full, 1);
+    mbar_init(&sh.code_empty, 128);
     mbar_init(&sh.mma_done, 1);
     mbar_init(&sh.never, 1);
     fence_barrier_init();
   }
-  __syncthreads();
-  long long from = incl - mine, all = 0;
-#pragma unroll
-  for (int w = 0; w < kAccThreads / 32; ++w) {
-    if (w < warp) from += sh.scan[w];
-    all += sh.scan[w];
-  }
-  const long long share = (all + gridDim.x - 1) / gridDim.x;
-  const long long c_first = blockIdx.x * share, c_end = min(c_first + share, all);
-  if (c_first < c_end && c_first >= from && c_first < from + mine) {
-    // the sequence that holds the share's first cost; a unit belongs to the share that its own first lies in
-    for (int b = b_from; b < b_to; ++b) {
-      const AccSeq<N> x(p, b);
-      const long long n = x.total(p);
-      if (c_first < from + n) {
-        sh.first_unit = (int)((c_first - from + x.cost() - 1) / x.cost());
-        sh.first_cost = from + (long long)sh.first_unit * x.cost();
-        sh.first_b = b;
-        break;
-      }
-      from += n;
-    }
-  }
-  __syncwarp();
   if (warp == kMmaWarp) {
     tmem_alloc(&sh.tmem_base, C::kTmemCols);
     tmem_relinquish();
   }
+  if (tokens * p.group < N) {
+    // rows of a block that no token fills: S = 0 there, and a log-sum-exp of infinity, so that full blocks need no mask
+    for (int i = threadIdx.x; i < C::kQStages * C::kQBytes / 16; i += C::kThreads)
+      *reinterpret_cast<uint4*>(smem + C::kQOff + i * 16) = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+  }
   tc_fence_before();
-  __syncthreads();
+  long long count;
+  const int parts = find_units<C::kThreads>(p, C::kChunk ? g.max_parts : 1, sh.scan, sh.first_b, sh.first, count,
+                                            [&](long long all, int parts, long long& want) {
+    if (C::kChunk) {
+      want = blockIdx.x;
+      return all * parts - want;     // (every gridDim.x-th from there on)
+    }
+    const long long share = (all + gridDim.x - 1) / gridDim.x;
+    want = blockIdx.x * share;
+    return min(share, all - want);
+  });
   tc_fence_after();
   const uint32_t tmem = sh.tmem_base;
   // (a CTA without a unit walks none; all of them free their tensor memory below)
-  AccCursor<N> cur(p, max(sh.first_b, 0), sh.first_b < 0 ? 0 : sh.first_unit, sh.first_b < 0 ? 0 : c_end - sh.first_cost);
+  Cursor cur(p, parts, sh.first_b, sh.first, count);
 
   if (warp == kKWarp) {
-    // ------------------------------------------------------------ K tiles, page by page
+    // ------------------------------------------------------------ K tiles (or their codes), page by page
     const int page_size = 1 << p.c.page_shift, box = min(page_size, kAccTile), boxes = kAccKeys / box;
     const uint32_t base = smem_u32(smem);
-    auto look = [&](const AccCursor<N>& c) {
-      int page = p.c.num_pages;         // out of range: zeros
-      if (c.valid(p) && lane < boxes && c.w.any(c.key() + lane * box, box)) {
-        const int x = find_page(p.c, c.b, c.key() + lane * box, kSitePagedPage);
-        if (x >= 0) page = x;
-      }
-      return page;
+    // a unit's entry of the table is loaded while the one before it waits for its slot
+    auto look = [&](const Cursor& c) {
+      const bool any = c.valid(p) && lane < boxes && c.w.any(c.key() + lane * box, box);
+      // (the walk ends at the sequence's length, which the table holds)
+      return any ? __ldg(p.c.table + c.b * p.c.table_stride + ((c.key() + lane * box) >> p.c.page_shift)) : p.c.num_pages;
     };
     if (lane == 0) tma_prefetch_desc(&tmK);
     int n = 0, page = look(cur);
     bool ok = true;
     while (cur.valid(p)) {
-      AccCursor<N> ahead = cur;
-      ahead.next(p);
+      Cursor ahead = cur;
+      ahead.next(p, parts);
       const int page_ahead = look(ahead);
-      const int s = n % C::kKStages;
-      ok = __all_sync(0xffffffffu, mbar_wait(&sh.k_empty[s], ((n / C::kKStages) & 1) ^ 1, abort_flag, p.c.status));
+      const int s = n % C::kKStages, x = n % C::kSideStages;
+      uint64_t* full = C::kConvert ? &sh.code_full : &sh.k_full[s];
+      ok = __all_sync(0xffffffffu, mbar_wait(&sh.side_empty[x], ((n / C::kSideStages) & 1) ^ 1, abort_flag, p.c.status) &&
+                                       (C::kConvert ? mbar_wait(&sh.code_empty, (n & 1) ^ 1, abort_flag, p.c.status)
+                                                    : mbar_wait(&sh.k_empty[s], ((n / C::kKStages) & 1) ^ 1, abort_flag, p.c.status)));
       if (!ok) break;
+      if (page < 0 || page > p.c.num_pages) {
+        report_bounds(p.c.status, kSitePagedPage, page);
+        page = p.c.num_pages;            // out of range: zeros
+      }
       const int tiles = cur.tile(1) ? 2 : 1;
-      if (lane == 0) mbar_arrive_expect_tx(&sh.k_full[s], tiles * C::kTileBytes);
+      const bool loads = lane < boxes && lane * box < tiles * kAccTile, real = loads && page < p.c.num_pages;
+      const int reals = __popc(__ballot_sync(0xffffffffu, real));
+      uint8_t* side = smem + C::kSideOff + x * C::kSideBytes;
+      if (lane < 16) reinterpret_cast<int*>(side + C::kSideBytes - 64)[lane] = real ? page : -1;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(full, tiles * kAccTile * D * (kFp8 ? 1 : 2));
+        mbar_arrive_expect_tx(&sh.side_full[x], reals * box * 4 * (kFp8 ? 2 : 1));
+      } else {
+        mbar_arrive(&sh.side_full[x]);
+      }
       __syncwarp();
-      if (lane < boxes && lane * box < tiles * kAccTile) {
-        const int row = lane * box;
-        const uint32_t dst = base + s * C::kPairBytes + (row / kAccTile) * C::kTileBytes + (row % kAccTile) * C::kAtomBytes;
+      const int row = lane * box, slot = (cur.key() + row) & (page_size - 1);
+      if (loads) {
+        if constexpr (C::kConvert) {
+          tma_load_page(base + C::kCodeOff + row * D, &tmK, full, 0, slot, cur.h, page);
+        } else {
+          const uint32_t dst =
+              base + C::kKOff + s * C::kPairBytes + (row / kAccTile) * C::kTileBytes + (row % kAccTile) * C::kAtomBytes;
 #pragma unroll
-        for (int a = 0; a < C::kAtoms; ++a)
-          tma_load_page(dst + a * kAccTile * C::kAtomBytes, &tmK, &sh.k_full[s], a * C::kAtomElems,
-                        (cur.key() + row) & (page_size - 1), cur.h, page);
+          for (int a = 0; a < C::kAtoms; ++a)
+            tma_load_page(dst + a * kAccTile * C::kAtomBytes, &tmK, full, a * C::kAtomElems, slot, cur.h, page);
+        }
+      }
+      if (real) {
+        const long long at = (long long)cur.h * page_size + slot;
+        bulk_load(side + row * 4, g.weights + page * g.weight_stride + at, box * 4, &sh.side_full[x]);
+        if constexpr (kFp8)
+          bulk_load(side + (kAccKeys + row) * 4, p.c.k_scale + page * p.c.scale_stride + at, box * 4, &sh.side_full[x]);
       }
       ++n;
       cur = ahead;
@@ -316,87 +425,122 @@ __global__ void __launch_bounds__(kAccThreads, 1)
     if (*abort_flag) {
       // let copies still in flight land before the CTA's shared memory goes away
       volatile uint32_t ignore_abort = 0;
-      for (int i = max(0, n - C::kKStages); i < n; ++i)
-        mbar_wait(&sh.k_full[i % C::kKStages], (i / C::kKStages) & 1, &ignore_abort, p.c.status);
+      if constexpr (C::kConvert) {
+        if (n > 0) mbar_wait(&sh.code_full, (n - 1) & 1, &ignore_abort, p.c.status);
+      } else {
+        for (int i = max(0, n - C::kKStages); i < n; ++i)
+          mbar_wait(&sh.k_full[i % C::kKStages], (i / C::kKStages) & 1, &ignore_abort, p.c.status);
+      }
+      for (int i = max(0, n - C::kSideStages); i < n; ++i)
+        mbar_wait(&sh.side_full[i % C::kSideStages], (i / C::kSideStages) & 1, &ignore_abort, p.c.status);
     }
   } else if (warp == kQWarp) {
-    // ------------------------------------------------------------ blocks of queries and their log-sum-exps
-    if (lane == 0) tma_prefetch_desc(&tmQ);
-    constexpr int kPer = (N + 31) / 32;
-    int n = 0;
-    bool ok = true;
-    for (; ok && cur.valid(p); cur.next(p)) {
-      const int last = cur.last_block(p, tokens);
-      for (int i = cur.first_block(tokens); i < last; ++i, ++n) {
-        float neg[kPer], factor[kPer];
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-          const int r = e * 32 + lane, t = i * tokens + r / p.group;
-          neg[e] = -INFINITY;
-          factor[e] = 0.f;
-          if (r < tokens * p.group && t < cur.s.n) {
-            const long long row = (long long)(cur.s.q0 + t) * p.Hq + cur.h * p.group + r % p.group;
-            const float lse = __ldg(g.lse + row);
-            // a row that saw no key weighs nothing
-            neg[e] = lse == -INFINITY ? -INFINITY : -1.4426950408889634f * lse;
-            if constexpr (kFp8) factor[e] = p.scale_log2 * __ldg(g.q_scale + row);
-          }
-        }
-        const int s = n % C::kQStages;
-        ok = __all_sync(0xffffffffu, mbar_wait(&sh.q_empty[s], ((n / C::kQStages) & 1) ^ 1, abort_flag, p.c.status));
-        if (!ok) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&sh.q_full[s], tokens * p.group * C::kRowBytes * (kFp8 ? kPieces : 1));
+    // ------------------------------------------------------------ blocks of queries
+    if constexpr (C::kPieced) cudaGridDependencySynchronize();   // the pieces are there (in every CTA: what follows
+                                                                 // in the stream waits for this launch only)
+    if (elect_one()) {
+      tma_prefetch_desc(&tmQ);
+      int n = 0;
+      bool ok = true;
+      for (; ok && cur.valid(p); cur.next(p, parts)) {
+        if (!C::kChunk && !cur.fresh) continue;
+        int i, last;
+        for (cur.blocks(p, parts, tokens, i, last); i < last; ++i, ++n) {
+          const int s = n % C::kQStages;
+          if (!(ok = mbar_wait(&sh.q_empty[s], ((n / C::kQStages) & 1) ^ 1, abort_flag, p.c.status))) break;
+          mbar_arrive_expect_tx(&sh.q_full[s], tokens * p.group * C::kRowBytes * (C::kPieced ? kPieces : 1));
           uint8_t* dst = smem + C::kQOff + s * C::kQBytes;
           const int token = cur.s.q0 + i * tokens, head = cur.h * p.group;
-          if constexpr (kFp8) {
+          if constexpr (C::kPieced) {
             for (int x = 0; x < kPieces; ++x) tma_load_page(smem_u32(dst + x * C::kQTile), &tmQ, &sh.q_full[s], 0, head, token, x);
           } else {
             for (int a = 0; a < C::kAtoms; ++a)
               tma_load_3d(dst + a * N * C::kAtomBytes, &tmQ, &sh.q_full[s], a * C::kAtomElems, head, token);
           }
         }
-        __syncwarp();
-        float* col = reinterpret_cast<float*>(smem + C::kColOff) + s * 2 * N;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e)
-          if (e * 32 + lane < N) {
-            col[e * 32 + lane] = neg[e];
-            if constexpr (kFp8) col[N + e * 32 + lane] = factor[e];
-          }
-        mbar_arrive(&sh.q_full[s]);
+      }
+      if (*abort_flag) {
+        volatile uint32_t ignore_abort = 0;
+        for (int i = max(0, n - C::kQStages); i < n; ++i)
+          mbar_wait(&sh.q_full[i % C::kQStages], (i / C::kQStages) & 1, &ignore_abort, p.c.status);
       }
     }
-    if (*abort_flag) {
-      volatile uint32_t ignore_abort = 0;
-      for (int i = max(0, n - C::kQStages); i < n; ++i)
-        mbar_wait(&sh.q_full[i % C::kQStages], (i / C::kQStages) & 1, &ignore_abort, p.c.status);
+  } else if (warp == kColWarp) {
+    // ------------------------------------------------------------ their log-sum-exps, four blocks at a time
+    constexpr int kPer = (N + 31) / 32, kAhead = C::kChunk ? 4 : 1;
+    if constexpr (C::kPieced) cudaGridDependencySynchronize();
+    int tr[kPer], off[kPer];               // a column's token within its block, its place behind the block's first row
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const int r = e * 32 + lane;
+      tr[e] = r < tokens * p.group ? r / p.group : INT_MAX;
+      off[e] = r / p.group * p.Hq + r % p.group;
+    }
+    int n = 0;
+    bool ok = true;
+    for (; ok && cur.valid(p); cur.next(p, parts)) {
+      if (!C::kChunk && !cur.fresh) continue;
+      int i, last;
+      for (cur.blocks(p, parts, tokens, i, last); ok && i < last; i += kAhead) {
+        float neg[kAhead][kPer], factor[kAhead][kPer];
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x)
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) {
+            neg[x][e] = -INFINITY;         // columns without a row weigh nothing, nor do rows that saw no key
+            factor[x][e] = 0.f;
+            const int t0 = (i + x) * tokens;
+            if (i + x < last && tr[e] < cur.s.n - t0) {
+              const long long row = (long long)(cur.s.q0 + t0) * p.Hq + cur.h * p.group + off[e];
+              neg[x][e] = __ldg(g.lse + row);
+              if constexpr (C::kPieced) factor[x][e] = __ldg(g.q_scale + row);
+            }
+          }
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) {
+          if (i + x >= last) break;
+          const int s = n % kColStages;
+          ok = __all_sync(0xffffffffu, mbar_wait(&sh.col_empty[s], ((n / kColStages) & 1) ^ 1, abort_flag, p.c.status));
+          if (!ok) break;
+          float* col = reinterpret_cast<float*>(smem + C::kColOff + s * C::kColBytes);
+#pragma unroll
+          for (int e = 0; e < kPer; ++e)
+            if (e * 32 + lane < N) {
+              col[e * 32 + lane] = neg[x][e] == -INFINITY ? -INFINITY : -neg[x][e];
+              if constexpr (C::kPieced) col[N + e * 32 + lane] = p.scale * factor[x][e];
+            }
+          mbar_arrive(&sh.col_full[s]);
+          ++n;
+        }
+      }
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ products
     if (elect_one()) {
-      const uint32_t sK = smem_u32(smem), sQ = smem_u32(smem + C::kQOff);
+      const uint32_t sK = smem_u32(smem + C::kKOff), sQ = smem_u32(smem + C::kQOff);
       int nk = 0, nq = 0, ns[2] = {0, 0};
       bool ok = true;
 #ifdef FA_TEST_HOOKS
       // failure-detection test: as in the few-rows kernel
       if (p.inject_stall) ok = mbar_wait(&sh.never, 0, abort_flag, p.c.status);
 #endif
-      for (; ok && cur.valid(p); cur.next(p), ++nk) {
-        const int ks = nk % C::kKStages, tiles = cur.tile(1) ? 2 : 1, last = cur.last_block(p, tokens);
+      for (; ok && cur.valid(p); cur.next(p, parts), ++nk) {
+        const int ks = nk % C::kKStages, tiles = cur.tile(1) ? 2 : 1;
         if (!(ok = mbar_wait(&sh.k_full[ks], (nk / C::kKStages) & 1, abort_flag, p.c.status))) break;
-        for (int i = cur.first_block(tokens); ok && i < last; ++i, ++nq) {
+        int i, last;
+        for (cur.blocks(p, parts, tokens, i, last); ok && i < last; ++i) {
           const int qs = nq % C::kQStages;
-          if (!(ok = mbar_wait(&sh.q_full[qs], (nq / C::kQStages) & 1, abort_flag, p.c.status))) break;
+          // few rows: a head's queries stay for all its units
+          if ((C::kChunk || cur.fresh) && !(ok = mbar_wait(&sh.q_full[qs], (nq / C::kQStages) & 1, abort_flag, p.c.status))) break;
           for (int t = 0; t < tiles; ++t) {
             const int buf = ns[t] % C::kBufs;
             if (!(ok = mbar_wait(&sh.s_empty[t][buf], ((ns[t] / C::kBufs) & 1) ^ 1, abort_flag, p.c.status))) break;
             tc_fence_after();
-            const uint32_t d = tmem + (t * C::kBufs + buf) * N;
+            const uint32_t d = tmem + (t * C::kBufs + buf) * C::kBufCols;
             const uint32_t a0 = sK + ks * C::kPairBytes + t * C::kTileBytes, b0 = sQ + qs * C::kQBytes;
-            if constexpr (kFp8) {
+            if constexpr (C::kPieced) {
 #pragma unroll
-              for (int x = 0; x < kPieces; ++x)
+              for (int x = 0; x < (C::kWide ? 1 : kPieces); ++x)
 #pragma unroll
                 for (int kk = 0; kk < D / 32; ++kk) {
                   const uint32_t a = a0 + kk * 32, b = b0 + x * C::kQTile + kk * 32;
@@ -414,7 +558,10 @@ __global__ void __launch_bounds__(kAccThreads, 1)
             tc_commit(&sh.s_full[t][buf]);
             ++ns[t];
           }
-          if (ok) tc_commit(&sh.q_empty[qs]);
+          if (ok && (C::kChunk || cur.last())) {
+            tc_commit(&sh.q_empty[qs]);
+            ++nq;
+          }
         }
         if (ok) tc_commit(&sh.k_empty[ks]);
       }
@@ -428,48 +575,29 @@ __global__ void __launch_bounds__(kAccThreads, 1)
   } else if (warp < 8) {
     // ------------------------------------------------------------ exponentials and sums: a thread per key
     const int t = warp / 4, row = t * kAccTile + (warp % 4) * 32 + lane;   // the thread's key within a unit
-    const uint32_t tS = tmem + t * C::kBufs * N + ((uint32_t)((warp % 4) * 32) << 16);
-    // the page of a unit's key is looked up two units ahead, what lies there is loaded one ahead
-    auto look = [&](const AccCursor<N>& c) {
-      AccKey k{false, false, -1, 0, 0.f, 0.f};
-      if (!c.valid(p)) return k;
-      const int key = c.key() + row;
-      k.mine = c.w.seen(key);
-      k.fresh = key >= c.s.pos0;
-      if (k.mine) k.page = __ldg(p.c.table + c.b * p.c.table_stride + (key >> p.c.page_shift));   // hi is within the table
-      k.at = ((long long)c.h << p.c.page_shift) + (key & ((1 << p.c.page_shift) - 1));
-      return k;
-    };
-    auto load = [&](AccKey& k) {
-      if (!k.mine) return;
-      if (k.page < 0 || k.page >= p.c.num_pages) {
-        report_bounds(p.c.status, kSitePagedPage, k.page);
-        k.mine = false;
-        return;
-      }
-      if (!k.fresh) k.old = g.weights[k.page * g.weight_stride + k.at];
-      if constexpr (kFp8) k.scale = __ldg(p.c.k_scale + k.page * p.c.scale_stride + k.at);
-    };
-    AccKey k0 = look(cur);
-    load(k0);
-    AccCursor<N> c1 = cur;
-    if (cur.valid(p)) c1.next(p);
-    AccKey k1 = look(c1);
-    int nq = 0, ns = 0;
+    const uint32_t tS = tmem + t * C::kBufs * C::kBufCols + ((uint32_t)((warp % 4) * 32) << 16);
+    const int box_shift = min(p.c.page_shift, 7);    // keys of a box of the loads
+    int nq = 0, ns = 0, nu = 0;
+    long long number = blockIdx.x;                   // chunks: of the part in the launch
     bool ok = true;
-    while (ok && cur.valid(p)) {
-      load(k1);
-      AccCursor<N> c2 = c1;
-      if (c1.valid(p)) c2.next(p);
-      const AccKey k2 = look(c2);
-      const int last = cur.last_block(p, tokens);
+    for (; ok && cur.valid(p); cur.next(p, parts), ++nu, number += gridDim.x) {
+      const int x = nu % C::kSideStages;
+      const uint8_t* side = smem + C::kSideOff + x * C::kSideBytes;
+      ok = __all_sync(0xffffffffu, mbar_wait(&sh.side_full[x], (nu / C::kSideStages) & 1, abort_flag, p.c.status));
+      if (!ok) break;
+      const int page = reinterpret_cast<const int*>(side + C::kSideBytes - 64)[row >> box_shift];
+      const float old = reinterpret_cast<const float*>(side)[row];
+      const float key_scale = kFp8 ? reinterpret_cast<const float*>(side)[kAccKeys + row] : 0.f;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.side_empty[x]);
       const bool active = cur.tile(t);
       const int key = cur.key() + row;
-      const float scale = kFp8 ? k0.scale : p.scale_log2;
       float total = 0.f;
-      for (int i = cur.first_block(tokens); i < last; ++i, ++nq) {
-        const int qs = nq % C::kQStages;
-        ok = __all_sync(0xffffffffu, mbar_wait(&sh.q_full[qs], (nq / C::kQStages) & 1, abort_flag, p.c.status));
+      int i, last;
+      for (cur.blocks(p, parts, tokens, i, last); i < last; ++i) {
+        const int cs = nq % kColStages;
+        if (C::kChunk || cur.fresh)
+          ok = __all_sync(0xffffffffu, mbar_wait(&sh.col_full[cs], (nq / kColStages) & 1, abort_flag, p.c.status));
         if (!ok) break;
         if (active) {
           const int buf = ns % C::kBufs;
@@ -482,38 +610,128 @@ __global__ void __launch_bounds__(kAccThreads, 1)
           int end = here;
           if (p.window && key >= p.sinks) end = (int)min((long long)here, max((long long)key + p.window - cur.s.pos0 - t0, 0ll));
           const int hi = end * p.group;
-          const float* col = reinterpret_cast<const float*>(smem + C::kColOff) + qs * 2 * N;
+          const float* col = reinterpret_cast<const float*>(smem + C::kColOff + cs * C::kColBytes);
+          const uint32_t at = tS + buf * C::kBufCols;
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          auto give = [&] {   // the buffer has been read
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.s_empty[t][buf]);
+          };
+          if (N >= 64 && __all_sync(0xffffffffu, lo == 0 && hi >= tokens * p.group)) {
+            // every row sees every key of the warp: 32 columns are on their way while as many are summed
+            uint32_t ra[32], rb[32];
+            tmem_ld32(at, ra);
 #pragma unroll
-          for (int c0 = 0; c0 < N; c0 += W) {
-            if (__all_sync(0xffffffffu, hi <= c0 || lo >= c0 + W)) continue;
-            uint32_t r[W];
-            if constexpr (W == 16)
-              tmem_ld16(tS + buf * N + c0, r);
-            else
-              tmem_ld32(tS + buf * N + c0, r);
-            tmem_ld_wait();
-            reg_fence(r);
-            if (__all_sync(0xffffffffu, lo <= c0 && hi >= c0 + W))
-              acc_columns<W, kFp8, false>(r, col + c0, col + N + c0, scale, 0, sum);
-            else
-              acc_columns<W, kFp8, true>(r, col + c0, col + N + c0, scale, low_bits(hi - c0) & ~low_bits(lo - c0), sum);
+            for (int c0 = 0; c0 < N; c0 += 64) {
+              tmem_ld_wait();
+              reg_fence(ra);
+              tmem_ld32(at + c0 + 32, rb);
+              acc_columns<32, C::kPieced, kFp8, false>(ra, col + c0, col + N + c0, p.scale, key_scale, 0, sum);
+              tmem_ld_wait();
+              reg_fence(rb);
+              if (c0 + 64 < N)
+                tmem_ld32(at + c0 + 64, ra);
+              else
+                give();
+              acc_columns<32, C::kPieced, kFp8, false>(rb, col + c0 + 32, col + N + c0 + 32, p.scale, key_scale, 0, sum);
+            }
+          } else {
+#pragma unroll
+            for (int c0 = 0; c0 < N; c0 += W) {
+              if (__all_sync(0xffffffffu, hi <= c0 || lo >= c0 + W)) continue;
+              uint32_t r[W];
+              auto get = [&](uint32_t (&to)[W], int c) {
+                if constexpr (W == 16)
+                  tmem_ld16(at + c, to);
+                else
+                  tmem_ld32(at + c, to);
+              };
+              get(r, c0);
+              if constexpr (C::kWide) {
+                uint32_t r1[W], r2[W];
+                get(r1, N + c0);
+                get(r2, 2 * N + c0);
+                tmem_ld_wait();
+                reg_fence(r);
+                reg_fence(r1);
+                reg_fence(r2);
+#pragma unroll
+                for (int e = 0; e < W; ++e)   // the smaller ones first
+                  r[e] = __float_as_uint(__uint_as_float(r[e]) + (__uint_as_float(r1[e]) + __uint_as_float(r2[e])));
+              } else {
+                tmem_ld_wait();
+                reg_fence(r);
+              }
+              acc_columns<W, C::kPieced, kFp8, true>(r, col + c0, col + N + c0, p.scale, key_scale,
+                                                     low_bits(hi - c0) & ~low_bits(lo - c0), sum);
+            }
+            give();
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.s_empty[t][buf]);
           ++ns;
           total += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         } else {
           __syncwarp();
         }
-        if (lane == 0) mbar_arrive(&sh.q_empty[qs]);
+        if (C::kChunk || cur.last()) {
+          if (lane == 0) mbar_arrive(&sh.col_empty[cs]);
+          ++nq;
+        }
       }
-      if (ok && k0.mine) g.weights[k0.page * g.weight_stride + k0.at] = k0.old + total;
-      cur = c1;
-      c1 = c2;
-      k0 = k1;
-      k1 = k2;
+      if (ok && cur.w.seen(key)) {
+        if (parts > 1)
+          g.part[number * kAccKeys + row] = total;
+        else if (page >= 0)
+          g.weights[page * g.weight_stride + ((long long)cur.h << p.c.page_shift) + (key & ((1 << p.c.page_shift) - 1))] =
+              (key >= cur.s.pos0 ? 0.f : old) + total;
+      }
+    }
+  }
+
+  if constexpr (C::kConvert) {
+    if (warp >= kConvertWarp) {
+      // ---------------------------------------------------------- codes -> BF16 operand tiles
+      // D / 16 neighbouring threads take one key's row, 16 codes each: two 16-byte chunks of a 64-column block,
+      // swizzled; the second block's threads take theirs in the other order, so that a row's threads meet
+      // different banks.  The scales are left to the sums.
+      constexpr int kPer = D / 16, kRowStep = 128 / kPer, kRows = kAccTile / kRowStep;
+      const int r0 = (threadIdx.x - 32 * kConvertWarp) / kPer, x = threadIdx.x % kPer, flip = x / 4;
+      const uint32_t c0 = (uint32_t)(flip * kAccTile * 128 + r0 * 128 + ((((x % 4) * 2 + flip) ^ (r0 & 7)) << 4));
+      const uint32_t c1 = (uint32_t)(flip * kAccTile * 128 + r0 * 128 + ((((x % 4) * 2 + 1 - flip) ^ (r0 & 7)) << 4));
+      static_assert(kRowStep % 8 == 0, "a thread's rows share one swizzle phase");
+      bool ok = true;
+      for (int n = 0; ok && cur.valid(p); cur.next(p, parts), ++n) {
+        const int s = n % C::kKStages, tiles = cur.tile(1) ? 2 : 1;
+        if (!(ok = mbar_wait(&sh.code_full, n & 1, abort_flag, p.c.status))) break;
+        uint4 codes[2][kRows];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < kRows; ++i)
+            if (t < tiles)
+              codes[t][i] = *reinterpret_cast<const uint4*>(smem + C::kCodeOff + (t * kAccTile + r0 + i * kRowStep) * D + x * 16);
+        mbar_arrive(&sh.code_empty);
+        if (!(ok = mbar_wait(&sh.k_empty[s], ((n / C::kKStages) & 1) ^ 1, abort_flag, p.c.status))) break;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < kRows; ++i) {
+            if (t >= tiles) continue;
+            const uint4 u = codes[t][i];
+            const uint32_t w[4] = {flip ? u.z : u.x, flip ? u.w : u.y, flip ? u.x : u.z, flip ? u.y : u.w};
+            uint32_t y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float2 f = e4m3x2_to_float2(w[e / 2] >> (16 * (e & 1)));
+              y[e] = pack_bf16x2(f.x, f.y);   // exact
+            }
+            const uint32_t tile = smem_u32(smem) + C::kKOff + s * C::kPairBytes + t * C::kTileBytes + i * kRowStep * 128;
+            sts128(tile + c0, make_uint4(y[0], y[1], y[2], y[3]));
+            sts128(tile + c1, make_uint4(y[4], y[5], y[6], y[7]));
+          }
+        fence_proxy_async_smem();
+        mbar_arrive(&sh.k_full[s]);
+      }
     }
   }
 
@@ -525,12 +743,37 @@ __global__ void __launch_bounds__(kAccThreads, 1)
   }
 }
 
+// Chunks whose units were cut: a unit's weights from its parts' sums, in their order.  A CTA has a unit, a thread a
+// key.  A programmatic launch: it gets ready beside the first kernel and waits for its end.
+__global__ void __launch_bounds__(kAccKeys) fa_accumulate_join(const __grid_constant__ Acc g) {
+  __shared__ long long scan[kAccKeys / 32], first;
+  __shared__ int first_b;
+  const Attn& p = g.a;
+  long long count;
+  const int parts = find_units<kAccKeys>(p, g.max_parts, scan, first_b, first, count, [&](long long all, int parts, long long& want) {
+    want = (long long)blockIdx.x * parts;
+    return parts > 1 && blockIdx.x < all ? 1 : 0;
+  });
+  cudaGridDependencySynchronize();   // before any exit: what follows must find the first kernel complete
+  if (first_b < 0) return;
+  const AccCursor<true> c(p, parts, first_b, first, 1);
+  const int key = c.key() + (int)threadIdx.x;
+  if (!c.w.seen(key)) return;
+  const int page = __ldg(p.c.table + c.b * p.c.table_stride + (key >> p.c.page_shift));
+  if (page < 0 || page >= p.c.num_pages) return;   // (recorded by the first kernel)
+  float sum = 0.f;
+  for (int i = 0; i < parts; ++i) sum += g.part[((long long)blockIdx.x * parts + i) * kAccKeys + threadIdx.x];
+  float* w = g.weights + page * g.weight_stride + ((long long)c.h << p.c.page_shift) + (key & ((1 << p.c.page_shift) - 1));
+  *w = (key >= c.s.pos0 ? 0.f : *w) + sum;
+}
+
 // The three E5M2 vectors of a query vector x: x = 2^e (p0 + p1 + p2), e such that the largest entry is in
 // [2^14, 2^15).  Each takes what is left, rounded to nearest.  D / 8 lanes have a vector.
 template <int D>
 __global__ void __launch_bounds__(256) split_queries_kernel(const __nv_bfloat16* __restrict__ q, long long q_stride, int T,
                                                             int Hq, uint8_t* __restrict__ pieces, float* __restrict__ scale) {
   constexpr int kLanes = D / 8, kVecs = 256 / kLanes;
+  cudaTriggerProgrammaticLaunchCompletion();   // the kernel that reads the pieces may get ready
   const long long vec = (long long)blockIdx.x * kVecs + threadIdx.x / kLanes, all = (long long)T * Hq;
   const int j = threadIdx.x % kLanes;
   const long long v = vec < all ? vec : all - 1;
@@ -580,15 +823,37 @@ __global__ void __launch_bounds__(256) split_queries_kernel(const __nv_bfloat16*
   if (j == 0) scale[vec] = __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
+// A launch that may start before the one before it in the stream has ended.
+template <typename... Args, typename... Given>
+static int launch_early(const char* what, void (*kern)(Args...), int grid, int threads, int smem, cudaStream_t s,
+                        const Given&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return check_cuda(cudaLaunchKernelEx(&cfg, kern, args...), what);
+}
+
 template <int D, bool kFp8, int N>
 static int launch_acc(const CUtensorMap& tq, const CUtensorMap& tk, const Acc& g, cudaStream_t s) {
+  using C = AccCfg<D, kFp8, N>;
+  constexpr int smem = acc_smem<D, kFp8, N>();
   auto kern = fa_accumulate_kernel<D, kFp8, N>;
   static std::atomic<uint64_t> prepared{0};
-  const int rc = prepare_kernel(reinterpret_cast<const void*>(kern), acc_smem<D, kFp8, N>(), kAccThreads, 0, "accumulate kernel",
-                                &prepared);
+  int rc = prepare_kernel(reinterpret_cast<const void*>(kern), smem, C::kThreads, 0, "accumulate kernel", &prepared);
   if (rc) return rc;
-  kern<<<sm_count(), kAccThreads, acc_smem<D, kFp8, N>(), s>>>(tq, tk, g);
-  return check_cuda(cudaGetLastError(), "launch fa_accumulate_kernel");
+  if (C::kPieced) return launch_early("launch fa_accumulate_kernel", kern, sm_count(), C::kThreads, smem, s, tq, tk, g);
+  kern<<<sm_count(), C::kThreads, smem, s>>>(tq, tk, g);
+  if ((rc = check_cuda(cudaGetLastError(), "launch fa_accumulate_kernel"))) return rc;
+  if (!C::kChunk || g.max_parts == 1) return FA_OK;
+  // (units are cut in two at least where there are half as many as parts at most)
+  return launch_early("launch fa_accumulate_join", fa_accumulate_join, kMostParts / 2, kAccKeys, 0, s, g);
 }
 
 template <int D, bool kFp8>
@@ -599,8 +864,20 @@ static int launch_columns(int columns, const CUtensorMap& tq, const CUtensorMap&
   return launch_acc<D, kFp8, 128>(tq, tk, g, s);
 }
 
-static int check_accumulate(int T, int Hq, int Hkv, int d) {
-  if (T < 0) return set_error(FA_ERR_INVALID_ARG, "T must be >= 0 (got %d)", T);
+// Columns of S, which hold all of a sequence's rows for a kv head, or a block of them.
+static int columns_of(int max_q, int group) {
+  const long long rows = (long long)max_q * group;
+  return rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128));
+}
+
+// Chunks: the most parts that a unit may be cut into.
+static int parts_of(int max_q, int group) {
+  const int tokens = 128 / group;
+  return (int)std::max(1ll, std::min(16ll, ((long long)max_q + tokens - 1) / tokens / kPartBlocks));
+}
+
+static int check_accumulate(int T, int max_q, int Hq, int Hkv, int d) {
+  if (T < 0 || max_q < 0) return set_error(FA_ERR_INVALID_ARG, "T, max_q must be >= 0 (got %d, %d)", T, max_q);
   if (Hkv < 1 || Hq < 1) return set_error(FA_ERR_INVALID_ARG, "Hq, Hkv must be >= 1 (got %d, %d)", Hq, Hkv);
   if (Hq % Hkv) return set_error(FA_ERR_INVALID_ARG, "Hq = %d is not a multiple of Hkv = %d", Hq, Hkv);
   if (Hq / Hkv > 128) return set_error(FA_ERR_UNSUPPORTED, "more than 128 query heads for a kv head (%d)", Hq / Hkv);
@@ -609,17 +886,22 @@ static int check_accumulate(int T, int Hq, int Hkv, int d) {
   return FA_OK;
 }
 
-// E4M3: the queries' pieces, then their factors.
+// Few rows over E4M3: the queries' pieces, then their factors.  Chunks: the parts' sums.
 static size_t pieces_bytes(int T, int Hq, int d) { return round_up((size_t)kPieces * T * Hq * d, 256); }
+static size_t accumulate_bytes(int T, int max_q, int Hq, int Hkv, int d, int dtype) {
+  const int group = Hq / Hkv;
+  if (columns_of(max_q, group) == 128) return parts_of(max_q, group) > 1 ? (size_t)kMostParts * kAccKeys * 4 : 0;
+  return dtype == FA_KV_E4M3 ? pieces_bytes(T, Hq, d) + round_up((size_t)T * Hq * 4, 256) : 0;
+}
 
 }  // namespace paged
 }  // namespace fa
 
-extern "C" size_t fa_kv_accumulate_workspace_size(int T, int Hq, int Hkv, int d, int dtype) {
+extern "C" size_t fa_kv_accumulate_workspace_size(int T, int max_q, int Hq, int Hkv, int d, int dtype) {
   using namespace fa;
   clear_error();
-  if (paged::check_accumulate(T, Hq, Hkv, d)) return 0;
-  return dtype == FA_KV_E4M3 ? paged::pieces_bytes(T, Hq, d) + round_up((size_t)T * Hq * 4, 256) : 0;
+  if (paged::check_accumulate(T, max_q, Hq, Hkv, d) || T == 0) return 0;
+  return paged::accumulate_bytes(T, max_q, Hq, Hkv, d, dtype);
 }
 
 extern "C" int fa_kv_accumulate(const fa_paged_kv* kv, float* weights, int64_t weight_stride, const void* q, int64_t q_stride,
@@ -631,13 +913,8 @@ extern "C" int fa_kv_accumulate(const fa_paged_kv* kv, float* weights, int64_t w
   paged::Acc g{};
   paged::Attn& p = g.a;
   int rc;
-  if ((rc = paged::check_cache(kv, &p.c)) || (rc = paged::check_accumulate(T, Hq, kv->Hkv, kv->d))) return rc;
-  if (max_q < 0) return set_error(FA_ERR_INVALID_ARG, "max_q must be >= 0 (got %d)", max_q);
-  if (!weights || (reinterpret_cast<uintptr_t>(weights) & 3))
-    return set_error(FA_ERR_INVALID_ARG, "weights must be a 4-byte aligned device pointer");
-  const long long page = (long long)kv->Hkv * kv->page_size;
-  if (weight_stride < page)
-    return set_error(FA_ERR_INVALID_ARG, "weight_stride %lld must be at least Hkv*page_size = %lld", (long long)weight_stride, page);
+  if ((rc = paged::check_cache(kv, &p.c)) || (rc = paged::check_accumulate(T, max_q, Hq, kv->Hkv, kv->d))) return rc;
+  if ((rc = paged::check_weights(kv, weights, weight_stride))) return rc;
   if ((rc = check_ptr(q, "q")) || (rc = paged::check_indptr(q_indptr, "q_indptr"))) return rc;
   if (!lse || (reinterpret_cast<uintptr_t>(lse) & 3)) return set_error(FA_ERR_INVALID_ARG, "lse must be a 4-byte aligned device pointer");
   if (q_stride < (int64_t)Hq * kv->d || q_stride % 8)
@@ -646,8 +923,8 @@ extern "C" int fa_kv_accumulate(const fa_paged_kv* kv, float* weights, int64_t w
   if (window < 0 || sinks < 0) return set_error(FA_ERR_INVALID_ARG, "window and sinks must be >= 0 (got %d, %d)", window, sinks);
   if (!window && sinks) return set_error(FA_ERR_INVALID_ARG, "sinks need a window");
   const bool fp8 = kv->dtype == FA_KV_E4M3;
-  const size_t need = fp8 ? fa_kv_accumulate_workspace_size(T, Hq, kv->Hkv, kv->d, kv->dtype) : 0;
   if (T == 0 || max_q == 0) return FA_OK;
+  const size_t need = paged::accumulate_bytes(T, max_q, Hq, kv->Hkv, kv->d, kv->dtype);
   if (need) {
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255))
       return set_error(FA_ERR_INVALID_ARG, "workspace must be a 256-byte aligned device pointer");
@@ -677,10 +954,14 @@ extern "C" int fa_kv_accumulate(const fa_paged_kv* kv, float* weights, int64_t w
   g.weight_stride = weight_stride;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int d = kv->d, box = kv->page_size < paged::kAccTile ? kv->page_size : paged::kAccTile;
-  const int columns = p.max_rows <= 16 ? 16 : (p.max_rows <= 32 ? 32 : (p.max_rows <= 64 ? 64 : 128));
+  const int columns = paged::columns_of(max_q, p.group);
+  const bool chunk = columns == 128;
+  g.max_parts = chunk ? paged::parts_of(max_q, p.group) : 1;
+  g.part = static_cast<float*>(workspace);
   CUtensorMap tq, tk;
-  if ((rc = make_tmap_pages(&tk, kv->k, fp8, d, kv->page_size, kv->Hkv, kv->num_pages, kv->page_stride, box))) return rc;
-  if (fp8) {
+  if ((rc = make_tmap_pages(&tk, kv->k, fp8, d, kv->page_size, kv->Hkv, kv->num_pages, kv->page_stride, box, fp8 && chunk)))
+    return rc;
+  if (fp8 && !chunk) {
     uint8_t* pieces = static_cast<uint8_t*>(workspace);
     float* factors = reinterpret_cast<float*>(pieces + paged::pieces_bytes(T, Hq, d));
     g.q_scale = factors;
@@ -691,9 +972,12 @@ extern "C" int fa_kv_accumulate(const fa_paged_kv* kv, float* weights, int64_t w
     else
       paged::split_queries_kernel<128><<<grid, 256, 0, s>>>(p.q, q_stride, T, Hq, pieces, factors);
     if ((rc = check_cuda(cudaGetLastError(), "launch split_queries_kernel"))) return rc;
-    if ((rc = make_tmap_pieces(&tq, pieces, T, Hq, d, paged::kPieces, p.group, columns / p.group))) return rc;
-    return d == 64 ? paged::launch_columns<64, true>(columns, tq, tk, g, s) : paged::launch_columns<128, true>(columns, tq, tk, g, s);
+    rc = make_tmap_pieces(&tq, pieces, T, Hq, d, paged::kPieces, p.group, columns / p.group);
+  } else {
+    rc = make_tmap_rows(&tq, q, T, Hq, d, q_stride, p.group, columns / p.group);
   }
-  if ((rc = make_tmap_rows(&tq, q, T, Hq, d, q_stride, p.group, columns / p.group))) return rc;
+  if (rc) return rc;
+  if (fp8)
+    return d == 64 ? paged::launch_columns<64, true>(columns, tq, tk, g, s) : paged::launch_columns<128, true>(columns, tq, tk, g, s);
   return d == 64 ? paged::launch_columns<64, false>(columns, tq, tk, g, s) : paged::launch_columns<128, false>(columns, tq, tk, g, s);
 }

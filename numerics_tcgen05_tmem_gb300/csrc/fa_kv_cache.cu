@@ -316,6 +316,15 @@ int check_cache(const fa_paged_kv* kv, Cache* c) {
   return FA_OK;
 }
 
+int check_weights(const fa_paged_kv* kv, const float* weights, long long stride) {
+  const int rc = check_ptr(weights, "weights");
+  if (rc) return rc;
+  const long long page = (long long)kv->Hkv * kv->page_size;
+  if (stride < page || stride % 4)
+    return set_error(FA_ERR_INVALID_ARG, "weight_stride %lld must be a multiple of 4 and at least Hkv*page_size = %lld", stride, page);
+  return FA_OK;
+}
+
 int check_indptr(const int32_t* p, const char* name) {
   if (!p || (reinterpret_cast<uintptr_t>(p) & 3))
     return set_error(FA_ERR_INVALID_ARG, "%s must be a 4-byte aligned device pointer", name);

@@ -286,11 +286,7 @@ extern "C" int fa_kv_evict(const fa_paged_kv* kv, float* weights, int64_t weight
   paged::Evict g{};
   int rc;
   if ((rc = paged::check_cache(kv, &g.c))) return rc;
-  const long long page = (long long)kv->Hkv * kv->page_size;
-  if (!weights || (reinterpret_cast<uintptr_t>(weights) & 3))
-    return set_error(FA_ERR_INVALID_ARG, "weights must be a 4-byte aligned device pointer");
-  if (weight_stride < page)
-    return set_error(FA_ERR_INVALID_ARG, "weight_stride %lld must be at least Hkv*page_size = %lld", (long long)weight_stride, page);
+  if ((rc = paged::check_weights(kv, weights, weight_stride))) return rc;
   if (keep < 1 || sinks < 0 || recent < 0) return set_error(FA_ERR_INVALID_ARG, "keep must be >= 1, sinks and recent >= 0 (got %d, %d, %d)", keep, sinks, recent);
   if ((long long)sinks + recent > keep)
     return set_error(FA_ERR_INVALID_ARG, "sinks + recent = %lld must be at most keep = %d", (long long)sinks + recent, keep);

@@ -7,15 +7,22 @@
 //   dx = r g - x r^3 / d sum(x o g).
 // r is computed again from x, which the backward reads in any case.
 //
-// Memory bounds all three: about 7 issue slots of a sub-partition go to a vector, while the copy rate gives
-// an SM 20 clocks for its 512 bytes.  d / 16 lanes take a vector, each two 16-byte parts that hold both
-// entries of its pairs, so that the rotation needs no exchange and the sums three (two) shuffles.
+// Memory bounds all three.  d / 16 lanes take a vector, each two 16-byte parts that hold both entries of its
+// pairs, so that the rotation needs no exchange and the sums three (two) shuffles.  Persistent CTAs, and a
+// thread's copies (cp.async) run two vectors ahead, into slots that only it reads: registers as the store of
+// what is on its way left the backward at 4.7 TB/s, where it now moves 6.0.
+//   8192 tokens, 32 + 32 heads, d = 128: forward 45 us, backward 63 us and 3 us for the weights' gradients
+//   (268 and 403 MB: 5.9 and 6.1 TB/s of the 6.8 of a plain copy); 8 x 1024 tokens, 12 + 12 heads, d = 64: 14 and 19 + 3 us,
+//   where a third is the start (frequencies, angles) and the last, partly filled round of tiles;
+//   23100 packed tokens, 32 + 8 + 8 heads, into a BF16 cache 61 us, 6.2 TB/s.
 //
 // Angles: position times frequency modulo one turn.  In FP32 a position of 2^20 would leave 0.06 rad of error.
 // A frequency is kept as a fraction of a turn in 64 bits; the product with a 32-bit position wraps at whole
 // turns by itself, and its upper 32 bits are the angle (error: pos * 2^-54 turns, from the double it comes from).
 #include <cuda_bf16.h>
 #include <math.h>
+
+#include <algorithm>
 
 #include "paged_attn.cuh"
 
@@ -25,8 +32,14 @@ namespace rotate {
 using paged::Cache;
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;    // vectors in flight for each lane group (backward: kUnrollBwd)
-constexpr int kUnrollBwd = 1;
+// Measured on 8192 tokens, 32 and 32 heads, d = 128 (forward and backward together), and on 23100 packed tokens, 32 and 8
+// heads, into BF16: as chosen 113 and 61 us; with two CTAs for the forward 118 and 66 (registers as the store of
+// what is on its way), with four of two stages 119 and 64, with one CTA for the backward 138; two heads for a
+// lane group 126 and 74, eight 113 and 73.
+constexpr int kCtas = 3;       // forward and append: CTAs on an SM
+constexpr int kBwdCtas = 2;    // backward
+constexpr int kStages = 3;     // vectors of a lane group that are worked on or on their way
+constexpr int kHeads = 4;      // heads of a token for one lane group, where there are enough tokens
 
 // Lane groups: kLanes neighbouring lanes hold a vector, lane j the 8-element parts a(j) and b(j).
 template <int D>
@@ -70,21 +83,15 @@ __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
   return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
 }
 
-// The first elements of lane j's parts.  Pairs (i, i + rot / 2): a and b lie rot / 2 apart.  Neighbouring
-// pairs, and lanes behind the rotated entries: 16 elements in a row.
-template <bool kInter>
+// The first elements of lane j's parts.  Neighbouring lanes take neighbouring 16 bytes, so that an access of the
+// lanes covers whole sectors (with 32 bytes in a row for each lane the forward took 59 us where it takes 45).
+// Pairs (i, i + rot / 2): a and b lie rot / 2 apart, and half the rest behind the rotated entries.  Neighbouring
+// pairs lie within a part.
+template <int D, bool kInter>
 __device__ __forceinline__ void part_columns(int j, int rot, int& a, int& b) {
-  const bool split = !kInter && 16 * j < rot;
-  a = split ? 8 * j : 16 * j;
-  b = split ? 8 * j + rot / 2 : 16 * j + 8;
-}
-
-__device__ __forceinline__ void load_weights(const void* w, int is_bf16, int col, float (&f)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    f[i] = w == nullptr ? 1.f
-                        : (is_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(w)[col + i])
-                                   : static_cast<const float*>(w)[col + i]);
+  const bool rest = !kInter && 16 * j >= rot;
+  a = rest ? 8 * j + rot / 2 : 8 * j;              // (rot + 8 (j - rot / 16))
+  b = a + (kInter ? D : (rest ? D - rot : rot)) / 2;
 }
 
 // Sum over the lanes of a group.
@@ -102,101 +109,159 @@ __device__ __forceinline__ float inverse_rms(float sum, int d, const Plan& p) {
 // The pairs of a lane turned by its eight angles (kSign = -1: back).
 template <bool kInter, int kSign>
 __device__ __forceinline__ void turn(Parts& v, const float (&c)[8], const float (&s)[8]) {
+  if constexpr (kInter) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float& x = kInter ? (i < 4 ? v.a[2 * i] : v.b[2 * i - 8]) : v.a[i];
-    float& y = kInter ? (i < 4 ? v.a[2 * i + 1] : v.b[2 * i - 7]) : v.b[i];
-    const float sn = kSign * s[i], x0 = x, y0 = y;
-    x = x0 * c[i] - y0 * sn;
-    y = y0 * c[i] + x0 * sn;
+    for (int i = 0; i < 8; ++i) {
+      float& x = i < 4 ? v.a[2 * i] : v.b[2 * i - 8];
+      float& y = i < 4 ? v.a[2 * i + 1] : v.b[2 * i - 7];
+      float p, q;
+      mul2(p, q, y, x, -kSign * s[i], kSign * s[i]);
+      fma2(x, y, x, y, c[i], c[i], p, q);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      float p0, p1, q0, q1;   // s y, s x
+      mul2(p0, p1, s[i], s[i + 1], v.b[i], v.b[i + 1]);
+      mul2(q0, q1, s[i], s[i + 1], v.a[i], v.a[i + 1]);
+      fma2(v.a[i], v.a[i + 1], v.a[i], v.a[i + 1], c[i], c[i + 1], -kSign * p0, -kSign * p1);
+      fma2(v.b[i], v.b[i + 1], v.b[i], v.b[i + 1], c[i], c[i + 1], kSign * q0, kSign * q1);
+    }
   }
 }
 
-// cos and sin of a tile's tokens.  The tables start behind the frequencies, kFreq of them.
-struct Table {
-  uint64_t* turns;   // [rot / 2] turns for each position, in units of 2^-64
-  float* cos;        // [tokens][rot / 2]
-  float* sin;
+// Shared memory of a CTA.  Lane j reads 16 bytes at j of a row of lanes, so that no two lanes meet in a bank.
+template <int D>
+struct Tables {
+  static constexpr int kLanes = Lanes<D>::kLanes, kMaxTokens = Lanes<D>::kGroups;
+  uint64_t turns[D / 2];                   // of a position, in units of 2^-64
+  float4 weight[4][kLanes];                // of the parts a and b, four each
+  float4 angle[2][kMaxTokens][4][kLanes];  // cos and sin of a tile's tokens, of this tile and of the next
 };
-template <int D>
-__device__ __forceinline__ Table table_at(void* smem, int tokens, int rot) {
-  uint64_t* t = static_cast<uint64_t*>(smem);
-  float* c = reinterpret_cast<float*>(t + D / 2);
-  return Table{t, c, c + tokens * (rot / 2)};
-}
-// bytes for `tokens` tokens at a time
-template <int D>
-constexpr int table_bytes(int tokens) {
-  return D / 2 * 8 + tokens * D * 4;
-}
 
-__device__ __forceinline__ void fill_turns(const Table& t, const Plan& p) {
-  if ((int)threadIdx.x < p.rot / 2) {
-    double f = p.inv_freq[threadIdx.x] * 0.15915494309189533577;   // 1 / (2 pi)
-    f -= floor(f);
-    t.turns[threadIdx.x] = f < 1.0 ? (uint64_t)__double2ull_rd(f * 18446744073709551616.0) : 0;
+template <int D, bool kInter>
+__device__ __forceinline__ void fill_weights(Tables<D>& t, const void* w, int is_bf16, int rot) {
+  if (threadIdx.x < D) {
+    const int j = threadIdx.x / 16, e = threadIdx.x % 16;
+    int a, b;
+    part_columns<D, kInter>(j, rot, a, b);
+    const int col = e < 8 ? a + e : b + e - 8;
+    float f = 1.f;
+    if (w != nullptr)
+      f = is_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(w)[col]) : static_cast<const float*>(w)[col];
+    reinterpret_cast<float*>(&t.weight[e / 4][j])[e % 4] = f;
   }
 }
 
-// position(i): that of the tile's token i.  Every thread of the CTA calls it; a barrier has to follow.
-template <class Position>
-__device__ __forceinline__ void fill_angles(const Table& t, int rot, int tokens, Position position) {
-  const int half = rot / 2;
-  for (int i = threadIdx.x; i < tokens * half; i += kThreads) {
-    const int token = i / half, f = i - token * half;
-    const uint64_t at = (uint64_t)(int64_t)position(token) * t.turns[f];
+// Which angles a thread computes: those of frequency f, kThreads >> shift threads for each.
+struct Mine {
+  int f, shift;
+  __device__ __forceinline__ explicit Mine(int rot) : shift(0) {
+    while ((2 << shift) < rot) ++shift;   // 2^shift >= rot / 2
+    f = threadIdx.x & ((1 << shift) - 1);
+  }
+};
+
+// The thread's frequency as a fraction of a turn.  (All threads of a frequency write the same, each reads
+// it back itself.)
+template <int D>
+__device__ __forceinline__ void fill_turns(Tables<D>& t, const Plan& p, int rot) {
+  const Mine m(rot);
+  if (2 * m.f >= rot) return;
+  double x = __ldg(p.inv_freq + m.f) * 0.15915494309189533577;   // 1 / (2 pi)
+  x -= floor(x);
+  t.turns[m.f] = x < 1.0 ? (uint64_t)__double2ull_rd(x * 18446744073709551616.0) : 0;   // (NaN: 0)
+}
+
+// position(i): that of the tile's token i.  A barrier has to follow.
+template <int D, bool kInter, class Position>
+__device__ __forceinline__ void fill_angles(Tables<D>& t, int buf, int rot, int tokens, Position position) {
+  const Mine m(rot);
+  if (2 * m.f >= rot) return;
+  // a lane's eight: of its eight pairs between a and b, or of four pairs in a and four in b
+  const int row = kInter ? m.f / (D / 4) : m.f % 8 / 4, lane = kInter ? m.f % (D / 4) / 4 : m.f / 8;
+  float* to = reinterpret_cast<float*>(&t.angle[buf][0][row][lane]) + m.f % 4;
+  for (int token = threadIdx.x >> m.shift; token < tokens; token += kThreads >> m.shift) {
+    const uint64_t at = (uint64_t)(int64_t)position(token) * t.turns[m.f];
     // the nearest quarter turn apart, the rest is within an eighth: its rounding to FP32 stays under 2^-25 rad
     const uint32_t u = (uint32_t)(at >> 32), quarter = (u + 0x20000000u) >> 30;
     float s0, c0;
     sincospif((float)(int32_t)(u - (quarter << 30)) * 0x1p-31f, &s0, &c0);   // a turn is 2^32, sincospi's is 2
-    float s = quarter & 1 ? c0 : s0, c = quarter & 1 ? s0 : c0;
-    if (quarter & 2) s = -s;
-    if ((quarter + 1) & 2) c = -c;
-    t.cos[i] = c;
-    t.sin[i] = s;
+    const float s = quarter & 1 ? c0 : s0, c = quarter & 1 ? s0 : c0;
+    constexpr int kRow = 4 * Lanes<D>::kLanes;   // floats of a row of lanes; cos has rows 0 and 1, sin 2 and 3
+    to[token * 4 * kRow] = (quarter + 1) & 2 ? -c : c;
+    to[token * 4 * kRow + 2 * kRow] = quarter & 2 ? -s : s;
   }
 }
 
-__device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
-  const float4 u = reinterpret_cast<const float4*>(p)[0], v = reinterpret_cast<const float4*>(p)[1];
+__device__ __forceinline__ void spread8(const float4& u, const float4& v, float (&f)[8]) {
   f[0] = u.x, f[1] = u.y, f[2] = u.z, f[3] = u.w, f[4] = v.x, f[5] = v.y, f[6] = v.z, f[7] = v.w;
 }
 // A lane's angles of a token: 1 and 0 behind the rotated entries.
-__device__ __forceinline__ void load_angles(const Table& t, int rot, int token, int j, float (&c)[8], float (&s)[8]) {
-  if (16 * j < rot) {
-    load8(t.cos + token * (rot / 2) + 8 * j, c);
-    load8(t.sin + token * (rot / 2) + 8 * j, s);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;
+template <int D, bool kInter>
+__device__ __forceinline__ void load_angles(const Tables<D>& t, int buf, int rot, int token, int j, float (&c)[8], float (&s)[8]) {
+  const float4 one = make_float4(1.f, 1.f, 1.f, 1.f), zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  const bool first = kInter ? 8 * j < rot : 16 * j < rot, second = kInter ? D / 2 + 8 * j < rot : first;
+  const auto& at = t.angle[buf][token];
+  spread8(first ? at[0][j] : one, second ? at[1][j] : one, c);
+  spread8(first ? at[2][j] : zero, second ? at[3][j] : zero, s);
+}
+
+// A thread's own copies of its 16-byte parts, kParts of a vector, on their way to slots of its own: no other
+// thread reads them, so that a wait for the thread's own copies is all it takes.  Every vector is copied before
+// anything is written in its place: an output may be its input.
+template <int kParts>
+struct Ring {
+  uint4 slot[kStages][kParts][kThreads];
+  __device__ __forceinline__ void copy(int stage, int part, const __nv_bfloat16* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&slot[stage][part][threadIdx.x])), "l"(from) : "memory");
   }
+  __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  // the oldest of kStages groups has landed
+  __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory"); }
+  __device__ __forceinline__ uint4 get(int stage, int part) const { return slot[stage][part][threadIdx.x]; }
+};
+
+// Sum of squares of a lane's parts.
+__device__ __forceinline__ float squares(const Parts& v) {
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    fma2(s[0], s[1], v.a[i], v.a[i + 1], v.a[i], v.a[i + 1], s[0], s[1]);
+    fma2(s[2], s[3], v.b[i], v.b[i + 1], v.b[i], v.b[i + 1], s[2], s[3]);
+  }
+  return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
 // One vector's parts normed and turned, in place.
 template <int D, bool kInter>
-__device__ __forceinline__ void forward_vector(Parts& v, const Plan& p, const float (&wa)[8], const float (&wb)[8],
-                                               const float (&c)[8], const float (&s)[8]) {
-  float sum = 0.f;
+__device__ __forceinline__ void forward_vector(Parts& v, const Plan& p, const Tables<D>& t, int j, const float (&c)[8],
+                                               const float (&s)[8]) {
+  if (p.norm) {
+    const float r = inverse_rms(group_sum<Lanes<D>::kLanes>(squares(v)), D, p);
+    float w[8];
+    spread8(t.weight[0][j], t.weight[1][j], w);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) sum += v.a[i] * v.a[i] + v.b[i] * v.b[i];
-  const float r = inverse_rms(group_sum<Lanes<D>::kLanes>(sum), D, p);
+    for (int i = 0; i < 8; i += 2) {
+      mul2(v.a[i], v.a[i + 1], v.a[i], v.a[i + 1], r, r);
+      mul2(v.a[i], v.a[i + 1], v.a[i], v.a[i + 1], w[i], w[i + 1]);
+    }
+    spread8(t.weight[2][j], t.weight[3][j], w);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    v.a[i] = v.a[i] * r * wa[i];
-    v.b[i] = v.b[i] * r * wb[i];
+    for (int i = 0; i < 8; i += 2) {
+      mul2(v.b[i], v.b[i + 1], v.b[i], v.b[i + 1], r, r);
+      mul2(v.b[i], v.b[i + 1], v.b[i], v.b[i + 1], w[i], w[i + 1]);
+    }
   }
   turn<kInter, 1>(v, c, s);
 }
 
-// (not through the read-only path: an output may be its input, every vector is read before it is written)
-__device__ __forceinline__ uint4 load16(const __nv_bfloat16* p) { return *reinterpret_cast<const uint4*>(p); }
-
 // The token of a dense batch: batch entry and place in it.
 struct Place {
-  long long b, n;
+  unsigned b, n;
 };
-__device__ __forceinline__ Place place_of(long long token, int N) {
-  const long long b = token / N;
+__device__ __forceinline__ Place place_of(unsigned token, int N) {
+  const unsigned b = token / (unsigned)N;
   return Place{b, token - b * N};
 }
 
@@ -204,172 +269,251 @@ struct Dense {
   Plan p;
   const int32_t* positions;   // NULL: 0, 1, ..
   long long pos_b;            // entries between two sequences' positions
-  long long tokens;           // B * N
+  unsigned tokens;            // B * N, under 2^31
   int N;
 };
 
-__device__ __forceinline__ int dense_position(const Dense& g, long long token) {
+__device__ __forceinline__ int dense_position(const Dense& g, unsigned token) {
   if (token >= g.tokens) return 0;
   const Place at = place_of(token, g.N);
   return g.positions == nullptr ? (int)at.n : __ldg(g.positions + at.b * g.pos_b + at.n);
 }
 
-// A CTA has kGroups >> shift tokens of one side; the first q.ctas CTAs are the queries'.
+// How a side's tokens are dealt: a tile has kGroups >> shift tokens, CTA i takes the tiles i, i + ctas, ..
+// Lane group x of a CTA has token x >> shift of the tile and the heads (x & groups - 1), + groups, ..
+struct Deal {
+  int groups, tokens, mine, head0;
+  unsigned tiles;
+  __device__ __forceinline__ Deal(int shift, int all_groups, int group, unsigned all)
+      : groups(1 << shift), tokens(all_groups >> shift), mine(group >> shift), head0(group & ((1 << shift) - 1)),
+        tiles((all + tokens - 1) / tokens) {}
+};
+
+// The vectors of a lane group, in the order in which it works on them; one of these runs ahead for the copies.
+struct Ahead {
+  unsigned tile;
+  int h, stage;
+};
+
+template <int D, int kParts>
+struct Shared {
+  Tables<D> t;
+  Ring<kParts> ring;
+};
+
+// The first q.ctas CTAs have the queries.  Copies run kStages - 1 vectors ahead, and the next tile's angles are
+// computed beside the current one's vectors: one barrier for a tile.
 template <int D, bool kInter>
-__global__ void __launch_bounds__(kThreads, 2) norm_rotate_kernel(const __grid_constant__ Dense g,
-                                                                  const __grid_constant__ Side q,
-                                                                  const __grid_constant__ Side k) {
+__global__ void __launch_bounds__(kThreads, kCtas) norm_rotate_kernel(const __grid_constant__ Dense g,
+                                                                      const __grid_constant__ Side q,
+                                                                      const __grid_constant__ Side k) {
   using L = Lanes<D>;
   extern __shared__ __align__(16) uint8_t smem[];
+  Tables<D>& t = reinterpret_cast<Shared<D, 2>*>(smem)->t;
+  Ring<2>& ring = reinterpret_cast<Shared<D, 2>*>(smem)->ring;
   const bool is_q = (int)blockIdx.x < q.ctas;
   const Side& side = is_q ? q : k;
-  const int tokens = L::kGroups >> side.shift, groups = 1 << side.shift;
-  const long long first = (long long)((int)blockIdx.x - (is_q ? 0 : q.ctas)) * tokens;
-  const int group = threadIdx.x / L::kLanes, j = threadIdx.x % L::kLanes;
-  const int mine = group >> side.shift, head0 = group & (groups - 1);
-  const long long token = first + mine;
-  const bool valid = token < g.tokens;
-  const Place at = place_of(valid ? token : 0, g.N);
+  const int j = threadIdx.x % L::kLanes, H = side.H;
+  const Deal d(side.shift, L::kGroups, threadIdx.x / L::kLanes, g.tokens);
   int ca, cb;
-  part_columns<kInter>(j, g.p.rot, ca, cb);
-  const __nv_bfloat16* x = side.x + at.b * side.x_b + at.n * side.x_n;
-  __nv_bfloat16* z = side.out + at.b * side.out_b + at.n * side.out_n;
+  part_columns<D, kInter>(j, g.p.rot, ca, cb);
+  unsigned tile = blockIdx.x - (is_q ? 0 : q.ctas);
 
-  uint4 xa[kUnroll], xb[kUnroll];
-  auto load = [&](int h0) {
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int h = h0 + u * groups;
-      if (valid && h < side.H) {
-        xa[u] = load16(x + h * side.x_h + ca);
-        xb[u] = load16(x + h * side.x_h + cb);
-      }
+  Ahead next{tile, d.head0, 0};
+  const __nv_bfloat16* from = nullptr;
+  auto seek = [&] {   // the first vector of next.tile
+    const unsigned token = next.tile * d.tokens + d.mine;
+    from = nullptr;
+    if (next.tile < d.tiles && token < g.tokens) {
+      const Place at = place_of(token, g.N);
+      from = side.x + at.b * side.x_b + at.n * side.x_n;
     }
   };
-  load(head0);   // in flight while the angles are computed
-  const Table t = table_at<D>(smem, tokens, g.p.rot);
-  fill_turns(t, g.p);
-  float wa[8], wb[8], c[8], s[8];
-  load_weights(side.w, side.w_bf16, ca, wa);
-  load_weights(side.w, side.w_bf16, cb, wb);
-  __syncthreads();
-  fill_angles(t, g.p.rot, tokens, [&](int i) { return dense_position(g, first + i); });
-  __syncthreads();
-  load_angles(t, g.p.rot, mine, j, c, s);
-  for (int h0 = head0; h0 - head0 < side.H; h0 += kUnroll * groups) {
-    if (h0 != head0) load(h0);
+  auto copy = [&] {
+    if (from != nullptr && next.h < H) {
+      ring.copy(next.stage, 0, from + next.h * side.x_h + ca);
+      ring.copy(next.stage, 1, from + next.h * side.x_h + cb);
+    }
+    ring.commit();
+    next.stage = next.stage + 1 == kStages ? 0 : next.stage + 1;
+    next.h += d.groups;
+    if (next.h - d.head0 >= H) {
+      next.h = d.head0;
+      next.tile += side.ctas;
+      seek();
+    }
+  };
+  seek();
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int h = h0 + u * groups;
-      if (h - head0 >= side.H) break;   // the same for the whole CTA: the shuffles need every lane
+  for (int i = 0; i < kStages - 1; ++i) copy();
+  fill_turns(t, g.p, g.p.rot);
+  fill_weights<D, kInter>(t, side.w, side.w_bf16, g.p.rot);
+  fill_angles<D, kInter>(t, 0, g.p.rot, d.tokens, [&](int i) { return dense_position(g, tile * d.tokens + i); });
+  __syncthreads();
+  int stage = 0;
+  for (int buf = 0; tile < d.tiles; tile += side.ctas, buf ^= 1) {
+    const unsigned after = tile + side.ctas, token = tile * d.tokens + d.mine;
+    if (after < d.tiles)
+      fill_angles<D, kInter>(t, buf ^ 1, g.p.rot, d.tokens, [&](int i) { return dense_position(g, after * d.tokens + i); });
+    const bool valid = token < g.tokens;
+    const Place at = place_of(valid ? token : 0, g.N);
+    __nv_bfloat16* z = side.out + at.b * side.out_b + at.n * side.out_n;
+    float c[8], s[8];
+    load_angles<D, kInter>(t, buf, g.p.rot, d.mine, j, c, s);
+    for (int h = d.head0; h - d.head0 < H; h += d.groups) {   // the same number of steps for the whole CTA
+      copy();
+      ring.wait();
       Parts v;
-      unpack(xa[u], v.a);
-      unpack(xb[u], v.b);
-      forward_vector<D, kInter>(v, g.p, wa, wb, c, s);
-      if (valid && h < side.H) {
+      unpack(ring.get(stage, 0), v.a);
+      unpack(ring.get(stage, 1), v.b);
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+      forward_vector<D, kInter>(v, g.p, t, j, c, s);
+      if (valid && h < H) {
         *reinterpret_cast<uint4*>(z + h * side.out_h + ca) = pack(v.a);
         *reinterpret_cast<uint4*>(z + h * side.out_h + cb) = pack(v.b);
       }
     }
+    __syncthreads();
   }
 }
 
-// CTA i of a side takes its tiles i, i + ctas, ..; the weights' gradients are summed in registers, then
-// over the CTA's groups, and the CTA's sum goes to part[CTA][d].
+// The weights' gradients are summed in registers, then over the CTA's groups, and the CTA's sum goes to
+// part[CTA][d].
 template <int D, bool kInter>
-__global__ void __launch_bounds__(kThreads, 2) norm_rotate_bwd_kernel(const __grid_constant__ Dense g,
-                                                                      const __grid_constant__ Side q,
-                                                                      const __grid_constant__ Side k,
-                                                                      float* __restrict__ part) {
+__global__ void __launch_bounds__(kThreads, kBwdCtas) norm_rotate_bwd_kernel(const __grid_constant__ Dense g,
+                                                                             const __grid_constant__ Side q,
+                                                                             const __grid_constant__ Side k,
+                                                                             float* __restrict__ part) {
   using L = Lanes<D>;
+  cudaTriggerProgrammaticLaunchCompletion();   // the weights' kernel may get ready; it waits for this one's end
   extern __shared__ __align__(16) uint8_t smem[];
+  Tables<D>& t = reinterpret_cast<Shared<D, 4>*>(smem)->t;
+  Ring<4>& ring = reinterpret_cast<Shared<D, 4>*>(smem)->ring;
   const bool is_q = (int)blockIdx.x < q.ctas;
   const Side& side = is_q ? q : k;
-  const int tokens = L::kGroups >> side.shift, groups = 1 << side.shift;
-  const int cta = (int)blockIdx.x - (is_q ? 0 : q.ctas);
-  const int group = threadIdx.x / L::kLanes, j = threadIdx.x % L::kLanes;
-  const int mine = group >> side.shift, head0 = group & (groups - 1);
+  const int j = threadIdx.x % L::kLanes, group = threadIdx.x / L::kLanes, H = side.H;
+  const Deal d(side.shift, L::kGroups, group, g.tokens);
   int ca, cb;
-  part_columns<kInter>(j, g.p.rot, ca, cb);
-  const Table t = table_at<D>(smem, tokens, g.p.rot);
-  fill_turns(t, g.p);
-  float wa[8], wb[8], dwa[8], dwb[8];
-  load_weights(side.w, side.w_bf16, ca, wa);
-  load_weights(side.w, side.w_bf16, cb, wb);
+  part_columns<D, kInter>(j, g.p.rot, ca, cb);
+  unsigned tile = blockIdx.x - (is_q ? 0 : q.ctas);
+  float dwa[8], dwb[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) dwa[i] = dwb[i] = 0.f;
 
-  const long long tiles = (g.tokens + tokens - 1) / tokens;
-  for (long long tile = cta; tile < tiles; tile += side.ctas) {
-    const long long token = tile * tokens + mine;
+  Ahead next{tile, d.head0, 0};
+  const __nv_bfloat16 *from = nullptr, *from_dz = nullptr;
+  auto seek = [&] {
+    const unsigned token = next.tile * d.tokens + d.mine;
+    from = nullptr;
+    if (next.tile < d.tiles && token < g.tokens) {
+      const Place at = place_of(token, g.N);
+      from = side.x + at.b * side.x_b + at.n * side.x_n;
+      from_dz = side.dz + at.b * side.dz_b + at.n * side.dz_n;
+    }
+  };
+  auto copy = [&] {
+    if (from != nullptr && next.h < H) {
+      ring.copy(next.stage, 0, from + next.h * side.x_h + ca);
+      ring.copy(next.stage, 1, from + next.h * side.x_h + cb);
+      ring.copy(next.stage, 2, from_dz + next.h * side.dz_h + ca);
+      ring.copy(next.stage, 3, from_dz + next.h * side.dz_h + cb);
+    }
+    ring.commit();
+    next.stage = next.stage + 1 == kStages ? 0 : next.stage + 1;
+    next.h += d.groups;
+    if (next.h - d.head0 >= H) {
+      next.h = d.head0;
+      next.tile += side.ctas;
+      seek();
+    }
+  };
+  seek();
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) copy();
+  fill_turns(t, g.p, g.p.rot);
+  fill_weights<D, kInter>(t, side.w, side.w_bf16, g.p.rot);
+  fill_angles<D, kInter>(t, 0, g.p.rot, d.tokens, [&](int i) { return dense_position(g, tile * d.tokens + i); });
+  __syncthreads();
+  int stage = 0;
+  for (int buf = 0; tile < d.tiles; tile += side.ctas, buf ^= 1) {
+    const unsigned after = tile + side.ctas, token = tile * d.tokens + d.mine;
+    if (after < d.tiles)
+      fill_angles<D, kInter>(t, buf ^ 1, g.p.rot, d.tokens, [&](int i) { return dense_position(g, after * d.tokens + i); });
     const bool valid = token < g.tokens;
     const Place at = place_of(valid ? token : 0, g.N);
-    const __nv_bfloat16* x = side.x + at.b * side.x_b + at.n * side.x_n;
-    const __nv_bfloat16* dz = side.dz + at.b * side.dz_b + at.n * side.dz_n;
     __nv_bfloat16* dx = side.out + at.b * side.out_b + at.n * side.out_n;
-    uint4 xa[kUnrollBwd], xb[kUnrollBwd], za[kUnrollBwd], zb[kUnrollBwd];
-    auto load = [&](int h0) {
+    float c[8], s[8];
+    load_angles<D, kInter>(t, buf, g.p.rot, d.mine, j, c, s);
+    for (int h = d.head0; h - d.head0 < H; h += d.groups) {   // the same number of steps for the whole CTA
+      copy();
+      ring.wait();
+      Parts v, dy;
+      unpack(ring.get(stage, 0), v.a);
+      unpack(ring.get(stage, 1), v.b);
+      unpack(ring.get(stage, 2), dy.a);
+      unpack(ring.get(stage, 3), dy.b);
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+      const bool real = valid && h < H;   // (else its slot holds what was there)
+      turn<kInter, -1>(dy, c, s);
+      float r = 1.f, back = 0.f;
+      if (g.p.norm) {
+        float dot[4] = {0.f, 0.f, 0.f, 0.f}, w[8], m0, m1;
+        spread8(t.weight[0][j], t.weight[1][j], w);
 #pragma unroll
-      for (int u = 0; u < kUnrollBwd; ++u) {
-        const int h = h0 + u * groups;
-        xa[u] = xb[u] = za[u] = zb[u] = make_uint4(0, 0, 0, 0);   // adds nothing to the weights' gradient
-        if (valid && h < side.H) {
-          xa[u] = load16(x + h * side.x_h + ca);
-          xb[u] = load16(x + h * side.x_h + cb);
-          za[u] = load16(dz + h * side.dz_h + ca);
-          zb[u] = load16(dz + h * side.dz_h + cb);
+        for (int i = 0; i < 8; i += 2) {
+          mul2(m0, m1, w[i], w[i + 1], dy.a[i], dy.a[i + 1]);
+          fma2(dot[0], dot[1], v.a[i], v.a[i + 1], m0, m1, dot[0], dot[1]);
+        }
+        spread8(t.weight[2][j], t.weight[3][j], w);
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          mul2(m0, m1, w[i], w[i + 1], dy.b[i], dy.b[i + 1]);
+          fma2(dot[2], dot[3], v.b[i], v.b[i + 1], m0, m1, dot[2], dot[3]);
+        }
+        const float sum = group_sum<L::kLanes>(squares(v));
+        const float all = group_sum<L::kLanes>((dot[0] + dot[1]) + (dot[2] + dot[3]));
+        r = inverse_rms(sum, D, g.p);
+        back = -all * r * r * (1.f / D);   // -sum(x o g) r^2 / d
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          mul2(v.a[i], v.a[i + 1], v.a[i], v.a[i + 1], r, r);   // x r
+          mul2(v.b[i], v.b[i + 1], v.b[i], v.b[i + 1], r, r);
+        }
+        if (real) {
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) {
+            fma2(dwa[i], dwa[i + 1], dy.a[i], dy.a[i + 1], v.a[i], v.a[i + 1], dwa[i], dwa[i + 1]);
+            fma2(dwb[i], dwb[i + 1], dy.b[i], dy.b[i + 1], v.b[i], v.b[i + 1], dwb[i], dwb[i + 1]);
+          }
         }
       }
-    };
-    load(head0);
-    __syncthreads();   // the turns are there; the last tile's angles have been read
-    fill_angles(t, g.p.rot, tokens, [&](int i) { return dense_position(g, tile * tokens + i); });
-    __syncthreads();
-    float c[8], s[8];
-    load_angles(t, g.p.rot, mine, j, c, s);
-    for (int h0 = head0; h0 - head0 < side.H; h0 += kUnrollBwd * groups) {
-      if (h0 != head0) load(h0);
+      // dx = r w dy - (x r) sum(x o g) r^2 / d
+      float w[8];
+      spread8(t.weight[0][j], t.weight[1][j], w);
 #pragma unroll
-      for (int u = 0; u < kUnrollBwd; ++u) {
-        const int h = h0 + u * groups;
-        if (h - head0 >= side.H) break;
-        Parts v, dy;
-        unpack(xa[u], v.a);
-        unpack(xb[u], v.b);
-        unpack(za[u], dy.a);
-        unpack(zb[u], dy.b);
-        turn<kInter, -1>(dy, c, s);
-        float sum = 0.f, dot = 0.f;
+      for (int i = 0; i < 8; i += 2) {
+        mul2(dy.a[i], dy.a[i + 1], dy.a[i], dy.a[i + 1], w[i], w[i + 1]);
+        mul2(dy.a[i], dy.a[i + 1], dy.a[i], dy.a[i + 1], r, r);
+        fma2(v.a[i], v.a[i + 1], v.a[i], v.a[i + 1], back, back, dy.a[i], dy.a[i + 1]);
+      }
+      spread8(t.weight[2][j], t.weight[3][j], w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          sum += v.a[i] * v.a[i] + v.b[i] * v.b[i];
-          dot += v.a[i] * (wa[i] * dy.a[i]) + v.b[i] * (wb[i] * dy.b[i]);
-        }
-        sum = group_sum<L::kLanes>(sum);
-        dot = group_sum<L::kLanes>(dot);
-        const float r = inverse_rms(sum, D, g.p);
-        const float back = g.p.norm ? dot * r * r * (1.f / D) : 0.f;   // sum(x o g) r^2 / d
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float ua = v.a[i] * r, ub = v.b[i] * r;
-          if (valid && h < side.H) {
-            dwa[i] += dy.a[i] * ua;
-            dwb[i] += dy.b[i] * ub;
-          }
-          v.a[i] = r * (wa[i] * dy.a[i]) - ua * back;
-          v.b[i] = r * (wb[i] * dy.b[i]) - ub * back;
-        }
-        if (valid && h < side.H) {
-          *reinterpret_cast<uint4*>(dx + h * side.out_h + ca) = pack(v.a);
-          *reinterpret_cast<uint4*>(dx + h * side.out_h + cb) = pack(v.b);
-        }
+      for (int i = 0; i < 8; i += 2) {
+        mul2(dy.b[i], dy.b[i + 1], dy.b[i], dy.b[i + 1], w[i], w[i + 1]);
+        mul2(dy.b[i], dy.b[i + 1], dy.b[i], dy.b[i + 1], r, r);
+        fma2(v.b[i], v.b[i + 1], v.b[i], v.b[i + 1], back, back, dy.b[i], dy.b[i + 1]);
+      }
+      if (real) {
+        *reinterpret_cast<uint4*>(dx + h * side.out_h + ca) = pack(v.a);
+        *reinterpret_cast<uint4*>(dx + h * side.out_h + cb) = pack(v.b);
       }
     }
+    __syncthreads();
   }
   if (part == nullptr) return;
   // the groups' sums: one row of d for each group in shared memory, summed in order
-  __syncthreads();
-  float* rows = reinterpret_cast<float*>(smem);
+  float* rows = reinterpret_cast<float*>(t.angle);
+  static_assert(sizeof(t.angle) >= L::kGroups * D * sizeof(float), "room for the groups' sums");
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     rows[group * D + ca + i] = dwa[i];
@@ -384,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rotate_bwd_kernel(const __gr
 }
 
 // The weights' gradients: the CTAs' sums, always in the same order.  A CTA has 32 columns of one side; its
-// 32 warps take every 32nd part each.
+// 32 warps take every 32nd part each.  A programmatic launch: it starts beside the last CTAs and waits for them.
 __global__ void __launch_bounds__(1024) weight_grad_kernel(const float* __restrict__ part, int d, int q_ctas, int k_ctas,
                                                            float* __restrict__ dqw, float* __restrict__ dkw) {
   __shared__ float sums[32][33];
@@ -393,6 +537,7 @@ __global__ void __launch_bounds__(1024) weight_grad_kernel(const float* __restri
   const int col = ((int)blockIdx.x - (is_q ? 0 : d / 32)) * 32 + lane;
   const float* from = part + (is_q ? 0 : (long long)q_ctas * d) + col;
   const int n = is_q ? q_ctas : k_ctas;
+  cudaGridDependencySynchronize();
   float sum = 0.f;
 #pragma unroll 4
   for (int i = warp; i < n; i += 32) sum += from[(long long)i * d];
@@ -447,111 +592,132 @@ __device__ __forceinline__ void quantize(const Parts& v, uint2& ca, uint2& cb, f
   }
 }
 
-// A CTA has kGroups >> shift tokens of the queries, the keys or the values (in the order of the CTAs).
+// Where a tile's tokens lie: page (negative: not written) and slot in the cache, position for the rotation.
+template <int kTokens>
+struct Places {
+  int page[3][kTokens], slot[3][kTokens], pos[3][kTokens];   // of this tile and the next two
+};
+
+// The CTAs have the queries, the keys and the values, in this order; the loop is norm_rotate_kernel's.
 template <int D, bool kInter, bool kFp8>
-__global__ void __launch_bounds__(kThreads, 2) qkv_append_kernel(const __grid_constant__ Packed g,
-                                                                 const __grid_constant__ Side q, const __grid_constant__ Side k,
-                                                                 const __grid_constant__ Side v) {
+__global__ void __launch_bounds__(kThreads, kCtas) qkv_append_kernel(const __grid_constant__ Packed g,
+                                                                     const __grid_constant__ Side q,
+                                                                     const __grid_constant__ Side k,
+                                                                     const __grid_constant__ Side v) {
   using L = Lanes<D>;
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ int at_page[L::kGroups], at_slot[L::kGroups], at_pos[L::kGroups];
-  int cta = blockIdx.x;
-  const int which = cta < q.ctas ? 0 : (cta < q.ctas + k.ctas ? 1 : 2);
-  cta -= which == 0 ? 0 : (which == 1 ? q.ctas : q.ctas + k.ctas);
+  Tables<D>& t = reinterpret_cast<Shared<D, 2>*>(smem)->t;
+  Ring<2>& ring = reinterpret_cast<Shared<D, 2>*>(smem)->ring;
+  __shared__ Places<L::kGroups> at;
+  unsigned tile = blockIdx.x;
+  const int which = (int)tile < q.ctas ? 0 : ((int)tile < q.ctas + k.ctas ? 1 : 2);
+  tile -= which == 0 ? 0 : (which == 1 ? q.ctas : q.ctas + k.ctas);
   const Side& side = which == 0 ? q : (which == 1 ? k : v);
-  const int tokens = L::kGroups >> side.shift, groups = 1 << side.shift;
-  const long long first = (long long)cta * tokens;
-  const int group = threadIdx.x / L::kLanes, j = threadIdx.x % L::kLanes;
-  const int mine = group >> side.shift, head0 = group & (groups - 1);
-  const long long token = first + mine;
-  const bool there = token < g.T;
+  const int j = threadIdx.x % L::kLanes, H = side.H, T = g.T;
+  const Deal d(side.shift, L::kGroups, threadIdx.x / L::kLanes, T);
   const int rot = which == 2 ? 0 : g.p.rot;
   int ca, cb;
-  part_columns<kInter>(j, rot, ca, cb);
-  const __nv_bfloat16* x = side.x + (there ? token : 0) * side.x_n;
+  part_columns<D, kInter>(j, rot, ca, cb);
 
-  uint4 xa[kUnroll], xb[kUnroll];
-  auto load = [&](int h0) {
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int h = h0 + u * groups;
-      if (there && h < side.H) {
-        xa[u] = load16(x + h * side.x_h + ca);
-        xb[u] = load16(x + h * side.x_h + cb);
-      }
+  Ahead next{tile, d.head0, 0};
+  auto copy = [&] {
+    const unsigned token = next.tile * d.tokens + d.mine;
+    if (next.tile < d.tiles && token < (unsigned)T && next.h < H) {
+      const __nv_bfloat16* from = side.x + token * side.x_n + next.h * D;
+      ring.copy(next.stage, 0, from + ca);
+      ring.copy(next.stage, 1, from + cb);
+    }
+    ring.commit();
+    next.stage = next.stage + 1 == kStages ? 0 : next.stage + 1;
+    next.h += d.groups;
+    if (next.h - d.head0 >= H) {
+      next.h = d.head0;
+      next.tile += side.ctas;
     }
   };
-  load(head0);
-  const Table t = table_at<D>(smem, tokens, rot);
-  if (which != 2) fill_turns(t, g.p);
-  if ((int)threadIdx.x < tokens) {
-    const long long i = first + threadIdx.x;
+  // the places of a tile's tokens, by one thread each: four loads that wait for one another
+  auto look = [&](unsigned at_tile, int slot) {
+    if ((int)threadIdx.x >= d.tokens || at_tile >= d.tiles) return;
+    const long long i = (long long)at_tile * d.tokens + threadIdx.x;
     int page = -1, pos = 0;
-    const int b = i < g.T ? paged::find_sequence(g.q_indptr, g.c.B, (int)i) : -1;
+    const int b = i < T ? paged::find_sequence(g.q_indptr, g.c.B, (int)i) : -1;
     if (b >= 0) {
       pos = __ldg(g.c.kv_len + b) - __ldg(g.q_indptr + b + 1) + (int)i;
       page = which == 0 ? 0 : paged::find_page(g.c, b, pos, kSitePagedAppend);
     }
-    at_page[threadIdx.x] = page;
-    at_slot[threadIdx.x] = pos & ((1 << g.c.page_shift) - 1);
-    at_pos[threadIdx.x] = b >= 0 && g.positions != nullptr ? __ldg(g.positions + i) : pos;
-  }
-  float wa[8], wb[8], c[8], s[8];
-  load_weights(side.w, side.w_bf16, ca, wa);
-  load_weights(side.w, side.w_bf16, cb, wb);
-  __syncthreads();
-  fill_angles(t, rot, tokens, [&](int i) { return at_pos[i]; });
-  __syncthreads();
-  load_angles(t, rot, mine, j, c, s);
-  const int page = at_page[mine];
-  const bool valid = there && page >= 0;
-  const long long page_size = 1ll << g.c.page_shift;
-  const long long to = which == 0 ? token * side.out_n : page * g.c.page_stride + at_slot[mine] * (long long)D;
-  const long long to_scale = page * g.c.scale_stride + at_slot[mine];
-  for (int h0 = head0; h0 - head0 < side.H; h0 += kUnroll * groups) {
-    if (h0 != head0) load(h0);
+    at.page[slot][threadIdx.x] = page;
+    at.slot[slot][threadIdx.x] = pos & ((1 << g.c.page_shift) - 1);
+    at.pos[slot][threadIdx.x] = b >= 0 && g.positions != nullptr ? __ldg(g.positions + i) : pos;
+  };
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int h = h0 + u * groups;
-      if (h - head0 >= side.H) break;
-      const bool stores = valid && h < side.H;
+  for (int i = 0; i < kStages - 1; ++i) copy();
+  look(tile, 0);
+  look(tile + side.ctas, 1);
+  fill_turns(t, g.p, rot);
+  if (which != 2) fill_weights<D, kInter>(t, side.w, side.w_bf16, rot);
+  __syncthreads();
+  fill_angles<D, kInter>(t, 0, rot, d.tokens, [&](int i) { return at.pos[0][i]; });
+  __syncthreads();
+  const long long page_size = 1ll << g.c.page_shift;
+  int stage = 0;
+  for (int buf = 0, here = 0; tile < d.tiles; tile += side.ctas, buf ^= 1) {
+    const unsigned after = tile + side.ctas, token = tile * d.tokens + d.mine;
+    const int ahead = here == 2 ? 0 : here + 1;
+    look(after + side.ctas, ahead == 2 ? 0 : ahead + 1);
+    if (after < d.tiles) fill_angles<D, kInter>(t, buf ^ 1, rot, d.tokens, [&](int i) { return at.pos[ahead][i]; });
+    const int page = at.page[here][d.mine], slot = at.slot[here][d.mine];
+    const bool valid = token < (unsigned)T && page >= 0;
+    const long long to = which == 0 ? token * side.out_n : page * g.c.page_stride + slot * (long long)D;
+    const long long to_h = which == 0 ? D : page_size * D, to_scale = page * g.c.scale_stride + slot;
+    float c[8], s[8];
+    load_angles<D, kInter>(t, buf, rot, d.mine, j, c, s);
+    for (int h = d.head0; h - d.head0 < H; h += d.groups) {
+      copy();
+      ring.wait();
+      uint4 a = ring.get(stage, 0), b = ring.get(stage, 1);
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+      const bool stores = valid && h < H;
       Parts y;
-      unpack(xa[u], y.a);
-      unpack(xb[u], y.b);
-      if (which != 2) forward_vector<D, kInter>(y, g.p, wa, wb, c, s);
-      if (which == 0) {
-        if (stores) {
-          *reinterpret_cast<uint4*>(side.out + to + h * side.out_h + ca) = pack(y.a);
-          *reinterpret_cast<uint4*>(side.out + to + h * side.out_h + cb) = pack(y.b);
+      unpack(a, y.a);
+      unpack(b, y.b);
+      if (which != 2) forward_vector<D, kInter>(y, g.p, t, j, c, s);
+      if (!kFp8 || which == 0) {
+        if (which != 2) {
+          a = pack(y.a);
+          b = pack(y.b);
         }
-      } else if constexpr (!kFp8) {
         if (stores) {
-          __nv_bfloat16* row = static_cast<__nv_bfloat16*>(which == 1 ? g.c.k : g.c.v) + to + h * page_size * D;
-          *reinterpret_cast<uint4*>(row + ca) = which == 2 ? xa[u] : pack(y.a);
-          *reinterpret_cast<uint4*>(row + cb) = which == 2 ? xb[u] : pack(y.b);
+          __nv_bfloat16* row = (which == 0 ? side.out : static_cast<__nv_bfloat16*>(which == 1 ? g.c.k : g.c.v)) + to + h * to_h;
+          *reinterpret_cast<uint4*>(row + ca) = a;
+          *reinterpret_cast<uint4*>(row + cb) = b;
         }
       } else {
         uint2 qa, qb;
         float scale;
         quantize<L::kLanes>(y, qa, qb, scale);
         if (stores) {
-          uint8_t* row = static_cast<uint8_t*>(which == 1 ? g.c.k : g.c.v) + to + h * page_size * D;
+          uint8_t* row = static_cast<uint8_t*>(which == 1 ? g.c.k : g.c.v) + to + h * to_h;
           *reinterpret_cast<uint2*>(row + ca) = qa;
           *reinterpret_cast<uint2*>(row + cb) = qb;
           if (j == 0) (which == 1 ? g.c.k_scale : g.c.v_scale)[to_scale + h * page_size] = scale;
         }
       }
     }
+    __syncthreads();   // everyone has read this tile's tables and written those that come
+    here = ahead;
   }
 }
 
 // ------------------------------------------------------------------------------------ host side
 
-// Lane groups for a token's H heads: as many as leave each group kUnroll heads, so that the angles are read
-// once for those; more where the batch is too small for that to fill the SMs.
-static int pick_shift(int H, int groups, int unroll, long long tokens) {
+// log2 of the lane groups for a token's H heads.  kHeads to 2 kHeads heads for each group, which reads the angles
+// once for them, dealt as evenly as one of the two numbers allows; more groups where the batch is too small for
+// that to fill the SMs.
+static int pick_shift(int H, int groups, long long tokens) {
   int shift = 0;
-  while ((unroll << shift) < H && (2 << shift) <= groups) ++shift;
+  while ((kHeads << shift) < H && (2 << shift) <= groups) ++shift;
+  const auto idle = [H](int x) { return (-H & ((1 << x) - 1)) << (8 - x); };   // of a round of the groups, in 1/256
+  if (shift > 0 && idle(shift - 1) < idle(shift)) --shift;
   while ((1 << shift) < H && (2 << shift) <= groups && tokens * (1 << shift) < (long long)groups * 2 * sm_count()) ++shift;
   return shift;
 }
@@ -612,9 +778,13 @@ static int check_positions(const int32_t* p) {
   return FA_OK;
 }
 
+// What a token of H heads costs, in quarters of a vector: its angles, computed once, as much as four vectors.
+static long long token_cost(int H, int rot, int d) { return 4ll * H + 16 * rot / d; }
+
+// A side with its share of `all` CTAs, at least one: cost of `costs`.
 template <int D>
 static Side make_side(const fa_heads* x, const fa_heads* dz, const fa_heads* out, const void* w, int w_bf16, int H,
-                      long long tokens, int unroll, int most_ctas) {
+                      long long tokens, long long cost, long long costs, int all) {
   Side s = {};
   s.x = static_cast<const __nv_bfloat16*>(x->p);
   s.x_b = x->stride_b, s.x_h = x->stride_h, s.x_n = x->stride_n;
@@ -627,32 +797,36 @@ static Side make_side(const fa_heads* x, const fa_heads* dz, const fa_heads* out
   s.w = w;
   s.w_bf16 = w_bf16;
   s.H = H;
-  s.shift = pick_shift(H, Lanes<D>::kGroups, unroll, tokens);
+  s.shift = pick_shift(H, Lanes<D>::kGroups, tokens);
   const int per = Lanes<D>::kGroups >> s.shift;
-  const long long tiles = (tokens + per - 1) / per;
-  s.ctas = (int)(tiles < most_ctas ? tiles : most_ctas);
+  const long long tiles = (tokens + per - 1) / per, share = std::max(1ll, all * cost / costs);
+  s.ctas = (int)std::min(tiles, share);
   return s;
 }
 
-// CTAs of the backward, two for each of 152 SMs; each side gets a share by its heads (together at most all).
-constexpr int kBwdCtas = 304;
-static int bwd_ctas(int H, int others) {
-  const int n = (int)((long long)kBwdCtas * H / ((long long)H + others));
-  return n < 1 ? 1 : n;
-}
+constexpr int kParts = 152 * kBwdCtas;   // CTAs of the backward at most, and its partial sums
 
-constexpr int kNoLimit = 0x7FFFFFFF;
+template <int D, int kRingParts>
+static int prepare(const void* kern, std::atomic<uint64_t>* done) {
+  constexpr int bytes = (int)sizeof(Shared<D, kRingParts>);
+  static_assert(kCtas * (sizeof(Shared<D, 2>) + sizeof(Places<Lanes<D>::kGroups>) + 1024) <= 228 * 1024 &&
+                    kBwdCtas * (sizeof(Shared<D, 4>) + 1024) <= 228 * 1024,
+                "an SM's CTAs fit its shared memory");
+  return prepare_kernel(kern, bytes, kThreads, 0, "norm and rotation", done);
+}
 
 template <int D>
 static int launch_forward(const fa_rotation* r, const Dense& g, const fa_heads* q, const fa_heads* k, const fa_heads* qo,
                           const fa_heads* ko, int Hq, int Hkv, cudaStream_t s) {
-  const Side sq = make_side<D>(q, nullptr, qo, r->q_weight, r->weight_bf16, Hq, g.tokens, kUnroll, kNoLimit);
-  const Side sk = make_side<D>(k, nullptr, ko, r->k_weight, r->weight_bf16, Hkv, g.tokens, kUnroll, kNoLimit);
-  const int most = sq.shift < sk.shift ? sq.shift : sk.shift;
-  const int smem = table_bytes<D>(Lanes<D>::kGroups >> most);
-  const unsigned grid = (unsigned)sq.ctas + (unsigned)sk.ctas;
+  const int all = kCtas * sm_count();
+  const long long cq = token_cost(Hq, r->rot, D), ck = token_cost(Hkv, r->rot, D);
+  const Side sq = make_side<D>(q, nullptr, qo, r->q_weight, r->weight_bf16, Hq, g.tokens, cq, cq + ck, all);
+  const Side sk = make_side<D>(k, nullptr, ko, r->k_weight, r->weight_bf16, Hkv, g.tokens, ck, cq + ck, all);
   auto kern = r->interleaved ? norm_rotate_kernel<D, true> : norm_rotate_kernel<D, false>;
-  kern<<<grid, kThreads, smem, s>>>(g, sq, sk);
+  static std::atomic<uint64_t> prepared[2];
+  const int rc = prepare<D, 2>(reinterpret_cast<const void*>(kern), &prepared[r->interleaved != 0]);
+  if (rc) return rc;
+  kern<<<sq.ctas + sk.ctas, kThreads, sizeof(Shared<D, 2>), s>>>(g, sq, sk);
   return check_cuda(cudaGetLastError(), "launch fa_norm_rotate");
 }
 
@@ -660,31 +834,44 @@ template <int D>
 static int launch_backward(const fa_rotation* r, const Dense& g, const fa_heads* q, const fa_heads* k, const fa_heads* dzq,
                            const fa_heads* dzk, const fa_heads* dq, const fa_heads* dk, float* dqw, float* dkw, float* part,
                            int Hq, int Hkv, cudaStream_t s) {
-  const Side sq = make_side<D>(q, dzq, dq, r->q_weight, r->weight_bf16, Hq, g.tokens, kUnrollBwd, bwd_ctas(Hq, Hkv));
-  const Side sk = make_side<D>(k, dzk, dk, r->k_weight, r->weight_bf16, Hkv, g.tokens, kUnrollBwd, bwd_ctas(Hkv, Hq));
-  const int most = sq.shift < sk.shift ? sq.shift : sk.shift;
-  const int table = table_bytes<D>(Lanes<D>::kGroups >> most), rows = Lanes<D>::kGroups * D * 4;
-  const int smem = table > rows ? table : rows;
+  // (rounded down, but one CTA at least for each side: together kParts at most)
+  const long long cq = token_cost(Hq, r->rot, D), ck = token_cost(Hkv, r->rot, D);
+  const Side sq = make_side<D>(q, dzq, dq, r->q_weight, r->weight_bf16, Hq, g.tokens, cq, cq + ck, kParts);
+  const Side sk = make_side<D>(k, dzk, dk, r->k_weight, r->weight_bf16, Hkv, g.tokens, ck, cq + ck, kParts);
   auto kern = r->interleaved ? norm_rotate_bwd_kernel<D, true> : norm_rotate_bwd_kernel<D, false>;
-  kern<<<sq.ctas + sk.ctas, kThreads, smem, s>>>(g, sq, sk, part);
-  const int rc = check_cuda(cudaGetLastError(), "launch fa_norm_rotate_bwd");
+  static std::atomic<uint64_t> prepared[2];
+  int rc = prepare<D, 4>(reinterpret_cast<const void*>(kern), &prepared[r->interleaved != 0]);
+  if (rc) return rc;
+  kern<<<sq.ctas + sk.ctas, kThreads, sizeof(Shared<D, 4>), s>>>(g, sq, sk, part);
+  rc = check_cuda(cudaGetLastError(), "launch fa_norm_rotate_bwd");
   if (rc || !part) return rc;
-  weight_grad_kernel<<<2 * D / 32, 1024, 0, s>>>(part, D, sq.ctas, sk.ctas, dqw, dkw);
-  return check_cuda(cudaGetLastError(), "launch fa_norm_rotate_bwd weights");
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2 * D / 32);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = s;
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return check_cuda(cudaLaunchKernelEx(&cfg, weight_grad_kernel, (const float*)part, D, sq.ctas, sk.ctas, dqw, dkw),
+                    "launch fa_norm_rotate_bwd weights");
 }
 
 template <int D>
 static int launch_append(const fa_rotation* r, const Packed& g, const fa_heads* q, const fa_heads* k, const fa_heads* v,
                          const fa_heads* qo, int Hq, int Hkv, bool fp8, cudaStream_t s) {
-  const Side sq = make_side<D>(q, nullptr, qo, r->q_weight, r->weight_bf16, Hq, g.T, kUnroll, kNoLimit);
-  const Side sk = make_side<D>(k, nullptr, k, r->k_weight, r->weight_bf16, Hkv, g.T, kUnroll, kNoLimit);
-  const Side sv = make_side<D>(v, nullptr, v, nullptr, 0, Hkv, g.T, kUnroll, kNoLimit);
-  const int most = sq.shift < sk.shift ? sq.shift : sk.shift;
-  const int smem = table_bytes<D>(Lanes<D>::kGroups >> most);
-  const unsigned grid = (unsigned)sq.ctas + (unsigned)sk.ctas + (unsigned)sv.ctas;
+  const int all = kCtas * sm_count();
+  const long long cq = token_cost(Hq, r->rot, D), ck = token_cost(Hkv, r->rot, D), cv = token_cost(Hkv, 0, D);
+  const Side sq = make_side<D>(q, nullptr, qo, r->q_weight, r->weight_bf16, Hq, g.T, cq, cq + ck + cv, all);
+  const Side sk = make_side<D>(k, nullptr, k, r->k_weight, r->weight_bf16, Hkv, g.T, ck, cq + ck + cv, all);
+  const Side sv = make_side<D>(v, nullptr, v, nullptr, 0, Hkv, g.T, cv, cq + ck + cv, all);
   auto kern = r->interleaved ? (fp8 ? qkv_append_kernel<D, true, true> : qkv_append_kernel<D, true, false>)
                              : (fp8 ? qkv_append_kernel<D, false, true> : qkv_append_kernel<D, false, false>);
-  kern<<<grid, kThreads, smem, s>>>(g, sq, sk, sv);
+  static std::atomic<uint64_t> prepared[4];
+  const int rc = prepare<D, 2>(reinterpret_cast<const void*>(kern), &prepared[2 * (r->interleaved != 0) + fp8]);
+  if (rc) return rc;
+  kern<<<sq.ctas + sk.ctas + sv.ctas, kThreads, sizeof(Shared<D, 2>), s>>>(g, sq, sk, sv);
   return check_cuda(cudaGetLastError(), "launch fa_qkv_append");
 }
 
@@ -704,7 +891,7 @@ extern "C" int fa_norm_rotate(const fa_rotation* rotation, const fa_heads* q, co
       (rc = rotate::check_heads(q_out, "q_out", B, Hq, N, true, d)) ||
       (rc = rotate::check_heads(k_out, "k_out", B, Hkv, N, true, d)) || (rc = rotate::check_positions(positions)))
     return rc;
-  const rotate::Dense g{p, positions, positions_stride, (long long)B * N, N};
+  const rotate::Dense g{p, positions, positions_stride, (unsigned)((long long)B * N), N};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return d == 64 ? rotate::launch_forward<64>(rotation, g, q, k, q_out, k_out, Hq, Hkv, s)
                  : rotate::launch_forward<128>(rotation, g, q, k, q_out, k_out, Hq, Hkv, s);
@@ -717,7 +904,7 @@ extern "C" size_t fa_norm_rotate_bwd_workspace_size(int B, int Hq, int Hkv, int 
     fa::set_error(FA_ERR_UNSUPPORTED, "head dim d=%d not supported (64 or 128)", d);
     return 0;
   }
-  return (size_t)fa::rotate::kBwdCtas * d * sizeof(float);   // a row of d for each CTA
+  return (size_t)fa::rotate::kParts * d * sizeof(float);   // a row of d for each CTA
 }
 
 extern "C" int fa_norm_rotate_bwd(const fa_rotation* rotation, const fa_heads* q, const fa_heads* k, const fa_heads* dzq,
@@ -748,7 +935,7 @@ extern "C" int fa_norm_rotate_bwd(const fa_rotation* rotation, const fa_heads* q
       return set_error(FA_ERR_INVALID_ARG, "workspace too small: %zu bytes, %zu needed", workspace_bytes, need);
     part = static_cast<float*>(workspace);
   }
-  const rotate::Dense g{p, positions, positions_stride, (long long)B * N, N};
+  const rotate::Dense g{p, positions, positions_stride, (unsigned)((long long)B * N), N};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return d == 64 ? rotate::launch_backward<64>(rotation, g, q, k, dzq, dzk, dq, dk, dq_weight, dk_weight, part, Hq, Hkv, s)
                  : rotate::launch_backward<128>(rotation, g, q, k, dzq, dzk, dq, dk, dq_weight, dk_weight, part, Hq, Hkv, s);

@@ -110,10 +110,6 @@ struct ChunkWork {
   }
 };
 
-__device__ __forceinline__ void sts128(uint32_t addr, const uint4& v) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-
 // How the launch's tiles (pair of tiles, kv head) are dealt: the first `whole` to one CTA each, every
 // other one to `splits` CTAs that take a share of its keys.
 struct ChunkGrid {

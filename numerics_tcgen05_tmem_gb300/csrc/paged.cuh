@@ -84,8 +84,10 @@ __device__ __forceinline__ int find_page(const Cache& c, int b, int pos, uint32_
   return page;
 }
 
-// Host side: checks a public cache description and fills `c`; an offsets array of B + 1 entries on the device.
+// Host side: checks a public cache description and fills `c`; weights of a cache's keys and their page stride; an
+// offsets array of B + 1 entries on the device.
 int check_cache(const fa_paged_kv* kv, Cache* c);
+int check_weights(const fa_paged_kv* kv, const float* weights, long long stride);
 int check_indptr(const int32_t* p, const char* name);
 
 }  // namespace paged

@@ -96,6 +96,10 @@ __device__ __forceinline__ void tma_load_page(uint32_t dst, const CUtensorMap* m
       : "memory");
 }
 
+__device__ __forceinline__ void sts128(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
 // Few rows: the most CTAs that fa_rows_kernel is launched with, and its partial results: two slots of
 // few_rows rows (8, 16, 32 or 64) for each CTA: the item that it continues, the item that it leaves
 // unfinished.

@@ -46,6 +46,7 @@ CASES = [  # lens, new, hq, hkv, d, page, window, sinks
     ([40, 9, 0, 700], [3, 0, 0, 1], 16, 1, 128, 256, None, 0), ([3, 600], [5, 7], 6, 3, 64, 16, None, 0),
     ([1500], [300], 8, 2, 128, 128, None, 0), ([257, 1000, 64], [257, 100, 1], 28, 4, 64, 16, None, 0),
     ([900, 2000], [400, 3], 12, 12, 128, 64, None, 0), ([130], [130], 128, 1, 64, 64, None, 0), ([700], [9], 100, 2, 128, 32, None, 0),
+    ([2100, 300], [2100, 70], 4, 1, 128, 64, None, 0), ([1030], [1030], 7, 1, 64, 16, 200, 3), ([5000], [600], 6, 1, 64, 64, None, 0),
     ([3000], [1], 8, 2, 64, 64, 500, 4), ([3000, 40], [200, 40], 4, 4, 64, 16, 300, 131), ([1200], [700], 3, 1, 128, 64, 1, 0),
     ([2000, 900], [1, 900], 14, 2, 128, 256, 129, 1), ([800], [60], 5, 1, 64, 128, 4096, 2), ([2 ** 11], [16], 4, 1, 128, 64, 17, 600),
 ]
@@ -254,8 +255,8 @@ def test_a_wait_that_runs_out_is_reported_and_nothing_else_breaks(monkeypatch, f
     pool, rows = W.make(c, seed=2)
     kv = binding._paged(c.k, c.v, c.table, c.kv_len, c.ks, c.vs)
     qd, ld = q.cuda(), lse.cuda()
-    n = binding.fa_kv_accumulate_workspace_size(sum(new), hq, 2, d, kv.dtype)
-    ws = torch.zeros((n + 512,), device="cuda", dtype=torch.uint8)
+    n = binding.fa_kv_accumulate_workspace_size(sum(new), max(new), hq, 2, d, kv.dtype)
+    ws = torch.zeros((-(-n // 256) * 256 + 512,), device="cuda", dtype=torch.uint8)
     stream = torch.cuda.current_stream().cuda_stream
 
     def call(w):

@@ -35,8 +35,8 @@ def evict(lib, kv=None, w=G, w_stride=32, out=1 << 21, out_stride=2, pages=2, ke
 @pytest.mark.parametrize("call", [accumulate, evict])
 @pytest.mark.parametrize("kw,code,word", [
     (dict(kv=cache(d=96)), UNS, "96"), (dict(kv=cache(page_size=48)), UNS, "page_size"), (dict(kv=cache(k_scale=None)), BAD, "k_scale"),
-    (dict(kv=cache(kv_len=None)), BAD, "kv_len"), (dict(w=None), BAD, "weights"), (dict(w=G + 2), BAD, "weights"),
-    (dict(w_stride=31), BAD, "weight_stride"),
+    (dict(kv=cache(kv_len=None)), BAD, "kv_len"), (dict(w=None), BAD, "weights"), (dict(w=G + 4), BAD, "weights"),
+    (dict(w_stride=31), BAD, "weight_stride"), (dict(w_stride=34), BAD, "weight_stride"),
 ])
 def test_bad_caches_and_weights_are_refused(lib, call, kw, code, word):
     assert call(lib, **kw) == code
@@ -62,12 +62,16 @@ def test_nothing_to_accumulate(lib):
 
 def test_workspace_size(lib):
     size = binding.fa_kv_accumulate_workspace_size
-    # E4M3: three bytes for each entry of q and a factor for each vector
-    assert size(5, 8, 2, 64, binding.FA_KV_E4M3) == 3 * 5 * 8 * 64 + 256
-    assert size(100, 32, 8, 128, binding.FA_KV_E4M3) == 3 * 3200 * 128 + 3200 * 4
-    assert size(100, 32, 8, 128, binding.FA_KV_BF16) == 0
-    for bad in (dict(d=96), dict(Hq=7), dict(Hkv=0), dict(T=-1), dict(T=0)):
-        a = dict(T=5, Hq=8, Hkv=2, d=64, dtype=binding.FA_KV_E4M3)
+    # few rows over E4M3: three bytes for each entry of q and a factor for each vector
+    assert size(5, 1, 8, 2, 64, binding.FA_KV_E4M3) == 3 * 5 * 8 * 64 + 256
+    assert size(100, 16, 32, 8, 128, binding.FA_KV_E4M3) == 3 * 3200 * 128 + 3200 * 4
+    assert size(100, 16, 32, 8, 128, binding.FA_KV_BF16) == 0
+    # chunks of eight blocks of 128 rows or more: the sums of 1216 parts of 256 keys
+    for dtype in (binding.FA_KV_BF16, binding.FA_KV_E4M3):
+        assert size(300, 224, 32, 8, 128, dtype) == 0
+        assert size(300, 225, 32, 8, 128, dtype) == size(9000, 9000, 32, 8, 64, dtype) == 1216 * 256 * 4
+    for bad in (dict(d=96), dict(Hq=7), dict(Hkv=0), dict(T=-1), dict(T=0), dict(max_q=-1)):
+        a = dict(T=5, max_q=1, Hq=8, Hkv=2, d=64, dtype=binding.FA_KV_E4M3)
         a.update(bad)
         assert size(**a) == 0
 
