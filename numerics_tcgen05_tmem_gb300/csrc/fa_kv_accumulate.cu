@@ -53,7 +53,7 @@ struct AccCfg {
   // the pieces side by side, 3 N columns of S that are added afterwards: the tensor core then reads K once.  (64
   // columns leave no room for that: S takes the pieces one after the other.)
   static constexpr bool kWide = kPieced && N <= 32;
-  static constexpr int kThreads = kConvert ? 512 : 384;
+  static constexpr int kSumWarps = 8, kThreads = 32 * (kSumWarps + (kConvert ? 8 : 4));
   // operands
   static constexpr int kRowBytes = D * (kPieced ? 1 : 2);
   static constexpr int kAtomBytes = kRowBytes < 128 ? kRowBytes : 128;   // swizzle atom row
@@ -286,13 +286,39 @@ __device__ __forceinline__ void acc_columns(const uint32_t (&r)[W], const float*
   }
 }
 
+// The pages of a unit's boxes, one for each lane (num_pages where there is nothing to read): one access to the table
+// serves as many of a sequence's units as the lanes hold.
+struct AccPages {
+  int b = -1, from = 0, page = 0;
+  // boxes of a unit, of 1 << shift keys each
+  template <class Cursor>
+  __device__ __forceinline__ int get(const Attn& p, const Cursor& c, int boxes, int shift) {
+    const int lane = threadIdx.x % 32, units = 32 / boxes;
+    if (c.b != b || c.j < from || c.j >= from + units) {
+      b = c.b;
+      from = c.j;
+      const int j = c.j + lane / boxes, key = c.w.at(j) + (lane % boxes << shift);
+      page = p.c.num_pages;
+      // (the walk ends at the sequence's length, which the table holds)
+      if (j < c.w.steps && c.w.any(key, 1 << shift)) {
+        page = __ldg(p.c.table + c.b * p.c.table_stride + (key >> p.c.page_shift));
+        if (page < 0 || page >= p.c.num_pages) {
+          report_bounds(p.c.status, kSitePagedPage, page);
+          page = p.c.num_pages;
+        }
+      }
+    }
+    return __shfl_sync(0xffffffffu, page, (c.j - from) * boxes + lane % boxes);
+  }
+};
+
 template <int D, bool kFp8, int N>
 __global__ void __launch_bounds__(AccCfg<D, kFp8, N>::kThreads, 1)
     fa_accumulate_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ Acc g) {
   using C = AccCfg<D, kFp8, N>;
   using Cursor = AccCursor<C::kChunk>;
-  constexpr int kKWarp = 8, kQWarp = 9, kMmaWarp = 10, kColWarp = 11, kConvertWarp = 12;
+  constexpr int kKWarp = C::kSumWarps, kQWarp = kKWarp + 1, kMmaWarp = kKWarp + 2, kColWarp = kKWarp + 3, kConvertWarp = kKWarp + 4;
   constexpr int W = N < 32 ? N : 32;    // columns taken at a time
   extern __shared__ __align__(1024) uint8_t smem[];
   const Attn& p = g.a;
@@ -304,6 +330,8 @@ __global__ void __launch_bounds__(AccCfg<D, kFp8, N>::kThreads, 1)
   volatile uint32_t* abort_flag = &sh.abort_flag;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int tokens = N / p.group;       // of a block of queries
+  // keys come in boxes of a page, of half a page of 256
+  const int page_size = 1 << p.c.page_shift, box_shift = min(p.c.page_shift, 7), boxes = kAccKeys >> box_shift;
 
   if (threadIdx.x == 0) {
     sh.abort_flag = 0;
@@ -317,11 +345,11 @@ __global__ void __launch_bounds__(AccCfg<D, kFp8, N>::kThreads, 1)
     }
     for (int s = 0; s < kColStages; ++s) {
       mbar_init(&sh.col_full[s], 32);
-      mbar_init(&sh.col_empty[s], 8);   // the warps that sum
+      mbar_init(&sh.col_empty[s], C::kSumWarps);
     }
     for (int s = 0; s < C::kSideStages; ++s) {
       mbar_init(&sh.side_full[s], 32);  // the loading warp's lanes (pages), one of them with the expected bytes
-      mbar_init(&sh.side_empty[s], 8);
+      mbar_init(&sh.side_empty[s], C::kSumWarps);
     }
     for (int t = 0; t < 2; ++t)
       for (int s = 0; s < C::kBufs; ++s) {
@@ -363,45 +391,21 @@ __global__ void __launch_bounds__(AccCfg<D, kFp8, N>::kThreads, 1)
 
   if (warp == kKWarp) {
     // ------------------------------------------------------------ K tiles (or their codes), page by page
-    const int page_size = 1 << p.c.page_shift, box = min(page_size, kAccTile), boxes = kAccKeys / box;
     const uint32_t base = smem_u32(smem);
-    // a unit's entry of the table is loaded while the one before it waits for its slot
-    auto look = [&](const Cursor& c) {
-      const bool any = c.valid(p) && lane < boxes && c.w.any(c.key() + lane * box, box);
-      // (the walk ends at the sequence's length, which the table holds)
-      return any ? __ldg(p.c.table + c.b * p.c.table_stride + ((c.key() + lane * box) >> p.c.page_shift)) : p.c.num_pages;
-    };
     if (lane == 0) tma_prefetch_desc(&tmK);
-    int n = 0, page = look(cur);
-    bool ok = true;
-    while (cur.valid(p)) {
-      Cursor ahead = cur;
-      ahead.next(p, parts);
-      const int page_ahead = look(ahead);
-      const int s = n % C::kKStages, x = n % C::kSideStages;
+    AccPages pages;
+    int n = 0;
+    for (; cur.valid(p); cur.next(p, parts), ++n) {
+      const int s = n % C::kKStages, tiles = cur.tile(1) ? 2 : 1;
+      const int page = pages.get(p, cur, boxes, box_shift);
       uint64_t* full = C::kConvert ? &sh.code_full : &sh.k_full[s];
-      ok = __all_sync(0xffffffffu, mbar_wait(&sh.side_empty[x], ((n / C::kSideStages) & 1) ^ 1, abort_flag, p.c.status) &&
-                                       (C::kConvert ? mbar_wait(&sh.code_empty, (n & 1) ^ 1, abort_flag, p.c.status)
-                                                    : mbar_wait(&sh.k_empty[s], ((n / C::kKStages) & 1) ^ 1, abort_flag, p.c.status)));
-      if (!ok) break;
-      if (page < 0 || page > p.c.num_pages) {
-        report_bounds(p.c.status, kSitePagedPage, page);
-        page = p.c.num_pages;            // out of range: zeros
-      }
-      const int tiles = cur.tile(1) ? 2 : 1;
-      const bool loads = lane < boxes && lane * box < tiles * kAccTile, real = loads && page < p.c.num_pages;
-      const int reals = __popc(__ballot_sync(0xffffffffu, real));
-      uint8_t* side = smem + C::kSideOff + x * C::kSideBytes;
-      if (lane < 16) reinterpret_cast<int*>(side + C::kSideBytes - 64)[lane] = real ? page : -1;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(full, tiles * kAccTile * D * (kFp8 ? 1 : 2));
-        mbar_arrive_expect_tx(&sh.side_full[x], reals * box * 4 * (kFp8 ? 2 : 1));
-      } else {
-        mbar_arrive(&sh.side_full[x]);
-      }
+      if (!__all_sync(0xffffffffu, C::kConvert ? mbar_wait(&sh.code_empty, (n & 1) ^ 1, abort_flag, p.c.status)
+                                               : mbar_wait(&sh.k_empty[s], ((n / C::kKStages) & 1) ^ 1, abort_flag, p.c.status)))
+        break;
+      if (lane == 0) mbar_arrive_expect_tx(full, tiles * kAccTile * D * (kFp8 ? 1 : 2));
       __syncwarp();
-      const int row = lane * box, slot = (cur.key() + row) & (page_size - 1);
-      if (loads) {
+      const int row = lane << box_shift, slot = (cur.key() + row) & (page_size - 1);
+      if (lane < boxes && row < tiles * kAccTile) {
         if constexpr (C::kConvert) {
           tma_load_page(base + C::kCodeOff + row * D, &tmK, full, 0, slot, cur.h, page);
         } else {
@@ -412,15 +416,6 @@ __global__ void __launch_bounds__(AccCfg<D, kFp8, N>::kThreads, 1)
             tma_load_page(dst + a * kAccTile * C::kAtomBytes, &tmK, full, a * C::kAtomElems, slot, cur.h, page);
         }
       }
-      if (real) {
-        const long long at = (long long)cur.h * page_size + slot;
-        bulk_load(side + row * 4, g.weights + page * g.weight_stride + at, box * 4, &sh.side_full[x]);
-        if constexpr (kFp8)
-          bulk_load(side + (kAccKeys + row) * 4, p.c.k_scale + page * p.c.scale_stride + at, box * 4, &sh.side_full[x]);
-      }
-      ++n;
-      cur = ahead;
-      page = page_ahead;
     }
     if (*abort_flag) {
       // let copies still in flight land before the CTA's shared memory goes away
@@ -431,8 +426,6 @@ __global__ void __launch_bounds__(AccCfg<D, kFp8, N>::kThreads, 1)
         for (int i = max(0, n - C::kKStages); i < n; ++i)
           mbar_wait(&sh.k_full[i % C::kKStages], (i / C::kKStages) & 1, &ignore_abort, p.c.status);
       }
-      for (int i = max(0, n - C::kSideStages); i < n; ++i)
-        mbar_wait(&sh.side_full[i % C::kSideStages], (i / C::kSideStages) & 1, &ignore_abort, p.c.status);
     }
   } else if (warp == kQWarp) {
     // ------------------------------------------------------------ blocks of queries
@@ -466,7 +459,7 @@ __global__ void __launch_bounds__(AccCfg<D, kFp8, N>::kThreads, 1)
       }
     }
   } else if (warp == kColWarp) {
-    // ------------------------------------------------------------ their log-sum-exps, four blocks at a time
+    // ------------------------------------------------------------ a unit's weights, scales and pages; its blocks' log-sum-exps
     constexpr int kPer = (N + 31) / 32, kAhead = C::kChunk ? 4 : 1;
     if constexpr (C::kPieced) cudaGridDependencySynchronize();
     int tr[kPer], off[kPer];               // a column's token within its block, its place behind the block's first row
@@ -476,9 +469,32 @@ __global__ void __launch_bounds__(AccCfg<D, kFp8, N>::kThreads, 1)
       tr[e] = r < tokens * p.group ? r / p.group : INT_MAX;
       off[e] = r / p.group * p.Hq + r % p.group;
     }
-    int n = 0;
+    AccPages pages;
+    int n = 0, nu = 0;
     bool ok = true;
     for (; ok && cur.valid(p); cur.next(p, parts)) {
+      {
+        const int x = nu % C::kSideStages, row = lane << box_shift;
+        const int page = pages.get(p, cur, boxes, box_shift);
+        const bool real = lane < boxes && page < p.c.num_pages;
+        const int reals = __popc(__ballot_sync(0xffffffffu, real));
+        ok = __all_sync(0xffffffffu, mbar_wait(&sh.side_empty[x], ((nu / C::kSideStages) & 1) ^ 1, abort_flag, p.c.status));
+        if (!ok) break;
+        uint8_t* side = smem + C::kSideOff + x * C::kSideBytes;
+        if (lane < 16) reinterpret_cast<int*>(side + C::kSideBytes - 64)[lane] = real ? page : -1;
+        if (lane == 0)
+          mbar_arrive_expect_tx(&sh.side_full[x], (reals << box_shift) * 4 * (kFp8 ? 2 : 1));
+        else
+          mbar_arrive(&sh.side_full[x]);
+        __syncwarp();
+        if (real) {
+          const long long at = (long long)cur.h * page_size + ((cur.key() + row) & (page_size - 1));
+          bulk_load(side + row * 4, g.weights + page * g.weight_stride + at, 4 << box_shift, &sh.side_full[x]);
+          if constexpr (kFp8)
+            bulk_load(side + (kAccKeys + row) * 4, p.c.k_scale + page * p.c.scale_stride + at, 4 << box_shift, &sh.side_full[x]);
+        }
+        ++nu;
+      }
       if (!C::kChunk && !cur.fresh) continue;
       int i, last;
       for (cur.blocks(p, parts, tokens, i, last); ok && i < last; i += kAhead) {
@@ -513,6 +529,11 @@ __global__ void __launch_bounds__(AccCfg<D, kFp8, N>::kThreads, 1)
           ++n;
         }
       }
+    }
+    if (*abort_flag) {
+      volatile uint32_t ignore_abort = 0;
+      for (int i = max(0, nu - C::kSideStages); i < nu; ++i)
+        mbar_wait(&sh.side_full[i % C::kSideStages], (i / C::kSideStages) & 1, &ignore_abort, p.c.status);
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ products
@@ -572,118 +593,144 @@ __global__ void __launch_bounds__(AccCfg<D, kFp8, N>::kThreads, 1)
         mbar_wait(&sh.mma_done, 0, &ignore_abort, p.c.status);
       }
     }
-  } else if (warp < 8) {
+  } else if (warp < C::kSumWarps) {
     // ------------------------------------------------------------ exponentials and sums: a thread per key
     const int t = warp / 4, row = t * kAccTile + (warp % 4) * 32 + lane;   // the thread's key within a unit
     const uint32_t tS = tmem + t * C::kBufs * C::kBufCols + ((uint32_t)((warp % 4) * 32) << 16);
-    const int box_shift = min(p.c.page_shift, 7);    // keys of a box of the loads
     int nq = 0, ns = 0, nu = 0;
     long long number = blockIdx.x;                   // chunks: of the part in the launch
     bool ok = true;
+    auto wait = [&](uint64_t* bar, int n, int stages) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, (n / stages) & 1, abort_flag, p.c.status));
+    };
+    auto give = [&](int buf) {                       // a buffer of S has been read
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.s_empty[t][buf]);
+    };
+    auto columns = [&](int n) { return reinterpret_cast<const float*>(smem + C::kColOff + n % kColStages * C::kColBytes); };
     for (; ok && cur.valid(p); cur.next(p, parts), ++nu, number += gridDim.x) {
       const int x = nu % C::kSideStages;
       const uint8_t* side = smem + C::kSideOff + x * C::kSideBytes;
-      ok = __all_sync(0xffffffffu, mbar_wait(&sh.side_full[x], (nu / C::kSideStages) & 1, abort_flag, p.c.status));
-      if (!ok) break;
+      if (!(ok = wait(&sh.side_full[x], nu, C::kSideStages))) break;
       const int page = reinterpret_cast<const int*>(side + C::kSideBytes - 64)[row >> box_shift];
       const float old = reinterpret_cast<const float*>(side)[row];
       const float key_scale = kFp8 ? reinterpret_cast<const float*>(side)[kAccKeys + row] : 0.f;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.side_empty[x]);
       const bool active = cur.tile(t);
-      const int key = cur.key() + row;
+      const int key = cur.key() + row, ahead = key - cur.s.pos0;   // the first token that sees the key, but for 0
       float total = 0.f;
       int i, last;
-      for (cur.blocks(p, parts, tokens, i, last); i < last; ++i) {
-        const int cs = nq % kColStages;
-        if (C::kChunk || cur.fresh)
-          ok = __all_sync(0xffffffffu, mbar_wait(&sh.col_full[cs], (nq / kColStages) & 1, abort_flag, p.c.status));
-        if (!ok) break;
+      cur.blocks(p, parts, tokens, i, last);
+      // chunks: the blocks [i_all, last_all) of which every row sees every key of the warp
+      int i_all = INT_MAX, last_all = 0;
+      if (C::kChunk && active) {
+        const int lo = ahead - lane, hi = lo + 31;   // (of the warp's first key and of its last)
+        i_all = (max(hi, 0) + tokens - 1) / tokens;
+        last_all = cur.s.n / tokens;
+        if (p.window && key - lane + 31 >= p.sinks)
+          last_all = (int)max(min((long long)last_all, ((long long)lo + p.window) / tokens), 0ll);
+        last_all = min(last_all, last);
+      }
+      while (i < last) {
+        if (C::kChunk && i >= i_all && i < last_all) {
+          // 32 columns of S are on their way while as many are summed, from one block to the next
+          uint32_t r[2][32];
+          if (!(ok = wait(&sh.s_full[t][ns % C::kBufs], ns, C::kBufs))) break;
+          tc_fence_after();
+          tmem_ld32(tS + ns % C::kBufs * C::kBufCols, r[0]);
+          for (; i < last_all; ++i, ++nq, ++ns) {
+            const int buf = ns % C::kBufs;
+            const float* col = columns(nq);
+            if (!(ok = wait(&sh.col_full[nq % kColStages], nq, kColStages))) break;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < N / 32; ++c) {
+              tmem_ld_wait();
+              reg_fence(r[c % 2]);
+              if (c + 1 < N / 32) {
+                tmem_ld32(tS + buf * C::kBufCols + (c + 1) * 32, r[(c + 1) % 2]);
+              } else {
+                give(buf);
+                if (i + 1 < last_all) {
+                  if (!(ok = wait(&sh.s_full[t][(ns + 1) % C::kBufs], ns + 1, C::kBufs))) break;
+                  tc_fence_after();
+                  tmem_ld32(tS + (ns + 1) % C::kBufs * C::kBufCols, r[(c + 1) % 2]);
+                }
+              }
+              acc_columns<32, false, kFp8, false>(r[c % 2], col + c * 32, nullptr, p.scale, key_scale, 0, sum);
+            }
+            if (!ok) break;
+            total += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.col_empty[nq % kColStages]);
+          }
+          tmem_ld_wait();
+          if (!ok) break;
+          continue;
+        }
+        if ((C::kChunk || cur.fresh) && !(ok = wait(&sh.col_full[nq % kColStages], nq, kColStages))) break;
         if (active) {
           const int buf = ns % C::kBufs;
-          ok = __all_sync(0xffffffffu, mbar_wait(&sh.s_full[t][buf], (ns / C::kBufs) & 1, abort_flag, p.c.status));
-          if (!ok) break;
+          if (!(ok = wait(&sh.s_full[t][buf], ns, C::kBufs))) break;
           tc_fence_after();
           // the rows that see the key: its own token's on, up to the last one whose window holds it
           const int t0 = i * tokens, here = min(cur.s.n - t0, tokens);
-          const int lo = min(max(key - cur.s.pos0 - t0, 0), here) * p.group;
+          const int lo = min(max(ahead - t0, 0), here) * p.group;
           int end = here;
-          if (p.window && key >= p.sinks) end = (int)min((long long)here, max((long long)key + p.window - cur.s.pos0 - t0, 0ll));
+          if (p.window && key >= p.sinks) end = (int)min((long long)here, max((long long)ahead + p.window - t0, 0ll));
           const int hi = end * p.group;
-          const float* col = reinterpret_cast<const float*>(smem + C::kColOff + cs * C::kColBytes);
+          const float* col = columns(nq);
           const uint32_t at = tS + buf * C::kBufCols;
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
-          auto give = [&] {   // the buffer has been read
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.s_empty[t][buf]);
-          };
-          if (N >= 64 && __all_sync(0xffffffffu, lo == 0 && hi >= tokens * p.group)) {
-            // every row sees every key of the warp: 32 columns are on their way while as many are summed
-            uint32_t ra[32], rb[32];
-            tmem_ld32(at, ra);
 #pragma unroll
-            for (int c0 = 0; c0 < N; c0 += 64) {
-              tmem_ld_wait();
-              reg_fence(ra);
-              tmem_ld32(at + c0 + 32, rb);
-              acc_columns<32, C::kPieced, kFp8, false>(ra, col + c0, col + N + c0, p.scale, key_scale, 0, sum);
-              tmem_ld_wait();
-              reg_fence(rb);
-              if (c0 + 64 < N)
-                tmem_ld32(at + c0 + 64, ra);
+          for (int c0 = 0; c0 < N; c0 += W) {
+            if (__all_sync(0xffffffffu, hi <= c0 || lo >= c0 + W)) continue;
+            uint32_t r[W];
+            auto get = [&](uint32_t (&to)[W], int c) {
+              if constexpr (W == 16)
+                tmem_ld16(at + c, to);
               else
-                give();
-              acc_columns<32, C::kPieced, kFp8, false>(rb, col + c0 + 32, col + N + c0 + 32, p.scale, key_scale, 0, sum);
-            }
-          } else {
+                tmem_ld32(at + c, to);
+            };
+            get(r, c0);
+            if constexpr (C::kWide) {
+              uint32_t r1[W], r2[W];
+              get(r1, N + c0);
+              get(r2, 2 * N + c0);
+              tmem_ld_wait();
+              reg_fence(r);
+              reg_fence(r1);
+              reg_fence(r2);
 #pragma unroll
-            for (int c0 = 0; c0 < N; c0 += W) {
-              if (__all_sync(0xffffffffu, hi <= c0 || lo >= c0 + W)) continue;
-              uint32_t r[W];
-              auto get = [&](uint32_t (&to)[W], int c) {
-                if constexpr (W == 16)
-                  tmem_ld16(at + c, to);
-                else
-                  tmem_ld32(at + c, to);
-              };
-              get(r, c0);
-              if constexpr (C::kWide) {
-                uint32_t r1[W], r2[W];
-                get(r1, N + c0);
-                get(r2, 2 * N + c0);
-                tmem_ld_wait();
-                reg_fence(r);
-                reg_fence(r1);
-                reg_fence(r2);
-#pragma unroll
-                for (int e = 0; e < W; ++e)   // the smaller ones first
-                  r[e] = __float_as_uint(__uint_as_float(r[e]) + (__uint_as_float(r1[e]) + __uint_as_float(r2[e])));
-              } else {
-                tmem_ld_wait();
-                reg_fence(r);
-              }
-              acc_columns<W, C::kPieced, kFp8, true>(r, col + c0, col + N + c0, p.scale, key_scale,
-                                                     low_bits(hi - c0) & ~low_bits(lo - c0), sum);
+              for (int e = 0; e < W; ++e)   // the smaller ones first
+                r[e] = __float_as_uint(__uint_as_float(r[e]) + (__uint_as_float(r1[e]) + __uint_as_float(r2[e])));
+            } else {
+              tmem_ld_wait();
+              reg_fence(r);
             }
-            give();
+            acc_columns<W, C::kPieced, kFp8, true>(r, col + c0, col + N + c0, p.scale, key_scale,
+                                                   low_bits(hi - c0) & ~low_bits(lo - c0), sum);
           }
+          give(buf);
           ++ns;
           total += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         } else {
           __syncwarp();
         }
         if (C::kChunk || cur.last()) {
-          if (lane == 0) mbar_arrive(&sh.col_empty[cs]);
+          if (lane == 0) mbar_arrive(&sh.col_empty[nq % kColStages]);
           ++nq;
         }
+        ++i;
       }
       if (ok && cur.w.seen(key)) {
         if (parts > 1)
           g.part[number * kAccKeys + row] = total;
         else if (page >= 0)
           g.weights[page * g.weight_stride + ((long long)cur.h << p.c.page_shift) + (key & ((1 << p.c.page_shift) - 1))] =
-              (key >= cur.s.pos0 ? 0.f : old) + total;
+              (ahead >= 0 ? 0.f : old) + total;
       }
     }
   }
@@ -703,21 +750,17 @@ __global__ void __launch_bounds__(AccCfg<D, kFp8, N>::kThreads, 1)
       for (int n = 0; ok && cur.valid(p); cur.next(p, parts), ++n) {
         const int s = n % C::kKStages, tiles = cur.tile(1) ? 2 : 1;
         if (!(ok = mbar_wait(&sh.code_full, n & 1, abort_flag, p.c.status))) break;
-        uint4 codes[2][kRows];
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
+#pragma unroll 1
+        for (int t = 0; t < tiles; ++t) {
+          uint4 codes[kRows];
 #pragma unroll
           for (int i = 0; i < kRows; ++i)
-            if (t < tiles)
-              codes[t][i] = *reinterpret_cast<const uint4*>(smem + C::kCodeOff + (t * kAccTile + r0 + i * kRowStep) * D + x * 16);
-        mbar_arrive(&sh.code_empty);
-        if (!(ok = mbar_wait(&sh.k_empty[s], ((n / C::kKStages) & 1) ^ 1, abort_flag, p.c.status))) break;
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
+            codes[i] = *reinterpret_cast<const uint4*>(smem + C::kCodeOff + (t * kAccTile + r0 + i * kRowStep) * D + x * 16);
+          if (t + 1 == tiles) mbar_arrive(&sh.code_empty);
+          if (t == 0 && !(ok = mbar_wait(&sh.k_empty[s], ((n / C::kKStages) & 1) ^ 1, abort_flag, p.c.status))) break;
 #pragma unroll
           for (int i = 0; i < kRows; ++i) {
-            if (t >= tiles) continue;
-            const uint4 u = codes[t][i];
+            const uint4 u = codes[i];
             const uint32_t w[4] = {flip ? u.z : u.x, flip ? u.w : u.y, flip ? u.x : u.z, flip ? u.y : u.w};
             uint32_t y[8];
 #pragma unroll
@@ -729,6 +772,8 @@ __global__ void __launch_bounds__(AccCfg<D, kFp8, N>::kThreads, 1)
             sts128(tile + c0, make_uint4(y[0], y[1], y[2], y[3]));
             sts128(tile + c1, make_uint4(y[4], y[5], y[6], y[7]));
           }
+        }
+        if (!ok) break;
         fence_proxy_async_smem();
         mbar_arrive(&sh.k_full[s]);
       }
