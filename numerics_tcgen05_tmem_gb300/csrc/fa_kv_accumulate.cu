@@ -54,6 +54,9 @@ struct AccCfg {
   // columns leave no room for that: S takes the pieces one after the other.)
   static constexpr bool kWide = kPieced && N <= 32;
   static constexpr int kSumWarps = 8, kThreads = 32 * (kSumWarps + (kConvert ? 8 : 4));
+  // CTAs on an SM: two where each holds three units' keys or more.  (A unit's hand-offs take longer than its 16 or 32 KB:
+  // decoding over 284k E4M3 keys, d = 128, 61 us with one.)
+  static constexpr int kCtas = N == 16 && D * (kFp8 ? 1 : 2) <= 128 ? 2 : 1;
   // operands
   static constexpr int kRowBytes = D * (kPieced ? 1 : 2);
   static constexpr int kAtomBytes = kRowBytes < 128 ? kRowBytes : 128;   // swizzle atom row
@@ -63,22 +66,22 @@ struct AccCfg {
   static constexpr int kQStages = kChunk ? (kConvert ? 3 : 4) : 2;
   static constexpr int kCodeBytes = kConvert ? kAccKeys * D : 0;         // a unit's codes
   static constexpr int kColBytes = (kPieced ? 2 : 1) * N * 4;            // a block's columns: -lse, and pieces: the factor
-  static constexpr int kSideStages = kChunk ? 2 : 8;
+  static constexpr int kSideStages = kChunk ? 2 : 8 / kCtas;
   static constexpr int kSideBytes = kAccKeys * 4 * (kFp8 ? 2 : 1) + 64;  // a unit's weights, scales and pages
   static constexpr int kQOff = 0;
   static constexpr int kCodeOff = kQOff + kQStages * kQBytes, kKOff = kCodeOff + kCodeBytes;
   static constexpr int kRest = kColStages * kColBytes + kSideStages * kSideBytes;
-  static constexpr int kRoom = 226 * 1024 - kKOff - kRest;
+  static constexpr int kRoom = (kCtas == 2 ? 112 : 226) * 1024 - kKOff - kRest;
   static constexpr int kKStages = kRoom / kPairBytes < 6 ? kRoom / kPairBytes : 6;
   static constexpr int kColOff = kKOff + kKStages * kPairBytes, kSideOff = kColOff + kColStages * kColBytes;
   static constexpr int kSharedOff = kColOff + kRest;
   // S: buffers of a tile, each kBufCols columns of tensor memory
   static constexpr int kSCols = kWide ? kPieces * N : N, kBufCols = kWide ? 4 * N : N;
-  static constexpr int kBufs = 2 * 4 * kBufCols <= 512 ? 4 : 2;
+  static constexpr int kBufs = 2 * 4 * kBufCols * kCtas <= 512 ? 4 : 2;
   static constexpr int kTmemCols = 2 * kBufs * kBufCols;
   static constexpr uint32_t kIdesc = kPieced ? idesc_e4m3(128, kSCols, false, false) | (1u << 10)   // B: E5M2
                                              : idesc_bf16(128, N, false, false);
-  static_assert(kKStages >= 1 && kTmemCols <= 512 && kTmemCols >= 32, "shared or tensor memory");
+  static_assert(kKStages >= 1 && kTmemCols * kCtas <= 512 && kTmemCols >= 32, "shared or tensor memory");
 };
 
 constexpr int kMaxKStages = 6, kMaxQStages = 4, kMaxBufs = 4, kMaxSideStages = 8, kMaxWarps = 16;
@@ -102,7 +105,7 @@ constexpr int acc_smem() {
 }
 template <int D, bool kFp8>
 constexpr bool acc_fits() {
-  return acc_smem<D, kFp8, 16>() <= 227 * 1024 && acc_smem<D, kFp8, 32>() <= 227 * 1024 && acc_smem<D, kFp8, 64>() <= 227 * 1024 &&
+  return AccCfg<D, kFp8, 16>::kCtas * (acc_smem<D, kFp8, 16>() + 1024) <= 228 * 1024 && acc_smem<D, kFp8, 32>() <= 227 * 1024 && acc_smem<D, kFp8, 64>() <= 227 * 1024 &&
          acc_smem<D, kFp8, 128>() <= 227 * 1024;
 }
 static_assert(acc_fits<64, false>() && acc_fits<64, true>() && acc_fits<128, false>() && acc_fits<128, true>(),
@@ -313,7 +316,7 @@ struct AccPages {
 };
 
 template <int D, bool kFp8, int N>
-__global__ void __launch_bounds__(AccCfg<D, kFp8, N>::kThreads, 1)
+__global__ void __launch_bounds__(AccCfg<D, kFp8, N>::kThreads, AccCfg<D, kFp8, N>::kCtas)
     fa_accumulate_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ Acc g) {
   using C = AccCfg<D, kFp8, N>;
@@ -893,8 +896,9 @@ static int launch_acc(const CUtensorMap& tq, const CUtensorMap& tk, const Acc& g
   static std::atomic<uint64_t> prepared{0};
   int rc = prepare_kernel(reinterpret_cast<const void*>(kern), smem, C::kThreads, 0, "accumulate kernel", &prepared);
   if (rc) return rc;
-  if (C::kPieced) return launch_early("launch fa_accumulate_kernel", kern, sm_count(), C::kThreads, smem, s, tq, tk, g);
-  kern<<<sm_count(), C::kThreads, smem, s>>>(tq, tk, g);
+  const int grid = C::kCtas * sm_count();
+  if (C::kPieced) return launch_early("launch fa_accumulate_kernel", kern, grid, C::kThreads, smem, s, tq, tk, g);
+  kern<<<grid, C::kThreads, smem, s>>>(tq, tk, g);
   if ((rc = check_cuda(cudaGetLastError(), "launch fa_accumulate_kernel"))) return rc;
   if (!C::kChunk || g.max_parts == 1) return FA_OK;
   // (units are cut in two at least where there are half as many as parts at most)
