@@ -19,6 +19,7 @@ namespace paged {
 
 constexpr int kSelectThreads = 512;
 constexpr int kDigit = 11, kBins = 1 << kDigit;
+constexpr int kCached = 16384;   // weights that stay in shared memory between the passes
 
 struct Evict {
   Cache c;
@@ -50,10 +51,12 @@ __device__ __forceinline__ int evict_length(const Cache& c, int b) {
 }
 
 __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __grid_constant__ Evict g) {
-  constexpr int kWarps = kSelectThreads / 32;
+  constexpr int kWarps = kSelectThreads / 32, kStep = 4 * kSelectThreads;   // a thread has four keys at a time
+  extern __shared__ __align__(16) uint32_t cached[];
   __shared__ uint32_t bins[kBins];
-  __shared__ int warp_sum[2][kWarps];
+  __shared__ int warp_sum[kWarps];
   __shared__ int found_bin, found_above;
+  cudaTriggerProgrammaticLaunchCompletion();   // the moving kernel may get ready; it waits for this one's end
   const int b = blockIdx.x / g.c.Hkv, h = blockIdx.x - b * g.c.Hkv;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int n = evict_length(g.c, b), kept = min(n, g.keep);
@@ -65,14 +68,19 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
     return;
   }
   const int page_mask = (1 << g.c.page_shift) - 1;
-  auto order_at = [&](int key) {
-    const int page = __ldg(g.c.table + b * g.c.table_stride + (key >> g.c.page_shift));
+  const int32_t* table = g.c.table + b * g.c.table_stride;
+  // the order of the four weights at `key`, which lie in one page
+  auto read = [&](int key) {
+    const int page = __ldg(table + (key >> g.c.page_shift));
     if (page < 0 || page >= g.c.num_pages) {
       report_bounds(g.c.status, kSitePagedEvict, page);
-      return 0u;
+      return make_uint4(0, 0, 0, 0);
     }
-    return weight_order(g.weights[page * g.weight_stride + ((long long)h << g.c.page_shift) + (key & page_mask)]);
+    const float4 w = *reinterpret_cast<const float4*>(g.weights + page * g.weight_stride + ((long long)h << g.c.page_shift) +
+                                                      (key & page_mask));
+    return make_uint4(weight_order(w.x), weight_order(w.y), weight_order(w.z), weight_order(w.w));
   };
+  auto again = [&](int key) { return key < kCached ? *reinterpret_cast<const uint4*>(cached + key) : read(key); };
   // the candidates [lo, hi), of which `want` stay: those above `limit`, and the first `ties` that equal it
   const int lo = g.sinks, hi = n - g.recent, want = g.keep - g.sinks - g.recent;
   uint32_t limit = 0xFFFFFFFFu;
@@ -86,9 +94,14 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
       shift -= digit;
       for (int i = threadIdx.x; i < kBins; i += kSelectThreads) bins[i] = 0;
       __syncthreads();
-      for (int key = lo + (int)threadIdx.x; key < hi; key += kSelectThreads) {
-        const uint32_t x = order_at(key);
-        if (pass == 0 || (x >> above) == prefix) atomicAdd(&bins[x >> shift & ((1 << digit) - 1)], 1u);
+      for (int key = 4 * (int)threadIdx.x; key < hi; key += kStep) {
+        const uint4 u = pass == 0 ? read(key) : again(key);
+        if (pass == 0 && key < kCached) *reinterpret_cast<uint4*>(cached + key) = u;   // read back by this thread
+        const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (key + e >= lo && key + e < hi && (pass == 0 || (x[e] >> above) == prefix))
+            atomicAdd(&bins[x[e] >> shift & ((1 << digit) - 1)], 1u);
       }
       __syncthreads();
       // from the largest bin down: the one in which the count reaches `left`.  A thread has kBins / threads bins.
@@ -103,10 +116,10 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
         const int x = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += x;
       }
-      if (lane == 31) warp_sum[0][warp] = incl;
+      if (lane == 31) warp_sum[warp] = incl;
       __syncthreads();
       int before = incl - mine;
-      for (int w = 0; w < warp; ++w) before += warp_sum[0][w];
+      for (int w = 0; w < warp; ++w) before += warp_sum[w];
       if (before < left && before + mine >= left) {
         int i = 0;
         while (before + (int)bins[top - i] < left) before += (int)bins[top - i++];
@@ -120,38 +133,48 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
     limit = prefix;
     ties = left;
   }
-  // in order: what stays, 512 positions at a time
-  int placed = 0, tied = 0;    // before this step
-  for (int base = 0; base < n; base += kSelectThreads) {
-    const int key = base + (int)threadIdx.x;
-    bool stays = key < n && (key < lo || key >= hi), equal = false;
-    if (key < n && !stays && want > 0) {
-      const uint32_t x = order_at(key);
-      stays = x > limit;
-      equal = x == limit;
+  // in order: what stays.  A key's place is the number of those before it that stay for sure, and of those that
+  // equal the limit, `ties` at most.
+  int sure_before = 0, equal_before = 0;    // before this step
+  for (int base = 0; base < n; base += kStep) {
+    const int key = base + 4 * (int)threadIdx.x;
+    uint32_t x[4] = {0, 0, 0, 0};
+    if (want > 0 && key < hi) {
+      const uint4 u = again(key);
+      x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
     }
-    const uint32_t equals = __ballot_sync(0xffffffffu, equal), sure = __ballot_sync(0xffffffffu, stays);
-    if (lane == 0) {
-      warp_sum[0][warp] = __popc(equals);
-      warp_sum[1][warp] = __popc(sure);
+    bool sure[4], equal[4];
+    int counts = 0;                          // equal ones in the upper half
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const bool inside = key + e >= lo && key + e < hi;
+      sure[e] = key + e < n && (!inside || (want > 0 && x[e] > limit));
+      equal[e] = inside && want > 0 && x[e] == limit;
+      counts += (sure[e] ? 1 : 0) + (equal[e] ? 1 << 16 : 0);
     }
+    int incl = counts;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
     __syncthreads();
-    int eq_before = tied, at = placed;
+    int excl = incl - counts, all = 0;
+#pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const int e = warp_sum[0][w], s = warp_sum[1][w];
-      if (w < warp) {
-        at += s + max(min(e, ties - eq_before), 0);
-        eq_before += e;
-      }
-      placed += s + max(min(e, ties - tied), 0);
-      tied += e;
+      if (w < warp) excl += warp_sum[w];
+      all += warp_sum[w];
     }
-    const uint32_t lower = low_bits(lane);
-    const int my_eq = eq_before + __popc(equals & lower);
-    if (equal && my_eq < ties) stays = true;
-    // of this warp's lower lanes: the sure ones, and the equal ones that are still wanted
-    at += __popc(sure & lower) + max(min(my_eq, ties) - min(eq_before, ties), 0);
-    if (stays) out[at] = key;
+    int at_sure = sure_before + (excl & 0xFFFF), at_equal = equal_before + (excl >> 16);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (sure[e] || (equal[e] && at_equal < ties)) out[at_sure + min(at_equal, ties)] = key + e;
+      at_sure += sure[e] ? 1 : 0;
+      at_equal += equal[e] ? 1 : 0;
+    }
+    sure_before += all & 0xFFFF;
+    equal_before += all >> 16;
     __syncthreads();
   }
 }
@@ -175,54 +198,56 @@ __device__ __forceinline__ Spot spot_of(const Cache& c, const int32_t* table, lo
   return s;
 }
 
-// Into other pages.  A CTA has kMoveVecs kept keys of one (sequence, kv head), K and V; kRow / 16 lanes a vector.
-constexpr int kMoveThreads = 256, kMoveVecs = 64;
+// Into other pages.  A warp has 32 kept keys of one (sequence, kv head): a lane looks one up and moves its scales and
+// weight, then kRow / 16 lanes move a vector, eight loads of each lane in flight.
+constexpr int kMoveThreads = 256, kMoveVecs = 32;
 
 template <int kRow>    // bytes of a vector
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ Evict g, int chunks) {
-  constexpr int kLanes = kRow / 16, kGroups = kMoveThreads / kLanes, kUnroll = 4;
-  __shared__ Spot from[kMoveVecs], to[kMoveVecs];
-  const int item = blockIdx.x / chunks, first = (blockIdx.x - item * chunks) * kMoveVecs;
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ Evict g, int chunks, long long warps) {
+  constexpr int kLanes = kRow / 16, kGroups = 32 / kLanes, kSteps = kMoveVecs / kGroups, kUnroll = 8;
+  static_assert(2 * kSteps % kUnroll == 0, "K and V in whole rounds");
+  cudaGridDependencySynchronize();
+  const int lane = threadIdx.x % 32;
+  const long long w = (long long)blockIdx.x * (kMoveThreads / 32) + threadIdx.x / 32;
+  if (w >= warps) return;
+  const int item = (int)(w / chunks), first = (int)(w - (long long)item * chunks) * kMoveVecs;
   const int b = item / g.c.Hkv, h = item - b * g.c.Hkv;
-  const int here = min(__ldg(g.kept_len + b) - first, kMoveVecs);
+  const int here = min(g.kept_len[b] - first, kMoveVecs);
   if (here <= 0) return;
   const long long page_size = 1ll << g.c.page_shift;
-  if ((int)threadIdx.x < here) {
-    const int key = g.kept[(long long)item * g.keep + first + threadIdx.x];
-    const Spot f = spot_of(g.c, g.c.table, g.c.table_stride, g.c.max_pages, b, key);
-    Spot t = spot_of(g.c, g.table_out, g.table_out_stride, g.max_pages_out, b, first + threadIdx.x);
-    if (f.page < 0) t.page = -1;
-    from[threadIdx.x] = f;
-    to[threadIdx.x] = t;
-    if (t.page >= 0) {
+  const int elem = g.c.k_scale != nullptr ? 1 : 2;
+  long long from = -1, to = -1;       // the lane's vector: bytes from the pool's start
+  if (lane < here) {
+    const Spot f = spot_of(g.c, g.c.table, g.c.table_stride, g.c.max_pages, b, g.kept[(long long)item * g.keep + first + lane]);
+    const Spot t = spot_of(g.c, g.table_out, g.table_out_stride, g.max_pages_out, b, first + lane);
+    if (f.page >= 0 && t.page >= 0) {
       const long long f_at = h * page_size + f.slot, t_at = h * page_size + t.slot;
+      from = f.page * g.c.page_stride * elem + f_at * kRow;
+      to = t.page * g.c.page_stride * elem + t_at * kRow;
       g.weights[t.page * g.weight_stride + t_at] = g.weights[f.page * g.weight_stride + f_at];
       if (g.c.k_scale != nullptr) {
-        g.c.k_scale[t.page * g.c.scale_stride + t_at] = g.c.k_scale[f.page * g.c.scale_stride + f_at];
-        g.c.v_scale[t.page * g.c.scale_stride + t_at] = g.c.v_scale[f.page * g.c.scale_stride + f_at];
+        const long long f_s = f.page * g.c.scale_stride + f_at, t_s = t.page * g.c.scale_stride + t_at;
+        const float ks = g.c.k_scale[f_s], vs = g.c.v_scale[f_s];
+        g.c.k_scale[t_s] = ks;
+        g.c.v_scale[t_s] = vs;
       }
     }
   }
-  __syncthreads();
-  const int elem = g.c.k_scale != nullptr ? 1 : 2;
-  const int col = threadIdx.x % kLanes * 16;
-  const long long page_bytes = g.c.page_stride * elem;
-  for (int i0 = threadIdx.x / kLanes; i0 < 2 * here; i0 += kUnroll * kGroups) {
+  const int col = lane % kLanes * 16;
+#pragma unroll
+  for (int s0 = 0; s0 < 2 * kSteps; s0 += kUnroll) {
     uint4 x[kUnroll];
+    long long dst[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int i = i0 + u * kGroups, v = i >> 1;
-      if (i < 2 * here && to[v].page >= 0)
-        x[u] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>((i & 1) ? g.c.v : g.c.k) + from[v].page * page_bytes +
-                                               (h * page_size + from[v].slot) * kRow + col);
+      const int s = s0 + u, v = s / 2 * kGroups + lane / kLanes;      // K and V of the same vectors in turn
+      const long long src = __shfl_sync(0xffffffffu, from, v);
+      dst[u] = __shfl_sync(0xffffffffu, to, v);
+      if (dst[u] >= 0) x[u] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>((s & 1) ? g.c.v : g.c.k) + src + col);
     }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int i = i0 + u * kGroups, v = i >> 1;
-      if (i < 2 * here && to[v].page >= 0)
-        *reinterpret_cast<uint4*>(static_cast<uint8_t*>((i & 1) ? g.c.v : g.c.k) + to[v].page * page_bytes +
-                                  (h * page_size + to[v].slot) * kRow + col) = x[u];
-    }
+    for (int u = 0; u < kUnroll; ++u)
+      if (dst[u] >= 0) *reinterpret_cast<uint4*>(static_cast<uint8_t*>(((s0 + u) & 1) ? g.c.v : g.c.k) + dst[u] + col) = x[u];
   }
 }
 
@@ -235,7 +260,8 @@ __global__ void __launch_bounds__(kMoveThreads) evict_shift_kernel(const __grid_
   const int slices = row_bytes / kSlice;
   const int slice = blockIdx.x % slices, is_v = blockIdx.x / slices % 2, item = blockIdx.x / slices / 2;
   const int b = item / g.c.Hkv, h = item - b * g.c.Hkv;
-  const int kept = __ldg(g.kept_len + b);
+  cudaGridDependencySynchronize();
+  const int kept = g.kept_len[b];
   const int32_t* keys = g.kept + (long long)item * g.keep;
   const int group = threadIdx.x / kLanes, lane = threadIdx.x % kLanes, col = slice * kSlice + lane * 16;
   const long long page_size = 1ll << g.c.page_shift;
@@ -323,14 +349,25 @@ extern "C" int fa_kv_evict(const fa_paged_kv* kv, float* weights, int64_t weight
   g.kept_len = kept_len;
   g.kept = kept;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  paged::evict_select_kernel<<<(unsigned)items, paged::kSelectThreads, 0, s>>>(g);
+  constexpr int cache = paged::kCached * 4;
+  static std::atomic<uint64_t> prepared{0};
+  if ((rc = prepare_kernel(reinterpret_cast<const void*>(paged::evict_select_kernel), cache, paged::kSelectThreads, 0,
+                           "evict_select_kernel", &prepared)))
+    return rc;
+  paged::evict_select_kernel<<<(unsigned)items, paged::kSelectThreads, cache, s>>>(g);
   if ((rc = check_cuda(cudaGetLastError(), "launch evict_select_kernel"))) return rc;
   const int row = kv->d * (kv->dtype == FA_KV_E4M3 ? 1 : 2);
-  if (in_place) {
-    paged::evict_shift_kernel<<<(unsigned)(items * 2 * (row / paged::kSlice)), paged::kMoveThreads, 0, s>>>(g, row);
-    return check_cuda(cudaGetLastError(), "launch evict_shift_kernel");
-  }
+  const long long warps = items * chunks, per = paged::kMoveThreads / 32;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(in_place ? items * 2 * (row / paged::kSlice) : (warps + per - 1) / per));
+  cfg.blockDim = dim3(paged::kMoveThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  if (in_place) return check_cuda(cudaLaunchKernelEx(&cfg, paged::evict_shift_kernel, g, row), "launch evict_shift_kernel");
   auto kern = row == 64 ? paged::evict_move_kernel<64> : (row == 128 ? paged::evict_move_kernel<128> : paged::evict_move_kernel<256>);
-  kern<<<(unsigned)(items * chunks), paged::kMoveThreads, 0, s>>>(g, (int)chunks);
-  return check_cuda(cudaGetLastError(), "launch evict_move_kernel");
+  return check_cuda(cudaLaunchKernelEx(&cfg, kern, g, (int)chunks, warps), "launch evict_move_kernel");
 }
