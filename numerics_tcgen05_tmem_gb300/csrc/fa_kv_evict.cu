@@ -8,8 +8,8 @@
 //           kept positions.
 //   move    the kept vectors, their scales and weights: bandwidth work, 16 bytes a thread.
 // In place a vector only ever moves to a lower position, to where nothing is that is still to be read as long
-// as the vectors are taken in order: a CTA takes all of one head's K or V, 64 bytes wide, step by step, and
-// waits between a step's loads and its stores.
+// as the vectors are taken in order: a CTA takes all of one head's K or V, 64 (or 32) bytes wide, step by step,
+// and waits between a step's loads and its stores.
 #include <algorithm>
 
 #include "paged_attn.cuh"
@@ -17,9 +17,7 @@
 namespace fa {
 namespace paged {
 
-constexpr int kSelectThreads = 512;
 constexpr int kDigit = 11, kBins = 1 << kDigit;
-constexpr int kCached = 16384;   // weights that stay in shared memory between the passes
 
 struct Evict {
   Cache c;
@@ -50,7 +48,12 @@ __device__ __forceinline__ int evict_length(const Cache& c, int b) {
   return n;
 }
 
-__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __grid_constant__ Evict g) {
+// kCached weights stay in shared memory between the passes.  512 threads and 8192 weights, three CTAs on an SM beside
+// the moving kernel's first ones (with 16384: the selection 2 us faster, the call on 64 sequences of 4.4k keys 117 us
+// instead of 105); 1024 and 40960 for long sequences where there are fewer CTAs than two for each SM (one of 40k
+// keys: 49 us with the smaller form).
+template <int kSelectThreads, int kCached>
+__global__ void __launch_bounds__(kSelectThreads, 1536 / kSelectThreads) evict_select_kernel(const __grid_constant__ Evict g) {
   constexpr int kWarps = kSelectThreads / 32, kStep = 4 * kSelectThreads;   // a thread has four keys at a time
   extern __shared__ __align__(16) uint32_t cached[];
   __shared__ uint32_t bins[kBins];
@@ -70,16 +73,19 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
   const int page_mask = (1 << g.c.page_shift) - 1;
   const int32_t* table = g.c.table + b * g.c.table_stride;
   // the order of the four weights at `key`, which lie in one page
-  auto read = [&](int key) {
-    const int page = __ldg(table + (key >> g.c.page_shift));
+  auto page_at = [&](int key) { return key < n ? __ldg(table + (key >> g.c.page_shift)) : -1; };
+  auto read_page = [&](int key, int page) {
     if (page < 0 || page >= g.c.num_pages) {
-      report_bounds(g.c.status, kSitePagedEvict, page);
-      return make_uint4(0, 0, 0, 0);
+      if (key < n) report_bounds(g.c.status, kSitePagedEvict, page);
+      return make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    const float4 w = *reinterpret_cast<const float4*>(g.weights + page * g.weight_stride + ((long long)h << g.c.page_shift) +
-                                                      (key & page_mask));
+    return *reinterpret_cast<const float4*>(g.weights + page * g.weight_stride + ((long long)h << g.c.page_shift) +
+                                            (key & page_mask));
+  };
+  auto ordered = [](const float4& w) {
     return make_uint4(weight_order(w.x), weight_order(w.y), weight_order(w.z), weight_order(w.w));
   };
+  auto read = [&](int key) { return ordered(read_page(key, page_at(key))); };
   auto again = [&](int key) { return key < kCached ? *reinterpret_cast<const uint4*>(cached + key) : read(key); };
   // the candidates [lo, hi), of which `want` stay: those above `limit`, and the first `ties` that equal it
   const int lo = g.sinks, hi = n - g.recent, want = g.keep - g.sinks - g.recent;
@@ -94,14 +100,32 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
       shift -= digit;
       for (int i = threadIdx.x; i < kBins; i += kSelectThreads) bins[i] = 0;
       __syncthreads();
-      for (int key = 4 * (int)threadIdx.x; key < hi; key += kStep) {
-        const uint4 u = pass == 0 ? read(key) : again(key);
-        if (pass == 0 && key < kCached) *reinterpret_cast<uint4*>(cached + key) = u;   // read back by this thread
+      auto count = [&](int key, const uint4& u) {
         const uint32_t x[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (key + e >= lo && key + e < hi && (pass == 0 || (x[e] >> above) == prefix))
             atomicAdd(&bins[x[e] >> shift & ((1 << digit) - 1)], 1u);
+      };
+      int key = 4 * (int)threadIdx.x;
+      if (pass > 0)
+        for (; key < min(hi, kCached); key += kStep) count(key, *reinterpret_cast<const uint4*>(cached + key));
+      constexpr int kFlight = 4;        // accesses of a thread on their way
+      for (; key < hi; key += kFlight * kStep) {
+        int page[kFlight];
+        float4 w[kFlight];
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) page[i] = page_at(key + i * kStep);
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) w[i] = read_page(key + i * kStep, page[i]);
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) {
+          const int at = key + i * kStep;
+          if (at >= hi) break;
+          const uint4 u = ordered(w[i]);
+          if (pass == 0 && at < kCached) *reinterpret_cast<uint4*>(cached + at) = u;   // read back by this thread
+          count(at, u);
+        }
       }
       __syncthreads();
       // from the largest bin down: the one in which the count reaches `left`.  A thread has kBins / threads bins.
@@ -136,13 +160,12 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
   // in order: what stays.  A key's place is the number of those before it that stay for sure, and of those that
   // equal the limit, `ties` at most.
   int sure_before = 0, equal_before = 0;    // before this step
+  auto get = [&](int key) { return want > 0 && key < hi ? again(key) : make_uint4(0, 0, 0, 0); };
+  uint4 next = get(4 * (int)threadIdx.x);
   for (int base = 0; base < n; base += kStep) {
     const int key = base + 4 * (int)threadIdx.x;
-    uint32_t x[4] = {0, 0, 0, 0};
-    if (want > 0 && key < hi) {
-      const uint4 u = again(key);
-      x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
-    }
+    const uint32_t x[4] = {next.x, next.y, next.z, next.w};
+    next = get(key + kStep);
     bool sure[4], equal[4];
     int counts = 0;                          // equal ones in the upper half
 #pragma unroll
@@ -198,21 +221,22 @@ __device__ __forceinline__ Spot spot_of(const Cache& c, const int32_t* table, lo
   return s;
 }
 
-// Into other pages.  A warp has 32 kept keys of one (sequence, kv head): a lane looks one up and moves its scales and
-// weight, then kRow / 16 lanes move a vector, eight loads of each lane in flight.
-constexpr int kMoveThreads = 256, kMoveVecs = 32;
+// Into other pages.  A warp has kVecs kept keys of one (sequence, kv head): a lane looks one up and moves its scales and
+// weight, then kRow / 16 lanes move a vector, eight loads of each lane in flight.  32 keys; 8 where that would
+// leave SMs with a few warps (one sequence cut from 4.5k keys to 2k: 14.2 us with 32, 12.0 with 8).
+constexpr int kMoveThreads = 256;
 
-template <int kRow>    // bytes of a vector
+template <int kRow, int kVecs>    // kRow: bytes of a vector
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ Evict g, int chunks, long long warps) {
-  constexpr int kLanes = kRow / 16, kGroups = 32 / kLanes, kSteps = kMoveVecs / kGroups, kUnroll = 8;
+  constexpr int kLanes = kRow / 16, kGroups = 32 / kLanes, kSteps = kVecs / kGroups, kUnroll = 2 * kSteps < 8 ? 2 * kSteps : 8;
   static_assert(2 * kSteps % kUnroll == 0, "K and V in whole rounds");
   cudaGridDependencySynchronize();
   const int lane = threadIdx.x % 32;
   const long long w = (long long)blockIdx.x * (kMoveThreads / 32) + threadIdx.x / 32;
   if (w >= warps) return;
-  const int item = (int)(w / chunks), first = (int)(w - (long long)item * chunks) * kMoveVecs;
+  const int item = (int)(w / chunks), first = (int)(w - (long long)item * chunks) * kVecs;
   const int b = item / g.c.Hkv, h = item - b * g.c.Hkv;
-  const int here = min(g.kept_len[b] - first, kMoveVecs);
+  const int here = min(g.kept_len[b] - first, kVecs);
   if (here <= 0) return;
   const long long page_size = 1ll << g.c.page_shift;
   const int elem = g.c.k_scale != nullptr ? 1 : 2;
@@ -251,10 +275,10 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
   }
 }
 
-// Within the same pages.  A CTA has one (sequence, kv head), K or V, 64 bytes of each vector; the first slice's
-// CTAs also move the scales, that of K the weights.
-constexpr int kSlice = 64;
-
+// Within the same pages.  A CTA has one (sequence, kv head), K or V, kSlice bytes of each vector; the first slice's
+// CTAs also move the scales, that of K the weights.  While a step's vectors are on their way the next step's places
+// are looked up.
+template <int kSlice>
 __global__ void __launch_bounds__(kMoveThreads) evict_shift_kernel(const __grid_constant__ Evict g, int row_bytes) {
   constexpr int kLanes = kSlice / 16, kGroups = kMoveThreads / kLanes, kUnroll = 4, kStep = kGroups * kUnroll;
   const int slices = row_bytes / kSlice;
@@ -269,33 +293,41 @@ __global__ void __launch_bounds__(kMoveThreads) evict_shift_kernel(const __grid_
   uint8_t* pool = static_cast<uint8_t*>(is_v ? g.c.v : g.c.k);
   float* scales = is_v ? g.c.v_scale : g.c.k_scale;
   const bool moves_scale = scales != nullptr && slice == 0 && lane == 0, moves_weight = !is_v && slice == 0 && lane == 1;
-  for (int i0 = 0; i0 < kept; i0 += kStep) {
-    uint4 x[kUnroll];
-    float s[kUnroll];
-    Spot to[kUnroll];
+  Spot from[kUnroll], to[kUnroll];    // to: -1 where nothing moves
+  auto look = [&](int i0) {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int i = i0 + u * kGroups + group;
       to[u].page = -1;
-      if (i >= kept) continue;
-      const int key = keys[i];
-      if (key == i) continue;            // it stays where it is
-      const Spot f = spot_of(g.c, g.c.table, g.c.table_stride, g.c.max_pages, b, key);
-      if (f.page < 0) continue;
-      to[u] = spot_of(g.c, g.c.table, g.c.table_stride, g.c.max_pages, b, i);
-      const long long at = h * page_size + f.slot;
-      x[u] = *reinterpret_cast<const uint4*>(pool + f.page * page_bytes + at * row_bytes + col);
-      if (moves_scale) s[u] = scales[f.page * g.c.scale_stride + at];
-      if (moves_weight) s[u] = g.weights[f.page * g.weight_stride + at];
+      const int key = i < kept ? keys[i] : i;
+      if (key == i) continue;          // it stays where it is
+      from[u] = spot_of(g.c, g.c.table, g.c.table_stride, g.c.max_pages, b, key);
+      if (from[u].page >= 0) to[u] = spot_of(g.c, g.c.table, g.c.table_stride, g.c.max_pages, b, i);
     }
+  };
+  look(0);
+  for (int i0 = 0; i0 < kept; i0 += kStep) {
+    uint4 x[kUnroll];
+    float s[kUnroll];
+    Spot here[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      here[u] = to[u];
+      if (to[u].page < 0) continue;
+      const long long at = h * page_size + from[u].slot;
+      x[u] = *reinterpret_cast<const uint4*>(pool + from[u].page * page_bytes + at * row_bytes + col);
+      if (moves_scale) s[u] = scales[from[u].page * g.c.scale_stride + at];
+      if (moves_weight) s[u] = g.weights[from[u].page * g.weight_stride + at];
+    }
+    look(i0 + kStep);
     __syncthreads();   // every load of this step comes before its stores; those of the next step read higher positions
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      if (to[u].page < 0) continue;
-      const long long at = h * page_size + to[u].slot;
-      *reinterpret_cast<uint4*>(pool + to[u].page * page_bytes + at * row_bytes + col) = x[u];
-      if (moves_scale) scales[to[u].page * g.c.scale_stride + at] = s[u];
-      if (moves_weight) g.weights[to[u].page * g.weight_stride + at] = s[u];
+      if (here[u].page < 0) continue;
+      const long long at = h * page_size + here[u].slot;
+      *reinterpret_cast<uint4*>(pool + here[u].page * page_bytes + at * row_bytes + col) = x[u];
+      if (moves_scale) scales[here[u].page * g.c.scale_stride + at] = s[u];
+      if (moves_weight) g.weights[here[u].page * g.weight_stride + at] = s[u];
     }
   }
 }
@@ -333,9 +365,9 @@ extern "C" int fa_kv_evict(const fa_paged_kv* kv, float* weights, int64_t weight
   if (kept_len == kv->kv_len)   // every head's CTA reads the length
     return set_error(FA_ERR_INVALID_ARG, "kept_len must not be kv_len itself");
   const long long items = (long long)kv->B * kv->Hkv, most = keep < max_kv ? keep : max_kv;
-  const long long chunks = (most + paged::kMoveVecs - 1) / paged::kMoveVecs;
-  if (items * std::max(chunks, 8ll) >= (1ll << 31))
-    return set_error(FA_ERR_INVALID_ARG, "B*Hkv*keep/%d must be < 2^31", paged::kMoveVecs);
+  const int vecs = items * ((most + 31) / 32) >= 32ll * sm_count() ? 32 : 8;   // of a warp that moves
+  const long long chunks = (most + vecs - 1) / vecs;
+  if (items * std::max(chunks, 8ll) >= (1ll << 31)) return set_error(FA_ERR_INVALID_ARG, "B*Hkv*keep/32 must be < 2^31");
   g.c.status = device_status_word();
   if (!g.c.status) return set_error(FA_ERR_CUDA, "could not allocate the device status record");
   g.weights = weights;
@@ -349,17 +381,20 @@ extern "C" int fa_kv_evict(const fa_paged_kv* kv, float* weights, int64_t weight
   g.kept_len = kept_len;
   g.kept = kept;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  constexpr int cache = paged::kCached * 4;
-  static std::atomic<uint64_t> prepared{0};
-  if ((rc = prepare_kernel(reinterpret_cast<const void*>(paged::evict_select_kernel), cache, paged::kSelectThreads, 0,
-                           "evict_select_kernel", &prepared)))
+  const bool wide = items < 2ll * sm_count() && max_kv > 16384;
+  const int cache = (wide ? 40960 : 8192) * 4;
+  auto select = wide ? paged::evict_select_kernel<1024, 40960> : paged::evict_select_kernel<512, 8192>;
+  static std::atomic<uint64_t> prepared[2];
+  if ((rc = prepare_kernel(reinterpret_cast<const void*>(select), cache, wide ? 1024 : 512, 0, "evict_select_kernel", &prepared[wide])))
     return rc;
-  paged::evict_select_kernel<<<(unsigned)items, paged::kSelectThreads, cache, s>>>(g);
+  select<<<(unsigned)items, wide ? 1024 : 512, cache, s>>>(g);
   if ((rc = check_cuda(cudaGetLastError(), "launch evict_select_kernel"))) return rc;
   const int row = kv->d * (kv->dtype == FA_KV_E4M3 ? 1 : 2);
   const long long warps = items * chunks, per = paged::kMoveThreads / 32;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(in_place ? items * 2 * (row / paged::kSlice) : (warps + per - 1) / per));
+  // in place: 64 bytes of a vector, 32 where that leaves SMs without a CTA
+  const int slice = items * 2 * (row / 64) < 2ll * sm_count() ? 32 : 64;
+  cfg.gridDim = dim3((unsigned)(in_place ? items * 2 * (row / slice) : (warps + per - 1) / per));
   cfg.blockDim = dim3(paged::kMoveThreads);
   cfg.stream = s;
   cudaLaunchAttribute early;
@@ -367,7 +402,11 @@ extern "C" int fa_kv_evict(const fa_paged_kv* kv, float* weights, int64_t weight
   early.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
-  if (in_place) return check_cuda(cudaLaunchKernelEx(&cfg, paged::evict_shift_kernel, g, row), "launch evict_shift_kernel");
-  auto kern = row == 64 ? paged::evict_move_kernel<64> : (row == 128 ? paged::evict_move_kernel<128> : paged::evict_move_kernel<256>);
+  if (in_place)
+    return check_cuda(cudaLaunchKernelEx(&cfg, slice == 32 ? paged::evict_shift_kernel<32> : paged::evict_shift_kernel<64>, g, row),
+                      "launch evict_shift_kernel");
+  auto kern = row == 64    ? (vecs == 8 ? paged::evict_move_kernel<64, 8> : paged::evict_move_kernel<64, 32>)
+              : row == 128 ? (vecs == 8 ? paged::evict_move_kernel<128, 8> : paged::evict_move_kernel<128, 32>)
+                           : (vecs == 8 ? paged::evict_move_kernel<256, 8> : paged::evict_move_kernel<256, 32>);
   return check_cuda(cudaLaunchKernelEx(&cfg, kern, g, (int)chunks, warps), "launch evict_move_kernel");
 }
