@@ -193,7 +193,7 @@ struct AccCursor {
     }
   }
   __device__ __forceinline__ void place(const Attn& p, int parts) {
-    const int r = (int)(left / parts);   // (units are under 2^31: a sequence has 2^22 blocks of keys at most)
+    const int r = (int)(left / parts);   // (a sequence's units are under 2^27)
     part = (int)(left - (long long)r * parts);
     j = r / p.c.Hkv;
     h = r - j * p.c.Hkv;
@@ -972,6 +972,10 @@ extern "C" int fa_kv_accumulate(const fa_paged_kv* kv, float* weights, int64_t w
   if (window < 0 || sinks < 0) return set_error(FA_ERR_INVALID_ARG, "window and sinks must be >= 0 (got %d, %d)", window, sinks);
   if (!window && sinks) return set_error(FA_ERR_INVALID_ARG, "sinks need a window");
   const bool fp8 = kv->dtype == FA_KV_E4M3;
+  const int max_kv = kv->max_pages * kv->page_size;
+  // a sequence's units are counted in 32 bits
+  if ((long long)kv->Hkv * (max_kv / paged::kAccKeys + 1) >= (1ll << 31) / 16)
+    return set_error(FA_ERR_INVALID_ARG, "Hkv * max_pages * page_size must be < 2^35");
   if (T == 0 || max_q == 0) return FA_OK;
   const size_t need = paged::accumulate_bytes(T, max_q, Hq, kv->Hkv, kv->d, kv->dtype);
   if (need) {
@@ -982,7 +986,6 @@ extern "C" int fa_kv_accumulate(const fa_paged_kv* kv, float* weights, int64_t w
   }
   p.c.status = device_status_word();
   if (!p.c.status) return set_error(FA_ERR_CUDA, "could not allocate the device status record");
-  const int max_kv = kv->max_pages * kv->page_size;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.q_stride = q_stride;
   p.q_indptr = q_indptr;

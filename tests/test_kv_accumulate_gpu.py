@@ -241,6 +241,45 @@ def test_views_and_refusals():
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("most", [1, 40])
+def test_more_sequences_than_threads(fmt, most):
+    # 900 of them, some without keys or without new tokens; one with a chunk where most = 40
+    g = torch.Generator().manual_seed(most)
+    lens = torch.randint(0, 20, (900,), generator=g).tolist()
+    new = [min(n, 1) if i % 7 else 0 for i, n in enumerate(lens)]
+    lens[500], new[500] = 600, most
+    c = P.make(lens, 1, 64, 16, fmt, seed=most)
+    q = torch.randn((sum(new), 4, 64), generator=g).to(torch.bfloat16)
+    lse = W.log_sum_exps(c, q, new, 0.125)
+    pool, rows = W.make(c, seed=1)
+    check(c, pool, rows, q, lse, new, 0.125)
+
+
+def test_a_program_of_captured_steps():
+    # two calls captured one behind the other share a workspace, as a stream's calls do
+    c = P.make([2000, 50], 2, 64, 32, "e4m3", seed=12)
+    q = torch.randn((2, 8, 64), generator=torch.Generator().manual_seed(12)).to(torch.bfloat16).cuda()
+    lse = W.log_sum_exps(c, q.cpu(), [1, 1], 0.125).cuda()
+    ws = torch.empty(binding.fa_kv_accumulate_workspace_size(2, 1, 8, 2, 64, binding.FA_KV_E4M3), device="cuda", dtype=torch.uint8)
+    a, ip = W.make(c, seed=1)[0].cuda(), P.indptr([1, 1])
+    b = a.clone()
+    call = lambda w, x, **kw: binding.kv_accumulate(w, x, lse, c.k, c.v, c.table, c.kv_len, ip, 1, k_scale=c.ks, v_scale=c.vs, **kw)
+    q2 = q.flip(1).contiguous()
+    call(b, q)
+    call(b, q2)
+    graph, start = torch.cuda.CUDAGraph(), a.clone()
+    with torch.cuda.graph(graph):
+        call(a, q, workspace=ws)
+        call(a, q2, workspace=ws)
+    for _ in range(2):
+        a.copy_(start)
+        graph.replay()
+    assert torch.equal(bits(a), bits(b))
+    with pytest.raises(binding.FAError):
+        call(a, q, workspace=ws[:-256])
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
 @pytest.mark.parametrize("new", [[1, 1, 1], [1, 200, 2, 30]])
 def test_a_wait_that_runs_out_is_reported_and_nothing_else_breaks(monkeypatch, fmt, new):
     # test build with an injected stall (100 ms limit)

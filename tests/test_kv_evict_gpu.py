@@ -162,6 +162,35 @@ def test_python_refusals():
             binding.kv_evict(w, *args, **bad)
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+def test_many_sequences(in_place):
+    g = torch.Generator().manual_seed(4)
+    lens = torch.randint(0, 150, (400,), generator=g).tolist()
+    c = P.make(lens, 1, 64, 16, "e4m3", seed=4, spare=3 + sum(-(-min(n, 60) // 16) for n in lens))
+    w = W.make(c, seed=4)[0].cuda()
+    table_out = c.table if in_place else free_table(c, 60).cuda()
+    after, want_len, want_kept = expected(c, w, table_out, 60, 3, 20)
+    kept_len, kept = binding.kv_evict(w, c.k, c.v, c.table, c.kv_len, 60, sinks=3, recent=20, table_out=table_out, k_scale=c.ks, v_scale=c.vs)
+    binding.device_status()
+    assert torch.equal(kept_len.cpu(), want_len) and torch.equal(kept.cpu(), want_kept)
+    for x, y in zip(pools(c, w), after):
+        assert torch.equal(bits(x), bits(y))
+
+
+def test_source_pages_may_be_shared():
+    # two sequences over the same pages, each moved to pages of its own
+    c = P.make([200, 200], 2, 64, 16, "bf16", seed=6, spare=30)
+    c.table[1] = c.table[0]
+    w = W.make(c, seed=6)[0].cuda()
+    table_out = free_table(c, 64).cuda()
+    after, _, want_kept = expected(c, w, table_out, 64, 2, 10)
+    kept_len, kept = binding.kv_evict(w, c.k, c.v, c.table, c.kv_len, 64, sinks=2, recent=10, table_out=table_out)
+    binding.device_status()
+    assert torch.equal(kept.cpu(), want_kept) and torch.equal(kept[0], kept[1])
+    for x, y in zip(pools(c, w), after):
+        assert torch.equal(bits(x), bits(y))
+
+
 def test_serving_with_a_budget():
     """Prompt, decoding steps and evictions, each step through the calls that a program makes; the outputs of the last step
     against 64-bit attention over the keys that were kept, rotated at their own positions."""

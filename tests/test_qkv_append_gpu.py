@@ -155,6 +155,18 @@ def test_bad_entries_are_reported_and_skipped(fmt):
         assert torch.equal(a[[0, 1, 2, 6, 7, 8]], b[[0, 1, 2, 6, 7, 8]])
 
 
+def test_queries_in_place():
+    lens = new = [70, 3, 200]
+    c = P.make(lens, 2, 128, 64, "bf16", seed=3)
+    g = torch.Generator().manual_seed(3)
+    rows, _, _ = R.heads(1, 273, 8, 2, 128, g)
+    q, k, v = (x.contiguous().cuda() for x in rows[0].split([8, 2, 2], 1))
+    f = R.frequencies(128).cuda()
+    call = lambda **kw: binding.qkv_append(q, k, v, c.k, c.v, c.table, c.kv_len, P.indptr(new), f, **kw)
+    want = call()
+    assert call(out=q) is q and torch.equal(q, want)
+
+
 def test_graph_follows_lengths_and_tables():
     c = P.make([30, 60], 2, 128, 16, "e4m3", seed=9)
     g = torch.Generator().manual_seed(9)
