@@ -9,11 +9,14 @@
 //   * a unit is 256 keys (two tiles) of one sequence and kv head; a persistent CTA takes its units one after the
 //     other and streams, for each, the query blocks that see its keys.  No atomics, the same bits in every call.
 //   * few rows (decoding): the bytes of K bound it.  A CTA has a run of units, most of them of one head, whose
-//     queries stay in shared memory; a ring of K tiles is kept full.
-//   * chunks: one exponential per pair and head, 32 a clock and SM, against 512 clocks of tensor work for
-//     256 x 128 x 128: the exponentials bound it.  Units are dealt round by round, early keys, which most tokens
-//     see, first.  Where there are few of them each is cut into parts by its query blocks, whose sums a second
-//     kernel joins in order.
+//     queries stay in shared memory; a ring of K tiles is kept full.  64 sequences, 284k keys, 8 kv heads of 128:
+//     E4M3 55 us (85 % of the copy rate), BF16 95 us (93 %).
+//   * chunks: 256 x 128 pairs of a head cost 1024 clocks of tensor work and as many exponentials as the special
+//     function units do in half of that, but a pair takes two or three issue slots of the summing warps beside its
+//     exponential, and these bound it: without the products the kernel would take 421 of 444 us, without the
+//     exponentials 331.  2048 tokens over 34k keys, 32 heads of 128: 428 us, 1295 TFLOP/s.  Units are dealt round by
+//     round, early keys, which most tokens see, first.  Where there are few of them each is cut into parts by its
+//     query blocks, whose sums a second kernel joins in order.
 // E4M3 caches, few rows: the codes are the operand as they are (kind::f8f6f4).  A query vector goes into three E5M2
 // vectors that add up to it: BF16 has 8 significant bits, E5M2 3, and its exponents reach 2^-31 of the largest
 // entry, so the sum is exact down to entries of 2^-24 of it.  Chunks: a warpgroup turns the codes into BF16, once for
@@ -53,7 +56,10 @@ struct AccCfg {
   // the pieces side by side, 3 N columns of S that are added afterwards: the tensor core then reads K once.  (64
   // columns leave no room for that: S takes the pieces one after the other.)
   static constexpr bool kWide = kPieced && N <= 32;
-  static constexpr int kSumWarps = 8, kThreads = 32 * (kSumWarps + (kConvert ? 8 : 4));
+  // chunks, d = 128: two warps share a block's columns, 64 each, and add their sums at the end of a unit (2048 tokens
+  // over 34k keys 428 us, with one 442; d = 64 422 and 419).  With converters beside them they would spill.
+  static constexpr int kHalves = kChunk && !kConvert && D == 128 ? 2 : 1;
+  static constexpr int kSumWarps = 8 * kHalves, kThreads = 32 * (kSumWarps + (kConvert ? 8 : 4));
   // CTAs on an SM: two where each holds three units' keys or more.  (A unit's hand-offs take longer than its 16 or 32 KB:
   // decoding over 284k E4M3 keys, d = 128, 61 us with one.)
   static constexpr int kCtas = N == 16 && D * (kFp8 ? 1 : 2) <= 128 ? 2 : 1;
@@ -70,10 +76,12 @@ struct AccCfg {
   static constexpr int kSideBytes = kAccKeys * 4 * (kFp8 ? 2 : 1) + 64;  // a unit's weights, scales and pages
   static constexpr int kQOff = 0;
   static constexpr int kCodeOff = kQOff + kQStages * kQBytes, kKOff = kCodeOff + kCodeBytes;
-  static constexpr int kRest = kColStages * kColBytes + kSideStages * kSideBytes;
+  static constexpr int kHalfBytes = kHalves == 2 ? 2 * kAccKeys * 4 : 0; // two units' sums over the second half
+  static constexpr int kRest = kColStages * kColBytes + kSideStages * kSideBytes + kHalfBytes;
   static constexpr int kRoom = (kCtas == 2 ? 112 : 226) * 1024 - kKOff - kRest;
   static constexpr int kKStages = kRoom / kPairBytes < 6 ? kRoom / kPairBytes : 6;
   static constexpr int kColOff = kKOff + kKStages * kPairBytes, kSideOff = kColOff + kColStages * kColBytes;
+  static constexpr int kHalfOff = kSideOff + kSideStages * kSideBytes;
   static constexpr int kSharedOff = kColOff + kRest;
   // S: buffers of a tile, each kBufCols columns of tensor memory
   static constexpr int kSCols = kWide ? kPieces * N : N, kBufCols = kWide ? 4 * N : N;
@@ -84,13 +92,14 @@ struct AccCfg {
   static_assert(kKStages >= 1 && kTmemCols * kCtas <= 512 && kTmemCols >= 32, "shared or tensor memory");
 };
 
-constexpr int kMaxKStages = 6, kMaxQStages = 4, kMaxBufs = 4, kMaxSideStages = 8, kMaxWarps = 16;
+constexpr int kMaxKStages = 6, kMaxQStages = 4, kMaxBufs = 4, kMaxSideStages = 8, kMaxWarps = 20;
 
 struct AccShared {
   uint64_t k_full[kMaxKStages], k_empty[kMaxKStages], q_full[kMaxQStages], q_empty[kMaxQStages];
   uint64_t col_full[kColStages], col_empty[kColStages], side_full[kMaxSideStages], side_empty[kMaxSideStages];
   uint64_t s_full[2][kMaxBufs], s_empty[2][kMaxBufs];
   uint64_t code_full, code_empty;  // E4M3 chunks: a unit's codes have landed / have been read
+  uint64_t half_full[2][2], half_empty[2][2];  // sums over the second half of the columns: by tile, two units'
   uint64_t mma_done;
   uint64_t never;                  // test builds only: a barrier nothing arrives on
   long long scan[kMaxWarps];
@@ -105,7 +114,8 @@ constexpr int acc_smem() {
 }
 template <int D, bool kFp8>
 constexpr bool acc_fits() {
-  return AccCfg<D, kFp8, 16>::kCtas * (acc_smem<D, kFp8, 16>() + 1024) <= 228 * 1024 && acc_smem<D, kFp8, 32>() <= 227 * 1024 && acc_smem<D, kFp8, 64>() <= 227 * 1024 &&
+  return AccCfg<D, kFp8, 16>::kCtas * (acc_smem<D, kFp8, 16>() + 1024) <= 228 * 1024 &&
+         acc_smem<D, kFp8, 32>() <= 227 * 1024 && acc_smem<D, kFp8, 64>() <= 227 * 1024 &&
          acc_smem<D, kFp8, 128>() <= 227 * 1024;
 }
 static_assert(acc_fits<64, false>() && acc_fits<64, true>() && acc_fits<128, false>() && acc_fits<128, true>(),
@@ -357,7 +367,12 @@ __global__ void __launch_bounds__(AccCfg<D, kFp8, N>::kThreads, AccCfg<D, kFp8, 
     for (int t = 0; t < 2; ++t)
       for (int s = 0; s < C::kBufs; ++s) {
         mbar_init(&sh.s_full[t][s], 1);
-        mbar_init(&sh.s_empty[t][s], 4);
+        mbar_init(&sh.s_empty[t][s], 4 * C::kHalves);
+      }
+    for (int t = 0; t < 2; ++t)
+      for (int s = 0; s < 2; ++s) {
+        mbar_init(&sh.half_full[t][s], 4);
+        mbar_init(&sh.half_empty[t][s], 4);
       }
     mbar_init(&sh.code_full, 1);
     mbar_init(&sh.code_empty, 128);
@@ -597,9 +612,11 @@ __global__ void __launch_bounds__(AccCfg<D, kFp8, N>::kThreads, AccCfg<D, kFp8, 
       }
     }
   } else if (warp < C::kSumWarps) {
-    // ------------------------------------------------------------ exponentials and sums: a thread per key
-    const int t = warp / 4, row = t * kAccTile + (warp % 4) * 32 + lane;   // the thread's key within a unit
-    const uint32_t tS = tmem + t * C::kBufs * C::kBufCols + ((uint32_t)((warp % 4) * 32) << 16);
+    // ------------------------------------------------------------ exponentials and sums: a thread (or two) per key
+    constexpr int kCols = N / C::kHalves;            // of a block, from col0 on: what this warp sums
+    const int t = warp / (4 * C::kHalves), half = warp / 4 % C::kHalves, col0 = half * kCols;
+    const int row = t * kAccTile + (warp % 4) * 32 + lane;   // the thread's key within a unit
+    const uint32_t tS = tmem + t * C::kBufs * C::kBufCols + col0 + ((uint32_t)((warp % 4) * 32) << 16);
     int nq = 0, ns = 0, nu = 0;
     long long number = blockIdx.x;                   // chunks: of the part in the launch
     bool ok = true;
@@ -611,7 +628,9 @@ __global__ void __launch_bounds__(AccCfg<D, kFp8, N>::kThreads, AccCfg<D, kFp8, 
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.s_empty[t][buf]);
     };
-    auto columns = [&](int n) { return reinterpret_cast<const float*>(smem + C::kColOff + n % kColStages * C::kColBytes); };
+    auto columns = [&](int n) {
+      return reinterpret_cast<const float*>(smem + C::kColOff + n % kColStages * C::kColBytes) + col0;
+    };
     for (; ok && cur.valid(p); cur.next(p, parts), ++nu, number += gridDim.x) {
       const int x = nu % C::kSideStages;
       const uint8_t* side = smem + C::kSideOff + x * C::kSideBytes;
@@ -638,38 +657,28 @@ __global__ void __launch_bounds__(AccCfg<D, kFp8, N>::kThreads, AccCfg<D, kFp8, 
       }
       while (i < last) {
         if (C::kChunk && i >= i_all && i < last_all) {
-          // 32 columns of S are on their way while as many are summed, from one block to the next
-          uint32_t r[2][32];
-          if (!(ok = wait(&sh.s_full[t][ns % C::kBufs], ns, C::kBufs))) break;
-          tc_fence_after();
-          tmem_ld32(tS + ns % C::kBufs * C::kBufCols, r[0]);
           for (; i < last_all; ++i, ++nq, ++ns) {
             const int buf = ns % C::kBufs;
             const float* col = columns(nq);
+            if (!(ok = wait(&sh.s_full[t][buf], ns, C::kBufs))) break;
+            tc_fence_after();
+            uint32_t r[32];
+            tmem_ld32(tS + buf * C::kBufCols, r);
             if (!(ok = wait(&sh.col_full[nq % kColStages], nq, kColStages))) break;
             float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int c = 0; c < N / 32; ++c) {
+            for (int c = 0; c < kCols / 32; ++c) {
               tmem_ld_wait();
-              reg_fence(r[c % 2]);
-              if (c + 1 < N / 32) {
-                tmem_ld32(tS + buf * C::kBufCols + (c + 1) * 32, r[(c + 1) % 2]);
-              } else {
-                give(buf);
-                if (i + 1 < last_all) {
-                  if (!(ok = wait(&sh.s_full[t][(ns + 1) % C::kBufs], ns + 1, C::kBufs))) break;
-                  tc_fence_after();
-                  tmem_ld32(tS + (ns + 1) % C::kBufs * C::kBufCols, r[(c + 1) % 2]);
-                }
-              }
-              acc_columns<32, false, kFp8, false>(r[c % 2], col + c * 32, nullptr, p.scale, key_scale, 0, sum);
+              reg_fence(r);
+              if (c + 1 == kCols / 32) give(buf);
+              acc_columns<32, false, kFp8, false>(r, col + c * 32, nullptr, p.scale, key_scale, 0, sum);
+              if (c + 1 < kCols / 32) tmem_ld32(tS + buf * C::kBufCols + (c + 1) * 32, r);
             }
-            if (!ok) break;
             total += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.col_empty[nq % kColStages]);
           }
-          tmem_ld_wait();
+          tmem_ld_wait();   // (where a wait gave up)
           if (!ok) break;
           continue;
         }
@@ -680,15 +689,15 @@ __global__ void __launch_bounds__(AccCfg<D, kFp8, N>::kThreads, AccCfg<D, kFp8, 
           tc_fence_after();
           // the rows that see the key: its own token's on, up to the last one whose window holds it
           const int t0 = i * tokens, here = min(cur.s.n - t0, tokens);
-          const int lo = min(max(ahead - t0, 0), here) * p.group;
+          const int lo = min(max(ahead - t0, 0), here) * p.group - col0;
           int end = here;
           if (p.window && key >= p.sinks) end = (int)min((long long)here, max((long long)ahead + p.window - t0, 0ll));
-          const int hi = end * p.group;
+          const int hi = end * p.group - col0;
           const float* col = columns(nq);
           const uint32_t at = tS + buf * C::kBufCols;
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int c0 = 0; c0 < N; c0 += W) {
+          for (int c0 = 0; c0 < kCols; c0 += W) {
             if (__all_sync(0xffffffffu, hi <= c0 || lo >= c0 + W)) continue;
             uint32_t r[W];
             auto get = [&](uint32_t (&to)[W], int c) {
@@ -727,6 +736,23 @@ __global__ void __launch_bounds__(AccCfg<D, kFp8, N>::kThreads, AccCfg<D, kFp8, 
           ++nq;
         }
         ++i;
+      }
+      if constexpr (C::kHalves == 2) {
+        // the second half's sums go to the first half's threads
+        if (!ok) break;
+        const int y = nu % 2;
+        float* sums = reinterpret_cast<float*>(smem + C::kHalfOff) + y * kAccKeys;
+        if (half == 1) {
+          if (!(ok = wait(&sh.half_empty[t][y], nu + 2, 2))) break;   // (free at first)
+          sums[row] = total;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.half_full[t][y]);
+          continue;
+        }
+        if (!(ok = wait(&sh.half_full[t][y], nu, 2))) break;
+        total += sums[row];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.half_empty[t][y]);
       }
       if (ok && cur.w.seen(key)) {
         if (parts > 1)
