@@ -663,10 +663,14 @@ def _positions(positions, B, N, dev):
 
 def _empty_as(t, stream):
     """A fresh tensor of t's shape, its tokens in front of its heads in memory where t's are."""
-    B, H, N, d = t.shape
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _empty_as(t, None)
+    shape = t.shape
+    B, H, N, d = shape
     if t.stride(1) < t.stride(2):
-        return _empty((B, N, H, d), t.dtype, t, stream).transpose(1, 2)
-    return _empty((B, H, N, d), t.dtype, t, stream)
+        return t.new_empty_strided(shape, (N * H * d, d, H * d, 1))
+    return t.new_empty(shape)
 
 
 def norm_rotate(q, k, inv_freq, positions=None, q_weight=None, k_weight=None, eps: float = 1e-6, interleaved: bool = False,
@@ -686,7 +690,7 @@ def norm_rotate(q, k, inv_freq, positions=None, q_weight=None, k_weight=None, ep
     hq, hk = _heads(q, "q", sq, dev), _heads(k, "k", sk, dev)
     pos, pos_stride = _positions(positions, sq[0], sq[2], dev)
     if out is None:
-        out = _empty(sq, torch.bfloat16, q, stream), _empty(sk, torch.bfloat16, q, stream)
+        out = _empty(sq, torch.bfloat16, q, stream), _empty(sk, torch.bfloat16, k, stream)
     oq, ok = out
     hoq, hok = _heads(oq, "out", sq, dev), _heads(ok, "out", sk, dev)
     with _on_device(q):

@@ -29,6 +29,7 @@ SHAPES = [  # B, N, hq, hkv, d, rot, interleaved
     (1, 1, 1, 1, 64, 64, False), (1, 1, 40, 8, 128, 128, False), (2, 129, 4, 4, 64, 64, True), (3, 77, 7, 1, 128, 64, False),
     (1, 333, 5, 3, 128, 48, True), (2, 50, 33, 2, 64, 16, False), (1, 1000, 2, 1, 128, 112, False), (5, 3, 12, 12, 64, 0, False),
     (1, 65, 130, 1, 64, 32, True), (4, 31, 9, 6, 128, 128, True), (1, 700, 16, 16, 64, 48, False),
+    (1, 129, 2, 2, 64, 64, False), (2, 8, 8, 1, 128, 128, False), (1, 40, 400, 1, 64, 64, False),   # (a side with one CTA)
 ]
 
 
