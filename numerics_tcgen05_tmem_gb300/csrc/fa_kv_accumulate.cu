@@ -273,15 +273,18 @@ __device__ __forceinline__ void acc_columns(const uint32_t (&r)[W], const float*
   for (int i = 0; i < W; i += 4) {
     const float4 l = *reinterpret_cast<const float4*>(neg_lse + i);
     float s0 = __uint_as_float(r[i]), s1 = __uint_as_float(r[i + 1]), s2 = __uint_as_float(r[i + 2]), s3 = __uint_as_float(r[i + 3]);
-    if constexpr (kScaled) {
-      mul2(s0, s1, s0, s1, key_scale, key_scale);
-      mul2(s2, s3, s2, s3, key_scale, key_scale);
-    }
     if constexpr (kPieced) {
+      // the query's factor first: codes times q stays in FP32's range, where pieces times a large key's scale would not
       const float4 f = *reinterpret_cast<const float4*>(factor + i);
-      fma2(s0, s1, s0, s1, f.x, f.y, l.x, l.y);
-      fma2(s2, s3, s2, s3, f.z, f.w, l.z, l.w);
+      mul2(s0, s1, s0, s1, f.x, f.y);
+      mul2(s2, s3, s2, s3, f.z, f.w);
+      fma2(s0, s1, s0, s1, key_scale, key_scale, l.x, l.y);
+      fma2(s2, s3, s2, s3, key_scale, key_scale, l.z, l.w);
     } else {
+      if constexpr (kScaled) {
+        mul2(s0, s1, s0, s1, key_scale, key_scale);
+        mul2(s2, s3, s2, s3, key_scale, key_scale);
+      }
       fma2(s0, s1, s0, s1, scale, scale, l.x, l.y);
       fma2(s2, s3, s2, s3, scale, scale, l.z, l.w);
     }

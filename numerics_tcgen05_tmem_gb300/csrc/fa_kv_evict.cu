@@ -7,6 +7,8 @@
 //           (11, 11 and 10 of them, a histogram each in shared memory), then one pass in order that writes the
 //           kept positions.
 //   move    the kept vectors, their scales and weights: bandwidth work, 16 bytes a thread.
+// Measured: 64 sequences of 4.4k keys, 8 heads of 128, cut to 2000 in other pages, E4M3 105 us (66 at the copy rate;
+// the selection 27, whose longest sequence the first moves wait for), BF16 158; one sequence of 4.5k to 2k 12 us.
 // In place a vector only ever moves to a lower position, to where nothing is that is still to be read as long
 // as the vectors are taken in order: a CTA takes all of one head's K or V, 64 (or 32) bytes wide, step by step,
 // and waits between a step's loads and its stores.
@@ -192,7 +194,8 @@ __global__ void __launch_bounds__(kSelectThreads, 1536 / kSelectThreads) evict_s
     int at_sure = sure_before + (excl & 0xFFFF), at_equal = equal_before + (excl >> 16);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      if (sure[e] || (equal[e] && at_equal < ties)) out[at_sure + min(at_equal, ties)] = key + e;
+      const int place = at_sure + min(at_equal, ties);   // (under keep, unless weights change during the call)
+      if ((sure[e] || (equal[e] && at_equal < ties)) && place < kept) out[place] = key + e;
       at_sure += sure[e] ? 1 : 0;
       at_equal += equal[e] ? 1 : 0;
     }
@@ -345,7 +348,8 @@ extern "C" int fa_kv_evict(const fa_paged_kv* kv, float* weights, int64_t weight
   int rc;
   if ((rc = paged::check_cache(kv, &g.c))) return rc;
   if ((rc = paged::check_weights(kv, weights, weight_stride))) return rc;
-  if (keep < 1 || sinks < 0 || recent < 0) return set_error(FA_ERR_INVALID_ARG, "keep must be >= 1, sinks and recent >= 0 (got %d, %d, %d)", keep, sinks, recent);
+  if (keep < 1 || sinks < 0 || recent < 0)
+    return set_error(FA_ERR_INVALID_ARG, "keep must be >= 1, sinks and recent >= 0 (got %d, %d, %d)", keep, sinks, recent);
   if ((long long)sinks + recent > keep)
     return set_error(FA_ERR_INVALID_ARG, "sinks + recent = %lld must be at most keep = %d", (long long)sinks + recent, keep);
   const bool in_place = !table_out || table_out == kv->block_table;

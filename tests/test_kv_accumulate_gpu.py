@@ -114,6 +114,19 @@ def test_large_and_small_queries_over_e4m3():
     assert (off <= ref[1]).all(), float((off / ref[1]).max())
 
 
+@pytest.mark.parametrize("new,hq,hkv", [([1, 3], 4, 1), ([2, 7], 8, 2), ([1, 40], 2, 2)])
+def test_keys_and_queries_near_the_ends_of_the_range(new, hq, hkv):
+    # keys past 2^110 with queries as small, whose products are ordinary; and the other way round
+    for up in (110, -110):
+        c = P.make([300, 70], hkv, 128, 16, "e4m3", seed=11)
+        c.ks.mul_(2.0 ** up)
+        c.values = [(k * 2.0 ** up, v) for k, v in c.values]
+        q = torch.randn((sum(new), hq, 128), generator=torch.Generator().manual_seed(11)).mul(2.0 ** -up).to(torch.bfloat16)
+        lse = W.log_sum_exps(c, q, new, 0.125)
+        pool, rows = W.make(c, seed=11)
+        check(c, pool, rows, q, lse, new, 0.125)
+
+
 def test_special_values():
     # a NaN key, a NaN query, a lse of -inf and +inf: only what they reach
     lens, new, hq, hkv, d = [300, 300], [2, 1], 2, 1, 64
