@@ -11,10 +11,9 @@
 //   * few rows (decoding): the bytes of K bound it.  A CTA has a run of units, most of them of one head, whose
 //     queries stay in shared memory; a ring of K tiles is kept full.  64 sequences, 284k keys, 8 kv heads of 128:
 //     E4M3 55 us (85 % of the copy rate), BF16 95 us (93 %).
-//   * chunks: 256 x 128 pairs of a head cost 1024 clocks of tensor work and as many exponentials as the special
-//     function units do in half of that, but a pair takes two or three issue slots of the summing warps beside its
-//     exponential, and these bound it: without the products the kernel would take 421 of 444 us, without the
-//     exponentials 331.  2048 tokens over 34k keys, 32 heads of 128: 428 us, 1295 TFLOP/s.  Units are dealt round by
+//   * chunks: 256 x 128 pairs of a head take 1024 clocks of tensor work, and as many for their exponentials (32 a clock
+//     and SM); both together, with the sums between them, bound it.  2048 tokens over 34k keys, 32 heads of 128: 406 us,
+//     1364 TFLOP/s (without the products 367, without the exponentials 367, with neither 266).  Units are dealt round by
 //     round, early keys, which most tokens see, first.  Where there are few of them each is cut into parts by its
 //     query blocks, whose sums a second kernel joins in order.
 // E4M3 caches, few rows: the codes are the operand as they are (kind::f8f6f4).  A query vector goes into three E5M2
@@ -34,6 +33,7 @@ namespace paged {
 constexpr int kAccKeys = 256;        // of a unit
 constexpr int kAccTile = 128;        // keys of a tile
 constexpr int kPieces = 3;           // E5M2 vectors of a query vector
+constexpr float kLog2e = 1.4426950408889634f, kLog2eRest = (float)(1.4426950408889634 - (double)kLog2e);
 constexpr int kColStages = 4;        // blocks of queries whose log-sum-exps are in shared memory
 // Chunks: units are cut into parts until there are about eight for each of 152 SMs, none of less than four
 // query blocks.
@@ -45,6 +45,7 @@ struct Acc {
   float* weights;          // [pages][Hkv][page_size]
   long long weight_stride;
   const float* q_scale;    // E4M3, few rows: [T, Hq], what the pieces are to be multiplied by
+  float scale_log2;        // scale log2(e)
   float* part;             // chunks: [kMostParts][kAccKeys], the parts' sums
   int max_parts;           // of a unit
 };
@@ -56,9 +57,9 @@ struct AccCfg {
   // the pieces side by side, 3 N columns of S that are added afterwards: the tensor core then reads K once.  (64
   // columns leave no room for that: S takes the pieces one after the other.)
   static constexpr bool kWide = kPieced && N <= 32;
-  // chunks, d = 128: two warps share a block's columns, 64 each, and add their sums at the end of a unit (2048 tokens
-  // over 34k keys 428 us, with one 442; d = 64 422 and 419).  With converters beside them they would spill.
-  static constexpr int kHalves = kChunk && !kConvert && D == 128 ? 2 : 1;
+  // chunks: two warps share a block's columns, 64 each, and add their sums at the end of a unit (2048 tokens over 34k keys
+  // 406 us, with one 423).  Not with converters beside them: 80 registers are too few (466 us, 431).
+  static constexpr int kHalves = kChunk && !kConvert ? 2 : 1;
   static constexpr int kSumWarps = 8 * kHalves, kThreads = 32 * (kSumWarps + (kConvert ? 8 : 4));
   // CTAs on an SM: two where each holds three units' keys or more.  (A unit's hand-offs take longer than its 16 or 32 KB:
   // decoding over 284k E4M3 keys, d = 128, 61 us with one.)
@@ -263,33 +264,25 @@ struct AccCursor {
   __device__ __forceinline__ bool tile(int t) const { return key() + t * kAccTile < w.hi; }
 };
 
-// sum += of the columns: exp(S f - lse), of those in `mask` alone where kMasked.  The difference is taken before it
-// goes to base 2: for the keys that weigh most it is small, and so is the error that the product adds.
-template <int W, bool kPieced, bool kScaled, bool kMasked>
-__device__ __forceinline__ void acc_columns(const uint32_t (&r)[W], const float* neg_lse, const float* factor, float scale,
-                                            float key_scale, uint32_t mask, float (&sum)[4]) {
-  constexpr float kLog2e = 1.4426950408889634f;
+// sum += of the columns: 2^(S f factor - l), of those in `mask` alone where kMasked; l is lse log2(e), and the factors
+// hold scale log2(e), so that an exponential takes one product and sum.  (A product with log2(e) behind the difference
+// of natural logarithms costs two instructions more for four columns: 2048 tokens over 34k keys 428 us, this 406.)
+// kPieced: the query's factor first: codes times q stays in FP32's range, where pieces times a large key's scale
+// would not.
+template <int W, bool kPieced, bool kMasked>
+__device__ __forceinline__ void acc_columns(const uint32_t (&r)[W], const float* neg_lse, const float* factor, float f,
+                                            uint32_t mask, float (&sum)[4]) {
 #pragma unroll
   for (int i = 0; i < W; i += 4) {
     const float4 l = *reinterpret_cast<const float4*>(neg_lse + i);
     float s0 = __uint_as_float(r[i]), s1 = __uint_as_float(r[i + 1]), s2 = __uint_as_float(r[i + 2]), s3 = __uint_as_float(r[i + 3]);
     if constexpr (kPieced) {
-      // the query's factor first: codes times q stays in FP32's range, where pieces times a large key's scale would not
-      const float4 f = *reinterpret_cast<const float4*>(factor + i);
-      mul2(s0, s1, s0, s1, f.x, f.y);
-      mul2(s2, s3, s2, s3, f.z, f.w);
-      fma2(s0, s1, s0, s1, key_scale, key_scale, l.x, l.y);
-      fma2(s2, s3, s2, s3, key_scale, key_scale, l.z, l.w);
-    } else {
-      if constexpr (kScaled) {
-        mul2(s0, s1, s0, s1, key_scale, key_scale);
-        mul2(s2, s3, s2, s3, key_scale, key_scale);
-      }
-      fma2(s0, s1, s0, s1, scale, scale, l.x, l.y);
-      fma2(s2, s3, s2, s3, scale, scale, l.z, l.w);
+      const float4 y = *reinterpret_cast<const float4*>(factor + i);
+      mul2(s0, s1, s0, s1, y.x, y.y);
+      mul2(s2, s3, s2, s3, y.z, y.w);
     }
-    mul2(s0, s1, s0, s1, kLog2e, kLog2e);
-    mul2(s2, s3, s2, s3, kLog2e, kLog2e);
+    fma2(s0, s1, s0, s1, f, f, l.x, l.y);
+    fma2(s2, s3, s2, s3, f, f, l.z, l.w);
     float e0 = ex2_approx(s0), e1 = ex2_approx(s1), e2 = ex2_approx(s2), e3 = ex2_approx(s3);
     if constexpr (kMasked) {
       e0 = mask >> i & 1 ? e0 : 0.f;
@@ -543,8 +536,10 @@ __global__ void __launch_bounds__(AccCfg<D, kFp8, N>::kThreads, AccCfg<D, kFp8, 
 #pragma unroll
           for (int e = 0; e < kPer; ++e)
             if (e * 32 + lane < N) {
-              col[e * 32 + lane] = neg[x][e] == -INFINITY ? -INFINITY : -neg[x][e];
-              if constexpr (C::kPieced) col[N + e * 32 + lane] = p.scale * factor[x][e];
+              // -lse log2(e), the constant in two parts: its rounding would be the same for all
+              const float l = neg[x][e];
+              col[e * 32 + lane] = isinf(l) ? -INFINITY : -fmaf(l, kLog2e, l * kLog2eRest);
+              if constexpr (C::kPieced) col[N + e * 32 + lane] = g.scale_log2 * factor[x][e];
             }
           mbar_arrive(&sh.col_full[s]);
           ++n;
@@ -640,7 +635,8 @@ __global__ void __launch_bounds__(AccCfg<D, kFp8, N>::kThreads, AccCfg<D, kFp8, 
       if (!(ok = wait(&sh.side_full[x], nu, C::kSideStages))) break;
       const int page = reinterpret_cast<const int*>(side + C::kSideBytes - 64)[row >> box_shift];
       const float old = reinterpret_cast<const float*>(side)[row];
-      const float key_scale = kFp8 ? reinterpret_cast<const float*>(side)[kAccKeys + row] : 0.f;
+      const float key_scale = kFp8 ? reinterpret_cast<const float*>(side)[kAccKeys + row] : 1.f;
+      const float f = C::kPieced ? key_scale : key_scale * g.scale_log2;   // (a power of two: exact)
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.side_empty[x]);
       const bool active = cur.tile(t);
@@ -674,7 +670,7 @@ __global__ void __launch_bounds__(AccCfg<D, kFp8, N>::kThreads, AccCfg<D, kFp8, 
               tmem_ld_wait();
               reg_fence(r);
               if (c + 1 == kCols / 32) give(buf);
-              acc_columns<32, false, kFp8, false>(r, col + c * 32, nullptr, p.scale, key_scale, 0, sum);
+              acc_columns<32, false, false>(r, col + c * 32, nullptr, f, 0, sum);
               if (c + 1 < kCols / 32) tmem_ld32(tS + buf * C::kBufCols + (c + 1) * 32, r);
             }
             total += (sum[0] + sum[1]) + (sum[2] + sum[3]);
@@ -725,8 +721,7 @@ __global__ void __launch_bounds__(AccCfg<D, kFp8, N>::kThreads, AccCfg<D, kFp8, 
               tmem_ld_wait();
               reg_fence(r);
             }
-            acc_columns<W, C::kPieced, kFp8, true>(r, col + c0, col + N + c0, p.scale, key_scale,
-                                                   low_bits(hi - c0) & ~low_bits(lo - c0), sum);
+            acc_columns<W, C::kPieced, true>(r, col + c0, col + N + c0, f, low_bits(hi - c0) & ~low_bits(lo - c0), sum);
           }
           give(buf);
           ++ns;
@@ -1021,11 +1016,15 @@ extern "C" int fa_kv_accumulate(const fa_paged_kv* kv, float* weights, int64_t w
   p.T = T;
   p.Hq = Hq;
   p.group = Hq / kv->Hkv;
+  const int columns = paged::columns_of(max_q, p.group);
   p.max_rows = (int)((long long)max_q * p.group < INT32_MAX ? max_q * p.group : INT32_MAX);
   p.window = window >= max_kv ? 0 : window;
   p.sinks = std::min(sinks, max_kv);
-  p.scale = scale;
-  p.scale_log2 = scale * 1.4426950408889634f;
+  // The tensor core cuts a sum to FP32 after every 16 products instead of rounding it: half a unit of the last place
+  // each time, 0.36 2^-23 of the sum so far on average, which grows evenly.  (Weights of 2048 tokens over 34k keys were low
+  // by 7.7e-7 on average.)
+  const double cut = fp8 && columns != 128 ? 0 : (kv->d / 16 + 1) / 2. * 0.36 * 0x1p-23;
+  g.scale_log2 = (float)(scale * 1.4426950408889634 * (1 + cut));
 #ifdef FA_TEST_HOOKS
   const char* inject = getenv("FA_TEST_INJECT_STALL");
   p.inject_stall = (inject && inject[0] == '1') ? 1 : 0;
@@ -1035,7 +1034,6 @@ extern "C" int fa_kv_accumulate(const fa_paged_kv* kv, float* weights, int64_t w
   g.weight_stride = weight_stride;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int d = kv->d, box = kv->page_size < paged::kAccTile ? kv->page_size : paged::kAccTile;
-  const int columns = paged::columns_of(max_q, p.group);
   const bool chunk = columns == 128;
   g.max_parts = chunk ? paged::parts_of(max_q, p.group) : 1;
   g.part = static_cast<float*>(workspace);
