@@ -12,8 +12,8 @@
 //     queries stay in shared memory; a ring of K tiles is kept full.  64 sequences, 284k keys, 8 kv heads of 128:
 //     E4M3 55 us (85 % of the copy rate), BF16 95 us (93 %).
 //   * chunks: 256 x 128 pairs of a head take 1024 clocks of tensor work, and as many for their exponentials (32 a clock
-//     and SM); both together, with the sums between them, bound it.  2048 tokens over 34k keys, 32 heads of 128: 406 us,
-//     1364 TFLOP/s (without the products 367, without the exponentials 367, with neither 266).  Units are dealt round by
+//     and SM); both together, with the sums between them, bound it.  2048 tokens over 34k keys, 32 heads of 128: 390 us,
+//     1420 TFLOP/s (without the products 339).  Units are dealt round by
 //     round, early keys, which most tokens see, first.  Where there are few of them each is cut into parts by its
 //     query blocks, whose sums a second kernel joins in order.
 // E4M3 caches, few rows: the codes are the operand as they are (kind::f8f6f4).  A query vector goes into three E5M2
@@ -57,8 +57,9 @@ struct AccCfg {
   // the pieces side by side, 3 N columns of S that are added afterwards: the tensor core then reads K once.  (64
   // columns leave no room for that: S takes the pieces one after the other.)
   static constexpr bool kWide = kPieced && N <= 32;
-  // chunks: two warps share a block's columns, 64 each, and add their sums at the end of a unit (2048 tokens over 34k keys
-  // 406 us, with one 423).  Not with converters beside them: 80 registers are too few (466 us, 431).
+  // chunks: two sets of warps take the blocks in turn, the one with an even place (of its tile) the first buffer of S, the
+  // other the second, and add their sums at the end of a unit.  2048 tokens over 34k keys 390 us; two sets with half
+  // of each block's columns 406, one set 423.  Not with converters beside them: 80 registers are too few (466 us, 431).
   static constexpr int kHalves = kChunk && !kConvert ? 2 : 1;
   static constexpr int kSumWarps = 8 * kHalves, kThreads = 32 * (kSumWarps + (kConvert ? 8 : 4));
   // CTAs on an SM: two where each holds three units' keys or more.  (A unit's hand-offs take longer than its 16 or 32 KB:
@@ -77,7 +78,7 @@ struct AccCfg {
   static constexpr int kSideBytes = kAccKeys * 4 * (kFp8 ? 2 : 1) + 64;  // a unit's weights, scales and pages
   static constexpr int kQOff = 0;
   static constexpr int kCodeOff = kQOff + kQStages * kQBytes, kKOff = kCodeOff + kCodeBytes;
-  static constexpr int kHalfBytes = kHalves == 2 ? 2 * kAccKeys * 4 : 0; // two units' sums over the second half
+  static constexpr int kHalfBytes = kHalves == 2 ? 2 * kAccKeys * 4 : 0; // two units' sums of the second set
   static constexpr int kRest = kColStages * kColBytes + kSideStages * kSideBytes + kHalfBytes;
   static constexpr int kRoom = (kCtas == 2 ? 112 : 226) * 1024 - kKOff - kRest;
   static constexpr int kKStages = kRoom / kPairBytes < 6 ? kRoom / kPairBytes : 6;
@@ -100,7 +101,7 @@ struct AccShared {
   uint64_t col_full[kColStages], col_empty[kColStages], side_full[kMaxSideStages], side_empty[kMaxSideStages];
   uint64_t s_full[2][kMaxBufs], s_empty[2][kMaxBufs];
   uint64_t code_full, code_empty;  // E4M3 chunks: a unit's codes have landed / have been read
-  uint64_t half_full[2][2], half_empty[2][2];  // sums over the second half of the columns: by tile, two units'
+  uint64_t half_full[2][2], half_empty[2][2];  // sums of the second set of warps: by tile, two units'
   uint64_t mma_done;
   uint64_t never;                  // test builds only: a barrier nothing arrives on
   long long scan[kMaxWarps];
@@ -354,7 +355,7 @@ __global__ void __launch_bounds__(AccCfg<D, kFp8, N>::kThreads, AccCfg<D, kFp8, 
     }
     for (int s = 0; s < kColStages; ++s) {
       mbar_init(&sh.col_full[s], 32);
-      mbar_init(&sh.col_empty[s], C::kSumWarps);
+      mbar_init(&sh.col_empty[s], 8);    // four warps for each tile
     }
     for (int s = 0; s < C::kSideStages; ++s) {
       mbar_init(&sh.side_full[s], 32);  // the loading warp's lanes (pages), one of them with the expected bytes
@@ -363,7 +364,7 @@ __global__ void __launch_bounds__(AccCfg<D, kFp8, N>::kThreads, AccCfg<D, kFp8, 
     for (int t = 0; t < 2; ++t)
       for (int s = 0; s < C::kBufs; ++s) {
         mbar_init(&sh.s_full[t][s], 1);
-        mbar_init(&sh.s_empty[t][s], 4 * C::kHalves);
+        mbar_init(&sh.s_empty[t][s], 4);
       }
     for (int t = 0; t < 2; ++t)
       for (int s = 0; s < 2; ++s) {
@@ -610,11 +611,10 @@ __global__ void __launch_bounds__(AccCfg<D, kFp8, N>::kThreads, AccCfg<D, kFp8, 
       }
     }
   } else if (warp < C::kSumWarps) {
-    // ------------------------------------------------------------ exponentials and sums: a thread (or two) per key
-    constexpr int kCols = N / C::kHalves;            // of a block, from col0 on: what this warp sums
-    const int t = warp / (4 * C::kHalves), half = warp / 4 % C::kHalves, col0 = half * kCols;
+    // ------------------------------------------------------------ exponentials and sums: a thread (chunks: two) per key
+    const int t = warp / (4 * C::kHalves), half = warp / 4 % C::kHalves;
     const int row = t * kAccTile + (warp % 4) * 32 + lane;   // the thread's key within a unit
-    const uint32_t tS = tmem + t * C::kBufs * C::kBufCols + col0 + ((uint32_t)((warp % 4) * 32) << 16);
+    const uint32_t tS = tmem + t * C::kBufs * C::kBufCols + ((uint32_t)((warp % 4) * 32) << 16);
     int nq = 0, ns = 0, nu = 0;
     long long number = blockIdx.x;                   // chunks: of the part in the launch
     bool ok = true;
@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(AccCfg<D, kFp8, N>::kThreads, AccCfg<D, kFp8, 
       if (lane == 0) mbar_arrive(&sh.s_empty[t][buf]);
     };
     auto columns = [&](int n) {
-      return reinterpret_cast<const float*>(smem + C::kColOff + n % kColStages * C::kColBytes) + col0;
+      return reinterpret_cast<const float*>(smem + C::kColOff + n % kColStages * C::kColBytes);
     };
     for (; ok && cur.valid(p); cur.next(p, parts), ++nu, number += gridDim.x) {
       const int x = nu % C::kSideStages;
@@ -657,6 +657,7 @@ __global__ void __launch_bounds__(AccCfg<D, kFp8, N>::kThreads, AccCfg<D, kFp8, 
       while (i < last) {
         if (C::kChunk && i >= i_all && i < last_all) {
           for (; i < last_all; ++i, ++nq, ++ns) {
+            if (C::kHalves == 2 && ns % 2 != half) continue;   // the other set's
             const int buf = ns % C::kBufs;
             const float* col = columns(nq);
             if (!(ok = wait(&sh.s_full[t][buf], ns, C::kBufs))) break;
@@ -666,12 +667,12 @@ __global__ void __launch_bounds__(AccCfg<D, kFp8, N>::kThreads, AccCfg<D, kFp8, 
             if (!(ok = wait(&sh.col_full[nq % kColStages], nq, kColStages))) break;
             float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int c = 0; c < kCols / 32; ++c) {
+            for (int c = 0; c < N / 32; ++c) {
               tmem_ld_wait();
               reg_fence(r);
-              if (c + 1 == kCols / 32) give(buf);
+              if (c + 1 == N / 32) give(buf);
               acc_columns<32, false, false>(r, col + c * 32, nullptr, f, 0, sum);
-              if (c + 1 < kCols / 32) tmem_ld32(tS + buf * C::kBufCols + (c + 1) * 32, r);
+              if (c + 1 < N / 32) tmem_ld32(tS + buf * C::kBufCols + (c + 1) * 32, r);
             }
             total += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             __syncwarp();
@@ -681,6 +682,12 @@ __global__ void __launch_bounds__(AccCfg<D, kFp8, N>::kThreads, AccCfg<D, kFp8, 
           if (!ok) break;
           continue;
         }
+        if (C::kHalves == 2 && (active ? ns % 2 : 0) != half) {   // (a tile without keys: the first set's)
+          ns += active;
+          ++nq;
+          ++i;
+          continue;
+        }
         if ((C::kChunk || cur.fresh) && !(ok = wait(&sh.col_full[nq % kColStages], nq, kColStages))) break;
         if (active) {
           const int buf = ns % C::kBufs;
@@ -688,15 +695,15 @@ __global__ void __launch_bounds__(AccCfg<D, kFp8, N>::kThreads, AccCfg<D, kFp8, 
           tc_fence_after();
           // the rows that see the key: its own token's on, up to the last one whose window holds it
           const int t0 = i * tokens, here = min(cur.s.n - t0, tokens);
-          const int lo = min(max(ahead - t0, 0), here) * p.group - col0;
+          const int lo = min(max(ahead - t0, 0), here) * p.group;
           int end = here;
           if (p.window && key >= p.sinks) end = (int)min((long long)here, max((long long)ahead + p.window - t0, 0ll));
-          const int hi = end * p.group - col0;
+          const int hi = end * p.group;
           const float* col = columns(nq);
           const uint32_t at = tS + buf * C::kBufCols;
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int c0 = 0; c0 < kCols; c0 += W) {
+          for (int c0 = 0; c0 < N; c0 += W) {
             if (__all_sync(0xffffffffu, hi <= c0 || lo >= c0 + W)) continue;
             uint32_t r[W];
             auto get = [&](uint32_t (&to)[W], int c) {
@@ -736,7 +743,7 @@ __global__ void __launch_bounds__(AccCfg<D, kFp8, N>::kThreads, AccCfg<D, kFp8, 
         ++i;
       }
       if constexpr (C::kHalves == 2) {
-        // the second half's sums go to the first half's threads
+        // the second set's sums go to the first
         if (!ok) break;
         const int y = nu % 2;
         float* sums = reinterpret_cast<float*>(smem + C::kHalfOff) + y * kAccKeys;
