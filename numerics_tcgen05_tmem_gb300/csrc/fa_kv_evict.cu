@@ -6,9 +6,10 @@
 //   select  a CTA per (sequence, kv head): the smallest weight that stays, by three passes over the weights' bits
 //           (11, 11 and 10 of them, a histogram each in shared memory), then one pass in order that writes the
 //           kept positions.
-//   move    the kept vectors, their scales and weights: bandwidth work, 16 bytes a thread.
-// Measured: 64 sequences of 4.4k keys, 8 heads of 128, cut to 2000 in other pages, E4M3 105 us (66 at the copy rate;
-// the selection 27, whose longest sequence the first moves wait for), BF16 158; one sequence of 4.5k to 2k 12 us.
+//   move    the kept vectors, their scales and weights: bandwidth work, 16 bytes a thread; by the selecting CTAs or in a
+//           launch of its own.
+// Measured: 64 sequences of 4.4k keys on average, 8 heads of 128, cut to 2000 in other pages, E4M3 93 us (66 at the
+// copy rate; the selection alone takes 29, for its longest sequence), BF16 158; one sequence of 4.5k to 2k 12 us.
 // In place a vector only ever moves to a lower position, to where nothing is that is still to be read as long
 // as the vectors are taken in order: a CTA takes all of one head's K or V, 64 (or 32) bytes wide, step by step,
 // and waits between a step's loads and its stores.
@@ -50,18 +51,84 @@ __device__ __forceinline__ int evict_length(const Cache& c, int b) {
   return n;
 }
 
+// Where a key lies: its page and its offset within a page's head; page -1, recorded, where there is none.
+struct Spot {
+  int page, slot;
+};
+__device__ __forceinline__ Spot spot_of(const Cache& c, const int32_t* table, long long stride, int max_pages, int b, int key) {
+  const int i = key >> c.page_shift;
+  Spot s{-1, key & ((1 << c.page_shift) - 1)};
+  if (key < 0 || i >= max_pages) {
+    report_bounds(c.status, kSitePagedEvict, key);
+    return s;
+  }
+  s.page = __ldg(table + b * stride + i);
+  if (s.page < 0 || s.page >= c.num_pages) {
+    report_bounds(c.status, kSitePagedEvict, s.page);
+    s.page = -1;
+  }
+  return s;
+}
+
+// The kept keys first .. first + here - 1 of a (sequence, kv head), at most kVecs, to their places in table_out: a lane of the
+// warp looks one up and moves its scales and weight, then kRow / 16 lanes move a vector, kMost loads of a lane in flight.
+template <int kRow, int kVecs, int kMost>    // kRow: bytes of a vector
+__device__ __forceinline__ void move_keys(const Evict& g, int item, int first, int here) {
+  constexpr int kLanes = kRow / 16, kGroups = 32 / kLanes, kSteps = kVecs / kGroups;
+  constexpr int kUnroll = 2 * kSteps < kMost ? 2 * kSteps : kMost;
+  static_assert(2 * kSteps % kUnroll == 0, "K and V in whole rounds");
+  const int lane = threadIdx.x % 32;
+  const int b = item / g.c.Hkv, h = item - b * g.c.Hkv;
+  const long long page_size = 1ll << g.c.page_shift;
+  const int elem = g.c.k_scale != nullptr ? 1 : 2;
+  long long from = -1, to = -1;       // the lane's vector: bytes from the pool's start
+  if (lane < here) {
+    const Spot f = spot_of(g.c, g.c.table, g.c.table_stride, g.c.max_pages, b, g.kept[(long long)item * g.keep + first + lane]);
+    const Spot t = spot_of(g.c, g.table_out, g.table_out_stride, g.max_pages_out, b, first + lane);
+    if (f.page >= 0 && t.page >= 0) {
+      const long long f_at = h * page_size + f.slot, t_at = h * page_size + t.slot;
+      from = f.page * g.c.page_stride * elem + f_at * kRow;
+      to = t.page * g.c.page_stride * elem + t_at * kRow;
+      g.weights[t.page * g.weight_stride + t_at] = g.weights[f.page * g.weight_stride + f_at];
+      if (g.c.k_scale != nullptr) {
+        const long long f_s = f.page * g.c.scale_stride + f_at, t_s = t.page * g.c.scale_stride + t_at;
+        const float ks = g.c.k_scale[f_s], vs = g.c.v_scale[f_s];
+        g.c.k_scale[t_s] = ks;
+        g.c.v_scale[t_s] = vs;
+      }
+    }
+  }
+  const int col = lane % kLanes * 16;
+#pragma unroll
+  for (int s0 = 0; s0 < 2 * kSteps; s0 += kUnroll) {
+    uint4 x[kUnroll];
+    long long dst[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int s = s0 + u, v = s / 2 * kGroups + lane / kLanes;      // K and V of the same vectors in turn
+      const long long src = __shfl_sync(0xffffffffu, from, v);
+      dst[u] = __shfl_sync(0xffffffffu, to, v);
+      if (dst[u] >= 0) x[u] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>((s & 1) ? g.c.v : g.c.k) + src + col);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      if (dst[u] >= 0) *reinterpret_cast<uint4*>(static_cast<uint8_t*>(((s0 + u) & 1) ? g.c.v : g.c.k) + dst[u] + col) = x[u];
+  }
+}
+
 // kCached weights stay in shared memory between the passes.  512 threads and 8192 weights, three CTAs on an SM beside
 // the moving kernel's first ones (with 16384: the selection 2 us faster, the call on 64 sequences of 4.4k keys 117 us
 // instead of 105); 1024 and 40960 for long sequences where there are fewer CTAs than two for each SM (one of 40k
 // keys: 49 us with the smaller form).
-template <int kSelectThreads, int kCached>
+// kRow > 0: the CTA also moves its keys, vectors of kRow bytes, into other pages, two loads of a lane in flight (40 registers).
+template <int kSelectThreads, int kCached, int kRow>
 __global__ void __launch_bounds__(kSelectThreads, 1536 / kSelectThreads) evict_select_kernel(const __grid_constant__ Evict g) {
   constexpr int kWarps = kSelectThreads / 32, kStep = 4 * kSelectThreads;   // a thread has four keys at a time
   extern __shared__ __align__(16) uint32_t cached[];
   __shared__ uint32_t bins[kBins];
   __shared__ int warp_sum[kWarps];
   __shared__ int found_bin, found_above;
-  cudaTriggerProgrammaticLaunchCompletion();   // the moving kernel may get ready; it waits for this one's end
+  cudaTriggerProgrammaticLaunchCompletion();   // a moving kernel may get ready; it waits for this one's end
   const int b = blockIdx.x / g.c.Hkv, h = blockIdx.x - b * g.c.Hkv;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int n = evict_length(g.c, b), kept = min(n, g.keep);
@@ -70,6 +137,11 @@ __global__ void __launch_bounds__(kSelectThreads, 1536 / kSelectThreads) evict_s
   for (int i = kept + (int)threadIdx.x; i < g.keep; i += kSelectThreads) out[i] = -1;
   if (n <= g.keep) {
     for (int i = threadIdx.x; i < n; i += kSelectThreads) out[i] = i;
+    if constexpr (kRow > 0) {
+      __syncthreads();
+      for (int first = 32 * warp; first < kept; first += 32 * kWarps)
+        move_keys<kRow, 32, 2>(g, blockIdx.x, first, min(kept - first, 32));
+    }
     return;
   }
   const int page_mask = (1 << g.c.page_shift) - 1;
@@ -203,79 +275,24 @@ __global__ void __launch_bounds__(kSelectThreads, 1536 / kSelectThreads) evict_s
     equal_before += all >> 16;
     __syncthreads();
   }
+  if constexpr (kRow > 0)
+    for (int first = 32 * warp; first < kept; first += 32 * kWarps)
+      move_keys<kRow, 32, 2>(g, blockIdx.x, first, min(kept - first, 32));
 }
 
-// Where a key lies: its page and its offset within a page's head; page -1, recorded, where there is none.
-struct Spot {
-  int page, slot;
-};
-__device__ __forceinline__ Spot spot_of(const Cache& c, const int32_t* table, long long stride, int max_pages, int b, int key) {
-  const int i = key >> c.page_shift;
-  Spot s{-1, key & ((1 << c.page_shift) - 1)};
-  if (key < 0 || i >= max_pages) {
-    report_bounds(c.status, kSitePagedEvict, key);
-    return s;
-  }
-  s.page = __ldg(table + b * stride + i);
-  if (s.page < 0 || s.page >= c.num_pages) {
-    report_bounds(c.status, kSitePagedEvict, s.page);
-    s.page = -1;
-  }
-  return s;
-}
-
-// Into other pages.  A warp has kVecs kept keys of one (sequence, kv head): a lane looks one up and moves its scales and
-// weight, then kRow / 16 lanes move a vector, eight loads of each lane in flight.  32 keys; 8 where that would
-// leave SMs with a few warps (one sequence cut from 4.5k keys to 2k: 14.2 us with 32, 12.0 with 8).
+// Into other pages: a warp has kVecs kept keys of one (sequence, kv head).  32 keys; 8 where that would leave SMs with a few
+// warps (one sequence cut from 4.5k keys to 2k: 14.2 us with 32, 12.0 with 8).
 constexpr int kMoveThreads = 256;
 
 template <int kRow, int kVecs>    // kRow: bytes of a vector
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ Evict g, int chunks, long long warps) {
-  constexpr int kLanes = kRow / 16, kGroups = 32 / kLanes, kSteps = kVecs / kGroups, kUnroll = 2 * kSteps < 8 ? 2 * kSteps : 8;
-  static_assert(2 * kSteps % kUnroll == 0, "K and V in whole rounds");
   cudaGridDependencySynchronize();
-  const int lane = threadIdx.x % 32;
   const long long w = (long long)blockIdx.x * (kMoveThreads / 32) + threadIdx.x / 32;
   if (w >= warps) return;
   const int item = (int)(w / chunks), first = (int)(w - (long long)item * chunks) * kVecs;
-  const int b = item / g.c.Hkv, h = item - b * g.c.Hkv;
-  const int here = min(g.kept_len[b] - first, kVecs);
+  const int here = min(g.kept_len[item / g.c.Hkv] - first, kVecs);
   if (here <= 0) return;
-  const long long page_size = 1ll << g.c.page_shift;
-  const int elem = g.c.k_scale != nullptr ? 1 : 2;
-  long long from = -1, to = -1;       // the lane's vector: bytes from the pool's start
-  if (lane < here) {
-    const Spot f = spot_of(g.c, g.c.table, g.c.table_stride, g.c.max_pages, b, g.kept[(long long)item * g.keep + first + lane]);
-    const Spot t = spot_of(g.c, g.table_out, g.table_out_stride, g.max_pages_out, b, first + lane);
-    if (f.page >= 0 && t.page >= 0) {
-      const long long f_at = h * page_size + f.slot, t_at = h * page_size + t.slot;
-      from = f.page * g.c.page_stride * elem + f_at * kRow;
-      to = t.page * g.c.page_stride * elem + t_at * kRow;
-      g.weights[t.page * g.weight_stride + t_at] = g.weights[f.page * g.weight_stride + f_at];
-      if (g.c.k_scale != nullptr) {
-        const long long f_s = f.page * g.c.scale_stride + f_at, t_s = t.page * g.c.scale_stride + t_at;
-        const float ks = g.c.k_scale[f_s], vs = g.c.v_scale[f_s];
-        g.c.k_scale[t_s] = ks;
-        g.c.v_scale[t_s] = vs;
-      }
-    }
-  }
-  const int col = lane % kLanes * 16;
-#pragma unroll
-  for (int s0 = 0; s0 < 2 * kSteps; s0 += kUnroll) {
-    uint4 x[kUnroll];
-    long long dst[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int s = s0 + u, v = s / 2 * kGroups + lane / kLanes;      // K and V of the same vectors in turn
-      const long long src = __shfl_sync(0xffffffffu, from, v);
-      dst[u] = __shfl_sync(0xffffffffu, to, v);
-      if (dst[u] >= 0) x[u] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>((s & 1) ? g.c.v : g.c.k) + src + col);
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      if (dst[u] >= 0) *reinterpret_cast<uint4*>(static_cast<uint8_t*>(((s0 + u) & 1) ? g.c.v : g.c.k) + dst[u] + col) = x[u];
-  }
+  move_keys<kRow, kVecs, 8>(g, item, first, here);
 }
 
 // Within the same pages.  A CTA has one (sequence, kv head), K or V, kSlice bytes of each vector; the first slice's
@@ -385,15 +402,22 @@ extern "C" int fa_kv_evict(const fa_paged_kv* kv, float* weights, int64_t weight
   g.kept_len = kept_len;
   g.kept = kept;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const bool wide = items < 2ll * sm_count() && max_kv > 16384;
-  const int cache = (wide ? 40960 : 8192) * 4;
-  auto select = wide ? paged::evict_select_kernel<1024, 40960> : paged::evict_select_kernel<512, 8192>;
-  static std::atomic<uint64_t> prepared[2];
-  if ((rc = prepare_kernel(reinterpret_cast<const void*>(select), cache, wide ? 1024 : 512, 0, "evict_select_kernel", &prepared[wide])))
-    return rc;
-  select<<<(unsigned)items, wide ? 1024 : 512, cache, s>>>(g);
-  if ((rc = check_cuda(cudaGetLastError(), "launch evict_select_kernel"))) return rc;
+  // One launch where there are CTAs enough to fill the SMs: a CTA moves its own keys, while others still select.  64 sequences,
+  // 8 heads, to 2000 keys, E4M3: of 0.5k to 16k keys 106 -> 93 us, to 500 keys 57 -> 45; of 4.4k each, where 512 CTAs are a
+  // ninth more than run at once, 116 -> 121.  Vectors of 256 bytes: 158 -> 154 and 182 -> 200, not taken.
   const int row = kv->d * (kv->dtype == FA_KV_E4M3 ? 1 : 2);
+  const bool many = items >= 2ll * sm_count(), own = many && !in_place && row <= 128, wide = !many && max_kv > 16384;
+  const int cache = (wide ? 40960 : 8192) * 4, threads = wide ? 1024 : 512;
+  auto select = wide              ? paged::evict_select_kernel<1024, 40960, 0>
+                : !own            ? paged::evict_select_kernel<512, 8192, 0>
+                : row == 64       ? paged::evict_select_kernel<512, 8192, 64>
+                                  : paged::evict_select_kernel<512, 8192, 128>;
+  static std::atomic<uint64_t> prepared[4];
+  if ((rc = prepare_kernel(reinterpret_cast<const void*>(select), cache, threads, 0, "evict_select_kernel",
+                           &prepared[wide ? 0 : !own ? 1 : row == 64 ? 2 : 3])))
+    return rc;
+  select<<<(unsigned)items, threads, cache, s>>>(g);
+  if ((rc = check_cuda(cudaGetLastError(), "launch evict_select_kernel")) || own) return rc;
   const long long warps = items * chunks, per = paged::kMoveThreads / 32;
   cudaLaunchConfig_t cfg{};
   // in place: 64 bytes of a vector, 32 where that leaves SMs without a CTA

@@ -177,6 +177,22 @@ def test_many_sequences(in_place):
         assert torch.equal(bits(x), bits(y))
 
 
+@pytest.mark.parametrize("fmt,d,in_place", [("e4m3", 128, False), ("e4m3", 64, False), ("bf16", 64, False), ("bf16", 128, False),
+                                            ("e4m3", 64, True)])
+def test_more_heads_of_sequences_than_run_at_once(fmt, d, in_place):
+    # more than two (sequence, kv head) pairs for each SM, the longest past what is kept on chip
+    lens = [700, 8900, 64, 0, 1, 65, 101, 32] + torch.randint(0, 150, (102,), generator=torch.Generator().manual_seed(d)).tolist()
+    c = P.make(lens, 3, d, 32, fmt, seed=d, spare=3 + sum(-(-min(n, 100) // 32) for n in lens))
+    w = W.make(c, seed=d)[0].cuda()
+    table_out = c.table if in_place else free_table(c, 100).cuda()
+    after, want_len, want_kept = expected(c, w, table_out, 100, 4, 33)
+    kept_len, kept = binding.kv_evict(w, c.k, c.v, c.table, c.kv_len, 100, sinks=4, recent=33, table_out=table_out, k_scale=c.ks, v_scale=c.vs)
+    binding.device_status()
+    assert torch.equal(kept_len.cpu(), want_len) and torch.equal(kept.cpu(), want_kept)
+    for x, y in zip(pools(c, w), after):
+        assert torch.equal(bits(x), bits(y))
+
+
 def test_source_pages_may_be_shared():
     # two sequences over the same pages, each moved to pages of its own
     c = P.make([200, 200], 2, 64, 16, "bf16", seed=6, spare=30)
