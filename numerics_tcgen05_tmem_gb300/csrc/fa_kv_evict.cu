@@ -8,8 +8,8 @@
 //           kept positions.
 //   move    the kept vectors, their scales and weights: bandwidth work, 16 bytes a thread; by the selecting CTAs or in a
 //           launch of its own.
-// Measured: 64 sequences of 4.4k keys on average, 8 heads of 128, cut to 2000 in other pages, E4M3 93 us (66 at the
-// copy rate; the selection alone takes 29, for its longest sequence), BF16 158; one sequence of 4.5k to 2k 12 us.
+// Measured: 64 sequences of 4.4k keys on average, 8 heads of 128, cut to 2000 in other pages, E4M3 90 us (66 at the
+// copy rate; the selection alone takes 29, for its longest sequence), BF16 157; one sequence of 4.5k to 2k 12 us.
 // In place a vector only ever moves to a lower position, to where nothing is that is still to be read as long
 // as the vectors are taken in order: a CTA takes all of one head's K or V, 64 (or 32) bytes wide, step by step,
 // and waits between a step's loads and its stores.
@@ -102,17 +102,20 @@ __device__ __forceinline__ void move_keys(const Evict& g, int item, int first, i
 #pragma unroll
   for (int s0 = 0; s0 < 2 * kSteps; s0 += kUnroll) {
     uint4 x[kUnroll];
-    long long dst[kUnroll];
+    bool moves[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int s = s0 + u, v = s / 2 * kGroups + lane / kLanes;      // K and V of the same vectors in turn
       const long long src = __shfl_sync(0xffffffffu, from, v);
-      dst[u] = __shfl_sync(0xffffffffu, to, v);
-      if (dst[u] >= 0) x[u] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>((s & 1) ? g.c.v : g.c.k) + src + col);
+      moves[u] = src >= 0;
+      if (moves[u]) x[u] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>((s & 1) ? g.c.v : g.c.k) + src + col);
     }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      if (dst[u] >= 0) *reinterpret_cast<uint4*>(static_cast<uint8_t*>(((s0 + u) & 1) ? g.c.v : g.c.k) + dst[u] + col) = x[u];
+    for (int u = 0; u < kUnroll; ++u) {
+      const int s = s0 + u;
+      const long long dst = __shfl_sync(0xffffffffu, to, s / 2 * kGroups + lane / kLanes);
+      if (moves[u]) *reinterpret_cast<uint4*>(static_cast<uint8_t*>((s & 1) ? g.c.v : g.c.k) + dst + col) = x[u];
+    }
   }
 }
 
@@ -120,7 +123,8 @@ __device__ __forceinline__ void move_keys(const Evict& g, int item, int first, i
 // the moving kernel's first ones (with 16384: the selection 2 us faster, the call on 64 sequences of 4.4k keys 117 us
 // instead of 105); 1024 and 40960 for long sequences where there are fewer CTAs than two for each SM (one of 40k
 // keys: 49 us with the smaller form).
-// kRow > 0: the CTA also moves its keys, vectors of kRow bytes, into other pages, two loads of a lane in flight (40 registers).
+// kRow > 0: the CTA also moves its keys, vectors of kRow bytes, into other pages, two loads of a lane in flight (40 registers;
+// four spill: 99 us where two take 90).
 template <int kSelectThreads, int kCached, int kRow>
 __global__ void __launch_bounds__(kSelectThreads, 1536 / kSelectThreads) evict_select_kernel(const __grid_constant__ Evict g) {
   constexpr int kWarps = kSelectThreads / 32, kStep = 4 * kSelectThreads;   // a thread has four keys at a time
@@ -403,8 +407,8 @@ extern "C" int fa_kv_evict(const fa_paged_kv* kv, float* weights, int64_t weight
   g.kept = kept;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // One launch where there are CTAs enough to fill the SMs: a CTA moves its own keys, while others still select.  64 sequences,
-  // 8 heads, to 2000 keys, E4M3: of 0.5k to 16k keys 106 -> 93 us, to 500 keys 57 -> 45; of 4.4k each, where 512 CTAs are a
-  // ninth more than run at once, 116 -> 121.  Vectors of 256 bytes: 158 -> 154 and 182 -> 200, not taken.
+  // 8 heads, to 2000 keys, E4M3: of 0.5k to 16k keys 106 -> 90 us, to 500 keys 57 -> 44; of 4.4k each, where 512 CTAs are a
+  // ninth more than run at once, 116 -> 118.  Vectors of 256 bytes: 158 -> 154 and 182 -> 200, not taken.
   const int row = kv->d * (kv->dtype == FA_KV_E4M3 ? 1 : 2);
   const bool many = items >= 2ll * sm_count(), own = many && !in_place && row <= 128, wide = !many && max_kv > 16384;
   const int cache = (wide ? 40960 : 8192) * 4, threads = wide ? 1024 : 512;
