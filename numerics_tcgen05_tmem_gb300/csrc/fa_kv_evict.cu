@@ -8,8 +8,8 @@
 //           kept positions.
 //   move    the kept vectors, their scales and weights: bandwidth work, 16 bytes a thread; by the selecting CTAs or in a
 //           launch of its own.
-// Measured: 64 sequences of 4.4k keys on average, 8 heads of 128, cut to 2000 in other pages, E4M3 90 us (66 at the
-// copy rate; the selection alone takes 29, for its longest sequence), BF16 157; one sequence of 4.5k to 2k 12 us.
+// Measured: 64 sequences of 4.4k keys on average, 8 heads of 128, cut to 2000 in other pages, E4M3 87 us (66 at the
+// copy rate; the selection alone takes 29, for its longest sequence), BF16 145; one sequence of 4.5k to 2k 12 us.
 // In place a vector only ever moves to a lower position, to where nothing is that is still to be read as long
 // as the vectors are taken in order: a CTA takes all of one head's K or V, 64 (or 32) bytes wide, step by step,
 // and waits between a step's loads and its stores.
@@ -123,20 +123,43 @@ __device__ __forceinline__ void move_keys(const Evict& g, int item, int first, i
 // the moving kernel's first ones (with 16384: the selection 2 us faster, the call on 64 sequences of 4.4k keys 117 us
 // instead of 105); 1024 and 40960 for long sequences where there are fewer CTAs than two for each SM (one of 40k
 // keys: 49 us with the smaller form).
-// kRow > 0: the CTA also moves its keys, vectors of kRow bytes, into other pages, two loads of a lane in flight (40 registers;
-// four spill: 99 us where two take 90).
+// kRow > 0: the CTA also moves its keys, vectors of kRow bytes, into other pages.  Two CTAs on an SM, four loads of a lane in
+// flight (three and two: 90 us where these take 87; 256 threads 112).  The longest sequences, of kMostSorted at most,
+// come first, so that the CTAs that start last have little to do (64 of 0.5k to 16k keys: 101 -> 87 us).
+constexpr int kMostSorted = 256;
+
 template <int kSelectThreads, int kCached, int kRow>
-__global__ void __launch_bounds__(kSelectThreads, 1536 / kSelectThreads) evict_select_kernel(const __grid_constant__ Evict g) {
+__global__ void __launch_bounds__(kSelectThreads, kRow > 0 ? 2 : 1536 / kSelectThreads)
+    evict_select_kernel(const __grid_constant__ Evict g) {
   constexpr int kWarps = kSelectThreads / 32, kStep = 4 * kSelectThreads;   // a thread has four keys at a time
   extern __shared__ __align__(16) uint32_t cached[];
   __shared__ uint32_t bins[kBins];
   __shared__ int warp_sum[kWarps];
   __shared__ int found_bin, found_above;
   cudaTriggerProgrammaticLaunchCompletion();   // a moving kernel may get ready; it waits for this one's end
-  const int b = blockIdx.x / g.c.Hkv, h = blockIdx.x - b * g.c.Hkv;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  int b = blockIdx.x / g.c.Hkv;
+  const int h = blockIdx.x - b * g.c.Hkv;
+  if constexpr (kRow > 0) {
+    // the sequence that comes in this place
+    __shared__ int place;
+    if (g.c.B <= kMostSorted) {
+      int* len = reinterpret_cast<int*>(cached);
+      for (int i = threadIdx.x; i < g.c.B; i += kSelectThreads) len[i] = __ldg(g.c.kv_len + i);
+      __syncthreads();
+      for (int i = threadIdx.x; i < g.c.B; i += kSelectThreads) {
+        const int mine = len[i];
+        int before = 0;
+        for (int x = 0; x < g.c.B; ++x) before += len[x] > mine || (len[x] == mine && x < i) ? 1 : 0;
+        if (before == b) place = i;
+      }
+      __syncthreads();
+      b = place;
+    }
+  }
+  const int item = b * g.c.Hkv + h;
   const int n = evict_length(g.c, b), kept = min(n, g.keep);
-  int32_t* out = g.kept + (long long)blockIdx.x * g.keep;
+  int32_t* out = g.kept + (long long)item * g.keep;
   if (h == 0 && threadIdx.x == 0) g.kept_len[b] = kept;
   for (int i = kept + (int)threadIdx.x; i < g.keep; i += kSelectThreads) out[i] = -1;
   if (n <= g.keep) {
@@ -144,7 +167,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1536 / kSelectThreads) evict_s
     if constexpr (kRow > 0) {
       __syncthreads();
       for (int first = 32 * warp; first < kept; first += 32 * kWarps)
-        move_keys<kRow, 32, 2>(g, blockIdx.x, first, min(kept - first, 32));
+        move_keys<kRow, 32, 4>(g, item, first, min(kept - first, 32));
     }
     return;
   }
@@ -281,7 +304,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1536 / kSelectThreads) evict_s
   }
   if constexpr (kRow > 0)
     for (int first = 32 * warp; first < kept; first += 32 * kWarps)
-      move_keys<kRow, 32, 2>(g, blockIdx.x, first, min(kept - first, 32));
+      move_keys<kRow, 32, 4>(g, item, first, min(kept - first, 32));
 }
 
 // Into other pages: a warp has kVecs kept keys of one (sequence, kv head).  32 keys; 8 where that would leave SMs with a few
@@ -406,19 +429,21 @@ extern "C" int fa_kv_evict(const fa_paged_kv* kv, float* weights, int64_t weight
   g.kept_len = kept_len;
   g.kept = kept;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  // One launch where there are CTAs enough to fill the SMs: a CTA moves its own keys, while others still select.  64 sequences,
-  // 8 heads, to 2000 keys, E4M3: of 0.5k to 16k keys 106 -> 90 us, to 500 keys 57 -> 44; of 4.4k each, where 512 CTAs are a
-  // ninth more than run at once, 116 -> 118.  Vectors of 256 bytes: 158 -> 154 and 182 -> 200, not taken.
+  // One launch where there is a CTA for each SM at least: a CTA moves its own keys, while others still select.  8 heads of 128, to
+  // 2000 keys, E4M3: 64 sequences of 0.5k to 16k keys 106 -> 87 us (BF16 157 -> 145), to 500 keys 57 -> 41, of 4.4k each
+  // 116 -> 109; 32 sequences 58 -> 52; 40 of 4.4k each, a few CTAs more than run at once, 76 -> 84.  Long sequences
+  // where CTAs of 512 threads leave room select with 1024 (20 of 5k to 40k keys: 93 us, moving their own 106).
   const int row = kv->d * (kv->dtype == FA_KV_E4M3 ? 1 : 2);
-  const bool many = items >= 2ll * sm_count(), own = many && !in_place && row <= 128, wide = !many && max_kv > 16384;
+  const bool wide = items < 2ll * sm_count() && max_kv > 16384, own = items >= sm_count() && !in_place && !wide;
   const int cache = (wide ? 40960 : 8192) * 4, threads = wide ? 1024 : 512;
   auto select = wide              ? paged::evict_select_kernel<1024, 40960, 0>
                 : !own            ? paged::evict_select_kernel<512, 8192, 0>
                 : row == 64       ? paged::evict_select_kernel<512, 8192, 64>
-                                  : paged::evict_select_kernel<512, 8192, 128>;
-  static std::atomic<uint64_t> prepared[4];
+                : row == 128      ? paged::evict_select_kernel<512, 8192, 128>
+                                  : paged::evict_select_kernel<512, 8192, 256>;
+  static std::atomic<uint64_t> prepared[5];
   if ((rc = prepare_kernel(reinterpret_cast<const void*>(select), cache, threads, 0, "evict_select_kernel",
-                           &prepared[wide ? 0 : !own ? 1 : row == 64 ? 2 : 3])))
+                           &prepared[wide ? 0 : !own ? 1 : row == 64 ? 2 : row == 128 ? 3 : 4])))
     return rc;
   select<<<(unsigned)items, threads, cache, s>>>(g);
   if ((rc = check_cuda(cudaGetLastError(), "launch evict_select_kernel")) || own) return rc;
