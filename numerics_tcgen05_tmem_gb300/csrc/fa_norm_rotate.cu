@@ -778,8 +778,12 @@ static int check_positions(const int32_t* p) {
   return FA_OK;
 }
 
-// What a token of H heads costs, in quarters of a vector: its angles, computed once, as much as four vectors.
-static long long token_cost(int H, int rot, int d) { return 4ll * H + 16 * rot / d; }
+// What a token of H heads costs, in quarters of a vector; its angles, computed once, as much as `angles` quarters for whole
+// heads.  Measured as the split that is fastest: forward 24 (15003 tokens, 28 + 4 heads, d = 128: 43.7 us, with 16 46.9; 16384
+// tokens, 32 + 8: 57.6 and 57.1), backward and append 16 (8192 tokens, 32 + 8, both passes: 78.8 us, with 24 80.5;
+// 23100 tokens into BF16 61.1, with 12 62.6, with 24 63.0).
+constexpr int kForwardAngles = 24, kAngles = 16;
+static long long token_cost(int H, int rot, int d, int angles) { return 4ll * H + angles * rot / d; }
 
 // A side with its share of `all` CTAs, at least one: cost of `costs`.
 template <int D>
@@ -819,7 +823,7 @@ template <int D>
 static int launch_forward(const fa_rotation* r, const Dense& g, const fa_heads* q, const fa_heads* k, const fa_heads* qo,
                           const fa_heads* ko, int Hq, int Hkv, cudaStream_t s) {
   const int all = kCtas * sm_count();
-  const long long cq = token_cost(Hq, r->rot, D), ck = token_cost(Hkv, r->rot, D);
+  const long long cq = token_cost(Hq, r->rot, D, kForwardAngles), ck = token_cost(Hkv, r->rot, D, kForwardAngles);
   const Side sq = make_side<D>(q, nullptr, qo, r->q_weight, r->weight_bf16, Hq, g.tokens, cq, cq + ck, all);
   const Side sk = make_side<D>(k, nullptr, ko, r->k_weight, r->weight_bf16, Hkv, g.tokens, ck, cq + ck, all);
   auto kern = r->interleaved ? norm_rotate_kernel<D, true> : norm_rotate_kernel<D, false>;
@@ -835,7 +839,7 @@ static int launch_backward(const fa_rotation* r, const Dense& g, const fa_heads*
                            const fa_heads* dzk, const fa_heads* dq, const fa_heads* dk, float* dqw, float* dkw, float* part,
                            int Hq, int Hkv, cudaStream_t s) {
   // (rounded down, but one CTA at least for each side: together kParts at most)
-  const long long cq = token_cost(Hq, r->rot, D), ck = token_cost(Hkv, r->rot, D);
+  const long long cq = token_cost(Hq, r->rot, D, kAngles), ck = token_cost(Hkv, r->rot, D, kAngles);
   const Side sq = make_side<D>(q, dzq, dq, r->q_weight, r->weight_bf16, Hq, g.tokens, cq, cq + ck, kParts);
   const Side sk = make_side<D>(k, dzk, dk, r->k_weight, r->weight_bf16, Hkv, g.tokens, ck, cq + ck, kParts);
   auto kern = r->interleaved ? norm_rotate_bwd_kernel<D, true> : norm_rotate_bwd_kernel<D, false>;
@@ -862,7 +866,8 @@ template <int D>
 static int launch_append(const fa_rotation* r, const Packed& g, const fa_heads* q, const fa_heads* k, const fa_heads* v,
                          const fa_heads* qo, int Hq, int Hkv, bool fp8, cudaStream_t s) {
   const int all = kCtas * sm_count();
-  const long long cq = token_cost(Hq, r->rot, D), ck = token_cost(Hkv, r->rot, D), cv = token_cost(Hkv, 0, D);
+  const long long cq = token_cost(Hq, r->rot, D, kAngles), ck = token_cost(Hkv, r->rot, D, kAngles),
+                  cv = token_cost(Hkv, 0, D, kAngles);
   const Side sq = make_side<D>(q, nullptr, qo, r->q_weight, r->weight_bf16, Hq, g.T, cq, cq + ck + cv, all);
   const Side sk = make_side<D>(k, nullptr, k, r->k_weight, r->weight_bf16, Hkv, g.T, ck, cq + ck + cv, all);
   const Side sv = make_side<D>(v, nullptr, v, nullptr, 0, Hkv, g.T, cv, cq + ck + cv, all);
