@@ -1004,6 +1004,7 @@ extern "C" int fa_kv_accumulate(const fa_paged_kv* kv, float* weights, int64_t w
   if (!window && sinks) return set_error(FA_ERR_INVALID_ARG, "sinks need a window");
   const bool fp8 = kv->dtype == FA_KV_E4M3;
   const int max_kv = kv->max_pages * kv->page_size;
+  if (kv->B > (1 << 30)) return set_error(FA_ERR_INVALID_ARG, "B must be <= 2^30 (got %d)", kv->B);
   // a sequence's units are counted in 32 bits
   if ((long long)kv->Hkv * (max_kv / paged::kAccKeys + 1) >= (1ll << 31) / 16)
     return set_error(FA_ERR_INVALID_ARG, "Hkv * max_pages * page_size must be < 2^35");

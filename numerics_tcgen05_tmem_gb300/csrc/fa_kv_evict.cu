@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kSelectThreads, kRow > 0 ? 2 : 1536 / kSelectT
   const int n = evict_length(g.c, b), kept = min(n, g.keep);
   int32_t* out = g.kept + (long long)item * g.keep;
   if (h == 0 && threadIdx.x == 0) g.kept_len[b] = kept;
-  for (int i = kept + (int)threadIdx.x; i < g.keep; i += kSelectThreads) out[i] = -1;
+  for (uint32_t i = (uint32_t)kept + threadIdx.x; i < (uint32_t)g.keep; i += kSelectThreads) out[i] = -1;   // (keep: any int)
   if (n <= g.keep) {
     for (int i = threadIdx.x; i < n; i += kSelectThreads) out[i] = i;
     if constexpr (kRow > 0) {

@@ -956,6 +956,7 @@ extern "C" int fa_qkv_append(const fa_paged_kv* kv, const fa_rotation* rotation,
   int rc;
   if ((rc = paged::check_cache(kv, &g.c)) || (rc = rotate::check_rotation(rotation, kv->d, &g.p))) return rc;
   if (T < 0) return set_error(FA_ERR_INVALID_ARG, "T must be >= 0 (got %d)", T);
+  if (kv->B > (1 << 30)) return set_error(FA_ERR_INVALID_ARG, "B must be <= 2^30 (got %d)", kv->B);
   if (Hq < 1) return set_error(FA_ERR_INVALID_ARG, "Hq must be >= 1 (got %d)", Hq);
   const int d = kv->d, Hkv = kv->Hkv;
   if ((long long)T * (Hq > Hkv ? Hq : Hkv) >= (1ll << 31)) return set_error(FA_ERR_INVALID_ARG, "T*H must be < 2^31");

@@ -51,7 +51,7 @@ def test_bad_caches_and_weights_are_refused(lib, call, kw, code, word):
     (dict(window=4, sinks=-1), BAD, "sinks"), (dict(sinks=3), BAD, "sinks"), (dict(ws=None), BAD, "workspace"),
     (dict(ws=(1 << 21) + 64), BAD, "workspace"), (dict(nbytes=100), BAD, "too small"), (dict(T=1 << 29), BAD, "2^31"),
     (dict(kv=cache(Hkv=64, page_stride=64 * 16 * 64, scale_stride=1024, max_pages=1 << 26, table_stride=1 << 26), w_stride=1024, Hq=64,
-          stride=64 * 64), BAD, "2^35"),
+          stride=64 * 64), BAD, "2^35"), (dict(kv=cache(B=(1 << 30) + 1)), BAD, "2^30"),
 ])
 def test_bad_accumulate_arguments_are_refused(lib, kw, code, word):
     assert accumulate(lib, **kw) == code

@@ -59,6 +59,17 @@ def test_cache(fmt):
         assert torch.equal(x, y)
 
 
+def test_keep_of_any_size():
+    # what is behind the kept keys is filled up to the last of 2^31 - 1 places
+    pages = torch.zeros((24, 2, 1, PAGE, D), dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros((24, 1, PAGE), device="cuda")
+    table, kv_len = torch.arange(24, device="cuda", dtype=torch.int32)[None], torch.tensor([300], device="cuda", dtype=torch.int32)
+    left, kept = binding.kv_evict(w, pages[:, 0], pages[:, 1], table, kv_len, 2 ** 31 - 1)
+    binding.device_status()
+    assert int(left) == 300 and kept[0, 0, :300].tolist() == list(range(300))
+    assert int(kept[0, 0, 300:].max()) == -1 and int(kept[0, 0, 300:].min()) == -1
+
+
 def test_norm_rotate():
     N, hq, hkv, last = 2 ** 22 + 3, 4, 1, 65
     rows = torch.randn((1, N, hq + hkv, D), device="cuda", dtype=torch.bfloat16)

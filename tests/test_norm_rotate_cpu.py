@@ -96,7 +96,7 @@ def append(lib, kv=None, q=G, q_stride=512, out=G, Hq=8, k=G, v=G, stride=128, i
     (dict(T=1 << 30), BAD, "2^31"), (dict(q=None), BAD, "q is NULL"), (dict(out=G + 8), BAD, "q_out"), (dict(k=None), BAD, "k_new"),
     (dict(v=G + 2), BAD, "v_new"), (dict(ip=None), BAD, "q_indptr"), (dict(pos=G + 1), BAD, "positions"),
     (dict(q_stride=504), BAD, "q_stride"), (dict(q_stride=516), BAD, "q_stride"), (dict(stride=120), BAD, "new_stride"),
-    (dict(stride=132), BAD, "new_stride"),
+    (dict(stride=132), BAD, "new_stride"), (dict(kv=cache(B=(1 << 30) + 1)), BAD, "2^30"),
 ])
 def test_bad_append_arguments_are_refused(lib, kw, code, word):
     assert append(lib, **kw) == code
