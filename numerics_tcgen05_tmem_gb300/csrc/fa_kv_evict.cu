@@ -412,6 +412,8 @@ extern "C" int fa_kv_evict(const fa_paged_kv* kv, float* weights, int64_t weight
     return set_error(FA_ERR_INVALID_ARG, "kept_len and kept must be 4-byte aligned device pointers");
   if (kept_len == kv->kv_len)   // every head's CTA reads the length
     return set_error(FA_ERR_INVALID_ARG, "kept_len must not be kv_len itself");
+  if (kept == kept_len || kept == kv->kv_len || kept == kv->block_table || kept == table_out)
+    return set_error(FA_ERR_INVALID_ARG, "kept is another tensor of the call");
   const long long items = (long long)kv->B * kv->Hkv, most = keep < max_kv ? keep : max_kv;
   const int vecs = items * ((most + 31) / 32) >= 32ll * sm_count() ? 32 : 8;   // of a warp that moves
   const long long chunks = (most + vecs - 1) / vecs;

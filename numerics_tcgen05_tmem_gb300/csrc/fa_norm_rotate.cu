@@ -23,6 +23,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <initializer_list>
 
 #include "paged_attn.cuh"
 
@@ -766,6 +767,19 @@ static int check_heads(const fa_heads* x, const char* name, int B, int H, int N,
   return FA_OK;
 }
 
+// An output may start where one of its `own` inputs does, if its vectors lie where that one's do, and where no other
+// tensor of the call does.  (Views of one projection overlap as ranges, so more than the starts cannot be compared.)
+static int check_out(const fa_heads* out, const char* name, int B, int H, int N, std::initializer_list<const fa_heads*> own,
+                     std::initializer_list<const fa_heads*> others) {
+  for (const fa_heads* x : own)
+    if (x->p == out->p && ((B > 1 && x->stride_b != out->stride_b) || (H > 1 && x->stride_h != out->stride_h) ||
+                           (N > 1 && x->stride_n != out->stride_n)))
+      return set_error(FA_ERR_INVALID_ARG, "%s may be an input with the same strides only", name);
+  for (const fa_heads* x : others)
+    if (x->p == out->p) return set_error(FA_ERR_INVALID_ARG, "%s is another tensor of the call", name);
+  return FA_OK;
+}
+
 static int check_sizes(int B, int Hq, int Hkv, int N) {
   if (B < 1 || Hq < 1 || Hkv < 1 || N < 1)
     return set_error(FA_ERR_INVALID_ARG, "B, Hq, Hkv, N must be >= 1 (got %d, %d, %d, %d)", B, Hq, Hkv, N);
@@ -894,7 +908,9 @@ extern "C" int fa_norm_rotate(const fa_rotation* rotation, const fa_heads* q, co
   if ((rc = rotate::check_sizes(B, Hq, Hkv, N)) || (rc = rotate::check_rotation(rotation, d, &p)) ||
       (rc = rotate::check_heads(q, "q", B, Hq, N, false, d)) || (rc = rotate::check_heads(k, "k", B, Hkv, N, false, d)) ||
       (rc = rotate::check_heads(q_out, "q_out", B, Hq, N, true, d)) ||
-      (rc = rotate::check_heads(k_out, "k_out", B, Hkv, N, true, d)) || (rc = rotate::check_positions(positions)))
+      (rc = rotate::check_heads(k_out, "k_out", B, Hkv, N, true, d)) ||
+      (rc = rotate::check_positions(positions)) || (rc = rotate::check_out(q_out, "q_out", B, Hq, N, {q}, {k, k_out})) ||
+      (rc = rotate::check_out(k_out, "k_out", B, Hkv, N, {k}, {q})))
     return rc;
   const rotate::Dense g{p, positions, positions_stride, (unsigned)((long long)B * N), N};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -925,9 +941,12 @@ extern "C" int fa_norm_rotate_bwd(const fa_rotation* rotation, const fa_heads* q
       (rc = rotate::check_heads(q, "q", B, Hq, N, false, d)) || (rc = rotate::check_heads(k, "k", B, Hkv, N, false, d)) ||
       (rc = rotate::check_heads(dzq, "dzq", B, Hq, N, false, d)) || (rc = rotate::check_heads(dzk, "dzk", B, Hkv, N, false, d)) ||
       (rc = rotate::check_heads(dq, "dq", B, Hq, N, true, d)) || (rc = rotate::check_heads(dk, "dk", B, Hkv, N, true, d)) ||
+      (rc = rotate::check_out(dq, "dq", B, Hq, N, {q, dzq}, {k, dzk, dk})) ||
+      (rc = rotate::check_out(dk, "dk", B, Hkv, N, {k, dzk}, {q, dzq})) ||
       (rc = rotate::check_positions(positions)))
     return rc;
   if (!dq_weight != !dk_weight) return set_error(FA_ERR_INVALID_ARG, "dq_weight and dk_weight are given together or not at all");
+  if (dq_weight && dq_weight == dk_weight) return set_error(FA_ERR_INVALID_ARG, "dq_weight and dk_weight are one tensor");
   if ((reinterpret_cast<uintptr_t>(dq_weight) & 3) || (reinterpret_cast<uintptr_t>(dk_weight) & 3))
     return set_error(FA_ERR_INVALID_ARG, "dq_weight, dk_weight are not 4-byte aligned");
   if (dq_weight && !p.norm) return set_error(FA_ERR_INVALID_ARG, "weight gradients need the norm");
@@ -970,6 +989,8 @@ extern "C" int fa_qkv_append(const fa_paged_kv* kv, const fa_rotation* rotation,
   if (new_stride < (int64_t)Hkv * d || new_stride % 8)
     return set_error(FA_ERR_INVALID_ARG, "new_stride %lld must be a multiple of 8 and at least Hkv*d = %lld",
                      (long long)new_stride, (long long)Hkv * d);
+  if (q_out == k_new || q_out == v_new || (q_out == q && T > 1 && q_stride != (int64_t)Hq * d))
+    return set_error(FA_ERR_INVALID_ARG, "q_out may be q, where that is contiguous, and no other input");
   if (T == 0) return FA_OK;
   g.c.status = device_status_word();
   if (!g.c.status) return set_error(FA_ERR_CUDA, "could not allocate the device status record");

@@ -28,7 +28,7 @@ def accumulate(lib, kv=None, w=G, w_stride=32, q=G, stride=512, lse=G, ip=G, T=5
 
 
 def evict(lib, kv=None, w=G, w_stride=32, out=1 << 21, out_stride=2, pages=2, keep=20, sinks=0, recent=0, kept_len=1 << 22,
-          kept=1 << 22):
+          kept=1 << 23):
     return lib.fa_kv_evict(kv or cache(), w, w_stride, out, out_stride, pages, keep, sinks, recent, kept_len, kept, None)
 
 
@@ -83,7 +83,8 @@ def test_workspace_size(lib):
     (dict(sinks=2 ** 31 - 1, recent=2 ** 31 - 1), BAD, "at most keep"), (dict(out=(1 << 21) + 2), BAD, "table_out"),
     (dict(pages=0), BAD, "table_out"), (dict(out_stride=1), BAD, "table_out"), (dict(pages=1), BAD, "room"),
     (dict(keep=33), BAD, "room"), (dict(kept_len=None), BAD, "kept"), (dict(kept=None), BAD, "kept"), (dict(kept=(1 << 22) + 1), BAD, "kept"),
-    (dict(kept_len=G), BAD, "kv_len itself"),
+    (dict(kept_len=G), BAD, "kv_len itself"), (dict(kept=1 << 22), BAD, "another"), (dict(kept=G), BAD, "another"),
+    (dict(kept=1 << 21), BAD, "another"),
     (dict(kv=cache(B=1 << 27, Hkv=8, page_stride=8 * 16 * 64, scale_stride=128), w_stride=128), BAD, "2^31"),
 ])
 def test_bad_evictions_are_refused(lib, kw, code, word):

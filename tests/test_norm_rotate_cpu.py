@@ -28,14 +28,13 @@ def view(p=G, b=4 * 100 * 64, h=64, n=4 * 64):
 
 
 def forward(lib, q=None, k=None, qo=None, ko=None, B=2, Hq=4, Hkv=4, N=100, d=64, pos=G, **kw):
-    v = [x or view() for x in (q, k, qo, ko)]
+    v = [x or view(G + (i << 24)) for i, x in enumerate((q, k, qo, ko))]
     return lib.fa_norm_rotate(rotation(**kw), *v, B, Hq, Hkv, N, d, pos, 0, None)
 
 
-def backward(lib, q=None, dz=None, dx=None, dw=(G, G), B=2, Hq=4, Hkv=4, N=100, d=64, pos=G, ws=1 << 21, nbytes=1 << 30, **kw):
-    q, dz, dx = (x or view() for x in (q, dz, dx))
-    return lib.fa_norm_rotate_bwd(rotation(**kw), q, view(), dz, view(), dx, view(), *dw, B, Hq, Hkv, N, d, pos, 0, ws, nbytes,
-                                  None)
+def backward(lib, q=None, dz=None, dx=None, k=None, dzk=None, dk=None, dw=(G, 2 * G), B=2, Hq=4, Hkv=4, N=100, d=64, pos=G, ws=1 << 21, nbytes=1 << 30, **kw):
+    v = [x or view(G + (i << 24)) for i, x in enumerate((q, k, dz, dzk, dx, dk))]
+    return lib.fa_norm_rotate_bwd(rotation(**kw), *v, *dw, B, Hq, Hkv, N, d, pos, 0, ws, nbytes, None)
 
 
 def test_struct_layouts_match_the_header():
@@ -65,6 +64,17 @@ def test_overlapping_outputs_are_refused(lib):
         assert forward(lib, ko=bad) == BAD and backward(lib, dx=bad) == BAD
 
 
+def test_outputs_that_are_other_tensors_are_refused(lib):
+    at = [view(G + (i << 24)) for i in range(6)]
+    other = view(G, h=6400, n=64)          # the queries' start, other strides
+    for bad in (dict(qo=at[1]), dict(ko=at[0]), dict(qo=at[3]), dict(k=at[0], qo=at[0]), dict(qo=other)):
+        assert forward(lib, **bad) == BAD and ("another tensor" in binding.last_error() or "same strides" in binding.last_error())
+    for bad in (dict(dx=at[1]), dict(dx=at[3]), dict(dx=at[5]), dict(dk=at[0]), dict(dk=at[2]), dict(dx=other), dict(dz=at[3], dx=at[3]),
+                dict(dw=(G, G))):
+        assert backward(lib, **bad) == BAD
+        assert any(w in binding.last_error() for w in ("another tensor", "same strides", "one tensor"))
+
+
 def test_bad_backward_arguments_are_refused(lib):
     assert backward(lib, dw=(G, None)) == BAD and "together" in binding.last_error()
     assert backward(lib, dw=(G + 2, G)) == BAD
@@ -86,7 +96,7 @@ def cache(**kw):
     return binding.PagedKV(*(f[n] for n, _ in binding.PagedKV._fields_))
 
 
-def append(lib, kv=None, q=G, q_stride=512, out=G, Hq=8, k=G, v=G, stride=128, ip=G, pos=None, T=5, **kw):
+def append(lib, kv=None, q=G, q_stride=512, out=2 * G, Hq=8, k=3 * G, v=4 * G, stride=128, ip=G, pos=None, T=5, **kw):
     return lib.fa_qkv_append(kv or cache(), rotation(**kw), q, q_stride, out, Hq, k, v, stride, ip, pos, T, None)
 
 
@@ -96,7 +106,8 @@ def append(lib, kv=None, q=G, q_stride=512, out=G, Hq=8, k=G, v=G, stride=128, i
     (dict(T=1 << 30), BAD, "2^31"), (dict(q=None), BAD, "q is NULL"), (dict(out=G + 8), BAD, "q_out"), (dict(k=None), BAD, "k_new"),
     (dict(v=G + 2), BAD, "v_new"), (dict(ip=None), BAD, "q_indptr"), (dict(pos=G + 1), BAD, "positions"),
     (dict(q_stride=504), BAD, "q_stride"), (dict(q_stride=516), BAD, "q_stride"), (dict(stride=120), BAD, "new_stride"),
-    (dict(stride=132), BAD, "new_stride"), (dict(kv=cache(B=(1 << 30) + 1)), BAD, "2^30"),
+    (dict(stride=132), BAD, "new_stride"), (dict(out=3 * G), BAD, "q_out"), (dict(out=4 * G), BAD, "q_out"),
+    (dict(out=G, q_stride=520), BAD, "q_out"), (dict(kv=cache(B=(1 << 30) + 1)), BAD, "2^30"),
 ])
 def test_bad_append_arguments_are_refused(lib, kw, code, word):
     assert append(lib, **kw) == code
