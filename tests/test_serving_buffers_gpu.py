@@ -1,4 +1,4 @@
-"""Every tensor that the calls around attention allocate belongs to the stream that the call runs on."""
+"""Every tensor that the calls around attention allocate belongs to the stream that the call runs on; programs on two streams."""
 import pytest
 import torch
 
@@ -43,3 +43,44 @@ def test_outputs_belong_to_the_calls_stream(name):
         torch.cuda.synchronize()
         assert got and all(owner(t) == want for t in got)
     binding.device_status()
+
+
+@pytest.mark.parametrize("formats", [("e4m3", "bf16"), ("e4m3", "e4m3")])
+def test_programs_on_two_streams_at_once(formats):
+    # each with a cache of its own; the sums of both are those of one program alone
+    def program(i, fmt, stream):
+        hkv, d, new = (2, 128, [200, 1]) if i else (4, 64, [1, 1])
+        lens = [5000, 900]
+        g = torch.Generator().manual_seed(i)
+        with torch.cuda.stream(stream):
+            c = P.make(lens, hkv, d, 32, fmt, seed=i)
+            w = torch.zeros((c.P, hkv, 32), device="cuda")
+            rows = torch.randn((sum(new), 3 * hkv, d), generator=g).to(torch.bfloat16).cuda()
+            f, ip = R.frequencies(d).cuda(), P.indptr(new)
+            sc = {} if c.ks is None else dict(k_scale=c.ks, v_scale=c.vs)
+            cache = (c.k, c.v, c.table, c.kv_len)
+
+        def step():
+            q = binding.qkv_append(rows[:, :hkv], rows[:, hkv:2 * hkv], rows[:, 2 * hkv:], *cache, ip, f, stream=stream, **sc)
+            _, lse = binding.forward_paged(q, *cache, ip, max(new), stream=stream, **sc)
+            binding.kv_accumulate(w, q, lse, *cache, ip, max(new), stream=stream, **sc)
+            left, kept = binding.kv_evict(w, *cache, 6000, stream=stream, **sc)
+            return [q, lse, w, left, kept]
+        return step
+
+    alone = [program(i, fmt, torch.cuda.current_stream()) for i, fmt in enumerate(formats)]
+    want = []
+    for step in alone:
+        for _ in range(6):
+            out = step()
+        torch.cuda.synchronize()
+        want.append(out)
+    steps = [program(i, fmt, torch.cuda.Stream()) for i, fmt in enumerate(formats)]
+    torch.cuda.synchronize()
+    for _ in range(6):
+        got = [step() for step in steps]
+    torch.cuda.synchronize()
+    binding.device_status()
+    for x, y in zip(want, got):
+        for a, b in zip(x, y):
+            assert torch.equal(a.nan_to_num(), b.nan_to_num())
