@@ -446,6 +446,7 @@ int fa_norm_rotate(const fa_rotation* rotation, const fa_heads* q, const fa_head
 
 /*
  * fa_norm_rotate_bwd -- its backward: from the inputs q, k of the forward and the gradients dzq, dzk of its outputs.
+ *   Without the norm q and k are not read (what they hold has no part in the gradients).
  *   dq, dk       : outputs (each may be its dz or its input, with the same strides)
  *   dq_weight, dk_weight : outputs, FP32 [d], both or neither (NULL); with the norm only.  Summed in a fixed order:
  *                  the same bits in every call on the same data.

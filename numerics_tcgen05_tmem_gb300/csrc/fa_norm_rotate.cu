@@ -4,7 +4,7 @@
 // A vector x is one head of one token, d elements; its first `rot` are rotated in pairs (a, b):
 //   r = 1 / sqrt(mean x^2 + eps), y = w o x r,  z_a = y_a cos - y_b sin,  z_b = y_b cos + y_a sin.
 // Backward: dy is dz rotated by the opposite angle, g = w o dy, dw = sum of dy o x r over the vectors,
-//   dx = r g - x r^3 / d sum(x o g).
+//   dx = r g - x r^3 / d sum(x o g)   (without the norm dx = dy).
 // r is computed again from x, which the backward reads in any case.
 //
 // Memory bounds all three.  d / 16 lanes take a vector, each two 16-byte parts that hold both entries of its
@@ -378,6 +378,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_rotate_kernel(const __gr
   }
 }
 
+// Without the norm dx is dz turned back: x is not read, so that what it holds (NaN in an unused row) stays out of dx.
 // The weights' gradients are summed in registers, then over the CTA's groups, and the CTA's sum goes to
 // part[CTA][d].
 template <int D, bool kInter>
@@ -414,8 +415,10 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) norm_rotate_bwd_kernel(con
   };
   auto copy = [&] {
     if (from != nullptr && next.h < H) {
-      ring.copy(next.stage, 0, from + next.h * side.x_h + ca);
-      ring.copy(next.stage, 1, from + next.h * side.x_h + cb);
+      if (g.p.norm) {
+        ring.copy(next.stage, 0, from + next.h * side.x_h + ca);
+        ring.copy(next.stage, 1, from + next.h * side.x_h + cb);
+      }
       ring.copy(next.stage, 2, from_dz + next.h * side.dz_h + ca);
       ring.copy(next.stage, 3, from_dz + next.h * side.dz_h + cb);
     }
@@ -448,16 +451,15 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) norm_rotate_bwd_kernel(con
     for (int h = d.head0; h - d.head0 < H; h += d.groups) {   // the same number of steps for the whole CTA
       copy();
       ring.wait();
-      Parts v, dy;
-      unpack(ring.get(stage, 0), v.a);
-      unpack(ring.get(stage, 1), v.b);
+      Parts dy;
       unpack(ring.get(stage, 2), dy.a);
       unpack(ring.get(stage, 3), dy.b);
-      stage = stage + 1 == kStages ? 0 : stage + 1;
       const bool real = valid && h < H;   // (else its slot holds what was there)
       turn<kInter, -1>(dy, c, s);
-      float r = 1.f, back = 0.f;
       if (g.p.norm) {
+        Parts v;
+        unpack(ring.get(stage, 0), v.a);
+        unpack(ring.get(stage, 1), v.b);
         float dot[4] = {0.f, 0.f, 0.f, 0.f}, w[8], m0, m1;
         spread8(t.weight[0][j], t.weight[1][j], w);
 #pragma unroll
@@ -473,8 +475,8 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) norm_rotate_bwd_kernel(con
         }
         const float sum = group_sum<L::kLanes>(squares(v));
         const float all = group_sum<L::kLanes>((dot[0] + dot[1]) + (dot[2] + dot[3]));
-        r = inverse_rms(sum, D, g.p);
-        back = -all * r * r * (1.f / D);   // -sum(x o g) r^2 / d
+        const float r = inverse_rms(sum, D, g.p);
+        const float back = -all * r * r * (1.f / D);   // -sum(x o g) r^2 / d
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
           mul2(v.a[i], v.a[i + 1], v.a[i], v.a[i + 1], r, r);   // x r
@@ -487,26 +489,26 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) norm_rotate_bwd_kernel(con
             fma2(dwb[i], dwb[i + 1], dy.b[i], dy.b[i + 1], v.b[i], v.b[i + 1], dwb[i], dwb[i + 1]);
           }
         }
-      }
-      // dx = r w dy - (x r) sum(x o g) r^2 / d
-      float w[8];
-      spread8(t.weight[0][j], t.weight[1][j], w);
+        // dx = r w dy - (x r) sum(x o g) r^2 / d
+        spread8(t.weight[0][j], t.weight[1][j], w);
 #pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        mul2(dy.a[i], dy.a[i + 1], dy.a[i], dy.a[i + 1], w[i], w[i + 1]);
-        mul2(dy.a[i], dy.a[i + 1], dy.a[i], dy.a[i + 1], r, r);
-        fma2(v.a[i], v.a[i + 1], v.a[i], v.a[i + 1], back, back, dy.a[i], dy.a[i + 1]);
-      }
-      spread8(t.weight[2][j], t.weight[3][j], w);
+        for (int i = 0; i < 8; i += 2) {
+          mul2(dy.a[i], dy.a[i + 1], dy.a[i], dy.a[i + 1], w[i], w[i + 1]);
+          mul2(dy.a[i], dy.a[i + 1], dy.a[i], dy.a[i + 1], r, r);
+          fma2(dy.a[i], dy.a[i + 1], v.a[i], v.a[i + 1], back, back, dy.a[i], dy.a[i + 1]);
+        }
+        spread8(t.weight[2][j], t.weight[3][j], w);
 #pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        mul2(dy.b[i], dy.b[i + 1], dy.b[i], dy.b[i + 1], w[i], w[i + 1]);
-        mul2(dy.b[i], dy.b[i + 1], dy.b[i], dy.b[i + 1], r, r);
-        fma2(v.b[i], v.b[i + 1], v.b[i], v.b[i + 1], back, back, dy.b[i], dy.b[i + 1]);
+        for (int i = 0; i < 8; i += 2) {
+          mul2(dy.b[i], dy.b[i + 1], dy.b[i], dy.b[i + 1], w[i], w[i + 1]);
+          mul2(dy.b[i], dy.b[i + 1], dy.b[i], dy.b[i + 1], r, r);
+          fma2(dy.b[i], dy.b[i + 1], v.b[i], v.b[i + 1], back, back, dy.b[i], dy.b[i + 1]);
+        }
       }
+      stage = stage + 1 == kStages ? 0 : stage + 1;
       if (real) {
-        *reinterpret_cast<uint4*>(dx + h * side.out_h + ca) = pack(v.a);
-        *reinterpret_cast<uint4*>(dx + h * side.out_h + cb) = pack(v.b);
+        *reinterpret_cast<uint4*>(dx + h * side.out_h + ca) = pack(dy.a);
+        *reinterpret_cast<uint4*>(dx + h * side.out_h + cb) = pack(dy.b);
       }
     }
     __syncthreads();
