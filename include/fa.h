@@ -410,7 +410,7 @@ int fa_fwd_paged(const fa_paged_kv* kv, const void* q, int64_t q_stride, const i
  *   z_a = y_a cos(t) - y_b sin(t),  z_b = y_b cos(t) + y_a sin(t),  t = position * inv_freq[i],
  * where pair i < rot / 2 is (a, b) = (i, i + rot / 2), or (2 i, 2 i + 1) with `interleaved`; the entries from rot on
  * keep y.  Sums, angles and products are FP32 (angles modulo one turn in 64-bit integers, so that far positions
- * lose nothing); the result is rounded once.  A vector whose sum of squares passes FP32's range gives zeros.
+ * lose nothing); the result is rounded once.  Squares past FP32's range are no exception: any finite x is normed.
  *   inv_freq : FP64 [rot / 2] on the device, radians for each position (not used with rot = 0)
  *   q_weight, k_weight : [d] on the device, FP32, or BF16 with weight_bf16; NULL means ones
  *   rot      : rotated entries, a multiple of 16 from 0 (the norm alone) to d

@@ -5,7 +5,9 @@
 //   r = 1 / sqrt(mean x^2 + eps), y = w o x r,  z_a = y_a cos - y_b sin,  z_b = y_b cos + y_a sin.
 // Backward: dy is dz rotated by the opposite angle, g = w o dy, dw = sum of dy o x r over the vectors,
 //   dx = r g - x r^3 / d sum(x o g)   (without the norm dx = dy).
-// r is computed again from x, which the backward reads in any case.
+// r is computed again from x, which the backward reads in any case.  Where the squares leave FP32's range
+// (entries past 2^56, or all under 2^-38 and eps as small) x is multiplied by a power of two first: y does not change, and
+// dx takes the factor at its end.
 //
 // Memory bounds all three.  d / 16 lanes take a vector, each two 16-byte parts that hold both entries of its
 // pairs, so that the rotation needs no exchange and the sums three (two) shuffles.  Persistent CTAs, and a
@@ -54,6 +56,7 @@ struct Plan {
   const double* inv_freq;
   int rot, norm;
   float eps;
+  float least_sum;   // of a lane's squares, from which on their rounding is FP32's (0 where eps is far above what is lost)
 };
 
 // Queries or keys: where they lie and which CTAs have them.  2^shift lane groups share a token's heads.
@@ -101,10 +104,6 @@ __device__ __forceinline__ float group_sum(float x) {
 #pragma unroll
   for (int o = kLanes / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
-}
-
-__device__ __forceinline__ float inverse_rms(float sum, int d, const Plan& p) {
-  return p.norm ? __frsqrt_rn(sum * (1.f / d) + p.eps) : 1.f;
 }
 
 // The pairs of a lane turned by its eight angles (kSign = -1: back).
@@ -234,12 +233,63 @@ __device__ __forceinline__ float squares(const Parts& v) {
   return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
+__device__ __forceinline__ void scale_vector(Parts& v, float f) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    mul2(v.a[i], v.a[i + 1], v.a[i], v.a[i + 1], f, f);
+    mul2(v.b[i], v.b[i + 1], v.b[i], v.b[i + 1], f, f);
+  }
+}
+
+// What 1 / rms is computed from: a lane's sum of squares and eps, of the vector times `factor`.
+struct Squares {
+  float sum, eps, factor;
+  bool scaled;   // whether a vector of the warp has a factor that may not be 1
+};
+constexpr float kLargestSum = 0x1p116f;   // of a lane; eight of them stay in range
+
+// The factor is 1 but for vectors of which a lane's sum is out of [p.least_sum, kLargestSum): theirs is the power of two that
+// brings the largest entry to [1, 2) (and eps under 4, where it is more than that entry's square).  Zeros, and vectors with
+// an entry that is not finite, stay.  real: whether it is a vector, not what its slot held before.  The vote takes 1 % (8192
+// tokens, 32 + 32 heads, both passes 113.3 -> 114.6 us; neighbouring pairs 2 to 4 %); a vote on 1 / rms itself, behind the sums
+// over the lanes, 3 %.
+template <int D>
+__device__ __forceinline__ Squares vector_squares(Parts& v, const Plan& p, bool real) {
+  constexpr int kLanes = Lanes<D>::kLanes;
+  Squares q{squares(v), p.eps, 1.f, false};
+  const bool out = real && !(q.sum >= p.least_sum && q.sum < kLargestSum);
+  if (__any_sync(0xffffffffu, out)) {
+    q.scaled = true;
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      amax = max(amax, max(__float_as_uint(v.a[i]) & 0x7FFFFFFFu, __float_as_uint(v.b[i]) & 0x7FFFFFFFu));
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const unsigned mine = __ballot_sync(0xffffffffu, out) >> (threadIdx.x % 32 / kLanes * kLanes) & ((1u << kLanes) - 1);
+    if (mine != 0 && amax != 0 && amax < 0x7F800000u) {
+      const int e_eps = p.eps > 0.f ? ((int)(__float_as_uint(p.eps) >> 23) - 127) >> 1 : -127;
+      const int e = min(max(max((int)(amax >> 23) - 127, e_eps), -126), 126);   // both 2^e and 2^-e are normal numbers
+      q.factor = __uint_as_float((uint32_t)(127 - e) << 23);
+      scale_vector(v, q.factor);
+      q.sum = squares(v);
+      q.eps = p.eps * q.factor * q.factor;
+    }
+  }
+  return q;
+}
+
+template <int D>
+__device__ __forceinline__ float inverse_rms(const Squares& q) {
+  return __frsqrt_rn(group_sum<Lanes<D>::kLanes>(q.sum) * (1.f / D) + q.eps);
+}
+
 // One vector's parts normed and turned, in place.
 template <int D, bool kInter>
 __device__ __forceinline__ void forward_vector(Parts& v, const Plan& p, const Tables<D>& t, int j, const float (&c)[8],
-                                               const float (&s)[8]) {
+                                               const float (&s)[8], bool real) {
   if (p.norm) {
-    const float r = inverse_rms(group_sum<Lanes<D>::kLanes>(squares(v)), D, p);
+    const float r = inverse_rms<D>(vector_squares<D>(v, p, real));
     float w[8];
     spread8(t.weight[0][j], t.weight[1][j], w);
 #pragma unroll
@@ -322,18 +372,20 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_rotate_kernel(const __gr
 
   Ahead next{tile, d.head0, 0};
   const __nv_bfloat16* from = nullptr;
+  const long long x_step = d.groups * side.x_h, out_step = d.groups * side.out_h;
   auto seek = [&] {   // the first vector of next.tile
     const unsigned token = next.tile * d.tokens + d.mine;
     from = nullptr;
     if (next.tile < d.tiles && token < g.tokens) {
       const Place at = place_of(token, g.N);
-      from = side.x + at.b * side.x_b + at.n * side.x_n;
+      from = side.x + at.b * side.x_b + at.n * side.x_n + d.head0 * side.x_h + ca;
     }
   };
   auto copy = [&] {
     if (from != nullptr && next.h < H) {
-      ring.copy(next.stage, 0, from + next.h * side.x_h + ca);
-      ring.copy(next.stage, 1, from + next.h * side.x_h + cb);
+      ring.copy(next.stage, 0, from);
+      ring.copy(next.stage, 1, from + (cb - ca));
+      from += x_step;
     }
     ring.commit();
     next.stage = next.stage + 1 == kStages ? 0 : next.stage + 1;
@@ -358,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_rotate_kernel(const __gr
       fill_angles<D, kInter>(t, buf ^ 1, g.p.rot, d.tokens, [&](int i) { return dense_position(g, after * d.tokens + i); });
     const bool valid = token < g.tokens;
     const Place at = place_of(valid ? token : 0, g.N);
-    __nv_bfloat16* z = side.out + at.b * side.out_b + at.n * side.out_n;
+    __nv_bfloat16* z = side.out + at.b * side.out_b + at.n * side.out_n + d.head0 * side.out_h + ca;
     float c[8], s[8];
     load_angles<D, kInter>(t, buf, g.p.rot, d.mine, j, c, s);
     for (int h = d.head0; h - d.head0 < H; h += d.groups) {   // the same number of steps for the whole CTA
@@ -368,11 +420,13 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_rotate_kernel(const __gr
       unpack(ring.get(stage, 0), v.a);
       unpack(ring.get(stage, 1), v.b);
       stage = stage + 1 == kStages ? 0 : stage + 1;
-      forward_vector<D, kInter>(v, g.p, t, j, c, s);
-      if (valid && h < H) {
-        *reinterpret_cast<uint4*>(z + h * side.out_h + ca) = pack(v.a);
-        *reinterpret_cast<uint4*>(z + h * side.out_h + cb) = pack(v.b);
+      const bool real = valid && h < H;
+      forward_vector<D, kInter>(v, g.p, t, j, c, s, real);
+      if (real) {
+        *reinterpret_cast<uint4*>(z) = pack(v.a);
+        *reinterpret_cast<uint4*>(z + (cb - ca)) = pack(v.b);
       }
+      z += out_step;
     }
     __syncthreads();
   }
@@ -404,23 +458,26 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) norm_rotate_bwd_kernel(con
 
   Ahead next{tile, d.head0, 0};
   const __nv_bfloat16 *from = nullptr, *from_dz = nullptr;
+  const long long x_step = d.groups * side.x_h, dz_step = d.groups * side.dz_h, out_step = d.groups * side.out_h;
   auto seek = [&] {
     const unsigned token = next.tile * d.tokens + d.mine;
     from = nullptr;
     if (next.tile < d.tiles && token < g.tokens) {
       const Place at = place_of(token, g.N);
-      from = side.x + at.b * side.x_b + at.n * side.x_n;
-      from_dz = side.dz + at.b * side.dz_b + at.n * side.dz_n;
+      from = side.x + at.b * side.x_b + at.n * side.x_n + d.head0 * side.x_h + ca;
+      from_dz = side.dz + at.b * side.dz_b + at.n * side.dz_n + d.head0 * side.dz_h + ca;
     }
   };
   auto copy = [&] {
     if (from != nullptr && next.h < H) {
       if (g.p.norm) {
-        ring.copy(next.stage, 0, from + next.h * side.x_h + ca);
-        ring.copy(next.stage, 1, from + next.h * side.x_h + cb);
+        ring.copy(next.stage, 0, from);
+        ring.copy(next.stage, 1, from + (cb - ca));
+        from += x_step;
       }
-      ring.copy(next.stage, 2, from_dz + next.h * side.dz_h + ca);
-      ring.copy(next.stage, 3, from_dz + next.h * side.dz_h + cb);
+      ring.copy(next.stage, 2, from_dz);
+      ring.copy(next.stage, 3, from_dz + (cb - ca));
+      from_dz += dz_step;
     }
     ring.commit();
     next.stage = next.stage + 1 == kStages ? 0 : next.stage + 1;
@@ -445,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) norm_rotate_bwd_kernel(con
       fill_angles<D, kInter>(t, buf ^ 1, g.p.rot, d.tokens, [&](int i) { return dense_position(g, after * d.tokens + i); });
     const bool valid = token < g.tokens;
     const Place at = place_of(valid ? token : 0, g.N);
-    __nv_bfloat16* dx = side.out + at.b * side.out_b + at.n * side.out_n;
+    __nv_bfloat16* dx = side.out + at.b * side.out_b + at.n * side.out_n + d.head0 * side.out_h + ca;
     float c[8], s[8];
     load_angles<D, kInter>(t, buf, g.p.rot, d.mine, j, c, s);
     for (int h = d.head0; h - d.head0 < H; h += d.groups) {   // the same number of steps for the whole CTA
@@ -460,6 +517,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) norm_rotate_bwd_kernel(con
         Parts v;
         unpack(ring.get(stage, 0), v.a);
         unpack(ring.get(stage, 1), v.b);
+        const Squares sq = vector_squares<D>(v, g.p, real);
         float dot[4] = {0.f, 0.f, 0.f, 0.f}, w[8], m0, m1;
         spread8(t.weight[0][j], t.weight[1][j], w);
 #pragma unroll
@@ -473,9 +531,8 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) norm_rotate_bwd_kernel(con
           mul2(m0, m1, w[i], w[i + 1], dy.b[i], dy.b[i + 1]);
           fma2(dot[2], dot[3], v.b[i], v.b[i + 1], m0, m1, dot[2], dot[3]);
         }
-        const float sum = group_sum<L::kLanes>(squares(v));
         const float all = group_sum<L::kLanes>((dot[0] + dot[1]) + (dot[2] + dot[3]));
-        const float r = inverse_rms(sum, D, g.p);
+        const float r = inverse_rms<D>(sq);
         const float back = -all * r * r * (1.f / D);   // -sum(x o g) r^2 / d
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
@@ -504,12 +561,14 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) norm_rotate_bwd_kernel(con
           mul2(dy.b[i], dy.b[i + 1], dy.b[i], dy.b[i + 1], r, r);
           fma2(dy.b[i], dy.b[i + 1], v.b[i], v.b[i + 1], back, back, dy.b[i], dy.b[i + 1]);
         }
+        if (sq.scaled) scale_vector(dy, sq.factor);
       }
       stage = stage + 1 == kStages ? 0 : stage + 1;
       if (real) {
-        *reinterpret_cast<uint4*>(dx + h * side.out_h + ca) = pack(dy.a);
-        *reinterpret_cast<uint4*>(dx + h * side.out_h + cb) = pack(dy.b);
+        *reinterpret_cast<uint4*>(dx) = pack(dy.a);
+        *reinterpret_cast<uint4*>(dx + (cb - ca)) = pack(dy.b);
       }
+      dx += out_step;
     }
     __syncthreads();
   }
@@ -623,12 +682,17 @@ __global__ void __launch_bounds__(kThreads, kCtas) qkv_append_kernel(const __gri
   part_columns<D, kInter>(j, rot, ca, cb);
 
   Ahead next{tile, d.head0, 0};
-  auto copy = [&] {
+  const __nv_bfloat16* from = nullptr;
+  auto seek = [&] {
     const unsigned token = next.tile * d.tokens + d.mine;
-    if (next.tile < d.tiles && token < (unsigned)T && next.h < H) {
-      const __nv_bfloat16* from = side.x + token * side.x_n + next.h * D;
-      ring.copy(next.stage, 0, from + ca);
-      ring.copy(next.stage, 1, from + cb);
+    from = nullptr;
+    if (next.tile < d.tiles && token < (unsigned)T) from = side.x + token * side.x_n + d.head0 * D + ca;
+  };
+  auto copy = [&] {
+    if (from != nullptr && next.h < H) {
+      ring.copy(next.stage, 0, from);
+      ring.copy(next.stage, 1, from + (cb - ca));
+      from += d.groups * D;
     }
     ring.commit();
     next.stage = next.stage + 1 == kStages ? 0 : next.stage + 1;
@@ -636,8 +700,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) qkv_append_kernel(const __gri
     if (next.h - d.head0 >= H) {
       next.h = d.head0;
       next.tile += side.ctas;
+      seek();
     }
   };
+  seek();
   // the places of a tile's tokens, by one thread each: four loads that wait for one another
   auto look = [&](unsigned at_tile, int slot) {
     if ((int)threadIdx.x >= d.tokens || at_tile >= d.tiles) return;
@@ -683,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) qkv_append_kernel(const __gri
       Parts y;
       unpack(a, y.a);
       unpack(b, y.b);
-      if (which != 2) forward_vector<D, kInter>(y, g.p, t, j, c, s);
+      if (which != 2) forward_vector<D, kInter>(y, g.p, t, j, c, s, stores);
       if (!kFp8 || which == 0) {
         if (which != 2) {
           a = pack(y.a);
@@ -738,7 +804,7 @@ static int check_rotation(const fa_rotation* r, int d, Plan* p) {
   const int align = r->weight_bf16 ? 1 : 3;
   if ((reinterpret_cast<uintptr_t>(r->q_weight) & align) || (reinterpret_cast<uintptr_t>(r->k_weight) & align))
     return set_error(FA_ERR_INVALID_ARG, "q_weight, k_weight are not aligned to their type");
-  *p = Plan{r->inv_freq, r->rot, r->norm != 0, r->eps};
+  *p = Plan{r->inv_freq, r->rot, r->norm != 0, r->eps, r->eps >= 0x1p-80f ? 0.f : 0x1p-76f};
   return FA_OK;
 }
 
