@@ -581,7 +581,9 @@ __global__ void __launch_bounds__(AccCfg<D, kFp8, N>::kThreads, AccCfg<D, kFp8, 
               for (int x = 0; x < (C::kWide ? 1 : kPieces); ++x)
 #pragma unroll
                 for (int kk = 0; kk < D / 32; ++kk) {
-                  const uint32_t a = a0 + kk * 32, b = b0 + x * C::kQTile + kk * 32;
+                  // one after the other: the smallest piece first, so that few steps cut a sum of full size (d = 128,
+                  // products of one sign: S low by 0.18 2^-23 of it on average, the largest first 0.40)
+                  const uint32_t a = a0 + kk * 32, b = b0 + (C::kWide ? 0 : kPieces - 1 - x) * C::kQTile + kk * 32;
                   if constexpr (C::kAtomBytes == 128)
                     mma_ss_f8(d, sdesc_sw128(a, 16, 1024), sdesc_sw128(b, 16, 1024), C::kIdesc, x + kk > 0);
                   else

@@ -59,7 +59,7 @@ def test_weights_over_the_attention_calls_log_sum_exps(fmt, d, T):
 
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("one_sign", [False, True])
-@pytest.mark.parametrize("most", [(4, 17)])
+@pytest.mark.parametrize("most", [(4, 17), (4, 8)])
 def test_forms_over_e4m3_agree_on_average(d, one_sign, most):
     # max_q settles the form: 32, 64 or 128 columns for 8 heads of 4, 8 and 17 tokens.  They add up the same products, and none
     # may be off by more than half a unit of the last place of q . k on average, which products of one sign would show.  Two
