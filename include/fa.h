@@ -435,7 +435,8 @@ typedef struct {
 /*
  * fa_norm_rotate -- norm and rotation of q [B, Hq, N, d] and k [B, Hkv, N, d].
  *   q_out, k_out : outputs, whose heads of tokens may not overlap; an output may be its input (same strides),
- *                  and may not overlap an input otherwise
+ *                  and is refused if it shares memory with an input otherwise, or with the other output (views of one
+ *                  buffer whose vectors lie beside each other are fine)
  *   positions    : int32 on the device, sequence b's at positions + b * positions_stride (0: the same for all),
  *                  any 32-bit value; NULL means 0 .. N - 1
  * Returns FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED or FA_ERR_CUDA.
@@ -447,7 +448,7 @@ int fa_norm_rotate(const fa_rotation* rotation, const fa_heads* q, const fa_head
 /*
  * fa_norm_rotate_bwd -- its backward: from the inputs q, k of the forward and the gradients dzq, dzk of its outputs.
  *   Without the norm q and k are not read (what they hold has no part in the gradients).
- *   dq, dk       : outputs (each may be its dz or its input, with the same strides)
+ *   dq, dk       : outputs (each may be its dz or its input, with the same strides; as in fa_norm_rotate otherwise)
  *   dq_weight, dk_weight : outputs, FP32 [d], both or neither (NULL); with the norm only.  Summed in a fixed order:
  *                  the same bits in every call on the same data.
  *   workspace    : device scratch of at least fa_norm_rotate_bwd_workspace_size(B, Hq, Hkv, N, d) bytes (0 for invalid
@@ -516,7 +517,7 @@ int fa_kv_accumulate(const fa_paged_kv* kv, float* weights, int64_t weight_strid
  *               block_table itself: in place; no page may then belong to two sequences.
  *   kept_len  : output, int32 [B]: min(kv_len, keep), the new lengths (kv_len is not written, and kept_len is not kv_len)
  *   kept      : output, int32 [B, Hkv, keep]: the position of each kept key, -1 behind kept_len
- *   sinks + recent <= keep
+ *   kept_len and kept share no memory with each other, the tables or kv_len;  sinks + recent <= keep
  * Slots behind the new length stay as they were.  Returns FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED or FA_ERR_CUDA.
  */
 int fa_kv_evict(const fa_paged_kv* kv, float* weights, int64_t weight_stride, const int32_t* table_out,

@@ -15,6 +15,7 @@
 // and waits between a step's loads and its stores.
 #include <algorithm>
 
+#include "overlap.h"
 #include "paged_attn.cuh"
 
 namespace fa {
@@ -412,12 +413,19 @@ extern "C" int fa_kv_evict(const fa_paged_kv* kv, float* weights, int64_t weight
     return set_error(FA_ERR_INVALID_ARG, "kept_len and kept must be 4-byte aligned device pointers");
   if (kept_len == kv->kv_len)   // every head's CTA reads the length
     return set_error(FA_ERR_INVALID_ARG, "kept_len must not be kv_len itself");
-  if (kept == kept_len || kept == kv->kv_len || kept == kv->block_table || kept == table_out)
-    return set_error(FA_ERR_INVALID_ARG, "kept is another tensor of the call");
   const long long items = (long long)kv->B * kv->Hkv, most = keep < max_kv ? keep : max_kv;
   const int vecs = items * ((most + 31) / 32) >= 32ll * sm_count() ? 32 : 8;   // of a warp that moves
   const long long chunks = (most + vecs - 1) / vecs;
   if (items * std::max(chunks, 8ll) >= (1ll << 31)) return set_error(FA_ERR_INVALID_ARG, "B*Hkv*keep/32 must be < 2^31");
+  const auto ints = [](const void* p, long long rows, long long n, long long stride) { return Pieces{p, 4 * n, {rows, 1, 1}, {4 * stride, 0, 0}}; };
+  const Pieces out[2] = {ints(kept_len, 1, kv->B, 0), ints(kept, 1, items * keep, 0)};
+  const Pieces in[3] = {ints(kv->kv_len, 1, kv->B, 0), ints(kv->block_table, kv->B, kv->max_pages, kv->table_stride),
+                        ints(table_out, kv->B, max_pages_out, table_out_stride)};
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < (in_place ? 2 : 3); ++j)
+      if (pieces_overlap(out[i], in[j]))
+        return set_error(FA_ERR_INVALID_ARG, "%s overlaps another tensor of the call", i == 0 ? "kept_len" : "kept");
+  if (pieces_overlap(out[0], out[1])) return set_error(FA_ERR_INVALID_ARG, "kept overlaps another tensor of the call, kept_len");
   g.c.status = device_status_word();
   if (!g.c.status) return set_error(FA_ERR_CUDA, "could not allocate the device status record");
   g.weights = weights;

@@ -27,6 +27,7 @@
 #include <algorithm>
 #include <initializer_list>
 
+#include "overlap.h"
 #include "paged_attn.cuh"
 
 namespace fa {
@@ -835,16 +836,30 @@ static int check_heads(const fa_heads* x, const char* name, int B, int H, int N,
   return FA_OK;
 }
 
-// An output may start where one of its `own` inputs does, if its vectors lie where that one's do, and where no other
-// tensor of the call does.  (Views of one projection overlap as ranges, so more than the starts cannot be compared.)
-static int check_out(const fa_heads* out, const char* name, int B, int H, int N, std::initializer_list<const fa_heads*> own,
-                     std::initializer_list<const fa_heads*> others) {
-  for (const fa_heads* x : own)
-    if (x->p == out->p && ((B > 1 && x->stride_b != out->stride_b) || (H > 1 && x->stride_h != out->stride_h) ||
-                           (N > 1 && x->stride_n != out->stride_n)))
-      return set_error(FA_ERR_INVALID_ARG, "%s may be an input with the same strides only", name);
-  for (const fa_heads* x : others)
-    if (x->p == out->p) return set_error(FA_ERR_INVALID_ARG, "%s is another tensor of the call", name);
+static Pieces pieces_of(const fa_heads* x, int B, int H, int N, int d) {
+  return Pieces{x->p, 2ll * d, {B, H, N}, {B > 1 ? 2 * x->stride_b : 0, H > 1 ? 2 * x->stride_h : 0, N > 1 ? 2 * x->stride_n : 0}};
+}
+
+// A tensor of a call and its heads.
+struct Named {
+  const fa_heads* x;
+  int H;
+};
+
+// An output of H heads may be one of its `own` inputs, with the same strides, and shares no memory with the call's other
+// tensors.
+static int check_out(const fa_heads* out, const char* name, int B, int H, int N, int d, std::initializer_list<const fa_heads*> own,
+                     std::initializer_list<Named> others) {
+  const Pieces o = pieces_of(out, B, H, N, d);
+  for (const fa_heads* x : own) {
+    const bool same = x->p == out->p && (B == 1 || x->stride_b == out->stride_b) && (H == 1 || x->stride_h == out->stride_h) &&
+                      (N == 1 || x->stride_n == out->stride_n);
+    if (!same && pieces_overlap(o, pieces_of(x, B, H, N, d)))
+      return set_error(FA_ERR_INVALID_ARG, "%s overlaps an input: it may be that input, with the same strides, only", name);
+  }
+  for (const Named& t : others)
+    if (pieces_overlap(o, pieces_of(t.x, B, t.H, N, d)))
+      return set_error(FA_ERR_INVALID_ARG, "%s overlaps another tensor of the call", name);
   return FA_OK;
 }
 
@@ -977,8 +992,8 @@ extern "C" int fa_norm_rotate(const fa_rotation* rotation, const fa_heads* q, co
       (rc = rotate::check_heads(q, "q", B, Hq, N, false, d)) || (rc = rotate::check_heads(k, "k", B, Hkv, N, false, d)) ||
       (rc = rotate::check_heads(q_out, "q_out", B, Hq, N, true, d)) ||
       (rc = rotate::check_heads(k_out, "k_out", B, Hkv, N, true, d)) ||
-      (rc = rotate::check_positions(positions)) || (rc = rotate::check_out(q_out, "q_out", B, Hq, N, {q}, {k, k_out})) ||
-      (rc = rotate::check_out(k_out, "k_out", B, Hkv, N, {k}, {q})))
+      (rc = rotate::check_positions(positions)) || (rc = rotate::check_out(q_out, "q_out", B, Hq, N, d, {q}, {{k, Hkv}, {k_out, Hkv}})) ||
+      (rc = rotate::check_out(k_out, "k_out", B, Hkv, N, d, {k}, {{q, Hq}})))
     return rc;
   const rotate::Dense g{p, positions, positions_stride, (unsigned)((long long)B * N), N};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -1009,12 +1024,13 @@ extern "C" int fa_norm_rotate_bwd(const fa_rotation* rotation, const fa_heads* q
       (rc = rotate::check_heads(q, "q", B, Hq, N, false, d)) || (rc = rotate::check_heads(k, "k", B, Hkv, N, false, d)) ||
       (rc = rotate::check_heads(dzq, "dzq", B, Hq, N, false, d)) || (rc = rotate::check_heads(dzk, "dzk", B, Hkv, N, false, d)) ||
       (rc = rotate::check_heads(dq, "dq", B, Hq, N, true, d)) || (rc = rotate::check_heads(dk, "dk", B, Hkv, N, true, d)) ||
-      (rc = rotate::check_out(dq, "dq", B, Hq, N, {q, dzq}, {k, dzk, dk})) ||
-      (rc = rotate::check_out(dk, "dk", B, Hkv, N, {k, dzk}, {q, dzq})) ||
+      (rc = rotate::check_out(dq, "dq", B, Hq, N, d, {q, dzq}, {{k, Hkv}, {dzk, Hkv}, {dk, Hkv}})) ||
+      (rc = rotate::check_out(dk, "dk", B, Hkv, N, d, {k, dzk}, {{q, Hq}, {dzq, Hq}})) ||
       (rc = rotate::check_positions(positions)))
     return rc;
   if (!dq_weight != !dk_weight) return set_error(FA_ERR_INVALID_ARG, "dq_weight and dk_weight are given together or not at all");
-  if (dq_weight && dq_weight == dk_weight) return set_error(FA_ERR_INVALID_ARG, "dq_weight and dk_weight are one tensor");
+  if (dq_weight && pieces_overlap({dq_weight, 4ll * d, {1, 1, 1}, {}}, {dk_weight, 4ll * d, {1, 1, 1}, {}}))
+    return set_error(FA_ERR_INVALID_ARG, "dq_weight and dk_weight are one tensor, or overlap");
   if ((reinterpret_cast<uintptr_t>(dq_weight) & 3) || (reinterpret_cast<uintptr_t>(dk_weight) & 3))
     return set_error(FA_ERR_INVALID_ARG, "dq_weight, dk_weight are not 4-byte aligned");
   if (dq_weight && !p.norm) return set_error(FA_ERR_INVALID_ARG, "weight gradients need the norm");
@@ -1057,9 +1073,12 @@ extern "C" int fa_qkv_append(const fa_paged_kv* kv, const fa_rotation* rotation,
   if (new_stride < (int64_t)Hkv * d || new_stride % 8)
     return set_error(FA_ERR_INVALID_ARG, "new_stride %lld must be a multiple of 8 and at least Hkv*d = %lld",
                      (long long)new_stride, (long long)Hkv * d);
-  if (q_out == k_new || q_out == v_new || (q_out == q && T > 1 && q_stride != (int64_t)Hq * d))
-    return set_error(FA_ERR_INVALID_ARG, "q_out may be q, where that is contiguous, and no other input");
   if (T == 0) return FA_OK;
+  const auto rows = [T](const void* p, long long elems, long long stride) { return Pieces{p, 2 * elems, {T, 1, 1}, {2 * stride, 0, 0}}; };
+  const Pieces out = rows(q_out, (long long)Hq * d, (long long)Hq * d);
+  if ((!(q_out == q && (T == 1 || q_stride == (int64_t)Hq * d)) && pieces_overlap(out, rows(q, (long long)Hq * d, q_stride))) ||
+      pieces_overlap(out, rows(k_new, (long long)Hkv * d, new_stride)) || pieces_overlap(out, rows(v_new, (long long)Hkv * d, new_stride)))
+    return set_error(FA_ERR_INVALID_ARG, "q_out may be q, where that is contiguous, and overlaps no input otherwise");
   g.c.status = device_status_word();
   if (!g.c.status) return set_error(FA_ERR_CUDA, "could not allocate the device status record");
   g.q_indptr = q_indptr;
