@@ -85,7 +85,12 @@ __device__ __forceinline__ void move_keys(const Evict& g, int item, int first, i
   long long from = -1, to = -1;       // the lane's vector: bytes from the pool's start
   if (lane < here) {
     const Spot f = spot_of(g.c, g.c.table, g.c.table_stride, g.c.max_pages, b, g.kept[(long long)item * g.keep + first + lane]);
-    const Spot t = spot_of(g.c, g.table_out, g.table_out_stride, g.max_pages_out, b, first + lane);
+    Spot t = spot_of(g.c, g.table_out, g.table_out_stride, g.max_pages_out, b, first + lane);
+    // a copy of the sequence's own table: other keys of the page are still to be read
+    if (t.page >= 0 && t.page == __ldg(g.c.table + b * g.c.table_stride + (first + lane >> g.c.page_shift))) {
+      report_bounds(g.c.status, kSitePagedEvict, t.page);
+      t.page = -1;
+    }
     if (f.page >= 0 && t.page >= 0) {
       const long long f_at = h * page_size + f.slot, t_at = h * page_size + t.slot;
       from = f.page * g.c.page_stride * elem + f_at * kRow;

@@ -74,7 +74,7 @@ enum : uint32_t {
   kSitePagedLen = 32,      // attention: a sequence's length exceeds its table, or its rows the tensor
   kSitePagedPage = 33,     // attention: a page of the table is out of range
   kSitePagedPieces = 34,   // attention: the record of a split item's pieces is not a valid one
-  kSitePagedEvict = 35,    // eviction: a kept position or a page of either table is out of range
+  kSitePagedEvict = 35,    // eviction: a kept position or a page of either table is out of range, or a page moves to itself
 };
 
 // Record a failed index check: the flag, and the site and index of the first one seen.
