@@ -496,8 +496,8 @@ int fa_qkv_append(const fa_paged_kv* kv, const fa_rotation* rotation, const void
  *              needed and for invalid sizes), 256-byte aligned (NULL where that is 0); its contents on entry do
  *              not matter.  Calls that may overlap need workspaces of their own.
  * With BF16 keys `scale` is raised by 0.9 (d = 64) or 1.6 (d = 128) units of 2^-23 of itself, rounded to FP32: what the tensor
- * core's sums lose on average.  q . k is exact but for its FP32 sum, and, for few rows over an E4M3 cache, entries of q under 2^-23 of the head's
- * largest one.
+ * core's sums lose on average.  q . k is exact but for its FP32 sum, and, for few rows over an E4M3 cache, entries of q
+ * under 2^-23 of the head's largest one, which may be off by 2^-31 of that.
  * Returns FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED or FA_ERR_CUDA; T = 0 or max_q = 0 launches nothing.
  */
 size_t fa_kv_accumulate_workspace_size(int T, int max_q, int Hq, int Hkv, int d, int dtype);

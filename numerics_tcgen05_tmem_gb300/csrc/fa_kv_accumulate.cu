@@ -17,8 +17,8 @@
 //     round, early keys, which most tokens see, first.  Where there are few of them each is cut into parts by its
 //     query blocks, whose sums a second kernel joins in order.
 // E4M3 caches, few rows: the codes are the operand as they are (kind::f8f6f4).  A query vector goes into three E5M2
-// vectors that add up to it: BF16 has 8 significant bits, E5M2 3, and its exponents reach 2^-31 of the largest
-// entry, so the sum is exact down to entries of 2^-24 of it.  Chunks: a warpgroup turns the codes into BF16, once for
+// vectors that add up to it: BF16 has 8 significant bits, E5M2 3, and its smallest step is 2^-30 of the largest entry or
+// less.  Entries of at least 2^-23 of the largest are exact, smaller ones off by 2^-31 of it at most.  Chunks: a warpgroup turns the codes into BF16, once for
 // all the query blocks of a unit.  The key's scale multiplies S in FP32.
 #include <limits.h>
 #include <stdlib.h>
