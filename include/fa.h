@@ -489,8 +489,9 @@ int fa_qkv_append(const fa_paged_kv* kv, const fa_rotation* rotation, const void
  *   kv, q, q_stride, q_indptr, T, max_q, Hq, window, sinks, scale : fa_fwd_paged's (v is not read)
  *   lse      : FP32 [T, Hq], that call's output; -inf (a row that saw no key) weighs nothing
  * Weights of keys that no new token sees, of sequences without new tokens, and behind a sequence's end stay as they
- * are.  Sums are FP32, each key's in a fixed order: the same bits in every call on the same data.  Sequences in
- * one call must not share pages (a shared key would have one weight for all of them).  Hkv * max_pages * page_size is
+ * are.  Sums are FP32, each key's in a fixed order: the same bits in every call on the same data.  Sequences with
+ * new tokens in one call must not share pages that these see (a shared key would have one weight for all of them; one
+ * of the sums is lost.  Builds with FA_DEBUG_BOUNDS record it as FA_ERR_DEVICE_BOUNDS).  Hkv * max_pages * page_size is
  * under 2^35, B at most 2^30.
  * workspace  : device scratch of at least fa_kv_accumulate_workspace_size(T, max_q, Hq, Hkv, d, dtype) bytes (0 where none is
  *              needed and for invalid sizes), 256-byte aligned (NULL where that is 0); its contents on entry do

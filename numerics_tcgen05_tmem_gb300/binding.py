@@ -793,7 +793,8 @@ def kv_accumulate(weights, q, lse, k_cache, v_cache, block_table, kv_len, q_indp
     weights: float32 [pages, Hkv, page_size], one for each key of the cache.  For key j of a sequence and kv head:
     weights[j] = (0 if j is a new token's else weights[j]) + the sum over the new tokens i that see j and the
     query heads of the kv head of exp(scale q_i . k_j - lse_i).
-    q, lse and the other arguments are those of forward_paged and its output; the cache holds the new keys.
+    q, lse and the other arguments are those of forward_paged and its output; the cache holds the new keys.  Two
+    sequences of one call must not share pages, as they may for forward_paged: a shared key's weight would lose one's sum.
     workspace: fa_kv_accumulate_workspace_size bytes, for calls that do not overlap; else allocated.
     """
     kv = _paged(k_cache, v_cache, block_table, kv_len, k_scale, v_scale)

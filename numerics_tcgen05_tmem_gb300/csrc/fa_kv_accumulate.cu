@@ -296,6 +296,21 @@ __device__ __forceinline__ void acc_columns(const uint32_t (&r)[W], const float*
   }
 }
 
+#ifdef FA_DEBUG_BOUNDS
+// Whether a page whose keys sequence b's new tokens see is one of another sequence's: the CTAs of both would read and
+// write its weights, and one of the sums be lost.
+__device__ __forceinline__ void check_not_shared(const Attn& p, int b, int page) {
+  const int shift = p.c.page_shift;
+  for (int x = 0; x < p.c.B; ++x) {
+    const AccSeq other(p, x);
+    if (x == b || other.w.steps == 0) continue;
+    for (int i = 0; i << shift < other.w.hi; ++i)
+      if (other.w.any(i << shift, 1 << shift) && __ldg(p.c.table + x * p.c.table_stride + i) == page)
+        report_bounds(p.c.status, kSitePagedShared, page);
+  }
+}
+#endif
+
 // The pages of a unit's boxes, one for each lane (num_pages where there is nothing to read): one access to the table
 // serves as many of a sequence's units as the lanes hold.
 struct AccPages {
@@ -414,6 +429,10 @@ __global__ void __launch_bounds__(AccCfg<D, kFp8, N>::kThreads, AccCfg<D, kFp8, 
     for (; cur.valid(p); cur.next(p, parts), ++n) {
       const int s = n % C::kKStages, tiles = cur.tile(1) ? 2 : 1;
       const int page = pages.get(p, cur, boxes, box_shift);
+#ifdef FA_DEBUG_BOUNDS
+      if (lane < boxes && page < p.c.num_pages) check_not_shared(p, cur.b, page);
+      __syncwarp();
+#endif
       uint64_t* full = C::kConvert ? &sh.code_full : &sh.k_full[s];
       if (!__all_sync(0xffffffffu, C::kConvert ? mbar_wait(&sh.code_empty, (n & 1) ^ 1, abort_flag, p.c.status)
                                                : mbar_wait(&sh.k_empty[s], ((n / C::kKStages) & 1) ^ 1, abort_flag, p.c.status)))

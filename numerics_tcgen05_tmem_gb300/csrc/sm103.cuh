@@ -75,6 +75,7 @@ enum : uint32_t {
   kSitePagedPage = 33,     // attention: a page of the table is out of range
   kSitePagedPieces = 34,   // attention: the record of a split item's pieces is not a valid one
   kSitePagedEvict = 35,    // eviction: a kept position or a page of either table is out of range, or a page moves to itself
+  kSitePagedShared = 36,   // accumulated weights (FA_DEBUG_BOUNDS): a page is that of two sequences
 };
 
 // Record a failed index check: the flag, and the site and index of the first one seen.
