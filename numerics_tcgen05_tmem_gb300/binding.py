@@ -835,8 +835,8 @@ def kv_evict(weights, k_cache, v_cache, block_table, kv_len, keep, sinks: int = 
 
     The first ``sinks`` keys, the newest ``recent`` ones and, of the others, those with the largest weights (of equal
     ones the first) move in order, with their values, scales and weights, to the positions 0, 1, ... of the sequence
-    in table_out: int32 [B, pages], free pages of the same pool (not a copy of block_table: that is recorded, and
-    nothing moves); None: in place, where no two sequences share pages.
+    in table_out: int32 [B, pages], free pages of the same pool (not a copy of block_table: keys that were to
+    move within it are recorded, and do not); None: in place, where no two sequences share pages.
     weights: float32 [pages, Hkv, page_size] (kv_accumulate).
     kept_len: int32 [B], min(kv_len, keep): the lengths for the calls that follow (kv_len itself is not
     written).  kept: int32 [B, Hkv, keep], the kept keys' former positions, -1 behind kept_len.  Both are

@@ -84,11 +84,12 @@ __device__ __forceinline__ void move_keys(const Evict& g, int item, int first, i
   const int elem = g.c.k_scale != nullptr ? 1 : 2;
   long long from = -1, to = -1;       // the lane's vector: bytes from the pool's start
   if (lane < here) {
-    const Spot f = spot_of(g.c, g.c.table, g.c.table_stride, g.c.max_pages, b, g.kept[(long long)item * g.keep + first + lane]);
+    const int key = g.kept[(long long)item * g.keep + first + lane];
+    const Spot f = spot_of(g.c, g.c.table, g.c.table_stride, g.c.max_pages, b, key);
     Spot t = spot_of(g.c, g.table_out, g.table_out_stride, g.max_pages_out, b, first + lane);
-    // a copy of the sequence's own table: other keys of the page are still to be read
+    // a page of the sequence's own, as in a copy of its table: other keys of the page are still to be read
     if (t.page >= 0 && t.page == __ldg(g.c.table + b * g.c.table_stride + (first + lane >> g.c.page_shift))) {
-      report_bounds(g.c.status, kSitePagedEvict, t.page);
+      if (key != first + lane) report_bounds(g.c.status, kSitePagedEvict, t.page);   // (else it is there)
       t.page = -1;
     }
     if (f.page >= 0 && t.page >= 0) {
