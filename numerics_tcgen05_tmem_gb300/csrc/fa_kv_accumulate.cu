@@ -12,14 +12,14 @@
 //     queries stay in shared memory; a ring of K tiles is kept full.  64 sequences, 284k keys, 8 kv heads of 128:
 //     E4M3 55 us (85 % of the copy rate), BF16 95 us (93 %).
 //   * chunks: 256 x 128 pairs of a head take 1024 clocks of tensor work, and as many for their exponentials (32 a clock
-//     and SM); both together, with the sums between them, bound it.  2048 tokens over 34k keys, 32 heads of 128: 390 us,
-//     1420 TFLOP/s (without the products 339).  Units are dealt round by
-//     round, early keys, which most tokens see, first.  Where there are few of them each is cut into parts by its
-//     query blocks, whose sums a second kernel joins in order.
+//     and SM); both together, with the sums between them, bound it.  2048 tokens over 34k keys, 32 heads of 128: 388
+//     to 411 us, 1350 to 1430 TFLOP/s, from run to run (without the products 339).  Units are dealt round by round, early
+//     keys, which most tokens see, first.  Where there are few of them each is cut into parts by its query blocks, whose sums
+//     a second kernel joins in order.
 // E4M3 caches, few rows: the codes are the operand as they are (kind::f8f6f4).  A query vector goes into three E5M2
 // vectors that add up to it: BF16 has 8 significant bits, E5M2 3, and its smallest step is 2^-30 of the largest entry or
-// less.  Entries of at least 2^-23 of the largest are exact, smaller ones off by 2^-31 of it at most.  Chunks: a warpgroup turns the codes into BF16, once for
-// all the query blocks of a unit.  The key's scale multiplies S in FP32.
+// less.  Entries of at least 2^-23 of the largest are exact, smaller ones off by 2^-31 of it at most.  Chunks: a warpgroup
+// turns the codes into BF16, once for all the query blocks of a unit.  The key's scale multiplies S in FP32.
 #include <limits.h>
 #include <stdlib.h>
 
@@ -58,8 +58,8 @@ struct AccCfg {
   // columns leave no room for that: S takes the pieces one after the other.)
   static constexpr bool kWide = kPieced && N <= 32;
   // chunks: two sets of warps take the blocks in turn, the one with an even place (of its tile) the first buffer of S, the
-  // other the second, and add their sums at the end of a unit.  2048 tokens over 34k keys 390 us; two sets with half
-  // of each block's columns 406, one set 423.  Not with converters beside them: 80 registers are too few (466 us, 431).
+  // other the second, and add their sums at the end of a unit.  2048 tokens over 34k keys 390 us (at best, as the
+  // other figures here); two sets with half of each block's columns 406, one set 423.  Not with converters beside them: 80 registers are too few (466 us, 431).
   static constexpr int kHalves = kChunk && !kConvert ? 2 : 1;
   static constexpr int kSumWarps = 8 * kHalves, kThreads = 32 * (kSumWarps + (kConvert ? 8 : 4));
   // CTAs on an SM: two where each holds three units' keys or more.  (A unit's hand-offs take longer than its 16 or 32 KB:

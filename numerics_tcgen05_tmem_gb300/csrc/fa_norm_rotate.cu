@@ -12,10 +12,10 @@
 // Memory bounds all three.  d / 16 lanes take a vector, each two 16-byte parts that hold both entries of its
 // pairs, so that the rotation needs no exchange and the sums three (two) shuffles.  Persistent CTAs, and a
 // thread's copies (cp.async) run two vectors ahead, into slots that only it reads: registers as the store of
-// what is on its way left the backward at 4.7 TB/s, where it now moves 6.0.
-//   8192 tokens, 32 + 32 heads, d = 128: forward 45 us, backward 63 us and 3 us for the weights' gradients
-//   (268 and 403 MB: 5.9 and 6.1 TB/s of the 6.8 of a plain copy); 8 x 1024 tokens, 12 + 12 heads, d = 64: 14 and 19 + 3 us,
-//   where a third is the start (frequencies, angles) and the last, partly filled round of tiles;
+// what is on its way left the backward at 4.7 TB/s, where it now moves 6.1.
+//   8192 tokens, 32 + 32 heads, d = 128: forward 45 us, backward 66 us and 3 us for the weights' gradients, without the
+//   norm 48 us (268, 403 and 268 MB: 6.0, 6.1 and 5.6 TB/s of the 6.8 of a plain copy); 8 x 1024 tokens, 12 + 12 heads,
+//   d = 64: 14.5 and 19 + 3 us, where a third is the start (frequencies, angles) and the last, partly filled round of tiles;
 //   23100 packed tokens, 32 + 8 + 8 heads, into a BF16 cache 61 us, 6.2 TB/s.
 //
 // Angles: position times frequency modulo one turn.  In FP32 a position of 2^20 would leave 0.06 rad of error.
