@@ -515,7 +515,8 @@ int fa_kv_accumulate(const fa_paged_kv* kv, float* weights, int64_t weight_strid
  *   table_out : int32 [B][max_pages_out], rows table_out_stride apart: the pages to move to, with room for
  *               min(keep, max_pages * page_size) keys; pages of the same pool that no sequence of the call has in
  *               block_table (a page that the sequence has in the same place, as in a copy of block_table, is not
- *               written; keys that were to move there are recorded as FA_ERR_DEVICE_BOUNDS).  The source pages stay as they are (and may be shared by sequences).  NULL, or
+ *               written; keys that were to move there are recorded as FA_ERR_DEVICE_BOUNDS).  The source pages
+ *               stay as they are (and may be shared by sequences).  NULL, or
  *               block_table itself: in place; no page may then belong to two sequences.
  *   kept_len  : output, int32 [B]: min(kv_len, keep), the new lengths (kv_len is not written, and kept_len is not kv_len)
  *   kept      : output, int32 [B, Hkv, keep]: the position of each kept key, -1 behind kept_len

@@ -59,7 +59,8 @@ struct AccCfg {
   static constexpr bool kWide = kPieced && N <= 32;
   // chunks: two sets of warps take the blocks in turn, the one with an even place (of its tile) the first buffer of S, the
   // other the second, and add their sums at the end of a unit.  2048 tokens over 34k keys 390 us (at best, as the
-  // other figures here); two sets with half of each block's columns 406, one set 423.  Not with converters beside them: 80 registers are too few (466 us, 431).
+  // other figures here); two sets with half of each block's columns 406, one set 423.  Not with converters beside them: 80
+  // registers are too few (466 us, 431).
   static constexpr int kHalves = kChunk && !kConvert ? 2 : 1;
   static constexpr int kSumWarps = 8 * kHalves, kThreads = 32 * (kSumWarps + (kConvert ? 8 : 4));
   // CTAs on an SM: two where each holds three units' keys or more.  (A unit's hand-offs take longer than its 16 or 32 KB:
@@ -1056,7 +1057,7 @@ extern "C" int fa_kv_accumulate(const fa_paged_kv* kv, float* weights, int64_t w
   // by 7.7e-7 on average.)  The scale is raised by that for BF16 keys, so that a weight is what its formula says of the
   // log-sum-exp that it is given: 1024 tokens over 16k keys, d = 128: 1.1e-7 off, without 5.5e-7.  (The attention call cuts its
   // sums alike, and its log-sum-exps are 8e-7 low of values near 10: rows sum to 1 + 8e-7 for it, without the raise
-  // 1 + 2e-7.)  Of E4M3 codes' products, 12 bits wide, little is cut: 0 to 0.25 2^-23, and no raise.
+  // 1 + 2e-7.)  Of E4M3 codes' products, 12 bits wide, little is cut: 0 to 0.5 2^-23, and no raise.
   const double cut = fp8 ? 0 : (kv->d / 16 + 1) / 2. * 0.36 * 0x1p-23;
   g.scale_log2 = (float)(scale * 1.4426950408889634 * (1 + cut));
 #ifdef FA_TEST_HOOKS

@@ -88,7 +88,7 @@ __device__ __forceinline__ void move_keys(const Evict& g, int item, int first, i
     const Spot f = spot_of(g.c, g.c.table, g.c.table_stride, g.c.max_pages, b, key);
     Spot t = spot_of(g.c, g.table_out, g.table_out_stride, g.max_pages_out, b, first + lane);
     // a page of the sequence's own, as in a copy of its table: other keys of the page are still to be read
-    if (t.page >= 0 && t.page == __ldg(g.c.table + b * g.c.table_stride + (first + lane >> g.c.page_shift))) {
+    if (t.page >= 0 && t.page == __ldg(g.c.table + b * g.c.table_stride + ((first + lane) >> g.c.page_shift))) {
       if (key != first + lane) report_bounds(g.c.status, kSitePagedEvict, t.page);   // (else it is there)
       t.page = -1;
     }
